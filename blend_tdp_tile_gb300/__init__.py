@@ -29,6 +29,8 @@ __all__ = [
     "tdp_pos_bounds", "tdp_split", "tdp_split_tma", "tdp_norm_filter", "tdp_split_filter", "tdp_blend", "tdp_cond_blend",
     "tdp_cond_records_size", "tdp_cond_records", "tdp_cond_blend_records",
     "tdp_tile_mean", "tdp_blend_partial", "tdp_blend_store", "tdp_blend_cond",
+    "TDP_MAX_HEAD_DIM", "TDP_MAX_STATES", "tdp_cross_attn", "tdp_cross_attn_grad", "tdp_cross_attn_workspace",
+    "tdp_group_norm", "tdp_group_norm_grad", "tdp_group_norm_workspace", "tdp_dropout_add", "tdp_dropout_grad",
     "tdp_balanced_tile_split", "tdp_tiles_for_size", "tdp_rank_tiles",
     "tdp_status_str", "tdp_last_error_detail",
     "alloc_split_outputs", "alloc_filter_outputs", "LIB_PATH",
@@ -39,6 +41,9 @@ LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libtdp.so")
 TDP_OK = 0
 TDP_F32, TDP_BF16 = 0, 1
 TDP_MAX_TILES_PER_DIM = 64
+TDP_MAX_HEAD_DIM = 128
+TDP_MAX_STATES = 1 << 20
+_ACTS = {"none": 0, "silu": 1}
 
 
 class TdpError(RuntimeError):
@@ -55,6 +60,13 @@ class _Problem(ctypes.Structure):
     _fields_ = [("B", ctypes.c_int32), ("F", ctypes.c_int32), ("H", ctypes.c_int32),
                 ("W", ctypes.c_int32), ("C", ctypes.c_int32), ("dtype", ctypes.c_int32),
                 ("dim", _DimCfg * 3)]
+
+
+class _XAttn(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("q_heads", "kv_heads", "head_dim", "states", "mask_per_tile")] + \
+               [("scale", ctypes.c_float)] + \
+               [(n, ctypes.c_int64) for n in ("q_row", "q_head", "k_item", "k_state", "k_head",
+                                              "v_item", "v_state", "v_head")]
 
 
 def _load():
@@ -96,6 +108,18 @@ def _load():
     lib.tdp_blend_partial.restype = ctypes.c_int
     lib.tdp_blend_store.argtypes = [vp, ctypes.c_int64, vp, vp, vp]
     lib.tdp_blend_store.restype = ctypes.c_int
+    i64, f32, f64, xap = ctypes.c_int64, ctypes.c_float, ctypes.c_double, ctypes.POINTER(_XAttn)
+    lib.tdp_cross_attn_workspace.argtypes = [vp, xap, i32, i64p]
+    lib.tdp_cross_attn.argtypes = [vp, xap, vp, vp, vp, vp, vp, vp, vp, i64, vp]
+    lib.tdp_cross_attn_grad.argtypes = [vp, xap] + [vp] * 11 + [i64, vp]
+    lib.tdp_group_norm_workspace.argtypes = [vp, i32, i32, i64p]
+    lib.tdp_group_norm.argtypes = [vp, i32, i32, f32, i32] + [vp] * 7 + [i64, vp]
+    lib.tdp_group_norm_grad.argtypes = [vp, i32, i32, i32] + [vp] * 10 + [i64, vp]
+    lib.tdp_dropout_add.argtypes = [vp, i64, f64, vp, vp, vp, vp, vp]
+    lib.tdp_dropout_grad.argtypes = [vp, i64, f64, vp, vp, vp, vp]
+    for name in ("tdp_cross_attn_workspace", "tdp_cross_attn", "tdp_cross_attn_grad", "tdp_group_norm_workspace",
+                 "tdp_group_norm", "tdp_group_norm_grad", "tdp_dropout_add", "tdp_dropout_grad"):
+        getattr(lib, name).restype = ctypes.c_int
     lib.tdp_balanced_tile_split.argtypes = [i32, ctypes.POINTER(i32), ctypes.POINTER(i32)]
     lib.tdp_balanced_tile_split.restype = ctypes.c_int
     lib.tdp_tiles_for_size.argtypes = [i32, i32, i32, ctypes.POINTER(i32)]
@@ -509,3 +533,183 @@ def alloc_filter_outputs(plan: Plan, N: int, device="cuda", slot=False):
     if slot:
         return keep, idx, count, kcount, Kout, torch.empty((nt, B, N), dtype=torch.int32, device=device)
     return keep, idx, count, kcount, Kout
+
+
+# ------------------------------------------------------------------ operators of the per-tile block
+def _rows(plan):
+    return plan.B * plan.total_tile_tokens
+
+
+def _strides(t, name, shape, dtypes):
+    """Element strides of a tensor of `shape` whose last dimension is contiguous (0 along dimensions of one)."""
+    torch = _torch()
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name}: must be a CUDA tensor")
+    if t.dtype not in dtypes:
+        raise ValueError(f"{name}: dtype {t.dtype} not in {dtypes}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.numel() and t.stride(-1) != 1:
+        raise ValueError(f"{name}: the last dimension must be contiguous")
+    if t.data_ptr() % 16 and t.numel():
+        raise ValueError(f"{name}: not 16-byte aligned")
+    return tuple(st if n > 1 else 0 for n, st in zip(t.shape[:-1], t.stride()[:-1]))
+
+
+def _workspace(ws, need, like, stream):
+    """A workspace of `need` bytes: the caller's, or one of torch's for the stream of the call."""
+    if ws is not None or need == 0:
+        return ws
+    torch = _torch()
+    if stream is None:
+        return torch.empty(need, dtype=torch.uint8, device=like.device)
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream, device=like.device)
+    with torch.cuda.stream(stream):
+        return torch.empty(need, dtype=torch.uint8, device=like.device)
+
+
+def _xattn_shape(plan, q, k, v, mask, scale):
+    """The C shape of a cross attention from its tensors."""
+    lat = _latent_dtypes(plan)
+    if q.dim() != 3 or k.dim() != 4:
+        raise ValueError("q must be [rows, heads, D] and k [B, states, heads, D]")
+    (_, Hq, D), (_, S, Hkv, _) = q.shape, k.shape
+    a = _XAttn()
+    a.q_heads, a.kv_heads, a.head_dim, a.states = Hq, Hkv, D, S
+    a.scale = D ** -0.5 if scale is None else scale
+    a.q_row, a.q_head = _strides(q, "q", (_rows(plan), Hq, D), lat)
+    a.k_item, a.k_state, a.k_head = _strides(k, "k", (plan.B, S, Hkv, D), lat)
+    a.v_item, a.v_state, a.v_head = _strides(v, "v", (plan.B, S, Hkv, D), lat)
+    a.mask_per_tile = int(mask is not None and mask.dim() == 3)
+    return a
+
+
+def _xattn_mask(c, plan, a, mask):
+    torch = _torch()
+    if mask is None:
+        return None
+    want = (plan.n_tiles, plan.B, a.states) if a.mask_per_tile else (plan.B, a.states)
+    if tuple(mask.shape) != want:
+        raise ValueError(f"mask: shape {tuple(mask.shape)}, expected {want}")
+    return c.ptr(mask, "mask", mask.numel(), (torch.uint8, torch.bool), 1)
+
+
+def _given(c, t, name):
+    c.named.append((name, t))
+    return t.data_ptr()
+
+
+def tdp_cross_attn_workspace(plan: Plan, q, k, v, mask=None, scale=None, grad=False) -> int:
+    """Bytes of workspace tdp_cross_attn (or, with grad, tdp_cross_attn_grad) takes for these tensors."""
+    n = ctypes.c_int64()
+    a = _xattn_shape(plan, q, k, v, mask, scale)
+    _check(_lib.tdp_cross_attn_workspace(plan.handle, ctypes.byref(a), int(grad), ctypes.byref(n)),
+           "tdp_cross_attn_workspace")
+    return int(n.value)
+
+
+def tdp_cross_attn(plan: Plan, q, k, v, mask, out, lse=None, scale=None, ws=None, stream=None):
+    """Tile rows q [R, Hq, D] attend to encoder states k, v [B, S, Hkv, D] into out [R, Hq, D] (and the
+    rows' log-sums into lse [R, Hq]).
+
+    q, k and v may be strided (slices of a fused projection).  mask: None, or uint8/bool [B, S] or
+    [n_tiles, B, S], nonzero = kept.  scale: None for 1/sqrt(D).  ws: None takes the workspace
+    from torch's allocator."""
+    torch = _torch()
+    a = _xattn_shape(plan, q, k, v, mask, scale)
+    n = ctypes.c_int64()
+    _check(_lib.tdp_cross_attn_workspace(plan.handle, ctypes.byref(a), 0, ctypes.byref(n)), "tdp_cross_attn")
+    ws = _workspace(ws, n.value, q, stream)
+    c = _Call("tdp_cross_attn")
+    c.run(_lib.tdp_cross_attn, plan.handle, ctypes.byref(a), _given(c, q, "q"), _given(c, k, "k"), _given(c, v, "v"),
+          _xattn_mask(c, plan, a, mask),
+          c.ptr(out, "out", q.numel(), _latent_dtypes(plan), 16),
+          c.ptr(lse, "lse", _rows(plan) * a.q_heads, (torch.float32,), 4),
+          None if ws is None else c.ptr(ws, "ws", ws.numel(), (torch.uint8,), 256),
+          0 if ws is None else ws.numel(), stream=stream)
+
+
+def tdp_cross_attn_grad(plan: Plan, q, k, v, mask, out, lse, dout, dq, dk, dv, scale=None, ws=None, stream=None):
+    """Gradients of tdp_cross_attn: dq [R, Hq, D], dk and dv [B, S, Hkv, D] (contiguous) from its
+    arguments, its out and lse, and dout [R, Hq, D]."""
+    torch = _torch()
+    lat = _latent_dtypes(plan)
+    a = _xattn_shape(plan, q, k, v, mask, scale)
+    n = ctypes.c_int64()
+    _check(_lib.tdp_cross_attn_workspace(plan.handle, ctypes.byref(a), 1, ctypes.byref(n)), "tdp_cross_attn_grad")
+    ws = _workspace(ws, n.value, q, stream)
+    c = _Call("tdp_cross_attn_grad")
+    c.run(_lib.tdp_cross_attn_grad, plan.handle, ctypes.byref(a), _given(c, q, "q"), _given(c, k, "k"),
+          _given(c, v, "v"), _xattn_mask(c, plan, a, mask), c.ptr(out, "out", q.numel(), lat, 16),
+          c.ptr(lse, "lse", _rows(plan) * a.q_heads, (torch.float32,), 4), c.ptr(dout, "dout", q.numel(), lat, 16),
+          c.ptr(dq, "dq", q.numel(), lat, 16), c.ptr(dk, "dk", k.numel(), lat, 16), c.ptr(dv, "dv", v.numel(), lat, 16),
+          None if ws is None else c.ptr(ws, "ws", ws.numel(), (torch.uint8,), 256),
+          0 if ws is None else ws.numel(), stream=stream)
+
+
+def tdp_group_norm_workspace(plan: Plan, C: int, groups: int) -> int:
+    """Bytes of workspace tdp_group_norm and tdp_group_norm_grad take for rows of C channels."""
+    n = ctypes.c_int64()
+    _check(_lib.tdp_group_norm_workspace(plan.handle, int(C), int(groups), ctypes.byref(n)), "tdp_group_norm_workspace")
+    return int(n.value)
+
+
+def _act(act):
+    if act not in _ACTS:
+        raise ValueError(f"act: {act!r} not in {sorted(_ACTS)}")
+    return _ACTS[act]
+
+
+def tdp_group_norm(plan: Plan, x, groups, gamma, beta, y, mean, rstd, eps=1e-5, act="none", ws=None, stream=None):
+    """y = act(group norm of every (tile, item) of tile-major rows x [R, C]); mean and rstd
+    [n_tiles, B, groups] are written too.  gamma, beta: [C] or None.  act: "none" or "silu"."""
+    f32, lat = (_torch().float32,), _latent_dtypes(plan)
+    C, ns = int(x.shape[-1]), plan.n_tiles * plan.B * int(groups)
+    ws = _workspace(ws, tdp_group_norm_workspace(plan, C, groups), x, stream)
+    c = _Call("tdp_group_norm")
+    c.run(_lib.tdp_group_norm, plan.handle, C, int(groups), float(eps), _act(act), c.ptr(x, "x", _rows(plan) * C, lat, 16),
+          c.ptr(gamma, "gamma", C, lat, 16), c.ptr(beta, "beta", C, lat, 16), c.ptr(y, "y", _rows(plan) * C, lat, 16),
+          c.ptr(mean, "mean", ns, f32, 4), c.ptr(rstd, "rstd", ns, f32, 4),
+          None if ws is None else c.ptr(ws, "ws", ws.numel(), (_torch().uint8,), 256),
+          0 if ws is None else ws.numel(), stream=stream)
+
+
+def tdp_group_norm_grad(plan: Plan, x, groups, gamma, beta, mean, rstd, dy, dx, dgamma=None, dbeta=None, act="none",
+                        ws=None, stream=None):
+    """Gradients of tdp_group_norm: dx [R, C] and, unless None, dgamma and dbeta [C] in fp32."""
+    f32, lat = (_torch().float32,), _latent_dtypes(plan)
+    C, ns = int(x.shape[-1]), plan.n_tiles * plan.B * int(groups)
+    ws = _workspace(ws, tdp_group_norm_workspace(plan, C, groups), x, stream)
+    c = _Call("tdp_group_norm_grad")
+    n = _rows(plan) * C
+    c.run(_lib.tdp_group_norm_grad, plan.handle, C, int(groups), _act(act), c.ptr(x, "x", n, lat, 16),
+          c.ptr(gamma, "gamma", C, lat, 16), c.ptr(beta, "beta", C, lat, 16), c.ptr(mean, "mean", ns, f32, 4),
+          c.ptr(rstd, "rstd", ns, f32, 4), c.ptr(dy, "dy", n, lat, 16), c.ptr(dx, "dx", n, lat, 16),
+          c.ptr(dgamma, "dgamma", C, f32, 4), c.ptr(dbeta, "dbeta", C, f32, 4),
+          None if ws is None else c.ptr(ws, "ws", ws.numel(), (_torch().uint8,), 256),
+          0 if ws is None else ws.numel(), stream=stream)
+
+
+def _rng(c, rng):
+    torch = _torch()
+    return c.ptr(rng, "rng", 2, (torch.int64, getattr(torch, "uint64", torch.int64)), 8)
+
+
+def tdp_dropout_add(plan: Plan, x, res, p, rng, out, stream=None):
+    """out = res + dropout(x): elements dropped with probability p by the generator of
+    rng (two 64-bit integers on the device: seed, offset), the others divided by 1 - p.  res may be None."""
+    lat, n = _latent_dtypes(plan), x.numel()
+    c = _Call("tdp_dropout_add")
+    c.run(_lib.tdp_dropout_add, plan.handle, n, float(p), _rng(c, rng), c.ptr(x, "x", n, lat, 16),
+          c.ptr(res, "res", n, lat, 16), c.ptr(out, "out", n, lat, 16), stream=stream)
+
+
+def tdp_dropout_grad(plan: Plan, dout, p, rng, dx, stream=None):
+    """dx of tdp_dropout_add with the same p and rng; the residual's gradient is dout itself."""
+    lat, n = _latent_dtypes(plan), dout.numel()
+    c = _Call("tdp_dropout_grad")
+    c.run(_lib.tdp_dropout_grad, plan.handle, n, float(p), _rng(c, rng), c.ptr(dout, "dout", n, lat, 16),
+          c.ptr(dx, "dx", n, lat, 16), stream=stream)

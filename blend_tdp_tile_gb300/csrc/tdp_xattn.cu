@@ -1,0 +1,705 @@
+// tdp_xattn.cu -- cross attention of the tiles' tokens to an encoder's states, and its
+// gradients: entry points and the CUDA-core kernels.
+//
+// out = softmax(scale * Q K^T over the kept states) V, one pass over the states with the
+// running maximum m and sum l of the softmax: a block holds 64 packed rows, takes 64
+// states at a time, and rescales its sums by exp(m_old - m_new) when the maximum grows.  With
+// few rows the states are split over blocks, whose outputs are joined by their log-sums.
+// The gradient computes p = exp(s - lse) again: one kernel walks the states for dq,
+// one walks the rows for dk and dv (split over the rows, joined in order: no
+// atomics).  States that a row's mask drops are read as zero and get p = 0.
+#include <algorithm>
+#include <atomic>
+
+#include "tdp.h"
+#include "tdp_xattn.h"
+
+namespace {
+
+constexpr int kXT = 256;        // threads: 16 x 16, each 4 rows x 4 states
+constexpr int kXM = 64;         // packed rows of a block
+constexpr int kXN = 64;         // states of a step
+constexpr float kLog2e = 1.4426950408889634f;
+
+template <int DP>
+struct xsm {
+    static constexpr int kLd = DP + 4;      // row stride: lanes 4 banks apart
+    static constexpr int kTile = 64 * kLd;
+    static constexpr int kPs = kXN + 4;
+};
+
+// 64 rows of D elements to smem as fp32, zero past D and where row(i) gives NULL.
+template <int BF16, int DP, typename Row>
+__device__ __forceinline__ void load_tile(float *dst, int32_t D, Row row)
+{
+    using E = tdp_elem<BF16>;
+    constexpr int V = E::kVec, NV = DP / V;
+    for (int32_t i = threadIdx.x; i < 64 * NV; i += kXT) {
+        const int32_t r = i / NV, c = i % NV;
+        const typename E::type *p = static_cast<const typename E::type *>(row(r));
+        float f[V];
+        if (p && c * V < D) {
+            E::unpack(*reinterpret_cast<const uint4 *>(p + c * V), f);
+        } else {
+#pragma unroll
+            for (int j = 0; j < V; ++j) f[j] = 0.f;
+        }
+#pragma unroll
+        for (int j = 0; j < V; j += 4)
+            *reinterpret_cast<float4 *>(dst + r * xsm<DP>::kLd + c * V + j) = make_float4(f[j], f[j + 1], f[j + 2], f[j + 3]);
+    }
+}
+
+// acc[i][j] = A[4 ty + i] . B[tx + 16 j] over DP.
+template <int DP>
+__device__ __forceinline__ void dot_tile(const float *A, const float *B, int ty, int tx, float (&acc)[4][4])
+{
+    constexpr int L = xsm<DP>::kLd;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[i][j] = 0.f;
+#pragma unroll 4
+    for (int d = 0; d < DP; d += 4) {
+        float4 x[4], y[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            x[i] = *reinterpret_cast<const float4 *>(A + (4 * ty + i) * L + d);
+            y[i] = *reinterpret_cast<const float4 *>(B + (tx + 16 * i) * L + d);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                acc[i][j] = fmaf(x[i].x, y[j].x, fmaf(x[i].y, y[j].y, fmaf(x[i].z, y[j].z, fmaf(x[i].w, y[j].w, acc[i][j]))));
+    }
+}
+
+// acc[i][4 c + e] += sum_j P[4 ty + i][j] * B[j][64 c + 4 tx + e]: rows of P times rows of B.
+template <int DP>
+__device__ __forceinline__ void mul_tile(const float *P, const float *B, int ty, int tx, float (&acc)[4][DP / 16])
+{
+    constexpr int L = xsm<DP>::kLd, LP = xsm<DP>::kPs;
+#pragma unroll 2
+    for (int j = 0; j < 64; j += 4) {
+        float p[4][4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            *reinterpret_cast<float4 *>(p[i]) = *reinterpret_cast<const float4 *>(P + (4 * ty + i) * LP + j);
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+#pragma unroll
+            for (int c = 0; c < DP / 64; ++c) {
+                const float4 b = *reinterpret_cast<const float4 *>(B + (j + u) * L + 64 * c + 4 * tx);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    acc[i][4 * c + 0] = fmaf(p[i][u], b.x, acc[i][4 * c + 0]);
+                    acc[i][4 * c + 1] = fmaf(p[i][u], b.y, acc[i][4 * c + 1]);
+                    acc[i][4 * c + 2] = fmaf(p[i][u], b.z, acc[i][4 * c + 2]);
+                    acc[i][4 * c + 3] = fmaf(p[i][u], b.w, acc[i][4 * c + 3]);
+                }
+            }
+    }
+}
+
+__device__ __forceinline__ float row_max16(float x)
+{
+    for (int o = 8; o; o >>= 1) x = fmaxf(x, __shfl_xor_sync(~0u, x, o));
+    return x;
+}
+__device__ __forceinline__ float row_sum16(float x)
+{
+    for (int o = 8; o; o >>= 1) x += __shfl_xor_sync(~0u, x, o);
+    return x;
+}
+
+// Mask of the 64 states from s0 on: bit j of word j / 32.
+__device__ __forceinline__ bool kept_bits(const uint8_t *mask, int32_t s0, int32_t S, uint32_t *bits)
+{
+    if (threadIdx.x < 64) {
+        const int32_t s = s0 + threadIdx.x;
+        const uint32_t w = __ballot_sync(~0u, s < S && (!mask || mask[s]));
+        if ((threadIdx.x & 31) == 0) bits[threadIdx.x >> 5] = w;
+    }
+    __syncthreads();
+    return (bits[0] | bits[1]) != 0;
+}
+
+// Offset of packed row r of key head kvh in rows and heads that lie `row` and `head` apart.
+__device__ __forceinline__ int64_t packed(const xattn_args &a, const tdp_seg &seg, int32_t kvh, int64_t r, int64_t row,
+                                          int64_t head)
+{
+    const int64_t tok = r / a.G;
+    return (seg.row0 + tok) * row + (kvh * a.G + (int32_t)(r - tok * a.G)) * head;
+}
+
+// log2 of the row's sum of exponentials; a row with no sum gets +inf, which makes its probabilities zero.
+__device__ __forceinline__ float lse2(float lse) { return lse == -INFINITY ? INFINITY : lse * kLog2e; }
+
+template <int BF16, int DP>
+__global__ void __launch_bounds__(kXT)
+tdp_xattn_simt_kernel(const __grid_constant__ tdp_geom g, const __grid_constant__ xattn_args a)
+{
+    using E = tdp_elem<BF16>;
+    using T = typename E::type;
+    extern __shared__ __align__(16) float sm[];
+    float *Qs = sm, *Ks = Qs + xsm<DP>::kTile, *Vs = Ks + xsm<DP>::kTile, *Ps = Vs + xsm<DP>::kTile;
+    __shared__ uint32_t bits[2];
+    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+    int32_t w = blockIdx.x;
+    const int32_t blk = w % a.blocks;
+    w /= a.blocks;
+    const int32_t kvh = w % a.Hkv;
+    w /= a.Hkv;
+    const int32_t part = w % a.split;
+    const tdp_seg seg = xattn_seg(g, a, w / a.split);
+    const int64_t r0 = (int64_t)blk * kXM, nr = seg.T * a.G - r0;
+    tdp_pdl_trigger();
+    tdp_pdl_wait();
+    if (nr <= 0) return;
+    const uint8_t *mask = xattn_mask(a, g, seg);
+    const T *q = static_cast<const T *>(a.q), *k = static_cast<const T *>(a.k) + seg.b * a.k_item + kvh * a.k_head,
+            *v = static_cast<const T *>(a.v) + seg.b * a.v_item + kvh * a.v_head;
+    load_tile<BF16, DP>(Qs, a.D, [&](int32_t r) { return r < nr ? q + packed(a, seg, kvh, r0 + r, a.q_row, a.q_head) : nullptr; });
+    float m[4], l[4], acc[4][DP / 16];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        m[i] = -INFINITY;
+        l[i] = 0.f;
+#pragma unroll
+        for (int c = 0; c < DP / 16; ++c) acc[i][c] = 0.f;
+    }
+    const float c2 = a.scale * kLog2e;
+    const int32_t tile0 = part * a.part, tile1 = min((a.S + kXN - 1) / kXN, tile0 + a.part);
+    for (int32_t t = tile0; t < tile1; ++t) {
+        __syncthreads();
+        if (!kept_bits(mask, t * kXN, a.S, bits)) continue;
+        const uint32_t b0 = bits[0], b1 = bits[1];
+        auto kept = [&](int32_t j) { return ((j < 32 ? b0 >> j : b1 >> (j - 32)) & 1) != 0; };
+        load_tile<BF16, DP>(Ks, a.D, [&](int32_t j) { return kept(j) ? k + (int64_t)(t * kXN + j) * a.k_state : nullptr; });
+        load_tile<BF16, DP>(Vs, a.D, [&](int32_t j) { return kept(j) ? v + (int64_t)(t * kXN + j) * a.v_state : nullptr; });
+        __syncthreads();
+        float s[4][4];
+        dot_tile<DP>(Qs, Ks, ty, tx, s);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            float top = -INFINITY;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                s[i][j] = kept(tx + 16 * j) ? s[i][j] * c2 : -INFINITY;
+                top = fmaxf(top, s[i][j]);
+            }
+            const float mn = fmaxf(m[i], row_max16(top));
+            const float base = mn == -INFINITY ? 0.f : mn, old = exp2f(m[i] - base);
+            float sum = 0.f;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float p = exp2f(s[i][j] - base);
+                sum += p;
+                Ps[(4 * ty + i) * xsm<DP>::kPs + tx + 16 * j] = p;
+            }
+            l[i] = l[i] * old + row_sum16(sum);
+            m[i] = mn;
+#pragma unroll
+            for (int c = 0; c < DP / 16; ++c) acc[i][c] *= old;
+        }
+        __syncwarp();       // a row's probabilities are written and read by one warp
+        mul_tile<DP>(Ps, Vs, ty, tx, acc);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int32_t r = 4 * ty + i;
+        if (r >= nr) continue;
+        const float inv = l[i] > 0.f || l[i] != l[i] ? 1.f / l[i] : 0.f;
+        const float lse = l[i] == 0.f ? -INFINITY : (m[i] + log2f(l[i])) * 0.6931471805599453f;
+        const int64_t h = packed(a, seg, kvh, r0 + r, a.Hq, 1);
+        if (a.split > 1) {
+            const int64_t at = (int64_t)part * a.rows * a.Hq + h;
+            if (tx == 0) a.pl[at] = lse;
+#pragma unroll
+            for (int c = 0; c < DP / 16; ++c) {
+                const int32_t d = 64 * (c / 4) + 4 * tx + c % 4;
+                if (d < a.D) a.po[at * a.D + d] = acc[i][c] * inv;
+            }
+        } else {
+            if (tx == 0 && a.lse) a.lse[h] = lse;
+#pragma unroll
+            for (int c = 0; c < DP / 16; ++c) {
+                const int32_t d = 64 * (c / 4) + 4 * tx + c % 4;
+                if (d < a.D) static_cast<T *>(a.out)[h * a.D + d] = (T)(acc[i][c] * inv);
+            }
+        }
+    }
+}
+
+// One warp per (row, head): out = sum_i exp(lse_i - lse) out_i over the parts of the states.
+template <int BF16>
+__global__ void __launch_bounds__(kXT)
+tdp_xattn_join_kernel(const xattn_args a)
+{
+    using T = typename tdp_elem<BF16>::type;
+    tdp_pdl_trigger();
+    tdp_pdl_wait();
+    const int64_t n = a.rows * a.Hq, h = ((int64_t)blockIdx.x * kXT + threadIdx.x) >> 5;
+    if (h >= n) return;
+    const int32_t lane = threadIdx.x & 31;
+    float top = -INFINITY;
+    for (int32_t i = 0; i < a.split; ++i) top = fmaxf(top, a.pl[i * n + h]);
+    const float base = top == -INFINITY ? 0.f : top;
+    float sum = 0.f, acc[TDP_MAX_HEAD_DIM / 32] = {};
+    for (int32_t i = 0; i < a.split; ++i) {
+        const float w = expf(a.pl[i * n + h] - base);
+        sum += w;
+        if (w != 0.f)
+            for (int c = 0; c < TDP_MAX_HEAD_DIM / 32; ++c)
+                if (lane + 32 * c < a.D) acc[c] += w * a.po[(i * n + h) * a.D + lane + 32 * c];
+    }
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    for (int c = 0; c < TDP_MAX_HEAD_DIM / 32; ++c)
+        if (lane + 32 * c < a.D) static_cast<T *>(a.out)[h * a.D + lane + 32 * c] = (T)(acc[c] * inv);
+    if (lane == 0 && a.lse) a.lse[h] = sum == 0.f ? -INFINITY : base + logf(sum);
+}
+
+// dq of 64 packed rows; delta = dout . out is written for the kernel that follows.
+template <int BF16, int DP>
+__global__ void __launch_bounds__(kXT)
+tdp_xattn_simt_dq_kernel(const __grid_constant__ tdp_geom g, const __grid_constant__ xattn_args a)
+{
+    using E = tdp_elem<BF16>;
+    using T = typename E::type;
+    extern __shared__ __align__(16) float sm[];
+    float *Qs = sm, *Ds = Qs + xsm<DP>::kTile, *Ks = Ds + xsm<DP>::kTile, *Vs = Ks + xsm<DP>::kTile,
+          *Ps = Vs + xsm<DP>::kTile;
+    __shared__ uint32_t bits[2];
+    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+    int32_t w = blockIdx.x;
+    const int32_t blk = w % a.blocks;
+    w /= a.blocks;
+    const int32_t kvh = w % a.Hkv;
+    const tdp_seg seg = xattn_seg(g, a, w / a.Hkv);
+    const int64_t r0 = (int64_t)blk * kXM, nr = seg.T * a.G - r0;
+    tdp_pdl_trigger();
+    tdp_pdl_wait();
+    if (nr <= 0) return;
+    const uint8_t *mask = xattn_mask(a, g, seg);
+    const T *q = static_cast<const T *>(a.q), *k = static_cast<const T *>(a.k) + seg.b * a.k_item + kvh * a.k_head,
+            *v = static_cast<const T *>(a.v) + seg.b * a.v_item + kvh * a.v_head;
+    auto row = [&](const void *p, int32_t r) -> const T * {
+        return r < nr ? static_cast<const T *>(p) + packed(a, seg, kvh, r0 + r, (int64_t)a.Hq * a.D, a.D) : nullptr;
+    };
+    load_tile<BF16, DP>(Qs, a.D, [&](int32_t r) { return row(a.o, r); });
+    load_tile<BF16, DP>(Ds, a.D, [&](int32_t r) { return row(a.dout, r); });
+    __syncthreads();
+    float lse[4], delta[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        float d = 0.f;
+        for (int c = tx; c < DP; c += 16) d += Qs[(4 * ty + i) * xsm<DP>::kLd + c] * Ds[(4 * ty + i) * xsm<DP>::kLd + c];
+        delta[i] = row_sum16(d);
+        const int32_t r = 4 * ty + i;
+        lse[i] = INFINITY;
+        if (r < nr) {
+            const int64_t h = packed(a, seg, kvh, r0 + r, a.Hq, 1);
+            lse[i] = lse2(a.lse[h]);
+            if (tx == 0) a.delta[h] = delta[i];
+        }
+    }
+    __syncthreads();
+    load_tile<BF16, DP>(Qs, a.D, [&](int32_t r) { return r < nr ? q + packed(a, seg, kvh, r0 + r, a.q_row, a.q_head) : nullptr; });
+    float acc[4][DP / 16];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int c = 0; c < DP / 16; ++c) acc[i][c] = 0.f;
+    const float c2 = a.scale * kLog2e;
+    for (int32_t t = 0; t * kXN < a.S; ++t) {
+        __syncthreads();
+        if (!kept_bits(mask, t * kXN, a.S, bits)) continue;
+        const uint32_t b0 = bits[0], b1 = bits[1];
+        auto kept = [&](int32_t j) { return ((j < 32 ? b0 >> j : b1 >> (j - 32)) & 1) != 0; };
+        load_tile<BF16, DP>(Ks, a.D, [&](int32_t j) { return kept(j) ? k + (int64_t)(t * kXN + j) * a.k_state : nullptr; });
+        load_tile<BF16, DP>(Vs, a.D, [&](int32_t j) { return kept(j) ? v + (int64_t)(t * kXN + j) * a.v_state : nullptr; });
+        __syncthreads();
+        float s[4][4], dp[4][4];
+        dot_tile<DP>(Qs, Ks, ty, tx, s);
+        dot_tile<DP>(Ds, Vs, ty, tx, dp);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                Ps[(4 * ty + i) * xsm<DP>::kPs + tx + 16 * j] =
+                    kept(tx + 16 * j) ? exp2f(s[i][j] * c2 - lse[i]) * (dp[i][j] - delta[i]) * a.scale : 0.f;
+        __syncwarp();
+        mul_tile<DP>(Ps, Ks, ty, tx, acc);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int32_t r = 4 * ty + i;
+        if (r >= nr) continue;
+        T *o = const_cast<T *>(row(a.dq, r));
+#pragma unroll
+        for (int c = 0; c < DP / 16; ++c) {
+            const int32_t d = 64 * (c / 4) + 4 * tx + c % 4;
+            if (d < a.D) o[d] = (T)acc[i][c];
+        }
+    }
+}
+
+// dk and dv of 64 states: the transposed tiles, states as rows, over a part of the row blocks of
+// every segment of the item.
+template <int BF16, int DP>
+__global__ void __launch_bounds__(kXT)
+tdp_xattn_simt_dkv_kernel(const __grid_constant__ tdp_geom g, const __grid_constant__ xattn_args a)
+{
+    using E = tdp_elem<BF16>;
+    using T = typename E::type;
+    extern __shared__ __align__(16) float sm[];
+    float *Ks = sm, *Vs = Ks + xsm<DP>::kTile, *Qs = Vs + xsm<DP>::kTile, *Ds = Qs + xsm<DP>::kTile,
+          *Ps = Ds + xsm<DP>::kTile, *Ss = Ps + 64 * xsm<DP>::kPs;
+    __shared__ uint32_t bits[2];
+    __shared__ float row_lse[kXM], row_delta[kXM];
+    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+    const int32_t tiles = (a.S + kXN - 1) / kXN;
+    int32_t w = blockIdx.x;
+    const int32_t t = w % tiles;
+    w /= tiles;
+    const int32_t kvh = w % a.Hkv;
+    w /= a.Hkv;
+    const int32_t part = w % a.split, b = w / a.split;
+    tdp_pdl_trigger();
+    tdp_pdl_wait();
+    const T *q = static_cast<const T *>(a.q), *k = static_cast<const T *>(a.k) + b * a.k_item + kvh * a.k_head,
+            *v = static_cast<const T *>(a.v) + b * a.v_item + kvh * a.v_head;
+    // a state no mask of its segments keeps is never multiplied by a kept probability, but
+    // another tile's may keep it: the tiles are loaded as they are and selected per segment
+    load_tile<BF16, DP>(Ks, a.D, [&](int32_t j) { return t * kXN + j < a.S ? k + (int64_t)(t * kXN + j) * a.k_state : nullptr; });
+    load_tile<BF16, DP>(Vs, a.D, [&](int32_t j) { return t * kXN + j < a.S ? v + (int64_t)(t * kXN + j) * a.v_state : nullptr; });
+    float dk[4][DP / 16], dv[4][DP / 16];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int c = 0; c < DP / 16; ++c) dk[i][c] = dv[i][c] = 0.f;
+    const float c2 = a.scale * kLog2e;
+    const int32_t nsegs = a.flat ? 1 : g.nt;
+    const int64_t first = (int64_t)part * a.part, last = min((int64_t)nsegs * a.blocks, first + a.part);
+    int32_t cur = -1;
+    bool any = false;
+    tdp_seg seg = {};
+    for (int64_t u = first; u < last; ++u) {
+        const int32_t sg = (int32_t)(u / a.blocks);
+        const int64_t r0 = (u % a.blocks) * kXM;
+        if (sg != cur) {
+            cur = sg;
+            seg = xattn_seg(g, a, sg * g.B + b);
+            __syncthreads();
+            any = kept_bits(xattn_mask(a, g, seg), t * kXN, a.S, bits);
+        }
+        const int64_t nr = seg.T * a.G - r0;
+        if (!any || nr <= 0) continue;
+        const uint32_t b0 = bits[0], b1 = bits[1];
+        auto kept = [&](int32_t j) { return ((j < 32 ? b0 >> j : b1 >> (j - 32)) & 1) != 0; };
+        __syncthreads();
+        load_tile<BF16, DP>(Qs, a.D, [&](int32_t r) { return r < nr ? q + packed(a, seg, kvh, r0 + r, a.q_row, a.q_head) : nullptr; });
+        load_tile<BF16, DP>(Ds, a.D, [&](int32_t r) {
+            return r < nr ? static_cast<const T *>(a.dout) + packed(a, seg, kvh, r0 + r, (int64_t)a.Hq * a.D, a.D) : nullptr;
+        });
+        if (threadIdx.x < kXM) {
+            float ls = INFINITY, de = 0.f;
+            if (threadIdx.x < nr) {
+                const int64_t h = packed(a, seg, kvh, r0 + threadIdx.x, a.Hq, 1);
+                ls = lse2(a.lse[h]);
+                de = a.delta[h];
+            }
+            row_lse[threadIdx.x] = ls;
+            row_delta[threadIdx.x] = de;
+        }
+        __syncthreads();
+        float s[4][4], dp[4][4];
+        dot_tile<DP>(Ks, Qs, ty, tx, s);
+        dot_tile<DP>(Vs, Ds, ty, tx, dp);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int32_t r = tx + 16 * j;
+                const bool on = kept(4 * ty + i);
+                const float p = on ? exp2f(s[i][j] * c2 - row_lse[r]) : 0.f;
+                Ps[(4 * ty + i) * xsm<DP>::kPs + r] = p;
+                Ss[(4 * ty + i) * xsm<DP>::kPs + r] = on ? p * (dp[i][j] - row_delta[r]) * a.scale : 0.f;
+            }
+        __syncwarp();
+        mul_tile<DP>(Ps, Ds, ty, tx, dv);
+        mul_tile<DP>(Ss, Qs, ty, tx, dk);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int32_t st = t * kXN + 4 * ty + i;
+        if (st >= a.S) continue;
+        const int64_t at = (((int64_t)b * a.S + st) * a.Hkv + kvh) * a.D, all = (int64_t)part * g.B * a.S * a.Hkv * a.D;
+#pragma unroll
+        for (int c = 0; c < DP / 16; ++c) {
+            const int32_t d = 64 * (c / 4) + 4 * tx + c % 4;
+            if (d >= a.D) continue;
+            if (a.split > 1) {
+                a.pk[all + at + d] = dk[i][c];
+                a.pv[all + at + d] = dv[i][c];
+            } else {
+                static_cast<T *>(a.dk)[at + d] = (T)dk[i][c];
+                static_cast<T *>(a.dv)[at + d] = (T)dv[i][c];
+            }
+        }
+    }
+}
+
+// dk and dv from their parts, four elements a thread, parts in order.
+template <int BF16>
+__global__ void __launch_bounds__(kXT)
+tdp_xattn_dkv_join_kernel(const xattn_args a, int64_t n)
+{
+    using T = typename tdp_elem<BF16>::type;
+    tdp_pdl_trigger();
+    tdp_pdl_wait();
+    const int64_t i = ((int64_t)blockIdx.x * kXT + threadIdx.x) * 4;
+    if (i >= 2 * n) return;
+    const float *p = i < n ? a.pk + i : a.pv + (i - n);
+    T *o = i < n ? static_cast<T *>(a.dk) + i : static_cast<T *>(a.dv) + (i - n);
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int32_t k = 0; k < a.split; ++k) {
+        const float4 x = *reinterpret_cast<const float4 *>(p + k * n);
+        s.x += x.x;
+        s.y += x.y;
+        s.z += x.z;
+        s.w += x.w;
+    }
+    o[0] = (T)s.x;
+    o[1] = (T)s.y;
+    o[2] = (T)s.z;
+    o[3] = (T)s.w;
+}
+
+constexpr int kSplitMax = 64;
+constexpr int kFill = 304;      // blocks below which the work is split: two for each SM
+
+int64_t align256(int64_t x) { return (x + 255) / 256 * 256; }
+
+// The launch's shape: segments, row blocks, parts, workspace.
+struct xattn_shape {
+    int64_t fwd_bytes, grad_bytes;
+    int64_t delta_at, pk_at, pv_at;
+    int32_t fsplit, fpart, bsplit, bpart;
+};
+
+tdp_status xattn_check(tdp_plan_t plan, const tdp_xattn *p, xattn_args *a, xattn_shape *sh)
+{
+    if (!plan || !p) return tdp_fail(TDP_ERR_INVALID_ARG, "null plan or shape");
+    const tdp_geom &g = plan->g;
+    if (p->q_heads < 1 || p->kv_heads < 1 || p->q_heads % p->kv_heads != 0 || p->head_dim < 1 || p->states < 0)
+        return tdp_fail(TDP_ERR_INVALID_ARG, "need heads >= 1, q_heads a multiple of kv_heads, head_dim >= 1 and states >= 0");
+    if (!(p->scale == p->scale) || p->scale - p->scale != 0.f)
+        return tdp_fail(TDP_ERR_INVALID_ARG, "scale must be finite");
+    if (p->head_dim > TDP_MAX_HEAD_DIM || p->states > TDP_MAX_STATES)
+        return tdp_fail(TDP_ERR_TOO_LARGE, "head_dim above TDP_MAX_HEAD_DIM or states above TDP_MAX_STATES");
+    const int64_t strides[8] = {p->q_row, p->q_head, p->k_item, p->k_state, p->k_head, p->v_item, p->v_state, p->v_head};
+    const int64_t V = 16 / g.esize;
+    if (p->head_dim % V != 0) return tdp_fail(TDP_ERR_MISALIGNED, "head_dim * element size must be a multiple of 16 bytes");
+    for (int64_t s : strides) {
+        if (s < 0) return tdp_fail(TDP_ERR_INVALID_ARG, "strides must not be negative");
+        if (s % V != 0) return tdp_fail(TDP_ERR_MISALIGNED, "strides must be multiples of 16 bytes");
+    }
+    *a = xattn_args{};
+    a->q_row = p->q_row;
+    a->q_head = p->q_head;
+    a->k_item = p->k_item;
+    a->k_state = p->k_state;
+    a->k_head = p->k_head;
+    a->v_item = p->v_item;
+    a->v_state = p->v_state;
+    a->v_head = p->v_head;
+    a->rows = (int64_t)g.B * g.total;
+    a->Hq = p->q_heads;
+    a->Hkv = p->kv_heads;
+    a->G = p->q_heads / p->kv_heads;
+    a->D = p->head_dim;
+    a->S = p->states;
+    a->scale = p->scale;
+    a->per_tile = p->mask_per_tile != 0 && g.nt > 1;
+    a->flat = g.B == 1 && !a->per_tile;
+    a->segs = a->flat ? 1 : g.nt * g.B;
+    const int64_t T = a->flat ? a->rows : tdp_max_tile_tokens(g);
+    if (a->rows > 0x7fffffffLL / a->Hq) return tdp_fail(TDP_ERR_TOO_LARGE, "rows * q_heads must be below 2^31");
+    a->blocks = (int32_t)((T * a->G + kXM - 1) / kXM);
+    const int64_t tiles = (a->S + kXN - 1) / kXN;
+    const int64_t grid = (int64_t)a->segs * a->Hkv * a->blocks, kvgrid = (int64_t)g.B * a->Hkv * tiles;
+    if (grid * kSplitMax > 0x7fffffffLL || kvgrid * kSplitMax > 0x7fffffffLL || (int64_t)a->segs * a->blocks > 0x7fffffffLL)
+        return tdp_fail(TDP_ERR_TOO_LARGE, "cross attention grid too large");
+    // few row blocks: the states in parts of four tiles or more, few enough to fill the device
+    sh->fsplit = 1;
+    sh->fpart = (int32_t)std::max<int64_t>(tiles, 1);
+    if (grid > 0 && grid < kFill && tiles > 4) {
+        const int64_t want = std::min<int64_t>({kSplitMax, (kFill + grid - 1) / grid, tiles / 4});
+        sh->fpart = (int32_t)((tiles + want - 1) / want);
+        sh->fsplit = (int32_t)((tiles + sh->fpart - 1) / sh->fpart);
+    }
+    // few state tiles: the row blocks in parts
+    const int64_t units = (int64_t)(a->flat ? 1 : g.nt) * a->blocks;
+    sh->bsplit = 1;
+    sh->bpart = (int32_t)std::max<int64_t>(units, 1);
+    if (kvgrid > 0 && kvgrid < kFill && units > 1) {
+        const int64_t want = std::min<int64_t>({kSplitMax, (kFill + kvgrid - 1) / kvgrid, units});
+        sh->bpart = (int32_t)((units + want - 1) / want);
+        sh->bsplit = (int32_t)((units + sh->bpart - 1) / sh->bpart);
+    }
+    const int64_t rh = a->rows * a->Hq, kv = (int64_t)g.B * a->S * a->Hkv * a->D;
+    sh->fwd_bytes = sh->fsplit > 1 ? align256(sh->fsplit * rh * 4) + sh->fsplit * rh * a->D * 4 : 0;
+    sh->delta_at = 0;
+    sh->pk_at = align256(rh * 4);
+    sh->pv_at = sh->pk_at + (sh->bsplit > 1 ? align256(sh->bsplit * kv * 4) : 0);
+    sh->grad_bytes = sh->pv_at + (sh->bsplit > 1 ? sh->bsplit * kv * 4 : 0);
+    return TDP_OK;
+}
+
+template <int BF16, int DP>
+struct simt_kernels {
+    static constexpr size_t kFwd = (3 * xsm<DP>::kTile + 64 * xsm<DP>::kPs) * 4;
+    static constexpr size_t kDq = (4 * xsm<DP>::kTile + 64 * xsm<DP>::kPs) * 4;
+    static constexpr size_t kDkv = (4 * xsm<DP>::kTile + 2 * 64 * xsm<DP>::kPs) * 4;
+    // Raise the kernels' dynamic shared-memory limits once per device.
+    static cudaError_t prepare()
+    {
+        static std::atomic<bool> done[64];
+        int dev = 0;
+        cudaError_t e = cudaGetDevice(&dev);
+        if (e != cudaSuccess || (dev < 64 && done[dev].load(std::memory_order_relaxed))) return e;
+        const auto attr = cudaFuncAttributeMaxDynamicSharedMemorySize;
+        e = cudaFuncSetAttribute(tdp_xattn_simt_kernel<BF16, DP>, attr, (int)kFwd);
+        if (e == cudaSuccess) e = cudaFuncSetAttribute(tdp_xattn_simt_dq_kernel<BF16, DP>, attr, (int)kDq);
+        if (e == cudaSuccess) e = cudaFuncSetAttribute(tdp_xattn_simt_dkv_kernel<BF16, DP>, attr, (int)kDkv);
+        if (e == cudaSuccess && dev < 64) done[dev].store(true, std::memory_order_relaxed);
+        return e;
+    }
+    static cudaError_t forward(const tdp_geom &g, const xattn_args &a, cudaStream_t s)
+    {
+        cudaError_t e = prepare();
+        if (e == cudaSuccess)
+            e = tdp_launch_smem(true, tdp_xattn_simt_kernel<BF16, DP>, (unsigned)(a.segs * a.split * a.Hkv * a.blocks), kXT, kFwd, s, g, a);
+        return e;
+    }
+    static cudaError_t dq(const tdp_geom &g, const xattn_args &a, cudaStream_t s)
+    {
+        cudaError_t e = prepare();
+        if (e == cudaSuccess)
+            e = tdp_launch_smem(true, tdp_xattn_simt_dq_kernel<BF16, DP>, (unsigned)(a.segs * a.Hkv * a.blocks), kXT, kDq, s, g, a);
+        return e;
+    }
+    static cudaError_t dkv(const tdp_geom &g, const xattn_args &a, cudaStream_t s)
+    {
+        const unsigned grid = (unsigned)(g.B * a.split * a.Hkv * ((a.S + kXN - 1) / kXN));
+        return tdp_launch_smem(true, tdp_xattn_simt_dkv_kernel<BF16, DP>, grid, kXT, kDkv, s, g, a);
+    }
+};
+
+}  // namespace
+
+extern "C" tdp_status tdp_cross_attn_workspace(tdp_plan_t plan, const tdp_xattn *p, int32_t grad, int64_t *bytes)
+{
+    xattn_args a;
+    xattn_shape sh;
+    if (!bytes) return tdp_fail(TDP_ERR_INVALID_ARG, "null bytes");
+    const tdp_status st = xattn_check(plan, p, &a, &sh);
+    if (st != TDP_OK) return st;
+    *bytes = grad ? sh.grad_bytes : sh.fwd_bytes;
+    return tdp_ok();
+}
+
+extern "C" tdp_status tdp_cross_attn(tdp_plan_t plan, const tdp_xattn *p, const void *q, const void *k, const void *v,
+                                     const uint8_t *mask, void *out, float *lse, void *ws, int64_t ws_bytes,
+                                     tdp_stream_t stream)
+{
+    xattn_args a;
+    xattn_shape sh;
+    const tdp_status st = xattn_check(plan, p, &a, &sh);
+    if (st != TDP_OK) return st;
+    const tdp_geom &g = plan->g;
+    if (g.B == 0) return tdp_ok();
+    if (!q || !out || (a.S > 0 && (!k || !v)) || (sh.fwd_bytes > 0 && (!ws || ws_bytes < sh.fwd_bytes)))
+        return tdp_fail(TDP_ERR_INVALID_ARG, "null q, k, v or out, or ws too small");
+    if (!tdp_aligned(q, 16) || !tdp_aligned(k, 16) || !tdp_aligned(v, 16) || !tdp_aligned(out, 16) ||
+        !tdp_aligned(lse, 4) || !tdp_aligned(ws, 256))
+        return tdp_fail(TDP_ERR_MISALIGNED, "q, k, v and out need 16-byte, lse 4-byte, ws 256-byte alignment");
+    a.q = q;
+    a.k = k;
+    a.v = v;
+    a.mask = mask;
+    a.out = out;
+    a.lse = lse;
+    a.split = sh.fsplit;
+    a.part = sh.fpart;
+    a.pl = reinterpret_cast<float *>(ws);
+    a.po = a.pl + align256(sh.fsplit * a.rows * a.Hq * 4) / 4;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    cudaError_t err;
+    if (g.dtype == TDP_BF16)
+        err = a.D <= 64 ? simt_kernels<1, 64>::forward(g, a, s) : simt_kernels<1, 128>::forward(g, a, s);
+    else
+        err = a.D <= 64 ? simt_kernels<0, 64>::forward(g, a, s) : simt_kernels<0, 128>::forward(g, a, s);
+    if (err == cudaSuccess && a.split > 1) {
+        const unsigned grid = (unsigned)((a.rows * a.Hq * 32 + kXT - 1) / kXT);
+        err = g.dtype == TDP_BF16 ? tdp_launch(true, tdp_xattn_join_kernel<1>, grid, kXT, s, a)
+                                  : tdp_launch(true, tdp_xattn_join_kernel<0>, grid, kXT, s, a);
+    }
+    return err == cudaSuccess ? tdp_ok() : tdp_fail(TDP_ERR_CUDA, cudaGetErrorString(err));
+}
+
+extern "C" tdp_status tdp_cross_attn_grad(tdp_plan_t plan, const tdp_xattn *p, const void *q, const void *k,
+                                          const void *v, const uint8_t *mask, const void *out, const float *lse,
+                                          const void *dout, void *dq, void *dk, void *dv, void *ws, int64_t ws_bytes,
+                                          tdp_stream_t stream)
+{
+    xattn_args a;
+    xattn_shape sh;
+    const tdp_status st = xattn_check(plan, p, &a, &sh);
+    if (st != TDP_OK) return st;
+    const tdp_geom &g = plan->g;
+    if (g.B == 0) return tdp_ok();
+    if (!q || !out || !lse || !dout || !dq || (a.S > 0 && (!k || !v || !dk || !dv)) || !ws || ws_bytes < sh.grad_bytes)
+        return tdp_fail(TDP_ERR_INVALID_ARG, "null buffer, or ws too small");
+    if (!tdp_aligned(q, 16) || !tdp_aligned(k, 16) || !tdp_aligned(v, 16) || !tdp_aligned(out, 16) ||
+        !tdp_aligned(dout, 16) || !tdp_aligned(dq, 16) || !tdp_aligned(dk, 16) || !tdp_aligned(dv, 16) ||
+        !tdp_aligned(lse, 4) || !tdp_aligned(ws, 256))
+        return tdp_fail(TDP_ERR_MISALIGNED, "elements need 16-byte, lse 4-byte, ws 256-byte alignment");
+    a.q = q;
+    a.k = k;
+    a.v = v;
+    a.mask = mask;
+    a.o = out;
+    a.lse = const_cast<float *>(lse);
+    a.dout = dout;
+    a.dq = dq;
+    a.dk = dk;
+    a.dv = dv;
+    unsigned char *w = reinterpret_cast<unsigned char *>(ws);
+    a.delta = reinterpret_cast<float *>(w + sh.delta_at);
+    a.pk = reinterpret_cast<float *>(w + sh.pk_at);
+    a.pv = reinterpret_cast<float *>(w + sh.pv_at);
+    a.split = sh.bsplit;
+    a.part = sh.bpart;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    cudaError_t err;
+    if (g.dtype == TDP_BF16)
+        err = a.D <= 64 ? simt_kernels<1, 64>::dq(g, a, s) : simt_kernels<1, 128>::dq(g, a, s);
+    else
+        err = a.D <= 64 ? simt_kernels<0, 64>::dq(g, a, s) : simt_kernels<0, 128>::dq(g, a, s);
+    if (err == cudaSuccess && a.S > 0) {
+        if (g.dtype == TDP_BF16)
+            err = a.D <= 64 ? simt_kernels<1, 64>::dkv(g, a, s) : simt_kernels<1, 128>::dkv(g, a, s);
+        else
+            err = a.D <= 64 ? simt_kernels<0, 64>::dkv(g, a, s) : simt_kernels<0, 128>::dkv(g, a, s);
+        if (err == cudaSuccess && a.split > 1) {
+            const int64_t n = (int64_t)g.B * a.S * a.Hkv * a.D;
+            const unsigned grid = (unsigned)((2 * n / 4 + kXT - 1) / kXT);
+            err = g.dtype == TDP_BF16 ? tdp_launch(true, tdp_xattn_dkv_join_kernel<1>, grid, kXT, s, a, n)
+                                      : tdp_launch(true, tdp_xattn_dkv_join_kernel<0>, grid, kXT, s, a, n);
+        }
+    }
+    return err == cudaSuccess ? tdp_ok() : tdp_fail(TDP_ERR_CUDA, cudaGetErrorString(err));
+}

@@ -402,6 +402,150 @@ tdp_status tdp_blend_partial(tdp_plan_t plan, int32_t rank, int32_t world, const
  */
 tdp_status tdp_blend_store(tdp_plan_t plan, int64_t n, const float *Zsum, void *Z, tdp_stream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * Operators of the per-tile block.
+ *
+ * What a transformer block runs on the tiles between tdp_split and tdp_blend: each works
+ * on TILE-MAJOR ROWS, the layout of Y with any width: tile t holds B * T_t rows (item 0's
+ * T_t tokens, then item 1's, ...) from row B*off_t on, R = B * total_tile_tokens rows in
+ * all.  The plan gives B, the tiles' tokens and the dtype; its C is not used, so one plan
+ * serves the latent's channels and a block's wider rows.  A plan with one tile per
+ * dimension is an untiled batch [B, T].
+ *
+ * `ws` is a device workspace of at least the bytes the _workspace call of the same
+ * arguments gives, 256-byte aligned, owned by the caller, not initialised, free for reuse
+ * once the call's work has run (calls on one stream may share it).  Sums, softmax
+ * statistics and moments are held in fp32; results do not depend on the order in which
+ * blocks run.
+ * ------------------------------------------------------------------------- */
+
+/* Largest head dimension and most encoder states per item of tdp_cross_attn. */
+#define TDP_MAX_HEAD_DIM 128
+#define TDP_MAX_STATES (1 << 20)
+
+/* Shapes and strides of one cross attention.  Strides count elements; the head dimension
+ * is contiguous.  Every stride is a multiple of 16 bytes, and so is head_dim.  q_heads is a multiple
+ * of kv_heads: query head h reads key head h / (q_heads / kv_heads). */
+typedef struct {
+    int32_t q_heads, kv_heads;
+    int32_t head_dim;           /* D, at most TDP_MAX_HEAD_DIM */
+    int32_t states;             /* S, encoder states per batch item, at most TDP_MAX_STATES; may be 0 */
+    int32_t mask_per_tile;      /* nonzero: mask is [n_tiles, B, S]; zero: [B, S] */
+    float scale;                /* scores are scale * q.k */
+    int64_t q_row, q_head;                  /* q: from one tile-major row / head to the next */
+    int64_t k_item, k_state, k_head;        /* k: batch item, state, head */
+    int64_t v_item, v_state, v_head;        /* v */
+} tdp_xattn;
+
+/*
+ * tdp_cross_attn -- every tile's tokens attend to an encoder's states of another length.
+ *
+ * For row r of tile t and item b, head h, over the states s that the mask keeps:
+ *   p_s = exp(scale * q_r.k_s - lse_r),  out_r = sum_s p_s v_s,
+ *   lse_r = log sum_s exp(scale * q_r.k_s).
+ * A row that keeps no state gets out = 0 and lse = -infinity.  What k and v hold at a
+ * state no mask keeps (NaN and infinities too) has no effect; at a state that one
+ * tile's mask drops and another's keeps, it has none on the first.
+ *
+ *   q      device [R, q_heads, D] by q_row and q_head (plan dtype), read.
+ *   k, v   device [B, S, kv_heads, D] by their strides (plan dtype), read.
+ *   mask   device uint8 [B, S] or [n_tiles, B, S] (tdp_norm_filter's keep has the second
+ *          form), nonzero = kept; or NULL: every state is kept.
+ *   out    device [R, q_heads, D], contiguous (plan dtype), written.
+ *   lse    device fp32 [R, q_heads], written; or NULL.
+ *   ws     device workspace of tdp_cross_attn_workspace(plan, a, 0, ...) bytes.
+ * q, k, v and out must be 16-byte aligned; R * q_heads below 2^31.
+ * The first call on a device raises the kernels' shared-memory limits; make it before
+ * capturing a stream into a CUDA graph.
+ */
+tdp_status tdp_cross_attn_workspace(tdp_plan_t plan, const tdp_xattn *a, int32_t grad, int64_t *bytes);
+tdp_status tdp_cross_attn(tdp_plan_t plan, const tdp_xattn *a, const void *q, const void *k, const void *v,
+                          const uint8_t *mask, void *out, float *lse, void *ws, int64_t ws_bytes,
+                          tdp_stream_t stream);
+
+/*
+ * tdp_cross_attn_grad -- gradients of tdp_cross_attn.
+ *
+ * With p as above, delta_r = dout_r . out_r and ds = p * (dout_r . v_s - delta_r):
+ *   dq_r = scale * sum_s ds k_s,  dk_s = scale * sum ds q_r,  dv_s = sum p dout_r,
+ * the sums for dk and dv over all tiles, rows and the query heads that share the key head.
+ * States no mask keeps get dk = dv = 0, rows that keep no state dq = 0.
+ *
+ *   q, k, v, mask   as for tdp_cross_attn.
+ *   out, lse        device, from tdp_cross_attn with the same arguments, read.
+ *   dout            device [R, q_heads, D], contiguous, read.
+ *   dq              device [R, q_heads, D], contiguous, written.
+ *   dk, dv          device [B, S, kv_heads, D], contiguous, written.
+ *   ws              device workspace of tdp_cross_attn_workspace(plan, a, 1, ...) bytes.
+ */
+tdp_status tdp_cross_attn_grad(tdp_plan_t plan, const tdp_xattn *a, const void *q, const void *k, const void *v,
+                               const uint8_t *mask, const void *out, const float *lse, const void *dout, void *dq,
+                               void *dk, void *dv, void *ws, int64_t ws_bytes, tdp_stream_t stream);
+
+typedef enum { TDP_ACT_NONE = 0, TDP_ACT_SILU = 1 } tdp_act;
+
+/*
+ * tdp_group_norm -- group normalisation of each (tile, item), channels last, with an
+ * activation.
+ *
+ * Over the T_t tokens and the C/groups channels of each group of tile t, item b:
+ *   mean and rstd = 1/sqrt(var + eps) (biased variance),
+ *   z = (x - mean) * rstd * gamma_c + beta_c,  y = z (TDP_ACT_NONE) or z / (1 + exp(-z))
+ *   (TDP_ACT_SILU).
+ *
+ *   C, groups    channels per row (C * element size a multiple of 16) and groups (C % groups == 0).
+ *   x            device [R, C] tile-major rows (plan dtype), read.
+ *   gamma, beta  device [C] (plan dtype), read; or NULL: 1 and 0.
+ *   y            device [R, C] (plan dtype), written; may be x itself.
+ *   mean, rstd   device fp32 [n_tiles, B, groups], written.
+ */
+tdp_status tdp_group_norm_workspace(tdp_plan_t plan, int32_t C, int32_t groups, int64_t *bytes);
+tdp_status tdp_group_norm(tdp_plan_t plan, int32_t C, int32_t groups, float eps, int32_t act, const void *x,
+                          const void *gamma, const void *beta, void *y, float *mean, float *rstd, void *ws,
+                          int64_t ws_bytes, tdp_stream_t stream);
+
+/*
+ * tdp_group_norm_grad -- gradients of tdp_group_norm.
+ *
+ * With h = (x - mean) * rstd, z = h * gamma + beta and dz = dy * act'(z):
+ *   dgamma_c = sum dz * h,  dbeta_c = sum dz  over all tiles, items and tokens, and
+ *   dx = rstd * (g - mean(g) - h * mean(g * h)),  g = dz * gamma, means over the group.
+ *
+ *   x, gamma, beta   as for tdp_group_norm (x as it was before: not overwritten by y).
+ *   mean, rstd       device fp32 [n_tiles, B, groups] from tdp_group_norm, read.
+ *   dy               device [R, C] (plan dtype), read.
+ *   dx               device [R, C] (plan dtype), written; may be dy itself.
+ *   dgamma, dbeta    device fp32 [C], written; or both NULL.
+ */
+tdp_status tdp_group_norm_grad(tdp_plan_t plan, int32_t C, int32_t groups, int32_t act, const void *x,
+                               const void *gamma, const void *beta, const float *mean, const float *rstd,
+                               const void *dy, void *dx, float *dgamma, float *dbeta, void *ws, int64_t ws_bytes,
+                               tdp_stream_t stream);
+
+/*
+ * tdp_dropout_add, tdp_dropout_grad -- residual plus dropout from a counter-based
+ * generator, and its gradient; the mask is computed in registers and never stored.
+ *
+ * Element i has word i % 4 of Philox4x32-10 (Salmon, Moraes, Dror, Shaw, "Parallel random
+ * numbers: as easy as 1, 2, 3", 2011) with counter {i/4 low, i/4 high, rng[1] low, rng[1]
+ * high} and key {rng[0] low, rng[0] high} (32-bit words).  It is kept when the word is at
+ * least round(p * 2^32):
+ *   out_i = res_i + (kept ? x_i / (1 - p) : 0),   dx_i = kept ? dout_i / (1 - p) : 0.
+ * The gradient of the residual is dout itself.  A dropped element's x or dout (NaN too) has no effect.
+ *
+ *   n        elements (>= 0, any number).   p  in [0, 1]; p = 1 drops every element.
+ *   rng      device uint64 [2], seed and offset, read when the kernel runs: a captured CUDA
+ *            graph draws a new mask when the caller has changed them.
+ *   x, res   device [n] (plan dtype), read; res may be NULL (no residual).
+ *   out      device [n] (plan dtype), written; may be x or res itself.
+ *   dout, dx device [n] (plan dtype); dx may be dout itself.
+ * Pointers to elements must be 16-byte aligned, rng 8-byte.
+ */
+tdp_status tdp_dropout_add(tdp_plan_t plan, int64_t n, double p, const uint64_t *rng, const void *x, const void *res,
+                           void *out, tdp_stream_t stream);
+tdp_status tdp_dropout_grad(tdp_plan_t plan, int64_t n, double p, const uint64_t *rng, const void *dout, void *dx,
+                            tdp_stream_t stream);
+
 /*
  * Plan helpers (host only, no CUDA call).
  *
