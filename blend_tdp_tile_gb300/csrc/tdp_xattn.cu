@@ -13,6 +13,7 @@
 
 #include "tdp.h"
 #include "tdp_xattn.h"
+#include "tdp_xattn_tc.cuh"
 
 namespace {
 
@@ -479,15 +480,36 @@ tdp_xattn_dkv_join_kernel(const xattn_args a, int64_t n)
 
 constexpr int kSplitMax = 64;
 constexpr int kFill = 304;      // blocks below which the work is split: two for each SM
+constexpr int kSMs = 152;       // what splits are chosen for
 
 int64_t align256(int64_t x) { return (x + 255) / 256 * 256; }
 
-// The launch's shape: segments, row blocks, parts, workspace.
+// The launches' shapes and the workspace's layout.
 struct xattn_shape {
+    int64_t mask_rows, kept_bytes;          // bf16: lists of kept state tiles
     int64_t fwd_bytes, grad_bytes;
-    int64_t delta_at, pk_at, pv_at;
-    int32_t fsplit, fpart, bsplit, bpart;
+    int64_t pl_at, po_at;                   // forward
+    int64_t delta_at, pk_at, pv_at;         // gradient
+    int32_t fblocks, fsplit, fpart;
+    int32_t bsplit, bpart;
 };
+
+// Parts of `tiles` state tiles for `items` row blocks: as many as make the device's rounds of
+// blocks, each as long as its tiles and about two more of setting up, take the least time.
+int32_t split_states(int64_t items, int64_t tiles)
+{
+    if (items == 0 || items >= kSMs || tiles < 2) return 1;
+    int64_t best = 0;
+    int32_t split = 1;
+    for (int32_t s = 1; s <= std::min<int64_t>(kSplitMax, tiles); ++s) {
+        const int64_t cost = (items * s + kSMs - 1) / kSMs * ((tiles + s - 1) / s + 2) + (s > 1 ? 3 : 0);
+        if (s == 1 || cost < best) {
+            best = cost;
+            split = s;
+        }
+    }
+    return split;
+}
 
 tdp_status xattn_check(tdp_plan_t plan, const tdp_xattn *p, xattn_args *a, xattn_shape *sh)
 {
@@ -505,7 +527,11 @@ tdp_status xattn_check(tdp_plan_t plan, const tdp_xattn *p, xattn_args *a, xattn
     for (int64_t s : strides) {
         if (s < 0) return tdp_fail(TDP_ERR_INVALID_ARG, "strides must not be negative");
         if (s % V != 0) return tdp_fail(TDP_ERR_MISALIGNED, "strides must be multiples of 16 bytes");
+        if (s >= ((int64_t)1 << 38)) return tdp_fail(TDP_ERR_TOO_LARGE, "strides must be below 2^38 elements");
     }
+    if ((p->q_row == 0 && (int64_t)g.B * g.total > 1) || (p->q_head == 0 && p->q_heads > 1) ||
+        ((p->k_state == 0 || p->v_state == 0) && p->states > 1))
+        return tdp_fail(TDP_ERR_INVALID_ARG, "rows, query heads and states cannot be broadcast (stride 0)");
     *a = xattn_args{};
     a->q_row = p->q_row;
     a->q_head = p->q_head;
@@ -528,17 +554,31 @@ tdp_status xattn_check(tdp_plan_t plan, const tdp_xattn *p, xattn_args *a, xattn
     const int64_t T = a->flat ? a->rows : tdp_max_tile_tokens(g);
     if (a->rows > 0x7fffffffLL / a->Hq) return tdp_fail(TDP_ERR_TOO_LARGE, "rows * q_heads must be below 2^31");
     a->blocks = (int32_t)((T * a->G + kXM - 1) / kXM);
-    const int64_t tiles = (a->S + kXN - 1) / kXN;
+    const bool bf16 = g.dtype == TDP_BF16;
+    const int64_t tiles = (a->S + kXN - 1) / kXN, tiles128 = (a->S + tdp_xt::kKeys - 1) / tdp_xt::kKeys;
     const int64_t grid = (int64_t)a->segs * a->Hkv * a->blocks, kvgrid = (int64_t)g.B * a->Hkv * tiles;
     if (grid * kSplitMax > 0x7fffffffLL || kvgrid * kSplitMax > 0x7fffffffLL || (int64_t)a->segs * a->blocks > 0x7fffffffLL)
         return tdp_fail(TDP_ERR_TOO_LARGE, "cross attention grid too large");
-    // few row blocks: the states in parts of four tiles or more, few enough to fill the device
+    sh->mask_rows = a->per_tile ? (int64_t)g.nt * g.B : g.B;
+    sh->kept_bytes = bf16 ? align256(sh->mask_rows * tiles128 * 16) + align256(sh->mask_rows * tiles128 * 4) + align256(sh->mask_rows * 4) : 0;
     sh->fsplit = 1;
     sh->fpart = (int32_t)std::max<int64_t>(tiles, 1);
-    if (grid > 0 && grid < kFill && tiles > 4) {
-        const int64_t want = std::min<int64_t>({kSplitMax, (kFill + grid - 1) / grid, tiles / 4});
-        sh->fpart = (int32_t)((tiles + want - 1) / want);
-        sh->fsplit = (int32_t)((tiles + sh->fpart - 1) / sh->fpart);
+    if (bf16) {
+        a->Gp = std::min(a->G, 128);
+        while (a->G % a->Gp != 0) --a->Gp;
+        a->TT = 128 / a->Gp;
+        sh->fblocks = (int32_t)((T + 2 * a->TT - 1) / (2 * a->TT));
+        const int64_t items = (int64_t)a->segs * (a->Hq / a->Gp) * sh->fblocks;
+        if (items * kSplitMax > 0x7fffffffLL) return tdp_fail(TDP_ERR_TOO_LARGE, "cross attention grid too large");
+        sh->fsplit = split_states(items, tiles128);
+    } else {
+        // few row blocks: the states in parts of four tiles or more, few enough to fill the device
+        sh->fblocks = a->blocks;
+        if (grid > 0 && grid < kFill && tiles > 4) {
+            const int64_t want = std::min<int64_t>({kSplitMax, (kFill + grid - 1) / grid, tiles / 4});
+            sh->fpart = (int32_t)((tiles + want - 1) / want);
+            sh->fsplit = (int32_t)((tiles + sh->fpart - 1) / sh->fpart);
+        }
     }
     // few state tiles: the row blocks in parts
     const int64_t units = (int64_t)(a->flat ? 1 : g.nt) * a->blocks;
@@ -550,12 +590,100 @@ tdp_status xattn_check(tdp_plan_t plan, const tdp_xattn *p, xattn_args *a, xattn
         sh->bsplit = (int32_t)((units + sh->bpart - 1) / sh->bpart);
     }
     const int64_t rh = a->rows * a->Hq, kv = (int64_t)g.B * a->S * a->Hkv * a->D;
-    sh->fwd_bytes = sh->fsplit > 1 ? align256(sh->fsplit * rh * 4) + sh->fsplit * rh * a->D * 4 : 0;
-    sh->delta_at = 0;
-    sh->pk_at = align256(rh * 4);
+    sh->pl_at = sh->kept_bytes;
+    sh->po_at = sh->pl_at + (sh->fsplit > 1 ? align256(sh->fsplit * rh * 4) : 0);
+    sh->fwd_bytes = sh->po_at + (sh->fsplit > 1 ? sh->fsplit * rh * a->D * 4 : 0);
+    sh->delta_at = sh->kept_bytes;
+    sh->pk_at = sh->delta_at + align256(rh * 4);
     sh->pv_at = sh->pk_at + (sh->bsplit > 1 ? align256(sh->bsplit * kv * 4) : 0);
     sh->grad_bytes = sh->pv_at + (sh->bsplit > 1 ? sh->bsplit * kv * 4 : 0);
     return TDP_OK;
+}
+
+// Multiprocessors of the current device, asked once.
+int sm_count()
+{
+    static std::atomic<int> count[64];
+    int dev = 0, n = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return kSMs;
+    if (dev < 64 && (n = count[dev].load(std::memory_order_relaxed)) > 0) return n;
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 1) return kSMs;
+    if (dev < 64) count[dev].store(n, std::memory_order_relaxed);
+    return n;
+}
+
+// Raise a kernel's dynamic shared-memory limit once per device (`done`: one flag each).
+template <typename K>
+cudaError_t allow_smem(K kernel, size_t bytes, std::atomic<bool> *done)
+{
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess || (dev < 64 && done[dev].load(std::memory_order_relaxed))) return e;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    if (e == cudaSuccess && dev < 64) done[dev].store(true, std::memory_order_relaxed);
+    return e;
+}
+
+// bf16: the lists of kept tiles, then the product kernel.
+cudaError_t tc_kept(const xattn_shape &sh, xattn_args *a, unsigned char *ws, cudaStream_t s)
+{
+    const int64_t tiles = (a->S + tdp_xt::kKeys - 1) / tdp_xt::kKeys;
+    a->kept_words = reinterpret_cast<uint4 *>(ws);
+    a->kept_tile = reinterpret_cast<int32_t *>(ws + align256(sh.mask_rows * tiles * 16));
+    a->kept_n = reinterpret_cast<int32_t *>(ws + align256(sh.mask_rows * tiles * 16) + align256(sh.mask_rows * tiles * 4));
+    if (!a->mask) return cudaSuccess;
+    const unsigned threads = (unsigned)std::min<int64_t>(1024, 32 * std::max<int64_t>(tiles, 1));
+    return tdp_launch(true, tdp_xt::tdp_xattn_kept_kernel, (unsigned)sh.mask_rows, threads, s, a->mask, a->S, a->kept_n, a->kept_tile, a->kept_words);
+}
+
+// Tensor map of bf16 rows: `dims` extents from the contiguous one on, strides and box of them.  A dimension of
+// one, or one that is broadcast (stride 0), has the smallest stride a map takes and is read at coordinate 0.
+bool tc_map(CUtensorMap *map, const void *p, int dims, const int64_t *extent, const int64_t *stride, const int64_t *box)
+{
+    PFN_cuTensorMapEncodeTiled_v12000 encode = tdp_encode_tiled();
+    if (!encode) return false;
+    cuuint64_t e[5], st[4];
+    cuuint32_t b[5], one[5];
+    for (int i = 0; i < dims; ++i) {
+        e[i] = i > 0 && stride[i] == 0 ? 1 : (cuuint64_t)std::max<int64_t>(extent[i], 1);
+        b[i] = (cuuint32_t)box[i];
+        one[i] = 1;
+        if (i > 0) st[i - 1] = (cuuint64_t)(stride[i] > 0 ? stride[i] * 2 : 16);
+    }
+    return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (cuuint32_t)dims, const_cast<void *>(p), e, st, b, one,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Maps of q-like rows [R, Hq, D] (a tile: Gp heads of TT tokens) and of states [B, S, Hkv, D] (128 states of a head).
+bool tc_row_map(CUtensorMap *map, const void *p, const xattn_args &a, int64_t row, int64_t head)
+{
+    const int64_t extent[3] = {a.D, a.Hq, a.rows}, stride[3] = {1, head, row}, box[3] = {64, a.Gp, a.TT};
+    return tc_map(map, p, 3, extent, stride, box);
+}
+bool tc_state_map(CUtensorMap *map, const void *p, const tdp_geom &g, const xattn_args &a, int64_t item, int64_t state, int64_t head)
+{
+    const int64_t extent[4] = {a.D, a.Hkv, a.S, g.B}, stride[4] = {1, head, state, item}, box[4] = {64, 1, tdp_xt::kKeys, 1};
+    return tc_map(map, p, 4, extent, stride, box);
+}
+
+template <int DP>
+cudaError_t tc_forward(const tdp_geom &g, const xattn_args &a, cudaStream_t s)
+{
+    static std::atomic<bool> done[64];
+    constexpr size_t bytes = tdp_xt::fwd_smem<DP>::kBytes;
+    cudaError_t e = allow_smem(tdp_xt::tdp_xattn_tc_kernel<DP>, bytes, done);
+    CUtensorMap q, k, v;
+    // with no states the kernel loads nothing: q stands in for the maps of k and v
+    if (e == cudaSuccess &&
+        (!tc_row_map(&q, a.q, a, a.q_row, a.q_head) ||
+         !tc_state_map(&k, a.S > 0 ? a.k : a.q, g, a, a.k_item, a.k_state, a.k_head) ||
+         !tc_state_map(&v, a.S > 0 ? a.v : a.q, g, a, a.v_item, a.v_state, a.v_head)))
+        e = cudaErrorInvalidValue;
+    const int32_t items = a.segs * a.split * (a.Hq / a.Gp) * a.blocks;
+    if (e == cudaSuccess)
+        e = tdp_launch_smem(true, tdp_xt::tdp_xattn_tc_kernel<DP>, (unsigned)std::min(items, sm_count()), tdp_xt::kThreads, bytes, s, g, a, q, k, v, items);
+    return e;
 }
 
 template <int BF16, int DP>
@@ -634,14 +762,18 @@ extern "C" tdp_status tdp_cross_attn(tdp_plan_t plan, const tdp_xattn *p, const 
     a.lse = lse;
     a.split = sh.fsplit;
     a.part = sh.fpart;
-    a.pl = reinterpret_cast<float *>(ws);
-    a.po = a.pl + align256(sh.fsplit * a.rows * a.Hq * 4) / 4;
+    a.blocks = sh.fblocks;
+    unsigned char *w = reinterpret_cast<unsigned char *>(ws);
+    a.pl = reinterpret_cast<float *>(w + sh.pl_at);
+    a.po = reinterpret_cast<float *>(w + sh.po_at);
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     cudaError_t err;
-    if (g.dtype == TDP_BF16)
-        err = a.D <= 64 ? simt_kernels<1, 64>::forward(g, a, s) : simt_kernels<1, 128>::forward(g, a, s);
-    else
+    if (g.dtype == TDP_BF16) {
+        err = tc_kept(sh, &a, w, s);
+        if (err == cudaSuccess) err = a.D <= 64 ? tc_forward<64>(g, a, s) : tc_forward<128>(g, a, s);
+    } else {
         err = a.D <= 64 ? simt_kernels<0, 64>::forward(g, a, s) : simt_kernels<0, 128>::forward(g, a, s);
+    }
     if (err == cudaSuccess && a.split > 1) {
         const unsigned grid = (unsigned)((a.rows * a.Hq * 32 + kXT - 1) / kXT);
         err = g.dtype == TDP_BF16 ? tdp_launch(true, tdp_xattn_join_kernel<1>, grid, kXT, s, a)

@@ -17,17 +17,22 @@ struct xattn_args {
     void *out, *dq, *dk, *dv;
     float *lse;                 // written by the forward (may be NULL), read by the gradient
     float *delta;               // [R, Hq] gradient: dout . out
+    int32_t *kept_n;            // bf16: [mask rows] kept 128-state tiles, their indexes and the masks of their states
+    int32_t *kept_tile;         //       [mask rows, tiles]
+    uint4 *kept_words;          //       [mask rows, tiles]
     float *po, *pl;             // forward split over states: partial out [split][R, Hq, D] and lse [split][R, Hq]
     float *pk, *pv;             // gradient split over rows: partial dk, dv [split][B, S, Hkv, D]
     int64_t q_row, q_head, k_item, k_state, k_head, v_item, v_state, v_head;
     int64_t rows;               // R
     int32_t Hq, Hkv, G, D, S;
+    // bf16: rows of a 128-row tile are Gp query heads of TT = 128 / Gp tokens, Gp the largest divisor of G up to 128
+    int32_t Gp, TT;
     int32_t flat;               // all tiles are one segment
     int32_t per_tile;           // mask row per segment, else per item
     int32_t segs;               // segments
     int32_t blocks;             // row blocks of the largest segment
     int32_t split;              // parts the states (forward) or the row blocks (dk, dv) are split into
-    int32_t part;               // 64-state tiles (forward) or row blocks (dk, dv) of a part
+    int32_t part;               // fp32: 64-state tiles (forward) or row blocks (dk, dv) of a part
     float scale;
 };
 

@@ -424,8 +424,9 @@ tdp_status tdp_blend_store(tdp_plan_t plan, int64_t n, const float *Zsum, void *
 #define TDP_MAX_STATES (1 << 20)
 
 /* Shapes and strides of one cross attention.  Strides count elements; the head dimension
- * is contiguous.  Every stride is a multiple of 16 bytes, and so is head_dim.  q_heads is a multiple
- * of kv_heads: query head h reads key head h / (q_heads / kv_heads). */
+ * is contiguous.  Every stride is a multiple of 16 bytes and below 2^38 elements, and so is head_dim; the
+ * item and head strides of k and v may be 0 (one item's or head's states for all), and a dimension of one ignores
+ * its stride.  q_heads is a multiple of kv_heads: query head h reads key head h / (q_heads / kv_heads). */
 typedef struct {
     int32_t q_heads, kv_heads;
     int32_t head_dim;           /* D, at most TDP_MAX_HEAD_DIM */
@@ -443,6 +444,7 @@ typedef struct {
  * For row r of tile t and item b, head h, over the states s that the mask keeps:
  *   p_s = exp(scale * q_r.k_s - lse_r),  out_r = sum_s p_s v_s,
  *   lse_r = log sum_s exp(scale * q_r.k_s).
+ * (Should a kernel's own wait run out, it gives up and fills its outputs with NaN.)
  * A row that keeps no state gets out = 0 and lse = -infinity.  What k and v hold at a
  * state no mask keeps (NaN and infinities too) has no effect; at a state that one
  * tile's mask drops and another's keeps, it has none on the first.

@@ -33,7 +33,8 @@ def _lib(tdp):
     (dict(scale=float("nan")), 1), (dict(scale=float("inf")), 1), (dict(k_state=-128), 1),
     (dict(head_dim=136), 5), (dict(states=(1 << 20) + 1), 5),
     (dict(head_dim=60), 4), (dict(q_row=252), 4), (dict(v_head=1), 4), (dict(k_item=2), 4),
-    (dict(q_heads=1 << 24, kv_heads=1 << 23), 5),
+    (dict(q_heads=1 << 24, kv_heads=1 << 23), 5), (dict(k_item=1 << 38), 5),
+    (dict(q_row=0), 1), (dict(q_head=0), 1), (dict(k_state=0), 1), (dict(v_state=0), 1),
 ])
 def test_cross_attn_shapes_refused(tdp, kw, status):  # noqa: F811
     n = ctypes.c_int64()
