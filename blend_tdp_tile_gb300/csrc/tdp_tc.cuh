@@ -37,10 +37,22 @@ __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity)
     return done != 0;
 }
 
+// This warp's number, uniform to the compiler.
+__device__ __forceinline__ int32_t warp_id() { return __shfl_sync(~0u, (int)(threadIdx.x >> 5), 0); }
+// One lane of a converged warp.  The tensor-core and tensor-map instructions take uniform registers: behind elect.sync
+// the compiler knows that one lane runs, behind a lane number it wraps each of them in a loop over the lanes
+// (2 KB and 75 cycles a product instead of 64).
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t on;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(on));
+    return on != 0;
+}
+
 // Wait for phase `parity`; false when the rounds ran out here or (`dead`) in another thread.
 __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int *dead)
 {
-    if (mbar_try(bar, parity)) return true;
+#pragma unroll 1
     for (uint32_t i = 0; i < kWaitRounds; ++i) {
         if (mbar_try(bar, parity)) return true;
         if (*dead) return false;
@@ -68,6 +80,23 @@ __device__ __forceinline__ void tma_load4(uint32_t dst, const CUtensorMap *map, 
         "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst),
         "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z), "r"(w)
         : "memory");
+}
+// Shared -> box of a tensor map; commit, then wait until the shared side has been read or all is done.
+__device__ __forceinline__ void tma_store3(const CUtensorMap *map, uint32_t src, int32_t x, int32_t y, int32_t z)
+{
+    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
+                     reinterpret_cast<uint64_t>(map)),
+                 "r"(src), "r"(x), "r"(y), "r"(z)
+                 : "memory");
+    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+__device__ __forceinline__ void tma_store_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+__device__ __forceinline__ void tma_store_done() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+// Barrier of one warpgroup.
+__device__ __forceinline__ void group_sync(int id) { asm volatile("bar.sync %0, 128;" ::"r"(id) : "memory"); }
+__device__ __forceinline__ void st_shared16(uint32_t dst, const uint32_t *r)
+{
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]) : "memory");
 }
 __device__ __forceinline__ void st_zero16(uint32_t dst)
 {
@@ -98,6 +127,20 @@ __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::aft
 __device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
+// Ties the 32 registers of a load to the point behind its wait: what uses them is not moved before it.
+__device__ __forceinline__ void tmem_have32(uint32_t *r)
+{
+    asm volatile("" : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]),
+                 "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]),
+                 "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]), "+r"(r[24]),
+                 "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]));
+    asm volatile("" : "+r"(r[30]), "+r"(r[31]));
+}
+__device__ __forceinline__ void tmem_have16(uint32_t *r)
+{
+    asm volatile("" : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]),
+                 "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]));
+}
 // 32 columns of this warp's 32 lanes, one lane a thread.
 __device__ __forceinline__ void tmem_ld32(uint32_t addr, uint32_t *r)
 {

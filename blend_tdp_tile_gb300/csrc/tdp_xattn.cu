@@ -571,6 +571,11 @@ tdp_status xattn_check(tdp_plan_t plan, const tdp_xattn *p, xattn_args *a, xattn
         const int64_t items = (int64_t)a->segs * (a->Hq / a->Gp) * sh->fblocks;
         if (items * kSplitMax > 0x7fffffffLL) return tdp_fail(TDP_ERR_TOO_LARGE, "cross attention grid too large");
         sh->fsplit = split_states(items, tiles128);
+        a->by_heads = fast_div_by(a->Hq / a->Gp);
+        a->by_group = fast_div_by(a->G);
+        a->by_B = fast_div_by(std::max(g.B, 1));
+        a->by_nH = fast_div_by(g.d[1].n);
+        a->by_nW = fast_div_by(g.d[2].n);
     } else {
         // few row blocks: the states in parts of four tiles or more, few enough to fill the device
         sh->fblocks = a->blocks;
@@ -673,16 +678,16 @@ cudaError_t tc_forward(const tdp_geom &g, const xattn_args &a, cudaStream_t s)
     static std::atomic<bool> done[64];
     constexpr size_t bytes = tdp_xt::fwd_smem<DP>::kBytes;
     cudaError_t e = allow_smem(tdp_xt::tdp_xattn_tc_kernel<DP>, bytes, done);
-    CUtensorMap q, k, v;
+    CUtensorMap q, k, v, o;
     // with no states the kernel loads nothing: q stands in for the maps of k and v
     if (e == cudaSuccess &&
-        (!tc_row_map(&q, a.q, a, a.q_row, a.q_head) ||
+        (!tc_row_map(&q, a.q, a, a.q_row, a.q_head) || !tc_row_map(&o, a.out, a, (int64_t)a.Hq * a.D, a.D) ||
          !tc_state_map(&k, a.S > 0 ? a.k : a.q, g, a, a.k_item, a.k_state, a.k_head) ||
          !tc_state_map(&v, a.S > 0 ? a.v : a.q, g, a, a.v_item, a.v_state, a.v_head)))
         e = cudaErrorInvalidValue;
     const int32_t items = a.segs * a.split * (a.Hq / a.Gp) * a.blocks;
     if (e == cudaSuccess)
-        e = tdp_launch_smem(true, tdp_xt::tdp_xattn_tc_kernel<DP>, (unsigned)std::min(items, sm_count()), tdp_xt::kThreads, bytes, s, g, a, q, k, v, items);
+        e = tdp_launch_smem(true, tdp_xt::tdp_xattn_tc_kernel<DP>, (unsigned)std::min(items, sm_count()), tdp_xt::kThreads, bytes, s, g, a, q, k, v, o, items);
     return e;
 }
 
@@ -763,6 +768,8 @@ extern "C" tdp_status tdp_cross_attn(tdp_plan_t plan, const tdp_xattn *p, const 
     a.split = sh.fsplit;
     a.part = sh.fpart;
     a.blocks = sh.fblocks;
+    a.by_blocks = fast_div_by(a.blocks);
+    a.by_split = fast_div_by(a.split);
     unsigned char *w = reinterpret_cast<unsigned char *>(ws);
     a.pl = reinterpret_cast<float *>(w + sh.pl_at);
     a.po = reinterpret_cast<float *>(w + sh.po_at);

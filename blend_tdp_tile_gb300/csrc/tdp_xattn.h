@@ -9,6 +9,32 @@
 #include "tdp_internal.h"
 #include "tdp_rows.cuh"
 
+// Division of n < 2^31 by a constant: q = n * mul >> shift, mul = ceil(2^shift / d), shift = 31 + ceil(log2 d) (T. Granlund,
+// P. Montgomery, "Division by invariant integers using multiplication", PLDI 1994).  The kernels decode a work item in
+// every role; the divide instruction sequence took longer than an output tile.
+struct fast_div {
+    uint32_t mul;
+    int32_t shift, d;
+    __device__ __forceinline__ int32_t div(int32_t n) const { return (int32_t)(((uint64_t)(uint32_t)n * mul) >> shift); }
+    // n becomes the quotient; the remainder is returned
+    __device__ __forceinline__ int32_t mod(int32_t &n) const
+    {
+        const int32_t q = div(n), r = n - q * d;
+        n = q;
+        return r;
+    }
+};
+static inline fast_div fast_div_by(int32_t d)
+{
+    int32_t s = 0;
+    while (((int64_t)1 << s) < d) ++s;
+    fast_div f;
+    f.d = d;
+    f.shift = 31 + s;
+    f.mul = (uint32_t)((((uint64_t)1 << f.shift) + d - 1) / d);
+    return f;
+}
+
 struct xattn_args {
     const void *q, *k, *v;
     const uint8_t *mask;
@@ -27,6 +53,7 @@ struct xattn_args {
     int32_t Hq, Hkv, G, D, S;
     // bf16: rows of a 128-row tile are Gp query heads of TT = 128 / Gp tokens, Gp the largest divisor of G up to 128
     int32_t Gp, TT;
+    fast_div by_blocks, by_heads, by_split, by_B, by_nH, by_nW, by_group;      // head blocks: Hq / Gp; by_group: G
     int32_t flat;               // all tiles are one segment
     int32_t per_tile;           // mask row per segment, else per item
     int32_t segs;               // segments
@@ -47,6 +74,27 @@ __device__ __forceinline__ tdp_seg xattn_seg(const tdp_geom &g, const xattn_args
         return r;
     }
     return tdp_seg_at(g, s);
+}
+
+// The same by multiplications (bf16 kernels).
+__device__ __forceinline__ tdp_seg xattn_seg_fast(const tdp_geom &g, const xattn_args &a, int32_t s)
+{
+    tdp_seg r;
+    if (a.flat) {
+        r.row0 = 0;
+        r.T = a.rows;
+        r.t = r.b = 0;
+        return r;
+    }
+    r.b = a.by_B.mod(s);
+    r.t = s;
+    const int32_t iW = a.by_nW.mod(s), iH = a.by_nH.mod(s), iF = s;
+    const int64_t SF = g.d[0].hi[iF] - g.d[0].lo[iF];
+    const int64_t SH = g.d[1].hi[iH] - g.d[1].lo[iH];
+    const int64_t SW = g.d[2].hi[iW] - g.d[2].lo[iW];
+    r.T = SF * SH * SW;
+    r.row0 = (int64_t)g.B * tdp_tile_off(g, iF, iH, iW) + (int64_t)r.b * r.T;
+    return r;
 }
 
 __device__ __forceinline__ const uint8_t *xattn_mask(const xattn_args &a, const tdp_geom &g, const tdp_seg &seg)
