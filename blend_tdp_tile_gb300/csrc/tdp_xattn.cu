@@ -13,7 +13,7 @@
 
 #include "tdp.h"
 #include "tdp_xattn.h"
-#include "tdp_xattn_tc.cuh"
+#include "tdp_xattn_grad_tc.cuh"
 
 namespace {
 
@@ -491,7 +491,7 @@ struct xattn_shape {
     int64_t pl_at, po_at;                   // forward
     int64_t delta_at, pk_at, pv_at;         // gradient
     int32_t fblocks, fsplit, fpart;
-    int32_t bsplit, bpart;
+    int32_t bblocks, bsplit, bpart;
 };
 
 // Parts of `tiles` state tiles for `items` row blocks: as many as make the device's rounds of
@@ -503,6 +503,24 @@ int32_t split_states(int64_t items, int64_t tiles)
     int32_t split = 1;
     for (int32_t s = 1; s <= std::min<int64_t>(kSplitMax, tiles); ++s) {
         const int64_t cost = (items * s + kSMs - 1) / kSMs * ((tiles + s - 1) / s + 2) + (s > 1 ? 3 : 0);
+        if (s == 1 || cost < best) {
+            best = cost;
+            split = s;
+        }
+    }
+    return split;
+}
+
+// Parts of the row blocks of a state tile (dk, dv; bf16): the device's rounds of blocks, each as long as its
+// row tiles and about three more, against the parts' way through memory (16 bytes an element written and read,
+// in row-tile times of 1.1 us).
+int64_t split_rows(int64_t base, int64_t units, int64_t heads, int64_t elements)
+{
+    int64_t split = 1;
+    double best = 0.;
+    for (int64_t s = 1; s <= std::min<int64_t>(kSplitMax, units); ++s) {
+        const double cost = (double)((base * s + kSMs - 1) / kSMs) * (double)((units + s - 1) / s * heads + 3) +
+                            (s > 1 ? (double)s * (double)elements * 2.1e-6 + 3. : 0.);
         if (s == 1 || cost < best) {
             best = cost;
             split = s;
@@ -560,7 +578,7 @@ tdp_status xattn_check(tdp_plan_t plan, const tdp_xattn *p, xattn_args *a, xattn
     if (grid * kSplitMax > 0x7fffffffLL || kvgrid * kSplitMax > 0x7fffffffLL || (int64_t)a->segs * a->blocks > 0x7fffffffLL)
         return tdp_fail(TDP_ERR_TOO_LARGE, "cross attention grid too large");
     sh->mask_rows = a->per_tile ? (int64_t)g.nt * g.B : g.B;
-    sh->kept_bytes = bf16 ? align256(sh->mask_rows * tiles128 * 16) + align256(sh->mask_rows * tiles128 * 4) + align256(sh->mask_rows * 4) : 0;
+    sh->kept_bytes = bf16 ? 2 * align256(sh->mask_rows * tiles128 * 16) + align256(sh->mask_rows * tiles128 * 4) + align256(sh->mask_rows * 4) : 0;
     sh->fsplit = 1;
     sh->fpart = (int32_t)std::max<int64_t>(tiles, 1);
     if (bf16) {
@@ -586,10 +604,17 @@ tdp_status xattn_check(tdp_plan_t plan, const tdp_xattn *p, xattn_args *a, xattn
         }
     }
     // few state tiles: the row blocks in parts
-    const int64_t units = (int64_t)(a->flat ? 1 : g.nt) * a->blocks;
+    sh->bblocks = bf16 ? (int32_t)((T + a->TT - 1) / a->TT) : a->blocks;
+    const int64_t units = (int64_t)(a->flat ? 1 : g.nt) * sh->bblocks;
     sh->bsplit = 1;
     sh->bpart = (int32_t)std::max<int64_t>(units, 1);
-    if (kvgrid > 0 && kvgrid < kFill && units > 1) {
+    if (bf16) {
+        const int64_t base = (int64_t)g.B * a->Hkv * tiles128, hbs = a->G / a->Gp;
+        if (units > 0x7fffffffLL || base * kSplitMax > 0x7fffffffLL) return tdp_fail(TDP_ERR_TOO_LARGE, "cross attention grid too large");
+        const int64_t s = split_rows(base, units, hbs, (int64_t)g.B * a->S * a->Hkv * a->D);
+        sh->bpart = (int32_t)std::max<int64_t>((units + s - 1) / s, 1);
+        sh->bsplit = (int32_t)std::max<int64_t>((units + sh->bpart - 1) / sh->bpart, 1);
+    } else if (kvgrid > 0 && kvgrid < kFill && units > 1) {
         const int64_t want = std::min<int64_t>({kSplitMax, (kFill + kvgrid - 1) / kvgrid, units});
         sh->bpart = (int32_t)((units + want - 1) / want);
         sh->bsplit = (int32_t)((units + sh->bpart - 1) / sh->bpart);
@@ -636,9 +661,10 @@ cudaError_t tc_kept(const xattn_shape &sh, xattn_args *a, unsigned char *ws, cud
     a->kept_words = reinterpret_cast<uint4 *>(ws);
     a->kept_tile = reinterpret_cast<int32_t *>(ws + align256(sh.mask_rows * tiles * 16));
     a->kept_n = reinterpret_cast<int32_t *>(ws + align256(sh.mask_rows * tiles * 16) + align256(sh.mask_rows * tiles * 4));
+    a->state_words = reinterpret_cast<uint4 *>(ws + sh.kept_bytes - align256(sh.mask_rows * tiles * 16));
     if (!a->mask) return cudaSuccess;
     const unsigned threads = (unsigned)std::min<int64_t>(1024, 32 * std::max<int64_t>(tiles, 1));
-    return tdp_launch(true, tdp_xt::tdp_xattn_kept_kernel, (unsigned)sh.mask_rows, threads, s, a->mask, a->S, a->kept_n, a->kept_tile, a->kept_words);
+    return tdp_launch(true, tdp_xt::tdp_xattn_kept_kernel, (unsigned)sh.mask_rows, threads, s, a->mask, a->S, a->kept_n, a->kept_tile, a->kept_words, a->state_words);
 }
 
 // Tensor map of bf16 rows: `dims` extents from the contiguous one on, strides and box of them.  A dimension of
@@ -688,6 +714,29 @@ cudaError_t tc_forward(const tdp_geom &g, const xattn_args &a, cudaStream_t s)
     const int32_t items = a.segs * a.split * (a.Hq / a.Gp) * a.blocks;
     if (e == cudaSuccess)
         e = tdp_launch_smem(true, tdp_xt::tdp_xattn_tc_kernel<DP>, (unsigned)std::min(items, sm_count()), tdp_xt::kThreads, bytes, s, g, a, q, k, v, o, items);
+    return e;
+}
+
+template <int DP>
+cudaError_t tc_grad(const tdp_geom &g, const xattn_args &a, cudaStream_t s)
+{
+    static std::atomic<bool> done_q[64], done_kv[64];
+    constexpr size_t bytes_q = tdp_xt::dq_smem<DP>::kBytes, bytes_kv = tdp_xt::dkv_smem<DP>::kBytes;
+    cudaError_t e = allow_smem(tdp_xt::tdp_xattn_dq_kernel<DP>, bytes_q, done_q);
+    if (e == cudaSuccess) e = allow_smem(tdp_xt::tdp_xattn_dkv_kernel<DP>, bytes_kv, done_kv);
+    CUtensorMap q, o, d, k, v;
+    const int64_t row = (int64_t)a.Hq * a.D;
+    if (e == cudaSuccess &&
+        (!tc_row_map(&q, a.q, a, a.q_row, a.q_head) || !tc_row_map(&o, a.o, a, row, a.D) || !tc_row_map(&d, a.dout, a, row, a.D) ||
+         !tc_state_map(&k, a.S > 0 ? a.k : a.q, g, a, a.k_item, a.k_state, a.k_head) ||
+         !tc_state_map(&v, a.S > 0 ? a.v : a.q, g, a, a.v_item, a.v_state, a.v_head)))
+        e = cudaErrorInvalidValue;
+    const int32_t items = a.segs * (a.Hq / a.Gp) * a.blocks;
+    if (e == cudaSuccess)
+        e = tdp_launch_smem(true, tdp_xt::tdp_xattn_dq_kernel<DP>, (unsigned)std::min(items, sm_count()), tdp_xt::kThreads, bytes_q, s, g, a, q, o, d, k, v, items);
+    const unsigned grid = (unsigned)(g.B * a.split * a.Hkv * ((a.S + tdp_xt::kKeys - 1) / tdp_xt::kKeys));
+    if (e == cudaSuccess && a.S > 0)
+        e = tdp_launch_smem(true, tdp_xt::tdp_xattn_dkv_kernel<DP>, grid, tdp_xt::kThreads, bytes_kv, s, g, a, q, d, k, v);
     return e;
 }
 
@@ -824,15 +873,16 @@ extern "C" tdp_status tdp_cross_attn_grad(tdp_plan_t plan, const tdp_xattn *p, c
     a.part = sh.bpart;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     cudaError_t err;
-    if (g.dtype == TDP_BF16)
-        err = a.D <= 64 ? simt_kernels<1, 64>::dq(g, a, s) : simt_kernels<1, 128>::dq(g, a, s);
-    else
+    if (g.dtype == TDP_BF16) {
+        a.blocks = sh.bblocks;
+        a.by_blocks = fast_div_by(a.blocks);
+        err = tc_kept(sh, &a, w, s);
+        if (err == cudaSuccess) err = a.D <= 64 ? tc_grad<64>(g, a, s) : tc_grad<128>(g, a, s);
+    } else {
         err = a.D <= 64 ? simt_kernels<0, 64>::dq(g, a, s) : simt_kernels<0, 128>::dq(g, a, s);
+        if (err == cudaSuccess && a.S > 0) err = a.D <= 64 ? simt_kernels<0, 64>::dkv(g, a, s) : simt_kernels<0, 128>::dkv(g, a, s);
+    }
     if (err == cudaSuccess && a.S > 0) {
-        if (g.dtype == TDP_BF16)
-            err = a.D <= 64 ? simt_kernels<1, 64>::dkv(g, a, s) : simt_kernels<1, 128>::dkv(g, a, s);
-        else
-            err = a.D <= 64 ? simt_kernels<0, 64>::dkv(g, a, s) : simt_kernels<0, 128>::dkv(g, a, s);
         if (err == cudaSuccess && a.split > 1) {
             const int64_t n = (int64_t)g.B * a.S * a.Hkv * a.D;
             const unsigned grid = (unsigned)((2 * n / 4 + kXT - 1) / kXT);

@@ -46,6 +46,7 @@ struct xattn_args {
     int32_t *kept_n;            // bf16: [mask rows] kept 128-state tiles, their indexes and the masks of their states
     int32_t *kept_tile;         //       [mask rows, tiles]
     uint4 *kept_words;          //       [mask rows, tiles]
+    uint4 *state_words;         //       masks of every tile's states [mask rows, tiles] (gradient)
     float *po, *pl;             // forward split over states: partial out [split][R, Hq, D] and lse [split][R, Hq]
     float *pk, *pv;             // gradient split over rows: partial dk, dv [split][B, S, Hkv, D]
     int64_t q_row, q_head, k_item, k_state, k_head, v_item, v_state, v_head;

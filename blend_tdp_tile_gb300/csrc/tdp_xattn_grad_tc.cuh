@@ -1,0 +1,756 @@
+// tdp_xattn_grad_tc.cuh -- gradients of the bf16 cross attention on the tensor cores (tcgen05).
+//
+// Two kernels compute p = exp2(c s - lse) again.  The first walks the kept state tiles for each tile of
+// 128 packed rows:   S = Q K^T, dP = dO V^T,  dS = p (dP - delta),  dQ += dS K,
+// and writes delta = dO . O for the second, which walks the row tiles for each tile of 128 states:
+//   S^T = K Q^T, dP^T = V dO^T,  dV += P^T dO,  dK += dS^T Q.
+// Seven products where a single kernel would have five, but dK and dV then need no atomics and no
+// exchange between blocks: a split over the rows writes fp32 parts that are joined in order.
+// In both, scores and their gradients live in tensor memory; two warpgroups share the columns of a tile (each
+// thread a lane and 64 columns) and write p and dS back as bf16 in place, as the next product's A operand:
+//   warps 0-3, 4-7   columns 0-63, 64-127; the output
+//   warp 8           loads tiles through tensor maps
+//   warp 9           issues the products
+//   warp 10          second kernel: each row's lse and delta
+//   warp 11          zeroes rows of a tile that must not count (their memory may hold anything, and 0 * NaN is not 0)
+#pragma once
+
+#include "tdp_xattn_tc.cuh"
+
+namespace tdp_xt {
+
+template <int DP>
+struct dq_smem {
+    static constexpr int kTile = 128 * DP * 2;
+    static constexpr int kStages = DP == 128 ? 4 : 8;       // even: a stage always holds K, or always V
+    static constexpr int kBytes = 1024 + (3 + kStages) * kTile + 512 + 1024;
+};
+
+template <int DP>
+struct dkv_smem {
+    static constexpr int kTile = 128 * DP * 2;
+    static constexpr int kStages = DP == 128 ? 4 : 8;       // even: a stage always holds Q, or always dO
+    static constexpr int kStats = 4;                        // row tiles of lse and delta
+    static constexpr int kBytes = 1024 + (2 + kStages) * kTile + kStats * 1024 + 512;
+};
+
+// Item of the first kernel: a segment's tile of TT tokens, a head block, all kept state tiles.
+__device__ __forceinline__ item dq_item_at(const tdp_geom &g, const xattn_args &a, int32_t w)
+{
+    item it;
+    const int32_t blk = a.by_blocks.mod(w);
+    it.head = a.by_heads.mod(w) * a.Gp;
+    it.kvh = a.by_group.div(it.head);
+    it.part = 0;
+    it.seg = xattn_seg_fast(g, a, w);
+    it.tok0 = (int64_t)blk * a.TT;
+    it.left = (int32_t)(it.seg.T - it.tok0);
+    const int32_t tiles = (a.S + kKeys - 1) / kKeys;
+    it.keys.S = a.S;
+    it.keys.tile = nullptr;
+    it.keys.words = nullptr;
+    it.keys.j0 = 0;
+    it.keys.n = tiles;
+    if (a.mask) {
+        const int64_t m = a.per_tile ? (int64_t)it.seg.t * g.B + it.seg.b : it.seg.b;
+        it.keys.n = __ldg(a.kept_n + m);
+        it.keys.tile = a.kept_tile + m * tiles;
+        it.keys.words = a.kept_words + m * tiles;
+    }
+    return it;
+}
+
+// log2 of the row's sum; a row with no sum gets +inf, which makes its probabilities zero.
+__device__ __forceinline__ float row_lse2(float lse) { return lse == -INFINITY ? INFINITY : lse * kLog2e; }
+
+template <int DP>
+__global__ void __launch_bounds__(kThreads, 1)
+tdp_xattn_dq_kernel(const __grid_constant__ tdp_geom g, const __grid_constant__ xattn_args a,
+                    const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_o,
+                    const __grid_constant__ CUtensorMap map_do, const __grid_constant__ CUtensorMap map_k,
+                    const __grid_constant__ CUtensorMap map_v, int32_t items)
+{
+    using SM = dq_smem<DP>;
+    using T = __nv_bfloat16;
+    constexpr int NST = SM::kStages;
+    extern __shared__ unsigned char raw[];
+    const uint32_t base = (smem_u32(raw) + 1023u) & ~1023u;
+    const uint32_t q_s = base, do_s = q_s + SM::kTile, o_s = do_s + SM::kTile, kv_s = o_s + SM::kTile,
+                   bars = kv_s + NST * SM::kTile, sums = bars + 512;
+    const uint32_t full = bars, empty = full + 8 * NST, clean = empty + 8 * NST, rfull = clean + 8 * NST, rempty = rfull + 24,
+                   sfull = rempty + 24, pfull = sfull + 16, dsfull = pfull + 8, done = dsfull + 8, drain = done + 8;
+    __shared__ uint32_t tmem_slot;
+    __shared__ int dead_flag;
+    volatile int *dead = &dead_flag;
+    const int32_t warp = warp_id(), lane = threadIdx.x & 31;
+    if (warp == 9) tmem_alloc(smem_u32(&tmem_slot), 512);
+    if (threadIdx.x == 0) {
+        dead_flag = 0;
+        for (int i = 0; i < NST; ++i) {
+            mbar_init(full + 8 * i, 1);
+            mbar_init(empty + 8 * i, 1);
+            mbar_init(clean + 8 * i, 1);
+        }
+        // row tiles: Q, dO, O; dO is given back by the products and by the warps that have read it for delta
+        for (int i = 0; i < 3; ++i) {
+            mbar_init(rfull + 8 * i, 1);
+            mbar_init(rempty + 8 * i, i == 0 ? 1 : i == 1 ? 9 : 8);
+        }
+        mbar_init(sfull, 1);
+        mbar_init(sfull + 8, 1);
+        mbar_init(pfull, 1);
+        mbar_init(dsfull, 8);
+        mbar_init(done, 1);
+        mbar_init(drain, 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    fence_before();
+    __syncthreads();
+    fence_after();
+    const uint32_t tm = tmem_slot;              // S: columns 0-127 and 128-255, taking turns; dP 256-383; dQ 384-
+    tdp_pdl_trigger();
+    tdp_pdl_wait();
+
+    bool ok = true;
+    uint32_t kv = 0, n_done = 0;                // K and V tiles and state tiles so far
+    uint32_t ph = 0;                            // phase of the per-item barriers
+    if (warp < 8) {
+        regs_inc<216>();
+        const int32_t half = warp >> 2, r = threadIdx.x & 127, rt = r / a.Gp, rh = r - rt * a.Gp;
+        const uint32_t lanes = tm + ((uint32_t)(warp & 3) << 21);
+        const float c = a.scale * kLog2e;
+        for (int32_t w = blockIdx.x; w < items; w += gridDim.x) {
+            const item it = dq_item_at(g, a, w);
+            const int32_t n = it.keys.n;
+            if (it.left <= 0) continue;
+            const bool mine = rt < a.TT && rt < it.left;
+            const int32_t h = ((int32_t)(it.seg.row0 + it.tok0) + rt) * a.Hq + it.head + rh;
+            if (n > 0) {
+                const float lse2 = mine ? row_lse2(a.lse[h]) : INFINITY;
+                // delta: each thread half of a row's products, the halves joined through shared memory
+                ok = ok && mbar_wait(rfull + 8, ph & 1, dead) && mbar_wait(rfull + 16, ph & 1, dead);
+                ph ^= 1;
+                float delta = 0.f;
+#pragma unroll
+                for (int i = 0; i < DP / 16; ++i) {
+                    const int32_t col = half * (DP / 16) + i;       // 16-byte chunk
+                    const uint32_t off = (col / 8) * 16384 + panel_off(r, col & 7);
+                    uint4 x, y;
+                    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w) : "r"(o_s + off));
+                    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(y.x), "=r"(y.y), "=r"(y.z), "=r"(y.w) : "r"(do_s + off));
+                    float fx[8], fy[8];
+                    tdp_elem<1>::unpack(x, fx);
+                    tdp_elem<1>::unpack(y, fy);
+#pragma unroll
+                    for (int u = 0; u < 8; ++u) delta = fmaf(fx[u], fy[u], delta);
+                }
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(rempty + 8);
+                    mbar_arrive(rempty + 16);
+                }
+                asm volatile("st.shared.f32 [%0], %1;" ::"r"(sums + 512 * half + 4 * r), "f"(delta) : "memory");
+                asm volatile("bar.sync 1, 256;" ::: "memory");
+                float other;
+                asm volatile("ld.shared.f32 %0, [%1];" : "=f"(other) : "r"(sums + 512 * (half ^ 1) + 4 * r));
+                asm volatile("bar.sync 1, 256;" ::: "memory");
+                delta = half ? other + delta : delta + other;
+                if (mine && half == 0) a.delta[h] = delta;
+                const uint64_t c2 = pair(c, c), l2 = pair(-lse2, -lse2), d2 = pair(-delta, -delta);
+#pragma unroll 1
+                for (int32_t j = 0; j < n && ok; ++j) {
+                    const uint32_t buf = n_done & 1, S = lanes + 128 * buf + 64 * half, P = lanes + 256 + 64 * half;
+                    const uint4 mk = it.keys.mask(j);
+                    ok = mbar_wait(sfull + 8 * buf, (n_done >> 1) & 1, dead) && mbar_wait(pfull, n_done & 1, dead);
+                    ++n_done;
+                    fence_after();
+                    uint32_t s[64], d[64];
+                    tmem_ld32(S, s);
+                    tmem_ld32(S + 32, s + 32);
+                    tmem_ld32(P, d);
+                    tmem_ld32(P + 32, d + 32);
+                    tmem_wait_ld();
+                    tmem_have32(s);
+                    tmem_have32(s + 32);
+                    tmem_have32(d);
+                    tmem_have32(d + 32);
+#pragma unroll
+                    for (int u = 0; u < 32; ++u) {
+                        float x, y;
+                        unpair(fma2(pair(__uint_as_float(s[2 * u]), __uint_as_float(s[2 * u + 1])), c2, l2), x, y);
+                        const uint64_t p = pair(exp2_fast(x), exp2_fast(y));
+                        unpair(mul2(p, add2(pair(__uint_as_float(d[2 * u]), __uint_as_float(d[2 * u + 1])), d2)), x, y);
+                        s[2 * u] = __float_as_uint(x);
+                        s[2 * u + 1] = __float_as_uint(y);
+                    }
+                    if (!whole(mk)) {
+                        const uint32_t w0 = half ? mk.z : mk.x, w1 = half ? mk.w : mk.y;
+#pragma unroll
+                        for (int u = 0; u < 32; ++u) {
+                            if (!((w0 >> u) & 1)) s[u] = 0;
+                            if (!((w1 >> u) & 1)) s[32 + u] = 0;
+                        }
+                    }
+                    // dS as bf16 over this half's scores
+#pragma unroll
+                    for (int v = 0; v < 2; ++v) {
+                        uint32_t b[16];
+#pragma unroll
+                        for (int u = 0; u < 16; ++u)
+                            b[u] = tdp_pack_bf16x2(__uint_as_float(s[32 * v + 2 * u]), __uint_as_float(s[32 * v + 2 * u + 1]));
+                        tmem_st16(S + 16 * v, b);
+                    }
+                    tmem_wait_st();
+                    fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(dsfull);
+                }
+                if (ok) ok = mbar_wait(done, (ph & 1) ^ 1, dead);
+                fence_after();
+            } else if (mine && half == 0) {
+                a.delta[h] = 0.f;
+            }
+            // dQ, half of the columns each; a lost wait leaves NaN
+            T *dst = static_cast<T *>(a.dq) + (int64_t)h * a.D;
+            const float f = ok ? a.scale : NAN;
+            const bool wide = a.D % 16 == 0 && (reinterpret_cast<uintptr_t>(a.dq) & 31) == 0;      // whole sectors
+#pragma unroll 1
+            for (int i = half * (DP / 64); i < (half + 1) * (DP / 64); ++i) {
+                uint32_t o[32];
+                if (n > 0) {
+                    tmem_ld32(lanes + 384 + 32 * i, o);
+                    tmem_wait_ld();
+                    tmem_have32(o);
+                } else {
+#pragma unroll
+                    for (int u = 0; u < 32; ++u) o[u] = 0;
+                }
+                uint32_t b[16];
+#pragma unroll
+                for (int u = 0; u < 16; ++u) b[u] = tdp_pack_bf16x2(__uint_as_float(o[2 * u]) * f, __uint_as_float(o[2 * u + 1]) * f);
+                if (mine) {
+                    if (wide) {
+#pragma unroll
+                        for (int u = 0; u < 16; u += 8)
+                            if (32 * i + 2 * u < a.D) st_global32(dst + 32 * i + 2 * u, b + u);
+                    } else {
+#pragma unroll
+                        for (int u = 0; u < 16; u += 4)
+                            if (32 * i + 2 * u < a.D) *reinterpret_cast<uint4 *>(dst + 32 * i + 2 * u) = make_uint4(b[u], b[u + 1], b[u + 2], b[u + 3]);
+                    }
+                }
+                __syncwarp();
+            }
+            fence_before();
+        }
+    } else {
+        regs_dec<72>();
+        for (int32_t w = blockIdx.x; w < items; w += gridDim.x) {
+            const item it = dq_item_at(g, a, w);
+            const int32_t n = it.keys.n;
+            if (it.left <= 0 || n == 0 || !ok) continue;
+            if (warp == 8) {
+                const int32_t row = (int32_t)(it.seg.row0 + it.tok0);
+                auto load_row = [&](const CUtensorMap *map, int i) {
+                    if (!(ok = ok && mbar_wait(rempty + 8 * i, (ph & 1) ^ 1, dead))) return;
+                    if (elect_one()) {
+                        mbar_expect(rfull + 8 * i, (uint32_t)(a.Gp * a.TT) * DP * 2);
+                        for (int p = 0; p < DP / 64; ++p)
+                            tma_load3(base + i * SM::kTile + p * 16384, map, rfull + 8 * i, 64 * p, it.head, row);
+                    }
+                    __syncwarp();
+                };
+#pragma unroll 1
+                for (int32_t i = 0; i < 2 * n && ok; ++i) {
+                    const bool v = i & 1;
+                    const uint32_t st = kv % NST;
+                    const int32_t head = (v ? a.v_head : a.k_head) > 0 ? it.kvh : 0, b = (v ? a.v_item : a.k_item) > 0 ? it.seg.b : 0;
+                    const int32_t state = it.keys.at(i >> 1) * kKeys;
+                    if (i == 0) load_row(&map_q, 0);
+                    if (i == 1) load_row(&map_do, 1);
+                    if (!(ok = ok && mbar_wait(empty + 8 * st, ((kv / NST) & 1) ^ 1, dead))) break;
+                    ++kv;
+                    if (elect_one()) {
+                        mbar_expect(full + 8 * st, SM::kTile);
+                        for (int p = 0; p < DP / 64; ++p)
+                            tma_load4(kv_s + st * SM::kTile + p * 16384, v ? &map_v : &map_k, full + 8 * st, 64 * p, head, state, b);
+                    }
+                    __syncwarp();
+                    if (i == 1) load_row(&map_o, 2);
+                }
+                ph ^= 1;
+            } else if (warp == 9) {
+                constexpr uint32_t id_s = idesc(128, 128, false, false), id_q = idesc(128, DP, false, true);
+                const uint32_t q_d = desc_rows(q_s), do_d = desc_rows(do_s);
+                const uint32_t k_full = a.mask ? clean : full;          // K comes by way of the cleaning warp where there is a mask
+                // product of two row-major tiles over the head dimension
+                auto rows = [&](uint32_t d, uint32_t x, uint32_t y) {
+#pragma unroll
+                    for (int i = 0; i < DP / 16; ++i) {
+                        mma_ss(d, x, y, id_s, i > 0);
+                        const uint32_t m = i % 4 == 3 ? (16384 - 96) >> 4 : 2;
+                        x += m;
+                        y += m;
+                    }
+                };
+                // round j: S of state tile j + 1 ahead, then dP of j + 1 and dQ of j once dS of j is there
+#pragma unroll 1
+                for (int32_t j = -1; j < n; ++j) {
+                    const uint32_t k0 = (kv + 2 * j) % NST, k1 = (kv + 2 * j + 2) % NST, v1 = k1 + 1;
+                    const uint32_t kph = ((kv + 2 * j + 2) / NST) & 1;
+                    const uint32_t s1 = tm + 128 * ((n_done + j + 1) & 1);
+                    if (j + 1 < n) {
+                        if (j < 0 && !(ok = mbar_wait(rfull, ph & 1, dead))) break;
+                        if (!(ok = mbar_wait(k_full + 8 * k1, kph, dead))) break;
+                        if (elect_one()) {
+                            rows(s1, q_d, desc_rows(kv_s + k1 * SM::kTile));
+                            mma_commit(sfull + 8 * ((n_done + j + 1) & 1));
+                            if (j + 2 == n) mma_commit(rempty);
+                        }
+                        __syncwarp();
+                    }
+                    if (j >= 0) {
+                        if (!(ok = mbar_wait(dsfull, (n_done + j) & 1, dead))) break;
+                        fence_after();
+                    }
+                    if (j + 1 < n) {
+                        if (j < 0 && !(ok = mbar_wait(rfull + 8, ph & 1, dead))) break;
+                        if (!(ok = mbar_wait(full + 8 * v1, kph, dead))) break;
+                        if (elect_one()) {
+                            rows(tm + 256, do_d, desc_rows(kv_s + v1 * SM::kTile));
+                            mma_commit(pfull);
+                            mma_commit(empty + 8 * v1);
+                            if (j + 2 == n) mma_commit(rempty + 8);
+                        }
+                        __syncwarp();
+                    }
+                    if (j >= 0) {
+                        const uint32_t ds = tm + 128 * ((n_done + j) & 1), y = desc_cols(kv_s + k0 * SM::kTile, 16384);
+                        if (elect_one()) {
+#pragma unroll
+                            for (int i = 0; i < 8; ++i)
+                                mma_ts(tm + 384, ds + 64 * (i / 4) + 8 * (i % 4), y + i * (2048 >> 4), id_q, j > 0 || i > 0);
+                            mma_commit(empty + 8 * k0);
+                            if (j + 1 == n) mma_commit(done);
+                        }
+                        __syncwarp();
+                    }
+                }
+                ph ^= 1;
+                kv += 2 * n;
+                n_done += n;
+            } else if (warp == 11 && a.mask) {
+#pragma unroll 1
+                for (int32_t j = 0; j < n; ++j) {
+                    const uint4 m = it.keys.mask(j);
+                    const uint32_t st = (kv + 2 * j) % NST;
+                    if (!(ok = mbar_wait(full + 8 * st, ((kv + 2 * j) / NST) & 1, dead))) break;
+                    constexpr int C = DP / 8;           // 16-byte chunks of a row
+#pragma unroll 1
+                    for (int32_t i = whole(m) ? 128 * C : lane; i < 128 * C; i += 32) {
+                        const int32_t row = i / C, col = i % C;
+                        const uint32_t word = row < 64 ? (row < 32 ? m.x : m.y) : (row < 96 ? m.z : m.w);
+                        if (!((word >> (row & 31)) & 1))
+                            st_zero16(kv_s + st * SM::kTile + (col / 8) * 16384 + panel_off(row, col & 7));
+                    }
+                    fence_async();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(clean + 8 * st);
+                }
+                kv += 2 * n;
+            }
+        }
+    }
+    // nothing may land, or be on its way, after the block has gone
+    auto landed = [&](uint32_t bar, uint32_t parity) {
+#pragma unroll 1
+        for (uint32_t i = 0; i < kWaitRounds && !mbar_try(bar, parity); ++i) {
+        }
+    };
+    if (warp == 8) {
+        for (uint32_t i = kv > NST ? kv - NST : 0; i < kv; ++i) landed(full + 8 * (i % NST), (i / NST) & 1);
+        for (int i = 0; i < 3; ++i) landed(rfull + 8 * i, (ph & 1) ^ 1);
+    } else if (warp == 9) {
+        if (elect_one()) mma_commit(drain);
+        __syncwarp();
+        landed(drain, 0);
+    }
+    __syncwarp();
+    fence_before();
+    __syncthreads();
+    if (warp == 9) tmem_free(tm, 512);
+}
+
+// Walk over the row tiles of one batch item that meet a tile of states: the part's units [u, last), unit u = block
+// u % blocks of the item's segment u / blocks.
+struct row_walk {
+    int32_t u, last, cur;
+    tdp_seg seg;
+    int64_t tok0;
+    int32_t left;                   // tokens from tok0 on
+    uint4 words;                    // kept states of the tile
+    __device__ __forceinline__ bool next(const tdp_geom &g, const xattn_args &a, int32_t b, int32_t tile)
+    {
+        while (u < last) {
+            const int32_t sg = a.by_blocks.div(u);
+            if (sg != cur) {
+                cur = sg;
+                seg = xattn_seg_fast(g, a, sg * g.B + b);
+                if (a.mask) {
+                    const int64_t m = a.per_tile ? (int64_t)seg.t * g.B + seg.b : seg.b;
+                    words = __ldg(a.state_words + m * ((a.S + kKeys - 1) / kKeys) + tile);
+                } else {
+                    key_list k;
+                    k.tile = nullptr;
+                    k.words = nullptr;
+                    k.j0 = tile;
+                    k.S = a.S;
+                    words = k.mask(0);
+                }
+            }
+            tok0 = (int64_t)(u - sg * a.blocks) * a.TT;
+            left = (int32_t)(seg.T - tok0);
+            if (left <= 0 || (words.x | words.y | words.z | words.w) == 0) {
+                u = (sg + 1) * a.blocks;
+                continue;
+            }
+            ++u;
+            return true;
+        }
+        return false;
+    }
+};
+
+template <int DP>
+__global__ void __launch_bounds__(kThreads, 1)
+tdp_xattn_dkv_kernel(const __grid_constant__ tdp_geom g, const __grid_constant__ xattn_args a,
+                     const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_do,
+                     const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v)
+{
+    using SM = dkv_smem<DP>;
+    using T = __nv_bfloat16;
+    constexpr int NST = SM::kStages, NSS = SM::kStats;
+    extern __shared__ unsigned char raw[];
+    const uint32_t base = (smem_u32(raw) + 1023u) & ~1023u;
+    const uint32_t k_s = base, v_s = k_s + SM::kTile, r_s = v_s + SM::kTile, stat_s = r_s + NST * SM::kTile, bars = stat_s + NSS * 1024;
+    const uint32_t full = bars, empty = full + 8 * NST, clean = empty + 8 * NST, tfull = clean + 8 * NST, tempty = tfull + 8 * NSS,
+                   kvfull = tempty + 8 * NSS, sfull = kvfull + 8, dpfull = sfull + 8, pready = dpfull + 8, dsready = pready + 8,
+                   drain = dsready + 8;
+    __shared__ uint32_t tmem_slot;
+    __shared__ int dead_flag;
+    volatile int *dead = &dead_flag;
+    const int32_t warp = warp_id(), lane = threadIdx.x & 31;
+    if (warp == 9) tmem_alloc(smem_u32(&tmem_slot), 512);
+    if (threadIdx.x == 0) {
+        dead_flag = 0;
+        for (int i = 0; i < NST; ++i) {
+            mbar_init(full + 8 * i, 1);
+            mbar_init(empty + 8 * i, 1);
+            mbar_init(clean + 8 * i, 1);
+        }
+        for (int i = 0; i < NSS; ++i) {
+            mbar_init(tfull + 8 * i, 1);
+            mbar_init(tempty + 8 * i, 8);
+        }
+        mbar_init(kvfull, 1);
+        mbar_init(sfull, 1);
+        mbar_init(dpfull, 1);
+        mbar_init(pready, 8);
+        mbar_init(dsready, 8);
+        mbar_init(drain, 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    // rows of a tile past Gp * TT are never loaded: zero once
+    for (uint32_t i = threadIdx.x; i < NST * SM::kTile / 16; i += kThreads) st_zero16(r_s + 16 * i);
+    fence_async();
+    fence_before();
+    __syncthreads();
+    fence_after();
+    const uint32_t tm = tmem_slot;              // S^T 0-127, dP^T 128-255, dV 256-, dK 384-
+    tdp_pdl_trigger();
+    tdp_pdl_wait();
+
+    const int32_t tiles = (a.S + kKeys - 1) / kKeys;
+    int32_t w = blockIdx.x;
+    const int32_t tile = w % tiles;
+    w /= tiles;
+    const int32_t kvh = w % a.Hkv;
+    w /= a.Hkv;
+    const int32_t part = w % a.split, b = w / a.split;
+    const int32_t units = (a.flat ? 1 : g.nt) * a.blocks, hbs = a.G / a.Gp;     // head blocks that share the key head
+    row_walk wk;
+    wk.u = min(units, part * a.part);
+    wk.last = min(units, wk.u + a.part);
+    wk.cur = -1;
+
+    // every role walks the same row tiles, each for the head blocks in turn
+    bool ok = true, any = false;
+    uint32_t n = 0;                             // row tiles so far
+    if (warp < 8) {
+        regs_inc<216>();
+        const int32_t half = warp >> 2, r = threadIdx.x & 127;
+        const uint32_t lanes = tm + ((uint32_t)(warp & 3) << 21), S = lanes + 64 * half, P = lanes + 128 + 64 * half;
+        const float c = a.scale * kLog2e;
+        const uint64_t c2 = pair(c, c);
+        while (ok && wk.next(g, a, b, tile)) {
+            const uint32_t word = r < 64 ? (r < 32 ? wk.words.x : wk.words.y) : (r < 96 ? wk.words.z : wk.words.w);
+            const bool kept = (word >> lane) & 1;
+#pragma unroll 1
+            for (int32_t hb = 0; hb < hbs && ok; ++hb, ++n) {
+                const uint32_t ss = n % NSS, st = stat_s + ss * 1024 + 256 * half;
+                any = true;
+                ok = mbar_wait(tfull + 8 * ss, (n / NSS) & 1, dead) && mbar_wait(sfull, n & 1, dead);
+                fence_after();
+                uint32_t s[64], x32[32];
+                tmem_ld32(S, s);
+                tmem_ld32(S + 32, s + 32);
+                tmem_wait_ld();
+                tmem_have32(s);
+                tmem_have32(s + 32);
+                // p, kept in registers for dS; as bf16 over this half's scores
+#pragma unroll
+                for (int v = 0; v < 2; ++v) {
+#pragma unroll
+                    for (int u = 0; u < 8; ++u) {
+                        uint64_t l0, l1;
+                        float p0, p1, p2, p3;
+                        asm volatile("ld.shared.v2.b64 {%0, %1}, [%2];" : "=l"(l0), "=l"(l1) : "r"(st + 128 * v + 16 * u));
+                        uint32_t *q = s + 32 * v + 4 * u;
+                        unpair(fma2(pair(__uint_as_float(q[0]), __uint_as_float(q[1])), c2, l0), p0, p1);
+                        unpair(fma2(pair(__uint_as_float(q[2]), __uint_as_float(q[3])), c2, l1), p2, p3);
+                        p0 = kept ? exp2_fast(p0) : 0.f;
+                        p1 = kept ? exp2_fast(p1) : 0.f;
+                        p2 = kept ? exp2_fast(p2) : 0.f;
+                        p3 = kept ? exp2_fast(p3) : 0.f;
+                        q[0] = __float_as_uint(p0);
+                        q[1] = __float_as_uint(p1);
+                        q[2] = __float_as_uint(p2);
+                        q[3] = __float_as_uint(p3);
+                        x32[2 * u] = tdp_pack_bf16x2(p0, p1);
+                        x32[2 * u + 1] = tdp_pack_bf16x2(p2, p3);
+                    }
+                    tmem_st16(S + 16 * v, x32);
+                }
+                tmem_wait_st();
+                fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(pready);
+                ok = ok && mbar_wait(dpfull, n & 1, dead);
+                fence_after();
+#pragma unroll
+                for (int v = 0; v < 2; ++v) {
+                    uint32_t b16[16];
+                    tmem_ld32(P + 32 * v, x32);
+                    tmem_wait_ld();
+                    tmem_have32(x32);
+#pragma unroll
+                    for (int u = 0; u < 8; ++u) {
+                        uint64_t d0, d1;
+                        float y0, y1, y2, y3;
+                        asm volatile("ld.shared.v2.b64 {%0, %1}, [%2];" : "=l"(d0), "=l"(d1) : "r"(st + 512 + 128 * v + 16 * u));
+                        const uint32_t *q = s + 32 * v + 4 * u, *d = x32 + 4 * u;
+                        unpair(mul2(pair(__uint_as_float(q[0]), __uint_as_float(q[1])), add2(pair(__uint_as_float(d[0]), __uint_as_float(d[1])), d0)), y0, y1);
+                        unpair(mul2(pair(__uint_as_float(q[2]), __uint_as_float(q[3])), add2(pair(__uint_as_float(d[2]), __uint_as_float(d[3])), d1)), y2, y3);
+                        b16[2 * u] = kept ? tdp_pack_bf16x2(y0, y1) : 0u;      // a dropped state's dP may be NaN
+                        b16[2 * u + 1] = kept ? tdp_pack_bf16x2(y2, y3) : 0u;
+                    }
+                    tmem_st16(P + 16 * v, b16);
+                }
+                tmem_wait_st();
+                fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(dsready);
+                    mbar_arrive(tempty + 8 * ss);
+                }
+            }
+        }
+        if (ok) ok = mbar_wait(drain, 0, dead);
+        fence_after();
+        // first warpgroup dV, second dK
+        const int32_t state = tile * kKeys + r;
+        const int64_t at = (((int64_t)b * a.S + state) * a.Hkv + kvh) * a.D;
+        const float f = !ok ? NAN : half ? a.scale : 1.f;
+        float *pf = (half ? a.pk : a.pv) + (int64_t)part * g.B * a.S * a.Hkv * a.D + at;
+        T *pb = static_cast<T *>(half ? a.dk : a.dv) + at;
+#pragma unroll 1
+        for (int i = 0; i < DP / 32; ++i) {
+            uint32_t o[32];
+            if (any) {
+                tmem_ld32(lanes + 256 + 128 * half + 32 * i, o);
+                tmem_wait_ld();
+                tmem_have32(o);
+            } else {
+#pragma unroll
+                for (int u = 0; u < 32; ++u) o[u] = 0;
+            }
+#pragma unroll
+            for (int u = 0; u < 32; ++u) o[u] = __float_as_uint(__uint_as_float(o[u]) * f);
+            if (state < a.S) {
+#pragma unroll
+                for (int u = 0; u < 32; u += 8) {
+                    if (32 * i + u >= a.D) continue;
+                    if (a.split > 1) {
+                        st_global32(pf + 32 * i + u, o + u);
+                    } else {
+                        float y[8];
+#pragma unroll
+                        for (int x = 0; x < 8; ++x) y[x] = __uint_as_float(o[u + x]);
+                        *reinterpret_cast<uint4 *>(pb + 32 * i + u) = tdp_elem<1>::pack(y);
+                    }
+                }
+            }
+            __syncwarp();
+        }
+        fence_before();
+    } else {
+        regs_dec<72>();
+        uint32_t ti = 0;                        // Q and dO tiles so far
+        constexpr uint32_t id_s = idesc(128, 128, false, false), id_o = idesc(128, DP, false, true);
+        auto rows = [&](uint32_t d, uint32_t x, uint32_t y) {
+#pragma unroll
+            for (int i = 0; i < DP / 16; ++i) {
+                mma_ss(d, x, y, id_s, i > 0);
+                const uint32_t m = i % 4 == 3 ? (16384 - 96) >> 4 : 2;
+                x += m;
+                y += m;
+            }
+        };
+        // A from tensor memory, 64 columns of it at each half; B: a row tile read by columns
+        auto cols = [&](uint32_t d, uint32_t p, uint32_t y, bool acc) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) mma_ts(d, p + 64 * (i / 4) + 8 * (i % 4), y + i * (2048 >> 4), id_o, acc || i > 0);
+        };
+        if (warp == 8 && elect_one()) {
+            const int32_t kh = a.k_head > 0 ? kvh : 0, kb = a.k_item > 0 ? b : 0, vh = a.v_head > 0 ? kvh : 0, vb = a.v_item > 0 ? b : 0;
+            mbar_expect(kvfull, 2 * SM::kTile);
+            for (int p = 0; p < DP / 64; ++p) {
+                tma_load4(k_s + p * 16384, &map_k, kvfull, 64 * p, kh, tile * kKeys, kb);
+                tma_load4(v_s + p * 16384, &map_v, kvfull, 64 * p, vh, tile * kKeys, vb);
+            }
+        }
+        __syncwarp();
+        if (warp == 9) ok = mbar_wait(kvfull, 0, dead);
+        // warp 9 runs one tile behind itself: dK and dP of a tile come after S of the next
+        uint32_t q_prev = 0;
+        while (ok && wk.next(g, a, b, tile)) {
+#pragma unroll 1
+            for (int32_t hb = 0; hb < hbs && ok; ++hb, ++n) {
+                const int32_t head = kvh * a.G + hb * a.Gp, row = (int32_t)(wk.seg.row0 + wk.tok0);
+                if (warp == 8) {
+#pragma unroll 1
+                    for (int i = 0; i < 2; ++i) {
+                        const uint32_t st = ti % NST;
+                        if (!(ok = mbar_wait(empty + 8 * st, ((ti / NST) & 1) ^ 1, dead))) break;
+                        ++ti;
+                        if (elect_one()) {
+                            mbar_expect(full + 8 * st, (uint32_t)(a.Gp * a.TT) * DP * 2);
+                            for (int p = 0; p < DP / 64; ++p)
+                                tma_load3(r_s + st * SM::kTile + p * 16384, i ? &map_do : &map_q, full + 8 * st, 64 * p, head, row);
+                        }
+                        __syncwarp();
+                    }
+                } else if (warp == 9) {
+                    const uint32_t qs = ti % NST, ds = qs + 1, tph = (ti / NST) & 1;
+                    const uint32_t q_t = r_s + qs * SM::kTile, do_t = r_s + ds * SM::kTile;
+                    ti += 2;
+                    if (n > 0) {
+                        // dV of the tile before, whose probabilities lie in S
+                        if (!(ok = mbar_wait(pready, (n - 1) & 1, dead))) break;
+                        fence_after();
+                        if (elect_one()) {
+                            cols(tm + 256, tm, desc_cols(r_s + (q_prev + 1) * SM::kTile, 16384), n > 1);
+                            mma_commit(empty + 8 * (q_prev + 1));
+                        }
+                        __syncwarp();
+                    }
+                    if (!(ok = mbar_wait(clean + 8 * qs, tph, dead))) break;
+                    if (elect_one()) {
+                        rows(tm, desc_rows(k_s), desc_rows(q_t));
+                        mma_commit(sfull);
+                    }
+                    __syncwarp();
+                    if (n > 0) {
+                        // dK of the tile before, whose dS lies in dP
+                        if (!(ok = mbar_wait(dsready, (n - 1) & 1, dead))) break;
+                        fence_after();
+                        if (elect_one()) {
+                            cols(tm + 384, tm + 128, desc_cols(r_s + q_prev * SM::kTile, 16384), n > 1);
+                            mma_commit(empty + 8 * q_prev);
+                        }
+                        __syncwarp();
+                    }
+                    if (!(ok = mbar_wait(clean + 8 * ds, tph, dead))) break;
+                    if (elect_one()) {
+                        rows(tm + 128, desc_rows(v_s), desc_rows(do_t));
+                        mma_commit(dpfull);
+                    }
+                    __syncwarp();
+                    q_prev = qs;
+                } else if (warp == 10) {
+                    const uint32_t ss = n % NSS, dst = stat_s + ss * 1024;
+                    if (!(ok = mbar_wait(tempty + 8 * ss, ((n / NSS) & 1) ^ 1, dead))) break;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int32_t r = 32 * i + lane, rt = r / a.Gp;
+                        float l = -INFINITY, d = 0.f;
+                        if (rt < a.TT && rt < wk.left) {
+                            const int32_t h = (row + rt) * a.Hq + head + r - rt * a.Gp;
+                            l = -row_lse2(__ldg(a.lse + h));
+                            d = -__ldcg(a.delta + h);
+                        }
+                        asm volatile("st.shared.f32 [%0], %1;" ::"r"(dst + 4 * r), "f"(l) : "memory");
+                        asm volatile("st.shared.f32 [%0], %1;" ::"r"(dst + 512 + 4 * r), "f"(d) : "memory");
+                    }
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(tfull + 8 * ss);
+                } else {
+                    // rows past the segment's end belong to another tile
+                    const int32_t rows_in = min(wk.left, a.TT) * a.Gp, rows_all = a.TT * a.Gp;
+                    constexpr int C = DP / 8;
+#pragma unroll 1
+                    for (int i = 0; i < 2; ++i) {
+                        const uint32_t st = ti % NST;
+                        if (!(ok = mbar_wait(full + 8 * st, (ti / NST) & 1, dead))) break;
+                        ++ti;
+#pragma unroll 1
+                        for (int32_t x = rows_in * C + lane; x < rows_all * C; x += 32)
+                            st_zero16(r_s + st * SM::kTile + (x % C / 8) * 16384 + panel_off(x / C, x % C & 7));
+                        fence_async();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(clean + 8 * st);
+                    }
+                }
+            }
+        }
+        auto landed = [&](uint32_t bar, uint32_t parity) {
+#pragma unroll 1
+            for (uint32_t i = 0; i < kWaitRounds && !mbar_try(bar, parity); ++i) {
+            }
+        };
+        if (warp == 9) {
+            if (n > 0 && ok) {
+                ok = mbar_wait(pready, (n - 1) & 1, dead);
+                fence_after();
+                if (ok && elect_one()) cols(tm + 256, tm, desc_cols(r_s + (q_prev + 1) * SM::kTile, 16384), n > 1);
+                __syncwarp();
+                ok = ok && mbar_wait(dsready, (n - 1) & 1, dead);
+                fence_after();
+                if (ok && elect_one()) cols(tm + 384, tm + 128, desc_cols(r_s + q_prev * SM::kTile, 16384), n > 1);
+                __syncwarp();
+            }
+            if (elect_one()) mma_commit(drain);
+            __syncwarp();
+            landed(drain, 0);
+        } else if (warp == 8) {
+            landed(kvfull, 0);
+            for (uint32_t i = ti > NST ? ti - NST : 0; i < ti; ++i) landed(full + 8 * (i % NST), (i / NST) & 1);
+        }
+    }
+    __syncwarp();
+    fence_before();
+    __syncthreads();
+    if (warp == 9) tmem_free(tm, 512);
+}
+
+}  // namespace tdp_xt

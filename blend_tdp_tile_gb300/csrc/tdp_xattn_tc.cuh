@@ -459,7 +459,8 @@ tdp_xattn_tc_kernel(const __grid_constant__ tdp_geom g, const __grid_constant__ 
 
 // One block per mask row: the 128-state tiles that keep a state, in order, and their masks.
 __global__ void __launch_bounds__(1024)
-tdp_xattn_kept_kernel(const uint8_t *mask, int32_t S, int32_t *kept_n, int32_t *kept_tile, uint4 *kept_words)
+tdp_xattn_kept_kernel(const uint8_t *mask, int32_t S, int32_t *kept_n, int32_t *kept_tile, uint4 *kept_words,
+                      uint4 *state_words)
 {
     __shared__ uint32_t found[2][32];
     const int32_t tiles = (S + kKeys - 1) / kKeys, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -478,6 +479,7 @@ tdp_xattn_kept_kernel(const uint8_t *mask, int32_t S, int32_t *kept_n, int32_t *
             w[i] = __ballot_sync(~0u, t < tiles && s < S && m[s] != 0);
         }
         const bool any = (w[0] | w[1] | w[2] | w[3]) != 0;
+        if (lane == 0 && t < tiles && state_words) state_words[row * tiles + t] = make_uint4(w[0], w[1], w[2], w[3]);
         if (lane == 0) found[odd][warp] = any;
         __syncthreads();
         const uint32_t all = __ballot_sync(~0u, lane < warps && found[odd][lane] != 0);
