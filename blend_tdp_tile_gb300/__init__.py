@@ -155,6 +155,7 @@ class Plan:
     def __init__(self, handle: int, problem: dict):
         self._h = ctypes.c_void_p(handle)
         self.problem = problem
+        self.sizes = {}             # workspace bytes by shape
         n = ctypes.c_int32()
         tot = ctypes.c_int64()
         _check(_lib.tdp_plan_info(self._h, ctypes.byref(n), ctypes.byref(tot), None, None), "tdp_plan_info")
@@ -235,18 +236,27 @@ def tdp_rank_tiles(plan: Plan, rank: int, world: int) -> np.ndarray:
 
 
 # ------------------------------------------------------------------ marshalling
+_torch_module = None
+
+
 def _torch():
-    import torch
-    return torch
+    """torch, imported at the first call that handles tensors."""
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
 
 
 def _ptr(t, name, numel, dtypes, align):
     """Device pointer of a CUDA tensor after size/dtype/contiguity checks; None -> NULL."""
     if t is None:
         return None
-    torch = _torch()
-    if not isinstance(t, torch.Tensor):
+    if not isinstance(t, _torch().Tensor):
         raise TypeError(f"{name}: expected a torch.Tensor")
+    p = t.data_ptr()
+    if t.is_cuda and t.dtype in dtypes and t.numel() == numel and not p % align and t.is_contiguous():
+        return p
     if not t.is_cuda:
         raise ValueError(f"{name}: must be a CUDA tensor")
     if not t.is_contiguous():
@@ -255,10 +265,7 @@ def _ptr(t, name, numel, dtypes, align):
         raise ValueError(f"{name}: dtype {t.dtype} not in {dtypes}")
     if t.numel() != numel:
         raise ValueError(f"{name}: {t.numel()} elements, expected {numel}")
-    p = t.data_ptr()
-    if p % align:
-        raise ValueError(f"{name}: not {align}-byte aligned")
-    return p
+    raise ValueError(f"{name}: not {align}-byte aligned")
 
 
 def _common_device(where, named):
@@ -282,7 +289,9 @@ def _stream_handle(where, stream, dev):
     """Raw cudaStream_t for `stream` on device `dev`: None -> that device's current torch
     stream; a torch stream must belong to `dev`; an int is taken as a raw handle."""
     if stream is None:
-        return _torch().cuda.current_stream(dev).cuda_stream
+        torch = _torch()
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)      # the handle without a Stream object around it
+        return torch.cuda.current_stream(dev).cuda_stream if raw is None or dev is None else raw(dev.index)
     if isinstance(stream, int):
         return stream
     sdev = getattr(stream, "device", None)
@@ -309,13 +318,15 @@ class _Call:
         dev = _common_device(self.where, self.named)
         if dev is None:
             dev = torch.device("cuda", torch.cuda.current_device())
+        if dev.index == torch.cuda.current_device():
+            _check(fn(*args, _stream_handle(self.where, stream, dev)), self.where)
+            return
         with torch.cuda.device(dev):
             _check(fn(*args, _stream_handle(self.where, stream, dev)), self.where)
 
 
 def _latent_dtypes(plan):
-    torch = _torch()
-    return (torch.float32,) if plan.dtype == TDP_F32 else (torch.bfloat16,)
+    return (_torch().float32,) if plan.dtype == TDP_F32 else (_torch().bfloat16,)
 
 
 def tdp_pos_bounds(plan: Plan, P, mn, mx, stream=None):
@@ -652,9 +663,12 @@ def tdp_cross_attn_grad(plan: Plan, q, k, v, mask, out, lse, dout, dq, dk, dv, s
 
 def tdp_group_norm_workspace(plan: Plan, C: int, groups: int) -> int:
     """Bytes of workspace tdp_group_norm and tdp_group_norm_grad take for rows of C channels."""
-    n = ctypes.c_int64()
-    _check(_lib.tdp_group_norm_workspace(plan.handle, int(C), int(groups), ctypes.byref(n)), "tdp_group_norm_workspace")
-    return int(n.value)
+    got = plan.sizes.get((C, groups))
+    if got is None:
+        n = ctypes.c_int64()
+        _check(_lib.tdp_group_norm_workspace(plan.handle, int(C), int(groups), ctypes.byref(n)), "tdp_group_norm_workspace")
+        got = plan.sizes[C, groups] = int(n.value)
+    return got
 
 
 def _act(act):

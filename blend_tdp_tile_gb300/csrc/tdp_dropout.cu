@@ -4,6 +4,7 @@
 // Philox4x32-10 of counter {i/4, offset} and key seed (J. Salmon, M. Moraes, R. Dror,
 // D. Shaw, "Parallel random numbers: as easy as 1, 2, 3", SC 2011): the mask is a function
 // of the element's index, so the gradient computes it again and nothing is stored.
+#include <algorithm>
 #include <cmath>
 
 #include "tdp.h"
@@ -13,64 +14,102 @@
 namespace {
 
 constexpr int kDropThreads = 256;
+constexpr int kDropUnroll = 2;      // vectors a thread loads before it computes
 
-// Philox4x32-10: ten rounds of two 32x32 -> 64-bit products, the key bumped between rounds.
-__device__ __forceinline__ uint4 philox10(uint64_t index, uint64_t offset, uint64_t seed)
+// Round keys of Philox4x32-10: the key and its nine bumps.
+struct philox_keys {
+    uint32_t k0[10], k1[10];
+    __device__ __forceinline__ explicit philox_keys(uint64_t seed)
+    {
+#pragma unroll
+        for (int r = 0; r < 10; ++r) {
+            k0[r] = (uint32_t)seed + r * 0x9E3779B9u;
+            k1[r] = (uint32_t)(seed >> 32) + r * 0xBB67AE85u;
+        }
+    }
+};
+
+// Ten rounds of two 32x32 -> 64-bit products.
+__device__ __forceinline__ uint4 philox10(uint64_t index, uint64_t offset, const philox_keys &k)
 {
     uint32_t c0 = (uint32_t)index, c1 = (uint32_t)(index >> 32), c2 = (uint32_t)offset, c3 = (uint32_t)(offset >> 32);
-    uint32_t k0 = (uint32_t)seed, k1 = (uint32_t)(seed >> 32);
 #pragma unroll
     for (int r = 0; r < 10; ++r) {
         const uint64_t p0 = (uint64_t)c0 * 0xD2511F53u, p1 = (uint64_t)c2 * 0xCD9E8D57u;
-        c0 = (uint32_t)(p1 >> 32) ^ c1 ^ k0;
+        c0 = (uint32_t)(p1 >> 32) ^ c1 ^ k.k0[r];
         c1 = (uint32_t)p1;
-        c2 = (uint32_t)(p0 >> 32) ^ c3 ^ k1;
+        c2 = (uint32_t)(p0 >> 32) ^ c3 ^ k.k1[r];
         c3 = (uint32_t)p0;
-        k0 += 0x9E3779B9u;
-        k1 += 0xBB67AE85u;
     }
     return make_uint4(c0, c1, c2, c3);
 }
 
-// One 16-byte vector a thread and step (4 fp32 or 8 bf16 elements: one or two counters); the
-// vector that holds the end is done element by element.
+// The words of vector i's elements.
+template <int V>
+__device__ __forceinline__ void drop_words(int64_t i, uint64_t offset, const philox_keys &k, uint32_t *w)
+{
+#pragma unroll
+    for (int j = 0; j < V / 4; ++j) {
+        const uint4 u = philox10((uint64_t)i * (V / 4) + j, offset, k);
+        w[4 * j] = u.x;
+        w[4 * j + 1] = u.y;
+        w[4 * j + 2] = u.z;
+        w[4 * j + 3] = u.w;
+    }
+}
+
+// 16-byte vectors (4 fp32 or 8 bf16 elements: one or two counters), kDropUnroll of them a thread and step; the vector that
+// holds the end is done element by element by one thread.  `thr` is at most 2^32 - 1; p = 1 has all = 1.
 template <int BF16, int RES>
 __global__ void __launch_bounds__(kDropThreads)
-tdp_dropout_kernel(int64_t n, uint64_t thr, float scale, const uint64_t *__restrict__ rng, const void *x,
+tdp_dropout_kernel(int64_t n, uint32_t thr, int all, float scale, const uint64_t *__restrict__ rng, const void *x,
                    const void *res, void *out)
 {
     using E = tdp_elem<BF16>;
-    constexpr int V = E::kVec;
+    constexpr int V = E::kVec, U = kDropUnroll;
     tdp_pdl_trigger();
     tdp_pdl_wait();
-    const uint64_t seed = rng[0], offset = rng[1];
-    const int64_t nv = (n + V - 1) / V;
-    for (int64_t i = (int64_t)blockIdx.x * kDropThreads + threadIdx.x; i < nv; i += (int64_t)gridDim.x * kDropThreads) {
-        uint32_t w[V];
+    const uint64_t offset = rng[1];
+    const philox_keys keys(rng[0]);
+    const int64_t nv = n / V;
+    const uint4 *xv = reinterpret_cast<const uint4 *>(x), *rv = reinterpret_cast<const uint4 *>(res);
+    for (int64_t i0 = (int64_t)blockIdx.x * (kDropThreads * U) + threadIdx.x; i0 < nv; i0 += (int64_t)gridDim.x * (kDropThreads * U)) {
+        uint4 a[U], r[U];
 #pragma unroll
-        for (int j = 0; j < V / 4; ++j) {
-            const uint4 u = philox10((uint64_t)i * (V / 4) + j, offset, seed);
-            w[4 * j] = u.x;
-            w[4 * j + 1] = u.y;
-            w[4 * j + 2] = u.z;
-            w[4 * j + 3] = u.w;
+        for (int u = 0; u < U; ++u) {
+            const int64_t i = i0 + u * kDropThreads;
+            if (i < nv) {
+                a[u] = __ldcs(xv + i);
+                if (RES) r[u] = __ldcs(rv + i);
+            }
         }
-        if ((i + 1) * V <= n) {
-            float f[V], r[V];
-            E::unpack(reinterpret_cast<const uint4 *>(x)[i], f);
-            if (RES) E::unpack(reinterpret_cast<const uint4 *>(res)[i], r);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int64_t i = i0 + u * kDropThreads;
+            if (i >= nv) break;
+            uint32_t w[V];
+            float f[V], g[V];
+            drop_words<V>(i, offset, keys, w);
+            E::unpack(a[u], f);
+            if (RES) E::unpack(r[u], g);
 #pragma unroll
             for (int j = 0; j < V; ++j) {
-                const float k = w[j] >= thr ? f[j] * scale : 0.f;
-                f[j] = RES ? r[j] + k : k;
+                const float k = w[j] >= thr && !all ? f[j] * scale : 0.f;
+                f[j] = RES ? g[j] + k : k;
             }
-            reinterpret_cast<uint4 *>(out)[i] = E::pack(f);
-        } else {
-            for (int64_t e = i * V; e < n; ++e) {
-                using T = typename E::type;
-                const float k = w[e - i * V] >= thr ? (float)reinterpret_cast<const T *>(x)[e] * scale : 0.f;
-                reinterpret_cast<T *>(out)[e] = (T)(RES ? (float)reinterpret_cast<const T *>(res)[e] + k : k);
-            }
+            __stcs(reinterpret_cast<uint4 *>(out) + i, E::pack(f));
+        }
+    }
+    if (n % V != 0 && blockIdx.x == 0 && threadIdx.x == 0) {
+        using T = typename E::type;
+        uint32_t w[V];
+        drop_words<V>(nv, offset, keys, w);
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            const int64_t e = nv * V + j;
+            if (e >= n) break;
+            const float k = w[j] >= thr && !all ? (float)reinterpret_cast<const T *>(x)[e] * scale : 0.f;
+            reinterpret_cast<T *>(out)[e] = (T)(RES ? (float)reinterpret_cast<const T *>(res)[e] + k : k);
         }
     }
 }
@@ -86,14 +125,14 @@ tdp_status dropout(tdp_plan_t plan, int64_t n, double p, const uint64_t *rng, co
         return tdp_fail(TDP_ERR_MISALIGNED, "elements need 16-byte, rng 8-byte alignment");
     if (n > ((int64_t)1 << 56)) return tdp_fail(TDP_ERR_TOO_LARGE, "n above 2^56");
     const uint64_t thr = (uint64_t)std::llrint(p * 4294967296.0);
+    const int all = thr > 0xffffffffull;
     const float scale = p < 1.0 ? (float)(1.0 / (1.0 - p)) : 0.f;
-    const int V = plan->g.dtype == TDP_BF16 ? 8 : 4;
-    const int64_t blocks = ((n + V - 1) / V + kDropThreads - 1) / kDropThreads;
-    const unsigned grid = (unsigned)(blocks < 0x7fffffff ? blocks : 0x7fffffff);
+    const int64_t step = (int64_t)kDropThreads * kDropUnroll * (plan->g.dtype == TDP_BF16 ? 8 : 4);
+    const unsigned grid = (unsigned)std::min<int64_t>((n + step - 1) / step, 152 * 64);
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     auto *kernel = plan->g.dtype == TDP_BF16 ? (res ? tdp_dropout_kernel<1, 1> : tdp_dropout_kernel<1, 0>)
                                              : (res ? tdp_dropout_kernel<0, 1> : tdp_dropout_kernel<0, 0>);
-    const cudaError_t err = tdp_launch(true, kernel, grid, kDropThreads, s, n, thr, scale, rng, x, res, out);
+    const cudaError_t err = tdp_launch(true, kernel, grid, kDropThreads, s, n, (uint32_t)thr, all, scale, rng, x, res, out);
     return err == cudaSuccess ? tdp_ok() : tdp_fail(TDP_ERR_CUDA, cudaGetErrorString(err));
 }
 

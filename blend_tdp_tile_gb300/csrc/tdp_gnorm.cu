@@ -6,11 +6,19 @@
 // dz = dy * act'(z) and g = dz * gamma the gradient is
 //   dx = rstd * (g - mean(g) - h * mean(g * h)),  dgamma = sum dz * h,  dbeta = sum dz.
 //
-// Three launches each way: per-channel sums of chunks of rows; their join; the elementwise
-// pass.  The moments of a chunk are kept as (mean, sum of squared deviations) and joined by
-// T. Chan's rule, so that a mean far from zero costs no digits; every join runs in a fixed
-// order.
+// Bound by memory.  Three ways, by size:
+//   - tdp_gn_cluster_kernel: segments that fit the shared memory of a cluster of up to eight blocks.  One
+//     launch; x (and dy) are read once and the sums go round the cluster through distributed shared memory.
+//   - tdp_gn_sums_kernel, tdp_gn_apply_kernel: larger segments.  Sums of chunks of rows, then the elementwise pass, whose
+//     blocks join their segment's chunks themselves and run through the rows backwards, so that what the sums
+//     read last is found in the 129 MB L2.  (One grid that takes chunks of sums and, some segments later, of the
+//     elementwise pass in turn would read everything once, but its tickets, joins and flags cost 8 us a
+//     chunk: 934 us at best where these two take 6xx us, 635 million bf16 values.)
+//   - rows wider than a block's 256 vectors: sums, join and elementwise pass as launches of their own.
+// Variances are sums of squared deviations, of a block's values about their mean or joined by
+// T. Chan's rule, so that a mean far from zero costs no digits.  Every join runs in a fixed order.
 #include <algorithm>
+#include <atomic>
 
 #include "tdp.h"
 #include "tdp_internal.h"
@@ -19,155 +27,697 @@
 namespace {
 
 constexpr int kGnThreads = 256;
-constexpr int kGnRows = 256;      // rows of a chunk
+constexpr int kGnWideRows = 256;            // rows of a chunk, wide rows
+constexpr int kGnChunkMost = 512 << 10;     // bytes of x of a chunk; fewer while the chunks do not fill the device
+constexpr int kGnChunkLeast = 32 << 10;
+constexpr int kGnFill = 152 * 8;            // chunks that fill it
+constexpr int kClThreads = 512;
+constexpr int kClBytes = 48 << 10;          // values a cluster's block takes before the cluster grows
+constexpr int kClSmem = 224 << 10;          // shared memory of a block at most
 
-// ACT'(z) and ACT(z); SiLU is z * s, s = 1 / (1 + exp(-z)).
-__device__ __forceinline__ float sigmoidf(float z) { return __fdividef(1.f, 1.f + __expf(-z)); }
-
-// exp(-z) past 2^126 makes the fast division return 0 / inf = 0 in the forward and s = 0 in the
-// gradient: SiLU's limits.
+// SiLU is z * s, s = 1 / (1 + exp(-z)); its slope s + z s (1 - s).  exp(-z) overflows to infinity for z below -88: s = 0,
+// SiLU's limit.  The gradient kernels are bound by instructions as much as by memory: two table instructions and a
+// dozen others an element.
+__device__ __forceinline__ float sigmoidf(float z)
+{
+    float e, s;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(z * -1.4426950408889634f));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s) : "f"(1.f + e));
+    return s;
+}
 template <int ACT>
 __device__ __forceinline__ float act(float z) { return ACT ? z * sigmoidf(z) : z; }
 template <int ACT>
 __device__ __forceinline__ float act_grad(float z)
 {
     if (!ACT) return 1.f;
-    const float s = sigmoidf(z);
-    return s * (1.f + z * (1.f - s));
+    const float s = sigmoidf(z), t = z * s;
+    return fmaf(-t, s, t) + s;
 }
 
 struct gn_args {
-    int32_t C, G, chunks;       // channels, groups, chunks per segment
+    int32_t C, G, cg;           // channels, groups, channels per group
+    fast_div by_cg;
+    int32_t chunks, rows;       // chunks per segment, rows per chunk
     float eps;
     const void *x, *gamma, *beta, *dy;
     void *y;                    // y or dx
     float *mean, *rstd;         // [segments, G]
     float *dgamma, *dbeta;      // [C]
-    float *part;                // [segments, chunks, C, 2]
-    float *coef;                // [segments, C, 2] (gradient: sums over the segment)
+    float *part;                // sums of chunks per channel [segments, chunks, C, 2]
+    float *gpart;               // ... per group [segments, chunks, G, 2]
+    float *coef;                // wide, gradient: a segment's sums [segments, C, 2]
+    float *gmean;               // wide, gradient: means of g and g * h [segments, G, 2]
 };
 
-// Column of 16-byte vectors and first row of this thread: vectors of a row side by side,
-// then rows; blockIdx.y takes further vectors of rows wider than the block.
-struct gn_lane {
-    int32_t col, row, step;
-    bool on;
+// A thread's vector of channels: 16 bytes, 8 bytes of bf16 in the gradient (its seven constants a channel leave
+// registers for four channels).
+template <int BF16, int GRAD>
+struct gn_vec {
+    static constexpr int V = BF16 && !GRAD ? 8 : 4;
+    using type = uint4;
+    static __device__ __forceinline__ void unpack(const uint4 &u, float *f) { tdp_elem<BF16>::unpack(u, f); }
+    static __device__ __forceinline__ uint4 pack(const float *f) { return tdp_elem<BF16>::pack(f); }
 };
-__device__ __forceinline__ gn_lane gn_lane_of(int32_t CV)
+template <>
+struct gn_vec<1, 1> {
+    static constexpr int V = 4;
+    using type = uint2;
+    static __device__ __forceinline__ void unpack(const uint2 &u, float *f)
+    {
+        f[0] = tdp_bf16_lo(u.x);
+        f[1] = tdp_bf16_hi(u.x);
+        f[2] = tdp_bf16_lo(u.y);
+        f[3] = tdp_bf16_hi(u.y);
+    }
+    static __device__ __forceinline__ uint2 pack(const float *f) { return make_uint2(tdp_pack_bf16x2(f[0], f[1]), tdp_pack_bf16x2(f[2], f[3])); }
+};
+constexpr int gn_width(int bf16, int grad) { return bf16 && !grad ? 8 : 4; }
+
+template <int BF16>
+__device__ __forceinline__ float param(const void *p, int32_t c, float none)
 {
-    const int32_t w = CV < kGnThreads ? CV : kGnThreads;
-    gn_lane l;
-    l.step = kGnThreads / w;
-    l.row = threadIdx.x / w;
-    l.col = blockIdx.y * kGnThreads + threadIdx.x % w;
-    l.on = l.row < l.step && l.col < CV;
-    return l;
+    using T = typename tdp_elem<BF16>::type;
+    return p ? (float)static_cast<const T *>(p)[c] : none;
 }
 
-// Sums of a chunk's rows per channel.  Forward (GRAD = 0): mean and squared deviations,
-// each thread about its own first value.  Gradient: sum dz, sum dz * h.
+// A thread's column of V channels and their constants.
+template <int BF16, int GRAD>
+struct gn_cols {
+    using E = gn_vec<BF16, GRAD>;
+    static constexpr int V = E::V;
+    float mu[V], a[V], b[V];        // z = (x - mu) * a + b
+    float rs[V], ga[V], m1[V], m2[V];
+    __device__ __forceinline__ void params(const gn_args &g, int32_t col)
+    {
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            ga[j] = 1.f;
+            b[j] = 0.f;
+        }
+        if (g.gamma) E::unpack(__ldg(static_cast<const typename E::type *>(g.gamma) + col), ga);
+        if (g.beta) E::unpack(__ldg(static_cast<const typename E::type *>(g.beta) + col), b);
+    }
+    __device__ __forceinline__ void moments(const gn_args &g, int64_t s, int32_t col)
+    {
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            const int64_t gr = s * g.G + g.by_cg.div(col * V + j);
+            mu[j] = __ldcg(g.mean + gr);
+            rs[j] = __ldcg(g.rstd + gr);
+        }
+        params(g, col);
+#pragma unroll
+        for (int j = 0; j < V; ++j) a[j] = rs[j] * ga[j];
+    }
+    __device__ __forceinline__ void means(const gn_args &g, int64_t s, int32_t col)
+    {
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            const int64_t gr = s * g.G + g.by_cg.div(col * V + j);
+            m1[j] = __ldcg(g.gmean + 2 * gr) * rs[j];
+            m2[j] = __ldcg(g.gmean + 2 * gr + 1) * rs[j];
+        }
+    }
+    template <int ACT>
+    __device__ __forceinline__ void forward(float *f) const
+    {
+#pragma unroll
+        for (int j = 0; j < V; ++j) f[j] = act<ACT>((f[j] - mu[j]) * a[j] + b[j]);
+    }
+    // dz and h of one row
+    template <int ACT>
+    __device__ __forceinline__ void grad(const float *x, const float *dy, int j, float &dz, float &h) const
+    {
+        h = (x[j] - mu[j]) * rs[j];
+        dz = dy[j] * act_grad<ACT>(h * ga[j] + b[j]);
+    }
+    template <int ACT>
+    __device__ __forceinline__ void backward(const float *x, float *dy) const
+    {
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            float dz, h;
+            grad<ACT>(x, dy, j, dz, h);
+            dy[j] = fmaf(dz, a[j], -fmaf(h, m2[j], m1[j]));        // a = rstd * gamma, m1 and m2 times rstd
+        }
+    }
+};
+
+__device__ __forceinline__ float warp_sum(float x)
+{
+    for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(~0u, x, o);
+    return x;
+}
+
+// Moments of a group from parts (mean m_i, squared deviations q_i, n_i values each), one warp; value i by at(i).
+template <typename At>
+__device__ __forceinline__ void join_moments(int32_t parts, float n, At at, float &mean, float &q)
+{
+    const int32_t lane = threadIdx.x & 31;
+    mean = 0.f;
+    for (int32_t i = lane; i < parts; i += 32) {
+        const float3 p = at(i);
+        mean += p.x * (p.z / n);
+    }
+    mean = warp_sum(mean);
+    q = 0.f;
+    for (int32_t i = lane; i < parts; i += 32) {
+        const float3 p = at(i);
+        q += p.y + p.z * (p.x - mean) * (p.x - mean);
+    }
+    q = warp_sum(q);
+}
+
+// Threads of a block on rows of CV <= kThreads vectors: `step` rows side by side.
+struct gn_lane {
+    int32_t col, row, step, w;
+    bool on;
+    __device__ __forceinline__ gn_lane(int32_t CV, int32_t threads)
+    {
+        w = CV;
+        step = threads / w;
+        row = threadIdx.x / w;
+        col = threadIdx.x - row * w;
+        on = row < step;
+    }
+};
+
+// ------------------------------------------------------------------ two passes
+// Adds up (GRAD) or joins by Chan's rule the row lanes' values (s1, s2) of each channel; red holds threads * V
+// pairs, then a count per thread.  Afterwards row lane 0's entries are the block's.  n: this thread's rows.
+template <int V, int GRAD>
+__device__ __forceinline__ void join_lanes(float2 *red, const gn_lane &l, float n, const float *s1, const float *s2)
+{
+    float2 *mine = red + threadIdx.x * V;
+    float *count = reinterpret_cast<float *>(red + kGnThreads * V) + threadIdx.x;
+#pragma unroll
+    for (int j = 0; j < V; ++j) mine[j] = make_float2(s1[j], s2[j]);
+    *count = n;
+    __syncthreads();
+    for (int32_t live = l.step; live > 1;) {
+        const int32_t half = (live + 1) / 2;
+        if (l.on && l.row + half < live) {
+            const float2 *o = mine + half * l.w * V;
+            if (GRAD) {
+#pragma unroll
+                for (int j = 0; j < V; ++j) mine[j] = make_float2(mine[j].x + o[j].x, mine[j].y + o[j].y);
+            } else {
+                const float na = *count, nb = count[half * l.w];
+                if (nb > 0.f) {
+                    const float wb = nb / (na + nb);
+#pragma unroll
+                    for (int j = 0; j < V; ++j) {
+                        const float d = o[j].x - mine[j].x;
+                        mine[j] = make_float2(mine[j].x + d * wb, mine[j].y + o[j].y + d * d * na * wb);
+                    }
+                    *count = na + nb;
+                }
+            }
+        }
+        __syncthreads();
+        live = half;
+    }
+}
+
+// Sums of one chunk of a segment: per group (gradient: of g and g * h, and per channel of dz and dz * h).
 template <int BF16, int GRAD, int ACT>
-__global__ void __launch_bounds__(kGnThreads)
+__global__ void __launch_bounds__(kGnThreads, GRAD ? 3 : 4)
 tdp_gn_sums_kernel(const __grid_constant__ tdp_geom g, const gn_args a)
 {
-    using E = tdp_elem<BF16>;
-    constexpr int V = E::kVec;
-    __shared__ float red[kGnThreads * V * 2];
-    const int32_t s = blockIdx.x / a.chunks, ch = blockIdx.x % a.chunks;
+    using E = gn_vec<BF16, GRAD>;
+    using X = typename E::type;
+    constexpr int V = E::V, U = 4;
+    __shared__ float2 red[kGnThreads * V + kGnThreads / 2];
+    const int32_t s = blockIdx.x / a.chunks, ch = blockIdx.x % a.chunks, CV = a.C / V;
     const tdp_seg seg = tdp_seg_at(g, s);
-    const int64_t r0 = (int64_t)ch * kGnRows;
-    const int32_t rows = (int32_t)min((int64_t)kGnRows, seg.T - r0);
-    const int32_t CV = a.C / V, cg = a.C / a.G;
-    const gn_lane l = gn_lane_of(CV);
+    const int64_t r0 = (int64_t)ch * a.rows;
+    const int32_t rows = (int32_t)min((int64_t)a.rows, seg.T - r0);
+    const gn_lane l(CV, kGnThreads);
     tdp_pdl_trigger();
     tdp_pdl_wait();
     if (rows <= 0) return;
-    float p[V], s1[V], s2[V];
+    float p[V], s1[V], s2[V], n = 0.f;
 #pragma unroll
     for (int j = 0; j < V; ++j) p[j] = s1[j] = s2[j] = 0.f;
-    int32_t n = 0;
-    if (l.on) {
-        const uint4 *x = reinterpret_cast<const uint4 *>(a.x) + (seg.row0 + r0) * CV + l.col;
-        if (!GRAD) {
-            for (int32_t r = l.row; r < rows; r += l.step, ++n) {
-                float f[V];
-                E::unpack(x[(int64_t)r * CV], f);
-#pragma unroll
-                for (int j = 0; j < V; ++j) {
-                    if (n == 0) p[j] = f[j];
-                    const float d = f[j] - p[j];
-                    s1[j] += d;
-                    s2[j] += d * d;
-                }
-            }
-            if (n > 0) {
-#pragma unroll
-                for (int j = 0; j < V; ++j) {
-                    const float m = s1[j] / n;
-                    s2[j] -= s1[j] * m;         // squared deviations from the thread's mean
-                    s1[j] = p[j] + m;
-                }
-            }
-        } else {
-            const uint4 *dy = reinterpret_cast<const uint4 *>(a.dy) + (seg.row0 + r0) * CV + l.col;
-            float mu[V], rs[V], ga[V], be[V];
+    if (l.on && l.row < rows) {
+        const X *x = reinterpret_cast<const X *>(a.x) + (seg.row0 + r0) * CV + l.col;
+        const X *dy = reinterpret_cast<const X *>(a.dy) + (seg.row0 + r0) * CV + l.col;
+        gn_cols<BF16, GRAD> k;
+        const int32_t mine = (rows - l.row + l.step - 1) / l.step, step = l.step * CV;     // rows of this thread
+        auto add = [&](const X &xv, const X &dv) {
+            float f[V], e[V];
+            E::unpack(xv, f);
+            if (GRAD) E::unpack(dv, e);
 #pragma unroll
             for (int j = 0; j < V; ++j) {
-                const int32_t c = l.col * V + j;
-                mu[j] = a.mean[(int64_t)s * a.G + c / cg];
-                rs[j] = a.rstd[(int64_t)s * a.G + c / cg];
-                ga[j] = a.gamma ? (float)reinterpret_cast<const typename E::type *>(a.gamma)[c] : 1.f;
-                be[j] = a.beta ? (float)reinterpret_cast<const typename E::type *>(a.beta)[c] : 0.f;
-            }
-            for (int32_t r = l.row; r < rows; r += l.step) {
-                float f[V], d[V];
-                E::unpack(x[(int64_t)r * CV], f);
-                E::unpack(dy[(int64_t)r * CV], d);
-#pragma unroll
-                for (int j = 0; j < V; ++j) {
-                    const float h = (f[j] - mu[j]) * rs[j];
-                    const float dz = d[j] * act_grad<ACT>(h * ga[j] + be[j]);
-                    s1[j] += dz;
-                    s2[j] += dz * h;
-                }
-            }
-        }
-    }
-#pragma unroll
-    for (int j = 0; j < V; ++j) {
-        red[(threadIdx.x * V + j) * 2] = s1[j];
-        red[(threadIdx.x * V + j) * 2 + 1] = s2[j];
-    }
-    __syncthreads();
-    // the first row lane joins the lanes of its channels, in order
-    if (l.on && l.row == 0) {
-        const int32_t w = CV < kGnThreads ? CV : kGnThreads;
-        float *out = a.part + (((int64_t)s * a.chunks + ch) * a.C + l.col * V) * 2;
-#pragma unroll
-        for (int j = 0; j < V; ++j) {
-            float A = s1[j], Q = s2[j], N = (float)((rows + l.step - 1) / l.step);
-            for (int32_t k = 1; k < l.step && k < rows; ++k) {
-                const float *o = red + ((threadIdx.x + k * w) * V + j) * 2;
                 if (GRAD) {
-                    A += o[0];
-                    Q += o[1];
+                    float dz, h;
+                    k.template grad<ACT>(f, e, j, dz, h);
+                    s1[j] += dz;
+                    s2[j] = fmaf(dz, h, s2[j]);
                 } else {
-                    const float m = (float)((rows - k + l.step - 1) / l.step), d = o[0] - A;
-                    A += d * (m / (N + m));
-                    Q += o[1] + d * d * (N * m / (N + m));
-                    N += m;
+                    const float t = f[j] - p[j];
+                    s1[j] += t;
+                    s2[j] = fmaf(t, t, s2[j]);
                 }
             }
-            out[2 * j] = A;
-            out[2 * j + 1] = Q;
+        };
+        int32_t off = l.row * CV, i = 0;
+        if (GRAD) k.moments(a, s, l.col);
+        else E::unpack(x[off], p);              // deviations from the thread's own first value
+        for (; i + U <= mine; i += U) {
+            X u[U], d[U];
+#pragma unroll
+            for (int v = 0; v < U; ++v) {
+                u[v] = x[off + v * step];
+                if (GRAD) d[v] = dy[off + v * step];
+            }
+            off += U * step;
+#pragma unroll
+            for (int v = 0; v < U; ++v) add(u[v], d[v]);
         }
+        for (; i < mine; ++i, off += step) add(x[off], GRAD ? dy[off] : X());
+        if (!GRAD) {
+            n = (float)mine;
+            const float inv = 1.f / n;
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                const float m = s1[j] * inv;
+                s2[j] -= s1[j] * m;             // squared deviations from the thread's mean
+                s1[j] = p[j] + m;
+            }
+        }
+    }
+    join_lanes<V, GRAD>(red, l, n, s1, s2);
+    float2 *out = reinterpret_cast<float2 *>(a.gpart) + ((int64_t)s * a.chunks + ch) * a.G;
+    if (GRAD && a.dgamma) {
+        float2 *chan = reinterpret_cast<float2 *>(a.part) + ((int64_t)s * a.chunks + ch) * a.C;
+        for (int32_t c = threadIdx.x; c < a.C; c += kGnThreads) chan[c] = red[c];
+    }
+    for (int32_t gr = threadIdx.x >> 5; gr < a.G; gr += kGnThreads / 32) {
+        float m = 0.f, q = 0.f;
+        if (GRAD) {
+            for (int32_t i = threadIdx.x & 31; i < a.cg; i += 32) {
+                const float2 v = red[gr * a.cg + i];
+                const float w = param<BF16>(a.gamma, gr * a.cg + i, 1.f);
+                m += v.x * w;
+                q += v.y * w;
+            }
+            m = warp_sum(m);
+            q = warp_sum(q);
+        } else {
+            join_moments(a.cg, (float)a.cg * rows, [&](int32_t i) {
+                const float2 v = red[gr * a.cg + i];
+                return make_float3(v.x, v.y, (float)rows);
+            }, m, q);
+        }
+        if ((threadIdx.x & 31) == 0) out[gr] = make_float2(m, q);
     }
 }
 
-// One warp per (segment, group): the group's moments from its channels' and chunks' (mean, squared
-// deviations): first the mean, then the deviations about it.
+// The elementwise pass of one chunk, chunks from the last to the first; the block joins its segment's sums.
+template <int BF16, int GRAD, int ACT>
+__global__ void __launch_bounds__(kGnThreads, GRAD ? 3 : 4)
+tdp_gn_apply_kernel(const __grid_constant__ tdp_geom g, const gn_args a)
+{
+    using E = gn_vec<BF16, GRAD>;
+    using X = typename E::type;
+    constexpr int V = E::V, U = 4;
+    extern __shared__ __align__(16) unsigned char dyn[];
+    float2 *grp = reinterpret_cast<float2 *>(dyn);             // [G]
+    const int32_t unit = gridDim.x - 1 - blockIdx.x, s = unit / a.chunks, ch = unit % a.chunks, CV = a.C / V;
+    const tdp_seg seg = tdp_seg_at(g, s);
+    const int64_t r0 = (int64_t)ch * a.rows;
+    const int32_t rows = (int32_t)min((int64_t)a.rows, seg.T - r0), chunks = (int32_t)((seg.T + a.rows - 1) / a.rows);
+    const gn_lane l(CV, kGnThreads);
+    tdp_pdl_trigger();
+    tdp_pdl_wait();
+    if (rows <= 0) return;
+    const int64_t at = (seg.row0 + r0) * CV + l.col;
+    const X *x = reinterpret_cast<const X *>(a.x) + at, *dy = reinterpret_cast<const X *>(a.dy) + at;
+    X *y = reinterpret_cast<X *>(a.y) + at;
+    const int32_t mine = l.on ? (rows - l.row + l.step - 1) / l.step : 0, step = l.step * CV;        // rows of this thread
+    int32_t off = l.row * CV, i = 0;
+    X u[U], d[U];
+    auto load = [&]() {
+#pragma unroll
+        for (int v = 0; v < U; ++v) {
+            u[v] = __ldcs(x + off + v * step);
+            if (GRAD) d[v] = __ldcs(dy + off + v * step);
+        }
+    };
+    if (U <= mine) load();              // ahead of the join
+    const float n = (float)seg.T * a.cg;
+    const float2 *part = reinterpret_cast<const float2 *>(a.gpart) + (int64_t)s * a.chunks * a.G;
+    for (int32_t gr = threadIdx.x >> 5; gr < a.G; gr += kGnThreads / 32) {
+        const int32_t lane = threadIdx.x & 31;
+        float m = 0.f, q = 0.f;
+        if (GRAD) {
+            for (int32_t i = lane; i < chunks; i += 32) {
+                const float2 v = part[(int64_t)i * a.G + gr];
+                m += v.x;
+                q += v.y;
+            }
+            m = warp_sum(m) / n;
+            q = warp_sum(q) / n;
+        } else {
+            join_moments(chunks, n, [&](int32_t i) {
+                const float2 v = part[(int64_t)i * a.G + gr];
+                return make_float3(v.x, v.y, (float)min((int64_t)a.rows, seg.T - (int64_t)i * a.rows) * a.cg);
+            }, m, q);
+            q = 1.f / sqrtf(q / n + a.eps);
+            if (ch == 0 && lane == 0) {
+                a.mean[(int64_t)s * a.G + gr] = m;
+                a.rstd[(int64_t)s * a.G + gr] = q;
+            }
+        }
+        if (lane == 0) grp[gr] = make_float2(m, q);
+    }
+    __syncthreads();
+    if (!l.on || l.row >= rows) return;
+    gn_cols<BF16, GRAD> k;
+    if (GRAD) k.moments(a, s, l.col);
+    else k.params(a, l.col);
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+        const float2 v = grp[a.by_cg.div(l.col * V + j)];
+        if (GRAD) {
+            k.m1[j] = v.x * k.rs[j];
+            k.m2[j] = v.y * k.rs[j];
+        } else {
+            k.mu[j] = v.x;
+            k.a[j] = v.y * k.ga[j];
+        }
+    }
+    auto put = [&](const X &xv, const X &dv, int32_t o) {
+        float f[V], e[V];
+        E::unpack(xv, f);
+        if (GRAD) {
+            E::unpack(dv, e);
+            k.template backward<ACT>(f, e);
+            __stcs(y + o, E::pack(e));
+        } else {
+            k.template forward<ACT>(f);
+            __stcs(y + o, E::pack(f));
+        }
+    };
+    for (; i + U <= mine; i += U) {
+        if (i > 0) load();
+#pragma unroll
+        for (int v = 0; v < U; ++v) put(u[v], d[v], off + v * step);
+        off += U * step;
+    }
+    for (; i < mine; ++i, off += step) put(__ldcs(x + off), GRAD ? __ldcs(dy + off) : X(), off);
+}
+
+// ------------------------------------------------------------------ cluster
+__device__ __forceinline__ uint32_t cluster_rank()
+{
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_sync()
+{
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// A float of the shared memory of block `rank` of the cluster.
+__device__ __forceinline__ float cluster_ld(const float *p, uint32_t rank)
+{
+    uint32_t at;
+    float v;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"((uint32_t)__cvta_generic_to_shared(p)), "r"(rank));
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
+    return v;
+}
+
+// The block's sums of each channel from its row lanes' (s1, s2): into chan[c].
+template <int V>
+__device__ __forceinline__ void add_lanes(float2 *red, const gn_lane &l, const float *s1, const float *s2)
+{
+    float2 *mine = red + threadIdx.x * V;
+#pragma unroll
+    for (int j = 0; j < V; ++j) mine[j] = make_float2(s1[j], s2[j]);
+    __syncthreads();
+    for (int32_t live = l.step; live > 1;) {
+        const int32_t half = (live + 1) / 2;
+        if (l.on && l.row + half < live) {
+            const float2 *o = mine + half * l.w * V;
+#pragma unroll
+            for (int j = 0; j < V; ++j) mine[j] = make_float2(mine[j].x + o[j].x, mine[j].y + o[j].y);
+        }
+        __syncthreads();
+        live = half;
+    }
+}
+
+// Groups' sums over the whole cluster of the channel sums chan[c] (component 0 or both), weighted by w(c);
+// out[2 * G]: this block's, all[2 * G]: the cluster's, ranks in order.
+template <typename W>
+__device__ __forceinline__ void cluster_groups(const gn_args &a, const float2 *chan, float *out, float *all, uint32_t blocks, W w)
+{
+    for (int32_t gr = threadIdx.x >> 5; gr < a.G; gr += kClThreads / 32) {
+        float x = 0.f, y = 0.f;
+        for (int32_t i = threadIdx.x & 31; i < a.cg; i += 32) {
+            const int32_t c = gr * a.cg + i;
+            const float k = w(c);
+            x += chan[c].x * k;
+            y += chan[c].y * k;
+        }
+        x = warp_sum(x);
+        y = warp_sum(y);
+        if ((threadIdx.x & 31) == 0) {
+            out[2 * gr] = x;
+            out[2 * gr + 1] = y;
+        }
+    }
+    if (blocks == 1) {
+        __syncthreads();
+        for (int32_t i = threadIdx.x; i < 2 * a.G; i += kClThreads) all[i] = out[i];
+    } else {
+        cluster_sync();
+        for (int32_t i = threadIdx.x; i < 2 * a.G; i += kClThreads) {
+            float t = 0.f;
+            for (uint32_t r = 0; r < blocks; ++r) t += cluster_ld(out + i, r);
+            all[i] = t;
+        }
+    }
+    __syncthreads();
+}
+
+// One cluster per segment; block `rank` keeps its share of the rows in shared memory.
+template <int BF16, int GRAD, int ACT>
+__global__ void __launch_bounds__(kClThreads)
+tdp_gn_cluster_kernel(const __grid_constant__ tdp_geom g, const __grid_constant__ gn_args a, int32_t blocks, int32_t keep)
+{
+    using E = gn_vec<BF16, GRAD>;
+    using X = typename E::type;
+    constexpr int V = E::V;
+    extern __shared__ __align__(16) unsigned char dyn[];
+    float2 *red = reinterpret_cast<float2 *>(dyn);                              // [threads, V]
+    float *out = reinterpret_cast<float *>(red + kClThreads * V), *all = out + 4 * a.G;
+    X *xs = reinterpret_cast<X *>(dyn + kClThreads * V * 8 + ((6 * a.G * 4 + 15) & ~15)), *ds = xs + keep;
+    const uint32_t rank = blocks > 1 ? cluster_rank() : 0;
+    const int32_t s = blockIdx.x / blocks;
+    const tdp_seg seg = tdp_seg_at(g, s);
+    const int32_t T = (int32_t)seg.T, r0 = (int32_t)((int64_t)T * rank / blocks), rows = (int32_t)((int64_t)T * (rank + 1) / blocks) - r0;
+    const int32_t CV = a.C / V;
+    const gn_lane l(CV, kClThreads);
+    const int64_t at = (seg.row0 + r0) * CV;
+    const X *x = reinterpret_cast<const X *>(a.x) + at, *dy = reinterpret_cast<const X *>(a.dy) + at;
+    X *y = reinterpret_cast<X *>(a.y) + at;
+    const float n = (float)T * a.cg;
+    tdp_pdl_trigger();
+    tdp_pdl_wait();
+    float s1[V], s2[V];
+#pragma unroll
+    for (int j = 0; j < V; ++j) s1[j] = s2[j] = 0.f;
+    gn_cols<BF16, GRAD> k;
+    if (GRAD && l.on) k.moments(a, s, l.col);
+    if (l.on)
+#pragma unroll 4
+        for (int32_t r = l.row; r < rows; r += l.step) {
+            const int32_t i = r * CV + l.col;
+            const X u = x[i];
+            float f[V], e[V];
+            E::unpack(u, f);
+            xs[i] = u;
+            if (GRAD) {
+                const X d = dy[i];
+                ds[i] = d;
+                E::unpack(d, e);
+#pragma unroll
+                for (int j = 0; j < V; ++j) {
+                    float dz, h;
+                    k.template grad<ACT>(f, e, j, dz, h);
+                    s1[j] += dz;
+                    s2[j] += dz * h;
+                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < V; ++j) s1[j] += f[j];
+            }
+        }
+    add_lanes<V>(red, l, s1, s2);
+    if (GRAD) {
+        // this block's part of dgamma and dbeta
+        float2 *part = reinterpret_cast<float2 *>(a.part) + (int64_t)blockIdx.x * a.C;
+        if (a.dgamma)
+            for (int32_t c = threadIdx.x; c < a.C; c += kClThreads) part[c] = red[c];
+        cluster_groups(a, red, out, all, blocks, [&](int32_t c) { return param<BF16>(a.gamma, c, 1.f); });
+        if (l.on) {
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                const int32_t gr = (l.col * V + j) / a.cg;
+                k.m1[j] = all[2 * gr] / n * k.rs[j];
+                k.m2[j] = all[2 * gr + 1] / n * k.rs[j];
+            }
+        }
+    } else {
+        cluster_groups(a, red, out, all, blocks, [](int32_t) { return 1.f; });
+        if (l.on) {
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                k.mu[j] = all[2 * ((l.col * V + j) / a.cg)] / n;
+                s1[j] = s2[j] = 0.f;
+            }
+            for (int32_t r = l.row; r < rows; r += l.step) {
+                float f[V];
+                E::unpack(xs[r * CV + l.col], f);
+#pragma unroll
+                for (int j = 0; j < V; ++j) s1[j] += (f[j] - k.mu[j]) * (f[j] - k.mu[j]);
+            }
+        }
+        __syncthreads();
+        add_lanes<V>(red, l, s1, s2);
+        // the first sums may still be read by another block: these go beside them
+        cluster_groups(a, red, out + 2 * a.G, all, blocks, [](int32_t) { return 1.f; });
+        if (l.on) {
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                const int32_t c = l.col * V + j;
+                k.rs[j] = 1.f / sqrtf(all[2 * (c / a.cg)] / n + a.eps);
+                k.a[j] = k.rs[j] * param<BF16>(a.gamma, c, 1.f);
+                k.b[j] = param<BF16>(a.beta, c, 0.f);
+                if (rank == 0 && l.row == 0 && c % a.cg == 0) {
+                    a.mean[(int64_t)s * a.G + c / a.cg] = k.mu[j];
+                    a.rstd[(int64_t)s * a.G + c / a.cg] = k.rs[j];
+                }
+            }
+        }
+    }
+    if (l.on)
+#pragma unroll 2
+        for (int32_t r = l.row; r < rows; r += l.step) {
+            const int32_t i = r * CV + l.col;
+            float f[V], e[V];
+            E::unpack(xs[i], f);
+            if (GRAD) {
+                E::unpack(ds[i], e);
+                k.template backward<ACT>(f, e);
+                y[i] = E::pack(e);
+            } else {
+                k.template forward<ACT>(f);
+                y[i] = E::pack(f);
+            }
+        }
+    if (blocks > 1) cluster_sync();     // a block's shared memory is read until here
+}
+
+// dgamma and dbeta from `parts` sums per channel: a block per eight channels (64 bytes of each part), 32 threads a
+// channel, their sums added in order.  Parts of segments shorter than the longest (chunk >= chunks(s)) were not written.
 __global__ void __launch_bounds__(kGnThreads)
-tdp_gn_moments_kernel(const __grid_constant__ tdp_geom g, const gn_args a)
+tdp_gn_param_kernel(const __grid_constant__ tdp_geom g, const gn_args a, const float2 *part, int32_t parts, int32_t ragged)
+{
+    __shared__ float2 red[kGnThreads];
+    tdp_pdl_trigger();
+    tdp_pdl_wait();
+    const int32_t c = blockIdx.x * 8 + (threadIdx.x & 7), k = threadIdx.x >> 3;
+    float2 t = make_float2(0.f, 0.f);
+    if (c < a.C) {
+        int32_t seg = -1;
+        int64_t T = 0;
+#pragma unroll 4
+        for (int32_t i = k; i < parts; i += kGnThreads / 8) {
+            if (ragged) {
+                const int32_t s = i / a.chunks;
+                if (s != seg) {
+                    seg = s;
+                    T = tdp_seg_at(g, s).T;
+                }
+                if ((int64_t)(i - s * a.chunks) * a.rows >= T) continue;
+            }
+            const float2 v = part[(int64_t)i * a.C + c];
+            t.x += v.x;
+            t.y += v.y;
+        }
+    }
+    red[threadIdx.x] = t;
+    __syncthreads();
+    if (threadIdx.x >= 8 || c >= a.C) return;
+    for (int i = 1; i < kGnThreads / 8; ++i) {
+        t.x += red[threadIdx.x + 8 * i].x;
+        t.y += red[threadIdx.x + 8 * i].y;
+    }
+    a.dbeta[c] = t.x;
+    a.dgamma[c] = t.y;
+}
+
+// ------------------------------------------------------------------ wide rows
+// A thread per column of vectors; blockIdx.y takes 256 of them.
+template <int BF16, int GRAD, int ACT>
+__global__ void __launch_bounds__(kGnThreads)
+tdp_gn_wide_sums_kernel(const __grid_constant__ tdp_geom g, const gn_args a)
+{
+    using E = gn_vec<BF16, GRAD>;
+    using X = typename E::type;
+    constexpr int V = E::V;
+    const int32_t s = blockIdx.x / a.chunks, ch = blockIdx.x % a.chunks, CV = a.C / V, col = blockIdx.y * kGnThreads + threadIdx.x;
+    const tdp_seg seg = tdp_seg_at(g, s);
+    const int64_t r0 = (int64_t)ch * a.rows;
+    const int32_t rows = (int32_t)min((int64_t)a.rows, seg.T - r0);
+    tdp_pdl_trigger();
+    tdp_pdl_wait();
+    if (rows <= 0 || col >= CV) return;
+    const int64_t at = (seg.row0 + r0) * CV + col;
+    const X *x = reinterpret_cast<const X *>(a.x) + at, *dy = reinterpret_cast<const X *>(a.dy) + at;
+    float p[V], s1[V], s2[V];
+#pragma unroll
+    for (int j = 0; j < V; ++j) s1[j] = s2[j] = 0.f;
+    E::unpack(x[0], p);
+    gn_cols<BF16, GRAD> k;
+    if (GRAD) k.moments(a, s, col);
+    for (int32_t r = 0; r < rows; ++r) {
+        float f[V], e[V];
+        E::unpack(x[(int64_t)r * CV], f);
+        if (GRAD) E::unpack(dy[(int64_t)r * CV], e);
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            if (GRAD) {
+                float dz, h;
+                k.template grad<ACT>(f, e, j, dz, h);
+                s1[j] += dz;
+                s2[j] += dz * h;
+            } else {
+                const float t = f[j] - p[j];
+                s1[j] += t;
+                s2[j] += t * t;
+            }
+        }
+    }
+    float2 *out = reinterpret_cast<float2 *>(a.part) + ((int64_t)s * a.chunks + ch) * a.C + col * V;
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+        const float m = s1[j] / rows;
+        out[j] = GRAD ? make_float2(s1[j], s2[j]) : make_float2(p[j] + m, s2[j] - s1[j] * m);
+    }
+}
+
+// One warp per (segment, group): the group's moments, or (gradient) its channels' sums and means of g and g * h.
+template <int BF16, int GRAD>
+__global__ void __launch_bounds__(kGnThreads)
+tdp_gn_wide_join_kernel(const __grid_constant__ tdp_geom g, const gn_args a)
 {
     tdp_pdl_trigger();
     tdp_pdl_wait();
@@ -176,137 +726,93 @@ tdp_gn_moments_kernel(const __grid_constant__ tdp_geom g, const gn_args a)
     if (w >= (int64_t)g.nt * g.B * a.G) return;
     const int32_t s = (int32_t)(w / a.G), gr = (int32_t)(w % a.G);
     const tdp_seg seg = tdp_seg_at(g, s);
-    const int32_t cg = a.C / a.G, chunks = (int32_t)((seg.T + kGnRows - 1) / kGnRows);
-    const float *part = a.part + ((int64_t)s * a.chunks * a.C + gr * cg) * 2;
-    const float n = (float)seg.T * cg;
-    float mean = 0.f;
-    for (int32_t i = lane; i < chunks * cg; i += 32) {
-        const int32_t k = i / cg;
-        const float m = (float)min((int64_t)kGnRows, seg.T - (int64_t)k * kGnRows);
-        mean += part[((int64_t)k * a.C + i % cg) * 2] * (m / n);
-    }
-    for (int o = 16; o; o >>= 1) mean += __shfl_xor_sync(~0u, mean, o);
-    float q = 0.f;
-    for (int32_t i = lane; i < chunks * cg; i += 32) {
-        const int32_t k = i / cg;
-        const float m = (float)min((int64_t)kGnRows, seg.T - (int64_t)k * kGnRows);
-        const float *o = part + ((int64_t)k * a.C + i % cg) * 2;
-        q += o[1] + m * (o[0] - mean) * (o[0] - mean);
-    }
-    for (int o = 16; o; o >>= 1) q += __shfl_xor_sync(~0u, q, o);
-    if (lane == 0) {
-        a.mean[w] = mean;
-        a.rstd[w] = 1.f / sqrtf(q / n + a.eps);
-    }
-}
-
-// One thread per (segment, channel): the chunks' gradient sums of the segment.
-__global__ void __launch_bounds__(kGnThreads)
-tdp_gn_join_kernel(const __grid_constant__ tdp_geom g, const gn_args a)
-{
-    tdp_pdl_trigger();
-    tdp_pdl_wait();
-    const int64_t i = (int64_t)blockIdx.x * kGnThreads + threadIdx.x;
-    if (i >= (int64_t)g.nt * g.B * a.C) return;
-    const int32_t s = (int32_t)(i / a.C), c = (int32_t)(i % a.C);
-    const int32_t chunks = (int32_t)((tdp_seg_at(g, s).T + kGnRows - 1) / kGnRows);
-    float s1 = 0.f, s2 = 0.f;
-    for (int32_t k = 0; k < chunks; ++k) {
-        const float *o = a.part + (((int64_t)s * a.chunks + k) * a.C + c) * 2;
-        s1 += o[0];
-        s2 += o[1];
-    }
-    a.coef[2 * i] = s1;
-    a.coef[2 * i + 1] = s2;
-}
-
-// One warp per channel: dgamma and dbeta, the segments' sums joined.
-__global__ void __launch_bounds__(kGnThreads)
-tdp_gn_param_kernel(const __grid_constant__ tdp_geom g, const gn_args a)
-{
-    tdp_pdl_trigger();
-    tdp_pdl_wait();
-    const int32_t c = (int32_t)(((int64_t)blockIdx.x * kGnThreads + threadIdx.x) >> 5), lane = threadIdx.x & 31;
-    if (c >= a.C) return;
-    float s1 = 0.f, s2 = 0.f;
-    for (int32_t s = lane; s < g.nt * g.B; s += 32) {
-        s1 += a.coef[((int64_t)s * a.C + c) * 2];
-        s2 += a.coef[((int64_t)s * a.C + c) * 2 + 1];
-    }
-    for (int o = 16; o; o >>= 1) {
-        s1 += __shfl_xor_sync(~0u, s1, o);
-        s2 += __shfl_xor_sync(~0u, s2, o);
-    }
-    if (lane == 0) {
-        a.dbeta[c] = s1;
-        a.dgamma[c] = s2;
+    const int32_t chunks = (int32_t)((seg.T + a.rows - 1) / a.rows);
+    const float2 *part = reinterpret_cast<const float2 *>(a.part) + (int64_t)s * a.chunks * a.C + gr * a.cg;
+    const float n = (float)seg.T * a.cg;
+    if (!GRAD) {
+        float m, q;
+        join_moments(chunks * a.cg, n, [&](int32_t i) {
+            const int32_t k = i / a.cg;
+            const float2 v = part[(int64_t)k * a.C + i - k * a.cg];
+            return make_float3(v.x, v.y, (float)min((int64_t)a.rows, seg.T - (int64_t)k * a.rows));
+        }, m, q);
+        if (lane == 0) {
+            a.mean[w] = m;
+            a.rstd[w] = 1.f / sqrtf(q / n + a.eps);
+        }
+    } else {
+        float x = 0.f, y = 0.f;
+        for (int32_t i = lane; i < a.cg; i += 32) {
+            float2 t = make_float2(0.f, 0.f);
+            for (int32_t k = 0; k < chunks; ++k) {
+                const float2 v = part[(int64_t)k * a.C + i];
+                t.x += v.x;
+                t.y += v.y;
+            }
+            reinterpret_cast<float2 *>(a.coef)[(int64_t)s * a.C + gr * a.cg + i] = t;
+            const float k = param<BF16>(a.gamma, gr * a.cg + i, 1.f);
+            x += t.x * k;
+            y += t.y * k;
+        }
+        x = warp_sum(x);
+        y = warp_sum(y);
+        if (lane == 0) {
+            a.gmean[2 * w] = x / n;
+            a.gmean[2 * w + 1] = y / n;
+        }
     }
 }
 
-// The elementwise pass: y from x, or dx from x and dy.
 template <int BF16, int GRAD, int ACT>
 __global__ void __launch_bounds__(kGnThreads)
-tdp_gn_apply_kernel(const __grid_constant__ tdp_geom g, const gn_args a)
+tdp_gn_wide_apply_kernel(const __grid_constant__ tdp_geom g, const gn_args a)
 {
-    using E = tdp_elem<BF16>;
-    constexpr int V = E::kVec;
-    const int32_t s = blockIdx.x / a.chunks, ch = blockIdx.x % a.chunks;
+    using E = gn_vec<BF16, GRAD>;
+    using X = typename E::type;
+    constexpr int V = E::V;
+    const int32_t s = blockIdx.x / a.chunks, ch = blockIdx.x % a.chunks, CV = a.C / V, col = blockIdx.y * kGnThreads + threadIdx.x;
     const tdp_seg seg = tdp_seg_at(g, s);
-    const int64_t r0 = (int64_t)ch * kGnRows;
-    const int32_t rows = (int32_t)min((int64_t)kGnRows, seg.T - r0);
-    const int32_t CV = a.C / V, cg = a.C / a.G;
-    const gn_lane l = gn_lane_of(CV);
+    const int64_t r0 = (int64_t)ch * a.rows;
+    const int32_t rows = (int32_t)min((int64_t)a.rows, seg.T - r0);
     tdp_pdl_trigger();
     tdp_pdl_wait();
-    if (rows <= 0 || !l.on) return;
-    float mu[V], rs[V], ga[V], be[V], m1[V], m2[V];
-#pragma unroll
-    for (int j = 0; j < V; ++j) {
-        const int32_t c = l.col * V + j, gr = c / cg;
-        mu[j] = a.mean[(int64_t)s * a.G + gr];
-        rs[j] = a.rstd[(int64_t)s * a.G + gr];
-        ga[j] = a.gamma ? (float)reinterpret_cast<const typename E::type *>(a.gamma)[c] : 1.f;
-        be[j] = a.beta ? (float)reinterpret_cast<const typename E::type *>(a.beta)[c] : 0.f;
-        m1[j] = m2[j] = 0.f;
-        if (GRAD) {     // means of g and g * h over the group
-            if (j > 0 && gr == (c - 1) / cg) {
-                m1[j] = m1[j - 1];
-                m2[j] = m2[j - 1];
-            } else {
-                for (int32_t k = gr * cg; k < (gr + 1) * cg; ++k) {
-                    const float w = a.gamma ? (float)reinterpret_cast<const typename E::type *>(a.gamma)[k] : 1.f;
-                    m1[j] += w * a.coef[((int64_t)s * a.C + k) * 2];
-                    m2[j] += w * a.coef[((int64_t)s * a.C + k) * 2 + 1];
-                }
-                m1[j] /= (float)seg.T * cg;
-                m2[j] /= (float)seg.T * cg;
-            }
-        }
-    }
-    const int64_t at = (seg.row0 + r0) * CV + l.col;
-    const uint4 *x = reinterpret_cast<const uint4 *>(a.x) + at;
-    const uint4 *dy = reinterpret_cast<const uint4 *>(a.dy) + at;
-    uint4 *y = reinterpret_cast<uint4 *>(a.y) + at;
-    for (int32_t r = l.row; r < rows; r += l.step) {
-        float f[V], d[V];
+    if (rows <= 0 || col >= CV) return;
+    const int64_t at = (seg.row0 + r0) * CV + col;
+    const X *x = reinterpret_cast<const X *>(a.x) + at, *dy = reinterpret_cast<const X *>(a.dy) + at;
+    X *y = reinterpret_cast<X *>(a.y) + at;
+    gn_cols<BF16, GRAD> k;
+    k.moments(a, s, col);
+    if (GRAD) k.means(a, s, col);
+    for (int32_t r = 0; r < rows; ++r) {
+        float f[V], e[V];
         E::unpack(x[(int64_t)r * CV], f);
-        if (GRAD) E::unpack(dy[(int64_t)r * CV], d);
-#pragma unroll
-        for (int j = 0; j < V; ++j) {
-            const float h = (f[j] - mu[j]) * rs[j], z = h * ga[j] + be[j];
-            f[j] = GRAD ? rs[j] * (d[j] * act_grad<ACT>(z) * ga[j] - m1[j] - h * m2[j]) : act<ACT>(z);
+        if (GRAD) {
+            E::unpack(dy[(int64_t)r * CV], e);
+            k.template backward<ACT>(f, e);
+            y[(int64_t)r * CV] = E::pack(e);
+        } else {
+            k.template forward<ACT>(f);
+            y[(int64_t)r * CV] = E::pack(f);
         }
-        y[(int64_t)r * CV] = E::pack(f);
     }
 }
 
-int64_t gn_part_bytes(const tdp_geom &g, int32_t C, int64_t chunks)
+// ------------------------------------------------------------------ host
+enum gn_way { kWide, kCluster, kTwoPass };
+
+struct gn_plan {
+    gn_way way;
+    int32_t chunks, rows, blocks, keep;         // blocks: of a cluster; keep: vectors of its largest block
+    size_t smem;
+    int64_t gpart_at, coef_at, gmean_at, bytes;
+};
+
+size_t cluster_smem(int32_t G, int V, int64_t bytes)
 {
-    return (int64_t)g.nt * g.B * chunks * C * 8;
+    return (size_t)kClThreads * V * 8 + ((6 * (size_t)G * 4 + 15) & ~(size_t)15) + (size_t)bytes;
 }
 
-// Workspace: part, then coef.
-tdp_status gn_check(tdp_plan_t plan, int32_t C, int32_t groups, int64_t *bytes, int64_t *chunks)
+tdp_status gn_check(tdp_plan_t plan, int32_t C, int32_t groups, int grad, gn_plan *p)
 {
     if (!plan) return tdp_fail(TDP_ERR_INVALID_ARG, "null plan");
     const tdp_geom &g = plan->g;
@@ -314,56 +820,129 @@ tdp_status gn_check(tdp_plan_t plan, int32_t C, int32_t groups, int64_t *bytes, 
         return tdp_fail(TDP_ERR_INVALID_ARG, "need groups >= 1 dividing C");
     if (((int64_t)C * g.esize) % 16 != 0)
         return tdp_fail(TDP_ERR_MISALIGNED, "C * element size must be a multiple of 16 bytes");
-    *chunks = (tdp_max_tile_tokens(g) + kGnRows - 1) / kGnRows;
-    if ((int64_t)g.nt * g.B * *chunks > 0x7fffffffLL || (int64_t)C * g.esize / 16 > (int64_t)kGnThreads * 65535 ||
-        (int64_t)g.B * g.total > ((int64_t)1 << 56) / C)
+    const int V = gn_width(g.dtype == TDP_BF16, grad);
+    const int64_t CV = C / V, bytes = V * g.esize, T = tdp_max_tile_tokens(g), segs = (int64_t)g.nt * g.B;
+    if (CV > (int64_t)kGnThreads * 65535 || (int64_t)g.B * g.total > ((int64_t)1 << 56) / C)
         return tdp_fail(TDP_ERR_TOO_LARGE, "group normalisation beyond index ranges");
-    *bytes = gn_part_bytes(g, C, *chunks) + (int64_t)g.nt * g.B * C * 8;
+    p->blocks = 1;
+    p->keep = 0;
+    p->smem = 0;
+    // clusters of up to eight blocks hold a segment
+    const int64_t value = CV * bytes * (grad ? 2 : 1);
+    while (p->blocks < 8 && (T + p->blocks - 1) / p->blocks * value > kClBytes) p->blocks *= 2;
+    const int64_t rows = (T + p->blocks - 1) / p->blocks;
+    const int64_t most = (kClSmem - (int64_t)cluster_smem(std::min(groups, 1024), V, 0)) / value;
+    if (CV <= kGnThreads && groups <= 1024 && rows <= most && segs * p->blocks <= 0x7fffffffLL) {
+        p->way = kCluster;
+        p->keep = (int32_t)(rows * CV);
+        p->smem = cluster_smem(groups, V, rows * value);
+        p->chunks = p->blocks;
+        p->rows = (int32_t)rows;
+    } else if (CV <= kGnThreads && groups <= 4096) {
+        p->way = kTwoPass;
+        const int64_t fill = segs * T * CV * bytes / kGnFill;
+        p->rows = (int32_t)std::max<int64_t>(std::min<int64_t>(std::max<int64_t>(fill, kGnChunkLeast), kGnChunkMost) / (CV * bytes), 1);
+    } else {
+        p->way = kWide;
+        p->rows = kGnWideRows;
+    }
+    if (p->way != kCluster) {
+        const int64_t chunks = (T + p->rows - 1) / p->rows;
+        if (chunks * segs > 0x7fffffffLL) return tdp_fail(TDP_ERR_TOO_LARGE, "group normalisation beyond index ranges");
+        p->chunks = (int32_t)chunks;
+    }
+    auto up = [](int64_t x) { return (x + 255) / 256 * 256; };
+    p->gpart_at = up(segs * p->chunks * C * 8);
+    p->coef_at = p->gpart_at + up(segs * p->chunks * groups * 8);
+    p->gmean_at = p->coef_at + up(segs * C * 8);
+    p->bytes = p->gmean_at + up(segs * groups * 8);
     return TDP_OK;
 }
 
-template <int GRAD>
-cudaError_t gn_launch(const tdp_geom &g, gn_args a, int32_t act, cudaStream_t s)
+template <typename K, typename... A>
+cudaError_t gn_launch(K kernel, dim3 grid, int threads, size_t smem, int cluster, cudaStream_t s, A... args)
 {
-    const int V = g.dtype == TDP_BF16 ? 8 : 4;
-    const int32_t segs = g.nt * g.B;
-    const dim3 grid((unsigned)(segs * a.chunks), (unsigned)((a.C / V + kGnThreads - 1) / kGnThreads));
-    auto launch = [&](auto *k, dim3 gr) {
-        cudaLaunchAttribute attr[1];
-        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-        attr[0].val.programmaticStreamSerializationAllowed = 1;
-        cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = gr;
-        cfg.blockDim = dim3(kGnThreads);
-        cfg.stream = s;
-        cfg.attrs = attr;
-        cfg.numAttrs = 1;
-        return cudaLaunchKernelEx(&cfg, k, g, a);
-    };
-    auto blocks = [&](int64_t threads) { return dim3((unsigned)((threads + kGnThreads - 1) / kGnThreads)); };
-    cudaError_t err = g.dtype == TDP_BF16
-                          ? launch(act ? tdp_gn_sums_kernel<1, GRAD, 1> : tdp_gn_sums_kernel<1, GRAD, 0>, grid)
-                          : launch(act ? tdp_gn_sums_kernel<0, GRAD, 1> : tdp_gn_sums_kernel<0, GRAD, 0>, grid);
-    if (err == cudaSuccess)
-        err = GRAD ? launch(tdp_gn_join_kernel, blocks((int64_t)segs * a.C))
-                   : launch(tdp_gn_moments_kernel, blocks((int64_t)segs * a.G * 32));
-    if (err == cudaSuccess && GRAD && a.dgamma) err = launch(tdp_gn_param_kernel, blocks((int64_t)a.C * 32));
-    if (err == cudaSuccess)
-        err = g.dtype == TDP_BF16
-                  ? launch(act ? tdp_gn_apply_kernel<1, GRAD, 1> : tdp_gn_apply_kernel<1, GRAD, 0>, grid)
-                  : launch(act ? tdp_gn_apply_kernel<0, GRAD, 1> : tdp_gn_apply_kernel<0, GRAD, 0>, grid);
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = cluster;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+template <int BF16, int GRAD, int ACT>
+cudaError_t gn_run(const tdp_geom &g, const gn_plan &p, const gn_args &a, cudaStream_t s)
+{
+    const int64_t segs = (int64_t)g.nt * g.B;
+    constexpr int V = gn_width(BF16, GRAD);
+    cudaError_t err = cudaSuccess;
+    const dim3 channels((unsigned)((a.C + 7) / 8));
+    auto blocks = [](int64_t threads) { return dim3((unsigned)((threads + kGnThreads - 1) / kGnThreads)); };
+    if (p.way == kCluster) {
+        // the kernel's shared-memory limit, raised once per device
+        static std::atomic<bool> done[64];
+        int dev = 0;
+        err = cudaGetDevice(&dev);
+        if (err == cudaSuccess && (dev >= 64 || !done[dev].load(std::memory_order_relaxed))) {
+            err = cudaFuncSetAttribute(tdp_gn_cluster_kernel<BF16, GRAD, ACT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       kClSmem);
+            if (err == cudaSuccess && dev < 64) done[dev].store(true, std::memory_order_relaxed);
+        }
+        if (err == cudaSuccess)
+            err = gn_launch(tdp_gn_cluster_kernel<BF16, GRAD, ACT>, dim3((unsigned)(segs * p.blocks)), kClThreads, p.smem, p.blocks, s, g, a, p.blocks, p.keep);
+        if (err == cudaSuccess && GRAD && a.dgamma)
+            err = gn_launch(tdp_gn_param_kernel, channels, kGnThreads, 0, 1, s, g, a, (const float2 *)a.part, (int32_t)(segs * p.blocks), 0);
+    } else if (p.way == kTwoPass) {
+        const dim3 grid((unsigned)(segs * p.chunks));
+        err = gn_launch(tdp_gn_sums_kernel<BF16, GRAD, ACT>, grid, kGnThreads, 0, 1, s, g, a);
+        if (err == cudaSuccess) err = gn_launch(tdp_gn_apply_kernel<BF16, GRAD, ACT>, grid, kGnThreads, (size_t)a.G * 8, 1, s, g, a);
+        if (err == cudaSuccess && GRAD && a.dgamma)
+            err = gn_launch(tdp_gn_param_kernel, channels, kGnThreads, 0, 1, s, g, a, (const float2 *)a.part, (int32_t)(segs * p.chunks), 1);
+    } else {
+        const dim3 grid((unsigned)(segs * p.chunks), (unsigned)((a.C / V + kGnThreads - 1) / kGnThreads));
+        err = gn_launch(tdp_gn_wide_sums_kernel<BF16, GRAD, ACT>, grid, kGnThreads, 0, 1, s, g, a);
+        if (err == cudaSuccess) err = gn_launch(tdp_gn_wide_join_kernel<BF16, GRAD>, blocks(segs * a.G * 32), kGnThreads, 0, 1, s, g, a);
+        if (err == cudaSuccess && GRAD && a.dgamma)
+            err = gn_launch(tdp_gn_param_kernel, channels, kGnThreads, 0, 1, s, g, a, (const float2 *)a.coef, (int32_t)segs, 0);
+        if (err == cudaSuccess) err = gn_launch(tdp_gn_wide_apply_kernel<BF16, GRAD, ACT>, grid, kGnThreads, 0, 1, s, g, a);
+    }
     return err;
+}
+
+template <int GRAD>
+cudaError_t gn_dispatch(const tdp_geom &g, const gn_plan &p, gn_args a, int32_t act, void *ws, cudaStream_t s)
+{
+    unsigned char *w = static_cast<unsigned char *>(ws);
+    a.cg = a.C / a.G;
+    a.by_cg = fast_div_by(a.cg);
+    a.chunks = p.chunks;
+    a.rows = p.rows;
+    a.part = reinterpret_cast<float *>(w);
+    a.gpart = reinterpret_cast<float *>(w + p.gpart_at);
+    a.coef = reinterpret_cast<float *>(w + p.coef_at);
+    a.gmean = reinterpret_cast<float *>(w + p.gmean_at);
+    if (g.dtype == TDP_BF16) return act ? gn_run<1, GRAD, 1>(g, p, a, s) : gn_run<1, GRAD, 0>(g, p, a, s);
+    return act ? gn_run<0, GRAD, 1>(g, p, a, s) : gn_run<0, GRAD, 0>(g, p, a, s);
 }
 
 }  // namespace
 
 extern "C" tdp_status tdp_group_norm_workspace(tdp_plan_t plan, int32_t C, int32_t groups, int64_t *bytes)
 {
-    int64_t chunks, need;
+    gn_plan f, b;
     if (!bytes) return tdp_fail(TDP_ERR_INVALID_ARG, "null bytes");
-    const tdp_status st = gn_check(plan, C, groups, &need, &chunks);
+    tdp_status st = gn_check(plan, C, groups, 0, &f);
+    if (st == TDP_OK) st = gn_check(plan, C, groups, 1, &b);
     if (st != TDP_OK) return st;
-    *bytes = need;
+    *bytes = std::max(f.bytes, b.bytes);
     return tdp_ok();
 }
 
@@ -371,13 +950,13 @@ extern "C" tdp_status tdp_group_norm(tdp_plan_t plan, int32_t C, int32_t groups,
                                      const void *gamma, const void *beta, void *y, float *mean, float *rstd, void *ws,
                                      int64_t ws_bytes, tdp_stream_t stream)
 {
-    int64_t chunks, need;
-    const tdp_status st = gn_check(plan, C, groups, &need, &chunks);
+    gn_plan p;
+    const tdp_status st = gn_check(plan, C, groups, 0, &p);
     if (st != TDP_OK) return st;
     if (!(eps >= 0.f) || (act != TDP_ACT_NONE && act != TDP_ACT_SILU))
         return tdp_fail(TDP_ERR_INVALID_ARG, "need eps >= 0 and a known act");
     if (plan->g.B == 0) return tdp_ok();
-    if (!x || !y || !mean || !rstd || !ws || ws_bytes < need)
+    if (!x || !y || !mean || !rstd || !ws || ws_bytes < p.bytes)
         return tdp_fail(TDP_ERR_INVALID_ARG, "null x, y, mean, rstd or ws, or ws too small");
     if (!tdp_aligned(x, 16) || !tdp_aligned(y, 16) || !tdp_aligned(gamma, 16) || !tdp_aligned(beta, 16) ||
         !tdp_aligned(mean, 4) || !tdp_aligned(rstd, 4) || !tdp_aligned(ws, 256))
@@ -385,7 +964,6 @@ extern "C" tdp_status tdp_group_norm(tdp_plan_t plan, int32_t C, int32_t groups,
     gn_args a = {};
     a.C = C;
     a.G = groups;
-    a.chunks = (int32_t)chunks;
     a.eps = eps;
     a.x = x;
     a.gamma = gamma;
@@ -393,8 +971,7 @@ extern "C" tdp_status tdp_group_norm(tdp_plan_t plan, int32_t C, int32_t groups,
     a.y = y;
     a.mean = mean;
     a.rstd = rstd;
-    a.part = reinterpret_cast<float *>(ws);
-    const cudaError_t err = gn_launch<0>(plan->g, a, act, reinterpret_cast<cudaStream_t>(stream));
+    const cudaError_t err = gn_dispatch<0>(plan->g, p, a, act, ws, reinterpret_cast<cudaStream_t>(stream));
     return err == cudaSuccess ? tdp_ok() : tdp_fail(TDP_ERR_CUDA, cudaGetErrorString(err));
 }
 
@@ -403,8 +980,8 @@ extern "C" tdp_status tdp_group_norm_grad(tdp_plan_t plan, int32_t C, int32_t gr
                                           const void *dy, void *dx, float *dgamma, float *dbeta, void *ws,
                                           int64_t ws_bytes, tdp_stream_t stream)
 {
-    int64_t chunks, need;
-    const tdp_status st = gn_check(plan, C, groups, &need, &chunks);
+    gn_plan p;
+    const tdp_status st = gn_check(plan, C, groups, 1, &p);
     if (st != TDP_OK) return st;
     if (act != TDP_ACT_NONE && act != TDP_ACT_SILU) return tdp_fail(TDP_ERR_INVALID_ARG, "unknown act");
     if ((dgamma == nullptr) != (dbeta == nullptr))
@@ -416,7 +993,7 @@ extern "C" tdp_status tdp_group_norm_grad(tdp_plan_t plan, int32_t C, int32_t gr
         if (dbeta && err == cudaSuccess) err = cudaMemsetAsync(dbeta, 0, (size_t)C * 4, s);
         return err == cudaSuccess ? tdp_ok() : tdp_fail(TDP_ERR_CUDA, cudaGetErrorString(err));
     }
-    if (!x || !dy || !dx || !mean || !rstd || !ws || ws_bytes < need)
+    if (!x || !dy || !dx || !mean || !rstd || !ws || ws_bytes < p.bytes)
         return tdp_fail(TDP_ERR_INVALID_ARG, "null x, dy, dx, mean, rstd or ws, or ws too small");
     if (!tdp_aligned(x, 16) || !tdp_aligned(dy, 16) || !tdp_aligned(dx, 16) || !tdp_aligned(gamma, 16) ||
         !tdp_aligned(beta, 16) || !tdp_aligned(mean, 4) || !tdp_aligned(rstd, 4) || !tdp_aligned(dgamma, 4) ||
@@ -425,7 +1002,6 @@ extern "C" tdp_status tdp_group_norm_grad(tdp_plan_t plan, int32_t C, int32_t gr
     gn_args a = {};
     a.C = C;
     a.G = groups;
-    a.chunks = (int32_t)chunks;
     a.x = x;
     a.gamma = gamma;
     a.beta = beta;
@@ -435,8 +1011,6 @@ extern "C" tdp_status tdp_group_norm_grad(tdp_plan_t plan, int32_t C, int32_t gr
     a.rstd = const_cast<float *>(rstd);
     a.dgamma = dgamma;
     a.dbeta = dbeta;
-    a.part = reinterpret_cast<float *>(ws);
-    a.coef = a.part + gn_part_bytes(plan->g, C, chunks) / 4;
-    const cudaError_t err = gn_launch<1>(plan->g, a, act, s);
+    const cudaError_t err = gn_dispatch<1>(plan->g, p, a, act, ws, s);
     return err == cudaSuccess ? tdp_ok() : tdp_fail(TDP_ERR_CUDA, cudaGetErrorString(err));
 }

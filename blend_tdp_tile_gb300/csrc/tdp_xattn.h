@@ -9,32 +9,6 @@
 #include "tdp_internal.h"
 #include "tdp_rows.cuh"
 
-// Division of n < 2^31 by a constant: q = n * mul >> shift, mul = ceil(2^shift / d), shift = 31 + ceil(log2 d) (T. Granlund,
-// P. Montgomery, "Division by invariant integers using multiplication", PLDI 1994).  The kernels decode a work item in
-// every role; the divide instruction sequence took longer than an output tile.
-struct fast_div {
-    uint32_t mul;
-    int32_t shift, d;
-    __device__ __forceinline__ int32_t div(int32_t n) const { return (int32_t)(((uint64_t)(uint32_t)n * mul) >> shift); }
-    // n becomes the quotient; the remainder is returned
-    __device__ __forceinline__ int32_t mod(int32_t &n) const
-    {
-        const int32_t q = div(n), r = n - q * d;
-        n = q;
-        return r;
-    }
-};
-static inline fast_div fast_div_by(int32_t d)
-{
-    int32_t s = 0;
-    while (((int64_t)1 << s) < d) ++s;
-    fast_div f;
-    f.d = d;
-    f.shift = 31 + s;
-    f.mul = (uint32_t)((((uint64_t)1 << f.shift) + d - 1) / d);
-    return f;
-}
-
 struct xattn_args {
     const void *q, *k, *v;
     const uint8_t *mask;
