@@ -256,7 +256,13 @@ tdp_gn_sums_kernel(const __grid_constant__ tdp_geom g, const gn_args a)
     const gn_lane l(CV, kGnThreads);
     tdp_pdl_trigger();
     tdp_pdl_wait();
-    if (rows <= 0) return;
+    if (rows <= 0) {
+        // a shorter segment: its parts of dgamma and dbeta are nothing
+        if (GRAD && a.dgamma)
+            for (int32_t c = threadIdx.x; c < a.C; c += kGnThreads)
+                reinterpret_cast<float2 *>(a.part)[(int64_t)blockIdx.x * a.C + c] = make_float2(0.f, 0.f);
+        return;
+    }
     float p[V], s1[V], s2[V], n = 0.f;
 #pragma unroll
     for (int j = 0; j < V; ++j) p[j] = s1[j] = s2[j] = 0.f;
@@ -625,43 +631,34 @@ tdp_gn_cluster_kernel(const __grid_constant__ tdp_geom g, const __grid_constant_
     if (blocks > 1) cluster_sync();     // a block's shared memory is read until here
 }
 
-// dgamma and dbeta from `parts` sums per channel: a block per eight channels (64 bytes of each part), 32 threads a
-// channel, their sums added in order.  Parts of segments shorter than the longest (chunk >= chunks(s)) were not written.
+// dgamma and dbeta from `parts` sums per channel: a block per four channels (a sector of each part), 64 threads a
+// channel, their sums added in order.
 __global__ void __launch_bounds__(kGnThreads)
-tdp_gn_param_kernel(const __grid_constant__ tdp_geom g, const gn_args a, const float2 *part, int32_t parts, int32_t ragged)
+tdp_gn_param_kernel(const gn_args a, const float2 *part, int32_t parts)
 {
     __shared__ float2 red[kGnThreads];
     tdp_pdl_trigger();
     tdp_pdl_wait();
-    const int32_t c = blockIdx.x * 8 + (threadIdx.x & 7), k = threadIdx.x >> 3;
+    const int32_t c = blockIdx.x * 4 + (threadIdx.x & 3);
     float2 t = make_float2(0.f, 0.f);
-    if (c < a.C) {
-        int32_t seg = -1;
-        int64_t T = 0;
-#pragma unroll 4
-        for (int32_t i = k; i < parts; i += kGnThreads / 8) {
-            if (ragged) {
-                const int32_t s = i / a.chunks;
-                if (s != seg) {
-                    seg = s;
-                    T = tdp_seg_at(g, s).T;
-                }
-                if ((int64_t)(i - s * a.chunks) * a.rows >= T) continue;
-            }
+    if (c < a.C)
+#pragma unroll 8
+        for (int32_t i = threadIdx.x >> 2; i < parts; i += kGnThreads / 4) {
             const float2 v = part[(int64_t)i * a.C + c];
             t.x += v.x;
             t.y += v.y;
         }
-    }
     red[threadIdx.x] = t;
-    __syncthreads();
-    if (threadIdx.x >= 8 || c >= a.C) return;
-    for (int i = 1; i < kGnThreads / 8; ++i) {
-        t.x += red[threadIdx.x + 8 * i].x;
-        t.y += red[threadIdx.x + 8 * i].y;
+    for (int k = kGnThreads / 2; k >= 4; k /= 2) {
+        __syncthreads();
+        if (threadIdx.x < k) {
+            red[threadIdx.x].x += red[threadIdx.x + k].x;
+            red[threadIdx.x].y += red[threadIdx.x + k].y;
+        }
     }
-    a.dbeta[c] = t.x;
-    a.dgamma[c] = t.y;
+    if (threadIdx.x >= 4 || c >= a.C) return;
+    a.dbeta[c] = red[threadIdx.x].x;
+    a.dgamma[c] = red[threadIdx.x].y;
 }
 
 // ------------------------------------------------------------------ wide rows
@@ -884,7 +881,7 @@ cudaError_t gn_run(const tdp_geom &g, const gn_plan &p, const gn_args &a, cudaSt
     const int64_t segs = (int64_t)g.nt * g.B;
     constexpr int V = gn_width(BF16, GRAD);
     cudaError_t err = cudaSuccess;
-    const dim3 channels((unsigned)((a.C + 7) / 8));
+    const dim3 channels((unsigned)((a.C + 3) / 4));
     auto blocks = [](int64_t threads) { return dim3((unsigned)((threads + kGnThreads - 1) / kGnThreads)); };
     if (p.way == kCluster) {
         // the kernel's shared-memory limit, raised once per device
@@ -899,19 +896,19 @@ cudaError_t gn_run(const tdp_geom &g, const gn_plan &p, const gn_args &a, cudaSt
         if (err == cudaSuccess)
             err = gn_launch(tdp_gn_cluster_kernel<BF16, GRAD, ACT>, dim3((unsigned)(segs * p.blocks)), kClThreads, p.smem, p.blocks, s, g, a, p.blocks, p.keep);
         if (err == cudaSuccess && GRAD && a.dgamma)
-            err = gn_launch(tdp_gn_param_kernel, channels, kGnThreads, 0, 1, s, g, a, (const float2 *)a.part, (int32_t)(segs * p.blocks), 0);
+            err = gn_launch(tdp_gn_param_kernel, channels, kGnThreads, 0, 1, s, a, (const float2 *)a.part, (int32_t)(segs * p.blocks));
     } else if (p.way == kTwoPass) {
         const dim3 grid((unsigned)(segs * p.chunks));
         err = gn_launch(tdp_gn_sums_kernel<BF16, GRAD, ACT>, grid, kGnThreads, 0, 1, s, g, a);
         if (err == cudaSuccess) err = gn_launch(tdp_gn_apply_kernel<BF16, GRAD, ACT>, grid, kGnThreads, (size_t)a.G * 8, 1, s, g, a);
         if (err == cudaSuccess && GRAD && a.dgamma)
-            err = gn_launch(tdp_gn_param_kernel, channels, kGnThreads, 0, 1, s, g, a, (const float2 *)a.part, (int32_t)(segs * p.chunks), 1);
+            err = gn_launch(tdp_gn_param_kernel, channels, kGnThreads, 0, 1, s, a, (const float2 *)a.part, (int32_t)(segs * p.chunks));
     } else {
         const dim3 grid((unsigned)(segs * p.chunks), (unsigned)((a.C / V + kGnThreads - 1) / kGnThreads));
         err = gn_launch(tdp_gn_wide_sums_kernel<BF16, GRAD, ACT>, grid, kGnThreads, 0, 1, s, g, a);
         if (err == cudaSuccess) err = gn_launch(tdp_gn_wide_join_kernel<BF16, GRAD>, blocks(segs * a.G * 32), kGnThreads, 0, 1, s, g, a);
         if (err == cudaSuccess && GRAD && a.dgamma)
-            err = gn_launch(tdp_gn_param_kernel, channels, kGnThreads, 0, 1, s, g, a, (const float2 *)a.coef, (int32_t)segs, 0);
+            err = gn_launch(tdp_gn_param_kernel, channels, kGnThreads, 0, 1, s, a, (const float2 *)a.coef, (int32_t)segs);
         if (err == cudaSuccess) err = gn_launch(tdp_gn_wide_apply_kernel<BF16, GRAD, ACT>, grid, kGnThreads, 0, 1, s, g, a);
     }
     return err;

@@ -49,6 +49,20 @@ __device__ __forceinline__ bool elect_one()
     return on != 0;
 }
 
+// The same without suspending the thread.
+__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity)
+{
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return done != 0;
+}
+
 // Wait for phase `parity`; false when the rounds ran out here or (`dead`) in another thread.
 __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int *dead)
 {

@@ -244,16 +244,20 @@ tdp_xattn_join_kernel(const xattn_args a)
     const int64_t n = a.rows * a.Hq, h = ((int64_t)blockIdx.x * kXT + threadIdx.x) >> 5;
     if (h >= n) return;
     const int32_t lane = threadIdx.x & 31;
-    float top = -INFINITY;
-    for (int32_t i = 0; i < a.split; ++i) top = fmaxf(top, a.pl[i * n + h]);
-    const float base = top == -INFINITY ? 0.f : top;
-    float sum = 0.f, acc[TDP_MAX_HEAD_DIM / 32] = {};
+    // a part's lse a lane (two past 32 parts)
+    const float l0 = lane < a.split ? a.pl[lane * n + h] : -INFINITY, l1 = lane + 32 < a.split ? a.pl[(lane + 32) * n + h] : -INFINITY;
+    float top = fmaxf(l0, l1);
+    for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
+    const float base = top == -INFINITY ? 0.f : top, w0 = expf(l0 - base), w1 = expf(l1 - base);
+    float sum = w0 + w1, acc[TDP_MAX_HEAD_DIM / 32] = {};
+    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
+#pragma unroll 4
     for (int32_t i = 0; i < a.split; ++i) {
-        const float w = expf(a.pl[i * n + h] - base);
-        sum += w;
-        if (w != 0.f)
-            for (int c = 0; c < TDP_MAX_HEAD_DIM / 32; ++c)
-                if (lane + 32 * c < a.D) acc[c] += w * a.po[(i * n + h) * a.D + lane + 32 * c];
+        const float w = __shfl_sync(~0u, i < 32 ? w0 : w1, i & 31);
+        for (int c = 0; c < TDP_MAX_HEAD_DIM / 32; ++c) {
+            const float x = lane + 32 * c < a.D ? a.po[(i * n + h) * a.D + lane + 32 * c] : 0.f;
+            if (w != 0.f) acc[c] += w * x;
+        }
     }
     const float inv = sum == 0.f ? 0.f : 1.f / sum;
     for (int c = 0; c < TDP_MAX_HEAD_DIM / 32; ++c)
@@ -478,7 +482,7 @@ tdp_xattn_dkv_join_kernel(const xattn_args a, int64_t n)
     o[3] = (T)s.w;
 }
 
-constexpr int kSplitMax = 64;
+constexpr int kSplitMax = 64;  // two parts a lane in the join
 constexpr int kFill = 304;      // blocks below which the work is split: two for each SM
 constexpr int kSMs = 152;       // what splits are chosen for
 
@@ -494,16 +498,17 @@ struct xattn_shape {
     int32_t bblocks, bsplit, bpart;
 };
 
-// Parts of `tiles` state tiles for `items` row blocks: as many as make the device's rounds of
-// blocks, each as long as its tiles and about two more of setting up, take the least time.
+// Parts of `tiles` state tiles for `items` row blocks, fewer than the device's SMs: as many as make the device's
+// rounds of blocks, each as long as its tiles and one more, take the least time.  (Few rows are bound by
+// reading the states, which goes on from one block's item to the next.)
 int32_t split_states(int64_t items, int64_t tiles)
 {
     if (items == 0 || items >= kSMs || tiles < 2) return 1;
     int64_t best = 0;
     int32_t split = 1;
     for (int32_t s = 1; s <= std::min<int64_t>(kSplitMax, tiles); ++s) {
-        const int64_t cost = (items * s + kSMs - 1) / kSMs * ((tiles + s - 1) / s + 2) + (s > 1 ? 3 : 0);
-        if (s == 1 || cost < best) {
+        const int64_t cost = (items * s + kSMs - 1) / kSMs * ((tiles + s - 1) / s + 1) + (s > 1 ? 3 : 0);
+        if (s == 1 || cost <= best) {
             best = cost;
             split = s;
         }

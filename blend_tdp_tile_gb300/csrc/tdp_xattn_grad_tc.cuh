@@ -11,7 +11,7 @@
 //   warps 0-3, 4-7   columns 0-63, 64-127; the output
 //   warp 8           loads tiles through tensor maps
 //   warp 9           issues the products
-//   warp 10          second kernel: each row's lse and delta
+//   warp 10          each row's lse and delta (first kernel: dO . O, an item ahead of the warpgroups)
 //   warp 11          zeroes rows of a tile that must not count (their memory may hold anything, and 0 * NaN is not 0)
 #pragma once
 
@@ -19,11 +19,26 @@
 
 namespace tdp_xt {
 
+// A place in a ring of N stages and the phase of its barriers.
+template <int N>
+struct ring {
+    uint32_t st, ph;
+    __device__ __forceinline__ void next()
+    {
+        if (++st == N) {
+            st = 0;
+            ph ^= 1;
+        }
+    }
+};
+
 template <int DP>
 struct dq_smem {
     static constexpr int kTile = 128 * DP * 2;
-    static constexpr int kStages = DP == 128 ? 4 : 8;       // even: a stage always holds K, or always V
-    static constexpr int kBytes = 1024 + (3 + kStages) * kTile + 512 + 1024;
+    // A ring of O, then K and V in turn, of each item.  K stays from S to dQ: at five stages the next K and V still
+    // come in time (with two K and two V stages S waited for its K in every round).
+    static constexpr int kStages = DP == 128 ? 5 : 8;
+    static constexpr int kBytes = 1024 + (2 + kStages) * kTile + 512 + 1024;
 };
 
 template <int DP>
@@ -75,10 +90,10 @@ tdp_xattn_dq_kernel(const __grid_constant__ tdp_geom g, const __grid_constant__ 
     constexpr int NST = SM::kStages;
     extern __shared__ unsigned char raw[];
     const uint32_t base = (smem_u32(raw) + 1023u) & ~1023u;
-    const uint32_t q_s = base, do_s = q_s + SM::kTile, o_s = do_s + SM::kTile, kv_s = o_s + SM::kTile,
-                   bars = kv_s + NST * SM::kTile, sums = bars + 512;
-    const uint32_t full = bars, empty = full + 8 * NST, clean = empty + 8 * NST, rfull = clean + 8 * NST, rempty = rfull + 24,
-                   sfull = rempty + 24, pfull = sfull + 16, dsfull = pfull + 8, done = dsfull + 8, drain = done + 8;
+    const uint32_t q_s = base, do_s = q_s + SM::kTile, kv_s = do_s + SM::kTile, bars = kv_s + NST * SM::kTile, stat_s = bars + 512;
+    const uint32_t full = bars, empty = full + 8 * NST, clean = empty + 8 * NST, rfull = clean + 32, rempty = rfull + 16,
+                   tfull = rempty + 16, tempty = tfull + 8, sfull = tempty + 8, pfull = sfull + 16, dsfull = pfull + 8,
+                   done = dsfull + 8, drain = done + 8;
     __shared__ uint32_t tmem_slot;
     __shared__ int dead_flag;
     volatile int *dead = &dead_flag;
@@ -89,15 +104,15 @@ tdp_xattn_dq_kernel(const __grid_constant__ tdp_geom g, const __grid_constant__ 
         for (int i = 0; i < NST; ++i) {
             mbar_init(full + 8 * i, 1);
             mbar_init(empty + 8 * i, 1);
-            mbar_init(clean + 8 * i, 1);
         }
-        // row tiles: Q, dO, O; dO is given back by the products and by the warps that have read it for delta
-        for (int i = 0; i < 3; ++i) {
-            mbar_init(rfull + 8 * i, 1);
-            mbar_init(rempty + 8 * i, i == 0 ? 1 : i == 1 ? 9 : 8);
+        for (int i = 0; i < 4; ++i) mbar_init(clean + 8 * i, 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(rfull + 8 * i, 1);            // Q, dO
+            mbar_init(rempty + 8 * i, i ? 2 : 1);   // dO is given back by the products and by delta
+            mbar_init(sfull + 8 * i, 1);
         }
-        mbar_init(sfull, 1);
-        mbar_init(sfull + 8, 1);
+        mbar_init(tfull, 1);
+        mbar_init(tempty, 8);
         mbar_init(pfull, 1);
         mbar_init(dsfull, 8);
         mbar_init(done, 1);
@@ -112,13 +127,14 @@ tdp_xattn_dq_kernel(const __grid_constant__ tdp_geom g, const __grid_constant__ 
     tdp_pdl_wait();
 
     bool ok = true;
-    uint32_t kv = 0, n_done = 0;                // K and V tiles and state tiles so far
-    uint32_t ph = 0;                            // phase of the per-item barriers
+    ring<NST> kv = {0, 0};
+    uint32_t n_done = 0, n_items = 0;           // state tiles and items so far
     if (warp < 8) {
         regs_inc<216>();
         const int32_t half = warp >> 2, r = threadIdx.x & 127, rt = r / a.Gp, rh = r - rt * a.Gp;
         const uint32_t lanes = tm + ((uint32_t)(warp & 3) << 21);
         const float c = a.scale * kLog2e;
+        const bool wide = a.D % 16 == 0 && (reinterpret_cast<uintptr_t>(a.dq) & 31) == 0;      // whole sectors
         for (int32_t w = blockIdx.x; w < items; w += gridDim.x) {
             const item it = dq_item_at(g, a, w);
             const int32_t n = it.keys.n;
@@ -126,37 +142,14 @@ tdp_xattn_dq_kernel(const __grid_constant__ tdp_geom g, const __grid_constant__ 
             const bool mine = rt < a.TT && rt < it.left;
             const int32_t h = ((int32_t)(it.seg.row0 + it.tok0) + rt) * a.Hq + it.head + rh;
             if (n > 0) {
-                const float lse2 = mine ? row_lse2(a.lse[h]) : INFINITY;
-                // delta: each thread half of a row's products, the halves joined through shared memory
-                ok = ok && mbar_wait(rfull + 8, ph & 1, dead) && mbar_wait(rfull + 16, ph & 1, dead);
-                ph ^= 1;
-                float delta = 0.f;
-#pragma unroll
-                for (int i = 0; i < DP / 16; ++i) {
-                    const int32_t col = half * (DP / 16) + i;       // 16-byte chunk
-                    const uint32_t off = (col / 8) * 16384 + panel_off(r, col & 7);
-                    uint4 x, y;
-                    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w) : "r"(o_s + off));
-                    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(y.x), "=r"(y.y), "=r"(y.z), "=r"(y.w) : "r"(do_s + off));
-                    float fx[8], fy[8];
-                    tdp_elem<1>::unpack(x, fx);
-                    tdp_elem<1>::unpack(y, fy);
-#pragma unroll
-                    for (int u = 0; u < 8; ++u) delta = fmaf(fx[u], fy[u], delta);
-                }
+                const uint32_t st = stat_s + 4 * r;
+                ok = ok && mbar_wait(tfull, n_items & 1, dead);
+                float l, d;
+                asm volatile("ld.shared.f32 %0, [%1];" : "=f"(l) : "r"(st) : "memory");
+                asm volatile("ld.shared.f32 %0, [%1];" : "=f"(d) : "r"(st + 512) : "memory");
                 __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive(rempty + 8);
-                    mbar_arrive(rempty + 16);
-                }
-                asm volatile("st.shared.f32 [%0], %1;" ::"r"(sums + 512 * half + 4 * r), "f"(delta) : "memory");
-                asm volatile("bar.sync 1, 256;" ::: "memory");
-                float other;
-                asm volatile("ld.shared.f32 %0, [%1];" : "=f"(other) : "r"(sums + 512 * (half ^ 1) + 4 * r));
-                asm volatile("bar.sync 1, 256;" ::: "memory");
-                delta = half ? other + delta : delta + other;
-                if (mine && half == 0) a.delta[h] = delta;
-                const uint64_t c2 = pair(c, c), l2 = pair(-lse2, -lse2), d2 = pair(-delta, -delta);
+                if (lane == 0) mbar_arrive(tempty);
+                const uint64_t c2 = pair(c, c), l2 = pair(l, l), d2 = pair(d, d);
 #pragma unroll 1
                 for (int32_t j = 0; j < n && ok; ++j) {
                     const uint32_t buf = n_done & 1, S = lanes + 128 * buf + 64 * half, P = lanes + 256 + 64 * half;
@@ -205,7 +198,8 @@ tdp_xattn_dq_kernel(const __grid_constant__ tdp_geom g, const __grid_constant__ 
                     __syncwarp();
                     if (lane == 0) mbar_arrive(dsfull);
                 }
-                if (ok) ok = mbar_wait(done, (ph & 1) ^ 1, dead);
+                if (ok) ok = mbar_wait(done, n_items & 1, dead);
+                ++n_items;
                 fence_after();
             } else if (mine && half == 0) {
                 a.delta[h] = 0.f;
@@ -213,7 +207,6 @@ tdp_xattn_dq_kernel(const __grid_constant__ tdp_geom g, const __grid_constant__ 
             // dQ, half of the columns each; a lost wait leaves NaN
             T *dst = static_cast<T *>(a.dq) + (int64_t)h * a.D;
             const float f = ok ? a.scale : NAN;
-            const bool wide = a.D % 16 == 0 && (reinterpret_cast<uintptr_t>(a.dq) & 31) == 0;      // whole sectors
 #pragma unroll 1
             for (int i = half * (DP / 64); i < (half + 1) * (DP / 64); ++i) {
                 uint32_t o[32];
@@ -245,120 +238,187 @@ tdp_xattn_dq_kernel(const __grid_constant__ tdp_geom g, const __grid_constant__ 
         }
     } else {
         regs_dec<72>();
+        uint32_t kc = 0;                        // K tiles so far
         for (int32_t w = blockIdx.x; w < items; w += gridDim.x) {
             const item it = dq_item_at(g, a, w);
             const int32_t n = it.keys.n;
             if (it.left <= 0 || n == 0 || !ok) continue;
+            const int32_t row = (int32_t)(it.seg.row0 + it.tok0);
+            const uint32_t ph = n_items & 1;
             if (warp == 8) {
-                const int32_t row = (int32_t)(it.seg.row0 + it.tok0);
+                const uint32_t row_bytes = (uint32_t)(a.Gp * a.TT) * DP * 2;
                 auto load_row = [&](const CUtensorMap *map, int i) {
-                    if (!(ok = ok && mbar_wait(rempty + 8 * i, (ph & 1) ^ 1, dead))) return;
+                    if (!(ok = ok && mbar_wait(rempty + 8 * i, ph ^ 1, dead))) return;
                     if (elect_one()) {
-                        mbar_expect(rfull + 8 * i, (uint32_t)(a.Gp * a.TT) * DP * 2);
+                        mbar_expect(rfull + 8 * i, row_bytes);
                         for (int p = 0; p < DP / 64; ++p)
                             tma_load3(base + i * SM::kTile + p * 16384, map, rfull + 8 * i, 64 * p, it.head, row);
                     }
                     __syncwarp();
                 };
+                // O, K 0, Q, V 0, dO, K 1, V 1, ...
 #pragma unroll 1
-                for (int32_t i = 0; i < 2 * n && ok; ++i) {
+                for (int32_t i = -1; i < 2 * n; ++i) {
                     const bool v = i & 1;
-                    const uint32_t st = kv % NST;
                     const int32_t head = (v ? a.v_head : a.k_head) > 0 ? it.kvh : 0, b = (v ? a.v_item : a.k_item) > 0 ? it.seg.b : 0;
-                    const int32_t state = it.keys.at(i >> 1) * kKeys;
-                    if (i == 0) load_row(&map_q, 0);
-                    if (i == 1) load_row(&map_do, 1);
-                    if (!(ok = ok && mbar_wait(empty + 8 * st, ((kv / NST) & 1) ^ 1, dead))) break;
-                    ++kv;
+                    const int32_t state = i < 0 ? 0 : it.keys.at(i >> 1) * kKeys;
+                    if (!(ok = ok && mbar_wait(empty + 8 * kv.st, kv.ph ^ 1, dead))) break;
                     if (elect_one()) {
-                        mbar_expect(full + 8 * st, SM::kTile);
-                        for (int p = 0; p < DP / 64; ++p)
-                            tma_load4(kv_s + st * SM::kTile + p * 16384, v ? &map_v : &map_k, full + 8 * st, 64 * p, head, state, b);
+                        const uint32_t dst = kv_s + kv.st * SM::kTile, bar = full + 8 * kv.st;
+                        mbar_expect(bar, i < 0 ? row_bytes : (uint32_t)SM::kTile);
+                        for (int p = 0; p < DP / 64; ++p) {
+                            if (i < 0) tma_load3(dst + p * 16384, &map_o, bar, 64 * p, it.head, row);
+                            else tma_load4(dst + p * 16384, v ? &map_v : &map_k, bar, 64 * p, head, state, b);
+                        }
                     }
                     __syncwarp();
-                    if (i == 1) load_row(&map_o, 2);
+                    kv.next();
+                    if (i == 0) load_row(&map_q, 0);
+                    if (i == 1) load_row(&map_do, 1);
                 }
-                ph ^= 1;
             } else if (warp == 9) {
                 constexpr uint32_t id_s = idesc(128, 128, false, false), id_q = idesc(128, DP, false, true);
                 const uint32_t q_d = desc_rows(q_s), do_d = desc_rows(do_s);
-                const uint32_t k_full = a.mask ? clean : full;          // K comes by way of the cleaning warp where there is a mask
-                // product of two row-major tiles over the head dimension
-                auto rows = [&](uint32_t d, uint32_t x, uint32_t y) {
-#pragma unroll
-                    for (int i = 0; i < DP / 16; ++i) {
-                        mma_ss(d, x, y, id_s, i > 0);
-                        const uint32_t m = i % 4 == 3 ? (16384 - 96) >> 4 : 2;
-                        x += m;
-                        y += m;
-                    }
+                // A product of eight (DP / 16) steps.  The tensor cores queue two of them, some 128 cycles, and a wait
+                // takes longer: the next product's barrier is looked at before the last two steps are issued.
+                bool there = false;
+                auto wait = [&](uint32_t bar, uint32_t parity) {
+                    if (!there) ok = ok && mbar_wait(bar, parity, dead);
+                    there = false;
+                    __syncwarp();
+                    return ok;
                 };
+                auto rows = [&](uint32_t d, uint32_t x, uint32_t y, uint32_t end, uint32_t end2, uint32_t end3, uint32_t next, uint32_t parity) {
+                    auto step = [&](int i) {
+                        const uint32_t o = (i / 4) * (16384 >> 4) + (i % 4) * 2;
+                        mma_ss(d, x + o, y + o, id_s, i > 0);
+                    };
+                    if (elect_one()) {
+#pragma unroll
+                        for (int i = 0; i < DP / 16 - 2; ++i) step(i);
+                    }
+                    there = next && mbar_test(next, parity);
+                    __syncwarp();
+                    if (elect_one()) {
+                        step(DP / 16 - 2);
+                        step(DP / 16 - 1);
+                        mma_commit(end);
+                        if (end2) mma_commit(end2);
+                        if (end3) mma_commit(end3);
+                    }
+                    __syncwarp();
+                };
+                kv.next();                      // O
+                uint32_t k_prev = 0;
                 // round j: S of state tile j + 1 ahead, then dP of j + 1 and dQ of j once dS of j is there
 #pragma unroll 1
                 for (int32_t j = -1; j < n; ++j) {
-                    const uint32_t k0 = (kv + 2 * j) % NST, k1 = (kv + 2 * j + 2) % NST, v1 = k1 + 1;
-                    const uint32_t kph = ((kv + 2 * j + 2) / NST) & 1;
-                    const uint32_t s1 = tm + 128 * ((n_done + j + 1) & 1);
+                    const uint32_t b1 = n_done & 1, k1 = kv.st;     // n_done: S products so far
                     if (j + 1 < n) {
-                        if (j < 0 && !(ok = mbar_wait(rfull, ph & 1, dead))) break;
-                        if (!(ok = mbar_wait(k_full + 8 * k1, kph, dead))) break;
-                        if (elect_one()) {
-                            rows(s1, q_d, desc_rows(kv_s + k1 * SM::kTile));
-                            mma_commit(sfull + 8 * ((n_done + j + 1) & 1));
-                            if (j + 2 == n) mma_commit(rempty);
-                        }
-                        __syncwarp();
+                        if (j < 0 && !(ok = mbar_wait(rfull, ph, dead))) break;
+                        // K comes by way of the cleaning warp where there is a mask
+                        if (!(a.mask ? wait(clean + 8 * (kc & 3), (kc >> 2) & 1) : wait(full + 8 * k1, kv.ph))) break;
+                        ++kc;
+                        rows(tm + 128 * b1, q_d, desc_rows(kv_s + k1 * SM::kTile), sfull + 8 * b1, j + 2 == n ? rempty : 0, 0,
+                             j >= 0 ? dsfull : 0, (n_done - 1) & 1);
+                        ++n_done;
+                        kv.next();
                     }
                     if (j >= 0) {
-                        if (!(ok = mbar_wait(dsfull, (n_done + j) & 1, dead))) break;
+                        if (!wait(dsfull, (j + 1 < n ? n_done : n_done + 1) & 1)) break;
                         fence_after();
                     }
                     if (j + 1 < n) {
-                        if (j < 0 && !(ok = mbar_wait(rfull + 8, ph & 1, dead))) break;
-                        if (!(ok = mbar_wait(full + 8 * v1, kph, dead))) break;
-                        if (elect_one()) {
-                            rows(tm + 256, do_d, desc_rows(kv_s + v1 * SM::kTile));
-                            mma_commit(pfull);
-                            mma_commit(empty + 8 * v1);
-                            if (j + 2 == n) mma_commit(rempty + 8);
-                        }
-                        __syncwarp();
+                        if (j < 0 && !(ok = mbar_wait(rfull + 8, ph, dead))) break;
+                        if (!wait(full + 8 * kv.st, kv.ph)) break;
+                        rows(tm + 256, do_d, desc_rows(kv_s + kv.st * SM::kTile), pfull, empty + 8 * kv.st, j + 2 == n ? rempty + 8 : 0, 0, 0);
+                        kv.next();
                     }
                     if (j >= 0) {
-                        const uint32_t ds = tm + 128 * ((n_done + j) & 1), y = desc_cols(kv_s + k0 * SM::kTile, 16384);
+                        const uint32_t ds = tm + 128 * ((j + 1 < n ? n_done : n_done + 1) & 1), y0 = desc_cols(kv_s + k_prev * SM::kTile, 16384);
+                        auto step = [&](int i) { mma_ts(tm + 384, ds + 64 * (i / 4) + 8 * (i % 4), y0 + i * (2048 >> 4), id_q, j > 0 || i > 0); };
                         if (elect_one()) {
 #pragma unroll
-                            for (int i = 0; i < 8; ++i)
-                                mma_ts(tm + 384, ds + 64 * (i / 4) + 8 * (i % 4), y + i * (2048 >> 4), id_q, j > 0 || i > 0);
-                            mma_commit(empty + 8 * k0);
+                            for (int i = 0; i < 6; ++i) step(i);
+                        }
+                        there = j + 2 < n && (a.mask ? mbar_test(clean + 8 * (kc & 3), (kc >> 2) & 1) : mbar_test(full + 8 * kv.st, kv.ph));
+                        __syncwarp();
+                        if (elect_one()) {
+                            step(6);
+                            step(7);
+                            mma_commit(empty + 8 * k_prev);
                             if (j + 1 == n) mma_commit(done);
                         }
                         __syncwarp();
                     }
+                    k_prev = k1;
                 }
-                ph ^= 1;
-                kv += 2 * n;
-                n_done += n;
-            } else if (warp == 11 && a.mask) {
+            } else if (warp == 10) {
+                // four rows a lane
+                float lse[4], delta[4];
+                int32_t hs[4];
+                bool mine[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int32_t r = 32 * i + lane, rt = r / a.Gp;
+                    mine[i] = rt < a.TT && rt < it.left;
+                    hs[i] = (row + rt) * a.Hq + it.head + r - rt * a.Gp;
+                    lse[i] = mine[i] ? __ldg(a.lse + hs[i]) : -INFINITY;
+                    delta[i] = 0.f;
+                }
+                ok = mbar_wait(full + 8 * kv.st, kv.ph, dead) && mbar_wait(rfull + 8, ph, dead);
+#pragma unroll 1
+                for (int c = 0; c < DP / 8; ++c)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const uint32_t off = (c / 8) * 16384 + panel_off(32 * i + lane, c & 7);
+                        uint4 x, y;
+                        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w) : "r"(kv_s + kv.st * SM::kTile + off));
+                        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(y.x), "=r"(y.y), "=r"(y.z), "=r"(y.w) : "r"(do_s + off));
+                        float fx[8], fy[8];
+                        tdp_elem<1>::unpack(x, fx);
+                        tdp_elem<1>::unpack(y, fy);
+#pragma unroll
+                        for (int u = 0; u < 8; ++u) delta[i] = fmaf(fx[u], fy[u], delta[i]);
+                    }
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(empty + 8 * kv.st);
+                    mbar_arrive(rempty + 8);
+                }
+                ok = ok && mbar_wait(tempty, ph ^ 1, dead);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    if (mine[i]) a.delta[hs[i]] = delta[i];
+                    asm volatile("st.shared.f32 [%0], %1;" ::"r"(stat_s + 4 * (32 * i + lane)), "f"(-row_lse2(lse[i])) : "memory");
+                    asm volatile("st.shared.f32 [%0], %1;" ::"r"(stat_s + 512 + 4 * (32 * i + lane)), "f"(-delta[i]) : "memory");
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(tfull);
+                for (int32_t i = 0; i < 1 + 2 * n; ++i) kv.next();
+            } else if (a.mask) {
+                kv.next();                      // O
 #pragma unroll 1
                 for (int32_t j = 0; j < n; ++j) {
                     const uint4 m = it.keys.mask(j);
-                    const uint32_t st = (kv + 2 * j) % NST;
-                    if (!(ok = mbar_wait(full + 8 * st, ((kv + 2 * j) / NST) & 1, dead))) break;
+                    if (!(ok = mbar_wait(full + 8 * kv.st, kv.ph, dead))) break;
                     constexpr int C = DP / 8;           // 16-byte chunks of a row
 #pragma unroll 1
                     for (int32_t i = whole(m) ? 128 * C : lane; i < 128 * C; i += 32) {
-                        const int32_t row = i / C, col = i % C;
-                        const uint32_t word = row < 64 ? (row < 32 ? m.x : m.y) : (row < 96 ? m.z : m.w);
-                        if (!((word >> (row & 31)) & 1))
-                            st_zero16(kv_s + st * SM::kTile + (col / 8) * 16384 + panel_off(row, col & 7));
+                        const int32_t krow = i / C, col = i % C;
+                        const uint32_t word = krow < 64 ? (krow < 32 ? m.x : m.y) : (krow < 96 ? m.z : m.w);
+                        if (!((word >> (krow & 31)) & 1))
+                            st_zero16(kv_s + kv.st * SM::kTile + (col / 8) * 16384 + panel_off(krow, col & 7));
                     }
                     fence_async();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(clean + 8 * st);
+                    if (lane == 0) mbar_arrive(clean + 8 * (kc & 3));
+                    ++kc;
+                    kv.next();
+                    kv.next();                  // V
                 }
-                kv += 2 * n;
             }
+            ++n_items;
         }
     }
     // nothing may land, or be on its way, after the block has gone
@@ -368,8 +428,8 @@ tdp_xattn_dq_kernel(const __grid_constant__ tdp_geom g, const __grid_constant__ 
         }
     };
     if (warp == 8) {
-        for (uint32_t i = kv > NST ? kv - NST : 0; i < kv; ++i) landed(full + 8 * (i % NST), (i / NST) & 1);
-        for (int i = 0; i < 3; ++i) landed(rfull + 8 * i, (ph & 1) ^ 1);
+        for (uint32_t i = 0; i < NST; ++i) landed(full + 8 * i, i < kv.st ? kv.ph : kv.ph ^ 1);
+        for (int i = 0; i < 2; ++i) landed(rfull + 8 * i, (n_items & 1) ^ 1);
     } else if (warp == 9) {
         if (elect_one()) mma_commit(drain);
         __syncwarp();
@@ -382,40 +442,32 @@ tdp_xattn_dq_kernel(const __grid_constant__ tdp_geom g, const __grid_constant__ 
 }
 
 // Walk over the row tiles of one batch item that meet a tile of states: the part's units [u, last), unit u = block
-// u % blocks of the item's segment u / blocks.
+// u % blocks of the item's segment u / blocks; a segment's run of blocks at a time.
 struct row_walk {
-    int32_t u, last, cur;
+    int32_t u, last;
     tdp_seg seg;
-    int64_t tok0;
-    int32_t left;                   // tokens from tok0 on
+    int32_t blk, end;               // the run's blocks
     uint4 words;                    // kept states of the tile
     __device__ __forceinline__ bool next(const tdp_geom &g, const xattn_args &a, int32_t b, int32_t tile)
     {
         while (u < last) {
             const int32_t sg = a.by_blocks.div(u);
-            if (sg != cur) {
-                cur = sg;
-                seg = xattn_seg_fast(g, a, sg * g.B + b);
-                if (a.mask) {
-                    const int64_t m = a.per_tile ? (int64_t)seg.t * g.B + seg.b : seg.b;
-                    words = __ldg(a.state_words + m * ((a.S + kKeys - 1) / kKeys) + tile);
-                } else {
-                    key_list k;
-                    k.tile = nullptr;
-                    k.words = nullptr;
-                    k.j0 = tile;
-                    k.S = a.S;
-                    words = k.mask(0);
-                }
+            seg = xattn_seg_fast(g, a, sg * g.B + b);
+            blk = u - sg * a.blocks;
+            end = min(blk + last - u, (int32_t)((seg.T + a.TT - 1) / a.TT));
+            u = (sg + 1) * a.blocks;
+            if (a.mask) {
+                const int64_t m = a.per_tile ? (int64_t)seg.t * g.B + seg.b : seg.b;
+                words = __ldg(a.state_words + m * ((a.S + kKeys - 1) / kKeys) + tile);
+            } else {
+                key_list k;
+                k.tile = nullptr;
+                k.words = nullptr;
+                k.j0 = tile;
+                k.S = a.S;
+                words = k.mask(0);
             }
-            tok0 = (int64_t)(u - sg * a.blocks) * a.TT;
-            left = (int32_t)(seg.T - tok0);
-            if (left <= 0 || (words.x | words.y | words.z | words.w) == 0) {
-                u = (sg + 1) * a.blocks;
-                continue;
-            }
-            ++u;
-            return true;
+            if (blk < end && (words.x | words.y | words.z | words.w) != 0) return true;
         }
         return false;
     }
@@ -481,7 +533,6 @@ tdp_xattn_dkv_kernel(const __grid_constant__ tdp_geom g, const __grid_constant__
     row_walk wk;
     wk.u = min(units, part * a.part);
     wk.last = min(units, wk.u + a.part);
-    wk.cur = -1;
 
     // every role walks the same row tiles, each for the head blocks in turn
     bool ok = true, any = false;
@@ -495,8 +546,9 @@ tdp_xattn_dkv_kernel(const __grid_constant__ tdp_geom g, const __grid_constant__
         while (ok && wk.next(g, a, b, tile)) {
             const uint32_t word = r < 64 ? (r < 32 ? wk.words.x : wk.words.y) : (r < 96 ? wk.words.z : wk.words.w);
             const bool kept = (word >> lane) & 1;
+            const int32_t tiles_in = (wk.end - wk.blk) * hbs;
 #pragma unroll 1
-            for (int32_t hb = 0; hb < hbs && ok; ++hb, ++n) {
+            for (int32_t i = 0; i < tiles_in && ok; ++i, ++n) {
                 const uint32_t ss = n % NSS, st = stat_s + ss * 1024 + 256 * half;
                 any = true;
                 ok = mbar_wait(tfull + 8 * ss, (n / NSS) & 1, dead) && mbar_wait(sfull, n & 1, dead);
@@ -607,19 +659,49 @@ tdp_xattn_dkv_kernel(const __grid_constant__ tdp_geom g, const __grid_constant__
         regs_dec<72>();
         uint32_t ti = 0;                        // Q and dO tiles so far
         constexpr uint32_t id_s = idesc(128, 128, false, false), id_o = idesc(128, DP, false, true);
-        auto rows = [&](uint32_t d, uint32_t x, uint32_t y) {
+        // A product of eight (DP / 16) steps.  The tensor cores queue two of them, some 128 cycles, and a wait with what
+        // surrounds it takes longer: the next product's barrier is looked at before the last two steps are issued.
+        bool there = false;
+        auto wait = [&](uint32_t bar, uint32_t parity) {
+            if (!there) ok = ok && mbar_wait(bar, parity, dead);
+            __syncwarp();
+            return ok;
+        };
+        // both operands row-major over the head dimension
+        auto rows = [&](uint32_t d, uint32_t x, uint32_t y, uint32_t done, uint32_t next, uint32_t parity) {
+            auto step = [&](int i) {
+                const uint32_t o = (i / 4) * (16384 >> 4) + (i % 4) * 2;       // next panel, or 32 bytes
+                mma_ss(d, x + o, y + o, id_s, i > 0);
+            };
+            if (elect_one()) {
 #pragma unroll
-            for (int i = 0; i < DP / 16; ++i) {
-                mma_ss(d, x, y, id_s, i > 0);
-                const uint32_t m = i % 4 == 3 ? (16384 - 96) >> 4 : 2;
-                x += m;
-                y += m;
+                for (int i = 0; i < DP / 16 - 2; ++i) step(i);
             }
+            there = mbar_test(next, parity);
+            __syncwarp();
+            if (elect_one()) {
+                step(DP / 16 - 2);
+                step(DP / 16 - 1);
+                mma_commit(done);
+            }
+            __syncwarp();
         };
         // A from tensor memory, 64 columns of it at each half; B: a row tile read by columns
-        auto cols = [&](uint32_t d, uint32_t p, uint32_t y, bool acc) {
+        auto cols = [&](uint32_t d, uint32_t p, uint32_t y, bool acc, uint32_t done, uint32_t next, uint32_t parity) {
+            auto step = [&](int i) { mma_ts(d, p + 64 * (i / 4) + 8 * (i % 4), y + i * (2048 >> 4), id_o, acc || i > 0); };
+            fence_after();
+            if (elect_one()) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) mma_ts(d, p + 64 * (i / 4) + 8 * (i % 4), y + i * (2048 >> 4), id_o, acc || i > 0);
+                for (int i = 0; i < 6; ++i) step(i);
+            }
+            there = next && mbar_test(next, parity);
+            __syncwarp();
+            if (elect_one()) {
+                step(6);
+                step(7);
+                mma_commit(done);
+            }
+            __syncwarp();
         };
         if (warp == 8 && elect_one()) {
             const int32_t kh = a.k_head > 0 ? kvh : 0, kb = a.k_item > 0 ? b : 0, vh = a.v_head > 0 ? kvh : 0, vb = a.v_item > 0 ? b : 0;
@@ -634,9 +716,15 @@ tdp_xattn_dkv_kernel(const __grid_constant__ tdp_geom g, const __grid_constant__
         // warp 9 runs one tile behind itself: dK and dP of a tile come after S of the next
         uint32_t q_prev = 0;
         while (ok && wk.next(g, a, b, tile)) {
+            int32_t hb = 0, tok = wk.blk * a.TT;        // head block and first token of the tile in its segment
+            const int32_t tiles_in = (wk.end - wk.blk) * hbs;
 #pragma unroll 1
-            for (int32_t hb = 0; hb < hbs && ok; ++hb, ++n) {
-                const int32_t head = kvh * a.G + hb * a.Gp, row = (int32_t)(wk.seg.row0 + wk.tok0);
+            for (int32_t t = 0; t < tiles_in && ok; ++t, ++n) {
+                const int32_t head = kvh * a.G + hb * a.Gp, row = (int32_t)wk.seg.row0 + tok, left = (int32_t)wk.seg.T - tok;
+                if (++hb == hbs) {
+                    hb = 0;
+                    tok += a.TT;
+                }
                 if (warp == 8) {
 #pragma unroll 1
                     for (int i = 0; i < 2; ++i) {
@@ -652,40 +740,23 @@ tdp_xattn_dkv_kernel(const __grid_constant__ tdp_geom g, const __grid_constant__
                     }
                 } else if (warp == 9) {
                     const uint32_t qs = ti % NST, ds = qs + 1, tph = (ti / NST) & 1;
-                    const uint32_t q_t = r_s + qs * SM::kTile, do_t = r_s + ds * SM::kTile;
+                    const uint32_t q_t = desc_rows(r_s + qs * SM::kTile), do_t = desc_rows(r_s + ds * SM::kTile);
+                    const uint32_t q_p = desc_cols(r_s + q_prev * SM::kTile, 16384), do_p = desc_cols(r_s + (q_prev + 1) * SM::kTile, 16384);
                     ti += 2;
                     if (n > 0) {
                         // dV of the tile before, whose probabilities lie in S
-                        if (!(ok = mbar_wait(pready, (n - 1) & 1, dead))) break;
-                        fence_after();
-                        if (elect_one()) {
-                            cols(tm + 256, tm, desc_cols(r_s + (q_prev + 1) * SM::kTile, 16384), n > 1);
-                            mma_commit(empty + 8 * (q_prev + 1));
-                        }
-                        __syncwarp();
+                        if (!wait(pready, (n - 1) & 1)) break;
+                        cols(tm + 256, tm, do_p, n > 1, empty + 8 * (q_prev + 1), clean + 8 * qs, tph);
                     }
-                    if (!(ok = mbar_wait(clean + 8 * qs, tph, dead))) break;
-                    if (elect_one()) {
-                        rows(tm, desc_rows(k_s), desc_rows(q_t));
-                        mma_commit(sfull);
-                    }
-                    __syncwarp();
+                    if (!wait(clean + 8 * qs, tph)) break;
+                    rows(tm, desc_rows(k_s), q_t, sfull, n > 0 ? dsready : clean + 8 * ds, n > 0 ? (n - 1) & 1 : tph);
                     if (n > 0) {
                         // dK of the tile before, whose dS lies in dP
-                        if (!(ok = mbar_wait(dsready, (n - 1) & 1, dead))) break;
-                        fence_after();
-                        if (elect_one()) {
-                            cols(tm + 384, tm + 128, desc_cols(r_s + q_prev * SM::kTile, 16384), n > 1);
-                            mma_commit(empty + 8 * q_prev);
-                        }
-                        __syncwarp();
+                        if (!wait(dsready, (n - 1) & 1)) break;
+                        cols(tm + 384, tm + 128, q_p, n > 1, empty + 8 * q_prev, clean + 8 * ds, tph);
                     }
-                    if (!(ok = mbar_wait(clean + 8 * ds, tph, dead))) break;
-                    if (elect_one()) {
-                        rows(tm + 128, desc_rows(v_s), desc_rows(do_t));
-                        mma_commit(dpfull);
-                    }
-                    __syncwarp();
+                    if (!wait(clean + 8 * ds, tph)) break;
+                    rows(tm + 128, desc_rows(v_s), do_t, dpfull, pready, n & 1);
                     q_prev = qs;
                 } else if (warp == 10) {
                     const uint32_t ss = n % NSS, dst = stat_s + ss * 1024;
@@ -694,7 +765,7 @@ tdp_xattn_dkv_kernel(const __grid_constant__ tdp_geom g, const __grid_constant__
                     for (int i = 0; i < 4; ++i) {
                         const int32_t r = 32 * i + lane, rt = r / a.Gp;
                         float l = -INFINITY, d = 0.f;
-                        if (rt < a.TT && rt < wk.left) {
+                        if (rt < a.TT && rt < left) {
                             const int32_t h = (row + rt) * a.Hq + head + r - rt * a.Gp;
                             l = -row_lse2(__ldg(a.lse + h));
                             d = -__ldcg(a.delta + h);
@@ -706,7 +777,7 @@ tdp_xattn_dkv_kernel(const __grid_constant__ tdp_geom g, const __grid_constant__
                     if (lane == 0) mbar_arrive(tfull + 8 * ss);
                 } else {
                     // rows past the segment's end belong to another tile
-                    const int32_t rows_in = min(wk.left, a.TT) * a.Gp, rows_all = a.TT * a.Gp;
+                    const int32_t rows_in = min(left, a.TT) * a.Gp, rows_all = a.TT * a.Gp;
                     constexpr int C = DP / 8;
 #pragma unroll 1
                     for (int i = 0; i < 2; ++i) {
@@ -730,14 +801,10 @@ tdp_xattn_dkv_kernel(const __grid_constant__ tdp_geom g, const __grid_constant__
         };
         if (warp == 9) {
             if (n > 0 && ok) {
-                ok = mbar_wait(pready, (n - 1) & 1, dead);
-                fence_after();
-                if (ok && elect_one()) cols(tm + 256, tm, desc_cols(r_s + (q_prev + 1) * SM::kTile, 16384), n > 1);
-                __syncwarp();
-                ok = ok && mbar_wait(dsready, (n - 1) & 1, dead);
-                fence_after();
-                if (ok && elect_one()) cols(tm + 384, tm + 128, desc_cols(r_s + q_prev * SM::kTile, 16384), n > 1);
-                __syncwarp();
+                if (wait(pready, (n - 1) & 1))
+                    cols(tm + 256, tm, desc_cols(r_s + (q_prev + 1) * SM::kTile, 16384), n > 1, empty + 8 * (q_prev + 1), dsready, (n - 1) & 1);
+                if (wait(dsready, (n - 1) & 1))
+                    cols(tm + 384, tm + 128, desc_cols(r_s + q_prev * SM::kTile, 16384), n > 1, empty + 8 * q_prev, 0, 0);
             }
             if (elect_one()) mma_commit(drain);
             __syncwarp();
