@@ -11,7 +11,7 @@
 //   warps 0-3, 4-7   columns 0-63, 64-127; the output
 //   warp 8           loads tiles through tensor maps
 //   warp 9           issues the products
-//   warp 10          each row's lse and delta (first kernel: dO . O, an item ahead of the warpgroups)
+//   warp 10          loads Q and dO (first kernel); each row's lse and delta (second)
 //   warp 11          zeroes rows of a tile that must not count (their memory may hold anything, and 0 * NaN is not 0)
 #pragma once
 
@@ -92,12 +92,12 @@ tdp_xattn_dq_kernel(const __grid_constant__ tdp_geom g, const __grid_constant__ 
     const uint32_t base = (smem_u32(raw) + 1023u) & ~1023u;
     const uint32_t q_s = base, do_s = q_s + SM::kTile, kv_s = do_s + SM::kTile, bars = kv_s + NST * SM::kTile, stat_s = bars + 512;
     const uint32_t full = bars, empty = full + 8 * NST, clean = empty + 8 * NST, rfull = clean + 32, rempty = rfull + 16,
-                   tfull = rempty + 16, tempty = tfull + 8, sfull = tempty + 8, pfull = sfull + 16, dsfull = pfull + 8,
+                   sfull = rempty + 16, pfull = sfull + 16, dsfull = pfull + 8,
                    done = dsfull + 8, drain = done + 8;
     __shared__ uint32_t tmem_slot;
     __shared__ int dead_flag;
     volatile int *dead = &dead_flag;
-    const int32_t warp = warp_id(), lane = threadIdx.x & 31;
+    const int32_t warp = role(), lane = threadIdx.x & 31;
     if (warp == 9) tmem_alloc(smem_u32(&tmem_slot), 512);
     if (threadIdx.x == 0) {
         dead_flag = 0;
@@ -111,8 +111,6 @@ tdp_xattn_dq_kernel(const __grid_constant__ tdp_geom g, const __grid_constant__ 
             mbar_init(rempty + 8 * i, i ? 2 : 1);   // dO is given back by the products and by delta
             mbar_init(sfull + 8 * i, 1);
         }
-        mbar_init(tfull, 1);
-        mbar_init(tempty, 8);
         mbar_init(pfull, 1);
         mbar_init(dsfull, 8);
         mbar_init(done, 1);
@@ -135,20 +133,62 @@ tdp_xattn_dq_kernel(const __grid_constant__ tdp_geom g, const __grid_constant__ 
         const uint32_t lanes = tm + ((uint32_t)(warp & 3) << 21);
         const float c = a.scale * kLog2e;
         const bool wide = a.D % 16 == 0 && (reinterpret_cast<uintptr_t>(a.dq) & 31) == 0;      // whole sectors
+        // An item's lse and delta = dO . O, made while the products of the item before run out: each thread half of a
+        // row's products, the halves joined through shared memory.
+        item it;
+        float l, d;
+        auto ahead = [&](int32_t w) {
+            it.left = 0;
+            if (w >= items) return;
+            it = dq_item_at(g, a, w);
+            if (it.left <= 0 || it.keys.n == 0) return;
+            const bool mine = rt < a.TT && rt < it.left;
+            const int32_t h = ((int32_t)(it.seg.row0 + it.tok0) + rt) * a.Hq + it.head + rh;
+            l = -row_lse2(mine ? __ldg(a.lse + h) : -INFINITY);
+            ok = ok && mbar_wait(full + 8 * kv.st, kv.ph, dead) && mbar_wait(rfull + 8, n_items & 1, dead);
+            ++n_items;
+            float sum = 0.f;
+            const uint32_t o_t = kv_s + kv.st * SM::kTile;
+#pragma unroll
+            for (int i = 0; i < DP / 16; ++i) {
+                const int32_t col = half * (DP / 16) + i;       // 16-byte chunk
+                const uint32_t off = (col / 8) * 16384 + panel_off(r, col & 7);
+                uint4 x, y;
+                asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w) : "r"(o_t + off) : "memory");
+                asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(y.x), "=r"(y.y), "=r"(y.z), "=r"(y.w) : "r"(do_s + off) : "memory");
+                float fx[8], fy[8];
+                tdp_elem<1>::unpack(x, fx);
+                tdp_elem<1>::unpack(y, fy);
+#pragma unroll
+                for (int u = 0; u < 8; ++u) sum = fmaf(fx[u], fy[u], sum);
+            }
+            asm volatile("st.shared.f32 [%0], %1;" ::"r"(stat_s + 512 * half + 4 * r), "f"(sum) : "memory");
+            asm volatile("bar.sync 1, 256;" ::: "memory");
+            if (warp == 0 && lane == 0) {
+                mbar_arrive(empty + 8 * kv.st);
+                mbar_arrive(rempty + 8);
+            }
+            float other;
+            asm volatile("ld.shared.f32 %0, [%1];" : "=f"(other) : "r"(stat_s + 512 * (half ^ 1) + 4 * r) : "memory");
+            asm volatile("bar.sync 1, 256;" ::: "memory");
+            d = half ? other + sum : sum + other;
+            if (mine && half == 0) a.delta[h] = d;
+            d = -d;
+            const uint32_t to = kv.st + 1 + 2 * it.keys.n, rounds = to / NST;
+            kv.st = to - rounds * NST;
+            kv.ph ^= rounds & 1;
+        };
+        ahead(blockIdx.x);
         for (int32_t w = blockIdx.x; w < items; w += gridDim.x) {
-            const item it = dq_item_at(g, a, w);
             const int32_t n = it.keys.n;
-            if (it.left <= 0) continue;
+            if (it.left <= 0) {
+                ahead(w + gridDim.x);
+                continue;
+            }
             const bool mine = rt < a.TT && rt < it.left;
             const int32_t h = ((int32_t)(it.seg.row0 + it.tok0) + rt) * a.Hq + it.head + rh;
             if (n > 0) {
-                const uint32_t st = stat_s + 4 * r;
-                ok = ok && mbar_wait(tfull, n_items & 1, dead);
-                float l, d;
-                asm volatile("ld.shared.f32 %0, [%1];" : "=f"(l) : "r"(st) : "memory");
-                asm volatile("ld.shared.f32 %0, [%1];" : "=f"(d) : "r"(st + 512) : "memory");
-                __syncwarp();
-                if (lane == 0) mbar_arrive(tempty);
+                const uint32_t done_ph = (n_items & 1) ^ 1;
                 const uint64_t c2 = pair(c, c), l2 = pair(l, l), d2 = pair(d, d);
 #pragma unroll 1
                 for (int32_t j = 0; j < n && ok; ++j) {
@@ -157,22 +197,22 @@ tdp_xattn_dq_kernel(const __grid_constant__ tdp_geom g, const __grid_constant__ 
                     ok = mbar_wait(sfull + 8 * buf, (n_done >> 1) & 1, dead) && mbar_wait(pfull, n_done & 1, dead);
                     ++n_done;
                     fence_after();
-                    uint32_t s[64], d[64];
+                    uint32_t s[64], e[64];
                     tmem_ld32(S, s);
                     tmem_ld32(S + 32, s + 32);
-                    tmem_ld32(P, d);
-                    tmem_ld32(P + 32, d + 32);
+                    tmem_ld32(P, e);
+                    tmem_ld32(P + 32, e + 32);
                     tmem_wait_ld();
                     tmem_have32(s);
                     tmem_have32(s + 32);
-                    tmem_have32(d);
-                    tmem_have32(d + 32);
+                    tmem_have32(e);
+                    tmem_have32(e + 32);
 #pragma unroll
                     for (int u = 0; u < 32; ++u) {
                         float x, y;
                         unpair(fma2(pair(__uint_as_float(s[2 * u]), __uint_as_float(s[2 * u + 1])), c2, l2), x, y);
                         const uint64_t p = pair(exp2_fast(x), exp2_fast(y));
-                        unpair(mul2(p, add2(pair(__uint_as_float(d[2 * u]), __uint_as_float(d[2 * u + 1])), d2)), x, y);
+                        unpair(mul2(p, add2(pair(__uint_as_float(e[2 * u]), __uint_as_float(e[2 * u + 1])), d2)), x, y);
                         s[2 * u] = __float_as_uint(x);
                         s[2 * u + 1] = __float_as_uint(y);
                     }
@@ -198,11 +238,12 @@ tdp_xattn_dq_kernel(const __grid_constant__ tdp_geom g, const __grid_constant__ 
                     __syncwarp();
                     if (lane == 0) mbar_arrive(dsfull);
                 }
-                if (ok) ok = mbar_wait(done, n_items & 1, dead);
-                ++n_items;
+                ahead(w + gridDim.x);
+                if (ok) ok = mbar_wait(done, done_ph, dead);
                 fence_after();
-            } else if (mine && half == 0) {
-                a.delta[h] = 0.f;
+            } else {
+                if (mine && half == 0) a.delta[h] = 0.f;
+                ahead(w + gridDim.x);
             }
             // dQ, half of the columns each; a lost wait leaves NaN
             T *dst = static_cast<T *>(a.dq) + (int64_t)h * a.D;
@@ -245,24 +286,15 @@ tdp_xattn_dq_kernel(const __grid_constant__ tdp_geom g, const __grid_constant__ 
             if (it.left <= 0 || n == 0 || !ok) continue;
             const int32_t row = (int32_t)(it.seg.row0 + it.tok0);
             const uint32_t ph = n_items & 1;
+            const uint32_t row_bytes = (uint32_t)(a.Gp * a.TT) * DP * 2;
             if (warp == 8) {
-                const uint32_t row_bytes = (uint32_t)(a.Gp * a.TT) * DP * 2;
-                auto load_row = [&](const CUtensorMap *map, int i) {
-                    if (!(ok = ok && mbar_wait(rempty + 8 * i, ph ^ 1, dead))) return;
-                    if (elect_one()) {
-                        mbar_expect(rfull + 8 * i, row_bytes);
-                        for (int p = 0; p < DP / 64; ++p)
-                            tma_load3(base + i * SM::kTile + p * 16384, map, rfull + 8 * i, 64 * p, it.head, row);
-                    }
-                    __syncwarp();
-                };
-                // O, K 0, Q, V 0, dO, K 1, V 1, ...
+                // O, K 0, V 0, K 1, ...
 #pragma unroll 1
                 for (int32_t i = -1; i < 2 * n; ++i) {
                     const bool v = i & 1;
                     const int32_t head = (v ? a.v_head : a.k_head) > 0 ? it.kvh : 0, b = (v ? a.v_item : a.k_item) > 0 ? it.seg.b : 0;
                     const int32_t state = i < 0 ? 0 : it.keys.at(i >> 1) * kKeys;
-                    if (!(ok = ok && mbar_wait(empty + 8 * kv.st, kv.ph ^ 1, dead))) break;
+                    if (!(ok = mbar_wait(empty + 8 * kv.st, kv.ph ^ 1, dead))) break;
                     if (elect_one()) {
                         const uint32_t dst = kv_s + kv.st * SM::kTile, bar = full + 8 * kv.st;
                         mbar_expect(bar, i < 0 ? row_bytes : (uint32_t)SM::kTile);
@@ -273,8 +305,17 @@ tdp_xattn_dq_kernel(const __grid_constant__ tdp_geom g, const __grid_constant__ 
                     }
                     __syncwarp();
                     kv.next();
-                    if (i == 0) load_row(&map_q, 0);
-                    if (i == 1) load_row(&map_do, 1);
+                }
+            } else if (warp == 10) {
+#pragma unroll 1
+                for (int i = 0; i < 2; ++i) {
+                    if (!(ok = mbar_wait(rempty + 8 * i, ph ^ 1, dead))) break;
+                    if (elect_one()) {
+                        mbar_expect(rfull + 8 * i, row_bytes);
+                        for (int p = 0; p < DP / 64; ++p)
+                            tma_load3(base + i * SM::kTile + p * 16384, i ? &map_do : &map_q, rfull + 8 * i, 64 * p, it.head, row);
+                    }
+                    __syncwarp();
                 }
             } else if (warp == 9) {
                 constexpr uint32_t id_s = idesc(128, 128, false, false), id_q = idesc(128, DP, false, true);
@@ -353,55 +394,14 @@ tdp_xattn_dq_kernel(const __grid_constant__ tdp_geom g, const __grid_constant__ 
                     }
                     k_prev = k1;
                 }
-            } else if (warp == 10) {
-                // four rows a lane
-                float lse[4], delta[4];
-                int32_t hs[4];
-                bool mine[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int32_t r = 32 * i + lane, rt = r / a.Gp;
-                    mine[i] = rt < a.TT && rt < it.left;
-                    hs[i] = (row + rt) * a.Hq + it.head + r - rt * a.Gp;
-                    lse[i] = mine[i] ? __ldg(a.lse + hs[i]) : -INFINITY;
-                    delta[i] = 0.f;
-                }
-                ok = mbar_wait(full + 8 * kv.st, kv.ph, dead) && mbar_wait(rfull + 8, ph, dead);
-#pragma unroll 1
-                for (int c = 0; c < DP / 8; ++c)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const uint32_t off = (c / 8) * 16384 + panel_off(32 * i + lane, c & 7);
-                        uint4 x, y;
-                        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w) : "r"(kv_s + kv.st * SM::kTile + off));
-                        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(y.x), "=r"(y.y), "=r"(y.z), "=r"(y.w) : "r"(do_s + off));
-                        float fx[8], fy[8];
-                        tdp_elem<1>::unpack(x, fx);
-                        tdp_elem<1>::unpack(y, fy);
-#pragma unroll
-                        for (int u = 0; u < 8; ++u) delta[i] = fmaf(fx[u], fy[u], delta[i]);
-                    }
-                __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive(empty + 8 * kv.st);
-                    mbar_arrive(rempty + 8);
-                }
-                ok = ok && mbar_wait(tempty, ph ^ 1, dead);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    if (mine[i]) a.delta[hs[i]] = delta[i];
-                    asm volatile("st.shared.f32 [%0], %1;" ::"r"(stat_s + 4 * (32 * i + lane)), "f"(-row_lse2(lse[i])) : "memory");
-                    asm volatile("st.shared.f32 [%0], %1;" ::"r"(stat_s + 512 + 4 * (32 * i + lane)), "f"(-delta[i]) : "memory");
-                }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(tfull);
-                for (int32_t i = 0; i < 1 + 2 * n; ++i) kv.next();
             } else if (a.mask) {
-                kv.next();                      // O
+                // every tile is waited for, in order: a wait for a phase two ahead of the barrier's would return at once
+                ok = mbar_wait(full + 8 * kv.st, kv.ph, dead);          // O
+                kv.next();
 #pragma unroll 1
                 for (int32_t j = 0; j < n; ++j) {
                     const uint4 m = it.keys.mask(j);
-                    if (!(ok = mbar_wait(full + 8 * kv.st, kv.ph, dead))) break;
+                    if (!(ok = ok && mbar_wait(full + 8 * kv.st, kv.ph, dead))) break;
                     constexpr int C = DP / 8;           // 16-byte chunks of a row
 #pragma unroll 1
                     for (int32_t i = whole(m) ? 128 * C : lane; i < 128 * C; i += 32) {
@@ -415,7 +415,8 @@ tdp_xattn_dq_kernel(const __grid_constant__ tdp_geom g, const __grid_constant__ 
                     if (lane == 0) mbar_arrive(clean + 8 * (kc & 3));
                     ++kc;
                     kv.next();
-                    kv.next();                  // V
+                    if (!(ok = mbar_wait(full + 8 * kv.st, kv.ph, dead))) break;       // V
+                    kv.next();
                 }
             }
             ++n_items;
@@ -429,6 +430,7 @@ tdp_xattn_dq_kernel(const __grid_constant__ tdp_geom g, const __grid_constant__ 
     };
     if (warp == 8) {
         for (uint32_t i = 0; i < NST; ++i) landed(full + 8 * i, i < kv.st ? kv.ph : kv.ph ^ 1);
+    } else if (warp == 10) {
         for (int i = 0; i < 2; ++i) landed(rfull + 8 * i, (n_items & 1) ^ 1);
     } else if (warp == 9) {
         if (elect_one()) mma_commit(drain);
@@ -491,7 +493,7 @@ tdp_xattn_dkv_kernel(const __grid_constant__ tdp_geom g, const __grid_constant__
     __shared__ uint32_t tmem_slot;
     __shared__ int dead_flag;
     volatile int *dead = &dead_flag;
-    const int32_t warp = warp_id(), lane = threadIdx.x & 31;
+    const int32_t warp = role(), lane = threadIdx.x & 31;
     if (warp == 9) tmem_alloc(smem_u32(&tmem_slot), 512);
     if (threadIdx.x == 0) {
         dead_flag = 0;

@@ -30,10 +30,20 @@ constexpr float kGrow = 8.f;            // log2 by which a maximum may grow befo
 template <int DP>
 struct fwd_smem {
     static constexpr int kTile = 128 * DP * 2;
-    static constexpr int kStages = DP == 128 ? 4 : 7;
+    // even: a stage always holds K or always V, so that the cleaning warp, which waits for V tiles alone, meets every
+    // phase of their stages' barriers (a wait for a phase two ahead returns at once)
+    static constexpr int kStages = DP == 128 ? 4 : 8;
     static constexpr int kOut = 16384;          // a panel of outputs on its way to memory, per tile
     static constexpr int kBytes = 1024 + (2 + kStages) * kTile + 2 * kOut + 512;
 };
+
+// Number of this warp's role: 0-7 are the hardware's warps 4-11, 8-11 its warps 0-3.  The warps that issue products
+// and loads come first because a scheduler prefers its oldest warps; behind the softmax's they waited for issue slots.
+__device__ __forceinline__ int32_t role()
+{
+    const int32_t w = warp_id();
+    return w < 4 ? w + 8 : w - 4;
+}
 
 // The kept state tiles of an item: with a mask, a list of tiles and of the masks of their states.
 struct key_list {
@@ -109,7 +119,7 @@ tdp_xattn_tc_kernel(const __grid_constant__ tdp_geom g, const __grid_constant__ 
     __shared__ uint32_t tmem_slot;
     __shared__ int dead_flag;
     volatile int *dead = &dead_flag;
-    const int32_t warp = warp_id(), lane = threadIdx.x & 31;
+    const int32_t warp = role(), lane = threadIdx.x & 31;
     if (warp == 9) tmem_alloc(smem_u32(&tmem_slot), 512);
     if (threadIdx.x == 0) {
         dead_flag = 0;
