@@ -13,7 +13,8 @@
 //     blocks join their segment's chunks themselves and run through the rows backwards, so that what the sums
 //     read last is found in the 129 MB L2.  (One grid that takes chunks of sums and, some segments later, of the
 //     elementwise pass in turn would read everything once, but its tickets, joins and flags cost 8 us a
-//     chunk: 934 us at best where these two take 6xx us, 635 million bf16 values.)
+//     chunk: 934 us at best where these two take 609 us, 635 million bf16 values.  Slices of a
+//     few channels kept in a cluster read 32-byte pieces of rows: 2171 us.)
 //   - rows wider than a block's 256 vectors: sums, join and elementwise pass as launches of their own.
 // Variances are sums of squared deviations, of a block's values about their mean or joined by
 // T. Chan's rule, so that a mean far from zero costs no digits.  Every join runs in a fixed order.

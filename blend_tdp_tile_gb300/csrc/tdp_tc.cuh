@@ -39,9 +39,8 @@ __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity)
 
 // This warp's number, uniform to the compiler.
 __device__ __forceinline__ int32_t warp_id() { return __shfl_sync(~0u, (int)(threadIdx.x >> 5), 0); }
-// One lane of a converged warp.  The tensor-core and tensor-map instructions take uniform registers: behind elect.sync
-// the compiler knows that one lane runs, behind a lane number it wraps each of them in a loop over the lanes
-// (2 KB and 75 cycles a product instead of 64).
+// One lane of a converged warp.  The tensor-core and tensor-map instructions take uniform registers; behind elect.sync the
+// compiler knows that a single lane runs (behind a lane number it adds some 120 bytes of code to each of them).
 __device__ __forceinline__ bool elect_one()
 {
     uint32_t on;

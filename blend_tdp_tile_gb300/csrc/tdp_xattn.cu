@@ -1,5 +1,5 @@
 // tdp_xattn.cu -- cross attention of the tiles' tokens to an encoder's states, and its
-// gradients: entry points and the CUDA-core kernels.
+// gradients: entry points and the fp32 kernels on the CUDA cores (bf16: tdp_xattn_tc.cuh, tdp_xattn_grad_tc.cuh).
 //
 // out = softmax(scale * Q K^T over the kept states) V, one pass over the states with the
 // running maximum m and sum l of the softmax: a block holds 64 packed rows, takes 64
@@ -29,25 +29,16 @@ struct xsm {
     static constexpr int kPs = kXN + 4;
 };
 
-// 64 rows of D elements to smem as fp32, zero past D and where row(i) gives NULL.
-template <int BF16, int DP, typename Row>
+// 64 rows of D elements to smem, zero past D and where row(i) gives NULL.
+template <int DP, typename Row>
 __device__ __forceinline__ void load_tile(float *dst, int32_t D, Row row)
 {
-    using E = tdp_elem<BF16>;
-    constexpr int V = E::kVec, NV = DP / V;
+    constexpr int NV = DP / 4;
     for (int32_t i = threadIdx.x; i < 64 * NV; i += kXT) {
         const int32_t r = i / NV, c = i % NV;
-        const typename E::type *p = static_cast<const typename E::type *>(row(r));
-        float f[V];
-        if (p && c * V < D) {
-            E::unpack(*reinterpret_cast<const uint4 *>(p + c * V), f);
-        } else {
-#pragma unroll
-            for (int j = 0; j < V; ++j) f[j] = 0.f;
-        }
-#pragma unroll
-        for (int j = 0; j < V; j += 4)
-            *reinterpret_cast<float4 *>(dst + r * xsm<DP>::kLd + c * V + j) = make_float4(f[j], f[j + 1], f[j + 2], f[j + 3]);
+        const float *p = row(r);
+        *reinterpret_cast<float4 *>(dst + r * xsm<DP>::kLd + c * 4) =
+            p && c * 4 < D ? *reinterpret_cast<const float4 *>(p + c * 4) : make_float4(0.f, 0.f, 0.f, 0.f);
     }
 }
 
@@ -134,15 +125,13 @@ __device__ __forceinline__ int64_t packed(const xattn_args &a, const tdp_seg &se
     return (seg.row0 + tok) * row + (kvh * a.G + (int32_t)(r - tok * a.G)) * head;
 }
 
-// log2 of the row's sum of exponentials; a row with no sum gets +inf, which makes its probabilities zero.
-__device__ __forceinline__ float lse2(float lse) { return lse == -INFINITY ? INFINITY : lse * kLog2e; }
+// A row's log-sum; a row with no sum gets +inf, which makes its probabilities zero.
+__device__ __forceinline__ float row_lse(float lse) { return lse == -INFINITY ? INFINITY : lse; }
 
-template <int BF16, int DP>
+template <int DP>
 __global__ void __launch_bounds__(kXT)
 tdp_xattn_simt_kernel(const __grid_constant__ tdp_geom g, const __grid_constant__ xattn_args a)
 {
-    using E = tdp_elem<BF16>;
-    using T = typename E::type;
     extern __shared__ __align__(16) float sm[];
     float *Qs = sm, *Ks = Qs + xsm<DP>::kTile, *Vs = Ks + xsm<DP>::kTile, *Ps = Vs + xsm<DP>::kTile;
     __shared__ uint32_t bits[2];
@@ -159,9 +148,9 @@ tdp_xattn_simt_kernel(const __grid_constant__ tdp_geom g, const __grid_constant_
     tdp_pdl_wait();
     if (nr <= 0) return;
     const uint8_t *mask = xattn_mask(a, g, seg);
-    const T *q = static_cast<const T *>(a.q), *k = static_cast<const T *>(a.k) + seg.b * a.k_item + kvh * a.k_head,
-            *v = static_cast<const T *>(a.v) + seg.b * a.v_item + kvh * a.v_head;
-    load_tile<BF16, DP>(Qs, a.D, [&](int32_t r) { return r < nr ? q + packed(a, seg, kvh, r0 + r, a.q_row, a.q_head) : nullptr; });
+    const float *q = static_cast<const float *>(a.q), *k = static_cast<const float *>(a.k) + seg.b * a.k_item + kvh * a.k_head,
+            *v = static_cast<const float *>(a.v) + seg.b * a.v_item + kvh * a.v_head;
+    load_tile<DP>(Qs, a.D, [&](int32_t r) { return r < nr ? q + packed(a, seg, kvh, r0 + r, a.q_row, a.q_head) : nullptr; });
     float m[4], l[4], acc[4][DP / 16];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -177,8 +166,8 @@ tdp_xattn_simt_kernel(const __grid_constant__ tdp_geom g, const __grid_constant_
         if (!kept_bits(mask, t * kXN, a.S, bits)) continue;
         const uint32_t b0 = bits[0], b1 = bits[1];
         auto kept = [&](int32_t j) { return ((j < 32 ? b0 >> j : b1 >> (j - 32)) & 1) != 0; };
-        load_tile<BF16, DP>(Ks, a.D, [&](int32_t j) { return kept(j) ? k + (int64_t)(t * kXN + j) * a.k_state : nullptr; });
-        load_tile<BF16, DP>(Vs, a.D, [&](int32_t j) { return kept(j) ? v + (int64_t)(t * kXN + j) * a.v_state : nullptr; });
+        load_tile<DP>(Ks, a.D, [&](int32_t j) { return kept(j) ? k + (int64_t)(t * kXN + j) * a.k_state : nullptr; });
+        load_tile<DP>(Vs, a.D, [&](int32_t j) { return kept(j) ? v + (int64_t)(t * kXN + j) * a.v_state : nullptr; });
         __syncthreads();
         float s[4][4];
         dot_tile<DP>(Qs, Ks, ty, tx, s);
@@ -227,7 +216,7 @@ tdp_xattn_simt_kernel(const __grid_constant__ tdp_geom g, const __grid_constant_
 #pragma unroll
             for (int c = 0; c < DP / 16; ++c) {
                 const int32_t d = 64 * (c / 4) + 4 * tx + c % 4;
-                if (d < a.D) static_cast<T *>(a.out)[h * a.D + d] = (T)(acc[i][c] * inv);
+                if (d < a.D) static_cast<float *>(a.out)[h * a.D + d] = acc[i][c] * inv;
             }
         }
     }
@@ -266,12 +255,10 @@ tdp_xattn_join_kernel(const xattn_args a)
 }
 
 // dq of 64 packed rows; delta = dout . out is written for the kernel that follows.
-template <int BF16, int DP>
+template <int DP>
 __global__ void __launch_bounds__(kXT)
 tdp_xattn_simt_dq_kernel(const __grid_constant__ tdp_geom g, const __grid_constant__ xattn_args a)
 {
-    using E = tdp_elem<BF16>;
-    using T = typename E::type;
     extern __shared__ __align__(16) float sm[];
     float *Qs = sm, *Ds = Qs + xsm<DP>::kTile, *Ks = Ds + xsm<DP>::kTile, *Vs = Ks + xsm<DP>::kTile,
           *Ps = Vs + xsm<DP>::kTile;
@@ -287,13 +274,13 @@ tdp_xattn_simt_dq_kernel(const __grid_constant__ tdp_geom g, const __grid_consta
     tdp_pdl_wait();
     if (nr <= 0) return;
     const uint8_t *mask = xattn_mask(a, g, seg);
-    const T *q = static_cast<const T *>(a.q), *k = static_cast<const T *>(a.k) + seg.b * a.k_item + kvh * a.k_head,
-            *v = static_cast<const T *>(a.v) + seg.b * a.v_item + kvh * a.v_head;
-    auto row = [&](const void *p, int32_t r) -> const T * {
-        return r < nr ? static_cast<const T *>(p) + packed(a, seg, kvh, r0 + r, (int64_t)a.Hq * a.D, a.D) : nullptr;
+    const float *q = static_cast<const float *>(a.q), *k = static_cast<const float *>(a.k) + seg.b * a.k_item + kvh * a.k_head,
+            *v = static_cast<const float *>(a.v) + seg.b * a.v_item + kvh * a.v_head;
+    auto row = [&](const void *p, int32_t r) -> const float * {
+        return r < nr ? static_cast<const float *>(p) + packed(a, seg, kvh, r0 + r, (int64_t)a.Hq * a.D, a.D) : nullptr;
     };
-    load_tile<BF16, DP>(Qs, a.D, [&](int32_t r) { return row(a.o, r); });
-    load_tile<BF16, DP>(Ds, a.D, [&](int32_t r) { return row(a.dout, r); });
+    load_tile<DP>(Qs, a.D, [&](int32_t r) { return row(a.o, r); });
+    load_tile<DP>(Ds, a.D, [&](int32_t r) { return row(a.dout, r); });
     __syncthreads();
     float lse[4], delta[4];
 #pragma unroll
@@ -305,25 +292,24 @@ tdp_xattn_simt_dq_kernel(const __grid_constant__ tdp_geom g, const __grid_consta
         lse[i] = INFINITY;
         if (r < nr) {
             const int64_t h = packed(a, seg, kvh, r0 + r, a.Hq, 1);
-            lse[i] = lse2(a.lse[h]);
+            lse[i] = row_lse(a.lse[h]);
             if (tx == 0) a.delta[h] = delta[i];
         }
     }
     __syncthreads();
-    load_tile<BF16, DP>(Qs, a.D, [&](int32_t r) { return r < nr ? q + packed(a, seg, kvh, r0 + r, a.q_row, a.q_head) : nullptr; });
+    load_tile<DP>(Qs, a.D, [&](int32_t r) { return r < nr ? q + packed(a, seg, kvh, r0 + r, a.q_row, a.q_head) : nullptr; });
     float acc[4][DP / 16];
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
         for (int c = 0; c < DP / 16; ++c) acc[i][c] = 0.f;
-    const float c2 = a.scale * kLog2e;
     for (int32_t t = 0; t * kXN < a.S; ++t) {
         __syncthreads();
         if (!kept_bits(mask, t * kXN, a.S, bits)) continue;
         const uint32_t b0 = bits[0], b1 = bits[1];
         auto kept = [&](int32_t j) { return ((j < 32 ? b0 >> j : b1 >> (j - 32)) & 1) != 0; };
-        load_tile<BF16, DP>(Ks, a.D, [&](int32_t j) { return kept(j) ? k + (int64_t)(t * kXN + j) * a.k_state : nullptr; });
-        load_tile<BF16, DP>(Vs, a.D, [&](int32_t j) { return kept(j) ? v + (int64_t)(t * kXN + j) * a.v_state : nullptr; });
+        load_tile<DP>(Ks, a.D, [&](int32_t j) { return kept(j) ? k + (int64_t)(t * kXN + j) * a.k_state : nullptr; });
+        load_tile<DP>(Vs, a.D, [&](int32_t j) { return kept(j) ? v + (int64_t)(t * kXN + j) * a.v_state : nullptr; });
         __syncthreads();
         float s[4][4], dp[4][4];
         dot_tile<DP>(Qs, Ks, ty, tx, s);
@@ -333,7 +319,7 @@ tdp_xattn_simt_dq_kernel(const __grid_constant__ tdp_geom g, const __grid_consta
 #pragma unroll
             for (int j = 0; j < 4; ++j)
                 Ps[(4 * ty + i) * xsm<DP>::kPs + tx + 16 * j] =
-                    kept(tx + 16 * j) ? exp2f(s[i][j] * c2 - lse[i]) * (dp[i][j] - delta[i]) * a.scale : 0.f;
+                    kept(tx + 16 * j) ? expf(fmaf(s[i][j], a.scale, -lse[i])) * (dp[i][j] - delta[i]) * a.scale : 0.f;
         __syncwarp();
         mul_tile<DP>(Ps, Ks, ty, tx, acc);
     }
@@ -341,28 +327,26 @@ tdp_xattn_simt_dq_kernel(const __grid_constant__ tdp_geom g, const __grid_consta
     for (int i = 0; i < 4; ++i) {
         const int32_t r = 4 * ty + i;
         if (r >= nr) continue;
-        T *o = const_cast<T *>(row(a.dq, r));
+        float *o = const_cast<float *>(row(a.dq, r));
 #pragma unroll
         for (int c = 0; c < DP / 16; ++c) {
             const int32_t d = 64 * (c / 4) + 4 * tx + c % 4;
-            if (d < a.D) o[d] = (T)acc[i][c];
+            if (d < a.D) o[d] = acc[i][c];
         }
     }
 }
 
 // dk and dv of 64 states: the transposed tiles, states as rows, over a part of the row blocks of
 // every segment of the item.
-template <int BF16, int DP>
+template <int DP>
 __global__ void __launch_bounds__(kXT)
 tdp_xattn_simt_dkv_kernel(const __grid_constant__ tdp_geom g, const __grid_constant__ xattn_args a)
 {
-    using E = tdp_elem<BF16>;
-    using T = typename E::type;
     extern __shared__ __align__(16) float sm[];
     float *Ks = sm, *Vs = Ks + xsm<DP>::kTile, *Qs = Vs + xsm<DP>::kTile, *Ds = Qs + xsm<DP>::kTile,
           *Ps = Ds + xsm<DP>::kTile, *Ss = Ps + 64 * xsm<DP>::kPs;
     __shared__ uint32_t bits[2];
-    __shared__ float row_lse[kXM], row_delta[kXM];
+    __shared__ float row_ls[kXM], row_delta[kXM];
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
     const int32_t tiles = (a.S + kXN - 1) / kXN;
     int32_t w = blockIdx.x;
@@ -373,18 +357,17 @@ tdp_xattn_simt_dkv_kernel(const __grid_constant__ tdp_geom g, const __grid_const
     const int32_t part = w % a.split, b = w / a.split;
     tdp_pdl_trigger();
     tdp_pdl_wait();
-    const T *q = static_cast<const T *>(a.q), *k = static_cast<const T *>(a.k) + b * a.k_item + kvh * a.k_head,
-            *v = static_cast<const T *>(a.v) + b * a.v_item + kvh * a.v_head;
+    const float *q = static_cast<const float *>(a.q), *k = static_cast<const float *>(a.k) + b * a.k_item + kvh * a.k_head,
+            *v = static_cast<const float *>(a.v) + b * a.v_item + kvh * a.v_head;
     // a state no mask of its segments keeps is never multiplied by a kept probability, but
     // another tile's may keep it: the tiles are loaded as they are and selected per segment
-    load_tile<BF16, DP>(Ks, a.D, [&](int32_t j) { return t * kXN + j < a.S ? k + (int64_t)(t * kXN + j) * a.k_state : nullptr; });
-    load_tile<BF16, DP>(Vs, a.D, [&](int32_t j) { return t * kXN + j < a.S ? v + (int64_t)(t * kXN + j) * a.v_state : nullptr; });
+    load_tile<DP>(Ks, a.D, [&](int32_t j) { return t * kXN + j < a.S ? k + (int64_t)(t * kXN + j) * a.k_state : nullptr; });
+    load_tile<DP>(Vs, a.D, [&](int32_t j) { return t * kXN + j < a.S ? v + (int64_t)(t * kXN + j) * a.v_state : nullptr; });
     float dk[4][DP / 16], dv[4][DP / 16];
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
         for (int c = 0; c < DP / 16; ++c) dk[i][c] = dv[i][c] = 0.f;
-    const float c2 = a.scale * kLog2e;
     const int32_t nsegs = a.flat ? 1 : g.nt;
     const int64_t first = (int64_t)part * a.part, last = min((int64_t)nsegs * a.blocks, first + a.part);
     int32_t cur = -1;
@@ -404,18 +387,18 @@ tdp_xattn_simt_dkv_kernel(const __grid_constant__ tdp_geom g, const __grid_const
         const uint32_t b0 = bits[0], b1 = bits[1];
         auto kept = [&](int32_t j) { return ((j < 32 ? b0 >> j : b1 >> (j - 32)) & 1) != 0; };
         __syncthreads();
-        load_tile<BF16, DP>(Qs, a.D, [&](int32_t r) { return r < nr ? q + packed(a, seg, kvh, r0 + r, a.q_row, a.q_head) : nullptr; });
-        load_tile<BF16, DP>(Ds, a.D, [&](int32_t r) {
-            return r < nr ? static_cast<const T *>(a.dout) + packed(a, seg, kvh, r0 + r, (int64_t)a.Hq * a.D, a.D) : nullptr;
+        load_tile<DP>(Qs, a.D, [&](int32_t r) { return r < nr ? q + packed(a, seg, kvh, r0 + r, a.q_row, a.q_head) : nullptr; });
+        load_tile<DP>(Ds, a.D, [&](int32_t r) {
+            return r < nr ? static_cast<const float *>(a.dout) + packed(a, seg, kvh, r0 + r, (int64_t)a.Hq * a.D, a.D) : nullptr;
         });
         if (threadIdx.x < kXM) {
             float ls = INFINITY, de = 0.f;
             if (threadIdx.x < nr) {
                 const int64_t h = packed(a, seg, kvh, r0 + threadIdx.x, a.Hq, 1);
-                ls = lse2(a.lse[h]);
+                ls = row_lse(a.lse[h]);
                 de = a.delta[h];
             }
-            row_lse[threadIdx.x] = ls;
+            row_ls[threadIdx.x] = ls;
             row_delta[threadIdx.x] = de;
         }
         __syncthreads();
@@ -428,7 +411,7 @@ tdp_xattn_simt_dkv_kernel(const __grid_constant__ tdp_geom g, const __grid_const
             for (int j = 0; j < 4; ++j) {
                 const int32_t r = tx + 16 * j;
                 const bool on = kept(4 * ty + i);
-                const float p = on ? exp2f(s[i][j] * c2 - row_lse[r]) : 0.f;
+                const float p = on ? expf(fmaf(s[i][j], a.scale, -row_ls[r])) : 0.f;
                 Ps[(4 * ty + i) * xsm<DP>::kPs + r] = p;
                 Ss[(4 * ty + i) * xsm<DP>::kPs + r] = on ? p * (dp[i][j] - row_delta[r]) * a.scale : 0.f;
             }
@@ -449,8 +432,8 @@ tdp_xattn_simt_dkv_kernel(const __grid_constant__ tdp_geom g, const __grid_const
                 a.pk[all + at + d] = dk[i][c];
                 a.pv[all + at + d] = dv[i][c];
             } else {
-                static_cast<T *>(a.dk)[at + d] = (T)dk[i][c];
-                static_cast<T *>(a.dv)[at + d] = (T)dv[i][c];
+                static_cast<float *>(a.dk)[at + d] = dk[i][c];
+                static_cast<float *>(a.dv)[at + d] = dv[i][c];
             }
         }
     }
@@ -745,7 +728,7 @@ cudaError_t tc_grad(const tdp_geom &g, const xattn_args &a, cudaStream_t s)
     return e;
 }
 
-template <int BF16, int DP>
+template <int DP>
 struct simt_kernels {
     static constexpr size_t kFwd = (3 * xsm<DP>::kTile + 64 * xsm<DP>::kPs) * 4;
     static constexpr size_t kDq = (4 * xsm<DP>::kTile + 64 * xsm<DP>::kPs) * 4;
@@ -758,9 +741,9 @@ struct simt_kernels {
         cudaError_t e = cudaGetDevice(&dev);
         if (e != cudaSuccess || (dev < 64 && done[dev].load(std::memory_order_relaxed))) return e;
         const auto attr = cudaFuncAttributeMaxDynamicSharedMemorySize;
-        e = cudaFuncSetAttribute(tdp_xattn_simt_kernel<BF16, DP>, attr, (int)kFwd);
-        if (e == cudaSuccess) e = cudaFuncSetAttribute(tdp_xattn_simt_dq_kernel<BF16, DP>, attr, (int)kDq);
-        if (e == cudaSuccess) e = cudaFuncSetAttribute(tdp_xattn_simt_dkv_kernel<BF16, DP>, attr, (int)kDkv);
+        e = cudaFuncSetAttribute(tdp_xattn_simt_kernel<DP>, attr, (int)kFwd);
+        if (e == cudaSuccess) e = cudaFuncSetAttribute(tdp_xattn_simt_dq_kernel<DP>, attr, (int)kDq);
+        if (e == cudaSuccess) e = cudaFuncSetAttribute(tdp_xattn_simt_dkv_kernel<DP>, attr, (int)kDkv);
         if (e == cudaSuccess && dev < 64) done[dev].store(true, std::memory_order_relaxed);
         return e;
     }
@@ -768,20 +751,20 @@ struct simt_kernels {
     {
         cudaError_t e = prepare();
         if (e == cudaSuccess)
-            e = tdp_launch_smem(true, tdp_xattn_simt_kernel<BF16, DP>, (unsigned)(a.segs * a.split * a.Hkv * a.blocks), kXT, kFwd, s, g, a);
+            e = tdp_launch_smem(true, tdp_xattn_simt_kernel<DP>, (unsigned)(a.segs * a.split * a.Hkv * a.blocks), kXT, kFwd, s, g, a);
         return e;
     }
     static cudaError_t dq(const tdp_geom &g, const xattn_args &a, cudaStream_t s)
     {
         cudaError_t e = prepare();
         if (e == cudaSuccess)
-            e = tdp_launch_smem(true, tdp_xattn_simt_dq_kernel<BF16, DP>, (unsigned)(a.segs * a.Hkv * a.blocks), kXT, kDq, s, g, a);
+            e = tdp_launch_smem(true, tdp_xattn_simt_dq_kernel<DP>, (unsigned)(a.segs * a.Hkv * a.blocks), kXT, kDq, s, g, a);
         return e;
     }
     static cudaError_t dkv(const tdp_geom &g, const xattn_args &a, cudaStream_t s)
     {
         const unsigned grid = (unsigned)(g.B * a.split * a.Hkv * ((a.S + kXN - 1) / kXN));
-        return tdp_launch_smem(true, tdp_xattn_simt_dkv_kernel<BF16, DP>, grid, kXT, kDkv, s, g, a);
+        return tdp_launch_smem(true, tdp_xattn_simt_dkv_kernel<DP>, grid, kXT, kDkv, s, g, a);
     }
 };
 
@@ -833,7 +816,7 @@ extern "C" tdp_status tdp_cross_attn(tdp_plan_t plan, const tdp_xattn *p, const 
         err = tc_kept(sh, &a, w, s);
         if (err == cudaSuccess) err = a.D <= 64 ? tc_forward<64>(g, a, s) : tc_forward<128>(g, a, s);
     } else {
-        err = a.D <= 64 ? simt_kernels<0, 64>::forward(g, a, s) : simt_kernels<0, 128>::forward(g, a, s);
+        err = a.D <= 64 ? simt_kernels<64>::forward(g, a, s) : simt_kernels<128>::forward(g, a, s);
     }
     if (err == cudaSuccess && a.split > 1) {
         const unsigned grid = (unsigned)((a.rows * a.Hq * 32 + kXT - 1) / kXT);
@@ -884,8 +867,8 @@ extern "C" tdp_status tdp_cross_attn_grad(tdp_plan_t plan, const tdp_xattn *p, c
         err = tc_kept(sh, &a, w, s);
         if (err == cudaSuccess) err = a.D <= 64 ? tc_grad<64>(g, a, s) : tc_grad<128>(g, a, s);
     } else {
-        err = a.D <= 64 ? simt_kernels<0, 64>::dq(g, a, s) : simt_kernels<0, 128>::dq(g, a, s);
-        if (err == cudaSuccess && a.S > 0) err = a.D <= 64 ? simt_kernels<0, 64>::dkv(g, a, s) : simt_kernels<0, 128>::dkv(g, a, s);
+        err = a.D <= 64 ? simt_kernels<64>::dq(g, a, s) : simt_kernels<128>::dq(g, a, s);
+        if (err == cudaSuccess && a.S > 0) err = a.D <= 64 ? simt_kernels<64>::dkv(g, a, s) : simt_kernels<128>::dkv(g, a, s);
     }
     if (err == cudaSuccess && a.S > 0) {
         if (err == cudaSuccess && a.split > 1) {

@@ -19,19 +19,6 @@
 
 namespace tdp_xt {
 
-// A place in a ring of N stages and the phase of its barriers.
-template <int N>
-struct ring {
-    uint32_t st, ph;
-    __device__ __forceinline__ void next()
-    {
-        if (++st == N) {
-            st = 0;
-            ph ^= 1;
-        }
-    }
-};
-
 template <int DP>
 struct dq_smem {
     static constexpr int kTile = 128 * DP * 2;

@@ -3,7 +3,7 @@
 // A block takes two tiles of 128 packed rows against the same key head and walks the kept
 // 128-state tiles.  For tile t: S_t = Q_t K^T (tensor memory, fp32), p = exp2(c S_t - m) by one warpgroup,
 // a row a thread, written back to tensor memory over S_t as bf16, O_t += P_t V.  While one tile's
-// probabilities are computed the other tile's products run:
+// probabilities are computed the other tile's products run; scores are made two or three (kScores) tiles ahead:
 //   warps 0-3, 4-7   softmax of tile 0, 1 and its output
 //   warp 8, 10       load K and V tiles, Q tiles, through tensor maps
 //   warp 9           issues the products; P V starts when half of the probabilities are there
@@ -33,6 +33,9 @@ struct fwd_smem {
     // even: a stage always holds K or always V, so that the cleaning warp, which waits for V tiles alone, meets every
     // phase of their stages' barriers (a wait for a phase two ahead returns at once)
     static constexpr int kStages = DP == 128 ? 4 : 8;
+    // Buffers of scores in tensor memory, beside the outputs.  The third lets a tile's next scores be made while its
+    // softmax works: 64 columns a head are bound by the softmax, not by the products.
+    static constexpr int kScores = DP == 128 ? 2 : 3;
     static constexpr int kOut = 16384;          // a panel of outputs on its way to memory, per tile
     static constexpr int kBytes = 1024 + (2 + kStages) * kTile + 2 * kOut + 512;
 };
@@ -44,6 +47,25 @@ __device__ __forceinline__ int32_t role()
     const int32_t w = warp_id();
     return w < 4 ? w + 8 : w - 4;
 }
+
+// A place in a ring of N stages and the phase of its barriers.
+template <int N>
+struct ring {
+    uint32_t st, ph;
+    __device__ __forceinline__ void next()
+    {
+        if (++st == N) {
+            st = 0;
+            ph ^= 1;
+        }
+    }
+    __device__ __forceinline__ void advance(uint32_t k)
+    {
+        const uint32_t to = st + k, rounds = to / N;
+        st = to - rounds * N;
+        ph ^= rounds & 1;
+    }
+};
 
 // The kept state tiles of an item: with a mask, a list of tiles and of the masks of their states.
 struct key_list {
@@ -109,13 +131,14 @@ tdp_xattn_tc_kernel(const __grid_constant__ tdp_geom g, const __grid_constant__ 
 {
     using SM = fwd_smem<DP>;
     using T = __nv_bfloat16;
-    constexpr int NST = SM::kStages;
+    constexpr int NST = SM::kStages, NB = SM::kScores;
+    constexpr uint32_t kO = NB * 128;           // first column of the outputs
     extern __shared__ unsigned char raw[];
     const uint32_t base = (smem_u32(raw) + 1023u) & ~1023u;
     const uint32_t q_s = base, kv_s = base + 2 * SM::kTile, out_s = kv_s + NST * SM::kTile,
                    bars = out_s + 2 * SM::kOut;
     const uint32_t full = bars, empty = full + 8 * NST, clean = empty + 8 * NST, qfull = clean + 8 * NST, qempty = qfull + 16,
-                   sfull = qempty + 16, phalf = sfull + 16, pfull = phalf + 16, odone = pfull + 16, drain = odone + 16;
+                   sfull = qempty + 16, phalf = sfull + 32, pfull = phalf + 8 * NB, odone = pfull + 8 * NB, drain = odone + 32;
     __shared__ uint32_t tmem_slot;
     __shared__ int dead_flag;
     volatile int *dead = &dead_flag;
@@ -131,10 +154,14 @@ tdp_xattn_tc_kernel(const __grid_constant__ tdp_geom g, const __grid_constant__ 
         for (int t = 0; t < 2; ++t) {
             mbar_init(qfull + 8 * t, 1);
             mbar_init(qempty + 8 * t, 1);
-            mbar_init(sfull + 8 * t, 1);
-            mbar_init(phalf + 8 * t, 4);
-            mbar_init(pfull + 8 * t, 4);
-            mbar_init(odone + 8 * t, 1);
+            for (int b = 0; b < 16; b += 8) {
+                mbar_init(sfull + 16 * t + b, 1);
+                mbar_init(odone + 16 * t + b, 1);
+            }
+        }
+        for (int b = 0; b < NB; ++b) {
+            mbar_init(phalf + 8 * b, 4);
+            mbar_init(pfull + 8 * b, 4);
         }
         mbar_init(drain, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -151,18 +178,26 @@ tdp_xattn_tc_kernel(const __grid_constant__ tdp_geom g, const __grid_constant__ 
     // for the three warps of a scheduler; 216 + 216 + 72 of them from here on.
     bool ok = true;
     uint32_t kv = 0;                        // K and V tiles so far: K and V take turns
-    uint32_t ph = 0, ph2 = 0;               // phases of this role's barriers, a bit each
+    uint32_t ph = 0, ph2 = 0;               // phases of this role's barriers, a bit each (softmax: score tiles so far)
     if (warp < 8) {
         regs_inc<216>();
         const int32_t t = warp >> 2;            // tile
-        const uint32_t S = tm + ((uint32_t)(warp & 3) << 21) + 128 * t, O = S + 256 + (DP - 128) * t;   // this warp's lanes
+        const uint32_t lanes = tm + ((uint32_t)(warp & 3) << 21), O = lanes + kO + DP * t;       // this warp's lanes
+        ring<NB> scores = {0, 0};               // buffer of the item's first scores
         // a scale of zero weighs every state alike, and so does one too small to matter; -inf stays -inf
         const float c = fmaxf(fabsf(a.scale) * kLog2e, 1e-30f);
         const int32_t r = threadIdx.x & 127, rt = r / a.Gp, rh = r - rt * a.Gp;         // row, its token and head
+        // A tile's scores and its P V have two barriers each, in turn.  The next scores may be there before these are looked
+        // at, and the products of the last step may still run: scores say that the products two steps back are done.
+        auto products = [&](uint32_t i) { return mbar_wait(odone + 16 * t + 8 * (i & 1), (i >> 1) & 1, dead); };
         for (int32_t w = blockIdx.x; w < items; w += gridDim.x) {
             const item it = item_at(g, a, w);
             const int32_t n = it.keys.n;
-            if (it.left <= t * a.TT) continue;
+            const uint32_t nt = it.left > a.TT ? 2 : it.left > 0 ? 1 : 0;
+            ring<NB> cur = scores;
+            scores.advance(n * nt);
+            if ((uint32_t)t >= nt) continue;
+            if (t == 1) cur.next();
             const bool mine = rt < a.TT && t * a.TT + rt < it.left;
             const bool warp_on = __any_sync(~0u, mine);
             const bool by_map = a.split == 1 && it.left - t * a.TT >= a.TT;
@@ -171,9 +206,11 @@ tdp_xattn_tc_kernel(const __grid_constant__ tdp_geom g, const __grid_constant__ 
 #pragma unroll 1
             for (int32_t j = 0; j < n && ok; ++j) {
                 const uint4 mk = it.keys.mask(j);
-                ok = mbar_wait(sfull + 8 * t, ph & 1, dead);
-                ph ^= 1;
+                const uint32_t S = lanes + 128 * cur.st, half = phalf + 8 * cur.st, whole_p = pfull + 8 * cur.st;
+                ok = mbar_wait(sfull + 16 * t + 8 * (ph & 1), (ph >> 1) & 1, dead);
                 if (!ok) break;
+                ++ph;
+                cur.advance(nt);
                 fence_after();
                 if (warp_on) {
                     if (!whole(mk)) {
@@ -217,7 +254,7 @@ tdp_xattn_tc_kernel(const __grid_constant__ tdp_geom g, const __grid_constant__ 
                         l *= f;
                         m = mn;
                         if (j > 0) {
-                            ok = mbar_wait(odone + 8 * t, ph2 & 1, dead);
+                            ok = products(ph - 2);
                             fence_after();
 #pragma unroll 1
                             for (int i = 0; i < DP / 16; ++i) {
@@ -252,7 +289,7 @@ tdp_xattn_tc_kernel(const __grid_constant__ tdp_geom g, const __grid_constant__ 
                     tmem_wait_st();
                     fence_before();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(phalf + 8 * t);
+                    if (lane == 0) mbar_arrive(half);
                     exp32(z, 2);
                     exp32(z + 32, 3);
                     float x, y;
@@ -260,17 +297,15 @@ tdp_xattn_tc_kernel(const __grid_constant__ tdp_geom g, const __grid_constant__ 
                     l += x + y;
                     tmem_wait_st();
                 } else if (lane == 0) {
-                    mbar_arrive(phalf + 8 * t);
+                    mbar_arrive(half);
                 }
-                if (j > 0) ph2 ^= 1;
                 fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(pfull + 8 * t);
+                if (lane == 0) mbar_arrive(whole_p);
             }
             // output: O / l, or zero where nothing is kept, or NaN after a lost wait
             if (n > 0 && ok) {
-                ok = mbar_wait(odone + 8 * t, ph2 & 1, dead);
-                ph2 ^= 1;
+                ok = products(ph - 1);
                 fence_after();
             }
             const int32_t h = (row0 + rt) * a.Hq + head + rh;
@@ -326,6 +361,7 @@ tdp_xattn_tc_kernel(const __grid_constant__ tdp_geom g, const __grid_constant__ 
         if (r == 0) tma_store_done();
     } else {
         regs_dec<72>();
+        ring<NB> made = {0, 0}, used = {0, 0};      // products: buffers of scores to be made and used
         for (int32_t w = blockIdx.x; w < items; w += gridDim.x) {
             const item it = item_at(g, a, w);
             const int32_t n = it.keys.n, nt = it.left > a.TT ? 2 : 1;
@@ -363,62 +399,95 @@ tdp_xattn_tc_kernel(const __grid_constant__ tdp_geom g, const __grid_constant__ 
             } else if (warp == 9) {
                 constexpr uint32_t id_pv = idesc(128, DP, false, true);
                 const uint32_t id_qk = idesc(128, 128, false, false) | (a.scale < 0.f ? kNegateA : 0u);
-                // round j: P V of state tile j, then Q K^T of tile j + 1, of each row tile
-#pragma unroll 1
-                for (int32_t j = -1; j < n && ok; ++j) {
-                    const uint32_t v = kv + 2 * j + 1, vs = v % NST, ks = (v + 1) % NST;
-#pragma unroll 1
-                    for (int q = 0; q < nt; ++q) {
-                        if (j >= 0) {
-                            // V comes by way of the cleaning warp where there is a mask
-                            if (q == 0) {
-                                ok = a.mask ? mbar_wait(clean + 8 * vs, (ph2 >> vs) & 1, dead) : mbar_wait(full + 8 * vs, (v / NST) & 1, dead);
-                                ph2 ^= 1u << vs;
-                            }
-                            const uint32_t y = desc_cols(kv_s + vs * SM::kTile, 16384), d = tm + 256 + DP * q, p = tm + 128 * q;
-                            if (!ok || !(ok = mbar_wait(phalf + 8 * q, (ph >> (2 + q)) & 1, dead))) break;
-                            fence_after();
-                            if (elect_one()) {
-#pragma unroll
-                                for (int i = 0; i < 4; ++i) mma_ts(d, p + 8 * i, y + i * (2048 >> 4), id_pv, j > 0 || i > 0);
-                            }
-                            __syncwarp();
-                            if (!(ok = mbar_wait(pfull + 8 * q, (ph >> (2 + q)) & 1, dead))) break;
-                            ph ^= 4u << q;
-                            fence_after();
-                            if (elect_one()) {
-#pragma unroll
-                                for (int i = 4; i < 8; ++i) mma_ts(d, p + 8 * i, y + i * (2048 >> 4), id_pv, 1);
-                                mma_commit(odone + 8 * q);
-                            }
-                            __syncwarp();
-                        } else {
-                            if (!(ok = mbar_wait(qfull + 8 * q, (ph >> q) & 1, dead))) break;
-                            ph ^= 1u << q;
-                        }
-                        if (j + 1 < n) {
-                            if (q == 0 && !(ok = mbar_wait(full + 8 * ks, ((v + 1) / NST) & 1, dead))) break;
-                            if (elect_one()) {
-                                uint32_t x = desc_rows(q_s + q * SM::kTile), y = desc_rows(kv_s + ks * SM::kTile);
-#pragma unroll
-                                for (int i = 0; i < DP / 16; ++i) {
-                                    mma_ss(tm + 128 * q, x, y, id_qk, i > 0);
-                                    const uint32_t d = i % 4 == 3 ? (16384 - 96) >> 4 : 2;      // next panel, or 32 bytes
-                                    x += d;
-                                    y += d;
-                                }
-                                mma_commit(sfull + 8 * q);
-                                if (j + 2 == n) mma_commit(qempty + 8 * q);
-                            }
-                            __syncwarp();
-                        }
+                // Steps i: row tile i % nt, state tile i / nt.  Scores are `look` steps ahead: P V of step i frees the buffer of the
+                // scores of step i + look.  (One row tile looks two ahead at most: its softmax then knows that the products of the
+                // step before last are done.)  The tensor cores queue two products, some 128 cycles, and a wait takes longer: the
+                // next barrier is looked at before the last two are issued.
+                const int32_t total = n * nt, look = nt == 2 ? NB : 2;
+                bool there = false;
+                auto wait = [&](uint32_t bar, uint32_t parity) {
+                    if (!there) ok = ok && mbar_wait(bar, parity, dead);
+                    there = false;
+                    __syncwarp();
+                    return ok;
+                };
+                auto stage = [&](uint32_t i) { return i % NST; };
+                auto phase = [&](uint32_t i) { return (i / NST) & 1; };
+                const uint32_t v_full = a.mask ? clean : full;
+                auto scores = [&](int32_t i) {
+                    const int32_t q = nt == 2 ? i & 1 : 0, j = nt == 2 ? i >> 1 : i;
+                    const uint32_t at = kv + 2 * j, s_t = tm + 128 * made.st;
+                    if (j == 0) {
+                        if (!(ok = ok && mbar_wait(qfull + 8 * q, (ph >> q) & 1, dead))) return;
+                        ph ^= 1u << q;
                     }
-                    if (!ok) break;
+                    if (q == 0 && !wait(full + 8 * stage(at), phase(at))) return;
+                    const uint32_t x = desc_rows(q_s + q * SM::kTile), y = desc_rows(kv_s + stage(at) * SM::kTile);
+                    auto step = [&](int k) {
+                        const uint32_t o = (k / 4) * (16384 >> 4) + (k % 4) * 2;       // next panel, or 32 bytes
+                        mma_ss(s_t, x + o, y + o, id_qk, k > 0);
+                    };
                     if (elect_one()) {
-                        if (j >= 0) mma_commit(empty + 8 * vs);
-                        if (j + 1 < n) mma_commit(empty + 8 * ks);
+#pragma unroll
+                        for (int k = 0; k < DP / 16 - 2; ++k) step(k);
+                    }
+                    there = mbar_test(phalf + 8 * used.st, used.ph);       // the next step's probabilities
+                    __syncwarp();
+                    if (elect_one()) {
+                        step(DP / 16 - 2);
+                        step(DP / 16 - 1);
+                        mma_commit(sfull + 16 * q + 8 * ((ph2 >> q) & 1));
+                        if (q == nt - 1) mma_commit(empty + 8 * stage(at));
+                        if (j == n - 1) mma_commit(qempty + 8 * q);
                     }
                     __syncwarp();
+                    ph2 ^= 1u << q;
+                    made.next();
+                };
+                for (int32_t i = 0; i < look && i < total && ok; ++i) {
+                    scores(i);
+                    there = false;
+                }
+#pragma unroll 1
+                for (int32_t i = 0; i < total && ok; ++i) {
+                    const int32_t q = nt == 2 ? i & 1 : 0, j = nt == 2 ? i >> 1 : i;
+                    const uint32_t at = kv + 2 * j + 1, half = phalf + 8 * used.st, whole_p = pfull + 8 * used.st, p_ph = used.ph;
+                    const uint32_t y = desc_cols(kv_s + stage(at) * SM::kTile, 16384), d = tm + kO + DP * q, p = tm + 128 * used.st;
+                    if (q == 0 && !(ok = mbar_wait(v_full + 8 * stage(at), phase(at), dead))) break;
+                    if (!wait(half, p_ph)) break;
+                    fence_after();
+                    auto step = [&](int k) { mma_ts(d, p + 8 * k, y + k * (2048 >> 4), id_pv, j > 0 || k > 0); };
+                    if (elect_one()) {
+                        step(0);
+                        step(1);
+                    }
+                    there = mbar_test(whole_p, p_ph);
+                    __syncwarp();
+                    if (elect_one()) {
+                        step(2);
+                        step(3);
+                    }
+                    __syncwarp();
+                    if (!wait(whole_p, p_ph)) break;
+                    fence_after();
+                    if (elect_one()) {
+                        step(4);
+                        step(5);
+                    }
+                    const uint32_t next_k = kv + 2 * ((i + look) / nt);
+                    there = i + look < total && (nt == 1 || (i + look) % 2 == 0) && mbar_test(full + 8 * stage(next_k), phase(next_k));
+                    __syncwarp();
+                    if (elect_one()) {
+                        step(6);
+                        step(7);
+                        mma_commit(odone + 16 * q + 8 * ((ph2 >> (2 + q)) & 1));
+                        if (q == nt - 1) mma_commit(empty + 8 * stage(at));
+                    }
+                    __syncwarp();
+                    ph2 ^= 4u << q;
+                    used.next();
+                    if (i + look < total) scores(i + look);
+                    else there = false;
                 }
                 kv += 2 * n;
             } else if (warp == 11 && a.mask) {
