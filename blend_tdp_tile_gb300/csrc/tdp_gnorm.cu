@@ -29,9 +29,9 @@ namespace {
 
 constexpr int kGnThreads = 256;
 constexpr int kGnWideRows = 256;            // rows of a chunk, wide rows
-constexpr int kGnChunkMost = 512 << 10;     // bytes of x of a chunk; fewer while the chunks do not fill the device
+constexpr int kGnBlocks = 4, kGnGradBlocks = 3;         // blocks an SM holds
+constexpr int kGnChunkMost = 700 << 10;     // bytes of x of a chunk
 constexpr int kGnChunkLeast = 32 << 10;
-constexpr int kGnFill = 152 * 8;            // chunks that fill it
 constexpr int kClThreads = 512;
 constexpr int kClBytes = 48 << 10;          // values a cluster's block takes before the cluster grows
 constexpr int kClSmem = 224 << 10;          // shared memory of a block at most
@@ -165,29 +165,49 @@ struct gn_cols {
     }
 };
 
-__device__ __forceinline__ float warp_sum(float x)
+// Sum over `width` neighbouring lanes (a power of two).
+__device__ __forceinline__ float lanes_sum(float x, int32_t width = 32)
 {
-    for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(~0u, x, o);
+    for (int o = width / 2; o; o >>= 1) x += __shfl_xor_sync(~0u, x, o);
     return x;
 }
 
-// Moments of a group from parts (mean m_i, squared deviations q_i, n_i values each), one warp; value i by at(i).
+// Threads of a block on groups: as many lanes a group as let all groups be joined at once, where there are few; a
+// warp each took four turns of dependent loads and shuffles at 32 groups, 3 us a block.  f(group, on) runs in
+// whole warps, past the last group too (on = false).
+struct gn_team {
+    int32_t width, lane, first, step;
+    __device__ __forceinline__ gn_team(int32_t G, int32_t threads)
+    {
+        width = 32;
+        while (width > 1 && threads / width < G) width >>= 1;
+        lane = threadIdx.x & (width - 1);
+        first = threadIdx.x / width;
+        step = threads / width;
+    }
+    template <typename F>
+    __device__ __forceinline__ void each(int32_t G, F f) const
+    {
+        for (int32_t g0 = 0; g0 < G; g0 += step) f(g0 + first, g0 + first < G);
+    }
+};
+
+// Moments of a group from parts (mean m_i, squared deviations q_i, n_i values each) by `width` lanes; value i by at(i).
 template <typename At>
-__device__ __forceinline__ void join_moments(int32_t parts, float n, At at, float &mean, float &q)
+__device__ __forceinline__ void join_moments(int32_t parts, int32_t lane, int32_t width, float n, At at, float &mean, float &q)
 {
-    const int32_t lane = threadIdx.x & 31;
     mean = 0.f;
-    for (int32_t i = lane; i < parts; i += 32) {
+    for (int32_t i = lane; i < parts; i += width) {
         const float3 p = at(i);
         mean += p.x * (p.z / n);
     }
-    mean = warp_sum(mean);
+    mean = lanes_sum(mean, width);
     q = 0.f;
-    for (int32_t i = lane; i < parts; i += 32) {
+    for (int32_t i = lane; i < parts; i += width) {
         const float3 p = at(i);
         q += p.y + p.z * (p.x - mean) * (p.x - mean);
     }
-    q = warp_sum(q);
+    q = lanes_sum(q, width);
 }
 
 // Threads of a block on rows of CV <= kThreads vectors: `step` rows side by side.
@@ -243,7 +263,7 @@ __device__ __forceinline__ void join_lanes(float2 *red, const gn_lane &l, float 
 
 // Sums of one chunk of a segment: per group (gradient: of g and g * h, and per channel of dz and dz * h).
 template <int BF16, int GRAD, int ACT>
-__global__ void __launch_bounds__(kGnThreads, GRAD ? 3 : 4)
+__global__ void __launch_bounds__(kGnThreads, GRAD ? kGnGradBlocks : kGnBlocks)
 tdp_gn_sums_kernel(const __grid_constant__ tdp_geom g, const gn_args a)
 {
     using E = gn_vec<BF16, GRAD>;
@@ -322,30 +342,32 @@ tdp_gn_sums_kernel(const __grid_constant__ tdp_geom g, const gn_args a)
         float2 *chan = reinterpret_cast<float2 *>(a.part) + ((int64_t)s * a.chunks + ch) * a.C;
         for (int32_t c = threadIdx.x; c < a.C; c += kGnThreads) chan[c] = red[c];
     }
-    for (int32_t gr = threadIdx.x >> 5; gr < a.G; gr += kGnThreads / 32) {
+    const gn_team team(a.G, kGnThreads);
+    team.each(a.G, [&](int32_t gr, bool on) {
         float m = 0.f, q = 0.f;
+        const int32_t many = on ? a.cg : 0;
         if (GRAD) {
-            for (int32_t i = threadIdx.x & 31; i < a.cg; i += 32) {
+            for (int32_t i = team.lane; i < many; i += team.width) {
                 const float2 v = red[gr * a.cg + i];
                 const float w = param<BF16>(a.gamma, gr * a.cg + i, 1.f);
                 m += v.x * w;
                 q += v.y * w;
             }
-            m = warp_sum(m);
-            q = warp_sum(q);
+            m = lanes_sum(m, team.width);
+            q = lanes_sum(q, team.width);
         } else {
-            join_moments(a.cg, (float)a.cg * rows, [&](int32_t i) {
+            join_moments(many, team.lane, team.width, (float)a.cg * rows, [&](int32_t i) {
                 const float2 v = red[gr * a.cg + i];
                 return make_float3(v.x, v.y, (float)rows);
             }, m, q);
         }
-        if ((threadIdx.x & 31) == 0) out[gr] = make_float2(m, q);
-    }
+        if (on && team.lane == 0) out[gr] = make_float2(m, q);
+    });
 }
 
 // The elementwise pass of one chunk, chunks from the last to the first; the block joins its segment's sums.
 template <int BF16, int GRAD, int ACT>
-__global__ void __launch_bounds__(kGnThreads, GRAD ? 3 : 4)
+__global__ void __launch_bounds__(kGnThreads, GRAD ? kGnGradBlocks : kGnBlocks)
 tdp_gn_apply_kernel(const __grid_constant__ tdp_geom g, const gn_args a)
 {
     using E = gn_vec<BF16, GRAD>;
@@ -377,30 +399,32 @@ tdp_gn_apply_kernel(const __grid_constant__ tdp_geom g, const gn_args a)
     if (U <= mine) load();              // ahead of the join
     const float n = (float)seg.T * a.cg;
     const float2 *part = reinterpret_cast<const float2 *>(a.gpart) + (int64_t)s * a.chunks * a.G;
-    for (int32_t gr = threadIdx.x >> 5; gr < a.G; gr += kGnThreads / 32) {
-        const int32_t lane = threadIdx.x & 31;
+    const gn_team team(a.G, kGnThreads);
+    team.each(a.G, [&](int32_t gr, bool on) {
         float m = 0.f, q = 0.f;
+        const int32_t many = on ? chunks : 0;
         if (GRAD) {
-            for (int32_t i = lane; i < chunks; i += 32) {
+#pragma unroll 4
+            for (int32_t i = team.lane; i < many; i += team.width) {
                 const float2 v = part[(int64_t)i * a.G + gr];
                 m += v.x;
                 q += v.y;
             }
-            m = warp_sum(m) / n;
-            q = warp_sum(q) / n;
+            m = lanes_sum(m, team.width) / n;
+            q = lanes_sum(q, team.width) / n;
         } else {
-            join_moments(chunks, n, [&](int32_t i) {
+            join_moments(many, team.lane, team.width, n, [&](int32_t i) {
                 const float2 v = part[(int64_t)i * a.G + gr];
                 return make_float3(v.x, v.y, (float)min((int64_t)a.rows, seg.T - (int64_t)i * a.rows) * a.cg);
             }, m, q);
             q = 1.f / sqrtf(q / n + a.eps);
-            if (ch == 0 && lane == 0) {
+            if (on && ch == 0 && team.lane == 0) {
                 a.mean[(int64_t)s * a.G + gr] = m;
                 a.rstd[(int64_t)s * a.G + gr] = q;
             }
         }
-        if (lane == 0) grp[gr] = make_float2(m, q);
-    }
+        if (on && team.lane == 0) grp[gr] = make_float2(m, q);
+    });
     __syncthreads();
     if (!l.on || l.row >= rows) return;
     gn_cols<BF16, GRAD> k;
@@ -492,8 +516,8 @@ __device__ __forceinline__ void cluster_groups(const gn_args &a, const float2 *c
             x += chan[c].x * k;
             y += chan[c].y * k;
         }
-        x = warp_sum(x);
-        y = warp_sum(y);
+        x = lanes_sum(x);
+        y = lanes_sum(y);
         if ((threadIdx.x & 31) == 0) {
             out[2 * gr] = x;
             out[2 * gr + 1] = y;
@@ -729,7 +753,7 @@ tdp_gn_wide_join_kernel(const __grid_constant__ tdp_geom g, const gn_args a)
     const float n = (float)seg.T * a.cg;
     if (!GRAD) {
         float m, q;
-        join_moments(chunks * a.cg, n, [&](int32_t i) {
+        join_moments(chunks * a.cg, lane, 32, n, [&](int32_t i) {
             const int32_t k = i / a.cg;
             const float2 v = part[(int64_t)k * a.C + i - k * a.cg];
             return make_float3(v.x, v.y, (float)min((int64_t)a.rows, seg.T - (int64_t)k * a.rows));
@@ -752,8 +776,8 @@ tdp_gn_wide_join_kernel(const __grid_constant__ tdp_geom g, const gn_args a)
             x += t.x * k;
             y += t.y * k;
         }
-        x = warp_sum(x);
-        y = warp_sum(y);
+        x = lanes_sum(x);
+        y = lanes_sum(y);
         if (lane == 0) {
             a.gmean[2 * w] = x / n;
             a.gmean[2 * w + 1] = y / n;
@@ -838,8 +862,11 @@ tdp_status gn_check(tdp_plan_t plan, int32_t C, int32_t groups, int grad, gn_pla
         p->rows = (int32_t)rows;
     } else if (CV <= kGnThreads && groups <= 4096) {
         p->way = kTwoPass;
-        const int64_t fill = segs * T * CV * bytes / kGnFill;
-        p->rows = (int32_t)std::max<int64_t>(std::min<int64_t>(std::max<int64_t>(fill, kGnChunkLeast), kGnChunkMost) / (CV * bytes), 1);
+        // chunks for whole rounds of the blocks that the device holds; a segment's last chunk is half full on average
+        const int64_t all = (int64_t)g.B * g.total, round = 152 * (grad ? kGnGradBlocks : kGnBlocks), most = round * kGnChunkMost;
+        const int64_t units = (all * CV * bytes + most - 1) / most * round;
+        const int64_t want = (all + units - 1) / std::max<int64_t>(units - segs / 2, 1), least = (kGnChunkLeast + CV * bytes - 1) / (CV * bytes);
+        p->rows = (int32_t)std::max(std::min(want, T), least);
     } else {
         p->way = kWide;
         p->rows = kGnWideRows;
