@@ -11,10 +11,11 @@
 //     launch; x (and dy) are read once and the sums go round the cluster through distributed shared memory.
 //   - tdp_gn_sums_kernel, tdp_gn_apply_kernel: larger segments.  Sums of chunks of rows, then the elementwise pass, whose
 //     blocks join their segment's chunks themselves and run through the rows backwards, so that what the sums
-//     read last is found in the 129 MB L2.  (One grid that takes chunks of sums and, some segments later, of the
-//     elementwise pass in turn would read everything once, but its tickets, joins and flags cost 8 us a
-//     chunk: 934 us at best where these two take 609 us, 635 million bf16 values.  Slices of a
-//     few channels kept in a cluster read 32-byte pieces of rows: 2171 us.)
+//     read last is found in the 129 MB L2.  Rows come by way of shared memory, some 96 KB an SM on their way: loads into
+//     registers, a batch after the other, took 601 us where this takes 570 (635 million bf16 values, 6.7 TB/s over the
+//     three times that they move), and 1075 us in the gradient where this takes 984.  Tried: one grid that takes chunks of
+//     sums and, some segments later, of the elementwise pass in turn reads everything once, but its tickets, joins and
+//     flags took 934 us; slices of a few channels kept in a cluster read 32-byte pieces of rows, 2171 us.
 //   - rows wider than a block's 256 vectors: sums, join and elementwise pass as launches of their own.
 // Variances are sums of squared deviations, of a block's values about their mean or joined by
 // T. Chan's rule, so that a mean far from zero costs no digits.  Every join runs in a fixed order.
@@ -29,9 +30,10 @@ namespace {
 
 constexpr int kGnThreads = 256;
 constexpr int kGnWideRows = 256;            // rows of a chunk, wide rows
-constexpr int kGnBlocks = 4, kGnGradBlocks = 3;         // blocks an SM holds
-constexpr int kGnChunkMost = 700 << 10;     // bytes of x of a chunk
+constexpr int kGnBlocks = 3;                // blocks that an SM holds
+constexpr int kGnChunkMost = 256 << 10;     // bytes of x of a chunk: 128 KB 620 us, 350 KB 575 us where this takes 570
 constexpr int kGnChunkLeast = 32 << 10;
+constexpr int kGnGroups = 4096;             // groups whose sums a block joins itself
 constexpr int kClThreads = 512;
 constexpr int kClBytes = 48 << 10;          // values a cluster's block takes before the cluster grows
 constexpr int kClSmem = 224 << 10;          // shared memory of a block at most
@@ -225,6 +227,71 @@ struct gn_lane {
 };
 
 // ------------------------------------------------------------------ two passes
+// A thread's vectors of x (and dy) by way of shared memory, kDeep - 1 groups of kGroup rows on their way at any time:
+// copied, and waited for, by the thread that uses them, so that no thread waits for another.
+template <int BF16, int GRAD>
+struct gn_feed {
+    using X = typename gn_vec<BF16, GRAD>::type;
+    static constexpr int kGroup = GRAD && !BF16 ? 2 : 4, kDeep = GRAD ? 3 : 4;
+    static constexpr int kBytes = kDeep * kGroup * kGnThreads * (int)sizeof(X) * (GRAD ? 2 : 1);
+    static_assert(kBytes >= kGnThreads * (gn_vec<BF16, GRAD>::V * 8 + 4), "the sums' join takes the same memory");
+    uint32_t at;
+    const X *x, *dy;
+    int32_t step, left, put = 0, get = 0;       // elements between rows; rows still to be asked for; stages
+    __device__ __forceinline__ gn_feed(void *smem, const X *x0, const X *dy0, int32_t step_, int32_t rows)
+        : at((uint32_t)__cvta_generic_to_shared(smem) + threadIdx.x * (int)sizeof(X)), x(x0), dy(dy0), step(step_), left(rows)
+    {
+#pragma unroll
+        for (int i = 0; i < kDeep - 1; ++i) ask();
+    }
+    static __device__ __forceinline__ void copy(uint32_t to, const X *from)
+    {
+        if (sizeof(X) == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+        else asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(to), "l"(from) : "memory");
+    }
+    __device__ __forceinline__ uint32_t slot(int32_t stage, int v, int which) const
+    {
+        return at + ((stage * kGroup + v) * (GRAD ? 2 : 1) + which) * (kGnThreads * (int)sizeof(X));
+    }
+    __device__ __forceinline__ void ask()
+    {
+#pragma unroll
+        for (int v = 0; v < kGroup; ++v)
+            if (v < left) {
+                copy(slot(put, v, 0), x);
+                x += step;
+                if (GRAD) {
+                    copy(slot(put, v, 1), dy);
+                    dy += step;
+                }
+            }
+        left -= kGroup;
+        put = put + 1 == kDeep ? 0 : put + 1;
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    }
+    static __device__ __forceinline__ X read(uint32_t from)
+    {
+        X v;
+        if constexpr (sizeof(X) == 16)
+            asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(from) : "memory");
+        else
+            asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(from) : "memory");
+        return v;
+    }
+    // the next group, its stage's successor asked for
+    __device__ __forceinline__ void next(X *u, X *d)
+    {
+        asm volatile("cp.async.wait_group %0;" ::"n"(kDeep - 2) : "memory");
+#pragma unroll
+        for (int v = 0; v < kGroup; ++v) {
+            u[v] = read(slot(get, v, 0));
+            if (GRAD) d[v] = read(slot(get, v, 1));
+        }
+        get = get + 1 == kDeep ? 0 : get + 1;
+        ask();
+    }
+};
+
 // Adds up (GRAD) or joins by Chan's rule the row lanes' values (s1, s2) of each channel; red holds threads * V
 // pairs, then a count per thread.  Afterwards row lane 0's entries are the block's.  n: this thread's rows.
 template <int V, int GRAD>
@@ -263,13 +330,14 @@ __device__ __forceinline__ void join_lanes(float2 *red, const gn_lane &l, float 
 
 // Sums of one chunk of a segment: per group (gradient: of g and g * h, and per channel of dz and dz * h).
 template <int BF16, int GRAD, int ACT>
-__global__ void __launch_bounds__(kGnThreads, GRAD ? kGnGradBlocks : kGnBlocks)
+__global__ void __launch_bounds__(kGnThreads, kGnBlocks)
 tdp_gn_sums_kernel(const __grid_constant__ tdp_geom g, const gn_args a)
 {
     using E = gn_vec<BF16, GRAD>;
     using X = typename E::type;
-    constexpr int V = E::V, U = 4;
-    __shared__ float2 red[kGnThreads * V + kGnThreads / 2];
+    constexpr int V = E::V;
+    extern __shared__ __align__(16) unsigned char dyn[];
+    float2 *red = reinterpret_cast<float2 *>(dyn);      // after the last rows: [threads * V + threads / 2]
     const int32_t s = blockIdx.x / a.chunks, ch = blockIdx.x % a.chunks, CV = a.C / V;
     const tdp_seg seg = tdp_seg_at(g, s);
     const int64_t r0 = (int64_t)ch * a.rows;
@@ -310,21 +378,17 @@ tdp_gn_sums_kernel(const __grid_constant__ tdp_geom g, const gn_args a)
                 }
             }
         };
-        int32_t off = l.row * CV, i = 0;
+        gn_feed<BF16, GRAD> feed(dyn, x + l.row * CV, dy + l.row * CV, step, mine);
         if (GRAD) k.moments(a, s, l.col);
-        else E::unpack(x[off], p);              // deviations from the thread's own first value
-        for (; i + U <= mine; i += U) {
+        constexpr int U = feed.kGroup;
+        for (int32_t i = 0; i < mine; i += U) {
             X u[U], d[U];
+            feed.next(u, d);
+            if (!GRAD && i == 0) E::unpack(u[0], p);            // deviations from the thread's own first value
 #pragma unroll
-            for (int v = 0; v < U; ++v) {
-                u[v] = x[off + v * step];
-                if (GRAD) d[v] = dy[off + v * step];
-            }
-            off += U * step;
-#pragma unroll
-            for (int v = 0; v < U; ++v) add(u[v], d[v]);
+            for (int v = 0; v < U; ++v)
+                if (i + v < mine) add(u[v], d[v]);
         }
-        for (; i < mine; ++i, off += step) add(x[off], GRAD ? dy[off] : X());
         if (!GRAD) {
             n = (float)mine;
             const float inv = 1.f / n;
@@ -336,6 +400,7 @@ tdp_gn_sums_kernel(const __grid_constant__ tdp_geom g, const gn_args a)
             }
         }
     }
+    __syncthreads();
     join_lanes<V, GRAD>(red, l, n, s1, s2);
     float2 *out = reinterpret_cast<float2 *>(a.gpart) + ((int64_t)s * a.chunks + ch) * a.G;
     if (GRAD && a.dgamma) {
@@ -367,14 +432,14 @@ tdp_gn_sums_kernel(const __grid_constant__ tdp_geom g, const gn_args a)
 
 // The elementwise pass of one chunk, chunks from the last to the first; the block joins its segment's sums.
 template <int BF16, int GRAD, int ACT>
-__global__ void __launch_bounds__(kGnThreads, GRAD ? kGnGradBlocks : kGnBlocks)
+__global__ void __launch_bounds__(kGnThreads, kGnBlocks)
 tdp_gn_apply_kernel(const __grid_constant__ tdp_geom g, const gn_args a)
 {
     using E = gn_vec<BF16, GRAD>;
     using X = typename E::type;
-    constexpr int V = E::V, U = 4;
+    constexpr int V = E::V;
     extern __shared__ __align__(16) unsigned char dyn[];
-    float2 *grp = reinterpret_cast<float2 *>(dyn);             // [G]
+    float2 *grp = reinterpret_cast<float2 *>(dyn + gn_feed<BF16, GRAD>::kBytes);             // [G]
     const int32_t unit = gridDim.x - 1 - blockIdx.x, s = unit / a.chunks, ch = unit % a.chunks, CV = a.C / V;
     const tdp_seg seg = tdp_seg_at(g, s);
     const int64_t r0 = (int64_t)ch * a.rows;
@@ -387,16 +452,7 @@ tdp_gn_apply_kernel(const __grid_constant__ tdp_geom g, const gn_args a)
     const X *x = reinterpret_cast<const X *>(a.x) + at, *dy = reinterpret_cast<const X *>(a.dy) + at;
     X *y = reinterpret_cast<X *>(a.y) + at;
     const int32_t mine = l.on ? (rows - l.row + l.step - 1) / l.step : 0, step = l.step * CV;        // rows of this thread
-    int32_t off = l.row * CV, i = 0;
-    X u[U], d[U];
-    auto load = [&]() {
-#pragma unroll
-        for (int v = 0; v < U; ++v) {
-            u[v] = __ldcs(x + off + v * step);
-            if (GRAD) d[v] = __ldcs(dy + off + v * step);
-        }
-    };
-    if (U <= mine) load();              // ahead of the join
+    gn_feed<BF16, GRAD> feed(dyn, x + l.row * CV, dy + l.row * CV, step, mine);         // ahead of the join
     const float n = (float)seg.T * a.cg;
     const float2 *part = reinterpret_cast<const float2 *>(a.gpart) + (int64_t)s * a.chunks * a.G;
     const gn_team team(a.G, kGnThreads);
@@ -453,13 +509,14 @@ tdp_gn_apply_kernel(const __grid_constant__ tdp_geom g, const gn_args a)
             __stcs(y + o, E::pack(f));
         }
     };
-    for (; i + U <= mine; i += U) {
-        if (i > 0) load();
+    constexpr int U = feed.kGroup;
+    for (int32_t i = 0, off = l.row * CV; i < mine; i += U) {
+        X u[U], d[U];
+        feed.next(u, d);
 #pragma unroll
-        for (int v = 0; v < U; ++v) put(u[v], d[v], off + v * step);
-        off += U * step;
+        for (int v = 0; v < U; ++v, off += step)
+            if (i + v < mine) put(u[v], d[v], off);
     }
-    for (; i < mine; ++i, off += step) put(__ldcs(x + off), GRAD ? __ldcs(dy + off) : X(), off);
 }
 
 // ------------------------------------------------------------------ cluster
@@ -860,10 +917,10 @@ tdp_status gn_check(tdp_plan_t plan, int32_t C, int32_t groups, int grad, gn_pla
         p->smem = cluster_smem(groups, V, rows * value);
         p->chunks = p->blocks;
         p->rows = (int32_t)rows;
-    } else if (CV <= kGnThreads && groups <= 4096) {
+    } else if (CV <= kGnThreads && groups <= kGnGroups) {
         p->way = kTwoPass;
         // chunks for whole rounds of the blocks that the device holds; a segment's last chunk is half full on average
-        const int64_t all = (int64_t)g.B * g.total, round = 152 * (grad ? kGnGradBlocks : kGnBlocks), most = round * kGnChunkMost;
+        const int64_t all = (int64_t)g.B * g.total, round = 152 * kGnBlocks, most = round * kGnChunkMost;
         const int64_t units = (all * CV * bytes + most - 1) / most * round;
         const int64_t want = (all + units - 1) / std::max<int64_t>(units - segs / 2, 1), least = (kGnChunkLeast + CV * bytes - 1) / (CV * bytes);
         p->rows = (int32_t)std::max(std::min(want, T), least);
@@ -911,24 +968,28 @@ cudaError_t gn_run(const tdp_geom &g, const gn_plan &p, const gn_args &a, cudaSt
     cudaError_t err = cudaSuccess;
     const dim3 channels((unsigned)((a.C + 3) / 4));
     auto blocks = [](int64_t threads) { return dim3((unsigned)((threads + kGnThreads - 1) / kGnThreads)); };
+    // the kernels' shared-memory limits, raised once per device
+    static std::atomic<bool> done[64];
+    constexpr int feed = gn_feed<BF16, GRAD>::kBytes;
+    int dev = 0;
+    err = cudaGetDevice(&dev);
+    if (err == cudaSuccess && (dev >= 64 || !done[dev].load(std::memory_order_relaxed))) {
+        const auto attr = cudaFuncAttributeMaxDynamicSharedMemorySize;
+        err = cudaFuncSetAttribute(tdp_gn_cluster_kernel<BF16, GRAD, ACT>, attr, kClSmem);
+        if (err == cudaSuccess) err = cudaFuncSetAttribute(tdp_gn_sums_kernel<BF16, GRAD, ACT>, attr, feed);
+        if (err == cudaSuccess) err = cudaFuncSetAttribute(tdp_gn_apply_kernel<BF16, GRAD, ACT>, attr, feed + kGnGroups * 8);
+        if (err == cudaSuccess && dev < 64) done[dev].store(true, std::memory_order_relaxed);
+    }
+    if (err != cudaSuccess) return err;
     if (p.way == kCluster) {
-        // the kernel's shared-memory limit, raised once per device
-        static std::atomic<bool> done[64];
-        int dev = 0;
-        err = cudaGetDevice(&dev);
-        if (err == cudaSuccess && (dev >= 64 || !done[dev].load(std::memory_order_relaxed))) {
-            err = cudaFuncSetAttribute(tdp_gn_cluster_kernel<BF16, GRAD, ACT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       kClSmem);
-            if (err == cudaSuccess && dev < 64) done[dev].store(true, std::memory_order_relaxed);
-        }
         if (err == cudaSuccess)
             err = gn_launch(tdp_gn_cluster_kernel<BF16, GRAD, ACT>, dim3((unsigned)(segs * p.blocks)), kClThreads, p.smem, p.blocks, s, g, a, p.blocks, p.keep);
         if (err == cudaSuccess && GRAD && a.dgamma)
             err = gn_launch(tdp_gn_param_kernel, channels, kGnThreads, 0, 1, s, a, (const float2 *)a.part, (int32_t)(segs * p.blocks));
     } else if (p.way == kTwoPass) {
         const dim3 grid((unsigned)(segs * p.chunks));
-        err = gn_launch(tdp_gn_sums_kernel<BF16, GRAD, ACT>, grid, kGnThreads, 0, 1, s, g, a);
-        if (err == cudaSuccess) err = gn_launch(tdp_gn_apply_kernel<BF16, GRAD, ACT>, grid, kGnThreads, (size_t)a.G * 8, 1, s, g, a);
+        err = gn_launch(tdp_gn_sums_kernel<BF16, GRAD, ACT>, grid, kGnThreads, (size_t)feed, 1, s, g, a);
+        if (err == cudaSuccess) err = gn_launch(tdp_gn_apply_kernel<BF16, GRAD, ACT>, grid, kGnThreads, (size_t)feed + a.G * 8, 1, s, g, a);
         if (err == cudaSuccess && GRAD && a.dgamma)
             err = gn_launch(tdp_gn_param_kernel, channels, kGnThreads, 0, 1, s, a, (const float2 *)a.part, (int32_t)(segs * p.chunks));
     } else {
