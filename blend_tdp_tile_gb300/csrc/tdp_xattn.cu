@@ -20,6 +20,7 @@ namespace {
 constexpr int kXT = 256;        // threads: 16 x 16, each 4 rows x 4 states
 constexpr int kXM = 64;         // packed rows of a block
 constexpr int kXN = 64;         // states of a step
+constexpr int kXJoin = 64;      // threads of a join
 constexpr float kLog2e = 1.4426950408889634f;
 
 template <int DP>
@@ -222,15 +223,15 @@ tdp_xattn_simt_kernel(const __grid_constant__ tdp_geom g, const __grid_constant_
     }
 }
 
-// One warp per (row, head): out = sum_i exp(lse_i - lse) out_i over the parts of the states.
+// One warp per (row, head), four columns a lane: out = sum_i exp(lse_i - lse) out_i over the parts of the states.
+// A handful of warps in most cases, bound by latency: eight parts' loads run at a time, on as many SMs as there are.
 template <int BF16>
-__global__ void __launch_bounds__(kXT)
+__global__ void __launch_bounds__(kXJoin)
 tdp_xattn_join_kernel(const xattn_args a)
 {
-    using T = typename tdp_elem<BF16>::type;
     tdp_pdl_trigger();
     tdp_pdl_wait();
-    const int64_t n = a.rows * a.Hq, h = ((int64_t)blockIdx.x * kXT + threadIdx.x) >> 5;
+    const int64_t n = a.rows * a.Hq, h = ((int64_t)blockIdx.x * kXJoin + threadIdx.x) >> 5;
     if (h >= n) return;
     const int32_t lane = threadIdx.x & 31;
     // a part's lse a lane (two past 32 parts)
@@ -238,19 +239,31 @@ tdp_xattn_join_kernel(const xattn_args a)
     float top = fmaxf(l0, l1);
     for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
     const float base = top == -INFINITY ? 0.f : top, w0 = expf(l0 - base), w1 = expf(l1 - base);
-    float sum = w0 + w1, acc[TDP_MAX_HEAD_DIM / 32] = {};
+    float sum = w0 + w1;
     for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
-#pragma unroll 4
+    const bool on = 4 * lane < a.D;
+    const float *po = a.po + h * a.D + 4 * lane;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
     for (int32_t i = 0; i < a.split; ++i) {
         const float w = __shfl_sync(~0u, i < 32 ? w0 : w1, i & 31);
-        for (int c = 0; c < TDP_MAX_HEAD_DIM / 32; ++c) {
-            const float x = lane + 32 * c < a.D ? a.po[(i * n + h) * a.D + lane + 32 * c] : 0.f;
-            if (w != 0.f) acc[c] += w * x;
+        const float4 x = on ? *reinterpret_cast<const float4 *>(po + i * n * a.D) : acc;
+        if (w != 0.f) {
+            acc.x += w * x.x;
+            acc.y += w * x.y;
+            acc.z += w * x.z;
+            acc.w += w * x.w;
         }
     }
     const float inv = sum == 0.f ? 0.f : 1.f / sum;
-    for (int c = 0; c < TDP_MAX_HEAD_DIM / 32; ++c)
-        if (lane + 32 * c < a.D) static_cast<T *>(a.out)[h * a.D + lane + 32 * c] = (T)(acc[c] * inv);
+    if (on) {
+        const int64_t at = h * a.D + 4 * lane;
+        if (BF16)
+            *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(a.out) + at) =
+                make_uint2(tdp_pack_bf16x2(acc.x * inv, acc.y * inv), tdp_pack_bf16x2(acc.z * inv, acc.w * inv));
+        else
+            *reinterpret_cast<float4 *>(static_cast<float *>(a.out) + at) = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+    }
     if (lane == 0 && a.lse) a.lse[h] = sum == 0.f ? -INFINITY : base + logf(sum);
 }
 
@@ -819,9 +832,9 @@ extern "C" tdp_status tdp_cross_attn(tdp_plan_t plan, const tdp_xattn *p, const 
         err = a.D <= 64 ? simt_kernels<64>::forward(g, a, s) : simt_kernels<128>::forward(g, a, s);
     }
     if (err == cudaSuccess && a.split > 1) {
-        const unsigned grid = (unsigned)((a.rows * a.Hq * 32 + kXT - 1) / kXT);
-        err = g.dtype == TDP_BF16 ? tdp_launch(true, tdp_xattn_join_kernel<1>, grid, kXT, s, a)
-                                  : tdp_launch(true, tdp_xattn_join_kernel<0>, grid, kXT, s, a);
+        const unsigned grid = (unsigned)((a.rows * a.Hq * 32 + kXJoin - 1) / kXJoin);
+        err = g.dtype == TDP_BF16 ? tdp_launch(true, tdp_xattn_join_kernel<1>, grid, kXJoin, s, a)
+                                  : tdp_launch(true, tdp_xattn_join_kernel<0>, grid, kXJoin, s, a);
     }
     return err == cudaSuccess ? tdp_ok() : tdp_fail(TDP_ERR_CUDA, cudaGetErrorString(err));
 }
