@@ -264,3 +264,26 @@ def test_offsets_past_32_bits(tdp):
     want, smax = ref.xattn([(0, 0, 0, 1)], *(x.float().cpu().numpy().astype(np.float64) for x in (q[-1:], k[-1:, -n:], v[-1:, -n:])), None, D ** -0.5)
     err = np.abs(out[-1].float().cpu().numpy() - want["out"][0][0])
     assert (err <= ref.xattn_unit("bf16", D, smax) * want["out"][1][0]).all()
+
+
+@pytest.mark.parametrize("S", [2, 4, 9, 40])
+@pytest.mark.parametrize("D", [64, 128])
+def test_few_states_lose_no_digits(tdp, S, D):
+    """With few states dP and delta nearly cancel.  dS and the gradient are each rounded to bf16 once: a rounding's error
+    is uniform over half a spacing, at most 2^-8 / sqrt(3) in the mean square, and two of them are independent."""
+    import torch
+    geom = B, dims, tiles, overlap = FLAT
+    segs, R = ref.segments(B, dims, tiles, overlap)
+    rng = np.random.default_rng(S)
+    t = lambda *s: torch.from_numpy(rng.standard_normal(s, dtype=np.float32)).bfloat16().cuda()  # noqa: E731
+    H, K = 8, 4
+    q, k, v, dout = t(R, H, D), t(B, S, K, D), t(B, S, K, D), t(R, H, D)
+    want, _ = ref.xattn(segs, *(x.double().cpu().numpy() for x in (q, k, v)), None, 1 / math.sqrt(D), dout.double().cpu().numpy())
+    plan = tdp.tdp_plan_create(B, *dims, 8, "bf16", tiles, overlap)
+    out, lse, dq, dk, dv = torch.empty_like(q), torch.empty((R, H), device="cuda"), torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
+    tdp.tdp_cross_attn(plan, q, k, v, None, out, lse)
+    tdp.tdp_cross_attn_grad(plan, q, k, v, None, out, lse, dout, dq, dk, dv)
+    for name, x in (("dq", dq), ("dk", dk), ("dv", dv)):
+        val = want[name][0]
+        err = np.linalg.norm(x.double().cpu().numpy() - val) / np.linalg.norm(val)
+        assert err < math.sqrt(2) * 2.0**-8 / math.sqrt(3), (name, err)
