@@ -726,6 +726,14 @@ tdp_xattn_dkv_kernel(const __grid_constant__ tdp_geom g, const __grid_constant__
         }
         __syncwarp();
         if (warp == 9) ok = mbar_wait(kvfull, 0, dead);
+        // warp 10: token in the tile, and place from the tile's first row, of the lane's four rows
+        int32_t st_tok[4], st_at[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int32_t x = 32 * i + lane, rt = x / a.Gp;
+            st_tok[i] = rt < a.TT ? rt : INT32_MAX;
+            st_at[i] = rt * a.Hq + x - rt * a.Gp;
+        }
         // warp 9 runs one tile behind itself: dK and dP of a tile come after S of the next
         uint32_t q_prev = 0;
         while (ok && wk.next(g, a, b, tile)) {
@@ -774,17 +782,21 @@ tdp_xattn_dkv_kernel(const __grid_constant__ tdp_geom g, const __grid_constant__
                 } else if (warp == 10) {
                     const uint32_t ss = n % NSS, dst = stat_s + ss * 1024;
                     if (!(ok = mbar_wait(tempty + 8 * ss, ((n / NSS) & 1) ^ 1, dead))) break;
+                    // all eight loads at once, from the tile's first row for rows that are not there: behind a condition each
+                    // they came one after the other, 6000 cycles a tile where the products take 2000
+                    const int32_t h0 = row * a.Hq + head;
+                    float l[4], d[4];
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        const int32_t r = 32 * i + lane, rt = r / a.Gp;
-                        float l = -INFINITY, d = 0.f;
-                        if (rt < a.TT && rt < left) {
-                            const int32_t h = (row + rt) * a.Hq + head + r - rt * a.Gp;
-                            l = -row_lse2(__ldg(a.lse + h));
-                            d = -__ldcg(a.delta + h);
-                        }
-                        asm volatile("st.shared.f32 [%0], %1;" ::"r"(dst + 4 * r), "f"(l) : "memory");
-                        asm volatile("st.shared.f32 [%0], %1;" ::"r"(dst + 512 + 4 * r), "f"(d) : "memory");
+                        const int32_t h = h0 + (st_tok[i] < left ? st_at[i] : 0);
+                        l[i] = __ldg(a.lse + h);
+                        d[i] = __ldcg(a.delta + h);
+                    }
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const bool on = st_tok[i] < left;
+                        asm volatile("st.shared.f32 [%0], %1;" ::"r"(dst + 4 * (32 * i + lane)), "f"(on ? -row_lse2(l[i]) : -INFINITY) : "memory");
+                        asm volatile("st.shared.f32 [%0], %1;" ::"r"(dst + 512 + 4 * (32 * i + lane)), "f"(on ? -d[i] : 0.f) : "memory");
                     }
                     __syncwarp();
                     if (lane == 0) mbar_arrive(tfull + 8 * ss);
