@@ -6,16 +6,17 @@
 // dz = dy * act'(z) and g = dz * gamma the gradient is
 //   dx = rstd * (g - mean(g) - h * mean(g * h)),  dgamma = sum dz * h,  dbeta = sum dz.
 //
-// Bound by memory.  Three ways, by size:
-//   - tdp_gn_cluster_kernel: segments that fit the shared memory of a cluster of up to eight blocks.  One
-//     launch; x (and dy) are read once and the sums go round the cluster through distributed shared memory.
-//   - tdp_gn_sums_kernel, tdp_gn_apply_kernel: larger segments.  Sums of chunks of rows, then the elementwise pass, whose
-//     blocks join their segment's chunks themselves and run through the rows backwards, so that what the sums
-//     read last is found in the 129 MB L2.  Rows come by way of shared memory, some 96 KB an SM on their way: loads into
+// Bound by memory.  Two ways, by size:
+//   - tdp_gn_sums_kernel, tdp_gn_apply_kernel: sums of chunks of rows, then the elementwise pass, whose blocks join
+//     their segment's chunks themselves and run through the rows backwards, so that what the sums
+//     read last is found in the 129 MB L2.  Rows come by way of shared memory, some 150 KB an SM on their way: loads into
 //     registers, a batch after the other, took 601 us where this takes 570 (635 million bf16 values, 6.7 TB/s over the
-//     three times that they move), and 1075 us in the gradient where this takes 984.  Tried: one grid that takes chunks of
-//     sums and, some segments later, of the elementwise pass in turn reads everything once, but its tickets, joins and
-//     flags took 934 us; slices of a few channels kept in a cluster read 32-byte pieces of rows, 2171 us.
+//     three times that they move), and 1075 us in the gradient where this takes 984.  Tried: segments kept in the shared
+//     memory of a cluster, read once in one launch: 97 us where this takes 35 (256 segments of 128 KB), 21 where this
+//     takes 13 (one of 256 KB), in a graph 7.8 where this takes 5.5 (four of 4 KB): what it saves comes from L2 anyway
+//     and its barriers cost more (the launch that it saves costs a host that launches one by one 4 us).  One grid
+//     that takes chunks of sums and, some segments later, of the elementwise pass in turn: its tickets, joins and
+//     flags took 934 us.  Slices of a few channels kept in a cluster read 32-byte pieces of rows, 2171 us.
 //   - rows wider than a block's 256 vectors: sums, join and elementwise pass as launches of their own.
 // Variances are sums of squared deviations, of a block's values about their mean or joined by
 // T. Chan's rule, so that a mean far from zero costs no digits.  Every join runs in a fixed order.
@@ -34,9 +35,6 @@ constexpr int kGnBlocks = 3;                // blocks that an SM holds
 constexpr int kGnChunkMost = 256 << 10;     // bytes of x of a chunk: 128 KB 620 us, 350 KB 575 us where this takes 570
 constexpr int kGnChunkLeast = 32 << 10;
 constexpr int kGnGroups = 4096;             // groups whose sums a block joins itself
-constexpr int kClThreads = 512;
-constexpr int kClBytes = 48 << 10;          // values a cluster's block takes before the cluster grows
-constexpr int kClSmem = 224 << 10;          // shared memory of a block at most
 
 // SiLU is z * s, s = 1 / (1 + exp(-z)); its slope s + z s (1 - s).  exp(-z) overflows to infinity for z below -88: s = 0,
 // SiLU's limit.  The gradient kernels are bound by instructions as much as by memory: two table instructions and a
@@ -62,6 +60,7 @@ struct gn_args {
     int32_t C, G, cg;           // channels, groups, channels per group
     fast_div by_cg;
     int32_t chunks, rows;       // chunks per segment, rows per chunk
+    uint32_t pblocks;           // blocks that add up dgamma and dbeta
     float eps;
     const void *x, *gamma, *beta, *dy;
     void *y;                    // y or dx
@@ -430,7 +429,34 @@ tdp_gn_sums_kernel(const __grid_constant__ tdp_geom g, const gn_args a)
     });
 }
 
-// The elementwise pass of one chunk, chunks from the last to the first; the block joins its segment's sums.
+// dgamma and dbeta from `parts` sums per channel: a block per four channels (a sector of each part), 64 threads a
+// channel, their sums added in order.  red: kGnThreads pairs.
+__device__ __forceinline__ void gn_params(const gn_args &a, const float2 *part, int32_t parts, int32_t block, float2 *red)
+{
+    const int32_t c = block * 4 + (threadIdx.x & 3);
+    float2 t = make_float2(0.f, 0.f);
+    if (c < a.C)
+#pragma unroll 8
+        for (int32_t i = threadIdx.x >> 2; i < parts; i += kGnThreads / 4) {
+            const float2 v = part[(int64_t)i * a.C + c];
+            t.x += v.x;
+            t.y += v.y;
+        }
+    red[threadIdx.x] = t;
+    for (int k = kGnThreads / 2; k >= 4; k /= 2) {
+        __syncthreads();
+        if (threadIdx.x < k) {
+            red[threadIdx.x].x += red[threadIdx.x + k].x;
+            red[threadIdx.x].y += red[threadIdx.x + k].y;
+        }
+    }
+    if (threadIdx.x >= 4 || c >= a.C) return;
+    a.dbeta[c] = red[threadIdx.x].x;
+    a.dgamma[c] = red[threadIdx.x].y;
+}
+
+// The elementwise pass of one chunk, chunks from the last to the first; the block joins its segment's sums.  In the
+// gradient the first a.pblocks blocks add up dgamma and dbeta under it (a launch of their own took 7 us).
 template <int BF16, int GRAD, int ACT>
 __global__ void __launch_bounds__(kGnThreads, kGnBlocks)
 tdp_gn_apply_kernel(const __grid_constant__ tdp_geom g, const gn_args a)
@@ -440,6 +466,12 @@ tdp_gn_apply_kernel(const __grid_constant__ tdp_geom g, const gn_args a)
     constexpr int V = E::V;
     extern __shared__ __align__(16) unsigned char dyn[];
     float2 *grp = reinterpret_cast<float2 *>(dyn + gn_feed<BF16, GRAD>::kBytes);             // [G]
+    if (GRAD && blockIdx.x < a.pblocks) {
+        tdp_pdl_trigger();
+        tdp_pdl_wait();
+        gn_params(a, reinterpret_cast<const float2 *>(a.part), (int32_t)(gridDim.x - a.pblocks), blockIdx.x, reinterpret_cast<float2 *>(dyn));
+        return;
+    }
     const int32_t unit = gridDim.x - 1 - blockIdx.x, s = unit / a.chunks, ch = unit % a.chunks, CV = a.C / V;
     const tdp_seg seg = tdp_seg_at(g, s);
     const int64_t r0 = (int64_t)ch * a.rows;
@@ -517,230 +549,6 @@ tdp_gn_apply_kernel(const __grid_constant__ tdp_geom g, const gn_args a)
         for (int v = 0; v < U; ++v, off += step)
             if (i + v < mine) put(u[v], d[v], off);
     }
-}
-
-// ------------------------------------------------------------------ cluster
-__device__ __forceinline__ uint32_t cluster_rank()
-{
-    uint32_t r;
-    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-    return r;
-}
-__device__ __forceinline__ void cluster_sync()
-{
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-// A float of the shared memory of block `rank` of the cluster.
-__device__ __forceinline__ float cluster_ld(const float *p, uint32_t rank)
-{
-    uint32_t at;
-    float v;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"((uint32_t)__cvta_generic_to_shared(p)), "r"(rank));
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
-    return v;
-}
-
-// The block's sums of each channel from its row lanes' (s1, s2): into chan[c].
-template <int V>
-__device__ __forceinline__ void add_lanes(float2 *red, const gn_lane &l, const float *s1, const float *s2)
-{
-    float2 *mine = red + threadIdx.x * V;
-#pragma unroll
-    for (int j = 0; j < V; ++j) mine[j] = make_float2(s1[j], s2[j]);
-    __syncthreads();
-    for (int32_t live = l.step; live > 1;) {
-        const int32_t half = (live + 1) / 2;
-        if (l.on && l.row + half < live) {
-            const float2 *o = mine + half * l.w * V;
-#pragma unroll
-            for (int j = 0; j < V; ++j) mine[j] = make_float2(mine[j].x + o[j].x, mine[j].y + o[j].y);
-        }
-        __syncthreads();
-        live = half;
-    }
-}
-
-// Groups' sums over the whole cluster of the channel sums chan[c] (component 0 or both), weighted by w(c);
-// out[2 * G]: this block's, all[2 * G]: the cluster's, ranks in order.
-template <typename W>
-__device__ __forceinline__ void cluster_groups(const gn_args &a, const float2 *chan, float *out, float *all, uint32_t blocks, W w)
-{
-    for (int32_t gr = threadIdx.x >> 5; gr < a.G; gr += kClThreads / 32) {
-        float x = 0.f, y = 0.f;
-        for (int32_t i = threadIdx.x & 31; i < a.cg; i += 32) {
-            const int32_t c = gr * a.cg + i;
-            const float k = w(c);
-            x += chan[c].x * k;
-            y += chan[c].y * k;
-        }
-        x = lanes_sum(x);
-        y = lanes_sum(y);
-        if ((threadIdx.x & 31) == 0) {
-            out[2 * gr] = x;
-            out[2 * gr + 1] = y;
-        }
-    }
-    if (blocks == 1) {
-        __syncthreads();
-        for (int32_t i = threadIdx.x; i < 2 * a.G; i += kClThreads) all[i] = out[i];
-    } else {
-        cluster_sync();
-        for (int32_t i = threadIdx.x; i < 2 * a.G; i += kClThreads) {
-            float t = 0.f;
-            for (uint32_t r = 0; r < blocks; ++r) t += cluster_ld(out + i, r);
-            all[i] = t;
-        }
-    }
-    __syncthreads();
-}
-
-// One cluster per segment; block `rank` keeps its share of the rows in shared memory.
-template <int BF16, int GRAD, int ACT>
-__global__ void __launch_bounds__(kClThreads)
-tdp_gn_cluster_kernel(const __grid_constant__ tdp_geom g, const __grid_constant__ gn_args a, int32_t blocks, int32_t keep)
-{
-    using E = gn_vec<BF16, GRAD>;
-    using X = typename E::type;
-    constexpr int V = E::V;
-    extern __shared__ __align__(16) unsigned char dyn[];
-    float2 *red = reinterpret_cast<float2 *>(dyn);                              // [threads, V]
-    float *out = reinterpret_cast<float *>(red + kClThreads * V), *all = out + 4 * a.G;
-    X *xs = reinterpret_cast<X *>(dyn + kClThreads * V * 8 + ((6 * a.G * 4 + 15) & ~15)), *ds = xs + keep;
-    const uint32_t rank = blocks > 1 ? cluster_rank() : 0;
-    const int32_t s = blockIdx.x / blocks;
-    const tdp_seg seg = tdp_seg_at(g, s);
-    const int32_t T = (int32_t)seg.T, r0 = (int32_t)((int64_t)T * rank / blocks), rows = (int32_t)((int64_t)T * (rank + 1) / blocks) - r0;
-    const int32_t CV = a.C / V;
-    const gn_lane l(CV, kClThreads);
-    const int64_t at = (seg.row0 + r0) * CV;
-    const X *x = reinterpret_cast<const X *>(a.x) + at, *dy = reinterpret_cast<const X *>(a.dy) + at;
-    X *y = reinterpret_cast<X *>(a.y) + at;
-    const float n = (float)T * a.cg;
-    tdp_pdl_trigger();
-    tdp_pdl_wait();
-    float s1[V], s2[V];
-#pragma unroll
-    for (int j = 0; j < V; ++j) s1[j] = s2[j] = 0.f;
-    gn_cols<BF16, GRAD> k;
-    if (GRAD && l.on) k.moments(a, s, l.col);
-    if (l.on)
-#pragma unroll 4
-        for (int32_t r = l.row; r < rows; r += l.step) {
-            const int32_t i = r * CV + l.col;
-            const X u = x[i];
-            float f[V], e[V];
-            E::unpack(u, f);
-            xs[i] = u;
-            if (GRAD) {
-                const X d = dy[i];
-                ds[i] = d;
-                E::unpack(d, e);
-#pragma unroll
-                for (int j = 0; j < V; ++j) {
-                    float dz, h;
-                    k.template grad<ACT>(f, e, j, dz, h);
-                    s1[j] += dz;
-                    s2[j] += dz * h;
-                }
-            } else {
-#pragma unroll
-                for (int j = 0; j < V; ++j) s1[j] += f[j];
-            }
-        }
-    add_lanes<V>(red, l, s1, s2);
-    if (GRAD) {
-        // this block's part of dgamma and dbeta
-        float2 *part = reinterpret_cast<float2 *>(a.part) + (int64_t)blockIdx.x * a.C;
-        if (a.dgamma)
-            for (int32_t c = threadIdx.x; c < a.C; c += kClThreads) part[c] = red[c];
-        cluster_groups(a, red, out, all, blocks, [&](int32_t c) { return param<BF16>(a.gamma, c, 1.f); });
-        if (l.on) {
-#pragma unroll
-            for (int j = 0; j < V; ++j) {
-                const int32_t gr = (l.col * V + j) / a.cg;
-                k.m1[j] = all[2 * gr] / n * k.rs[j];
-                k.m2[j] = all[2 * gr + 1] / n * k.rs[j];
-            }
-        }
-    } else {
-        cluster_groups(a, red, out, all, blocks, [](int32_t) { return 1.f; });
-        if (l.on) {
-#pragma unroll
-            for (int j = 0; j < V; ++j) {
-                k.mu[j] = all[2 * ((l.col * V + j) / a.cg)] / n;
-                s1[j] = s2[j] = 0.f;
-            }
-            for (int32_t r = l.row; r < rows; r += l.step) {
-                float f[V];
-                E::unpack(xs[r * CV + l.col], f);
-#pragma unroll
-                for (int j = 0; j < V; ++j) s1[j] += (f[j] - k.mu[j]) * (f[j] - k.mu[j]);
-            }
-        }
-        __syncthreads();
-        add_lanes<V>(red, l, s1, s2);
-        // the first sums may still be read by another block: these go beside them
-        cluster_groups(a, red, out + 2 * a.G, all, blocks, [](int32_t) { return 1.f; });
-        if (l.on) {
-#pragma unroll
-            for (int j = 0; j < V; ++j) {
-                const int32_t c = l.col * V + j;
-                k.rs[j] = 1.f / sqrtf(all[2 * (c / a.cg)] / n + a.eps);
-                k.a[j] = k.rs[j] * param<BF16>(a.gamma, c, 1.f);
-                k.b[j] = param<BF16>(a.beta, c, 0.f);
-                if (rank == 0 && l.row == 0 && c % a.cg == 0) {
-                    a.mean[(int64_t)s * a.G + c / a.cg] = k.mu[j];
-                    a.rstd[(int64_t)s * a.G + c / a.cg] = k.rs[j];
-                }
-            }
-        }
-    }
-    if (l.on)
-#pragma unroll 2
-        for (int32_t r = l.row; r < rows; r += l.step) {
-            const int32_t i = r * CV + l.col;
-            float f[V], e[V];
-            E::unpack(xs[i], f);
-            if (GRAD) {
-                E::unpack(ds[i], e);
-                k.template backward<ACT>(f, e);
-                y[i] = E::pack(e);
-            } else {
-                k.template forward<ACT>(f);
-                y[i] = E::pack(f);
-            }
-        }
-    if (blocks > 1) cluster_sync();     // a block's shared memory is read until here
-}
-
-// dgamma and dbeta from `parts` sums per channel: a block per four channels (a sector of each part), 64 threads a
-// channel, their sums added in order.
-__global__ void __launch_bounds__(kGnThreads)
-tdp_gn_param_kernel(const gn_args a, const float2 *part, int32_t parts)
-{
-    __shared__ float2 red[kGnThreads];
-    tdp_pdl_trigger();
-    tdp_pdl_wait();
-    const int32_t c = blockIdx.x * 4 + (threadIdx.x & 3);
-    float2 t = make_float2(0.f, 0.f);
-    if (c < a.C)
-#pragma unroll 8
-        for (int32_t i = threadIdx.x >> 2; i < parts; i += kGnThreads / 4) {
-            const float2 v = part[(int64_t)i * a.C + c];
-            t.x += v.x;
-            t.y += v.y;
-        }
-    red[threadIdx.x] = t;
-    for (int k = kGnThreads / 2; k >= 4; k /= 2) {
-        __syncthreads();
-        if (threadIdx.x < k) {
-            red[threadIdx.x].x += red[threadIdx.x + k].x;
-            red[threadIdx.x].y += red[threadIdx.x + k].y;
-        }
-    }
-    if (threadIdx.x >= 4 || c >= a.C) return;
-    a.dbeta[c] = red[threadIdx.x].x;
-    a.dgamma[c] = red[threadIdx.x].y;
 }
 
 // ------------------------------------------------------------------ wide rows
@@ -876,20 +684,21 @@ tdp_gn_wide_apply_kernel(const __grid_constant__ tdp_geom g, const gn_args a)
     }
 }
 
-// ------------------------------------------------------------------ host
-enum gn_way { kWide, kCluster, kTwoPass };
+__global__ void __launch_bounds__(kGnThreads)
+tdp_gn_wide_param_kernel(const gn_args a, int32_t segs)
+{
+    __shared__ float2 red[kGnThreads];
+    tdp_pdl_trigger();
+    tdp_pdl_wait();
+    gn_params(a, reinterpret_cast<const float2 *>(a.coef), segs, blockIdx.x, red);
+}
 
+// ------------------------------------------------------------------ host
 struct gn_plan {
-    gn_way way;
-    int32_t chunks, rows, blocks, keep;         // blocks: of a cluster; keep: vectors of its largest block
-    size_t smem;
+    bool wide;
+    int32_t chunks, rows;
     int64_t gpart_at, coef_at, gmean_at, bytes;
 };
-
-size_t cluster_smem(int32_t G, int V, int64_t bytes)
-{
-    return (size_t)kClThreads * V * 8 + ((6 * (size_t)G * 4 + 15) & ~(size_t)15) + (size_t)bytes;
-}
 
 tdp_status gn_check(tdp_plan_t plan, int32_t C, int32_t groups, int grad, gn_plan *p)
 {
@@ -903,36 +712,19 @@ tdp_status gn_check(tdp_plan_t plan, int32_t C, int32_t groups, int grad, gn_pla
     const int64_t CV = C / V, bytes = V * g.esize, T = tdp_max_tile_tokens(g), segs = (int64_t)g.nt * g.B;
     if (CV > (int64_t)kGnThreads * 65535 || (int64_t)g.B * g.total > ((int64_t)1 << 56) / C)
         return tdp_fail(TDP_ERR_TOO_LARGE, "group normalisation beyond index ranges");
-    p->blocks = 1;
-    p->keep = 0;
-    p->smem = 0;
-    // clusters of up to eight blocks hold a segment
-    const int64_t value = CV * bytes * (grad ? 2 : 1);
-    while (p->blocks < 8 && (T + p->blocks - 1) / p->blocks * value > kClBytes) p->blocks *= 2;
-    const int64_t rows = (T + p->blocks - 1) / p->blocks;
-    const int64_t most = (kClSmem - (int64_t)cluster_smem(std::min(groups, 1024), V, 0)) / value;
-    if (CV <= kGnThreads && groups <= 1024 && rows <= most && segs * p->blocks <= 0x7fffffffLL) {
-        p->way = kCluster;
-        p->keep = (int32_t)(rows * CV);
-        p->smem = cluster_smem(groups, V, rows * value);
-        p->chunks = p->blocks;
-        p->rows = (int32_t)rows;
-    } else if (CV <= kGnThreads && groups <= kGnGroups) {
-        p->way = kTwoPass;
+    p->wide = CV > kGnThreads || groups > kGnGroups;
+    if (p->wide) {
+        p->rows = kGnWideRows;
+    } else {
         // chunks for whole rounds of the blocks that the device holds; a segment's last chunk is half full on average
         const int64_t all = (int64_t)g.B * g.total, round = 152 * kGnBlocks, most = round * kGnChunkMost;
         const int64_t units = (all * CV * bytes + most - 1) / most * round;
         const int64_t want = (all + units - 1) / std::max<int64_t>(units - segs / 2, 1), least = (kGnChunkLeast + CV * bytes - 1) / (CV * bytes);
         p->rows = (int32_t)std::max(std::min(want, T), least);
-    } else {
-        p->way = kWide;
-        p->rows = kGnWideRows;
     }
-    if (p->way != kCluster) {
-        const int64_t chunks = (T + p->rows - 1) / p->rows;
-        if (chunks * segs > 0x7fffffffLL) return tdp_fail(TDP_ERR_TOO_LARGE, "group normalisation beyond index ranges");
-        p->chunks = (int32_t)chunks;
-    }
+    const int64_t chunks = (T + p->rows - 1) / p->rows;
+    if (chunks * segs > 0x7fffffffLL - (C + 3) / 4) return tdp_fail(TDP_ERR_TOO_LARGE, "group normalisation beyond index ranges");
+    p->chunks = (int32_t)chunks;
     auto up = [](int64_t x) { return (x + 255) / 256 * 256; };
     p->gpart_at = up(segs * p->chunks * C * 8);
     p->coef_at = p->gpart_at + up(segs * p->chunks * groups * 8);
@@ -942,21 +734,18 @@ tdp_status gn_check(tdp_plan_t plan, int32_t C, int32_t groups, int grad, gn_pla
 }
 
 template <typename K, typename... A>
-cudaError_t gn_launch(K kernel, dim3 grid, int threads, size_t smem, int cluster, cudaStream_t s, A... args)
+cudaError_t gn_launch(K kernel, dim3 grid, size_t smem, cudaStream_t s, A... args)
 {
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = cluster;
-    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cudaLaunchAttribute attr = {};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
-    cfg.blockDim = dim3(threads);
+    cfg.blockDim = dim3(kGnThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
-    cfg.attrs = attr;
-    cfg.numAttrs = cluster > 1 ? 2 : 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
@@ -966,39 +755,29 @@ cudaError_t gn_run(const tdp_geom &g, const gn_plan &p, const gn_args &a, cudaSt
     const int64_t segs = (int64_t)g.nt * g.B;
     constexpr int V = gn_width(BF16, GRAD);
     cudaError_t err = cudaSuccess;
-    const dim3 channels((unsigned)((a.C + 3) / 4));
     auto blocks = [](int64_t threads) { return dim3((unsigned)((threads + kGnThreads - 1) / kGnThreads)); };
-    // the kernels' shared-memory limits, raised once per device
-    static std::atomic<bool> done[64];
-    constexpr int feed = gn_feed<BF16, GRAD>::kBytes;
-    int dev = 0;
-    err = cudaGetDevice(&dev);
-    if (err == cudaSuccess && (dev >= 64 || !done[dev].load(std::memory_order_relaxed))) {
-        const auto attr = cudaFuncAttributeMaxDynamicSharedMemorySize;
-        err = cudaFuncSetAttribute(tdp_gn_cluster_kernel<BF16, GRAD, ACT>, attr, kClSmem);
-        if (err == cudaSuccess) err = cudaFuncSetAttribute(tdp_gn_sums_kernel<BF16, GRAD, ACT>, attr, feed);
-        if (err == cudaSuccess) err = cudaFuncSetAttribute(tdp_gn_apply_kernel<BF16, GRAD, ACT>, attr, feed + kGnGroups * 8);
-        if (err == cudaSuccess && dev < 64) done[dev].store(true, std::memory_order_relaxed);
-    }
-    if (err != cudaSuccess) return err;
-    if (p.way == kCluster) {
-        if (err == cudaSuccess)
-            err = gn_launch(tdp_gn_cluster_kernel<BF16, GRAD, ACT>, dim3((unsigned)(segs * p.blocks)), kClThreads, p.smem, p.blocks, s, g, a, p.blocks, p.keep);
-        if (err == cudaSuccess && GRAD && a.dgamma)
-            err = gn_launch(tdp_gn_param_kernel, channels, kGnThreads, 0, 1, s, a, (const float2 *)a.part, (int32_t)(segs * p.blocks));
-    } else if (p.way == kTwoPass) {
+    if (!p.wide) {
+        // the kernels' shared-memory limits, raised once per device
+        static std::atomic<bool> done[64];
+        constexpr int feed = gn_feed<BF16, GRAD>::kBytes;
+        int dev = 0;
+        err = cudaGetDevice(&dev);
+        if (err == cudaSuccess && (dev >= 64 || !done[dev].load(std::memory_order_relaxed))) {
+            const auto attr = cudaFuncAttributeMaxDynamicSharedMemorySize;
+            err = cudaFuncSetAttribute(tdp_gn_sums_kernel<BF16, GRAD, ACT>, attr, feed);
+            if (err == cudaSuccess) err = cudaFuncSetAttribute(tdp_gn_apply_kernel<BF16, GRAD, ACT>, attr, feed + kGnGroups * 8);
+            if (err == cudaSuccess && dev < 64) done[dev].store(true, std::memory_order_relaxed);
+        }
         const dim3 grid((unsigned)(segs * p.chunks));
-        err = gn_launch(tdp_gn_sums_kernel<BF16, GRAD, ACT>, grid, kGnThreads, (size_t)feed, 1, s, g, a);
-        if (err == cudaSuccess) err = gn_launch(tdp_gn_apply_kernel<BF16, GRAD, ACT>, grid, kGnThreads, (size_t)feed + a.G * 8, 1, s, g, a);
-        if (err == cudaSuccess && GRAD && a.dgamma)
-            err = gn_launch(tdp_gn_param_kernel, channels, kGnThreads, 0, 1, s, a, (const float2 *)a.part, (int32_t)(segs * p.chunks));
+        if (err == cudaSuccess) err = gn_launch(tdp_gn_sums_kernel<BF16, GRAD, ACT>, grid, (size_t)feed, s, g, a);
+        if (err == cudaSuccess) err = gn_launch(tdp_gn_apply_kernel<BF16, GRAD, ACT>, dim3(grid.x + a.pblocks), (size_t)feed + a.G * 8, s, g, a);
     } else {
         const dim3 grid((unsigned)(segs * p.chunks), (unsigned)((a.C / V + kGnThreads - 1) / kGnThreads));
-        err = gn_launch(tdp_gn_wide_sums_kernel<BF16, GRAD, ACT>, grid, kGnThreads, 0, 1, s, g, a);
-        if (err == cudaSuccess) err = gn_launch(tdp_gn_wide_join_kernel<BF16, GRAD>, blocks(segs * a.G * 32), kGnThreads, 0, 1, s, g, a);
+        err = gn_launch(tdp_gn_wide_sums_kernel<BF16, GRAD, ACT>, grid, 0, s, g, a);
+        if (err == cudaSuccess) err = gn_launch(tdp_gn_wide_join_kernel<BF16, GRAD>, blocks(segs * a.G * 32), 0, s, g, a);
         if (err == cudaSuccess && GRAD && a.dgamma)
-            err = gn_launch(tdp_gn_param_kernel, channels, kGnThreads, 0, 1, s, a, (const float2 *)a.coef, (int32_t)segs);
-        if (err == cudaSuccess) err = gn_launch(tdp_gn_wide_apply_kernel<BF16, GRAD, ACT>, grid, kGnThreads, 0, 1, s, g, a);
+            err = gn_launch(tdp_gn_wide_param_kernel, dim3((unsigned)((a.C + 3) / 4)), 0, s, a, (int32_t)segs);
+        if (err == cudaSuccess) err = gn_launch(tdp_gn_wide_apply_kernel<BF16, GRAD, ACT>, grid, 0, s, g, a);
     }
     return err;
 }
@@ -1011,6 +790,7 @@ cudaError_t gn_dispatch(const tdp_geom &g, const gn_plan &p, gn_args a, int32_t 
     a.by_cg = fast_div_by(a.cg);
     a.chunks = p.chunks;
     a.rows = p.rows;
+    a.pblocks = GRAD && a.dgamma ? (a.C + 3) / 4 : 0;
     a.part = reinterpret_cast<float *>(w);
     a.gpart = reinterpret_cast<float *>(w + p.gpart_at);
     a.coef = reinterpret_cast<float *>(w + p.coef_at);
