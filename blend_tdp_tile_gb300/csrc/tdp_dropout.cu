@@ -60,6 +60,8 @@ __device__ __forceinline__ void drop_words(int64_t i, uint64_t offset, const phi
 
 // 16-byte vectors (4 fp32 or 8 bf16 elements: one or two counters), kDropUnroll of them a thread and step; the vector that
 // holds the end is done element by element by one thread.  `thr` is at most 2^32 - 1; p = 1 has all = 1.
+// 105 million bf16 elements: 104 us, 6.1 TB/s, near the memory's rate; without the residual (the gradient) 95 us, 4.4 TB/s:
+// the generator's 20 wide products for four elements keep the integer multiplier 69 % busy.
 template <int BF16, int RES>
 __global__ void __launch_bounds__(kDropThreads)
 tdp_dropout_kernel(int64_t n, uint32_t thr, int all, float scale, const uint64_t *__restrict__ rng, const void *x,

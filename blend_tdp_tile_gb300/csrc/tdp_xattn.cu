@@ -8,6 +8,9 @@
 // The gradient computes p = exp(s - lse) again: one kernel walks the states for dq,
 // one walks the rows for dk and dv (split over the rows, joined in order: no
 // atomics).  States that a row's mask drops are read as zero and get p = 0.
+//
+// The fp32 kernels are bound by instructions: each thread makes 4 x 4 scores from 8 loads of four elements.  35840 rows of
+// 4 heads of 64 against 512 states take 649 us, 29 TFLOP/s, their gradients 2680 us, 25 TFLOP/s.
 #include <algorithm>
 #include <atomic>
 
@@ -479,7 +482,9 @@ tdp_xattn_dkv_join_kernel(const xattn_args a, int64_t n)
 }
 
 constexpr int kSplitMax = 64;  // two parts a lane in the join
-constexpr int kFill = 304;      // blocks below which the work is split: two for each SM
+// fp32: blocks below which the work is split, two for each SM.  Eight items of one token, 5000 states: 76 us against 680
+// unsplit; dk and dv of 512 states from 35840 rows: 2683 us against 12016.
+constexpr int kFill = 304;
 constexpr int kSMs = 152;       // what splits are chosen for
 
 int64_t align256(int64_t x) { return (x + 255) / 256 * 256; }
@@ -496,7 +501,8 @@ struct xattn_shape {
 
 // Parts of `tiles` state tiles for `items` row blocks, fewer than the device's SMs: as many as make the device's
 // rounds of blocks, each as long as its tiles and one more, take the least time.  (Few rows are bound by
-// reading the states, which goes on from one block's item to the next.)
+// reading the states, which goes on from one block's item to the next.)  Eight items of one token, 32 heads on 8, 8192
+// states: 68 us against 76 in one part (64 blocks).
 int32_t split_states(int64_t items, int64_t tiles)
 {
     if (items == 0 || items >= kSMs || tiles < 2) return 1;
@@ -514,7 +520,8 @@ int32_t split_states(int64_t items, int64_t tiles)
 
 // Parts of the row blocks of a state tile (dk, dv; bf16): the device's rounds of blocks, each as long as its
 // row tiles and about three more, against the parts' way through memory (16 bytes an element written and read,
-// in row-tile times of 1.1 us).
+// in row-tile times of 1.1 us).  35840 rows of 16 heads of 128 on 4, 640 states: gradients in 476 us against 1779 in one
+// part (20 blocks); 16 heads of 64, 1000 states (128 blocks): 515 against 509.
 int64_t split_rows(int64_t base, int64_t units, int64_t heads, int64_t elements)
 {
     int64_t split = 1;
@@ -827,6 +834,8 @@ extern "C" tdp_status tdp_cross_attn(tdp_plan_t plan, const tdp_xattn *p, const 
     cudaError_t err;
     if (g.dtype == TDP_BF16) {
         err = tc_kept(sh, &a, w, s);
+        // heads to 64 columns have kernels of their own: 156 us, gradients 515, against 200 and 693 in those for 128
+        // (35840 rows, 16 heads of 64, 1000 states)
         if (err == cudaSuccess) err = a.D <= 64 ? tc_forward<64>(g, a, s) : tc_forward<128>(g, a, s);
     } else {
         err = a.D <= 64 ? simt_kernels<64>::forward(g, a, s) : simt_kernels<128>::forward(g, a, s);
