@@ -417,14 +417,7 @@ tdp_xattn_dq_kernel(const __grid_constant__ tdp_geom g, const __grid_constant__ 
                 for (int32_t j = 0; j < n; ++j) {
                     const uint4 m = it.keys.mask(j);
                     if (!(ok = ok && mbar_wait(full + 8 * kv.st, kv.ph, dead))) break;
-                    constexpr int C = DP / 8;           // 16-byte chunks of a row
-#pragma unroll 1
-                    for (int32_t i = whole(m) ? 128 * C : lane; i < 128 * C; i += 32) {
-                        const int32_t krow = i / C, col = i % C;
-                        const uint32_t word = krow < 64 ? (krow < 32 ? m.x : m.y) : (krow < 96 ? m.z : m.w);
-                        if (!((word >> (krow & 31)) & 1))
-                            st_zero16(kv_s + kv.st * SM::kTile + (col / 8) * 16384 + panel_off(krow, col & 7));
-                    }
+                    zero_dropped<DP>(kv_s + kv.st * SM::kTile, m, lane);
                     fence_async();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(clean + 8 * (kc & 3));

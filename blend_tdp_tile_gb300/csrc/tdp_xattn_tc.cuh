@@ -89,6 +89,30 @@ struct key_list {
 };
 __device__ __forceinline__ bool whole(const uint4 &m) { return (m.x & m.y & m.z & m.w) == ~0u; }
 
+// Zeroes the rows of a tile whose states are dropped, two or four rows at a time: a warp.  (Row by row with a test each
+// took longer than the tile's products.)
+template <int DP>
+__device__ __forceinline__ void zero_dropped(uint32_t tile, const uint4 &m, int32_t lane)
+{
+    constexpr int C = DP / 8, R = 32 / C;       // 16-byte chunks of a row, rows at a time
+    const int32_t col = lane % C;
+#pragma unroll 1
+    for (int32_t i = 0; i < 4; ++i) {
+        uint32_t gone = ~(i < 2 ? (i ? m.y : m.x) : (i > 2 ? m.w : m.z));
+#pragma unroll 1
+        while (gone) {
+            int32_t row = -1;
+#pragma unroll
+            for (int p = 0; p < R; ++p) {
+                const int32_t r = __ffs(gone) - 1;
+                gone &= gone - 1;
+                if (lane / C == p) row = r;
+            }
+            if (row >= 0) st_zero16(tile + (col / 8) * 16384 + panel_off(32 * i + row, col & 7));
+        }
+    }
+}
+
 // One work item.
 struct item {
     tdp_seg seg;
@@ -219,22 +243,6 @@ tdp_xattn_tc_kernel(const __grid_constant__ tdp_geom g, const __grid_constant__ 
                 cur.advance(nt);
                 fence_after();
                 if (warp_on) {
-                    if (!whole(mk)) {
-                        // states that the mask drops: -inf, in place
-#pragma unroll 1
-                        for (int i = 0; i < 8; ++i) {
-                            const uint32_t word = (i < 4 ? (i < 2 ? mk.x : mk.y) : (i < 6 ? mk.z : mk.w)) >> (i & 1) * 16;
-                            uint32_t x[16];
-                            tmem_ld16(S + 16 * i, x);
-                            tmem_wait_ld();
-                            tmem_have16(x);
-#pragma unroll
-                            for (int u = 0; u < 16; ++u)
-                                if (!((word >> u) & 1)) x[u] = 0xff800000u;
-                            tmem_st16(S + 16 * i, x);
-                        }
-                        tmem_wait_st();
-                    }
                     uint32_t s[64], z[64];
                     tmem_ld32(S, s);
                     tmem_ld32(S + 32, s + 32);
@@ -245,6 +253,16 @@ tdp_xattn_tc_kernel(const __grid_constant__ tdp_geom g, const __grid_constant__ 
                     tmem_have32(s + 32);
                     tmem_have32(z);
                     tmem_have32(z + 32);
+                    if (!whole(mk)) {
+                        // states that the mask drops
+#pragma unroll
+                        for (int u = 0; u < 32; ++u) {
+                            if (!((mk.x >> u) & 1)) s[u] = 0xff800000u;
+                            if (!((mk.y >> u) & 1)) s[32 + u] = 0xff800000u;
+                            if (!((mk.z >> u) & 1)) z[u] = 0xff800000u;
+                            if (!((mk.w >> u) & 1)) z[32 + u] = 0xff800000u;
+                        }
+                    }
                     float top[4];
 #pragma unroll
                     for (int u = 0; u < 4; ++u) top[u] = fmaxf(__uint_as_float(z[u]), __uint_as_float(s[u]));
@@ -503,14 +521,7 @@ tdp_xattn_tc_kernel(const __grid_constant__ tdp_geom g, const __grid_constant__ 
                     const uint32_t v = kv + 2 * j + 1, st = v % NST;
                     ok = mbar_wait(full + 8 * st, (v / NST) & 1, dead);
                     if (!ok) break;
-                    constexpr int C = DP / 8;           // 16-byte chunks of a row
-#pragma unroll 1
-                    for (int32_t i = whole(m) ? 128 * C : lane; i < 128 * C; i += 32) {
-                        const int32_t row = i / C, col = i % C;
-                        const uint32_t word = row < 64 ? (row < 32 ? m.x : m.y) : (row < 96 ? m.z : m.w);
-                        if (!((word >> (row & 31)) & 1))
-                            st_zero16(kv_s + st * SM::kTile + (col / 8) * 16384 + panel_off(row, col & 7));
-                    }
+                    zero_dropped<DP>(kv_s + st * SM::kTile, m, lane);
                     fence_async();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(clean + 8 * st);
