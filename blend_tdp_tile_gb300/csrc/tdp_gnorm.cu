@@ -17,11 +17,14 @@
 //     and its barriers cost more (the launch that it saves costs a host that launches one by one 4 us).  One grid
 //     that takes chunks of sums and, some segments later, of the elementwise pass in turn: its tickets, joins and
 //     flags took 934 us.  Slices of a few channels kept in a cluster read 32-byte pieces of rows, 2171 us.
-//   - rows wider than a block's 256 vectors: sums, join and elementwise pass as launches of their own.
+//     Rows of more vectors than a block's 256 threads are split into slabs of whole groups (92 MB of 1280
+//     channels, the gradient: 93 us against 344 in the way below).
+//   - groups wider than 256 vectors: sums, join and elementwise pass as launches of their own.
 // Variances are sums of squared deviations, of a block's values about their mean or joined by
 // T. Chan's rule, so that a mean far from zero costs no digits.  Every join runs in a fixed order.
 #include <algorithm>
 #include <atomic>
+#include <numeric>
 
 #include "tdp.h"
 #include "tdp_internal.h"
@@ -30,11 +33,10 @@
 namespace {
 
 constexpr int kGnThreads = 256;
-constexpr int kGnWideRows = 256;            // rows of a chunk, wide rows
+constexpr int kGnWideRows = 256;            // rows of a chunk at most, groups wider than a block
 constexpr int kGnBlocks = 3;                // blocks that an SM holds
 constexpr int kGnChunkMost = 256 << 10;     // bytes of x of a chunk: 128 KB 620 us, 350 KB 575 us where this takes 570
 constexpr int kGnChunkLeast = 32 << 10;
-constexpr int kGnGroups = 4096;             // groups whose sums a block joins itself
 
 // SiLU is z * s, s = 1 / (1 + exp(-z)); its slope s + z s (1 - s).  exp(-z) overflows to infinity for z below -88: s = 0,
 // SiLU's limit.  The gradient kernels are bound by instructions as much as by memory: two table instructions and a
@@ -61,6 +63,7 @@ struct gn_args {
     fast_div by_cg;
     int32_t chunks, rows;       // chunks per segment, rows per chunk
     uint32_t pblocks;           // blocks that add up dgamma and dbeta
+    int32_t slabs, slab;        // blocks side by side on a row, channels of each: whole groups
     float eps;
     const void *x, *gamma, *beta, *dy;
     void *y;                    // y or dx
@@ -337,26 +340,28 @@ tdp_gn_sums_kernel(const __grid_constant__ tdp_geom g, const gn_args a)
     constexpr int V = E::V;
     extern __shared__ __align__(16) unsigned char dyn[];
     float2 *red = reinterpret_cast<float2 *>(dyn);      // after the last rows: [threads * V + threads / 2]
-    const int32_t s = blockIdx.x / a.chunks, ch = blockIdx.x % a.chunks, CV = a.C / V;
+    const int32_t unit = blockIdx.x / a.slabs, s = unit / a.chunks, ch = unit % a.chunks, CV = a.C / V;
+    const int32_t c0 = (blockIdx.x - unit * a.slabs) * a.slab, cs = min(a.slab, a.C - c0), G0 = c0 / a.cg, Gs = cs / a.cg;      // slab
     const tdp_seg seg = tdp_seg_at(g, s);
     const int64_t r0 = (int64_t)ch * a.rows;
     const int32_t rows = (int32_t)min((int64_t)a.rows, seg.T - r0);
-    const gn_lane l(CV, kGnThreads);
+    const gn_lane l(cs / V, kGnThreads);
+    float2 *chan = reinterpret_cast<float2 *>(a.part) + (int64_t)unit * a.C + c0;
     tdp_pdl_trigger();
     tdp_pdl_wait();
     if (rows <= 0) {
         // a shorter segment: its parts of dgamma and dbeta are nothing
         if (GRAD && a.dgamma)
-            for (int32_t c = threadIdx.x; c < a.C; c += kGnThreads)
-                reinterpret_cast<float2 *>(a.part)[(int64_t)blockIdx.x * a.C + c] = make_float2(0.f, 0.f);
+            for (int32_t c = threadIdx.x; c < cs; c += kGnThreads) chan[c] = make_float2(0.f, 0.f);
         return;
     }
     float p[V], s1[V], s2[V], n = 0.f;
 #pragma unroll
     for (int j = 0; j < V; ++j) p[j] = s1[j] = s2[j] = 0.f;
     if (l.on && l.row < rows) {
-        const X *x = reinterpret_cast<const X *>(a.x) + (seg.row0 + r0) * CV + l.col;
-        const X *dy = reinterpret_cast<const X *>(a.dy) + (seg.row0 + r0) * CV + l.col;
+        const int32_t col = c0 / V + l.col;
+        const X *x = reinterpret_cast<const X *>(a.x) + (seg.row0 + r0) * CV + col;
+        const X *dy = reinterpret_cast<const X *>(a.dy) + (seg.row0 + r0) * CV + col;
         gn_cols<BF16, GRAD> k;
         const int32_t mine = (rows - l.row + l.step - 1) / l.step, step = l.step * CV;     // rows of this thread
         auto add = [&](const X &xv, const X &dv) {
@@ -378,7 +383,7 @@ tdp_gn_sums_kernel(const __grid_constant__ tdp_geom g, const gn_args a)
             }
         };
         gn_feed<BF16, GRAD> feed(dyn, x + l.row * CV, dy + l.row * CV, step, mine);
-        if (GRAD) k.moments(a, s, l.col);
+        if (GRAD) k.moments(a, s, col);
         constexpr int U = feed.kGroup;
         for (int32_t i = 0; i < mine; i += U) {
             X u[U], d[U];
@@ -401,19 +406,17 @@ tdp_gn_sums_kernel(const __grid_constant__ tdp_geom g, const gn_args a)
     }
     __syncthreads();
     join_lanes<V, GRAD>(red, l, n, s1, s2);
-    float2 *out = reinterpret_cast<float2 *>(a.gpart) + ((int64_t)s * a.chunks + ch) * a.G;
-    if (GRAD && a.dgamma) {
-        float2 *chan = reinterpret_cast<float2 *>(a.part) + ((int64_t)s * a.chunks + ch) * a.C;
-        for (int32_t c = threadIdx.x; c < a.C; c += kGnThreads) chan[c] = red[c];
-    }
-    const gn_team team(a.G, kGnThreads);
-    team.each(a.G, [&](int32_t gr, bool on) {
+    float2 *out = reinterpret_cast<float2 *>(a.gpart) + (int64_t)unit * a.G + G0;
+    if (GRAD && a.dgamma)
+        for (int32_t c = threadIdx.x; c < cs; c += kGnThreads) chan[c] = red[c];
+    const gn_team team(Gs, kGnThreads);
+    team.each(Gs, [&](int32_t gr, bool on) {
         float m = 0.f, q = 0.f;
         const int32_t many = on ? a.cg : 0;
         if (GRAD) {
             for (int32_t i = team.lane; i < many; i += team.width) {
                 const float2 v = red[gr * a.cg + i];
-                const float w = param<BF16>(a.gamma, gr * a.cg + i, 1.f);
+                const float w = param<BF16>(a.gamma, c0 + gr * a.cg + i, 1.f);
                 m += v.x * w;
                 q += v.y * w;
             }
@@ -469,26 +472,28 @@ tdp_gn_apply_kernel(const __grid_constant__ tdp_geom g, const gn_args a)
     if (GRAD && blockIdx.x < a.pblocks) {
         tdp_pdl_trigger();
         tdp_pdl_wait();
-        gn_params(a, reinterpret_cast<const float2 *>(a.part), (int32_t)(gridDim.x - a.pblocks), blockIdx.x, reinterpret_cast<float2 *>(dyn));
+        gn_params(a, reinterpret_cast<const float2 *>(a.part), (int32_t)((gridDim.x - a.pblocks) / a.slabs), blockIdx.x, reinterpret_cast<float2 *>(dyn));
         return;
     }
-    const int32_t unit = gridDim.x - 1 - blockIdx.x, s = unit / a.chunks, ch = unit % a.chunks, CV = a.C / V;
+    const int32_t at_unit = gridDim.x - 1 - blockIdx.x, unit = at_unit / a.slabs, s = unit / a.chunks, ch = unit % a.chunks, CV = a.C / V;
+    const int32_t c0 = (at_unit - unit * a.slabs) * a.slab, cs = min(a.slab, a.C - c0), G0 = c0 / a.cg, Gs = cs / a.cg;      // slab
     const tdp_seg seg = tdp_seg_at(g, s);
     const int64_t r0 = (int64_t)ch * a.rows;
     const int32_t rows = (int32_t)min((int64_t)a.rows, seg.T - r0), chunks = (int32_t)((seg.T + a.rows - 1) / a.rows);
-    const gn_lane l(CV, kGnThreads);
+    const gn_lane l(cs / V, kGnThreads);
+    const int32_t col = c0 / V + l.col;
     tdp_pdl_trigger();
     tdp_pdl_wait();
     if (rows <= 0) return;
-    const int64_t at = (seg.row0 + r0) * CV + l.col;
+    const int64_t at = (seg.row0 + r0) * CV + col;
     const X *x = reinterpret_cast<const X *>(a.x) + at, *dy = reinterpret_cast<const X *>(a.dy) + at;
     X *y = reinterpret_cast<X *>(a.y) + at;
     const int32_t mine = l.on ? (rows - l.row + l.step - 1) / l.step : 0, step = l.step * CV;        // rows of this thread
     gn_feed<BF16, GRAD> feed(dyn, x + l.row * CV, dy + l.row * CV, step, mine);         // ahead of the join
     const float n = (float)seg.T * a.cg;
-    const float2 *part = reinterpret_cast<const float2 *>(a.gpart) + (int64_t)s * a.chunks * a.G;
-    const gn_team team(a.G, kGnThreads);
-    team.each(a.G, [&](int32_t gr, bool on) {
+    const float2 *part = reinterpret_cast<const float2 *>(a.gpart) + (int64_t)s * a.chunks * a.G + G0;
+    const gn_team team(Gs, kGnThreads);
+    team.each(Gs, [&](int32_t gr, bool on) {
         float m = 0.f, q = 0.f;
         const int32_t many = on ? chunks : 0;
         if (GRAD) {
@@ -507,8 +512,8 @@ tdp_gn_apply_kernel(const __grid_constant__ tdp_geom g, const gn_args a)
             }, m, q);
             q = 1.f / sqrtf(q / n + a.eps);
             if (on && ch == 0 && team.lane == 0) {
-                a.mean[(int64_t)s * a.G + gr] = m;
-                a.rstd[(int64_t)s * a.G + gr] = q;
+                a.mean[(int64_t)s * a.G + G0 + gr] = m;
+                a.rstd[(int64_t)s * a.G + G0 + gr] = q;
             }
         }
         if (on && team.lane == 0) grp[gr] = make_float2(m, q);
@@ -516,8 +521,8 @@ tdp_gn_apply_kernel(const __grid_constant__ tdp_geom g, const gn_args a)
     __syncthreads();
     if (!l.on || l.row >= rows) return;
     gn_cols<BF16, GRAD> k;
-    if (GRAD) k.moments(a, s, l.col);
-    else k.params(a, l.col);
+    if (GRAD) k.moments(a, s, col);
+    else k.params(a, col);
 #pragma unroll
     for (int j = 0; j < V; ++j) {
         const float2 v = grp[a.by_cg.div(l.col * V + j)];
@@ -551,7 +556,7 @@ tdp_gn_apply_kernel(const __grid_constant__ tdp_geom g, const gn_args a)
     }
 }
 
-// ------------------------------------------------------------------ wide rows
+// ------------------------------------------------------------------ wide groups
 // A thread per column of vectors; blockIdx.y takes 256 of them.
 template <int BF16, int GRAD, int ACT>
 __global__ void __launch_bounds__(kGnThreads)
@@ -575,6 +580,7 @@ tdp_gn_wide_sums_kernel(const __grid_constant__ tdp_geom g, const gn_args a)
     E::unpack(x[0], p);
     gn_cols<BF16, GRAD> k;
     if (GRAD) k.moments(a, s, col);
+#pragma unroll 4
     for (int32_t r = 0; r < rows; ++r) {
         float f[V], e[V];
         E::unpack(x[(int64_t)r * CV], f);
@@ -670,6 +676,7 @@ tdp_gn_wide_apply_kernel(const __grid_constant__ tdp_geom g, const gn_args a)
     gn_cols<BF16, GRAD> k;
     k.moments(a, s, col);
     if (GRAD) k.means(a, s, col);
+#pragma unroll 4
     for (int32_t r = 0; r < rows; ++r) {
         float f[V], e[V];
         E::unpack(x[(int64_t)r * CV], f);
@@ -696,7 +703,7 @@ tdp_gn_wide_param_kernel(const gn_args a, int32_t segs)
 // ------------------------------------------------------------------ host
 struct gn_plan {
     bool wide;
-    int32_t chunks, rows;
+    int32_t chunks, rows, slabs, slab;
     int64_t gpart_at, coef_at, gmean_at, bytes;
 };
 
@@ -712,18 +719,25 @@ tdp_status gn_check(tdp_plan_t plan, int32_t C, int32_t groups, int grad, gn_pla
     const int64_t CV = C / V, bytes = V * g.esize, T = tdp_max_tile_tokens(g), segs = (int64_t)g.nt * g.B;
     if (CV > (int64_t)kGnThreads * 65535 || (int64_t)g.B * g.total > ((int64_t)1 << 56) / C)
         return tdp_fail(TDP_ERR_TOO_LARGE, "group normalisation beyond index ranges");
-    p->wide = CV > kGnThreads || groups > kGnGroups;
+    // rows of more vectors than a block has threads are split into slabs of whole groups and vectors
+    const int64_t piece = std::lcm((int64_t)(C / groups), (int64_t)V), pieces = C / piece, fit = (int64_t)kGnThreads * V / piece;
+    p->wide = fit == 0;
+    p->slabs = p->wide ? 1 : (int32_t)((pieces + fit - 1) / fit);
+    p->slab = (int32_t)((pieces + p->slabs - 1) / p->slabs * piece);
     if (p->wide) {
-        p->rows = kGnWideRows;
+        // as many blocks as fill the device, of 16 rows at least
+        const int64_t fill = (int64_t)g.B * g.total * ((CV + kGnThreads - 1) / kGnThreads) / (152 * 8);
+        p->rows = (int32_t)std::min<int64_t>(std::max<int64_t>(fill, 16), kGnWideRows);
     } else {
         // chunks for whole rounds of the blocks that the device holds; a segment's last chunk is half full on average
         const int64_t all = (int64_t)g.B * g.total, round = 152 * kGnBlocks, most = round * kGnChunkMost;
         const int64_t units = (all * CV * bytes + most - 1) / most * round;
-        const int64_t want = (all + units - 1) / std::max<int64_t>(units - segs / 2, 1), least = (kGnChunkLeast + CV * bytes - 1) / (CV * bytes);
+        const int64_t want = (all * p->slabs + units - 1) / std::max<int64_t>(units - segs * p->slabs / 2, 1);
+        const int64_t row = (int64_t)p->slab * g.esize, least = (kGnChunkLeast + row - 1) / row;
         p->rows = (int32_t)std::max(std::min(want, T), least);
     }
     const int64_t chunks = (T + p->rows - 1) / p->rows;
-    if (chunks * segs > 0x7fffffffLL - (C + 3) / 4) return tdp_fail(TDP_ERR_TOO_LARGE, "group normalisation beyond index ranges");
+    if (chunks * segs * p->slabs > 0x7fffffffLL - (C + 3) / 4) return tdp_fail(TDP_ERR_TOO_LARGE, "group normalisation beyond index ranges");
     p->chunks = (int32_t)chunks;
     auto up = [](int64_t x) { return (x + 255) / 256 * 256; };
     p->gpart_at = up(segs * p->chunks * C * 8);
@@ -765,12 +779,12 @@ cudaError_t gn_run(const tdp_geom &g, const gn_plan &p, const gn_args &a, cudaSt
         if (err == cudaSuccess && (dev >= 64 || !done[dev].load(std::memory_order_relaxed))) {
             const auto attr = cudaFuncAttributeMaxDynamicSharedMemorySize;
             err = cudaFuncSetAttribute(tdp_gn_sums_kernel<BF16, GRAD, ACT>, attr, feed);
-            if (err == cudaSuccess) err = cudaFuncSetAttribute(tdp_gn_apply_kernel<BF16, GRAD, ACT>, attr, feed + kGnGroups * 8);
+            if (err == cudaSuccess) err = cudaFuncSetAttribute(tdp_gn_apply_kernel<BF16, GRAD, ACT>, attr, feed + kGnThreads * V * 8);
             if (err == cudaSuccess && dev < 64) done[dev].store(true, std::memory_order_relaxed);
         }
-        const dim3 grid((unsigned)(segs * p.chunks));
+        const dim3 grid((unsigned)(segs * p.chunks * p.slabs));
         if (err == cudaSuccess) err = gn_launch(tdp_gn_sums_kernel<BF16, GRAD, ACT>, grid, (size_t)feed, s, g, a);
-        if (err == cudaSuccess) err = gn_launch(tdp_gn_apply_kernel<BF16, GRAD, ACT>, dim3(grid.x + a.pblocks), (size_t)feed + a.G * 8, s, g, a);
+        if (err == cudaSuccess) err = gn_launch(tdp_gn_apply_kernel<BF16, GRAD, ACT>, dim3(grid.x + a.pblocks), (size_t)feed + a.slab / a.cg * 8, s, g, a);
     } else {
         const dim3 grid((unsigned)(segs * p.chunks), (unsigned)((a.C / V + kGnThreads - 1) / kGnThreads));
         err = gn_launch(tdp_gn_wide_sums_kernel<BF16, GRAD, ACT>, grid, 0, s, g, a);
@@ -790,6 +804,8 @@ cudaError_t gn_dispatch(const tdp_geom &g, const gn_plan &p, gn_args a, int32_t 
     a.by_cg = fast_div_by(a.cg);
     a.chunks = p.chunks;
     a.rows = p.rows;
+    a.slabs = p.slabs;
+    a.slab = p.slab;
     a.pblocks = GRAD && a.dgamma ? (a.C + 3) / 4 : 0;
     a.part = reinterpret_cast<float *>(w);
     a.gpart = reinterpret_cast<float *>(w + p.gpart_at);

@@ -198,3 +198,11 @@ def test_offsets_past_32_bits(tdp):
     tdp.tdp_group_norm_grad(plan, x, G, None, None, mean, rstd, x, dx)
     # dy = x: dx = rstd * (x - mean(x) - h * mean(x h)) = h * (1 - (1 - eps rstd^2)): nearly zero everywhere
     assert dx[a:].float().abs().max() < 1e-3
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("C,G", [(1280, 32), (2080, 2080), (3000, 25), (4096, 1), (5000, 5)])
+def test_rows_wider_than_a_block(tdp, dtype, C, G):
+    """Several slabs of whole groups a row, the last one narrower; groups wider than a block."""
+    run(tdp, TINY, dtype, C, G, "silu", True)
+    run(tdp, (2, (2, 17, 23), (1, 2, 2), (0, 2, 2)), dtype, C, G, "none", True)
