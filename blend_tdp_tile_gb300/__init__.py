@@ -20,6 +20,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import threading
 
 import numpy as np
 
@@ -156,6 +157,7 @@ class Plan:
         self._h = ctypes.c_void_p(handle)
         self.problem = problem
         self.sizes = {}             # workspace bytes by shape
+        self.scratch = {}           # small workspaces by device, stream and thread
         n = ctypes.c_int32()
         tot = ctypes.c_int64()
         _check(_lib.tdp_plan_info(self._h, ctypes.byref(n), ctypes.byref(tot), None, None), "tdp_plan_info")
@@ -569,13 +571,26 @@ def _strides(t, name, shape, dtypes):
     return tuple(st if n > 1 else 0 for n, st in zip(t.shape[:-1], t.stride()[:-1]))
 
 
-def _workspace(ws, need, like, stream):
-    """A workspace of `need` bytes: the caller's, or one of torch's for the stream of the call."""
+_SCRATCH = 1 << 20          # bytes of a workspace that a plan keeps
+
+
+def _workspace(ws, need, like, stream, plan):
+    """A workspace of `need` bytes: the caller's, or one of torch's for the stream of the call.
+
+    A small one stays with the plan, one per stream and thread, where calls follow one another: an allocation between
+    launches costs some 6 us, a third of a small call.  A call that is being captured gets its own, from the graph's pool."""
     if ws is not None or need == 0:
         return ws
     torch = _torch()
     if stream is None:
-        return torch.empty(need, dtype=torch.uint8, device=like.device)
+        raw, dev = getattr(torch._C, "_cuda_getCurrentRawStream", None), like.get_device()
+        if need > _SCRATCH or raw is None or dev < 0 or dev != torch.cuda.current_device() or torch.cuda.is_current_stream_capturing():
+            return torch.empty(need, dtype=torch.uint8, device=like.device)
+        key = dev, raw(dev), threading.get_ident()
+        kept = plan.scratch.get(key)
+        if kept is None or kept.numel() < need:
+            kept = plan.scratch[key] = torch.empty(need, dtype=torch.uint8, device=like.device)
+        return kept
     if isinstance(stream, int):
         stream = torch.cuda.ExternalStream(stream, device=like.device)
     with torch.cuda.stream(stream):
@@ -633,7 +648,7 @@ def tdp_cross_attn(plan: Plan, q, k, v, mask, out, lse=None, scale=None, ws=None
     a = _xattn_shape(plan, q, k, v, mask, scale)
     n = ctypes.c_int64()
     _check(_lib.tdp_cross_attn_workspace(plan.handle, ctypes.byref(a), 0, ctypes.byref(n)), "tdp_cross_attn")
-    ws = _workspace(ws, n.value, q, stream)
+    ws = _workspace(ws, n.value, q, stream, plan)
     c = _Call("tdp_cross_attn")
     c.run(_lib.tdp_cross_attn, plan.handle, ctypes.byref(a), _given(c, q, "q"), _given(c, k, "k"), _given(c, v, "v"),
           _xattn_mask(c, plan, a, mask),
@@ -651,7 +666,7 @@ def tdp_cross_attn_grad(plan: Plan, q, k, v, mask, out, lse, dout, dq, dk, dv, s
     a = _xattn_shape(plan, q, k, v, mask, scale)
     n = ctypes.c_int64()
     _check(_lib.tdp_cross_attn_workspace(plan.handle, ctypes.byref(a), 1, ctypes.byref(n)), "tdp_cross_attn_grad")
-    ws = _workspace(ws, n.value, q, stream)
+    ws = _workspace(ws, n.value, q, stream, plan)
     c = _Call("tdp_cross_attn_grad")
     c.run(_lib.tdp_cross_attn_grad, plan.handle, ctypes.byref(a), _given(c, q, "q"), _given(c, k, "k"),
           _given(c, v, "v"), _xattn_mask(c, plan, a, mask), c.ptr(out, "out", q.numel(), lat, 16),
@@ -682,7 +697,7 @@ def tdp_group_norm(plan: Plan, x, groups, gamma, beta, y, mean, rstd, eps=1e-5, 
     [n_tiles, B, groups] are written too.  gamma, beta: [C] or None.  act: "none" or "silu"."""
     f32, lat = (_torch().float32,), _latent_dtypes(plan)
     C, ns = int(x.shape[-1]), plan.n_tiles * plan.B * int(groups)
-    ws = _workspace(ws, tdp_group_norm_workspace(plan, C, groups), x, stream)
+    ws = _workspace(ws, tdp_group_norm_workspace(plan, C, groups), x, stream, plan)
     c = _Call("tdp_group_norm")
     c.run(_lib.tdp_group_norm, plan.handle, C, int(groups), float(eps), _act(act), c.ptr(x, "x", _rows(plan) * C, lat, 16),
           c.ptr(gamma, "gamma", C, lat, 16), c.ptr(beta, "beta", C, lat, 16), c.ptr(y, "y", _rows(plan) * C, lat, 16),
@@ -696,7 +711,7 @@ def tdp_group_norm_grad(plan: Plan, x, groups, gamma, beta, mean, rstd, dy, dx, 
     """Gradients of tdp_group_norm: dx [R, C] and, unless None, dgamma and dbeta [C] in fp32."""
     f32, lat = (_torch().float32,), _latent_dtypes(plan)
     C, ns = int(x.shape[-1]), plan.n_tiles * plan.B * int(groups)
-    ws = _workspace(ws, tdp_group_norm_workspace(plan, C, groups), x, stream)
+    ws = _workspace(ws, tdp_group_norm_workspace(plan, C, groups), x, stream, plan)
     c = _Call("tdp_group_norm_grad")
     n = _rows(plan) * C
     c.run(_lib.tdp_group_norm_grad, plan.handle, C, int(groups), _act(act), c.ptr(x, "x", n, lat, 16),

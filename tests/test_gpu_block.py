@@ -75,3 +75,36 @@ def test_example_runs_and_learns(tdp, name):
     spec.loader.exec_module(mod)
     Z, losses = mod.run(name, steps=6, log=lambda *_: None)
     assert torch.isfinite(Z.float()).all() and losses[-1] < losses[0]
+
+
+def test_kept_workspaces(tdp):
+    """A plan's small workspace serves calls of one stream; two streams at once and a graph use their own."""
+    import torch
+    plan = tdp.tdp_plan_create(1, 5, 9, 14, 8, "f32", (2, 2, 2), (2, 3, 3))
+    R, C, G = plan.B * plan.total_tile_tokens, 64, 8
+    x = [torch.randn(R, C, device="cuda") + i for i in range(2)]
+    stat = lambda: torch.empty(plan.n_tiles * plan.B * G, device="cuda")  # noqa: E731
+    y, st = [torch.empty_like(t) for t in x], [(stat(), stat()) for _ in x]
+    want = []
+    for t in x:
+        o = torch.empty_like(t)
+        tdp.tdp_group_norm(plan, t, G, None, None, o, stat(), stat())
+        want.append(o)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in x]
+    for _ in range(50):
+        for t, o, s, m in zip(x, y, streams, st):
+            with torch.cuda.stream(s):
+                tdp.tdp_group_norm(plan, t, G, None, None, o, *m)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(y, want))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        tdp.tdp_group_norm(plan, x[0], G, None, None, y[0], *st[0])
+    y[0].fill_(0)
+    for _ in range(20):         # replays beside calls of another stream
+        with torch.cuda.stream(streams[0]):
+            graph.replay()
+        tdp.tdp_group_norm(plan, x[1], G, None, None, y[1], *st[1])
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(y, want))
