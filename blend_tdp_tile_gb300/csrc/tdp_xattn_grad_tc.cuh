@@ -15,8 +15,9 @@
 //   warp 11          zeroes rows of a tile that must not count (their memory may hold anything, and 0 * NaN is not 0)
 //
 // 35840 rows, 16 heads of 128 on 4, 640 states: dq in 236 us (1.19 PFLOP/s, tensor pipe 50 % busy: one row tile, whose
-// products wait for its softmax), dk and dv in 230 us (1.63 PFLOP/s, 69 %).  Tried: dP's columns given back as soon as they
-// are read made a tile of dq 14 % shorter in one launch and no pass shorter, the clock falling at the power limit.
+// products wait for its softmax), dk and dv in 230 us (1.63 PFLOP/s, 69 %).  dP's columns are given back as soon as they
+// are read: a tile of dq takes 1920 cycles for 2240 in one launch; both gradients at 16 heads of 64, 1000 states, 523 us for
+// 544, at 128 columns 1 % less, the clock falling at the power limit.
 #pragma once
 
 #include "tdp_xattn_tc.cuh"
@@ -84,7 +85,7 @@ tdp_xattn_dq_kernel(const __grid_constant__ tdp_geom g, const __grid_constant__ 
     const uint32_t q_s = base, do_s = q_s + SM::kTile, kv_s = do_s + SM::kTile, bars = kv_s + NST * SM::kTile, stat_s = bars + 512;
     const uint32_t full = bars, empty = full + 8 * NST, clean = empty + 8 * NST, rfull = clean + 32, rempty = rfull + 16,
                    sfull = rempty + 16, pfull = sfull + 16, dsfull = pfull + 8,
-                   done = dsfull + 8, drain = done + 8;
+                   done = dsfull + 8, drain = done + 8, pread = drain + 8;
     __shared__ uint32_t tmem_slot;
     __shared__ int dead_flag;
     volatile int *dead = &dead_flag;
@@ -103,6 +104,7 @@ tdp_xattn_dq_kernel(const __grid_constant__ tdp_geom g, const __grid_constant__ 
             mbar_init(sfull + 8 * i, 1);
         }
         mbar_init(pfull, 1);
+        mbar_init(pread, 8);
         mbar_init(dsfull, 8);
         mbar_init(done, 1);
         mbar_init(drain, 1);
@@ -203,6 +205,10 @@ tdp_xattn_dq_kernel(const __grid_constant__ tdp_geom g, const __grid_constant__ 
                     tmem_have32(s + 32);
                     tmem_have32(e);
                     tmem_have32(e + 32);
+                    // dP may be made anew: the next tile's runs under this one's arithmetic
+                    fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(pread);
 #pragma unroll
                     for (int u = 0; u < 32; ++u) {
                         float x, y;
@@ -366,7 +372,7 @@ tdp_xattn_dq_kernel(const __grid_constant__ tdp_geom g, const __grid_constant__ 
                 };
                 kv.next();                      // O
                 uint32_t k_prev = 0;
-                // round j: S of state tile j + 1 ahead, then dP of j + 1 and dQ of j once dS of j is there
+                // round j: S of state tile j + 1 ahead, dP of j + 1 once that of j has been read, dQ of j once dS of j is there
 #pragma unroll 1
                 for (int32_t j = -1; j < n; ++j) {
                     const uint32_t b1 = n_done & 1, k1 = kv.st;     // n_done: S products so far
@@ -376,22 +382,28 @@ tdp_xattn_dq_kernel(const __grid_constant__ tdp_geom g, const __grid_constant__ 
                         if (!(a.mask ? wait(clean + 8 * (kc & 3), (kc >> 2) & 1) : wait(full + 8 * k1, kv.ph))) break;
                         ++kc;
                         rows(tm + 128 * b1, q_d, desc_rows(kv_s + k1 * SM::kTile), sfull + 8 * b1, j + 2 == n ? rempty : 0, 0,
-                             j >= 0 ? dsfull : 0, (n_done - 1) & 1);
+                             j >= 0 ? pread : 0, (n_done - 1) & 1);
                         ++n_done;
                         kv.next();
                     }
-                    if (j >= 0) {
-                        if (!wait(dsfull, (j + 1 < n ? n_done : n_done + 1) & 1)) break;
-                        fence_after();
-                    }
+                    const uint32_t tile = (j + 1 < n ? n_done : n_done + 1) & 1;         // parity of tile j
                     if (j + 1 < n) {
                         if (j < 0 && !(ok = mbar_wait(rfull + 8, ph, dead))) break;
+                        if (j >= 0) {
+                            if (!wait(pread, tile)) break;
+                            fence_after();
+                        }
                         if (!wait(full + 8 * kv.st, kv.ph)) break;
-                        rows(tm + 256, do_d, desc_rows(kv_s + kv.st * SM::kTile), pfull, empty + 8 * kv.st, j + 2 == n ? rempty + 8 : 0, 0, 0);
+                        rows(tm + 256, do_d, desc_rows(kv_s + kv.st * SM::kTile), pfull, empty + 8 * kv.st, j + 2 == n ? rempty + 8 : 0,
+                             j >= 0 ? dsfull : 0, tile);
                         kv.next();
                     }
                     if (j >= 0) {
-                        const uint32_t ds = tm + 128 * ((j + 1 < n ? n_done : n_done + 1) & 1), y0 = desc_cols(kv_s + k_prev * SM::kTile, 16384);
+                        if (!wait(dsfull, tile)) break;
+                        fence_after();
+                    }
+                    if (j >= 0) {
+                        const uint32_t ds = tm + 128 * tile, y0 = desc_cols(kv_s + k_prev * SM::kTile, 16384);
                         auto step = [&](int i) { mma_ts(tm + 384, ds + 64 * (i / 4) + 8 * (i % 4), y0 + i * (2048 >> 4), id_q, j > 0 || i > 0); };
                         if (elect_one()) {
 #pragma unroll
