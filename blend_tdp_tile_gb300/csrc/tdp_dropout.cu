@@ -14,7 +14,7 @@
 namespace {
 
 constexpr int kDropThreads = 256;
-constexpr int kDropUnroll = 2;      // vectors a thread loads before it computes
+constexpr uint32_t kPhilox0 = 0xD2511F53u, kPhilox1 = 0xCD9E8D57u;
 
 // Round keys of Philox4x32-10: the key and its nine bumps.
 struct philox_keys {
@@ -29,13 +29,29 @@ struct philox_keys {
     }
 };
 
+// What the first two rounds of a counter {index, offset} owe to the offset and the index's high word alone: two of the
+// twenty products, the same for four billion counters.
+struct philox_head {
+    uint32_t hi, c1, c0x;           // index's high word; round 1's input c1; hi(q0) ^ k1 of round 1
+    uint32_t lo;                    // lo(q0)
+    __device__ __forceinline__ void at(uint32_t high, uint64_t offset, const philox_keys &k)
+    {
+        const uint64_t p1 = (uint64_t)(uint32_t)offset * kPhilox1, q0 = (uint64_t)((uint32_t)(p1 >> 32) ^ high ^ k.k0[0]) * kPhilox0;
+        hi = high;
+        c1 = (uint32_t)p1;
+        c0x = (uint32_t)(q0 >> 32) ^ k.k1[1];
+        lo = (uint32_t)q0;
+    }
+};
+
 // Ten rounds of two 32x32 -> 64-bit products.
-__device__ __forceinline__ uint4 philox10(uint64_t index, uint64_t offset, const philox_keys &k)
+__device__ __forceinline__ uint4 philox10(uint32_t index, uint64_t offset, const philox_head &h, const philox_keys &k)
 {
-    uint32_t c0 = (uint32_t)index, c1 = (uint32_t)(index >> 32), c2 = (uint32_t)offset, c3 = (uint32_t)(offset >> 32);
+    const uint64_t f0 = (uint64_t)index * kPhilox0, f1 = (uint64_t)((uint32_t)(f0 >> 32) ^ (uint32_t)(offset >> 32) ^ k.k1[0]) * kPhilox1;
+    uint32_t c0 = (uint32_t)(f1 >> 32) ^ h.c1 ^ k.k0[1], c1 = (uint32_t)f1, c2 = h.c0x ^ (uint32_t)f0, c3 = h.lo;
 #pragma unroll
-    for (int r = 0; r < 10; ++r) {
-        const uint64_t p0 = (uint64_t)c0 * 0xD2511F53u, p1 = (uint64_t)c2 * 0xCD9E8D57u;
+    for (int r = 2; r < 10; ++r) {
+        const uint64_t p0 = (uint64_t)c0 * kPhilox0, p1 = (uint64_t)c2 * kPhilox1;
         c0 = (uint32_t)(p1 >> 32) ^ c1 ^ k.k0[r];
         c1 = (uint32_t)p1;
         c2 = (uint32_t)(p0 >> 32) ^ c3 ^ k.k1[r];
@@ -46,11 +62,13 @@ __device__ __forceinline__ uint4 philox10(uint64_t index, uint64_t offset, const
 
 // The words of vector i's elements.
 template <int V>
-__device__ __forceinline__ void drop_words(int64_t i, uint64_t offset, const philox_keys &k, uint32_t *w)
+__device__ __forceinline__ void drop_words(int64_t i, uint64_t offset, philox_head &h, const philox_keys &k, uint32_t *w)
 {
+    const uint64_t first = (uint64_t)i * (V / 4);           // of one or two counters, an even one where two: one high word
+    if ((uint32_t)(first >> 32) != h.hi) h.at((uint32_t)(first >> 32), offset, k);
 #pragma unroll
     for (int j = 0; j < V / 4; ++j) {
-        const uint4 u = philox10((uint64_t)i * (V / 4) + j, offset, k);
+        const uint4 u = philox10((uint32_t)first + j, offset, h, k);
         w[4 * j] = u.x;
         w[4 * j + 1] = u.y;
         w[4 * j + 2] = u.z;
@@ -58,21 +76,24 @@ __device__ __forceinline__ void drop_words(int64_t i, uint64_t offset, const phi
     }
 }
 
-// 16-byte vectors (4 fp32 or 8 bf16 elements: one or two counters), kDropUnroll of them a thread and step; the vector that
+// 16-byte vectors (4 fp32 or 8 bf16 elements: one or two counters); the vector that
 // holds the end is done element by element by one thread.  `thr` is at most 2^32 - 1; p = 1 has all = 1.
-// 105 million bf16 elements: 104 us, 6.1 TB/s, near the memory's rate; without the residual (the gradient) 95 us, 4.4 TB/s:
-// the generator's 20 wide products for four elements keep the integer multiplier 69 % busy.
+// 105 million bf16 elements: 102 us, 6.2 TB/s, near the memory's rate, with one vector of each input ahead of the
+// generator (107 with two); without the residual (the gradient) three: 92 us, 4.6 TB/s, for 97 with one.  There the
+// generator's wide products, 18 of 20 a thread's own, keep the integer multiplier busy.
 template <int BF16, int RES>
 __global__ void __launch_bounds__(kDropThreads)
 tdp_dropout_kernel(int64_t n, uint32_t thr, int all, float scale, const uint64_t *__restrict__ rng, const void *x,
                    const void *res, void *out)
 {
     using E = tdp_elem<BF16>;
-    constexpr int V = E::kVec, U = kDropUnroll;
+    constexpr int V = E::kVec, U = RES ? 1 : 3;
     tdp_pdl_trigger();
     tdp_pdl_wait();
     const uint64_t offset = rng[1];
     const philox_keys keys(rng[0]);
+    philox_head head;
+    head.at(0, offset, keys);
     const int64_t nv = n / V;
     const uint4 *xv = reinterpret_cast<const uint4 *>(x), *rv = reinterpret_cast<const uint4 *>(res);
     for (int64_t i0 = (int64_t)blockIdx.x * (kDropThreads * U) + threadIdx.x; i0 < nv; i0 += (int64_t)gridDim.x * (kDropThreads * U)) {
@@ -91,7 +112,7 @@ tdp_dropout_kernel(int64_t n, uint32_t thr, int all, float scale, const uint64_t
             if (i >= nv) break;
             uint32_t w[V];
             float f[V], g[V];
-            drop_words<V>(i, offset, keys, w);
+            drop_words<V>(i, offset, head, keys, w);
             E::unpack(a[u], f);
             if (RES) E::unpack(r[u], g);
 #pragma unroll
@@ -105,7 +126,7 @@ tdp_dropout_kernel(int64_t n, uint32_t thr, int all, float scale, const uint64_t
     if (n % V != 0 && blockIdx.x == 0 && threadIdx.x == 0) {
         using T = typename E::type;
         uint32_t w[V];
-        drop_words<V>(nv, offset, keys, w);
+        drop_words<V>(nv, offset, head, keys, w);
 #pragma unroll
         for (int j = 0; j < V; ++j) {
             const int64_t e = nv * V + j;
@@ -129,7 +150,7 @@ tdp_status dropout(tdp_plan_t plan, int64_t n, double p, const uint64_t *rng, co
     const uint64_t thr = (uint64_t)std::llrint(p * 4294967296.0);
     const int all = thr > 0xffffffffull;
     const float scale = p < 1.0 ? (float)(1.0 / (1.0 - p)) : 0.f;
-    const int64_t step = (int64_t)kDropThreads * kDropUnroll * (plan->g.dtype == TDP_BF16 ? 8 : 4);
+    const int64_t step = (int64_t)kDropThreads * (plan->g.dtype == TDP_BF16 ? 8 : 4);
     const unsigned grid = (unsigned)std::min<int64_t>((n + step - 1) / step, 152 * 64);
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     auto *kernel = plan->g.dtype == TDP_BF16 ? (res ? tdp_dropout_kernel<1, 1> : tdp_dropout_kernel<1, 0>)

@@ -115,3 +115,14 @@ def test_elements_past_32_bits(tdp):
     i = np.arange(n - 64, n, dtype=np.uint64)
     words = ref.philox_at(i // np.uint64(4), 11, 3)[np.arange(64), (i % np.uint64(4)).astype(int)]
     assert np.array_equal(x[-64:].float().cpu().numpy(), np.where(words >= 2 ** 31, 2.0, 0.0))
+
+
+def test_counters_past_32_bits(tdp):
+    """2^34 elements and some: the counter's second word is no longer zero."""
+    import torch
+    n, seed, offset, p = (1 << 34) + (1 << 20) + 3, 0x123456789ABCDEF0, (1 << 63) + 5, 0.3
+    x = torch.ones(n, dtype=torch.bfloat16, device="cuda")
+    tdp.tdp_dropout_grad(_plan(tdp, "bf16"), x, p, _rng(seed, offset), x)
+    for a, b in ((0, 4096), ((1 << 34) - 4096, (1 << 34) + 4096), ((n - 5000) // 4 * 4, n)):
+        words = ref.philox_at(np.arange(a // 4, (b + 3) // 4), seed, offset).reshape(-1)[:b - a]
+        assert np.array_equal(words >= np.uint64(round(p * 2 ** 32)), (x[a:b] != 0).cpu().numpy())
