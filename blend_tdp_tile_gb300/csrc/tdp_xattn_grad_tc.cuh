@@ -7,7 +7,8 @@
 // Seven products where a single kernel would have five, but dK and dV then need no atomics and no
 // exchange between blocks: a split over the rows writes fp32 parts that are joined in order.
 // In both, scores and their gradients live in tensor memory; two warpgroups share the columns of a tile (each
-// thread a lane and 64 columns) and write p and dS back as bf16 in place, as the next product's A operand:
+// thread a lane and 64 columns) and write p and dS back as bf16 in place, as the next product's A operand (rounded by a
+// relative 2^-8 at most, 0.0017 in the mean square, as the other operand and the gradient are):
 //   warps 0-3, 4-7   columns 0-63, 64-127; the output
 //   warp 8           loads tiles through tensor maps
 //   warp 9           issues the products

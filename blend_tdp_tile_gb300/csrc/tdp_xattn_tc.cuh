@@ -9,7 +9,8 @@
 //   warp 9           issues the products; P V starts when half of the probabilities are there
 //   warp 11          zeroes the rows of V that a mask drops (their memory may hold anything, and 0 * NaN is not 0)
 // The sums are rescaled only when a row's maximum has grown by more than 2^8 (p then stays below 2^8,
-// exact in the fp32 sums and no coarser in bf16); the last scale divides out.  A persistent grid, one block
+// exact in the fp32 sums and no coarser in bf16); the last scale divides out.  p is rounded to bf16, as the tensor cores
+// take it beside V's bf16: a relative 2^-8 at most, no more than V's own rounding; l sums p as it was before.  A persistent grid, one block
 // per SM, takes (segment, part of the states, head block, row block) items in turn: the next item's loads
 // and first products run under this one's output.
 //
