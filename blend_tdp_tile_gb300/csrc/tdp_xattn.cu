@@ -270,7 +270,7 @@ tdp_xattn_join_kernel(const xattn_args a)
     if (lane == 0 && a.lse) a.lse[h] = sum == 0.f ? -INFINITY : base + logf(sum);
 }
 
-// dq of 64 packed rows; delta = dout . out is written for the kernel that follows.
+// dq of 64 packed rows, or a part of the states' share of it; delta = dout . out is written for the kernel that follows.
 template <int DP>
 __global__ void __launch_bounds__(kXT)
 tdp_xattn_simt_dq_kernel(const __grid_constant__ tdp_geom g, const __grid_constant__ xattn_args a)
@@ -284,7 +284,9 @@ tdp_xattn_simt_dq_kernel(const __grid_constant__ tdp_geom g, const __grid_consta
     const int32_t blk = w % a.blocks;
     w /= a.blocks;
     const int32_t kvh = w % a.Hkv;
-    const tdp_seg seg = xattn_seg(g, a, w / a.Hkv);
+    w /= a.Hkv;
+    const int32_t part = w % a.qsplit;
+    const tdp_seg seg = xattn_seg(g, a, w / a.qsplit);
     const int64_t r0 = (int64_t)blk * kXM, nr = seg.T * a.G - r0;
     tdp_pdl_trigger();
     tdp_pdl_wait();
@@ -309,7 +311,7 @@ tdp_xattn_simt_dq_kernel(const __grid_constant__ tdp_geom g, const __grid_consta
         if (r < nr) {
             const int64_t h = packed(a, seg, kvh, r0 + r, a.Hq, 1);
             lse[i] = row_lse(a.lse[h]);
-            if (tx == 0) a.delta[h] = delta[i];
+            if (tx == 0 && part == 0) a.delta[h] = delta[i];
         }
     }
     __syncthreads();
@@ -319,7 +321,8 @@ tdp_xattn_simt_dq_kernel(const __grid_constant__ tdp_geom g, const __grid_consta
     for (int i = 0; i < 4; ++i)
 #pragma unroll
         for (int c = 0; c < DP / 16; ++c) acc[i][c] = 0.f;
-    for (int32_t t = 0; t * kXN < a.S; ++t) {
+    const int32_t last = min((a.S + kXN - 1) / kXN, (part + 1) * a.qpart);
+    for (int32_t t = part * a.qpart; t < last; ++t) {
         __syncthreads();
         if (!kept_bits(mask, t * kXN, a.S, bits)) continue;
         const uint32_t b0 = bits[0], b1 = bits[1];
@@ -343,7 +346,7 @@ tdp_xattn_simt_dq_kernel(const __grid_constant__ tdp_geom g, const __grid_consta
     for (int i = 0; i < 4; ++i) {
         const int32_t r = 4 * ty + i;
         if (r >= nr) continue;
-        float *o = const_cast<float *>(row(a.dq, r));
+        float *o = const_cast<float *>(a.qsplit > 1 ? row(a.pq + part * a.rows * a.Hq * a.D, r) : row(a.dq, r));
 #pragma unroll
         for (int c = 0; c < DP / 16; ++c) {
             const int32_t d = 64 * (c / 4) + 4 * tx + c % 4;
@@ -455,6 +458,26 @@ tdp_xattn_simt_dkv_kernel(const __grid_constant__ tdp_geom g, const __grid_const
     }
 }
 
+// fp32 dq from its parts, four elements a thread, parts in order.
+__global__ void __launch_bounds__(kXT)
+tdp_xattn_dq_join_kernel(const xattn_args a, int64_t n)
+{
+    tdp_pdl_trigger();
+    tdp_pdl_wait();
+    const int64_t i = ((int64_t)blockIdx.x * kXT + threadIdx.x) * 4;
+    if (i >= n) return;
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int32_t k = 0; k < a.qsplit; ++k) {
+        const float4 x = *reinterpret_cast<const float4 *>(a.pq + k * n + i);
+        s.x += x.x;
+        s.y += x.y;
+        s.z += x.z;
+        s.w += x.w;
+    }
+    *reinterpret_cast<float4 *>(static_cast<float *>(a.dq) + i) = s;
+}
+
 // dk and dv from their parts, four elements a thread, parts in order.
 template <int BF16>
 __global__ void __launch_bounds__(kXT)
@@ -483,7 +506,8 @@ tdp_xattn_dkv_join_kernel(const xattn_args a, int64_t n)
 
 constexpr int kSplitMax = 64;  // two parts a lane in the join
 // fp32: blocks below which the work is split, two for each SM.  Eight items of one token, 5000 states: 76 us against 680
-// unsplit; dk and dv of 512 states from 35840 rows: 2683 us against 12016.
+// unsplit; dk and dv of 512 states from 35840 rows: 2683 us against 12016; gradients of 64 rows, 4 heads of 128,
+// 3000 states, 174 us against 747 with dq unsplit.
 constexpr int kFill = 304;
 constexpr int kSMs = 152;       // what splits are chosen for
 
@@ -494,7 +518,7 @@ struct xattn_shape {
     int64_t mask_rows, kept_bytes;          // bf16: lists of kept state tiles
     int64_t fwd_bytes, grad_bytes;
     int64_t pl_at, po_at;                   // forward
-    int64_t delta_at, pk_at, pv_at;         // gradient
+    int64_t delta_at, pk_at, pv_at, pq_at;  // gradient
     int32_t fblocks, fsplit, fpart;
     int32_t bblocks, bsplit, bpart;
 };
@@ -634,7 +658,11 @@ tdp_status xattn_check(tdp_plan_t plan, const tdp_xattn *p, xattn_args *a, xattn
     sh->delta_at = sh->kept_bytes;
     sh->pk_at = sh->delta_at + align256(rh * 4);
     sh->pv_at = sh->pk_at + (sh->bsplit > 1 ? align256(sh->bsplit * kv * 4) : 0);
-    sh->grad_bytes = sh->pv_at + (sh->bsplit > 1 ? sh->bsplit * kv * 4 : 0);
+    sh->pq_at = sh->pv_at + (sh->bsplit > 1 ? align256(sh->bsplit * kv * 4) : 0);
+    // fp32: dq splits the states as the forward does
+    a->qsplit = bf16 ? 1 : sh->fsplit;
+    a->qpart = sh->fpart;
+    sh->grad_bytes = sh->pq_at + (a->qsplit > 1 ? a->qsplit * rh * a->D * 4 : 0);
     return TDP_OK;
 }
 
@@ -778,7 +806,7 @@ struct simt_kernels {
     {
         cudaError_t e = prepare();
         if (e == cudaSuccess)
-            e = tdp_launch_smem(true, tdp_xattn_simt_dq_kernel<DP>, (unsigned)(a.segs * a.Hkv * a.blocks), kXT, kDq, s, g, a);
+            e = tdp_launch_smem(true, tdp_xattn_simt_dq_kernel<DP>, (unsigned)(a.segs * a.qsplit * a.Hkv * a.blocks), kXT, kDq, s, g, a);
         return e;
     }
     static cudaError_t dkv(const tdp_geom &g, const xattn_args &a, cudaStream_t s)
@@ -879,6 +907,7 @@ extern "C" tdp_status tdp_cross_attn_grad(tdp_plan_t plan, const tdp_xattn *p, c
     a.delta = reinterpret_cast<float *>(w + sh.delta_at);
     a.pk = reinterpret_cast<float *>(w + sh.pk_at);
     a.pv = reinterpret_cast<float *>(w + sh.pv_at);
+    a.pq = reinterpret_cast<float *>(w + sh.pq_at);
     a.split = sh.bsplit;
     a.part = sh.bpart;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
@@ -898,6 +927,10 @@ extern "C" tdp_status tdp_cross_attn_grad(tdp_plan_t plan, const tdp_xattn *p, c
             const unsigned grid = (unsigned)((2 * n / 4 + kXT - 1) / kXT);
             err = g.dtype == TDP_BF16 ? tdp_launch(true, tdp_xattn_dkv_join_kernel<1>, grid, kXT, s, a, n)
                                       : tdp_launch(true, tdp_xattn_dkv_join_kernel<0>, grid, kXT, s, a, n);
+        }
+        if (err == cudaSuccess && a.qsplit > 1) {
+            const int64_t n = a.rows * a.Hq * a.D;
+            err = tdp_launch(true, tdp_xattn_dq_join_kernel, (unsigned)((n / 4 + kXT - 1) / kXT), kXT, s, a, n);
         }
     }
     return err == cudaSuccess ? tdp_ok() : tdp_fail(TDP_ERR_CUDA, cudaGetErrorString(err));

@@ -23,6 +23,7 @@ struct xattn_args {
     uint4 *state_words;         //       masks of every tile's states [mask rows, tiles] (gradient)
     float *po, *pl;             // forward split over states: partial out [split][R, Hq, D] and lse [split][R, Hq]
     float *pk, *pv;             // gradient split over rows: partial dk, dv [split][B, S, Hkv, D]
+    float *pq;                  // fp32 gradient split over states: partial dq [qsplit][R, Hq, D]
     int64_t q_row, q_head, k_item, k_state, k_head, v_item, v_state, v_head;
     int64_t rows;               // R
     int32_t Hq, Hkv, G, D, S;
@@ -35,6 +36,7 @@ struct xattn_args {
     int32_t blocks;             // row blocks of the largest segment
     int32_t split;              // parts the states (forward) or the row blocks (dk, dv) are split into
     int32_t part;               // fp32: 64-state tiles (forward) or row blocks (dk, dv) of a part
+    int32_t qsplit, qpart;      // fp32: parts the states are split into for dq, 64-state tiles of a part
     float scale;
 };
 

@@ -287,3 +287,11 @@ def test_few_states_lose_no_digits(tdp, S, D):
         val = want[name][0]
         err = np.linalg.norm(x.double().cpu().numpy() - val) / np.linalg.norm(val)
         assert err < math.sqrt(2) * 2.0**-8 / math.sqrt(3), (name, err)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("kind", ["none", "holes", "length"])
+def test_gradients_of_few_rows_long_states(tdp, dtype, kind):
+    """dq's sums over the states, split over blocks (fp32) and joined."""
+    run(tdp, one(64), dtype, 4, 4, 128, 2900, kind, True)
+    run(tdp, one(3, B=2), dtype, 6, 2, 64, 1300, kind, True, seed=4)
