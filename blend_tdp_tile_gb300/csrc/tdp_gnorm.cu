@@ -120,8 +120,9 @@ struct gn_cols {
             ga[j] = 1.f;
             b[j] = 0.f;
         }
-        if (g.gamma) E::unpack(__ldg(static_cast<const typename E::type *>(g.gamma) + col), ga);
-        if (g.beta) E::unpack(__ldg(static_cast<const typename E::type *>(g.beta) + col), b);
+        // plain loads: the kernel before, which may have written them, can overlap this one
+        if (g.gamma) E::unpack(static_cast<const typename E::type *>(g.gamma)[col], ga);
+        if (g.beta) E::unpack(static_cast<const typename E::type *>(g.beta)[col], b);
     }
     __device__ __forceinline__ void moments(const gn_args &g, int64_t s, int32_t col)
     {

@@ -61,7 +61,7 @@ __device__ __forceinline__ item dq_item_at(const tdp_geom &g, const xattn_args &
     it.keys.n = tiles;
     if (a.mask) {
         const int64_t m = a.per_tile ? (int64_t)it.seg.t * g.B + it.seg.b : it.seg.b;
-        it.keys.n = __ldg(a.kept_n + m);
+        it.keys.n = __ldcg(a.kept_n + m);
         it.keys.tile = a.kept_tile + m * tiles;
         it.keys.words = a.kept_words + m * tiles;
     }
@@ -147,7 +147,7 @@ tdp_xattn_dq_kernel(const __grid_constant__ tdp_geom g, const __grid_constant__ 
             if (it.left <= 0 || it.keys.n == 0) return;
             const bool mine = rt < a.TT && rt < it.left;
             const int32_t h = ((int32_t)(it.seg.row0 + it.tok0) + rt) * a.Hq + it.head + rh;
-            l = -row_lse2(mine ? __ldg(a.lse + h) : -INFINITY);
+            l = -row_lse2(mine ? __ldcg(a.lse + h) : -INFINITY);
             ok = ok && mbar_wait(full + 8 * kv.st, kv.ph, dead) && mbar_wait(rfull + 8, n_items & 1, dead);
             ++n_items;
             float sum = 0.f;
@@ -481,7 +481,7 @@ struct row_walk {
             u = (sg + 1) * a.blocks;
             if (a.mask) {
                 const int64_t m = a.per_tile ? (int64_t)seg.t * g.B + seg.b : seg.b;
-                words = __ldg(a.state_words + m * ((a.S + kKeys - 1) / kKeys) + tile);
+                words = __ldcg(a.state_words + m * ((a.S + kKeys - 1) / kKeys) + tile);
             } else {
                 key_list k;
                 k.tile = nullptr;
@@ -799,7 +799,7 @@ tdp_xattn_dkv_kernel(const __grid_constant__ tdp_geom g, const __grid_constant__
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const int32_t h = h0 + (st_tok[i] < left ? st_at[i] : 0);
-                        l[i] = __ldg(a.lse + h);
+                        l[i] = __ldcg(a.lse + h);
                         d[i] = __ldcg(a.delta + h);
                     }
 #pragma unroll
