@@ -94,9 +94,11 @@ tdp_xattn_dq_kernel(const __grid_constant__ tdp_geom g, const __grid_constant__ 
     if (warp == 9) tmem_alloc(smem_u32(&tmem_slot), 512);
     if (threadIdx.x == 0) {
         dead_flag = 0;
+        // a tile is given back by its last reader and, where there is a mask, by the cleaning warp, which waits for every
+        // tile: a stage filled again before it has looked would put its wait a phase behind
         for (int i = 0; i < NST; ++i) {
             mbar_init(full + 8 * i, 1);
-            mbar_init(empty + 8 * i, 1);
+            mbar_init(empty + 8 * i, a.mask ? 2 : 1);
         }
         for (int i = 0; i < 4; ++i) mbar_init(clean + 8 * i, 1);
         for (int i = 0; i < 2; ++i) {
@@ -423,20 +425,21 @@ tdp_xattn_dq_kernel(const __grid_constant__ tdp_geom g, const __grid_constant__ 
                     k_prev = k1;
                 }
             } else if (a.mask) {
-                // every tile is waited for, in order: a wait for a phase two ahead of the barrier's would return at once
-                ok = mbar_wait(full + 8 * kv.st, kv.ph, dead);          // O
-                kv.next();
+                // O, then K and V of each state tile: every one is waited for, in order, and given back
 #pragma unroll 1
-                for (int32_t j = 0; j < n; ++j) {
-                    const uint4 m = it.keys.mask(j);
-                    if (!(ok = ok && mbar_wait(full + 8 * kv.st, kv.ph, dead))) break;
-                    zero_dropped<DP>(kv_s + kv.st * SM::kTile, m, lane);
-                    fence_async();
+                for (int32_t i = -1; i < 2 * n; ++i) {
+                    if (!(ok = mbar_wait(full + 8 * kv.st, kv.ph, dead))) break;
+                    const bool k = i >= 0 && !(i & 1);
+                    if (k) {
+                        zero_dropped<DP>(kv_s + kv.st * SM::kTile, it.keys.mask(i >> 1), lane);
+                        fence_async();
+                    }
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(clean + 8 * (kc & 3));
-                    ++kc;
-                    kv.next();
-                    if (!(ok = mbar_wait(full + 8 * kv.st, kv.ph, dead))) break;       // V
+                    if (lane == 0) {
+                        if (k) mbar_arrive(clean + 8 * (kc & 3));
+                        mbar_arrive(empty + 8 * kv.st);
+                    }
+                    kc += k;
                     kv.next();
                 }
             }

@@ -81,3 +81,36 @@ def test_masks_in_turn_from_two_threads(tdp):
     [t.join() for t in threads]
     for at in range(2):
         assert len(got[at]) == 40 and all(_same(g, want[(i + at) % 3]) for i, g in enumerate(got[at]))
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("T,S", [(1, 1000), (130, 130), (3000, 257), (700, 5000)])
+def test_gradients_of_many_masked_tiles(tdp, D, T, S):
+    """Rows of K to be zeroed in every tile, items of one state tile to forty: every tile of the ring is met by all its
+    readers.  Each value of dq, dk and dv is a sum whose terms are rounded to bf16 twice and which is rounded once more: three
+    independent errors of 2^-8 / sqrt(3) in the mean square at most, against 64 bits; delta, from an output that is
+    rounded, adds a fourth."""
+    import torch
+    g = torch.Generator(device="cuda").manual_seed(T + S)
+    t = lambda *s: torch.randn(s, generator=g, device="cuda").bfloat16()  # noqa: E731
+    B, H, K = 3, 4, 2
+    plan = tdp.tdp_plan_create(B, 1, 1, T, 8, "bf16", (1, 1, 1), (0, 0, 0))
+    q, k, v, dout = t(B * T, H, D), t(B, S, K, D), t(B, S, K, D), t(B * T, H, D)
+    mask = torch.rand(B, S, generator=g, device="cuda") < 0.6
+    k[~mask], v[~mask] = float("nan"), float("inf")
+    first = _call(tdp, plan, q, k, v, dout, mask)
+    for _ in range(5):
+        assert _same(_call(tdp, plan, q, k, v, dout, mask), first)
+    for b in range(B):
+        on, rows = mask[b], slice(b * T, (b + 1) * T)
+        x, go = (a[rows].double().reshape(T, K, H // K, D) for a in (q, dout))
+        kk, vv = k[b, on].double(), v[b, on].double()
+        p = (torch.einsum("tkgd,skd->kgts", x, kk) * D ** -0.5).softmax(-1)
+        dp = torch.einsum("tkgd,skd->kgts", go, vv)
+        ds = p * (dp - (p * dp).sum(-1, keepdim=True)) * D ** -0.5
+        want = (torch.einsum("kgts,skd->tkgd", ds, kk).reshape(T, H, D), torch.einsum("kgts,tkgd->skd", ds, x),
+                torch.einsum("kgts,tkgd->skd", p, go))
+        for name, got, w in zip(("dq", "dk", "dv"), (first[2][rows], first[3][b, on], first[4][b, on]), want):
+            err = float((got.double() - w).norm() / w.norm())
+            assert err < 2 * 2.0 ** -8 / 3 ** 0.5, (name, b, err)
+    assert (first[3][~mask] == 0).all() and (first[4][~mask] == 0).all()
