@@ -138,6 +138,9 @@ tdp_xattn_dq_kernel(const __grid_constant__ tdp_geom g, const __grid_constant__ 
             asm volatile("bar.sync 1, 256;" ::: "memory");
             return half ? other + x : x + other;
         };
+        // After a lost wait, another thread's too, delta and dQ are NaN: a row's sums have parts of several threads, and the
+        // kernel that follows must not take a delta of what was not there.
+        auto sound = [&] { return ok && !*dead; };
         // An item's lse and delta = dO . O, made while the products of the item before run out: each thread half of a
         // row's products, the halves joined through shared memory.
         item it;
@@ -172,7 +175,7 @@ tdp_xattn_dq_kernel(const __grid_constant__ tdp_geom g, const __grid_constant__ 
                 mbar_arrive(empty + 8 * kv.st);
                 mbar_arrive(rempty + 8);
             }
-            if (mine && half == 0) a.delta[h] = d;
+            if (mine && half == 0) a.delta[h] = sound() ? d : NAN;
             d = -d;
             const uint32_t to = kv.st + 1 + 2 * it.keys.n, rounds = to / NST;
             kv.st = to - rounds * NST;
@@ -230,7 +233,7 @@ tdp_xattn_dq_kernel(const __grid_constant__ tdp_geom g, const __grid_constant__ 
                             if ((w1 >> u) & 1) sum = fmaf(__uint_as_float(s[32 + u]), __uint_as_float(e[32 + u]), sum);
                         }
                         sum = both(sum);
-                        if (mine && half == 0) a.delta[h] = sum;
+                        if (mine && half == 0) a.delta[h] = sound() ? sum : NAN;
                         d2 = pair(-sum, -sum);
                     }
 #pragma unroll
@@ -271,7 +274,7 @@ tdp_xattn_dq_kernel(const __grid_constant__ tdp_geom g, const __grid_constant__ 
             }
             // dQ, half of the columns each; a lost wait leaves NaN
             T *dst = static_cast<T *>(a.dq) + (int64_t)h * a.D;
-            const float f = ok ? a.scale : NAN;
+            const float f = sound() ? a.scale : NAN;
 #pragma unroll 1
             for (int i = half * (DP / 64); i < (half + 1) * (DP / 64); ++i) {
                 uint32_t o[32];
@@ -648,7 +651,8 @@ tdp_xattn_dkv_kernel(const __grid_constant__ tdp_geom g, const __grid_constant__
         // first warpgroup dV, second dK
         const int32_t state = tile * kKeys + r;
         const int64_t at = (((int64_t)b * a.S + state) * a.Hkv + kvh) * a.D;
-        const float f = !ok ? NAN : half ? a.scale : 1.f;
+        // a wait that any thread of the block has lost leaves NaN: the columns of a tile are shared
+        const float f = !ok || *dead ? NAN : half ? a.scale : 1.f;
         float *pf = (half ? a.pk : a.pv) + (int64_t)part * g.B * a.S * a.Hkv * a.D + at;
         T *pb = static_cast<T *>(half ? a.dk : a.dv) + at;
 #pragma unroll 1

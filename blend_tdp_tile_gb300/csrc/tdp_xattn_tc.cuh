@@ -329,13 +329,14 @@ tdp_xattn_tc_kernel(const __grid_constant__ tdp_geom g, const __grid_constant__ 
                 __syncwarp();
                 if (lane == 0) mbar_arrive(whole_p);
             }
-            // output: O / l, or zero where nothing is kept, or NaN after a lost wait
+            // output: O / l, or zero where nothing is kept, or NaN after a wait that any thread has lost
             if (n > 0 && ok) {
                 ok = products(ph - 1);
                 fence_after();
             }
             const int32_t h = (row0 + rt) * a.Hq + head + rh;
             const int64_t all = (int64_t)part * a.rows * a.Hq + h;
+            ok = __all_sync(~0u, ok && !*dead);
             const float inv = !ok ? NAN : l == 0.f ? 0.f : 1.f / l;
             const float lse = !ok ? NAN : l == 0.f ? -INFINITY : m * kLn2 + logf(l);
             if (mine && a.split > 1) a.pl[all] = lse;

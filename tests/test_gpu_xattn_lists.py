@@ -114,3 +114,21 @@ def test_gradients_of_many_masked_tiles(tdp, D, T, S):
             err = float((got.double() - w).norm() / w.norm())
             assert err < 2 * 2.0 ** -8 / 3 ** 0.5, (name, b, err)
     assert (first[3][~mask] == 0).all() and (first[4][~mask] == 0).all()
+
+
+@pytest.mark.parametrize("S", [100, 300])
+def test_a_forward_that_gave_up_shows_in_every_gradient(tdp, S):
+    """What a forward that gave up leaves in a row, NaN in out and lse, is found in that row's dq and in the dk and dv of its
+    item's states, and nowhere else."""
+    import torch
+    plan, q, k, v, dout, _ = _problem(tdp, 3, False, S=S)
+    out, lse = torch.empty_like(q), torch.empty(q.shape[:2], device="cuda")
+    tdp.tdp_cross_attn(plan, q, k, v, None, out, lse)
+    out[5, 1], lse[5, 1] = float("nan"), float("nan")          # item 0, key head 0
+    dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
+    tdp.tdp_cross_attn_grad(plan, q, k, v, None, out, lse, dout, dq, dk, dv)
+    lost = torch.zeros(q.shape[:2], dtype=torch.bool, device="cuda")
+    lost[5, 1] = True
+    assert torch.equal(dq.isnan().all(-1), lost) and torch.equal(dq.isnan().any(-1), lost)
+    for d in (dk, dv):
+        assert d[0, :, 0].isnan().all() and not d[1].isnan().any() and not d[0, :, 1].isnan().any()
