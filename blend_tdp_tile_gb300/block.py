@@ -8,11 +8,13 @@ put the library's operators on tile-major rows under torch's autograd:
   dropout_add(plan, x, res, p, rng)          residual + dropout whose mask is never stored
 
 ``TileBlock`` is one cross-attention sublayer of them: normalise, project, attend, project back,
-drop out and add.  All tiles go through each call at once; nothing is padded.
+drop out and add.  All tiles go through each call at once; nothing is padded.  The gradients are first ones: a
+derivative of theirs raises an error.
 """
 from __future__ import annotations
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import (Plan, tdp_cross_attn, tdp_cross_attn_grad, tdp_dropout_add, tdp_dropout_grad, tdp_group_norm,
                tdp_group_norm_grad)
@@ -32,6 +34,7 @@ class _GroupNorm(torch.autograd.Function):
         return y
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy):
         x, gamma, beta, mean, rstd = ctx.saved_tensors
         dx = torch.empty_like(x)
@@ -53,6 +56,7 @@ class _CrossAttn(torch.autograd.Function):
         return out
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dout):
         q, k, v, out, lse = ctx.saved_tensors
         dq = torch.empty_like(out)
@@ -73,6 +77,7 @@ class _DropoutAdd(torch.autograd.Function):
         return out
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dout):
         dout = dout.contiguous()
         dx = torch.empty_like(dout)
