@@ -51,17 +51,17 @@ class _CrossAttn(torch.autograd.Function):
         out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
         lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)
         tdp_cross_attn(plan, q, k, v, mask, out, lse, scale=scale)
-        ctx.plan, ctx.scale, ctx.mask = plan, scale, mask
-        ctx.save_for_backward(q, k, v, out, lse)
+        ctx.plan, ctx.scale = plan, scale
+        ctx.save_for_backward(q, k, v, mask, out, lse)      # the mask too: one refilled in between is an error
         return out
 
     @staticmethod
     @once_differentiable
     def backward(ctx, dout):
-        q, k, v, out, lse = ctx.saved_tensors
+        q, k, v, mask, out, lse = ctx.saved_tensors
         dq = torch.empty_like(out)
         dk, dv = (torch.empty(k.shape, dtype=k.dtype, device=k.device) for _ in range(2))
-        tdp_cross_attn_grad(ctx.plan, q, k, v, ctx.mask, out, lse, dout.contiguous(), dq, dk, dv, scale=ctx.scale)
+        tdp_cross_attn_grad(ctx.plan, q, k, v, mask, out, lse, dout.contiguous(), dq, dk, dv, scale=ctx.scale)
         return None, dq, dk, dv, None, None
 
 
@@ -92,7 +92,8 @@ def group_norm(plan: Plan, x, groups, gamma=None, beta=None, eps=1e-5, act="none
 
 def cross_attn(plan: Plan, q, k, v, mask=None, scale=None):
     """Tile rows q [R, Hq, D] attend to states k, v [B, S, Hkv, D] under mask [B, S] or [n_tiles, B, S];
-    gradients for q, k and v."""
+    gradients for q, k and v.  torch sees when it has changed one of them, or the mask, before the gradient, and
+    raises an error; it does not see what this library's calls (tdp_norm_filter's keep) write into them."""
     return _CrossAttn.apply(plan, q, k, v, mask, scale)
 
 

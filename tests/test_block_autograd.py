@@ -100,3 +100,15 @@ def test_first_derivatives(block, name):
     with torch.no_grad():
         fd = float(((f(x + h * u).double() - f(x - h * u).double()) * w).sum()) / (2 * h)
     assert abs(fd - float((got * u).sum())) < 1e-2 * float((got * u).abs().sum())
+
+
+def test_a_mask_refilled_before_backward_is_refused(block):
+    """lse belongs to the forward's mask; gradients under another one would be of no function."""
+    q, k, v = torch.randn(T, H, D, requires_grad=True), torch.randn(1, S, H, D), torch.randn(1, S, H, D)
+    mask = torch.tensor([[True, True, False, True, False]])
+    block.cross_attn(_Plan, q, k, v, mask).sum().backward()
+    assert q.grad is not None
+    out = block.cross_attn(_Plan, q, k, v, mask)
+    mask.fill_(True)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        out.sum().backward()
