@@ -22,10 +22,16 @@ from . import (Plan, tdp_cross_attn, tdp_cross_attn_grad, tdp_dropout_add, tdp_d
 __all__ = ["group_norm", "cross_attn", "dropout_add", "TileBlock"]
 
 
+def _dense(t):
+    """t as the library takes it: contiguous, on a 16-byte boundary (a cat's gradient starts anywhere)."""
+    t = t.contiguous()
+    return t if t.data_ptr() % 16 == 0 else t.clone()
+
+
 class _GroupNorm(torch.autograd.Function):
     @staticmethod
     def forward(ctx, plan, x, groups, gamma, beta, eps, act):
-        x = x.contiguous()
+        x = _dense(x)
         stats = [torch.empty((plan.n_tiles, plan.B, groups), dtype=torch.float32, device=x.device) for _ in range(2)]
         y = torch.empty_like(x)
         tdp_group_norm(plan, x, groups, gamma, beta, y, *stats, eps=eps, act=act)
@@ -40,7 +46,7 @@ class _GroupNorm(torch.autograd.Function):
         dx = torch.empty_like(x)
         params = gamma is not None or beta is not None
         dgamma, dbeta = (torch.empty(x.shape[-1], dtype=torch.float32, device=x.device) if params else None for _ in range(2))
-        tdp_group_norm_grad(ctx.plan, x, ctx.groups, gamma, beta, mean, rstd, dy.contiguous(), dx, dgamma, dbeta, act=ctx.act)
+        tdp_group_norm_grad(ctx.plan, x, ctx.groups, gamma, beta, mean, rstd, _dense(dy), dx, dgamma, dbeta, act=ctx.act)
         return (None, dx, None, None if gamma is None else dgamma.to(gamma.dtype),
                 None if beta is None else dbeta.to(beta.dtype), None, None)
 
@@ -61,16 +67,16 @@ class _CrossAttn(torch.autograd.Function):
         q, k, v, mask, out, lse = ctx.saved_tensors
         dq = torch.empty_like(out)
         dk, dv = (torch.empty(k.shape, dtype=k.dtype, device=k.device) for _ in range(2))
-        tdp_cross_attn_grad(ctx.plan, q, k, v, mask, out, lse, dout.contiguous(), dq, dk, dv, scale=ctx.scale)
+        tdp_cross_attn_grad(ctx.plan, q, k, v, mask, out, lse, _dense(dout), dq, dk, dv, scale=ctx.scale)
         return None, dq, dk, dv, None, None
 
 
 class _DropoutAdd(torch.autograd.Function):
     @staticmethod
     def forward(ctx, plan, x, res, p, rng):
-        x = x.contiguous()
+        x = _dense(x)
         out = torch.empty_like(x)
-        tdp_dropout_add(plan, x, None if res is None else res.contiguous(), p, rng, out)
+        tdp_dropout_add(plan, x, None if res is None else _dense(res), p, rng, out)
         ctx.plan, ctx.p, ctx.residual = plan, p, res is not None
         # the gradient draws the same words: it needs this call's seed and offset, not later ones
         ctx.save_for_backward(rng.clone())
@@ -79,7 +85,7 @@ class _DropoutAdd(torch.autograd.Function):
     @staticmethod
     @once_differentiable
     def backward(ctx, dout):
-        dout = dout.contiguous()
+        dout = _dense(dout)
         dx = torch.empty_like(dout)
         tdp_dropout_grad(ctx.plan, dout, ctx.p, ctx.saved_tensors[0], dx)
         return None, dx, dout if ctx.residual else None, None, None

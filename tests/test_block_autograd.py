@@ -112,3 +112,25 @@ def test_a_mask_refilled_before_backward_is_refused(block):
     mask.fill_(True)
     with pytest.raises(RuntimeError, match="modified by an inplace operation"):
         out.sum().backward()
+
+
+@pytest.mark.parametrize("offset", [0, 1, 3])
+@pytest.mark.parametrize("name", ["group_norm", "cross_attn", "dropout_add"])
+def test_gradients_that_are_slices_at_odd_offsets(block, name, offset):
+    """A cat's gradient is slices of one buffer: contiguous, and wherever they happen to start."""
+    f, x = _calls(block)[name]
+    w = torch.randn(offset + x.numel())
+    y = torch.cat([torch.zeros(offset, requires_grad=True) * 1, f(x).reshape(-1)])
+    got, = torch.autograd.grad((y * w).sum(), x)
+    want, = torch.autograd.grad((f(x).reshape(-1) * w[offset:].clone()).sum(), x)
+    assert torch.equal(got, want)
+
+
+def test_inputs_that_are_slices_at_odd_offsets(block):
+    """What the functions copy where it is not contiguous they copy where it is not aligned."""
+    rng = torch.zeros(2, dtype=torch.int64)
+    buf = torch.randn(2 * T * C + 2)
+    x, res = buf[1:1 + T * C].view(T, C), buf[1 + T * C:1 + 2 * T * C].view(T, C)
+    assert torch.equal(block.dropout_add(_Plan, x, res, 0.5, rng), block.dropout_add(_Plan, x.clone(), res.clone(), 0.5, rng))
+    gamma, beta = torch.randn(C), torch.randn(C)
+    assert torch.equal(block.group_norm(_Plan, x, 2, gamma, beta), block.group_norm(_Plan, x.clone(), 2, gamma, beta))
