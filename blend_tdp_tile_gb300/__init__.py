@@ -150,6 +150,13 @@ def _check(status: int, where: str):
         raise TdpError(status, where)
 
 
+class _Scratch(threading.local):
+    """A plan's small workspaces by device and stream, each thread's own."""
+
+    def __init__(self):
+        self.by_stream = {}
+
+
 class Plan:
     """Owning wrapper of a ``tdp_plan_t``; geometry read back through tdp_plan_info."""
 
@@ -157,7 +164,7 @@ class Plan:
         self._h = ctypes.c_void_p(handle)
         self.problem = problem
         self.sizes = {}             # workspace bytes by shape
-        self.scratch = {}           # small workspaces by device, stream and thread
+        self.scratch = _Scratch()
         n = ctypes.c_int32()
         tot = ctypes.c_int64()
         _check(_lib.tdp_plan_info(self._h, ctypes.byref(n), ctypes.byref(tot), None, None), "tdp_plan_info")
@@ -578,18 +585,24 @@ def _workspace(ws, need, like, stream, plan):
     """A workspace of `need` bytes: the caller's, or one of torch's for the stream of the call.
 
     A small one stays with the plan, one per stream and thread, where calls follow one another: an allocation between
-    launches costs some 6 us, a third of a small call.  A call that is being captured gets its own, from the graph's pool."""
+    launches costs some 6 us, a third of a small call.  It goes with its thread, and torch's streams are few and are never
+    destroyed; any other stream gets none, as its handle may come back for a new one.  A call that is being captured gets its
+    own, from the graph's pool."""
     if ws is not None or need == 0:
         return ws
     torch = _torch()
     if stream is None:
-        raw, dev = getattr(torch._C, "_cuda_getCurrentRawStream", None), like.get_device()
-        if need > _SCRATCH or raw is None or dev < 0 or dev != torch.cuda.current_device() or torch.cuda.is_current_stream_capturing():
+        current, raw = getattr(torch._C, "_cuda_getCurrentStream", None), getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        dev = like.get_device()
+        if need > _SCRATCH or current is None or raw is None or dev < 0 or dev != torch.cuda.current_device() or \
+                torch.cuda.is_current_stream_capturing():
             return torch.empty(need, dtype=torch.uint8, device=like.device)
-        key = dev, raw(dev), threading.get_ident()
-        kept = plan.scratch.get(key)
+        sid = current(dev)[0]
+        if sid and sid == raw(dev):         # not torch's: its id is its handle
+            return torch.empty(need, dtype=torch.uint8, device=like.device)
+        kept = plan.scratch.by_stream.get((dev, sid))
         if kept is None or kept.numel() < need:
-            kept = plan.scratch[key] = torch.empty(need, dtype=torch.uint8, device=like.device)
+            kept = plan.scratch.by_stream[dev, sid] = torch.empty(need, dtype=torch.uint8, device=like.device)
         return kept
     if isinstance(stream, int):
         stream = torch.cuda.ExternalStream(stream, device=like.device)
