@@ -198,15 +198,18 @@ struct gn_team {
 };
 
 // Moments of a group from parts (mean m_i, squared deviations q_i, n_i values each) by `width` lanes; value i by at(i).
+// The mean is summed from the first part's on: weighted means themselves would leave roundings of the mean's own size, a
+// spread where a group holds one value over and over.
 template <typename At>
 __device__ __forceinline__ void join_moments(int32_t parts, int32_t lane, int32_t width, float n, At at, float &mean, float &q)
 {
+    const float first = parts > 0 ? at(0).x : 0.f;
     mean = 0.f;
     for (int32_t i = lane; i < parts; i += width) {
         const float3 p = at(i);
-        mean += p.x * (p.z / n);
+        mean += (p.x - first) * (p.z / n);
     }
-    mean = lanes_sum(mean, width);
+    mean = first + lanes_sum(mean, width);
     q = 0.f;
     for (int32_t i = lane; i < parts; i += width) {
         const float3 p = at(i);
