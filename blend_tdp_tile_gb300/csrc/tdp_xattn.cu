@@ -610,7 +610,7 @@ tdp_status xattn_check(tdp_plan_t plan, const tdp_xattn *p, xattn_args *a, xattn
     if (grid * kSplitMax > 0x7fffffffLL || kvgrid * kSplitMax > 0x7fffffffLL || (int64_t)a->segs * a->blocks > 0x7fffffffLL)
         return tdp_fail(TDP_ERR_TOO_LARGE, "cross attention grid too large");
     sh->mask_rows = a->per_tile ? (int64_t)g.nt * g.B : g.B;
-    sh->kept_bytes = bf16 ? 2 * align256(sh->mask_rows * tiles128 * 16) + align256(sh->mask_rows * tiles128 * 4) + align256(sh->mask_rows * 4) : 0;
+    sh->kept_bytes = bf16 ? 2 * align256(sh->mask_rows * tiles128 * 16) + align256(sh->mask_rows * tiles128 * 4) + 2 * align256(sh->mask_rows * 4) : 0;
     sh->fsplit = 1;
     sh->fpart = (int32_t)std::max<int64_t>(tiles, 1);
     if (bf16) {
@@ -697,10 +697,11 @@ cudaError_t tc_kept(const xattn_shape &sh, xattn_args *a, unsigned char *ws, cud
     a->kept_words = reinterpret_cast<uint4 *>(ws);
     a->kept_tile = reinterpret_cast<int32_t *>(ws + align256(sh.mask_rows * tiles * 16));
     a->kept_n = reinterpret_cast<int32_t *>(ws + align256(sh.mask_rows * tiles * 16) + align256(sh.mask_rows * tiles * 4));
+    a->kept_states = a->kept_n + align256(sh.mask_rows * 4) / 4;
     a->state_words = reinterpret_cast<uint4 *>(ws + sh.kept_bytes - align256(sh.mask_rows * tiles * 16));
     if (!a->mask) return cudaSuccess;
     const unsigned threads = (unsigned)std::min<int64_t>(1024, 32 * std::max<int64_t>(tiles, 1));
-    return tdp_launch(true, tdp_xt::tdp_xattn_kept_kernel, (unsigned)sh.mask_rows, threads, s, a->mask, a->S, a->kept_n, a->kept_tile, a->kept_words, a->state_words);
+    return tdp_launch(true, tdp_xt::tdp_xattn_kept_kernel, (unsigned)sh.mask_rows, threads, s, a->mask, a->S, a->kept_n, a->kept_states, a->kept_tile, a->kept_words, a->state_words);
 }
 
 // Tensor map of bf16 rows: `dims` extents from the contiguous one on, strides and box of them.  A dimension of

@@ -18,6 +18,7 @@ struct xattn_args {
     float *lse;                 // written by the forward (may be NULL), read by the gradient
     float *delta;               // [R, Hq] gradient: dout . out
     int32_t *kept_n;            // bf16: [mask rows] kept 128-state tiles, their indexes and the masks of their states
+    int32_t *kept_states;       //       [mask rows] states in them
     int32_t *kept_tile;         //       [mask rows, tiles]
     uint4 *kept_words;          //       [mask rows, tiles]
     uint4 *state_words;         //       masks of every tile's states [mask rows, tiles] (gradient)

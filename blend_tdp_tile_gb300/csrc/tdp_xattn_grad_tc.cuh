@@ -42,6 +42,13 @@ struct dkv_smem {
     static constexpr int kBytes = 1024 + (2 + kStages) * kTile + kStats * 1024 + 512;
 };
 
+// Rows whose mask keeps up to this many states in several state tiles: the first kernel walks the tiles twice.  Few states
+// make delta as large as dP, and dO . O, with its O rounded to bf16, costs dS digits that delta = sum p dP over the row does
+// not: a relative error of dQ of 0.0046 against 0.0023 at two states, 0.0029 at eight, 0.00245 against 0.00237 at 64 (scores of a
+// spread of one; a softmax that a few of many states fill pays as much, whatever their number).  With one state tile
+// the row's dP is all there and the first walk is not needed.
+constexpr int32_t kFewStates = 64;
+
 // Item of the first kernel: a segment's tile of TT tokens, a head block, all kept state tiles.
 __device__ __forceinline__ item dq_item_at(const tdp_geom &g, const xattn_args &a, int32_t w)
 {
@@ -58,10 +65,11 @@ __device__ __forceinline__ item dq_item_at(const tdp_geom &g, const xattn_args &
     it.keys.tile = nullptr;
     it.keys.words = nullptr;
     it.keys.j0 = 0;
-    it.keys.n = tiles;
+    it.keys.n = it.rounds = tiles;
     if (a.mask) {
         const int64_t m = a.per_tile ? (int64_t)it.seg.t * g.B + it.seg.b : it.seg.b;
         it.keys.n = __ldcg(a.kept_n + m);
+        it.rounds = it.keys.n > 1 && __ldcg(a.kept_states + m) <= kFewStates ? 2 * it.keys.n : it.keys.n;
         it.keys.tile = a.kept_tile + m * tiles;
         it.keys.words = a.kept_words + m * tiles;
     }
@@ -177,7 +185,7 @@ tdp_xattn_dq_kernel(const __grid_constant__ tdp_geom g, const __grid_constant__ 
             }
             if (mine && half == 0) a.delta[h] = sound() ? d : NAN;
             d = -d;
-            const uint32_t to = kv.st + 1 + 2 * it.keys.n, rounds = to / NST;
+            const uint32_t to = kv.st + 1 + 2 * it.rounds, rounds = to / NST;
             kv.st = to - rounds * NST;
             kv.ph ^= rounds & 1;
         };
@@ -191,13 +199,17 @@ tdp_xattn_dq_kernel(const __grid_constant__ tdp_geom g, const __grid_constant__ 
             const bool mine = rt < a.TT && rt < it.left;
             const int32_t h = ((int32_t)(it.seg.row0 + it.tok0) + rt) * a.Hq + it.head + rh;
             if (n > 0) {
+                // delta from the probabilities: of the only tile, or of all tiles in a first walk, whose dS is zero
+                const int32_t rounds = it.rounds, first = rounds - n;
+                const bool tally = n == 1 || first > 0;
+                float sum = 0.f;
                 const uint32_t done_ph = (n_items & 1) ^ 1;
                 const uint64_t c2 = pair(c, c), l2 = pair(l, l);
                 uint64_t d2 = pair(d, d);
 #pragma unroll 1
-                for (int32_t j = 0; j < n && (ok || n == 1); ++j) {     // n = 1: all threads meet in both()
+                for (int32_t j = 0; j < rounds && (ok || tally); ++j) {     // tally: all threads meet in both()
                     const uint32_t buf = n_done & 1, S = lanes + 128 * buf + 64 * half, P = lanes + 256 + 64 * half;
-                    const uint4 mk = it.keys.mask(j);
+                    const uint4 mk = it.keys.mask(j < first ? j : j - first);
                     ok = ok && mbar_wait(sfull + 8 * buf, (n_done >> 1) & 1, dead) && mbar_wait(pfull, n_done & 1, dead);
                     ++n_done;
                     fence_after();
@@ -222,19 +234,19 @@ tdp_xattn_dq_kernel(const __grid_constant__ tdp_geom g, const __grid_constant__ 
                         s[2 * u] = __float_as_uint(exp2_fast(x));
                         s[2 * u + 1] = __float_as_uint(exp2_fast(y));
                     }
-                    const uint32_t w0 = half ? mk.z : mk.x, w1 = half ? mk.w : mk.y;
-                    if (n == 1) {
-                        // Few states: delta is as large as dP, and dO . O, its O rounded to bf16, would double the error of dS (0.0038
-                        // against 0.0024 relative at four states).  The whole row is here: delta = sum p dP.
-                        float sum = 0.f;
+                    uint32_t w0 = half ? mk.z : mk.x, w1 = half ? mk.w : mk.y;
+                    if (n == 1 || j < first) {
 #pragma unroll
                         for (int u = 0; u < 32; ++u) {
                             if ((w0 >> u) & 1) sum = fmaf(__uint_as_float(s[u]), __uint_as_float(e[u]), sum);
                             if ((w1 >> u) & 1) sum = fmaf(__uint_as_float(s[32 + u]), __uint_as_float(e[32 + u]), sum);
                         }
-                        sum = both(sum);
-                        if (mine && half == 0) a.delta[h] = sound() ? sum : NAN;
-                        d2 = pair(-sum, -sum);
+                        if (j + 1 >= first) {
+                            sum = both(sum);
+                            if (mine && half == 0) a.delta[h] = sound() ? sum : NAN;
+                            d2 = pair(-sum, -sum);
+                        }
+                        if (j < first) w0 = w1 = 0;
                     }
 #pragma unroll
                     for (int u = 0; u < 32; ++u) {
@@ -244,7 +256,7 @@ tdp_xattn_dq_kernel(const __grid_constant__ tdp_geom g, const __grid_constant__ 
                         s[2 * u] = __float_as_uint(x);
                         s[2 * u + 1] = __float_as_uint(y);
                     }
-                    if (!whole(mk)) {
+                    if ((w0 & w1) != ~0u) {
 #pragma unroll
                         for (int u = 0; u < 32; ++u) {
                             if (!((w0 >> u) & 1)) s[u] = 0;
@@ -309,7 +321,7 @@ tdp_xattn_dq_kernel(const __grid_constant__ tdp_geom g, const __grid_constant__ 
         uint32_t kc = 0;                        // K tiles so far
         for (int32_t w = blockIdx.x; w < items; w += gridDim.x) {
             const item it = dq_item_at(g, a, w);
-            const int32_t n = it.keys.n;
+            const int32_t tiles = it.keys.n, n = it.rounds;     // state tiles; those of all walks
             if (it.left <= 0 || n == 0 || !ok) continue;
             const int32_t row = (int32_t)(it.seg.row0 + it.tok0);
             const uint32_t ph = n_items & 1;
@@ -320,7 +332,7 @@ tdp_xattn_dq_kernel(const __grid_constant__ tdp_geom g, const __grid_constant__ 
                 for (int32_t i = -1; i < 2 * n; ++i) {
                     const bool v = i & 1;
                     const int32_t head = (v ? a.v_head : a.k_head) > 0 ? it.kvh : 0, b = (v ? a.v_item : a.k_item) > 0 ? it.seg.b : 0;
-                    const int32_t state = i < 0 ? 0 : it.keys.at(i >> 1) * kKeys;
+                    const int32_t state = i < 0 ? 0 : it.keys.at((i >> 1) < tiles ? i >> 1 : (i >> 1) - tiles) * kKeys;
                     if (!(ok = mbar_wait(empty + 8 * kv.st, kv.ph ^ 1, dead))) break;
                     if (elect_one()) {
                         const uint32_t dst = kv_s + kv.st * SM::kTile, bar = full + 8 * kv.st;
@@ -434,7 +446,7 @@ tdp_xattn_dq_kernel(const __grid_constant__ tdp_geom g, const __grid_constant__ 
                     if (!(ok = mbar_wait(full + 8 * kv.st, kv.ph, dead))) break;
                     const bool k = i >= 0 && !(i & 1);
                     if (k) {
-                        zero_dropped<DP>(kv_s + kv.st * SM::kTile, it.keys.mask(i >> 1), lane);
+                        zero_dropped<DP>(kv_s + kv.st * SM::kTile, it.keys.mask((i >> 1) < tiles ? i >> 1 : (i >> 1) - tiles), lane);
                         fence_async();
                     }
                     __syncwarp();

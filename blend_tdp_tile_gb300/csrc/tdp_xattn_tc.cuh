@@ -122,6 +122,7 @@ struct item {
     int32_t left;                   // tokens of the segment from there on; <= 0: nothing to do
     int32_t head;                   // first query head
     int32_t kvh, part;
+    int32_t rounds;                 // dq: walks over the kept state tiles, one or two, times their number
     key_list keys;
 };
 
@@ -556,19 +557,21 @@ tdp_xattn_tc_kernel(const __grid_constant__ tdp_geom g, const __grid_constant__ 
     if (warp == 9) tmem_free(tm, 512);
 }
 
-// One block per mask row: the 128-state tiles that keep a state, in order, and their masks.
+// One block per mask row: the 128-state tiles that keep a state, in order, their masks, and the kept states' number.
 __global__ void __launch_bounds__(1024)
-tdp_xattn_kept_kernel(const uint8_t *mask, int32_t S, int32_t *kept_n, int32_t *kept_tile, uint4 *kept_words,
+tdp_xattn_kept_kernel(const uint8_t *mask, int32_t S, int32_t *kept_n, int32_t *kept_states, int32_t *kept_tile, uint4 *kept_words,
                       uint4 *state_words)
 {
     __shared__ uint32_t found[2][32];
+    __shared__ int32_t states;
     const int32_t tiles = (S + kKeys - 1) / kKeys, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int64_t row = blockIdx.x;
     tdp_pdl_trigger();
     tdp_pdl_wait();
     const uint8_t *m = mask + row * S;
     const int32_t warps = blockDim.x >> 5;
-    int32_t n = 0;
+    int32_t n = 0, mine = 0;
+    if (threadIdx.x == 0) states = 0;
     for (int32_t t0 = 0, odd = 0; t0 < tiles; t0 += warps, odd ^= 1) {
         const int32_t t = t0 + warp;
         uint32_t w[4];
@@ -578,6 +581,7 @@ tdp_xattn_kept_kernel(const uint8_t *mask, int32_t S, int32_t *kept_n, int32_t *
             w[i] = __ballot_sync(~0u, t < tiles && s < S && m[s] != 0);
         }
         const bool any = (w[0] | w[1] | w[2] | w[3]) != 0;
+        mine += __popc(w[0]) + __popc(w[1]) + __popc(w[2]) + __popc(w[3]);
         if (lane == 0 && t < tiles && state_words) state_words[row * tiles + t] = make_uint4(w[0], w[1], w[2], w[3]);
         if (lane == 0) found[odd][warp] = any;
         __syncthreads();
@@ -589,7 +593,13 @@ tdp_xattn_kept_kernel(const uint8_t *mask, int32_t S, int32_t *kept_n, int32_t *
         }
         n += __popc(all);
     }
-    if (threadIdx.x == 0) kept_n[row] = n;
+    __syncthreads();
+    if (lane == 0) atomicAdd(&states, mine);        // whole numbers: their order is of no matter
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        kept_n[row] = n;
+        kept_states[row] = states;
+    }
 }
 
 }  // namespace tdp_xt
