@@ -510,6 +510,8 @@ constexpr int kSplitMax = 64;  // two parts a lane in the join
 // 3000 states, 174 us against 747 with dq unsplit.
 constexpr int kFill = 304;
 constexpr int kSMs = 152;       // what splits are chosen for
+// Items of a launch, parts included (what is split has few): blocks that step through them pass the end by less than the rest.
+constexpr int64_t kMostItems = 0x7fffffffLL - 65536;
 
 int64_t align256(int64_t x) { return (x + 255) / 256 * 256; }
 
@@ -607,8 +609,6 @@ tdp_status xattn_check(tdp_plan_t plan, const tdp_xattn *p, xattn_args *a, xattn
     const bool bf16 = g.dtype == TDP_BF16;
     const int64_t tiles = (a->S + kXN - 1) / kXN, tiles128 = (a->S + tdp_xt::kKeys - 1) / tdp_xt::kKeys;
     const int64_t grid = (int64_t)a->segs * a->Hkv * a->blocks, kvgrid = (int64_t)g.B * a->Hkv * tiles;
-    if (grid * kSplitMax > 0x7fffffffLL || kvgrid * kSplitMax > 0x7fffffffLL || (int64_t)a->segs * a->blocks > 0x7fffffffLL)
-        return tdp_fail(TDP_ERR_TOO_LARGE, "cross attention grid too large");
     sh->mask_rows = a->per_tile ? (int64_t)g.nt * g.B : g.B;
     sh->kept_bytes = bf16 ? 2 * align256(sh->mask_rows * tiles128 * 16) + align256(sh->mask_rows * tiles128 * 4) + 2 * align256(sh->mask_rows * 4) : 0;
     sh->fsplit = 1;
@@ -619,7 +619,7 @@ tdp_status xattn_check(tdp_plan_t plan, const tdp_xattn *p, xattn_args *a, xattn
         a->TT = 128 / a->Gp;
         sh->fblocks = (int32_t)((T + 2 * a->TT - 1) / (2 * a->TT));
         const int64_t items = (int64_t)a->segs * (a->Hq / a->Gp) * sh->fblocks;
-        if (items * kSplitMax > 0x7fffffffLL) return tdp_fail(TDP_ERR_TOO_LARGE, "cross attention grid too large");
+        if (items > kMostItems) return tdp_fail(TDP_ERR_TOO_LARGE, "cross attention grid too large");
         sh->fsplit = split_states(items, tiles128);
         a->by_heads = fast_div_by(a->Hq / a->Gp);
         a->by_group = fast_div_by(a->G);
@@ -627,6 +627,7 @@ tdp_status xattn_check(tdp_plan_t plan, const tdp_xattn *p, xattn_args *a, xattn
         a->by_nH = fast_div_by(g.d[1].n);
         a->by_nW = fast_div_by(g.d[2].n);
     } else {
+        if (grid > kMostItems || kvgrid > kMostItems) return tdp_fail(TDP_ERR_TOO_LARGE, "cross attention grid too large");
         // few row blocks: the states in parts of four tiles or more, few enough to fill the device
         sh->fblocks = a->blocks;
         if (grid > 0 && grid < kFill && tiles > 4) {
@@ -642,10 +643,12 @@ tdp_status xattn_check(tdp_plan_t plan, const tdp_xattn *p, xattn_args *a, xattn
     sh->bpart = (int32_t)std::max<int64_t>(units, 1);
     if (bf16) {
         const int64_t base = (int64_t)g.B * a->Hkv * tiles128, hbs = a->G / a->Gp;
-        if (units > 0x7fffffffLL || base * kSplitMax > 0x7fffffffLL) return tdp_fail(TDP_ERR_TOO_LARGE, "cross attention grid too large");
+        if (units > kMostItems || base > kMostItems || (int64_t)a->segs * (a->Hq / a->Gp) * sh->bblocks > kMostItems)
+            return tdp_fail(TDP_ERR_TOO_LARGE, "cross attention grid too large");
         const int64_t s = split_rows(base, units, hbs, (int64_t)g.B * a->S * a->Hkv * a->D);
         sh->bpart = (int32_t)std::max<int64_t>((units + s - 1) / s, 1);
         sh->bsplit = (int32_t)std::max<int64_t>((units + sh->bpart - 1) / sh->bpart, 1);
+        if (base * sh->bsplit > kMostItems) return tdp_fail(TDP_ERR_TOO_LARGE, "cross attention grid too large");
     } else if (kvgrid > 0 && kvgrid < kFill && units > 1) {
         const int64_t want = std::min<int64_t>({kSplitMax, (kFill + kvgrid - 1) / kvgrid, units});
         sh->bpart = (int32_t)((units + want - 1) / want);
