@@ -44,10 +44,11 @@ struct dkv_smem {
 
 // Rows whose mask keeps up to this many states in several state tiles: the first kernel walks the tiles twice.  Few states
 // make delta as large as dP, and dO . O, with its O rounded to bf16, costs dS digits that delta = sum p dP over the row does
-// not: a relative error of dQ of 0.0046 against 0.0023 at two states, 0.0029 at eight, 0.00245 against 0.00237 at 64 (scores of a
-// spread of one; a softmax that a few of many states fill pays as much, whatever their number).  With one state tile
-// the row's dP is all there and the first walk is not needed.
-constexpr int32_t kFewStates = 64;
+// not: a relative error of dQ of 0.0046 against 0.0023 at two states, 0.0032 at four, 0.0026 at 16, 0.00245 at 64 (scores of a
+// spread of one; a softmax that a few of many states fill pays as much, whatever their number).  The first walk costs both
+// gradients up to 1.7 times the time (35840 rows, 16 heads of 128, states in eight tiles: 2654 us against 1583): past 16
+// states it gives less than a tenth of the error.  With one state tile the row's dP is all there and it is not needed.
+constexpr int32_t kFewStates = 16;
 
 // Item of the first kernel: a segment's tile of TT tokens, a head block, all kept state tiles.
 __device__ __forceinline__ item dq_item_at(const tdp_geom &g, const xattn_args &a, int32_t w)
