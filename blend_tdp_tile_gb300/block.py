@@ -112,7 +112,11 @@ def dropout_add(plan: Plan, x, res, p, rng):
 class TileBlock(torch.nn.Module):
     """x + dropout(W_o attn(W_q silu(group_norm(x)), W_kv states)) on tile-major rows x [R, C].
 
-    One plan serves any width: its C is not used by the operators."""
+    One plan serves any width: its C is not used by the operators.
+
+    While training with p > 0 each call draws its mask from rng (two 64-bit integers on the device: seed, offset) and
+    leaves it as it is.  Blocks, or steps, that are given the same two drop the same elements: move the offset on between any two
+    calls, or give each block a seed of its own."""
 
     def __init__(self, channels, heads, kv_heads, head_dim, context, groups, p=0.0, dtype=torch.bfloat16, device="cuda"):
         super().__init__()

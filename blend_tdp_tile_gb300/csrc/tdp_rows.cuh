@@ -7,7 +7,8 @@
 
 // Division of n < 2^31 by a constant: q = n * mul >> shift, mul = ceil(2^shift / d), shift = 31 + ceil(log2 d) (T. Granlund,
 // P. Montgomery, "Division by invariant integers using multiplication", PLDI 1994).  Kernels that decode a work item
-// over and over use it: the divide instruction's sequence showed.
+// over and over use it: with n / d instead, attention of 35840 rows, 16 heads of 64, 600 of 1000 states takes 115 us for 111, of
+// 168960 rows, 16 heads of 128, 512 states 544 for 533.
 struct fast_div {
     uint32_t mul;
     int32_t shift, d;

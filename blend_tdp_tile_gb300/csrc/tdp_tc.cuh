@@ -39,8 +39,9 @@ __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity)
 
 // This warp's number, uniform to the compiler.
 __device__ __forceinline__ int32_t warp_id() { return __shfl_sync(~0u, (int)(threadIdx.x >> 5), 0); }
-// One lane of a converged warp.  The tensor-core and tensor-map instructions take uniform registers; behind elect.sync the
-// compiler knows that a single lane runs (behind a lane number it adds some 120 bytes of code to each of them).
+// One lane of a converged warp.  elect.sync tells the compiler that a single lane issues the tensor-core and tensor-map
+// instructions; chosen by its lane number instead, 35840 rows, 16 heads of 64, 600 of 1000 states take 153 us where this takes 111,
+// and 168960 rows, 16 heads of 128, 512 states 616 for 533.
 __device__ __forceinline__ bool elect_one()
 {
     uint32_t on;
