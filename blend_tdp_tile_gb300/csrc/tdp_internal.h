@@ -16,8 +16,6 @@ static inline bool tdp_aligned(const void *p, uintptr_t a)
 }
 
 #ifdef __CUDACC__
-#include <cuda.h>
-#include <cudaTypedefs.h>
 #include <cuda_runtime.h>
 
 #include <utility>
@@ -50,9 +48,6 @@ static inline cudaError_t tdp_launch(bool pdl, void (*kernel)(KArgs...), unsigne
 {
     return tdp_launch_smem(pdl, kernel, grid, block, 0, s, std::forward<Args>(args)...);
 }
-
-// The driver's tensor-map encoder, looked up once per process; NULL if it has none.
-PFN_cuTensorMapEncodeTiled_v12000 tdp_encode_tiled();
 
 // tdp_bounds_init_kernel (plain launch) then tdp_bounds_kernel (dependent launch)
 // on stream s: mn / mx of every (tile, batch item, dim).  Arguments checked by the caller.

@@ -39,24 +39,6 @@
 #include "tdp_device.cuh"
 #include "tdp_internal.h"
 
-// cuTensorMapEncodeTiled from the driver, looked up once per process.
-PFN_cuTensorMapEncodeTiled_v12000 tdp_encode_tiled()
-{
-    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-    static std::once_flag once;
-    std::call_once(once, [] {
-        void *p = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) ==
-                cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-        else
-            cudaGetLastError();
-    });
-    return fn;
-}
-
 namespace {
 
 constexpr int kPosWarpsPerCta = 3;                 // warps of a CTA that split the positions
@@ -335,6 +317,24 @@ tdp_split_tma_kernel(const __grid_constant__ CUtensorMap map, const __grid_const
     bulk_wait_all();
 }
 
+// cuTensorMapEncodeTiled from the driver, looked up once per process.
+PFN_cuTensorMapEncodeTiled_v12000 encode_tiled()
+{
+    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+    static std::once_flag once;
+    std::call_once(once, [] {
+        void *p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) ==
+                cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+        else
+            cudaGetLastError();
+    });
+    return fn;
+}
+
 // Multiprocessors of the current device (0 on error).
 int32_t device_sms()
 {
@@ -396,7 +396,7 @@ extern "C" tdp_status tdp_split_tma(tdp_plan_t plan, const void *X, const int32_
         return tdp_fail(TDP_ERR_TOO_LARGE,
                         "tdp_split_tma needs C <= 256, W-tiles at most 256 cells and two boxes of the widest "
                         "W-tile plus the position tables within 66 KB (tdp_split takes every shape)");
-    PFN_cuTensorMapEncodeTiled_v12000 encode = tdp_encode_tiled();
+    PFN_cuTensorMapEncodeTiled_v12000 encode = encode_tiled();
     if (!encode) return tdp_fail(TDP_ERR_CUDA, "cuTensorMapEncodeTiled not available from the driver");
 
     CUtensorMap map;

@@ -15,6 +15,7 @@
 #include <atomic>
 
 #include "tdp.h"
+#include "tdp_tensor_map.h"
 #include "tdp_xattn.h"
 #include "tdp_xattn_grad_tc.cuh"
 
