@@ -263,9 +263,10 @@ def _ptr(t, name, numel, dtypes, align):
         return None
     if not isinstance(t, _torch().Tensor):
         raise TypeError(f"{name}: expected a torch.Tensor")
-    p = t.data_ptr()
-    if t.is_cuda and t.dtype in dtypes and t.numel() == numel and not p % align and t.is_contiguous():
-        return p
+    if t.is_cuda and t.dtype in dtypes and t.numel() == numel and t.is_contiguous():
+        p = t.data_ptr()
+        if not p % align:
+            return p
     if not t.is_cuda:
         raise ValueError(f"{name}: must be a CUDA tensor")
     if not t.is_contiguous():
