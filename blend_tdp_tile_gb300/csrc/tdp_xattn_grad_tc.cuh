@@ -15,7 +15,7 @@
 //   warp 10          loads Q and dO (first kernel); each row's lse and delta (second)
 //   warp 11          zeroes rows of a tile that must not count (their memory may hold anything, and 0 * NaN is not 0)
 //
-// 35840 rows, 16 heads of 128 on 4, 640 states: dq in 236 us (1.19 PFLOP/s, tensor pipe 50 % busy: one row tile, whose
+// 35840 rows, 16 heads of 128 on 4, 640 states: dq in 232 us (1.22 PFLOP/s, tensor pipe 51 % busy: one row tile, whose
 // products wait for its softmax), dk and dv in 230 us (1.63 PFLOP/s, 69 %).  dP's columns are given back as soon as they
 // are read: a tile of dq takes 1920 cycles for 2240 in one launch; both gradients at 16 heads of 64, 1000 states, 523 us for
 // 544, at 128 columns 1 % less, the clock falling at the power limit.
@@ -46,7 +46,7 @@ struct dkv_smem {
 // make delta as large as dP, and dO . O, with its O rounded to bf16, costs dS digits that delta = sum p dP over the row does
 // not: a relative error of dQ of 0.0046 against 0.0023 at two states, 0.0032 at four, 0.0026 at 16, 0.00245 at 64 (scores of a
 // spread of one; a softmax that a few of many states fill pays as much, whatever their number).  The first walk costs both
-// gradients up to 1.7 times the time (35840 rows, 16 heads of 128, states in eight tiles: 2654 us against 1583): past 16
+// gradients up to 1.7 times the time (35840 rows, 16 heads of 128, states in eight tiles: 2606 us against 1564): past 16
 // states it gives less than a tenth of the error.  With one state tile the row's dP is all there and it is not needed.
 constexpr int32_t kFewStates = 16;
 
@@ -69,8 +69,8 @@ __device__ __forceinline__ item dq_item_at(const tdp_geom &g, const xattn_args &
     it.keys.n = it.rounds = tiles;
     if (a.mask) {
         const int64_t m = a.per_tile ? (int64_t)it.seg.t * g.B + it.seg.b : it.seg.b;
-        it.keys.n = __ldcg(a.kept_n + m);
-        it.rounds = it.keys.n > 1 && __ldcg(a.kept_states + m) <= kFewStates ? 2 * it.keys.n : it.keys.n;
+        it.keys.n = a.kept_n[m];
+        it.rounds = it.keys.n > 1 && a.kept_states[m] <= kFewStates ? 2 * it.keys.n : it.keys.n;
         it.keys.tile = a.kept_tile + m * tiles;
         it.keys.words = a.kept_words + m * tiles;
     }
@@ -161,7 +161,7 @@ tdp_xattn_dq_kernel(const __grid_constant__ tdp_geom g, const __grid_constant__ 
             if (it.left <= 0 || it.keys.n == 0) return;
             const bool mine = rt < a.TT && rt < it.left;
             const int32_t h = ((int32_t)(it.seg.row0 + it.tok0) + rt) * a.Hq + it.head + rh;
-            l = -row_lse2(mine ? __ldcg(a.lse + h) : -INFINITY);
+            l = -row_lse2(mine ? a.lse[h] : -INFINITY);
             ok = ok && mbar_wait(full + 8 * kv.st, kv.ph, dead) && mbar_wait(rfull + 8, n_items & 1, dead);
             ++n_items;
             float sum = 0.f;
@@ -500,7 +500,7 @@ struct row_walk {
             u = (sg + 1) * a.blocks;
             if (a.mask) {
                 const int64_t m = a.per_tile ? (int64_t)seg.t * g.B + seg.b : seg.b;
-                words = __ldcg(a.state_words + m * ((a.S + kKeys - 1) / kKeys) + tile);
+                words = a.state_words[m * ((a.S + kKeys - 1) / kKeys) + tile];
             } else {
                 key_list k;
                 k.tile = nullptr;
@@ -819,7 +819,7 @@ tdp_xattn_dkv_kernel(const __grid_constant__ tdp_geom g, const __grid_constant__
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const int32_t h = h0 + (st_tok[i] < left ? st_at[i] : 0);
-                        l[i] = __ldcg(a.lse + h);
+                        l[i] = a.lse[h];
                         d[i] = __ldcg(a.delta + h);
                     }
 #pragma unroll
