@@ -32,6 +32,8 @@ __all__ = [
     "tdp_tile_mean", "tdp_blend_partial", "tdp_blend_store", "tdp_blend_cond",
     "TDP_MAX_HEAD_DIM", "TDP_MAX_STATES", "tdp_cross_attn", "tdp_cross_attn_grad", "tdp_cross_attn_workspace",
     "tdp_group_norm", "tdp_group_norm_grad", "tdp_group_norm_workspace", "tdp_dropout_add", "tdp_dropout_grad",
+    "TDP_MAX_NORM_BYTES", "TDP_MAX_MATMUL8", "TDP_MAX_MATMUL8_ROWS", "TDP_MAX_ROPE_DIM", "tdp_rms_norm", "tdp_rms_norm_grad",
+    "tdp_rms_norm_grad_workspace", "tdp_quant8", "tdp_matmul8", "tdp_rope_freqs", "tdp_rope_table", "tdp_rope", "tdp_rope_grad",
     "tdp_balanced_tile_split", "tdp_tiles_for_size", "tdp_rank_tiles",
     "tdp_status_str", "tdp_last_error_detail",
     "alloc_split_outputs", "alloc_filter_outputs", "LIB_PATH",
@@ -44,7 +46,14 @@ TDP_F32, TDP_BF16 = 0, 1
 TDP_MAX_TILES_PER_DIM = 64
 TDP_MAX_HEAD_DIM = 128
 TDP_MAX_STATES = 1 << 20
+TDP_MAX_NORM_BYTES = 32768
+TDP_MAX_MATMUL8 = 1 << 20
+TDP_MAX_MATMUL8_ROWS = 1 << 30
+TDP_MAX_ROPE_DIM = 256
 _ACTS = {"none": 0, "silu": 1}
+_LAYOUTS = {"half": 0, "interleaved": 1}
+_PLACES = {"start": 0, "middle": 1}
+_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3}
 
 
 class TdpError(RuntimeError):
@@ -68,6 +77,11 @@ class _XAttn(ctypes.Structure):
                [("scale", ctypes.c_float)] + \
                [(n, ctypes.c_int64) for n in ("q_row", "q_head", "k_item", "k_state", "k_head",
                                               "v_item", "v_state", "v_head")]
+
+
+class _Rope(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("heads", "head_dim", "rot", "layout", "at")] + [("scale", ctypes.c_float)] + \
+               [(n, ctypes.c_int64) for n in ("x_row", "x_head", "out_row", "out_head")]
 
 
 def _load():
@@ -118,8 +132,18 @@ def _load():
     lib.tdp_group_norm_grad.argtypes = [vp, i32, i32, i32] + [vp] * 10 + [i64, vp]
     lib.tdp_dropout_add.argtypes = [vp, i64, f64, vp, vp, vp, vp, vp]
     lib.tdp_dropout_grad.argtypes = [vp, i64, f64, vp, vp, vp, vp]
+    lib.tdp_rms_norm.argtypes = [vp, i64, i32, f32] + [vp] * 11
+    lib.tdp_rms_norm_grad_workspace.argtypes = [vp, i64, i32, i64p]
+    lib.tdp_rms_norm_grad.argtypes = [vp, i64, i32] + [vp] * 10 + [i64, vp]
+    lib.tdp_quant8.argtypes = [vp, i64, i32] + [vp] * 4
+    lib.tdp_matmul8.argtypes = [vp, i64, i32, i32] + [vp] * 8
+    lib.tdp_rope_freqs.argtypes = [vp, f64, i32, f64, f64, vp, vp, ctypes.POINTER(f32)]
+    lib.tdp_rope_table.argtypes = [i32, vp, vp, vp]
+    lib.tdp_rope.argtypes = lib.tdp_rope_grad.argtypes = [vp, ctypes.POINTER(_Rope)] + [vp] * 5
     for name in ("tdp_cross_attn_workspace", "tdp_cross_attn", "tdp_cross_attn_grad", "tdp_group_norm_workspace",
-                 "tdp_group_norm", "tdp_group_norm_grad", "tdp_dropout_add", "tdp_dropout_grad"):
+                 "tdp_group_norm", "tdp_group_norm_grad", "tdp_dropout_add", "tdp_dropout_grad", "tdp_rms_norm",
+                 "tdp_rms_norm_grad_workspace", "tdp_rms_norm_grad", "tdp_quant8", "tdp_matmul8", "tdp_rope_freqs",
+                 "tdp_rope_table", "tdp_rope", "tdp_rope_grad"):
         getattr(lib, name).restype = ctypes.c_int
     lib.tdp_balanced_tile_split.argtypes = [i32, ctypes.POINTER(i32), ctypes.POINTER(i32)]
     lib.tdp_balanced_tile_split.restype = ctypes.c_int
@@ -756,3 +780,144 @@ def tdp_dropout_grad(plan: Plan, dout, p, rng, dx, stream=None):
     c = _Call("tdp_dropout_grad")
     c.run(_lib.tdp_dropout_grad, plan.handle, n, float(p), _rng(c, rng), c.ptr(dout, "dout", n, lat, 16),
           c.ptr(dx, "dx", n, lat, 16), stream=stream)
+
+
+def _bytes8():
+    """Types of 8-bit rows: e4m3, or its bytes."""
+    torch = _torch()
+    return (torch.float8_e4m3fn, torch.uint8)
+
+
+def _matrix(x, name):
+    """(rows, columns) of a tensor taken as rows of its last dimension."""
+    if not isinstance(x, _torch().Tensor):
+        raise TypeError(f"{name}: expected a torch.Tensor")
+    if x.dim() < 1 or x.shape[-1] < 1:
+        raise ValueError(f"{name}: shape {tuple(x.shape)} has no rows")
+    return x.numel() // x.shape[-1], int(x.shape[-1])
+
+
+def tdp_rms_norm(plan: Plan, x, w, y=None, res=None, h=None, rstd=None, y8=None, y8_scale=None, x8=None, x8_scale=None, eps=1e-6,
+                 stream=None):
+    """y = root-mean-square norm of the rows of h = x + res [.., C], times w [C] (res, w: or None).
+
+    Outputs, each or None: y and h in the plan's dtype, rstd [rows] in fp32, y8 with y8_scale [rows]: y in 8 bits (e4m3), x8 with
+    x8_scale: the rows before w, a checkpoint for tdp_rms_norm_grad."""
+    f32, lat, b8 = (_torch().float32,), _latent_dtypes(plan), _bytes8()
+    rows, C = _matrix(x, "x")
+    n = rows * C
+    c = _Call("tdp_rms_norm")
+    c.run(_lib.tdp_rms_norm, plan.handle, rows, C, float(eps), c.ptr(x, "x", n, lat, 16), c.ptr(res, "res", n, lat, 16),
+          c.ptr(w, "w", C, lat, 16), c.ptr(h, "h", n, lat, 16), c.ptr(y, "y", n, lat, 16), c.ptr(rstd, "rstd", rows, f32, 4),
+          c.ptr(y8, "y8", n, b8, 16), c.ptr(y8_scale, "y8_scale", rows, f32, 4), c.ptr(x8, "x8", n, b8, 16),
+          c.ptr(x8_scale, "x8_scale", rows, f32, 4), stream=stream)
+
+
+def tdp_rms_norm_grad_workspace(plan: Plan, rows: int, C: int) -> int:
+    """Bytes of workspace tdp_rms_norm_grad takes for dw."""
+    got = plan.sizes.get(("rms", rows, C))
+    if got is None:
+        n = ctypes.c_int64()
+        _check(_lib.tdp_rms_norm_grad_workspace(plan.handle, int(rows), int(C), ctypes.byref(n)), "tdp_rms_norm_grad_workspace")
+        got = plan.sizes["rms", rows, C] = int(n.value)
+    return got
+
+
+def tdp_rms_norm_grad(plan: Plan, dy, dx, w, rstd, h=None, x8=None, x8_scale=None, dh=None, dw=None, ws=None, stream=None):
+    """Gradients of tdp_rms_norm: dx [.., C] (of x, and of res alike) and, unless None, dw [C] in fp32, from h as the forward
+    left it or from its checkpoint x8, x8_scale.  dh: the gradient that comes by way of h, or None."""
+    f32, lat = (_torch().float32,), _latent_dtypes(plan)
+    rows, C = _matrix(dy, "dy")
+    n = rows * C
+    if dw is not None:
+        ws = _workspace(ws, tdp_rms_norm_grad_workspace(plan, rows, C), dy, stream, plan)
+    c = _Call("tdp_rms_norm_grad")
+    c.run(_lib.tdp_rms_norm_grad, plan.handle, rows, C, c.ptr(h, "h", n, lat, 16), c.ptr(x8, "x8", n, _bytes8(), 16),
+          c.ptr(x8_scale, "x8_scale", rows, f32, 4), c.ptr(rstd, "rstd", rows, f32, 4), c.ptr(w, "w", C, lat, 16),
+          c.ptr(dy, "dy", n, lat, 16), c.ptr(dh, "dh", n, lat, 16), c.ptr(dx, "dx", n, lat, 16), c.ptr(dw, "dw", C, f32, 4),
+          None if ws is None else c.ptr(ws, "ws", ws.numel(), (_torch().uint8,), 256),
+          0 if ws is None else ws.numel(), stream=stream)
+
+
+def tdp_quant8(plan: Plan, x, x8, x8_scale, stream=None):
+    """x8 [.., C] (e4m3) and x8_scale [rows]: the rows of x [.., C] in 8 bits, a scale a row."""
+    rows, C = _matrix(x, "x")
+    c = _Call("tdp_quant8")
+    c.run(_lib.tdp_quant8, plan.handle, rows, C, c.ptr(x, "x", rows * C, _latent_dtypes(plan), 16),
+          c.ptr(x8, "x8", rows * C, _bytes8(), 16), c.ptr(x8_scale, "x8_scale", rows, (_torch().float32,), 4), stream=stream)
+
+
+def tdp_matmul8(plan: Plan, x8, x8_scale, w8, w8_scale, out, bias=None, res=None, stream=None):
+    """out [.., N] = 8-bit rows x8 [.., K] (scales [rows]) times 8-bit weights w8 [N, K] (scales [N]), plus bias [N] and
+    res [.., N] (each or None)."""
+    f32, lat, b8 = (_torch().float32,), _latent_dtypes(plan), _bytes8()
+    (rows, K), (N, Kw) = _matrix(x8, "x8"), _matrix(w8, "w8")
+    if Kw != K:
+        raise ValueError(f"w8: rows of {Kw} values, x8 has {K}")
+    c = _Call("tdp_matmul8")
+    c.run(_lib.tdp_matmul8, plan.handle, rows, K, N, c.ptr(x8, "x8", rows * K, b8, 16), c.ptr(x8_scale, "x8_scale", rows, f32, 4),
+          c.ptr(w8, "w8", N * K, b8, 16), c.ptr(w8_scale, "w8_scale", N, f32, 16), c.ptr(bias, "bias", N, lat, 16),
+          c.ptr(res, "res", rows * N, lat, 16), c.ptr(out, "out", rows * N, lat, 16), stream=stream)
+
+
+def _named(value, names, what):
+    if value not in names:
+        raise ValueError(f"{what}: {value!r} not in {sorted(names)}")
+    return names[value]
+
+
+def tdp_rope_freqs(pairs, base=10000.0, scaling="none", factor=1.0, length=1.0):
+    """(freq float64 [n], axis int32 [n], scale) of a head's pairs, pairs = (a number an axis): base^(-i / pairs[a]), scaled for long contexts
+    by "linear", "ntk" or "yarn" (`length`: the trained one)."""
+    p = np.asarray(pairs, np.int32)
+    if p.shape != (3,):
+        raise ValueError("pairs: a number for each of the three axes")
+    n = int(np.maximum(p, 0).sum())
+    freq, axis, scale = np.zeros(n, np.float64), np.zeros(n, np.int32), ctypes.c_float()
+    _check(_lib.tdp_rope_freqs(p.ctypes.data_as(ctypes.c_void_p), float(base), _named(scaling, _SCALINGS, "scaling"), float(factor), float(length),
+                               freq.ctypes.data_as(ctypes.c_void_p), axis.ctypes.data_as(ctypes.c_void_p), ctypes.byref(scale)), "tdp_rope_freqs")
+    return freq, axis, float(scale.value)
+
+
+def tdp_rope_table(freq, axis):
+    """The table that tdp_rope reads, on the host: int64 [pairs] from frequencies (radians a position) and axes; move it to
+    the device once."""
+    freq, axis = np.ascontiguousarray(freq, np.float64), np.ascontiguousarray(axis, np.int32)
+    if freq.ndim != 1 or freq.shape != axis.shape:
+        raise ValueError("freq and axis: one number a pair")
+    table = np.zeros(len(freq), np.int64)
+    _check(_lib.tdp_rope_table(len(freq), freq.ctypes.data_as(ctypes.c_void_p), axis.ctypes.data_as(ctypes.c_void_p),
+                               table.ctypes.data_as(ctypes.c_void_p)), "tdp_rope_table")
+    return _torch().from_numpy(table)
+
+
+def _rope(where, fn, plan, x, Q, table, out, layout, at, scale, stream):
+    torch = _torch()
+    lat = _latent_dtypes(plan)
+    if not isinstance(x, torch.Tensor) or not isinstance(table, torch.Tensor):
+        raise TypeError(f"{where}: expected torch.Tensors")
+    if x.dim() != 3:
+        raise ValueError("rows must be [rows, heads, D]")
+    a = _Rope()
+    shape = (_rows(plan), int(x.shape[1]), int(x.shape[2]))
+    a.heads, a.head_dim, a.rot = shape[1], shape[2], 2 * table.numel()
+    a.layout, a.at, a.scale = _named(layout, _LAYOUTS, "layout"), _named(at, _PLACES, "at"), scale
+    a.x_row, a.x_head = _strides(x, "x", shape, lat)
+    a.out_row, a.out_head = _strides(out, "out", shape, lat)
+    c = _Call(where)
+    c.run(fn, plan.handle, ctypes.byref(a), _given(c, x, "x"), c.ptr(Q, "Q", 6 * shape[0], (torch.int32,), 8),
+          c.ptr(table, "table", table.numel(), (torch.int64,), 8), _given(c, out, "out"), stream=stream)
+
+
+def tdp_rope(plan: Plan, x, Q, table, out, layout="half", at="middle", scale=1.0, stream=None):
+    """out = tile rows x [R, heads, D], the first 2 * len(table) values of every head turned by the rows' positions Q (tile-major, from
+    tdp_split).  x and out may be strided (slices of a fused projection), and out x itself.
+
+    layout: pairs are values i and i + rot / 2 ("half") or 2 i and 2 i + 1 ("interleaved").  at: the "middle" or the "start" of a
+    token's interval is its position.  scale: factor of cos and sin, from tdp_rope_freqs."""
+    _rope("tdp_rope", _lib.tdp_rope, plan, x, Q, table, out, layout, at, scale, stream)
+
+
+def tdp_rope_grad(plan: Plan, dout, Q, table, dx, layout="half", at="middle", scale=1.0, stream=None):
+    """dx of tdp_rope with the same positions, table and names: dout turned back."""
+    _rope("tdp_rope_grad", _lib.tdp_rope_grad, plan, dout, Q, table, dx, layout, at, scale, stream)

@@ -1,0 +1,268 @@
+// tdp_matmul8.cu -- product of 8-bit rows and 8-bit weights (e4m3), a scale a row and a channel, bias and residual.
+//
+// out[r, n] = xs_r ws_n sum_k x8[r, k] w8[n, k] + bias_n + res[r, n].  Products of e4m3 values are exact in fp32, sums are
+// fp32 on the tensor cores (tcgen05, kind f8f6f4); scales, bias and residual come in fp32 behind the sum, one rounding
+// at the end.
+#include <algorithm>
+#include <atomic>
+
+#include "tdp.h"
+#include "tdp_internal.h"
+#include "tdp_matmul8.cuh"
+#include "tdp_tensor_map.h"
+
+namespace tdp_m8 {
+
+// Tiles of 128 channels by NT rows, one a block, K split over the blocks of a cluster.
+//
+// Channels are the lanes and rows the columns of the accumulator, so that few rows make a small tile: the weights' bytes bound
+// such a product, and a cluster's blocks each bring a part of K.  Warps 0-3 take the sums out of tensor memory, warp 4 loads, warp 5
+// issues the products.  The parts are joined through distributed shared memory, each block adding up its share of the
+// rows in the order of the parts.
+template <int NT>
+struct tile_smem {
+    static constexpr int kStage = 16384 + NT * 128;
+    static constexpr int kStages = NT <= 16 ? 5 : NT <= 64 ? 4 : 3;     // two blocks an SM
+    static constexpr int kBytes = 1024 + kStages * kStage;
+    static_assert(kStages * kStage >= NT * 512, "the parts lie where the stages were");
+};
+constexpr int kTileThreads = 192;
+
+template <int BF16, int NT>
+__global__ void __launch_bounds__(kTileThreads)
+tdp_matmul8_tile_kernel(const __grid_constant__ args a, const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x)
+{
+    using SM = tile_smem<NT>;
+    constexpr int NST = SM::kStages;
+    constexpr uint32_t kCols = NT < 32 ? 32 : NT;
+    extern __shared__ unsigned char raw[];
+    __shared__ uint64_t bar_mem[2 * NST + 1];
+    __shared__ uint32_t tmem_slot;
+    __shared__ int dead_flag;
+    volatile int *dead = &dead_flag;
+    const uint32_t base = (smem_u32(raw) + 1023u) & ~1023u, full = smem_u32(bar_mem), empty = full + 8 * NST, done = empty + 8 * NST;
+    const int32_t warp = warp_id(), lane = threadIdx.x & 31;
+    if (warp == 5) tmem_alloc(smem_u32(&tmem_slot), kCols);
+    if (threadIdx.x == 0) {
+        dead_flag = 0;
+        for (int i = 0; i < 2 * NST + 1; ++i) mbar_init(full + 8 * i, 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    fence_before();
+    __syncthreads();
+    fence_after();
+    const uint32_t tm = tmem_slot;
+    tdp_pdl_trigger();
+    tdp_pdl_wait();
+
+    const uint32_t split = cluster_size(), rank = cluster_rank();
+    const int32_t tile = blockIdx.x / split, tc = tile % a.tiles_c;
+    const int32_t ch0 = tc * 128;
+    const int64_t row0 = (int64_t)(tile / a.tiles_c) * NT;
+    const int32_t k0 = (int32_t)((int64_t)a.kb * rank / split), n = (int32_t)((int64_t)a.kb * (rank + 1) / split) - k0;
+    bool ok = true;
+    int32_t made = 0;
+    if (warp == 4) {
+#pragma unroll 1
+        for (; made < n; ++made) {
+            const int32_t st = made % NST;
+            if (!(ok = mbar_wait(empty + 8 * st, ((made / NST) & 1) ^ 1, dead))) break;
+            if (elect_one()) {
+                const uint32_t to = base + st * SM::kStage;
+                mbar_expect(full + 8 * st, SM::kStage);
+                tma_load2(to, &map_w, full + 8 * st, (k0 + made) * kK, ch0);
+                tma_load2(to + 16384, &map_x, full + 8 * st, (k0 + made) * kK, (int32_t)row0);
+            }
+            __syncwarp();
+        }
+        for (int32_t i = max(0, made - NST); i < made; ++i) landed(full + 8 * (i % NST), (i / NST) & 1);
+    } else if (warp == 5) {
+        constexpr uint32_t id = idesc8(128, NT);
+#pragma unroll 1
+        for (int32_t i = 0; i < n; ++i) {
+            const int32_t st = i % NST;
+            if (!(ok = mbar_wait(full + 8 * st, (i / NST) & 1, dead))) break;
+            fence_after();
+            if (elect_one()) {
+                const uint32_t w = desc_rows(base + st * SM::kStage), x = desc_rows(base + st * SM::kStage + 16384);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) mma8(tm, w + 2 * k, x + 2 * k, id, i > 0 || k > 0);
+                mma_commit(empty + 8 * st);
+            }
+            __syncwarp();
+        }
+        if (elect_one()) mma_commit(done);
+        __syncwarp();
+        landed(done, 0);
+    } else {
+        ok = mbar_wait(done, 0, dead);
+        fence_after();
+    }
+    __syncwarp();
+    // No block reads its stages any more, nothing is on its way to them: the parts take their place.
+    if (split > 1) cluster_sync();
+    else __syncthreads();
+    // part[from][row of the block's share][channel]
+    const int32_t share = NT / split, shift = __ffs(share) - 1;
+    if (warp < 4) {
+        ok = __all_sync(~0u, ok && !*dead);
+        const uint32_t from = tm + ((uint32_t)warp << 21);
+        constexpr int B = 16;
+#pragma unroll 1
+        for (int c0 = 0; c0 < NT; c0 += B) {
+            uint32_t v[B];
+            tmem_ld16(from + c0, v);
+            tmem_wait_ld();
+            tmem_have16(v);
+#pragma unroll
+            for (int c = 0; c < B; ++c) {
+                if (!ok) v[c] = 0x7fffffffu;
+                const uint32_t to = (c0 + c) >> shift, r = (c0 + c) & (share - 1);
+                asm volatile("st.shared::cluster.b32 [%0], %1;" ::"r"(at_rank(base + ((rank * share + r) * 128 + threadIdx.x) * 4, to)), "r"(v[c]) : "memory");
+            }
+        }
+        fence_before();
+    }
+    __syncwarp();
+    if (split > 1) cluster_sync();
+    else __syncthreads();
+    if (warp < 4) {
+        using E = tdp_elem<BF16>;
+        using T = typename E::type;
+        const int32_t ch = ch0 + 2 * (threadIdx.x & 63);
+        if (ch < a.N) {
+            const float2 w = __ldcg(reinterpret_cast<const float2 *>(a.ws + ch));
+            const T *bias = static_cast<const T *>(a.bias);
+            const float b0 = bias ? (float)bias[ch] : 0.f, b1 = bias ? (float)bias[ch + 1] : 0.f;
+            const float *part = reinterpret_cast<const float *>(raw + (base - smem_u32(raw))) + 2 * (threadIdx.x & 63);
+            for (int32_t r = threadIdx.x >> 6; r < share; r += 2) {
+                const int64_t row = row0 + (int64_t)rank * share + r;
+                if (row >= a.rows) break;
+                float2 s = make_float2(0.f, 0.f);
+                for (uint32_t f = 0; f < split; ++f) {
+                    const float2 p = *reinterpret_cast<const float2 *>(part + (f * share + r) * 128);
+                    s.x += p.x;
+                    s.y += p.y;
+                }
+                const float x = __ldcg(a.xs + row);
+                float v0 = fmaf(s.x * x, w.x, b0), v1 = fmaf(s.y * x, w.y, b1);
+                const int64_t at = row * a.N + ch;
+                if (BF16) {
+                    if (a.res) {
+                        const uint32_t u = *reinterpret_cast<const uint32_t *>(static_cast<const T *>(a.res) + at);
+                        v0 += tdp_bf16_lo(u);
+                        v1 += tdp_bf16_hi(u);
+                    }
+                    *reinterpret_cast<uint32_t *>(static_cast<T *>(a.out) + at) = tdp_pack_bf16x2(v0, v1);
+                } else {
+                    if (a.res) {
+                        const float2 u = *reinterpret_cast<const float2 *>(static_cast<const T *>(a.res) + at);
+                        v0 += u.x;
+                        v1 += u.y;
+                    }
+                    *reinterpret_cast<float2 *>(static_cast<T *>(a.out) + at) = make_float2(v0, v1);
+                }
+            }
+        }
+    }
+    fence_before();
+    __syncthreads();
+    if (warp == 5) tmem_free(tm, kCols);
+}
+
+}  // namespace tdp_m8
+
+namespace {
+
+using namespace tdp_m8;
+
+// Map of e4m3 rows: boxes of 128 values by `box` rows in 128-byte-swizzled panels; zeros past the ends.
+bool map8(CUtensorMap *map, const void *p, int64_t K, int64_t rows, int box)
+{
+    PFN_cuTensorMapEncodeTiled_v12000 encode = tdp_encode_tiled();
+    if (!encode) return false;
+    const cuuint64_t extent[2] = {(cuuint64_t)K, (cuuint64_t)rows}, stride[1] = {(cuuint64_t)K};
+    const cuuint32_t b[2] = {(cuuint32_t)kK, (cuuint32_t)box}, one[2] = {1, 1};
+    return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(p), extent, stride, b, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Raise a kernel's dynamic shared-memory limit once per device (`done`: one flag each).
+template <typename K>
+cudaError_t allow_smem(K kernel, size_t bytes, std::atomic<bool> *done)
+{
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess || (dev < 64 && done[dev].load(std::memory_order_relaxed))) return e;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    if (e == cudaSuccess && dev < 64) done[dev].store(true, std::memory_order_relaxed);
+    return e;
+}
+
+// A dependent launch of clusters of `size` blocks.
+template <typename... KArgs, typename... Args>
+cudaError_t launch_clusters(void (*kernel)(KArgs...), unsigned grid, unsigned size, unsigned block, size_t smem, cudaStream_t s, Args &&...args)
+{
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = size;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(block);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
+}
+
+template <int BF16, int NT>
+cudaError_t tile_launch(const args &a, const void *w8, const void *x8, int64_t K, cudaStream_t s)
+{
+    static std::atomic<bool> done[64];
+    constexpr size_t bytes = tile_smem<NT>::kBytes;
+    cudaError_t e = allow_smem(tdp_matmul8_tile_kernel<BF16, NT>, bytes, done);
+    CUtensorMap w, x;
+    if (e == cudaSuccess && (!map8(&w, w8, K, a.N, 128) || !map8(&x, x8, K, a.rows, NT))) e = cudaErrorInvalidValue;
+    if (e != cudaSuccess) return e;
+    // parts of K until the device is full
+    const int64_t tiles = (int64_t)a.tiles_c * ((a.rows + NT - 1) / NT);
+    unsigned split = 1;
+    while (split < 8 && 2 * split <= (unsigned)a.kb && tiles * split < 152) split *= 2;
+    return launch_clusters(tdp_matmul8_tile_kernel<BF16, NT>, (unsigned)(tiles * split), split, kTileThreads, bytes, s, a, w, x);
+}
+
+template <int BF16>
+cudaError_t matmul8(const args &a, const void *w8, const void *x8, int64_t K, cudaStream_t s)
+{
+    return a.rows <= 16 ? tile_launch<BF16, 16>(a, w8, x8, K, s) : a.rows <= 64 ? tile_launch<BF16, 64>(a, w8, x8, K, s)
+                                                                                : tile_launch<BF16, 128>(a, w8, x8, K, s);
+}
+
+}  // namespace
+
+extern "C" tdp_status tdp_matmul8(tdp_plan_t plan, int64_t rows, int32_t K, int32_t N, const uint8_t *x8, const float *x8_scale,
+                                  const uint8_t *w8, const float *w8_scale, const void *bias, const void *res, void *out,
+                                  tdp_stream_t stream)
+{
+    if (!plan) return tdp_fail(TDP_ERR_INVALID_ARG, "null plan");
+    const tdp_geom &g = plan->g;
+    if (rows < 0 || K < 1 || N < 1) return tdp_fail(TDP_ERR_INVALID_ARG, "need rows >= 0, K >= 1 and N >= 1");
+    if (K % 16 != 0 || (int64_t)N * g.esize % 16 != 0)
+        return tdp_fail(TDP_ERR_MISALIGNED, "K and N * element size must be multiples of 16 bytes");
+    if (K > TDP_MAX_MATMUL8 || N > TDP_MAX_MATMUL8 || rows > TDP_MAX_MATMUL8_ROWS)
+        return tdp_fail(TDP_ERR_TOO_LARGE, "K or N above TDP_MAX_MATMUL8, or rows above TDP_MAX_MATMUL8_ROWS");
+    if (rows == 0) return tdp_ok();
+    if (!x8 || !x8_scale || !w8 || !w8_scale || !out) return tdp_fail(TDP_ERR_INVALID_ARG, "null x8, w8, scales or out");
+    if (!tdp_aligned(x8, 16) || !tdp_aligned(w8, 16) || !tdp_aligned(bias, 16) || !tdp_aligned(res, 16) || !tdp_aligned(out, 16) ||
+        !tdp_aligned(x8_scale, 4) || !tdp_aligned(w8_scale, 16))
+        return tdp_fail(TDP_ERR_MISALIGNED, "rows, w8_scale and bias need 16-byte, x8_scale 4-byte alignment");
+    if ((rows + 127) / 128 * ((N + 127) / 128) > (1 << 28)) return tdp_fail(TDP_ERR_TOO_LARGE, "rows * N above 2^42");
+    args a = {x8_scale, w8_scale, bias, res, out, rows, N, (K + kK - 1) / kK, (N + 127) / 128};
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    const cudaError_t err = g.dtype == TDP_BF16 ? matmul8<1>(a, w8, x8, K, s) : matmul8<0>(a, w8, x8, K, s);
+    return err == cudaSuccess ? tdp_ok() : tdp_fail(TDP_ERR_CUDA, cudaGetErrorString(err));
+}

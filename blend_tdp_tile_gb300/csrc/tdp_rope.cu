@@ -1,0 +1,300 @@
+// tdp_rope.cu -- rotary positions: every head of a tile-major row turned by the row's position, and back.
+//
+// Pair i of a head, (a, b), belongs to an axis and has a frequency f_i: with p the row's position on that axis,
+//   a' = scale (a cos(p f) - b sin(p f)),  b' = scale (a sin(p f) + b cos(p f));  the gradient turns by -p f.
+// An angle is kept in turns: p f / 2 pi, of which only the fraction counts, is the low 64 bits of the product of an integer
+// position and the frequency in 2^-64 turns.  No reduction loses digits however far the position is: 2^32 positions off
+// the origin the angle is 2^-30 turns off, and 64-bit floats, a fiftieth of the rate of 32-bit ones here, are not needed.
+//
+// Bound by memory.  A thread makes the sines of its pairs once and takes them through the heads of its row, 16 bytes at
+// a time where the layout allows, several heads' loads ahead.
+#include <algorithm>
+#include <cmath>
+
+#include "tdp.h"
+#include "tdp_internal.h"
+#include "tdp_rows.cuh"
+
+namespace {
+
+constexpr int kRopeThreads = 256;
+constexpr int kRopeAhead = 4;               // heads whose loads a thread has under way
+constexpr double kInvFourPiHi = 0.07957747154594767;        // 1 / (4 pi), and what it lacks
+constexpr double kInvFourPiLo = -4.9196691687956215e-18;
+
+struct rope_args {
+    const void *x;
+    const int32_t *pos;
+    const int64_t *table;
+    void *out;
+    int64_t x_row, x_head, out_row, out_head;       // strides in bytes
+    int32_t heads, pairs;
+    int32_t turned, items;      // items of a head: those of pairs, and with them those behind the pairs
+    int32_t groups;             // heads side by side
+    int32_t rows;               // rows of a block
+    int32_t blocks;             // blocks of the largest segment
+    int32_t middle;
+    float sign, scale;
+};
+
+// W elements as fp32.
+template <int BF16, int W>
+__device__ __forceinline__ void load(const unsigned char *p, uint32_t *u)
+{
+    constexpr int B = W * (BF16 ? 2 : 4);
+    if (B == 16) {
+        const uint4 v = __ldcs(reinterpret_cast<const uint4 *>(p));
+        u[0] = v.x;
+        u[1] = v.y;
+        u[2] = v.z;
+        u[3] = v.w;
+    } else if (B == 8) {
+        const uint2 v = __ldcs(reinterpret_cast<const uint2 *>(p));
+        u[0] = v.x;
+        u[1] = v.y;
+    } else if (B == 4) {
+        u[0] = __ldcs(reinterpret_cast<const uint32_t *>(p));
+    } else {
+        u[0] = __ldcs(reinterpret_cast<const unsigned short *>(p));
+    }
+}
+template <int BF16, int W>
+__device__ __forceinline__ void store(unsigned char *p, const uint32_t *u)
+{
+    constexpr int B = W * (BF16 ? 2 : 4);
+    if (B == 16) *reinterpret_cast<uint4 *>(p) = make_uint4(u[0], u[1], u[2], u[3]);
+    else if (B == 8) *reinterpret_cast<uint2 *>(p) = make_uint2(u[0], u[1]);
+    else if (B == 4) *reinterpret_cast<uint32_t *>(p) = u[0];
+    else *reinterpret_cast<unsigned short *>(p) = (unsigned short)u[0];
+}
+template <int BF16, int W>
+__device__ __forceinline__ void unpack(const uint32_t *u, float *f)
+{
+#pragma unroll
+    for (int i = 0; i < W; ++i) f[i] = BF16 ? (i & 1 ? tdp_bf16_hi(u[i / 2]) : tdp_bf16_lo(u[i / 2])) : __uint_as_float(u[i]);
+}
+template <int BF16, int W>
+__device__ __forceinline__ void pack(const float *f, uint32_t *u)
+{
+    if (!BF16) {
+#pragma unroll
+        for (int i = 0; i < W; ++i) u[i] = __float_as_uint(f[i]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < W; i += 2) u[i / 2] = tdp_pack_bf16x2(f[i], i + 1 < W ? f[i + 1] : 0.f);
+    }
+}
+
+// HALF: element i and i + pairs are a pair, an item two vectors of W elements; otherwise elements 2 i and 2 i + 1, an item
+// one vector (W even).  W is 16 bytes where rot, and half of it, allow that.
+template <int BF16, int W, int HALF>
+__global__ void __launch_bounds__(kRopeThreads)
+tdp_rope_kernel(const __grid_constant__ tdp_geom g, const __grid_constant__ rope_args a)
+{
+    constexpr int B = W * (BF16 ? 2 : 4), U = (B + 3) / 4, P = HALF ? W : W / 2;
+    tdp_pdl_trigger();
+    tdp_pdl_wait();
+    const int32_t seg = blockIdx.x / a.blocks, blk = blockIdx.x - seg * a.blocks;
+    const tdp_seg sg = tdp_seg_at(g, seg);
+    const int32_t team = a.items * a.groups, tr = threadIdx.x / team, place = threadIdx.x - tr * team;
+    const int64_t j = (int64_t)blk * a.rows + tr;
+    if (tr >= a.rows || j >= sg.T) return;
+    const int32_t group = place / a.items, item = place - group * a.items;
+    const int64_t row = sg.row0 + j;
+    const bool turns = item < a.turned;
+    // where the item's vectors lie in a head
+    const int32_t o0 = turns ? item * B : (2 * a.pairs * (BF16 ? 2 : 4) + (item - a.turned) * B);
+    const int32_t o1 = o0 + a.pairs * (BF16 ? 2 : 4);
+    const unsigned char *x = static_cast<const unsigned char *>(a.x) + row * a.x_row + o0;
+    unsigned char *out = static_cast<unsigned char *>(a.out) + row * a.out_row + o0;
+    if (!turns) {
+        // what lies behind the pairs is copied
+        if (x == out && a.x_head == a.out_head) return;
+        for (int32_t h = group; h < a.heads; h += a.groups) {
+            uint32_t u[U];
+            load<BF16, W>(x + h * a.x_head, u);
+            store<BF16, W>(out + h * a.out_head, u);
+        }
+        return;
+    }
+    float c[P], s[P];
+    {
+        const int32_t *q = a.pos + 6 * sg.row0 + 2 * j;
+        int64_t p[3];
+#pragma unroll
+        for (int d = 0; d < 3; ++d) {
+            const int2 v = *reinterpret_cast<const int2 *>(q + 2 * d * sg.T);
+            p[d] = a.middle ? (int64_t)v.x + v.y : 2 * (int64_t)v.x;
+        }
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+            const int64_t f = a.table[item * P + i];
+            const int32_t axis = (int32_t)f & 3;
+            const uint64_t turn = (uint64_t)(f & ~3ll) * (uint64_t)(axis == 0 ? p[0] : axis == 1 ? p[1] : p[2]);
+            sincospif((float)(int32_t)(turn >> 32) * 0x1p-31f, &s[i], &c[i]);
+            c[i] *= a.scale;
+            s[i] *= a.sign * a.scale;
+        }
+    }
+    for (int32_t h0 = group; h0 < a.heads; h0 += kRopeAhead * a.groups) {
+        uint32_t u[kRopeAhead][U], v[kRopeAhead][U];
+#pragma unroll
+        for (int k = 0; k < kRopeAhead; ++k) {
+            const int32_t h = h0 + k * a.groups;
+            if (h >= a.heads) break;
+            load<BF16, W>(x + h * a.x_head, u[k]);
+            if (HALF) load<BF16, W>(x + h * a.x_head + (o1 - o0), v[k]);
+        }
+#pragma unroll
+        for (int k = 0; k < kRopeAhead; ++k) {
+            const int32_t h = h0 + k * a.groups;
+            if (h >= a.heads) break;
+            float e[W], f[W];
+            unpack<BF16, W>(u[k], e);
+            if (HALF) unpack<BF16, W>(v[k], f);
+#pragma unroll
+            for (int i = 0; i < P; ++i) {
+                float &l = HALF ? e[i] : e[2 * i], &r = HALF ? f[i] : e[2 * i + 1];
+                const float l0 = l;
+                l = l0 * c[i] - r * s[i];
+                r = l0 * s[i] + r * c[i];
+            }
+            pack<BF16, W>(e, u[k]);
+            store<BF16, W>(out + h * a.out_head, u[k]);
+            if (HALF) {
+                pack<BF16, W>(f, v[k]);
+                store<BF16, W>(out + h * a.out_head + (o1 - o0), v[k]);
+            }
+        }
+    }
+}
+
+tdp_status rope(tdp_plan_t plan, const tdp_rope_shape *p, const void *x, const int32_t *pos, const int64_t *table, void *out,
+                float sign, tdp_stream_t stream)
+{
+    if (!plan || !p) return tdp_fail(TDP_ERR_INVALID_ARG, "null plan or shape");
+    const tdp_geom &g = plan->g;
+    if (p->heads < 1 || p->head_dim < 1 || p->rot < 2 || p->rot % 2 != 0 || p->rot > p->head_dim)
+        return tdp_fail(TDP_ERR_INVALID_ARG, "need heads >= 1 and an even rot from 2 to head_dim");
+    if ((p->layout != TDP_ROPE_HALF && p->layout != TDP_ROPE_INTERLEAVED) || (p->at != TDP_ROPE_START && p->at != TDP_ROPE_MIDDLE))
+        return tdp_fail(TDP_ERR_INVALID_ARG, "unknown layout or place in the interval");
+    if (!(p->scale - p->scale == 0.f)) return tdp_fail(TDP_ERR_INVALID_ARG, "scale must be finite");
+    if (p->head_dim > TDP_MAX_ROPE_DIM) return tdp_fail(TDP_ERR_TOO_LARGE, "head_dim above TDP_MAX_ROPE_DIM");
+    const int64_t V = 16 / g.esize, strides[4] = {p->x_row, p->x_head, p->out_row, p->out_head};
+    if (p->head_dim % V != 0) return tdp_fail(TDP_ERR_MISALIGNED, "head_dim * element size must be a multiple of 16 bytes");
+    for (int64_t s : strides) {
+        if (s < 0) return tdp_fail(TDP_ERR_INVALID_ARG, "strides must not be negative");
+        if (s % V != 0) return tdp_fail(TDP_ERR_MISALIGNED, "strides must be multiples of 16 bytes");
+        if (s >= ((int64_t)1 << 38)) return tdp_fail(TDP_ERR_TOO_LARGE, "strides must be below 2^38 elements");
+    }
+    const int64_t R = (int64_t)g.B * g.total;
+    // a row's heads side by side, or a head's rows
+    const int64_t D = p->head_dim, oh = p->heads > 1 ? p->out_head : D, orow = R > 1 ? p->out_row : D;
+    if (!(oh >= D && (R <= 1 || orow >= (p->heads - 1) * oh + D)) && !(orow >= D && (p->heads == 1 || oh >= (R - 1) * orow + D)))
+        return tdp_fail(TDP_ERR_INVALID_ARG, "out's rows and heads overlap");
+    if (R == 0) return tdp_ok();
+    if (!x || !pos || !table || !out) return tdp_fail(TDP_ERR_INVALID_ARG, "null x, positions, table or out");
+    if (!tdp_aligned(x, 16) || !tdp_aligned(out, 16) || !tdp_aligned(pos, 8) || !tdp_aligned(table, 8))
+        return tdp_fail(TDP_ERR_MISALIGNED, "heads need 16-byte, positions and table 8-byte alignment");
+    // the widest vector that half of rot (or rot) is a multiple of
+    const int32_t half = p->layout == TDP_ROPE_HALF;
+    int32_t W = (int32_t)V;
+    while ((half ? p->rot / 2 : p->rot) % W != 0) W /= 2;
+    rope_args a = {};
+    a.x = x;
+    a.pos = pos;
+    a.table = table;
+    a.out = out;
+    a.x_row = p->x_row * g.esize;
+    a.x_head = p->heads > 1 ? p->x_head * g.esize : 0;
+    a.out_row = p->out_row * g.esize;
+    a.out_head = p->heads > 1 ? p->out_head * g.esize : 0;
+    a.heads = p->heads;
+    a.pairs = p->rot / 2;
+    a.turned = half ? a.pairs / W : p->rot / W;
+    a.items = a.turned + (p->head_dim - p->rot) / W;
+    // eight heads a thread where there are that many: its sines are made once
+    a.groups = std::max(1, std::min({p->heads, kRopeThreads / a.items, (p->heads + 7) / 8}));
+    a.rows = kRopeThreads / (a.items * a.groups);
+    const int64_t T = tdp_max_tile_tokens(g);
+    a.rows = (int32_t)std::min<int64_t>(a.rows, T);
+    const int64_t blocks = (T + a.rows - 1) / a.rows;
+    if (blocks * g.nt > 0x7fffffffLL / g.B) return tdp_fail(TDP_ERR_TOO_LARGE, "rotary positions: grid too large");
+    a.blocks = (int32_t)blocks;
+    a.middle = p->at == TDP_ROPE_MIDDLE;
+    a.sign = sign;
+    a.scale = p->scale;
+    const unsigned grid = (unsigned)(blocks * g.nt * g.B);
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+#define TDP_ROPE(BF, W) \
+    (half ? tdp_launch(true, tdp_rope_kernel<BF, W, 1>, grid, kRopeThreads, s, g, a) \
+          : tdp_launch(true, tdp_rope_kernel<BF, W, 0>, grid, kRopeThreads, s, g, a))
+    cudaError_t err;
+    if (g.dtype == TDP_BF16)
+        err = W == 8 ? TDP_ROPE(1, 8) : W == 4 ? TDP_ROPE(1, 4) : W == 2 ? TDP_ROPE(1, 2) :
+              tdp_launch(true, tdp_rope_kernel<1, 1, 1>, grid, kRopeThreads, s, g, a);      // odd halves alone
+    else
+        err = W == 4 ? TDP_ROPE(0, 4) : W == 2 ? TDP_ROPE(0, 2) : tdp_launch(true, tdp_rope_kernel<0, 1, 1>, grid, kRopeThreads, s, g, a);
+#undef TDP_ROPE
+    return err == cudaSuccess ? tdp_ok() : tdp_fail(TDP_ERR_CUDA, cudaGetErrorString(err));
+}
+
+}  // namespace
+
+extern "C" tdp_status tdp_rope(tdp_plan_t plan, const tdp_rope_shape *p, const void *x, const int32_t *pos, const int64_t *table,
+                               void *out, tdp_stream_t stream)
+{
+    return rope(plan, p, x, pos, table, out, 1.f, stream);
+}
+
+extern "C" tdp_status tdp_rope_grad(tdp_plan_t plan, const tdp_rope_shape *p, const void *dout, const int32_t *pos,
+                                    const int64_t *table, void *dx, tdp_stream_t stream)
+{
+    return rope(plan, p, dout, pos, table, dx, -1.f, stream);
+}
+
+extern "C" tdp_status tdp_rope_table(int32_t pairs, const double *freq, const int32_t *axis, int64_t *table)
+{
+    if (pairs < 0 || (pairs > 0 && (!freq || !axis || !table))) return tdp_fail(TDP_ERR_INVALID_ARG, "null array or negative pairs");
+    for (int32_t i = 0; i < pairs; ++i) {
+        if (axis[i] < 0 || axis[i] > 2 || !(std::fabs(freq[i]) <= 0x1p20)) return tdp_fail(TDP_ERR_INVALID_ARG, "axes are 0, 1, 2 and frequencies at most 2^20");
+    }
+    for (int32_t i = 0; i < pairs; ++i) {
+        // (start + end) / 2 is an integer times f / 4 pi turns.  The product to 106 bits, of the magnitude: the fraction of a
+        // negative number would lose its last bits.
+        const double f = std::fabs(freq[i]), hi = f * kInvFourPiHi, lo = std::fma(f, kInvFourPiHi, -hi) + f * kInvFourPiLo;
+        const double up = std::ldexp(hi - std::floor(hi), 32), top = std::floor(up);
+        const double rest = std::ldexp(up - top, 32) + std::ldexp(lo, 64);          // in 2^-64 turns
+        uint64_t turns = ((uint64_t)top << 32) + (uint64_t)(int64_t)std::floor(rest + 0.5);
+        turns = (freq[i] < 0 ? 0 - turns : turns) + 2;
+        table[i] = (int64_t)((turns & ~3ull) | (uint64_t)axis[i]);
+    }
+    return tdp_ok();
+}
+
+extern "C" tdp_status tdp_rope_freqs(const int32_t *pairs, double base, int32_t scaling, double factor, double length, double *freq,
+                                     int32_t *axis, float *scale)
+{
+    if (!pairs || !freq || !axis || !scale) return tdp_fail(TDP_ERR_INVALID_ARG, "null array");
+    if (pairs[0] < 0 || pairs[1] < 0 || pairs[2] < 0) return tdp_fail(TDP_ERR_INVALID_ARG, "negative pairs");
+    if (!(base > 0) || !std::isfinite(base) || scaling < TDP_ROPE_UNSCALED || scaling > TDP_ROPE_YARN)
+        return tdp_fail(TDP_ERR_INVALID_ARG, "need a finite base > 0 and a known scaling");
+    if (scaling != TDP_ROPE_UNSCALED && (!(factor >= 1) || !std::isfinite(factor))) return tdp_fail(TDP_ERR_INVALID_ARG, "need a finite factor >= 1");
+    if (scaling == TDP_ROPE_YARN && (!(length > 0) || !std::isfinite(length))) return tdp_fail(TDP_ERR_INVALID_ARG, "need a finite length > 0");
+    for (int32_t a = 0, at = 0; a < 3; ++a) {
+        const int32_t n = pairs[a];
+        const double b = scaling == TDP_ROPE_NTK && n > 1 ? base * std::pow(factor, (double)n / (n - 1)) : base;
+        for (int32_t i = 0; i < n; ++i, ++at) {
+            double f = std::pow(b, -(double)i / n);
+            if (scaling == TDP_ROPE_LINEAR) f /= factor;
+            if (scaling == TDP_ROPE_YARN) {
+                const double keep = std::min(1.0, std::max(0.0, (length * f / (2 * M_PI) - 1) / (32 - 1)));
+                f = f * keep + f / factor * (1 - keep);
+            }
+            freq[at] = f;
+            axis[at] = a;
+        }
+    }
+    *scale = scaling == TDP_ROPE_YARN ? (float)(0.1 * std::log(factor) + 1) : 1.f;
+    return tdp_ok();
+}

@@ -548,6 +548,154 @@ tdp_status tdp_dropout_add(tdp_plan_t plan, int64_t n, double p, const uint64_t 
 tdp_status tdp_dropout_grad(tdp_plan_t plan, int64_t n, double p, const uint64_t *rng, const void *dout, void *dx,
                             tdp_stream_t stream);
 
+/* Longest rows of tdp_rms_norm, its gradient and tdp_quant8, in bytes of the plan's dtype. */
+#define TDP_MAX_NORM_BYTES 32768
+
+/*
+ * tdp_rms_norm -- root-mean-square norm of rows, with the residual's addition, in the plan's
+ * dtype, in 8 bits, or both.
+ *
+ * For every row: h = x + res (x without res), rounded to the plan's dtype;
+ *   rstd = 1 / sqrt(mean h^2 + eps),  u = h * rstd,  y = u * w.
+ * 8 bits are e4m3 (one byte a value) with a scale a row: of a row v with largest magnitude m,
+ * counted as 2^-100 where it is less, the values are 448 v / m, to the nearest of e4m3's (the even one of two),
+ * and the scale is m / 448; value * scale is v to within half a step.  A row that holds NaN or
+ * an infinity has scale NaN and NaN in every place.  (Rows whose sum of squares is above the
+ * largest float have rstd = 0.)
+ *
+ *   rows, C     any number of rows (tile-major rows, heads, states) of C values; C * element
+ *               size a multiple of 16 and at most TDP_MAX_NORM_BYTES.
+ *   x, res      device [rows, C] (plan dtype), read; res may be NULL.
+ *   w           device [C] (plan dtype), read; NULL: 1.
+ *   h, y        device [rows, C] (plan dtype), written; either may be NULL, and either may be x
+ *               or res itself (not both the same).
+ *   rstd        device fp32 [rows], written; or NULL.  The gradient reads it.
+ *   y8, y8_scale   y in 8 bits: device uint8 [rows, C] and fp32 [rows], written; or both NULL.
+ *   x8, x8_scale   u in 8 bits, as a checkpoint for the gradient in place of h; or both NULL.
+ * At least one output.  Rows start on 16 bytes.
+ */
+tdp_status tdp_rms_norm(tdp_plan_t plan, int64_t rows, int32_t C, float eps, const void *x, const void *res,
+                        const void *w, void *h, void *y, float *rstd, uint8_t *y8, float *y8_scale, uint8_t *x8,
+                        float *x8_scale, tdp_stream_t stream);
+
+/*
+ * tdp_rms_norm_grad -- gradients of tdp_rms_norm, from the stream h or from its checkpoint in 8 bits.
+ *
+ * With u = h * rstd, or the checkpoint's values x8 * x8_scale, and g = dy * w:
+ *   dx = dh + rstd * (g - u * mean(g * u)),  dw = sum over all rows of dy * u.
+ * dx is the gradient of x and, alike, of res.
+ *
+ *   h            device [rows, C] (plan dtype) as the forward wrote it (x itself without a residual), read; or NULL.
+ *   x8, x8_scale device uint8 [rows, C] and fp32 [rows] from the forward, read, in place of h; or both NULL.
+ *   rstd         device fp32 [rows] from the forward, read.
+ *   w            as for tdp_rms_norm.
+ *   dy           device [rows, C] (plan dtype), read.
+ *   dh           device [rows, C] (plan dtype), the gradient that comes by way of h, read; or NULL: 0.
+ *   dx           device [rows, C] (plan dtype), written; may be dy or dh itself.
+ *   dw           device fp32 [C], written (zero without rows); or NULL.
+ *   ws           device workspace of tdp_rms_norm_grad_workspace(plan, rows, C, ...) bytes; not used without dw.
+ */
+tdp_status tdp_rms_norm_grad_workspace(tdp_plan_t plan, int64_t rows, int32_t C, int64_t *bytes);
+tdp_status tdp_rms_norm_grad(tdp_plan_t plan, int64_t rows, int32_t C, const void *h, const uint8_t *x8,
+                             const float *x8_scale, const float *rstd, const void *w, const void *dy, const void *dh,
+                             void *dx, float *dw, void *ws, int64_t ws_bytes, tdp_stream_t stream);
+
+/* Largest K and N, and most rows, of tdp_matmul8. */
+#define TDP_MAX_MATMUL8 (1 << 20)
+#define TDP_MAX_MATMUL8_ROWS (1 << 30)
+
+/*
+ * tdp_quant8 -- rows in 8 bits as tdp_rms_norm writes them: weights (a scale an output channel), attention outputs.
+ *
+ *   x             device [rows, C] (plan dtype), read; C as for tdp_rms_norm.
+ *   x8, x8_scale  device uint8 [rows, C] and fp32 [rows], written.
+ */
+tdp_status tdp_quant8(tdp_plan_t plan, int64_t rows, int32_t C, const void *x, uint8_t *x8, float *x8_scale,
+                      tdp_stream_t stream);
+
+/*
+ * tdp_matmul8 -- product of 8-bit rows with 8-bit weights.
+ *
+ * out[r, n] = x8_scale_r * w8_scale_n * sum_k x8[r, k] * w8[n, k] + bias_n + res[r, n], the sum in
+ * fp32, one rounding at the end.  For serving: it has no gradient.  (Should a kernel's own wait run
+ * out, it gives up and fills its outputs with NaN.)
+ *
+ *   rows, K, N     K a multiple of 16, N * element size a multiple of 16; at most TDP_MAX_MATMUL8
+ *                  each, rows at most TDP_MAX_MATMUL8_ROWS, rows * N at most 2^42.
+ *   x8, x8_scale   device e4m3 [rows, K] and fp32 [rows], read.
+ *   w8, w8_scale   device e4m3 [N, K] (an output channel a row) and fp32 [N] (16-byte aligned), read.
+ *   bias           device [N] (plan dtype), read; or NULL.
+ *   res            device [rows, N] (plan dtype), read; or NULL.
+ *   out            device [rows, N] (plan dtype), written; may be res itself.
+ * The first call on a device raises the kernels' shared-memory limits; make it before
+ * capturing a stream into a CUDA graph.
+ */
+tdp_status tdp_matmul8(tdp_plan_t plan, int64_t rows, int32_t K, int32_t N, const uint8_t *x8, const float *x8_scale,
+                       const uint8_t *w8, const float *w8_scale, const void *bias, const void *res, void *out,
+                       tdp_stream_t stream);
+
+/* Rotary positions: how a head's pairs lie (i and i + rot/2, or 2 i and 2 i + 1), which place of a
+ * token's interval counts, and how frequencies are scaled for contexts longer than the trained one. */
+typedef enum { TDP_ROPE_HALF = 0, TDP_ROPE_INTERLEAVED = 1 } tdp_rope_layout;
+typedef enum { TDP_ROPE_START = 0, TDP_ROPE_MIDDLE = 1 } tdp_rope_at;
+typedef enum { TDP_ROPE_UNSCALED = 0, TDP_ROPE_LINEAR = 1, TDP_ROPE_NTK = 2, TDP_ROPE_YARN = 3 } tdp_rope_scaling;
+
+/* Largest head dimension of tdp_rope. */
+#define TDP_MAX_ROPE_DIM 256
+
+/* Strides count elements; the head dimension is contiguous.  head_dim and strides are multiples of 16 bytes,
+ * and a dimension of one ignores its stride.  out's rows and heads must not overlap. */
+typedef struct {
+    int32_t heads, head_dim;
+    int32_t rot;                /* leading values of a head that turn (even); the rest is copied */
+    int32_t layout;             /* tdp_rope_layout */
+    int32_t at;                 /* tdp_rope_at */
+    float scale;                /* factor of cos and sin */
+    int64_t x_row, x_head;      /* from one tile-major row / head to the next */
+    int64_t out_row, out_head;
+} tdp_rope_shape;
+
+/*
+ * tdp_rope_freqs -- frequencies of a head's pairs over three axes (host only).
+ *
+ * Axis a has pairs[a] pairs, axis 0's first: f_i = base^(-i / pairs[a]), i = 0..pairs[a]-1.  Scaled by `factor` >= 1:
+ *   linear  f / factor (Chen et al., "Extending context window of large language models via positional
+ *           interpolation", 2023);
+ *   NTK     base * factor^(n / (n - 1)) for base, n = pairs[a]: the lowest frequency falls by factor;
+ *   YaRN    f * k + f / factor * (1 - k), k = clamp((length f / 2 pi - 1) / 31, 0, 1), and scale = 0.1 ln factor + 1
+ *           (Peng et al., "YaRN: efficient context window extension of large language models", 2023).
+ *   freq, axis   [pairs[0] + pairs[1] + pairs[2]], written.   scale  written (1 but for YaRN).
+ */
+tdp_status tdp_rope_freqs(const int32_t *pairs, double base, int32_t scaling, double factor, double length, double *freq,
+                          int32_t *axis, float *scale);
+
+/*
+ * tdp_rope_table -- the table that tdp_rope reads (host only; the caller copies it to the device).
+ *
+ *   freq   [pairs] radians a position, at most 2^20 in magnitude.   axis  [pairs] 0, 1 or 2.
+ *   table  int64 [pairs], written: freq / 4 pi, modulo 1, in 2^-64, the axis in its two lowest bits.
+ */
+tdp_status tdp_rope_table(int32_t pairs, const double *freq, const int32_t *axis, int64_t *table);
+
+/*
+ * tdp_rope, tdp_rope_grad -- rotary positions on tile-major rows, and their gradient.
+ *
+ * Pair i, (a, b), of every head of the row of token j of (tile t, item b), p the token's position (start or
+ * middle of its interval) on the pair's axis:
+ *   a' = scale * (a cos(p f_i) - b sin(p f_i)),  b' = scale * (a sin(p f_i) + b cos(p f_i));
+ * the gradient turns dout by -p f_i.  Angles are exact to 2^-30 turns at any int32 positions.
+ *
+ *   x, out     device [R, heads, head_dim] by their strides (plan dtype); out may be x itself with the same
+ *              strides, and must not overlap it otherwise.
+ *   Q          device tile-major positions from tdp_split (int32, B * total_tile_tokens * 6), read.  Tokens of
+ *              a plan with one tile a dimension have positions [B, 3, T, 2], conditioning tokens among them.
+ *   table      device int64 [rot / 2] from tdp_rope_table, read.
+ */
+tdp_status tdp_rope(tdp_plan_t plan, const tdp_rope_shape *a, const void *x, const int32_t *Q, const int64_t *table, void *out,
+                    tdp_stream_t stream);
+tdp_status tdp_rope_grad(tdp_plan_t plan, const tdp_rope_shape *a, const void *dout, const int32_t *Q, const int64_t *table,
+                         void *dx, tdp_stream_t stream);
+
 /*
  * Plan helpers (host only, no CUDA call).
  *
