@@ -170,6 +170,191 @@ tdp_matmul8_tile_kernel(const __grid_constant__ args a, const __grid_constant__ 
     if (warp == 5) tmem_free(tm, kCols);
 }
 
+// Tiles of 256 rows by 256 channels, each by a pair of blocks (cta_group::2), in turn.
+//
+// Each block brings 128 rows and 128 channels of a stage, and holds the sums of its rows against all 256 channels: half the
+// shared-memory and L2 traffic of tiles that one block holds alone.  Warp 0 loads, warp 1 of the pair's first block issues the
+// products of both, warps 4-7 take the sums out of one accumulator, a row a thread, while the next tile's are made in the other.
+struct pair_smem {
+    static constexpr int kStage = 32768;
+    static constexpr int kStages = 5;
+    static constexpr int kOut = 16384;          // a panel of outputs on its way to memory: 128 rows of 128 bytes
+    static constexpr int kBytes = 1024 + kStages * kStage + 2 * kOut;
+};
+constexpr int kPairThreads = 256;
+
+template <int BF16>
+__global__ void __launch_bounds__(kPairThreads, 1)
+tdp_matmul8_pair_kernel(const __grid_constant__ args a, const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_w,
+                        const __grid_constant__ CUtensorMap map_o)
+{
+    using SM = pair_smem;
+    using E = tdp_elem<BF16>;
+    using T = typename E::type;
+    constexpr int NST = SM::kStages;
+    extern __shared__ unsigned char raw[];
+    __shared__ uint64_t bar_mem[2 * NST + 5];
+    __shared__ __align__(16) float scales[2][2][256];        // of two tiles: channels' scales and bias
+    __shared__ uint32_t tmem_slot;
+    __shared__ int dead_flag;
+    volatile int *dead = &dead_flag;
+    const uint32_t base = (smem_u32(raw) + 1023u) & ~1023u, out_s = base + NST * SM::kStage;
+    const uint32_t full = smem_u32(bar_mem), empty = full + 8 * NST, sums = empty + 8 * NST, taken = sums + 16, drain = taken + 16;
+    const int32_t warp = warp_id(), lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_rank();
+    if (warp == 2) pair_alloc(smem_u32(&tmem_slot), 512);
+    if (threadIdx.x == 0) {
+        dead_flag = 0;
+        for (int i = 0; i < 2 * NST; ++i) mbar_init(full + 8 * i, 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(sums + 8 * i, 1);
+            mbar_init(taken + 8 * i, 8);        // the four warps of both blocks
+        }
+        mbar_init(drain, 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    fence_before();
+    __syncthreads();
+    cluster_sync();
+    fence_after();
+    const uint32_t tm = tmem_slot;
+    tdp_pdl_trigger();
+    tdp_pdl_wait();
+
+    const int32_t first = blockIdx.x >> 1, step = gridDim.x >> 1;
+    bool ok = true;
+    if (warp == 0) {
+        const uint32_t lead = at_rank(full, 0);
+        uint32_t i = 0;
+#pragma unroll 1
+        for (int32_t t = first; t < a.tiles && ok; t += step) {
+            const int32_t row = (t / a.tiles_c) * 256 + rank * 128, ch = (t % a.tiles_c) * 256 + rank * 128;
+#pragma unroll 1
+            for (int32_t k = 0; k < a.kb; ++k, ++i) {
+                const uint32_t st = i % NST, to = base + st * SM::kStage;
+                if (!(ok = mbar_wait(empty + 8 * st, ((i / NST) & 1) ^ 1, dead))) break;
+                if (elect_one()) {
+                    if (rank == 0) mbar_expect(full + 8 * st, 2 * SM::kStage);      // both blocks' loads complete here
+                    pair_load2(to, &map_x, lead + 8 * st, k * kK, row);
+                    pair_load2(to + 16384, &map_w, lead + 8 * st, k * kK, ch);
+                }
+                __syncwarp();
+            }
+        }
+        // what has been loaded has been used, and so has landed
+        for (uint32_t j = i > NST ? i - NST : 0; j < i; ++j) landed(empty + 8 * (j % NST), (j / NST) & 1);
+    } else if (warp == 1 && rank == 0) {
+        constexpr uint32_t id = idesc8(256, 256);
+        uint32_t i = 0, n = 0;
+#pragma unroll 1
+        for (int32_t t = first; t < a.tiles && ok; t += step, ++n) {
+            const uint32_t buf = n & 1;
+            if (!(ok = mbar_wait(taken + 8 * buf, ((n >> 1) & 1) ^ 1, dead))) break;
+            fence_after();
+#pragma unroll 1
+            for (int32_t k = 0; k < a.kb; ++k, ++i) {
+                const uint32_t st = i % NST;
+                if (!(ok = mbar_wait(full + 8 * st, (i / NST) & 1, dead))) break;
+                fence_after();
+                if (elect_one()) {
+                    const uint32_t x = desc_rows(base + st * SM::kStage), w = desc_rows(base + st * SM::kStage + 16384);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) pair_mma8(tm + 256 * buf, x + 2 * j, w + 2 * j, id, k > 0 || j > 0);
+                    pair_commit(empty + 8 * st);
+                    if (k == a.kb - 1) pair_commit(sums + 8 * buf);
+                }
+                __syncwarp();
+            }
+        }
+        if (elect_one()) pair_commit(drain);
+        __syncwarp();
+        landed(drain, 0);
+    } else if (warp >= 4) {
+        const int32_t r = threadIdx.x & 127;
+        const uint32_t lanes = tm + ((uint32_t)(warp & 3) << 21);
+        constexpr int W = BF16 ? 64 : 32;       // channels of a panel
+        uint32_t n = 0, panel = 0;
+#pragma unroll 1
+        for (int32_t t = first; t < a.tiles; t += step, ++n) {
+            const uint32_t buf = n & 1;
+            const int32_t row0 = (t / a.tiles_c) * 256 + rank * 128, ch0 = (t % a.tiles_c) * 256;
+            const int64_t row = row0 + r;
+            const bool on = row < a.rows;
+            const float x = on ? __ldcg(a.xs + row) : 0.f;
+#pragma unroll
+            for (int c = r; c < 256; c += 128) {
+                const bool in = ch0 + c < a.N;
+                scales[buf][0][c] = in ? __ldcg(a.ws + ch0 + c) : 0.f;
+                scales[buf][1][c] = in && a.bias ? (float)static_cast<const T *>(a.bias)[ch0 + c] : 0.f;
+            }
+            group_sync(1);          // the other buffer of scales is written next, one barrier from here
+            if (ok) ok = mbar_wait(sums + 8 * buf, (n >> 1) & 1, dead);
+            ok = __all_sync(~0u, ok && !*dead);
+            fence_after();
+            // panels with anything in them: each is stored, so that the one before the last is free
+            const int32_t end = row0 < a.rows ? min(256, a.N - ch0) : 0;
+            auto take = [&] {
+                fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_at(at_rank(taken + 8 * buf, 0));
+            };
+            if (end == 0) take();
+#pragma unroll 1
+            for (int c0 = 0; c0 < end; c0 += W, panel ^= 1) {
+                uint32_t v[W];
+                tmem_ld32(lanes + 256 * buf + c0, v);
+                if (BF16) tmem_ld32(lanes + 256 * buf + c0 + 32, v + W - 32);
+                uint4 s[8];
+                if (a.res) {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const int32_t ch = ch0 + c0 + j * E::kVec;
+                        s[j] = on && ch < a.N ? *reinterpret_cast<const uint4 *>(static_cast<const T *>(a.res) + row * a.N + ch) : make_uint4(0, 0, 0, 0);
+                    }
+                }
+                tmem_wait_ld();
+                tmem_have32(v);
+                if (BF16) tmem_have32(v + W - 32);
+                if (c0 + W >= end) take();
+                if (r == 0) tma_store_read_but_one();       // the panel has left
+                group_sync(1);
+                const uint32_t to = out_s + panel * SM::kOut;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    float f[E::kVec], g[E::kVec];
+                    if (a.res) E::unpack(s[j], g);
+#pragma unroll
+                    for (int q = 0; q < E::kVec; q += 4) {
+                        const float4 w = *reinterpret_cast<const float4 *>(&scales[buf][0][c0 + j * E::kVec + q]);
+                        const float4 b = *reinterpret_cast<const float4 *>(&scales[buf][1][c0 + j * E::kVec + q]);
+                        const uint32_t *u = v + j * E::kVec + q;
+                        f[q] = fmaf(__uint_as_float(u[0]) * x, w.x, b.x);
+                        f[q + 1] = fmaf(__uint_as_float(u[1]) * x, w.y, b.y);
+                        f[q + 2] = fmaf(__uint_as_float(u[2]) * x, w.z, b.z);
+                        f[q + 3] = fmaf(__uint_as_float(u[3]) * x, w.w, b.w);
+                    }
+#pragma unroll
+                    for (int q = 0; q < E::kVec; ++q) {
+                        if (a.res) f[q] += g[q];
+                        if (!ok) f[q] = NAN;
+                    }
+                    const uint4 p = E::pack(f);
+                    const uint32_t o[4] = {p.x, p.y, p.z, p.w};
+                    st_shared16(to + panel_off(r, j), o);
+                }
+                fence_async();
+                group_sync(1);
+                if (r == 0) tma_store2(&map_o, to, ch0 + c0, row0);
+            }
+        }
+        if (r == 0) tma_store_done();
+    }
+    __syncwarp();
+    fence_before();
+    cluster_sync();         // neither block leaves, or frees its sums, while the other's products or arrivals may come
+    if (warp == 2) pair_free(tm, 512);
+}
+
 }  // namespace tdp_m8
 
 namespace {
@@ -185,6 +370,17 @@ bool map8(CUtensorMap *map, const void *p, int64_t K, int64_t rows, int box)
     const cuuint32_t b[2] = {(cuuint32_t)kK, (cuuint32_t)box}, one[2] = {1, 1};
     return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(p), extent, stride, b, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
                   CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Map of the outputs: boxes of 128 bytes by 128 rows.
+bool map_out(CUtensorMap *map, void *p, int bf16, int64_t N, int64_t rows)
+{
+    PFN_cuTensorMapEncodeTiled_v12000 encode = tdp_encode_tiled();
+    if (!encode) return false;
+    const cuuint64_t extent[2] = {(cuuint64_t)N, (cuuint64_t)rows}, stride[1] = {(cuuint64_t)N * (bf16 ? 2 : 4)};
+    const cuuint32_t b[2] = {bf16 ? 64u : 32u, 128}, one[2] = {1, 1};
+    return encode(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, p, extent, stride, b, one,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 // Raise a kernel's dynamic shared-memory limit once per device (`done`: one flag each).
@@ -236,8 +432,23 @@ cudaError_t tile_launch(const args &a, const void *w8, const void *x8, int64_t K
 }
 
 template <int BF16>
+cudaError_t pair_launch(args a, const void *w8, const void *x8, int64_t K, cudaStream_t s)
+{
+    static std::atomic<bool> done[64];
+    constexpr size_t bytes = pair_smem::kBytes;
+    cudaError_t e = allow_smem(tdp_matmul8_pair_kernel<BF16>, bytes, done);
+    CUtensorMap w, x, o;
+    if (e == cudaSuccess && (!map8(&w, w8, K, a.N, 128) || !map8(&x, x8, K, a.rows, 128) || !map_out(&o, a.out, BF16, a.N, a.rows))) e = cudaErrorInvalidValue;
+    if (e != cudaSuccess) return e;
+    a.tiles_c = (a.N + 255) / 256;
+    a.tiles = a.tiles_c * (int32_t)((a.rows + 255) / 256);
+    return launch_clusters(tdp_matmul8_pair_kernel<BF16>, 2 * std::min(a.tiles, 76), 2, kPairThreads, bytes, s, a, x, w, o);
+}
+
+template <int BF16>
 cudaError_t matmul8(const args &a, const void *w8, const void *x8, int64_t K, cudaStream_t s)
 {
+    if ((a.rows + 255) / 256 * ((a.N + 255) / 256) >= 76) return pair_launch<BF16>(a, w8, x8, K, s);
     return a.rows <= 16 ? tile_launch<BF16, 16>(a, w8, x8, K, s) : a.rows <= 64 ? tile_launch<BF16, 64>(a, w8, x8, K, s)
                                                                                 : tile_launch<BF16, 128>(a, w8, x8, K, s);
 }
@@ -261,7 +472,7 @@ extern "C" tdp_status tdp_matmul8(tdp_plan_t plan, int64_t rows, int32_t K, int3
         !tdp_aligned(x8_scale, 4) || !tdp_aligned(w8_scale, 16))
         return tdp_fail(TDP_ERR_MISALIGNED, "rows, w8_scale and bias need 16-byte, x8_scale 4-byte alignment");
     if ((rows + 127) / 128 * ((N + 127) / 128) > (1 << 28)) return tdp_fail(TDP_ERR_TOO_LARGE, "rows * N above 2^42");
-    args a = {x8_scale, w8_scale, bias, res, out, rows, N, (K + kK - 1) / kK, (N + 127) / 128};
+    args a = {x8_scale, w8_scale, bias, res, out, rows, N, (K + kK - 1) / kK, (N + 127) / 128, 0};
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     const cudaError_t err = g.dtype == TDP_BF16 ? matmul8<1>(a, w8, x8, K, s) : matmul8<0>(a, w8, x8, K, s);
     return err == cudaSuccess ? tdp_ok() : tdp_fail(TDP_ERR_CUDA, cudaGetErrorString(err));

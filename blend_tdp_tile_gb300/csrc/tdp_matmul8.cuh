@@ -17,6 +17,7 @@ struct args {
     int64_t rows;
     int32_t N, kb;              // channels, stages of K in all
     int32_t tiles_c;            // channel tiles
+    int32_t tiles;              // pairs: tiles in all
 };
 
 // Instruction descriptor: e4m3 x e4m3 -> fp32, M x N, both operands by rows.
@@ -63,6 +64,57 @@ __device__ __forceinline__ uint32_t at_rank(uint32_t addr, uint32_t rank)
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
     return r;
 }
+
+// Arrives at a barrier of any block of the cluster.
+__device__ __forceinline__ void mbar_arrive_at(uint32_t cluster_bar)
+{
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
+}
+
+// ------------------------------------------------------------------ pairs of blocks (cta_group::2)
+__device__ __forceinline__ void pair_alloc(uint32_t slot, uint32_t cols)
+{
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(slot), "r"(cols) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void pair_free(uint32_t addr, uint32_t cols)
+{
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(cols) : "memory");
+}
+// Box -> this block's shared memory, completing on a barrier of either block of the pair.
+__device__ __forceinline__ void pair_load2(uint32_t dst, const CUtensorMap *map, uint32_t cluster_bar, int32_t x, int32_t y)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(cluster_bar), "r"(x), "r"(y)
+        : "memory");
+}
+// The product of the pair's tiles: each block holds half of A's rows, of B's and of D's, at the same addresses.
+__device__ __forceinline__ void pair_mma8(uint32_t d, uint32_t a, uint32_t b, uint32_t id, uint32_t acc)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\tsetp.ne.b32 p, %4, 0;\n\tmov.b64 da, {%1, %5};\n\tmov.b64 db, {%2, %5};\n\t"
+        "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], da, db, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "r"(b), "r"(id), "r"(acc), "r"(kDescHi)
+        : "memory");
+}
+// One arrival at `bar` of both blocks when every product this thread has issued is done.
+__device__ __forceinline__ void pair_commit(uint32_t bar)
+{
+    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+                 "h"((uint16_t)3)
+                 : "memory");
+}
+// Shared -> box of a tensor map.
+__device__ __forceinline__ void tma_store2(const CUtensorMap *map, uint32_t src, int32_t x, int32_t y)
+{
+    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];" ::"l"(reinterpret_cast<uint64_t>(map)),
+                 "r"(src), "r"(x), "r"(y)
+                 : "memory");
+    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+// All but the last store have been read.
+__device__ __forceinline__ void tma_store_read_but_one() { asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory"); }
 
 // Waits, with a limit, for what is on its way to `bar`.
 __device__ __forceinline__ void landed(uint32_t bar, uint32_t parity)

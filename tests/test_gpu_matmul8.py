@@ -56,7 +56,8 @@ def _check(tdp, dtype, rows, K, N, bias=True, res=True):
 
 
 SIZES = [(1, 16, 8), (8, 4096, 4096), (3, 32, 24), (16, 1040, 136), (17, 128, 128), (40, 48, 1000), (64, 272, 264), (65, 4096, 72), (100, 96, 2048),
-         (128, 512, 256), (129, 1040, 1004), (300, 2048, 640), (1237, 1040, 1004), (700, 16, 3000), (4000, 640, 520)]
+         (128, 512, 256), (129, 1040, 1004), (300, 2048, 640), (1237, 1040, 1004), (700, 16, 3000), (4000, 640, 520), (19500, 256, 264),
+         (5121, 144, 1000), (10000, 2048, 512)]
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
