@@ -174,14 +174,15 @@ tdp_matmul8_tile_kernel(const __grid_constant__ args a, const __grid_constant__ 
 //
 // Each block brings 128 rows and 128 channels of a stage, and holds the sums of its rows against all 256 channels: half the
 // shared-memory and L2 traffic of tiles that one block holds alone.  Warp 0 loads, warp 1 of the pair's first block issues the
-// products of both, warps 4-7 take the sums out of one accumulator, a row a thread, while the next tile's are made in the other.
+// products of both, warps 4-7 and 8-11 take the sums out of one accumulator, a row and 128 channels a thread, while the next
+// tile's are made in the other.
 struct pair_smem {
     static constexpr int kStage = 32768;
     static constexpr int kStages = 5;
     static constexpr int kOut = 16384;          // a panel of outputs on its way to memory: 128 rows of 128 bytes
     static constexpr int kBytes = 1024 + kStages * kStage + 2 * kOut;
 };
-constexpr int kPairThreads = 256;
+constexpr int kPairThreads = 384;
 
 template <int BF16>
 __global__ void __launch_bounds__(kPairThreads, 1)
@@ -194,7 +195,7 @@ tdp_matmul8_pair_kernel(const __grid_constant__ args a, const __grid_constant__ 
     constexpr int NST = SM::kStages;
     extern __shared__ unsigned char raw[];
     __shared__ uint64_t bar_mem[2 * NST + 5];
-    __shared__ __align__(16) float scales[2][2][256];        // of two tiles: channels' scales and bias
+    __shared__ __align__(16) float scales[2][2][256];        // channels' scales and bias, of two tiles
     __shared__ uint32_t tmem_slot;
     __shared__ int dead_flag;
     volatile int *dead = &dead_flag;
@@ -208,7 +209,7 @@ tdp_matmul8_pair_kernel(const __grid_constant__ args a, const __grid_constant__ 
         for (int i = 0; i < 2 * NST; ++i) mbar_init(full + 8 * i, 1);
         for (int i = 0; i < 2; ++i) {
             mbar_init(sums + 8 * i, 1);
-            mbar_init(taken + 8 * i, 8);        // the four warps of both blocks
+            mbar_init(taken + 8 * i, 16);       // the eight warps of both blocks
         }
         mbar_init(drain, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -270,37 +271,44 @@ tdp_matmul8_pair_kernel(const __grid_constant__ args a, const __grid_constant__ 
         __syncwarp();
         landed(drain, 0);
     } else if (warp >= 4) {
-        const int32_t r = threadIdx.x & 127;
-        const uint32_t lanes = tm + ((uint32_t)(warp & 3) << 21);
+        const int32_t r = threadIdx.x & 127, half = (warp - 4) >> 2;
+        const uint32_t lanes = tm + ((uint32_t)(warp & 3) << 21) + 128 * half, to = out_s + half * SM::kOut;
         constexpr int W = BF16 ? 64 : 32;       // channels of a panel
-        uint32_t n = 0, panel = 0;
+        // A tile's scales and bias are asked for while the tile before is worked on.
+        float x, w, b;
+        auto ask = [&](int32_t t) {
+            const int64_t row = (int64_t)(t / a.tiles_c) * 256 + rank * 128 + r;
+            const int32_t ch = (t % a.tiles_c) * 256 + 128 * half + r;
+            const bool in = ch < a.N;
+            x = row < a.rows ? __ldcg(a.xs + row) : 0.f;
+            w = in ? __ldcg(a.ws + ch) : 0.f;
+            b = in && a.bias ? (float)static_cast<const T *>(a.bias)[ch] : 0.f;
+        };
+        if (first < a.tiles) ask(first);
+        uint32_t n = 0;
 #pragma unroll 1
         for (int32_t t = first; t < a.tiles; t += step, ++n) {
             const uint32_t buf = n & 1;
-            const int32_t row0 = (t / a.tiles_c) * 256 + rank * 128, ch0 = (t % a.tiles_c) * 256;
+            const int32_t row0 = (t / a.tiles_c) * 256 + rank * 128, ch0 = (t % a.tiles_c) * 256 + 128 * half;
             const int64_t row = row0 + r;
             const bool on = row < a.rows;
-            const float x = on ? __ldcg(a.xs + row) : 0.f;
-#pragma unroll
-            for (int c = r; c < 256; c += 128) {
-                const bool in = ch0 + c < a.N;
-                scales[buf][0][c] = in ? __ldcg(a.ws + ch0 + c) : 0.f;
-                scales[buf][1][c] = in && a.bias ? (float)static_cast<const T *>(a.bias)[ch0 + c] : 0.f;
-            }
-            group_sync(1);          // the other buffer of scales is written next, one barrier from here
+            const float xs = x;
+            scales[buf][0][128 * half + r] = w;
+            scales[buf][1][128 * half + r] = b;
+            if (t + step < a.tiles) ask(t + step);
+            group_sync(1 + half);           // the other buffer of scales is written next, one barrier from here
             if (ok) ok = mbar_wait(sums + 8 * buf, (n >> 1) & 1, dead);
             ok = __all_sync(~0u, ok && !*dead);
             fence_after();
-            // panels with anything in them: each is stored, so that the one before the last is free
-            const int32_t end = row0 < a.rows ? min(256, a.N - ch0) : 0;
+            const int32_t end = row0 < a.rows ? min(128, a.N - ch0) : 0;
             auto take = [&] {
                 fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive_at(at_rank(taken + 8 * buf, 0));
             };
-            if (end == 0) take();
+            if (end <= 0) take();
 #pragma unroll 1
-            for (int c0 = 0; c0 < end; c0 += W, panel ^= 1) {
+            for (int c0 = 0; c0 < end; c0 += W) {
                 uint32_t v[W];
                 tmem_ld32(lanes + 256 * buf + c0, v);
                 if (BF16) tmem_ld32(lanes + 256 * buf + c0 + 32, v + W - 32);
@@ -316,22 +324,21 @@ tdp_matmul8_pair_kernel(const __grid_constant__ args a, const __grid_constant__ 
                 tmem_have32(v);
                 if (BF16) tmem_have32(v + W - 32);
                 if (c0 + W >= end) take();
-                if (r == 0) tma_store_read_but_one();       // the panel has left
-                group_sync(1);
-                const uint32_t to = out_s + panel * SM::kOut;
+                if (r == 0) tma_store_read();               // the panel before has left
+                group_sync(1 + half);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
                     float f[E::kVec], g[E::kVec];
                     if (a.res) E::unpack(s[j], g);
 #pragma unroll
                     for (int q = 0; q < E::kVec; q += 4) {
-                        const float4 w = *reinterpret_cast<const float4 *>(&scales[buf][0][c0 + j * E::kVec + q]);
-                        const float4 b = *reinterpret_cast<const float4 *>(&scales[buf][1][c0 + j * E::kVec + q]);
+                        const float4 w4 = *reinterpret_cast<const float4 *>(&scales[buf][0][128 * half + c0 + j * E::kVec + q]);
+                        const float4 b4 = *reinterpret_cast<const float4 *>(&scales[buf][1][128 * half + c0 + j * E::kVec + q]);
                         const uint32_t *u = v + j * E::kVec + q;
-                        f[q] = fmaf(__uint_as_float(u[0]) * x, w.x, b.x);
-                        f[q + 1] = fmaf(__uint_as_float(u[1]) * x, w.y, b.y);
-                        f[q + 2] = fmaf(__uint_as_float(u[2]) * x, w.z, b.z);
-                        f[q + 3] = fmaf(__uint_as_float(u[3]) * x, w.w, b.w);
+                        f[q] = fmaf(__uint_as_float(u[0]) * xs, w4.x, b4.x);
+                        f[q + 1] = fmaf(__uint_as_float(u[1]) * xs, w4.y, b4.y);
+                        f[q + 2] = fmaf(__uint_as_float(u[2]) * xs, w4.z, b4.z);
+                        f[q + 3] = fmaf(__uint_as_float(u[3]) * xs, w4.w, b4.w);
                     }
 #pragma unroll
                     for (int q = 0; q < E::kVec; ++q) {
@@ -343,7 +350,7 @@ tdp_matmul8_pair_kernel(const __grid_constant__ args a, const __grid_constant__ 
                     st_shared16(to + panel_off(r, j), o);
                 }
                 fence_async();
-                group_sync(1);
+                group_sync(1 + half);
                 if (r == 0) tma_store2(&map_o, to, ch0 + c0, row0);
             }
         }
