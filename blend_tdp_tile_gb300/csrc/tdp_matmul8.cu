@@ -174,15 +174,15 @@ tdp_matmul8_tile_kernel(const __grid_constant__ args a, const __grid_constant__ 
 //
 // Each block brings 128 rows and 128 channels of a stage, and holds the sums of its rows against all 256 channels: half the
 // shared-memory and L2 traffic of tiles that one block holds alone.  Warp 0 loads, warp 1 of the pair's first block issues the
-// products of both, warps 4-7 and 8-11 take the sums out of one accumulator, a row and 128 channels a thread, while the next
-// tile's are made in the other.
+// products of both, four warpgroups behind them take the sums out of one accumulator, a row and 64 channels a thread, while
+// the next tile's are made in the other.
 struct pair_smem {
     static constexpr int kStage = 32768;
-    static constexpr int kStages = 5;
+    static constexpr int kStages = 4;
     static constexpr int kOut = 16384;          // a panel of outputs on its way to memory: 128 rows of 128 bytes
-    static constexpr int kBytes = 1024 + kStages * kStage + 2 * kOut;
+    static constexpr int kBytes = 1024 + kStages * kStage + 4 * kOut;
 };
-constexpr int kPairThreads = 384;
+constexpr int kPairThreads = 640;
 
 template <int BF16>
 __global__ void __launch_bounds__(kPairThreads, 1)
@@ -209,7 +209,7 @@ tdp_matmul8_pair_kernel(const __grid_constant__ args a, const __grid_constant__ 
         for (int i = 0; i < 2 * NST; ++i) mbar_init(full + 8 * i, 1);
         for (int i = 0; i < 2; ++i) {
             mbar_init(sums + 8 * i, 1);
-            mbar_init(taken + 8 * i, 16);       // the eight warps of both blocks
+            mbar_init(taken + 8 * i, 32);       // sixteen warps of either block
         }
         mbar_init(drain, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -271,15 +271,14 @@ tdp_matmul8_pair_kernel(const __grid_constant__ args a, const __grid_constant__ 
         __syncwarp();
         landed(drain, 0);
     } else if (warp >= 4) {
-        const int32_t r = threadIdx.x & 127, half = (warp - 4) >> 2;
-        const uint32_t lanes = tm + ((uint32_t)(warp & 3) << 21) + 128 * half, to = out_s + half * SM::kOut;
-        constexpr int W = BF16 ? 64 : 32;       // channels of a panel
+        const int32_t r = threadIdx.x & 127, part = (warp - 4) >> 2;
+        const uint32_t lanes = tm + ((uint32_t)(warp & 3) << 21) + 64 * part, to = out_s + part * SM::kOut;
         // A tile's scales and bias are asked for while the tile before is worked on.
         float x, w, b;
         auto ask = [&](int32_t t) {
             const int64_t row = (int64_t)(t / a.tiles_c) * 256 + rank * 128 + r;
-            const int32_t ch = (t % a.tiles_c) * 256 + 128 * half + r;
-            const bool in = ch < a.N;
+            const int32_t ch = (t % a.tiles_c) * 256 + 64 * part + r;
+            const bool in = r < 64 && ch < a.N;
             x = row < a.rows ? __ldcg(a.xs + row) : 0.f;
             w = in ? __ldcg(a.ws + ch) : 0.f;
             b = in && a.bias ? (float)static_cast<const T *>(a.bias)[ch] : 0.f;
@@ -289,18 +288,21 @@ tdp_matmul8_pair_kernel(const __grid_constant__ args a, const __grid_constant__ 
 #pragma unroll 1
         for (int32_t t = first; t < a.tiles; t += step, ++n) {
             const uint32_t buf = n & 1;
-            const int32_t row0 = (t / a.tiles_c) * 256 + rank * 128, ch0 = (t % a.tiles_c) * 256 + 128 * half;
+            const int32_t row0 = (t / a.tiles_c) * 256 + rank * 128, ch0 = (t % a.tiles_c) * 256 + 64 * part;
             const int64_t row = row0 + r;
             const bool on = row < a.rows;
             const float xs = x;
-            scales[buf][0][128 * half + r] = w;
-            scales[buf][1][128 * half + r] = b;
+            if (r < 64) {
+                scales[buf][0][64 * part + r] = w;
+                scales[buf][1][64 * part + r] = b;
+            }
             if (t + step < a.tiles) ask(t + step);
-            group_sync(1 + half);           // the other buffer of scales is written next, one barrier from here
+            group_sync(1 + part);           // the other buffer of scales is written next, one barrier from here
             if (ok) ok = mbar_wait(sums + 8 * buf, (n >> 1) & 1, dead);
             ok = __all_sync(~0u, ok && !*dead);
             fence_after();
-            const int32_t end = row0 < a.rows ? min(128, a.N - ch0) : 0;
+            const uint64_t x2 = ok ? pair(xs, xs) : pair(NAN, NAN);
+            const int32_t end = row0 < a.rows ? min(64, a.N - ch0) : 0;
             auto take = [&] {
                 fence_before();
                 __syncwarp();
@@ -308,50 +310,50 @@ tdp_matmul8_pair_kernel(const __grid_constant__ args a, const __grid_constant__ 
             };
             if (end <= 0) take();
 #pragma unroll 1
-            for (int c0 = 0; c0 < end; c0 += W) {
-                uint32_t v[W];
+            for (int c0 = 0; c0 < end; c0 += 32) {
+                constexpr int NV = 32 / E::kVec;        // vectors of the 32 channels
+                uint32_t v[32];
                 tmem_ld32(lanes + 256 * buf + c0, v);
-                if (BF16) tmem_ld32(lanes + 256 * buf + c0 + 32, v + W - 32);
-                uint4 s[8];
+                uint4 s[NV];
                 if (a.res) {
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) {
+                    for (int j = 0; j < NV; ++j) {
                         const int32_t ch = ch0 + c0 + j * E::kVec;
                         s[j] = on && ch < a.N ? *reinterpret_cast<const uint4 *>(static_cast<const T *>(a.res) + row * a.N + ch) : make_uint4(0, 0, 0, 0);
                     }
                 }
                 tmem_wait_ld();
                 tmem_have32(v);
-                if (BF16) tmem_have32(v + W - 32);
-                if (c0 + W >= end) take();
-                if (r == 0) tma_store_read();               // the panel before has left
-                group_sync(1 + half);
+                if (c0 + 32 >= end) take();
+                if (!BF16 || c0 == 0) {
+                    if (r == 0) tma_store_read();           // the panel before has left
+                    group_sync(1 + part);
+                }
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
+                for (int j = 0; j < NV; ++j) {
                     float f[E::kVec], g[E::kVec];
                     if (a.res) E::unpack(s[j], g);
 #pragma unroll
                     for (int q = 0; q < E::kVec; q += 4) {
-                        const float4 w4 = *reinterpret_cast<const float4 *>(&scales[buf][0][128 * half + c0 + j * E::kVec + q]);
-                        const float4 b4 = *reinterpret_cast<const float4 *>(&scales[buf][1][128 * half + c0 + j * E::kVec + q]);
+                        const int c = 64 * part + c0 + j * E::kVec + q;
+                        const ulonglong2 w4 = *reinterpret_cast<const ulonglong2 *>(&scales[buf][0][c]), b4 = *reinterpret_cast<const ulonglong2 *>(&scales[buf][1][c]);
                         const uint32_t *u = v + j * E::kVec + q;
-                        f[q] = fmaf(__uint_as_float(u[0]) * xs, w4.x, b4.x);
-                        f[q + 1] = fmaf(__uint_as_float(u[1]) * xs, w4.y, b4.y);
-                        f[q + 2] = fmaf(__uint_as_float(u[2]) * xs, w4.z, b4.z);
-                        f[q + 3] = fmaf(__uint_as_float(u[3]) * xs, w4.w, b4.w);
+                        unpair(fma2(mul2(pair(__uint_as_float(u[0]), __uint_as_float(u[1])), x2), w4.x, b4.x), f[q], f[q + 1]);
+                        unpair(fma2(mul2(pair(__uint_as_float(u[2]), __uint_as_float(u[3])), x2), w4.y, b4.y), f[q + 2], f[q + 3]);
                     }
+                    if (a.res) {
 #pragma unroll
-                    for (int q = 0; q < E::kVec; ++q) {
-                        if (a.res) f[q] += g[q];
-                        if (!ok) f[q] = NAN;
+                        for (int q = 0; q < E::kVec; ++q) f[q] += g[q];
                     }
                     const uint4 p = E::pack(f);
                     const uint32_t o[4] = {p.x, p.y, p.z, p.w};
-                    st_shared16(to + panel_off(r, j), o);
+                    st_shared16(to + panel_off(r, (BF16 ? c0 / 8 : 0) + j), o);
                 }
-                fence_async();
-                group_sync(1 + half);
-                if (r == 0) tma_store2(&map_o, to, ch0 + c0, row0);
+                if (!BF16 || c0 + 32 >= end) {
+                    fence_async();
+                    group_sync(1 + part);
+                    if (r == 0) tma_store2(&map_o, to, BF16 ? ch0 : ch0 + c0, row0);
+                }
             }
         }
         if (r == 0) tma_store_done();
