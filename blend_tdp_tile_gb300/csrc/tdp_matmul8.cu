@@ -178,8 +178,8 @@ tdp_matmul8_tile_kernel(const __grid_constant__ args a, const __grid_constant__ 
 // the next tile's are made in the other.
 struct pair_smem {
     static constexpr int kStage = 32768;
-    static constexpr int kStages = 4;
-    static constexpr int kOut = 16384;          // a panel of outputs on its way to memory: 128 rows of 128 bytes
+    static constexpr int kStages = 5;
+    static constexpr int kOut = 8192;           // a panel of outputs on its way to memory: 128 rows of 64 bytes
     static constexpr int kBytes = 1024 + kStages * kStage + 4 * kOut;
 };
 constexpr int kPairThreads = 640;
@@ -273,6 +273,7 @@ tdp_matmul8_pair_kernel(const __grid_constant__ args a, const __grid_constant__ 
     } else if (warp >= 4) {
         const int32_t r = threadIdx.x & 127, part = (warp - 4) >> 2;
         const uint32_t lanes = tm + ((uint32_t)(warp & 3) << 21) + 64 * part, to = out_s + part * SM::kOut;
+        constexpr int W = BF16 ? 32 : 16;       // channels of a panel
         // A tile's scales and bias are asked for while the tile before is worked on.
         float x, w, b;
         auto ask = [&](int32_t t) {
@@ -310,27 +311,26 @@ tdp_matmul8_pair_kernel(const __grid_constant__ args a, const __grid_constant__ 
             };
             if (end <= 0) take();
 #pragma unroll 1
-            for (int c0 = 0; c0 < end; c0 += 32) {
-                constexpr int NV = 32 / E::kVec;        // vectors of the 32 channels
-                uint32_t v[32];
-                tmem_ld32(lanes + 256 * buf + c0, v);
-                uint4 s[NV];
+            for (int c0 = 0; c0 < end; c0 += W) {
+                uint32_t v[W];
+                if (BF16) tmem_ld32(lanes + 256 * buf + c0, v);
+                else tmem_ld16(lanes + 256 * buf + c0, v);
+                uint4 s[4];
                 if (a.res) {
 #pragma unroll
-                    for (int j = 0; j < NV; ++j) {
+                    for (int j = 0; j < 4; ++j) {
                         const int32_t ch = ch0 + c0 + j * E::kVec;
                         s[j] = on && ch < a.N ? *reinterpret_cast<const uint4 *>(static_cast<const T *>(a.res) + row * a.N + ch) : make_uint4(0, 0, 0, 0);
                     }
                 }
                 tmem_wait_ld();
-                tmem_have32(v);
-                if (c0 + 32 >= end) take();
-                if (!BF16 || c0 == 0) {
-                    if (r == 0) tma_store_read();           // the panel before has left
-                    group_sync(1 + part);
-                }
+                if (BF16) tmem_have32(v);
+                else tmem_have16(v);
+                if (c0 + W >= end) take();
+                if (r == 0) tma_store_read();           // the panel before has left
+                group_sync(1 + part);
 #pragma unroll
-                for (int j = 0; j < NV; ++j) {
+                for (int j = 0; j < 4; ++j) {
                     float f[E::kVec], g[E::kVec];
                     if (a.res) E::unpack(s[j], g);
 #pragma unroll
@@ -347,13 +347,11 @@ tdp_matmul8_pair_kernel(const __grid_constant__ args a, const __grid_constant__ 
                     }
                     const uint4 p = E::pack(f);
                     const uint32_t o[4] = {p.x, p.y, p.z, p.w};
-                    st_shared16(to + panel_off(r, (BF16 ? c0 / 8 : 0) + j), o);
+                    st_shared16(to + r * 64 + ((j ^ ((r >> 1) & 3)) << 4), o);      // the 64-byte swizzle of map_o
                 }
-                if (!BF16 || c0 + 32 >= end) {
-                    fence_async();
-                    group_sync(1 + part);
-                    if (r == 0) tma_store2(&map_o, to, BF16 ? ch0 : ch0 + c0, row0);
-                }
+                fence_async();
+                group_sync(1 + part);
+                if (r == 0) tma_store2(&map_o, to, ch0 + c0, row0);
             }
         }
         if (r == 0) tma_store_done();
@@ -381,15 +379,15 @@ bool map8(CUtensorMap *map, const void *p, int64_t K, int64_t rows, int box)
                   CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Map of the outputs: boxes of 128 bytes by 128 rows.
+// Map of the outputs: boxes of 64 bytes by 128 rows.
 bool map_out(CUtensorMap *map, void *p, int bf16, int64_t N, int64_t rows)
 {
     PFN_cuTensorMapEncodeTiled_v12000 encode = tdp_encode_tiled();
     if (!encode) return false;
     const cuuint64_t extent[2] = {(cuuint64_t)N, (cuuint64_t)rows}, stride[1] = {(cuuint64_t)N * (bf16 ? 2 : 4)};
-    const cuuint32_t b[2] = {bf16 ? 64u : 32u, 128}, one[2] = {1, 1};
+    const cuuint32_t b[2] = {bf16 ? 32u : 16u, 128}, one[2] = {1, 1};
     return encode(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, p, extent, stride, b, one,
-                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 // Raise a kernel's dynamic shared-memory limit once per device (`done`: one flag each).
