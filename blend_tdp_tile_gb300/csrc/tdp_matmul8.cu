@@ -179,8 +179,12 @@ tdp_matmul8_tile_kernel(const __grid_constant__ args a, const __grid_constant__ 
 struct pair_smem {
     static constexpr int kStage = 32768;
     static constexpr int kStages = 5;
-    static constexpr int kOut = 8192;           // a panel of outputs on its way to memory: 128 rows of 64 bytes
-    static constexpr int kBytes = 1024 + kStages * kStage + 4 * kOut;
+    static constexpr int kOut = 16384;          // two panels of outputs on their way to memory: 128 rows of 64 bytes
+    static constexpr int kScales = 2048;        // a tile's scales and bias of 256 channels
+    static constexpr int kBars = 8 * (2 * kStages + 5) + 8;
+    // all that a block may have but 768 bytes, which are for the start's rounding up to 1024
+    static constexpr int kBytes = 232448;
+    static_assert(kStages * kStage + 4 * kOut + kScales + kBars <= kBytes - 768, "room for the stages");
 };
 constexpr int kPairThreads = 640;
 
@@ -193,19 +197,18 @@ tdp_matmul8_pair_kernel(const __grid_constant__ args a, const __grid_constant__ 
     using E = tdp_elem<BF16>;
     using T = typename E::type;
     constexpr int NST = SM::kStages;
-    extern __shared__ unsigned char raw[];
-    __shared__ uint64_t bar_mem[2 * NST + 5];
-    __shared__ __align__(16) float scales[2][2][256];        // channels' scales and bias, of two tiles
-    __shared__ uint32_t tmem_slot;
-    __shared__ int dead_flag;
-    volatile int *dead = &dead_flag;
+    extern __shared__ __align__(1024) unsigned char raw[];
     const uint32_t base = (smem_u32(raw) + 1023u) & ~1023u, out_s = base + NST * SM::kStage;
-    const uint32_t full = smem_u32(bar_mem), empty = full + 8 * NST, sums = empty + 8 * NST, taken = sums + 16, drain = taken + 16;
+    unsigned char *tail = raw + (base - smem_u32(raw)) + NST * SM::kStage + 4 * SM::kOut;
+    float *scales = reinterpret_cast<float *>(tail);            // channels' scales, then their bias
+    volatile int *dead = reinterpret_cast<int *>(tail + SM::kScales);
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(tail + SM::kScales + 4);
+    const uint32_t full = smem_u32(tail + SM::kScales + 8), empty = full + 8 * NST, sums = empty + 8 * NST, taken = sums + 16, drain = taken + 16;
     const int32_t warp = warp_id(), lane = threadIdx.x & 31;
     const uint32_t rank = cluster_rank();
-    if (warp == 2) pair_alloc(smem_u32(&tmem_slot), 512);
+    if (warp == 2) pair_alloc(smem_u32(tmem_slot), 512);
     if (threadIdx.x == 0) {
-        dead_flag = 0;
+        *dead = 0;
         for (int i = 0; i < 2 * NST; ++i) mbar_init(full + 8 * i, 1);
         for (int i = 0; i < 2; ++i) {
             mbar_init(sums + 8 * i, 1);
@@ -218,7 +221,7 @@ tdp_matmul8_pair_kernel(const __grid_constant__ args a, const __grid_constant__ 
     __syncthreads();
     cluster_sync();
     fence_after();
-    const uint32_t tm = tmem_slot;
+    const uint32_t tm = *tmem_slot;
     tdp_pdl_trigger();
     tdp_pdl_wait();
 
@@ -273,7 +276,6 @@ tdp_matmul8_pair_kernel(const __grid_constant__ args a, const __grid_constant__ 
     } else if (warp >= 4) {
         const int32_t r = threadIdx.x & 127, part = (warp - 4) >> 2;
         const uint32_t lanes = tm + ((uint32_t)(warp & 3) << 21) + 64 * part, to = out_s + part * SM::kOut;
-        constexpr int W = BF16 ? 32 : 16;       // channels of a panel
         // A tile's scales and bias are asked for while the tile before is worked on.
         float x, w, b;
         auto ask = [&](int32_t t) {
@@ -285,7 +287,8 @@ tdp_matmul8_pair_kernel(const __grid_constant__ args a, const __grid_constant__ 
             b = in && a.bias ? (float)static_cast<const T *>(a.bias)[ch] : 0.f;
         };
         if (first < a.tiles) ask(first);
-        uint32_t n = 0;
+        uint32_t n = 0, panel = 0;
+        constexpr int W = BF16 ? 32 : 16;       // channels of a panel
 #pragma unroll 1
         for (int32_t t = first; t < a.tiles; t += step, ++n) {
             const uint32_t buf = n & 1;
@@ -294,11 +297,11 @@ tdp_matmul8_pair_kernel(const __grid_constant__ args a, const __grid_constant__ 
             const bool on = row < a.rows;
             const float xs = x;
             if (r < 64) {
-                scales[buf][0][64 * part + r] = w;
-                scales[buf][1][64 * part + r] = b;
+                scales[64 * part + r] = w;
+                scales[256 + 64 * part + r] = b;
             }
             if (t + step < a.tiles) ask(t + step);
-            group_sync(1 + part);           // the other buffer of scales is written next, one barrier from here
+            group_sync(1 + part);           // they are read before the panels' last barrier, and written behind it
             if (ok) ok = mbar_wait(sums + 8 * buf, (n >> 1) & 1, dead);
             ok = __all_sync(~0u, ok && !*dead);
             fence_after();
@@ -327,7 +330,7 @@ tdp_matmul8_pair_kernel(const __grid_constant__ args a, const __grid_constant__ 
                 if (BF16) tmem_have32(v);
                 else tmem_have16(v);
                 if (c0 + W >= end) take();
-                if (r == 0) tma_store_read();           // the panel before has left
+                if (r == 0) tma_store_read_but_one();   // the panel before the last has left
                 group_sync(1 + part);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
@@ -336,7 +339,7 @@ tdp_matmul8_pair_kernel(const __grid_constant__ args a, const __grid_constant__ 
 #pragma unroll
                     for (int q = 0; q < E::kVec; q += 4) {
                         const int c = 64 * part + c0 + j * E::kVec + q;
-                        const ulonglong2 w4 = *reinterpret_cast<const ulonglong2 *>(&scales[buf][0][c]), b4 = *reinterpret_cast<const ulonglong2 *>(&scales[buf][1][c]);
+                        const ulonglong2 w4 = *reinterpret_cast<const ulonglong2 *>(scales + c), b4 = *reinterpret_cast<const ulonglong2 *>(scales + 256 + c);
                         const uint32_t *u = v + j * E::kVec + q;
                         unpair(fma2(mul2(pair(__uint_as_float(u[0]), __uint_as_float(u[1])), x2), w4.x, b4.x), f[q], f[q + 1]);
                         unpair(fma2(mul2(pair(__uint_as_float(u[2]), __uint_as_float(u[3])), x2), w4.y, b4.y), f[q + 2], f[q + 3]);
@@ -347,11 +350,12 @@ tdp_matmul8_pair_kernel(const __grid_constant__ args a, const __grid_constant__ 
                     }
                     const uint4 p = E::pack(f);
                     const uint32_t o[4] = {p.x, p.y, p.z, p.w};
-                    st_shared16(to + r * 64 + ((j ^ ((r >> 1) & 3)) << 4), o);      // the 64-byte swizzle of map_o
+                    st_shared16(to + panel * 8192 + r * 64 + ((j ^ ((r >> 1) & 3)) << 4), o);      // the 64-byte swizzle of map_o
                 }
                 fence_async();
                 group_sync(1 + part);
-                if (r == 0) tma_store2(&map_o, to, ch0 + c0, row0);
+                if (r == 0) tma_store2(&map_o, to + panel * 8192, ch0 + c0, row0);
+                panel ^= 1;
             }
         }
         if (r == 0) tma_store_done();

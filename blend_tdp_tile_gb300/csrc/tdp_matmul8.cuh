@@ -113,6 +113,9 @@ __device__ __forceinline__ void tma_store2(const CUtensorMap *map, uint32_t src,
                  : "memory");
     asm volatile("cp.async.bulk.commit_group;" ::: "memory");
 }
+// All but the last store have been read.
+__device__ __forceinline__ void tma_store_read_but_one() { asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory"); }
+
 // Waits, with a limit, for what is on its way to `bar`.
 __device__ __forceinline__ void landed(uint32_t bar, uint32_t parity)
 {
