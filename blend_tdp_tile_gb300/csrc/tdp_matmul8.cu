@@ -22,7 +22,7 @@ namespace tdp_m8 {
 template <int NT>
 struct tile_smem {
     static constexpr int kStage = 16384 + NT * 128;
-    static constexpr int kStages = NT <= 16 ? 5 : NT <= 64 ? 4 : 3;     // two blocks an SM
+    static constexpr int kStages = NT <= 16 ? 5 : 4;        // two blocks an SM
     static constexpr int kBytes = 1024 + kStages * kStage;
     static_assert(kStages * kStage >= NT * 512, "the parts lie where the stages were");
 };
@@ -37,6 +37,7 @@ tdp_matmul8_tile_kernel(const __grid_constant__ args a, const __grid_constant__ 
     constexpr uint32_t kCols = NT < 32 ? 32 : NT;
     extern __shared__ unsigned char raw[];
     __shared__ uint64_t bar_mem[2 * NST + 1];
+    __shared__ float xs[NT];
     __shared__ uint32_t tmem_slot;
     __shared__ int dead_flag;
     volatile int *dead = &dead_flag;
@@ -60,6 +61,12 @@ tdp_matmul8_tile_kernel(const __grid_constant__ args a, const __grid_constant__ 
     const int32_t ch0 = tc * 128;
     const int64_t row0 = (int64_t)(tile / a.tiles_c) * NT;
     const int32_t k0 = (int32_t)((int64_t)a.kb * rank / split), n = (int32_t)((int64_t)a.kb * (rank + 1) / split) - k0;
+    using E = tdp_elem<BF16>;
+    using T = typename E::type;
+    const int32_t ch = ch0 + 2 * (threadIdx.x & 63);            // two channels of the output
+    const bool in = ch < a.N;
+    const T *bias = static_cast<const T *>(a.bias);
+    float2 w = make_float2(0.f, 0.f), b = w;
     bool ok = true;
     int32_t made = 0;
     if (warp == 4) {
@@ -95,6 +102,12 @@ tdp_matmul8_tile_kernel(const __grid_constant__ args a, const __grid_constant__ 
         __syncwarp();
         landed(done, 0);
     } else {
+        // what the end takes besides the sums, asked for under the products
+        if (threadIdx.x < NT) xs[threadIdx.x] = row0 + threadIdx.x < a.rows ? __ldcg(a.xs + row0 + threadIdx.x) : 0.f;
+        if (in) {
+            w = __ldcg(reinterpret_cast<const float2 *>(a.ws + ch));
+            if (bias) b = make_float2((float)bias[ch], (float)bias[ch + 1]);
+        }
         ok = mbar_wait(done, 0, dead);
         fence_after();
     }
@@ -107,13 +120,15 @@ tdp_matmul8_tile_kernel(const __grid_constant__ args a, const __grid_constant__ 
     if (warp < 4) {
         ok = __all_sync(~0u, ok && !*dead);
         const uint32_t from = tm + ((uint32_t)warp << 21);
-        constexpr int B = 16;
+        constexpr int B = NT < 32 ? 16 : 32;
 #pragma unroll 1
         for (int c0 = 0; c0 < NT; c0 += B) {
             uint32_t v[B];
-            tmem_ld16(from + c0, v);
+            if (B == 16) tmem_ld16(from + c0, v);
+            else tmem_ld32(from + c0, v);
             tmem_wait_ld();
-            tmem_have16(v);
+            if (B == 16) tmem_have16(v);
+            else tmem_have32(v);
 #pragma unroll
             for (int c = 0; c < B; ++c) {
                 if (!ok) v[c] = 0x7fffffffu;
@@ -126,42 +141,48 @@ tdp_matmul8_tile_kernel(const __grid_constant__ args a, const __grid_constant__ 
     __syncwarp();
     if (split > 1) cluster_sync();
     else __syncthreads();
-    if (warp < 4) {
-        using E = tdp_elem<BF16>;
-        using T = typename E::type;
-        const int32_t ch = ch0 + 2 * (threadIdx.x & 63);
-        if (ch < a.N) {
-            const float2 w = __ldcg(reinterpret_cast<const float2 *>(a.ws + ch));
-            const T *bias = static_cast<const T *>(a.bias);
-            const float b0 = bias ? (float)bias[ch] : 0.f, b1 = bias ? (float)bias[ch + 1] : 0.f;
-            const float *part = reinterpret_cast<const float *>(raw + (base - smem_u32(raw))) + 2 * (threadIdx.x & 63);
-            for (int32_t r = threadIdx.x >> 6; r < share; r += 2) {
-                const int64_t row = row0 + (int64_t)rank * share + r;
-                if (row >= a.rows) break;
-                float2 s = make_float2(0.f, 0.f);
-                for (uint32_t f = 0; f < split; ++f) {
-                    const float2 p = *reinterpret_cast<const float2 *>(part + (f * share + r) * 128);
-                    s.x += p.x;
-                    s.y += p.y;
+    if (warp < 4 && in) {
+        constexpr int U = 4;                // rows whose residuals a thread has under way
+        const float *part = reinterpret_cast<const float *>(raw + (base - smem_u32(raw))) + 2 * (threadIdx.x & 63);
+        const int64_t first = row0 + (int64_t)rank * share;
+        const int32_t end = (int32_t)min((int64_t)share, a.rows - first);
+#pragma unroll 1
+        for (int32_t r0 = threadIdx.x >> 6; r0 < end; r0 += 2 * U) {
+            uint2 s[U];
+            if (a.res) {
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    const T *at = static_cast<const T *>(a.res) + (first + min(r0 + 2 * u, end - 1)) * a.N + ch;
+                    if (BF16) s[u].x = *reinterpret_cast<const uint32_t *>(at);
+                    else s[u] = *reinterpret_cast<const uint2 *>(at);
                 }
-                const float x = __ldcg(a.xs + row);
-                float v0 = fmaf(s.x * x, w.x, b0), v1 = fmaf(s.y * x, w.y, b1);
-                const int64_t at = row * a.N + ch;
-                if (BF16) {
-                    if (a.res) {
-                        const uint32_t u = *reinterpret_cast<const uint32_t *>(static_cast<const T *>(a.res) + at);
-                        v0 += tdp_bf16_lo(u);
-                        v1 += tdp_bf16_hi(u);
-                    }
-                    *reinterpret_cast<uint32_t *>(static_cast<T *>(a.out) + at) = tdp_pack_bf16x2(v0, v1);
-                } else {
-                    if (a.res) {
-                        const float2 u = *reinterpret_cast<const float2 *>(static_cast<const T *>(a.res) + at);
-                        v0 += u.x;
-                        v1 += u.y;
-                    }
-                    *reinterpret_cast<float2 *>(static_cast<T *>(a.out) + at) = make_float2(v0, v1);
+            }
+            float2 sum[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) sum[u] = make_float2(0.f, 0.f);
+            for (uint32_t f = 0; f < split; ++f) {
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    const float2 p = *reinterpret_cast<const float2 *>(part + ((f << shift) + min(r0 + 2 * u, end - 1)) * 128);
+                    sum[u].x += p.x;
+                    sum[u].y += p.y;
                 }
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int32_t r = r0 + 2 * u;
+                if (r >= end) break;
+                float2 v = sum[u];
+                const float x = xs[rank * share + r];
+                v.x = fmaf(v.x * x, w.x, b.x);
+                v.y = fmaf(v.y * x, w.y, b.y);
+                if (a.res) {
+                    v.x += BF16 ? tdp_bf16_lo(s[u].x) : __uint_as_float(s[u].x);
+                    v.y += BF16 ? tdp_bf16_hi(s[u].x) : __uint_as_float(s[u].y);
+                }
+                T *to = static_cast<T *>(a.out) + (first + r) * a.N + ch;
+                if (BF16) *reinterpret_cast<uint32_t *>(to) = tdp_pack_bf16x2(v.x, v.y);
+                else *reinterpret_cast<float2 *>(to) = v;
             }
         }
     }
@@ -426,6 +447,14 @@ cudaError_t launch_clusters(void (*kernel)(KArgs...), unsigned grid, unsigned si
     return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
 }
 
+// Parts of K of a tile: until the device has a block for every SM.
+unsigned split_k(int64_t tiles, int32_t kb)
+{
+    unsigned split = 1;
+    while (split < 8 && 2 * split <= (unsigned)kb && tiles * split < 152) split *= 2;
+    return split;
+}
+
 template <int BF16, int NT>
 cudaError_t tile_launch(const args &a, const void *w8, const void *x8, int64_t K, cudaStream_t s)
 {
@@ -435,10 +464,8 @@ cudaError_t tile_launch(const args &a, const void *w8, const void *x8, int64_t K
     CUtensorMap w, x;
     if (e == cudaSuccess && (!map8(&w, w8, K, a.N, 128) || !map8(&x, x8, K, a.rows, NT))) e = cudaErrorInvalidValue;
     if (e != cudaSuccess) return e;
-    // parts of K until the device is full
     const int64_t tiles = (int64_t)a.tiles_c * ((a.rows + NT - 1) / NT);
-    unsigned split = 1;
-    while (split < 8 && 2 * split <= (unsigned)a.kb && tiles * split < 152) split *= 2;
+    const unsigned split = split_k(tiles, a.kb);
     return launch_clusters(tdp_matmul8_tile_kernel<BF16, NT>, (unsigned)(tiles * split), split, kTileThreads, bytes, s, a, w, x);
 }
 
@@ -456,12 +483,36 @@ cudaError_t pair_launch(args a, const void *w8, const void *x8, int64_t K, cudaS
     return launch_clusters(tdp_matmul8_pair_kernel<BF16>, 2 * std::min(a.tiles, 76), 2, kPairThreads, bytes, s, a, x, w, o);
 }
 
+// Rows of a tile, or 0 for pairs: the least time of launch and join plus rounds of resident blocks times stages of a block, in
+// us as measured.  K = N = 2048, 16 / 128 / 512 / 1024 / 2048 rows: 3.9 / 5.3 / 13.1 / 24.7 / - by 16 rows, 4.5 / 5.2 / 7.3 / 14.0 / -
+// by 32, 6.0 / 6.6 / 7.5 / 9.6 / - by 64, 8.8 / 9.3 / 9.5 / 9.8 / 10.6 by pairs; K = N = 4096: 4.7 / 9.9 / 37.7 / 70.6, 5.9 / 7.9 /
+// 21.5 / 41.5, 8.5 / 7.9 / 13.7 / 26.2 and 13.0 / 13.6 / 14.0 / 15.3 / 24.0.  (Tiles of 128 rows were never best.)
+int choose(int64_t rows, int32_t N, int32_t kb)
+{
+    constexpr int nt[3] = {16, 32, 64};
+    constexpr double base[3] = {3.3, 3.6, 4.4}, stage[3] = {0.20, 0.235, 0.285};
+    double least = 5.0 + 0.275 * kb * (double)(((rows + 255) / 256 * ((N + 255) / 256) + 75) / 76);
+    int best = 0;
+    for (int i = 0; i < 3; ++i) {
+        const int64_t tiles = (rows + nt[i] - 1) / nt[i] * ((N + 127) / 128), split = split_k(tiles, kb);
+        const double cost = base[i] + stage[i] * (double)((kb + split - 1) / split) * (double)((tiles * split + 303) / 304);
+        if (cost < least) {
+            least = cost;
+            best = nt[i];
+        }
+    }
+    return best;
+}
+
 template <int BF16>
 cudaError_t matmul8(const args &a, const void *w8, const void *x8, int64_t K, cudaStream_t s)
 {
-    if ((a.rows + 255) / 256 * ((a.N + 255) / 256) >= 76) return pair_launch<BF16>(a, w8, x8, K, s);
-    return a.rows <= 16 ? tile_launch<BF16, 16>(a, w8, x8, K, s) : a.rows <= 64 ? tile_launch<BF16, 64>(a, w8, x8, K, s)
-                                                                                : tile_launch<BF16, 128>(a, w8, x8, K, s);
+    switch (choose(a.rows, a.N, a.kb)) {
+    case 16: return tile_launch<BF16, 16>(a, w8, x8, K, s);
+    case 32: return tile_launch<BF16, 32>(a, w8, x8, K, s);
+    case 64: return tile_launch<BF16, 64>(a, w8, x8, K, s);
+    default: return pair_launch<BF16>(a, w8, x8, K, s);
+    }
 }
 
 }  // namespace
