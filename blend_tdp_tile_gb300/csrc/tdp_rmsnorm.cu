@@ -5,24 +5,33 @@
 //   dx = dh + rstd * (g - u * mean(g * u)),  dw = sum over rows of dy * u.
 // 8 bits (e4m3, a scale a row): v -> e4m3(448 v / m), m the row's largest |v|, scale m / 448.
 //
-// Bound by memory.  A row is read once: it stays in the registers of a team of lanes (a part of a warp, a warp, or up to
-// eight warps) while its sums and its largest value are joined, 16-byte vectors lane after lane.  Teams walk over the rows
-// with w in registers; the gradient keeps its sums for dw there too, joins a block's in shared memory and the blocks' in
-// a second launch, in a fixed order.
+// Bound by memory.  A row is read once: a team of lanes (a part of a warp, a warp, or up to eight warps) brings it to shared
+// memory, each lane its own 16-byte vectors, two rows ahead (the gradient one), some 130 KB an SM on their way; sums and largest
+// values are joined over the team, and the second pass reads shared memory or registers.  Nobody but the lane itself reads its
+// vectors, so no barrier stands between a copy and its use.  The gradient keeps its sums for dw in registers over all its rows, joins
+// a block's in shared memory and the blocks' in a second launch, in a fixed order.
 #include <cuda_fp16.h>
 
 #include <algorithm>
+#include <atomic>
 
 #include "tdp.h"
 #include "tdp_internal.h"
 #include "tdp_rows.cuh"
+#include "tdp_tc.cuh"
 
 namespace {
 
+using tdp_tc::add2;
+using tdp_tc::fma2;
+using tdp_tc::mul2;
+using tdp_tc::pair;
+using tdp_tc::unpair;
+
 constexpr int kNormThreads = 256;           // threads of a block at most: eight warps a row
-constexpr int kNormVecs = 8;                // vectors of a lane at most
-constexpr int kGradBlocks = 152 * 4;        // gradient: blocks at most, and so parts of dw
-constexpr uint32_t kLeastBits = 0x0d800000u;        // 2^-100
+constexpr int kNormVecs = 4;                // vectors of a lane, but for rows of more than 1024
+constexpr int kNormSmem = 196608;           // bytes of rows that an SM has on their way and at work
+constexpr float kLeast = 0x1p-100f;
 
 struct norm_args {
     int64_t rows;
@@ -48,66 +57,85 @@ struct norm_grad_args {
     float *part;                // [blocks, C]
 };
 
-template <int N>
-__device__ __forceinline__ void zero(float *f)
+// B bytes to shared memory on their way, zeros where `on` is false.
+template <int B>
+__device__ __forceinline__ void copy_async(uint32_t dst, const void *src, bool on)
 {
-#pragma unroll
-    for (int i = 0; i < N; ++i) f[i] = 0.f;
+    const int n = on ? B : 0;
+    if (B == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+    else asm volatile("cp.async.ca.shared.global [%0], [%1], %3, %2;" ::"r"(dst), "l"(src), "r"(n), "n"(B) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+// Largest magnitude; NaN goes before all else.
+__device__ __forceinline__ float max_nan(float a, float b)
+{
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
 }
 
-// Four values as e4m3, the first in the lowest byte; rounded to nearest even, past 448 to 448, NaN stays NaN.
-__device__ __forceinline__ uint32_t to_e4m3x4(float a, float b, float c, float d)
+// A vector of the plan's type as pairs of fp32, and back.
+template <int BF16>
+__device__ __forceinline__ void pairs_of(const uint4 &u, uint64_t *p)
 {
+    float f[8];
+    tdp_elem<BF16>::unpack(u, f);
+#pragma unroll
+    for (int j = 0; j < tdp_elem<BF16>::kVec / 2; ++j) p[j] = pair(f[2 * j], f[2 * j + 1]);
+}
+template <int BF16>
+__device__ __forceinline__ uint4 of_pairs(const uint64_t *p)
+{
+    float f[8];
+#pragma unroll
+    for (int j = 0; j < tdp_elem<BF16>::kVec / 2; ++j) unpair(p[j], f[2 * j], f[2 * j + 1]);
+    return tdp_elem<BF16>::pack(f);
+}
+template <int P>
+__device__ __forceinline__ void top_of(const uint64_t *p, float &top)
+{
+#pragma unroll
+    for (int j = 0; j < P; ++j) {
+        float a, b;
+        unpair(p[j], a, b);
+        top = max_nan(top, max_nan(fabsf(a), fabsf(b)));
+    }
+}
+
+// Two pairs as e4m3, the first in the lowest byte; rounded to nearest even, past 448 to 448, NaN stays NaN.
+__device__ __forceinline__ uint32_t to_e4m3x4(uint64_t p, uint64_t q)
+{
+    float a, b, c, d;
+    unpair(p, a, b);
+    unpair(q, c, d);
     uint16_t lo, hi;
     asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(b), "f"(a));
     asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(d), "f"(c));
     return (uint32_t)lo | ((uint32_t)hi << 16);
 }
-__device__ __forceinline__ void from_e4m3x4(uint32_t v, float *f)
+__device__ __forceinline__ void from_e4m3x4(uint32_t v, uint64_t *p)
 {
     uint32_t lo, hi;
     asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(lo) : "h"((uint16_t)v));
     asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(hi) : "h"((uint16_t)(v >> 16)));
     const float2 a = __half22float2(*reinterpret_cast<__half2 *>(&lo)), b = __half22float2(*reinterpret_cast<__half2 *>(&hi));
-    f[0] = a.x;
-    f[1] = a.y;
-    f[2] = b.x;
-    f[3] = b.y;
+    p[0] = pair(a.x, a.y);
+    p[1] = pair(b.x, b.y);
 }
-
-// A row's scale from the bits of its largest magnitude.  Magnitudes compare as integers, NaN above infinity above all else.
-// A row that holds either has scale NaN, and NaN in every place; one below 2^-100 is counted as if that were its largest.
-struct scale8 {
-    float part, inv, scale;
-    __device__ __forceinline__ explicit scale8(uint32_t top_bits)
-    {
-        const float top = top_bits >= 0x7f800000u ? __uint_as_float(0x7fffffffu) : __uint_as_float(max(top_bits, kLeastBits));
-        part = top * (1.f / 512);
-        inv = __frcp_rn(part);
-        scale = __fdiv_rn(top, 448.f);
-    }
-    // 448 v / top as (0.875 v) / (top / 512): no product overflows and a value midway between two of e4m3's comes out
-    // exact, so that it goes to the even one.  The quotient is corrected by its remainder (P. Markstein, "Computation of
-    // elementary functions on the IBM RISC System/6000 processor", 1990): the plain product v * inv put 0.5 % of bf16's values
-    // on the wrong side.
-    __device__ __forceinline__ float of(float v) const
-    {
-        const float a = 0.875f * v, q = a * inv;
-        return fmaf(fmaf(-q, part, a), inv, q);
-    }
-};
-
-// V values of a row in 8 bits.
-template <int V>
-__device__ __forceinline__ void store8(uint8_t *p, const float *f, const scale8 &s)
+template <int P>
+__device__ __forceinline__ void store8(uint8_t *p, const uint64_t *v)
 {
-    const uint32_t a = to_e4m3x4(s.of(f[0]), s.of(f[1]), s.of(f[2]), s.of(f[3]));
-    if (V == 8) {
-        *reinterpret_cast<uint2 *>(p) = make_uint2(a, to_e4m3x4(s.of(f[V - 4]), s.of(f[V - 3]), s.of(f[V - 2]), s.of(f[V - 1])));
-    } else {
-        *reinterpret_cast<uint32_t *>(p) = a;
-    }
+    const uint32_t a = to_e4m3x4(v[0], v[1]);
+    if (P == 4) *reinterpret_cast<uint2 *>(p) = make_uint2(a, to_e4m3x4(v[P - 2], v[P - 1]));
+    else *reinterpret_cast<uint32_t *>(p) = a;
 }
+
+// The largest magnitude that a row's scale is made of: NaN for a row that holds NaN or an infinity, which then has scale NaN
+// and NaN in every place; 2^-100 for less.
+__device__ __forceinline__ float top8(float top) { return top < INFINITY ? fmaxf(top, kLeast) : NAN; }
 
 // A thread's place: its row among those of a round, its lane in the row's team.
 struct team {
@@ -121,45 +149,68 @@ struct team {
 };
 
 // Sum, and two maxima, over a row's team; every lane has the same.  `turn` changes from round to round.
-__device__ __forceinline__ void join(int32_t lanes, int32_t warps, int32_t turn, float &sum, uint32_t &top, uint32_t &top2)
+template <int TOP>
+__device__ __forceinline__ void join(int32_t lanes, int32_t warps, int32_t turn, float &sum, float &top, float &top2)
 {
-    __shared__ float ssum[2][kNormThreads / 32];
-    __shared__ uint32_t stop[2][kNormThreads / 32], stop2[2][kNormThreads / 32];
+    __shared__ float ssum[2][kNormThreads / 32], stop[2][TOP ? kNormThreads / 32 : 1], stop2[2][TOP ? kNormThreads / 32 : 1];
     for (int32_t o = min(lanes, 32) / 2; o; o >>= 1) {
         sum += __shfl_xor_sync(~0u, sum, o);
-        top = max(top, __shfl_xor_sync(~0u, top, o));
-        top2 = max(top2, __shfl_xor_sync(~0u, top2, o));
+        if (TOP) {
+            top = max_nan(top, __shfl_xor_sync(~0u, top, o));
+            top2 = max_nan(top2, __shfl_xor_sync(~0u, top2, o));
+        }
     }
     if (warps == 1) return;
     const int32_t k = turn & 1, w = threadIdx.x >> 5;
     if ((threadIdx.x & 31) == 0) {
         ssum[k][w] = sum;
-        stop[k][w] = top;
-        stop2[k][w] = top2;
+        if (TOP) {
+            stop[k][w] = top;
+            stop2[k][w] = top2;
+        }
     }
     __syncthreads();            // the other half is written next: one barrier a round is enough
     sum = 0.f;
-    top = top2 = 0;
+    top = top2 = 0.f;
     for (int32_t i = 0; i < warps; ++i) {
         sum += ssum[k][i];
-        top = max(top, stop[k][i]);
-        top2 = max(top2, stop2[k][i]);
+        if (TOP) {
+            top = max_nan(top, stop[k][i]);
+            top2 = max_nan(top2, stop2[k][i]);
+        }
     }
 }
 
-__device__ __forceinline__ uint32_t magnitude(float f) { return __float_as_uint(f) & 0x7fffffffu; }
-
-// NORM 0: the rows themselves, in 8 bits.  Q8: with outputs in 8 bits.
-template <int BF16, int VPT, int NORM, int Q8>
+// NORM 0: the rows themselves, in 8 bits.  Q8: with outputs in 8 bits.  RES: with a residual.
+template <int BF16, int VPT, int NORM, int Q8, int RES>
 __global__ void __launch_bounds__(kNormThreads)
 tdp_rms_norm_kernel(const __grid_constant__ norm_args a)
 {
     using E = tdp_elem<BF16>;
-    constexpr int V = E::kVec;
+    constexpr int V = E::kVec, P = V / 2, IN = 1 + RES, S = RES ? 3 : 6;     // inputs, rows in shared memory
+    extern __shared__ __align__(16) uint4 slots[];      // [S][IN][VPT][threads]
     tdp_pdl_trigger();
     tdp_pdl_wait();
     const team t(a.lanes);
     const int64_t round = (int64_t)gridDim.x * t.rows;
+    const int32_t threads = blockDim.x;
+    const uint4 *mine = slots + threadIdx.x;
+    auto bring = [&](int64_t r0, int32_t stage) {
+        const int64_t r = r0 + t.row;
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            const int32_t c = t.lane + i * a.lanes;
+            const bool on = r < a.rows && c < a.nv;
+            const int64_t at = on ? r * a.nv + c : 0;
+            const uint32_t to = tdp_tc::smem_u32(mine + (stage * IN * VPT + i) * threads);
+            copy_async<16>(to, static_cast<const uint4 *>(a.x) + at, on);
+            if (RES) copy_async<16>(to + VPT * threads * 16, static_cast<const uint4 *>(a.res) + at, on);
+        }
+        copy_commit();
+    };
+    const int64_t first = (int64_t)blockIdx.x * t.rows;
+#pragma unroll
+    for (int s = 0; s < S - 1; ++s) bring(first + s * round, s);
     uint4 w[NORM ? VPT : 1];
     if (NORM && a.w) {
 #pragma unroll
@@ -169,187 +220,236 @@ tdp_rms_norm_kernel(const __grid_constant__ norm_args a)
         }
     }
     // whole warps take part in every round, past the last row too
-    const int64_t first = (int64_t)blockIdx.x * t.rows;
-    int32_t turn = 0;
+    int32_t turn = 0, stage = 0;
     for (int64_t r0 = first; r0 < a.rows; r0 += round, ++turn) {
+        bring(r0 + (S - 1) * round, stage == 0 ? S - 1 : stage - 1);
+        copy_wait<S - 1>();
         const int64_t r = r0 + t.row;
         const bool on = r < a.rows;
         const int64_t at = r * a.nv;
-        uint4 x[VPT], s[NORM ? VPT : 1];
+        uint4 x[VPT];
+        uint64_t sum2 = 0;
+        float top = 0.f, top2 = 0.f;            // of |h w| and |h|
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
             const int32_t c = t.lane + i * a.lanes;
-            const bool in = on && c < a.nv;
-            x[i] = in ? __ldcs(static_cast<const uint4 *>(a.x) + at + c) : make_uint4(0, 0, 0, 0);
-            if (NORM && a.res) s[i] = in ? __ldcs(static_cast<const uint4 *>(a.res) + at + c) : make_uint4(0, 0, 0, 0);
-        }
-        float sum = 0.f;
-        uint32_t top = 0, top2 = 0;         // of |h w| and |h|
-#pragma unroll
-        for (int i = 0; i < VPT; ++i) {
-            const int32_t c = t.lane + i * a.lanes;
-            float f[V];
-            E::unpack(x[i], f);
-            if (NORM && a.res) {
+            uint64_t f[P];
+            x[i] = mine[(stage * IN * VPT + i) * threads];
+            pairs_of<BF16>(x[i], f);
+            if (RES) {
                 // rounded here, whether h is kept or not: the gradient reads it as it is kept, and is that of this function
-                float g[V];
-                E::unpack(s[i], g);
+                uint64_t g[P];
+                pairs_of<BF16>(mine[((stage * IN + 1) * VPT + i) * threads], g);
 #pragma unroll
-                for (int j = 0; j < V; ++j) f[j] += g[j];
-                x[i] = E::pack(f);
-                E::unpack(x[i], f);
+                for (int j = 0; j < P; ++j) f[j] = add2(f[j], g[j]);
+                x[i] = of_pairs<BF16>(f);
+                if (BF16) pairs_of<BF16>(x[i], f);
             }
             if (NORM && a.h && on && c < a.nv) static_cast<uint4 *>(a.h)[at + c] = x[i];
+            if (NORM) {
 #pragma unroll
-            for (int j = 0; j < V; ++j) {
-                if (NORM) sum = fmaf(f[j], f[j], sum);
-                if (Q8) top2 = max(top2, magnitude(f[j]));
+                for (int j = 0; j < P; ++j) sum2 = fma2(f[j], f[j], sum2);
             }
+            if (Q8 && (!NORM || a.x8)) top_of<P>(f, top2);
             if (NORM && Q8 && a.y8) {
-                float g[V];
-                if (a.w) E::unpack(w[i], g);
+                if (a.w) {
+                    uint64_t g[P];
+                    pairs_of<BF16>(w[i], g);
 #pragma unroll
-                for (int j = 0; j < V; ++j) top = max(top, magnitude(a.w ? f[j] * g[j] : f[j]));
+                    for (int j = 0; j < P; ++j) f[j] = mul2(f[j], g[j]);
+                }
+                top_of<P>(f, top);
             }
         }
-        join(a.lanes, a.warps, turn, sum, top, top2);
-        float rstd = 1.f;
-        if (NORM) rstd = __frcp_rn(__fsqrt_rn(fmaf(sum, a.mean, a.eps)));
+        stage = stage == S - 1 ? 0 : stage + 1;
+        float sum, other;
+        unpair(sum2, sum, other);
+        sum += other;
+        join<Q8>(a.lanes, a.warps, turn, sum, top, top2);
+        const float rstd = NORM ? __frcp_rn(__fsqrt_rn(fmaf(sum, a.mean, a.eps))) : 1.f;
         if (NORM && a.rstd && on && t.lane == 0) a.rstd[r] = rstd;
-        scale8 s8(0), u8(0);
+        uint64_t ky = 0, kx = 0;
+        float part = 0.f, inv = 0.f;
         if (Q8 && NORM && a.y8) {
-            s8 = scale8(magnitude(__uint_as_float(top) * rstd));
-            if (on && t.lane == 0) a.y8_scale[r] = s8.scale;
+            const float m = top8(top * rstd);
+            if (on && t.lane == 0) a.y8_scale[r] = __fdiv_rn(m, 448.f);
+            const float k = __fdiv_rn(448.f, m);
+            ky = pair(k, k);
         }
         if (Q8 && a.x8) {
-            u8 = scale8(magnitude(__uint_as_float(top2) * rstd));
-            if (on && t.lane == 0) a.x8_scale[r] = u8.scale;
+            const float m = top8(top2 * rstd);
+            if (on && t.lane == 0) a.x8_scale[r] = __fdiv_rn(m, 448.f);
+            if (NORM) {
+                const float k = __fdiv_rn(448.f, m);
+                kx = pair(k, k);
+            } else {
+                part = -m * (1.f / 512);
+                inv = __frcp_rn(-part);
+            }
         }
         if (!on) continue;
+        const uint64_t rs = pair(rstd, rstd);
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
             const int32_t c = t.lane + i * a.lanes;
             if (c >= a.nv) break;
-            float f[V];
-            E::unpack(x[i], f);
+            uint64_t f[P], q[P];
+            pairs_of<BF16>(x[i], f);
+            if (!NORM) {
+                // 448 v / m as (0.875 v) / (m / 512): no product overflows and a value midway between two of e4m3's comes out
+                // exact, so that it goes to the even one.  The quotient is corrected by its remainder (P. Markstein, "Computation of
+                // elementary functions on the IBM RISC System/6000 processor", 1990): the plain product v * inv put 0.5 % of
+                // bf16's values on the wrong side.  (A norm's rows have no such values: there the product does.)
+                const uint64_t e = pair(0.875f, 0.875f), n = pair(part, part), k = pair(inv, inv);
 #pragma unroll
-            for (int j = 0; j < V; ++j) f[j] *= rstd;
-            if (Q8 && a.x8) store8<V>(a.x8 + (at + c) * V, f, u8);
-            if (NORM) {
-                if (a.w) {
-                    float g[V];
-                    E::unpack(w[i], g);
-#pragma unroll
-                    for (int j = 0; j < V; ++j) f[j] *= g[j];
+                for (int j = 0; j < P; ++j) {
+                    const uint64_t v = mul2(f[j], e);
+                    q[j] = mul2(v, k);
+                    q[j] = fma2(fma2(q[j], n, v), k, q[j]);
                 }
-                if (Q8 && a.y8) store8<V>(a.y8 + (at + c) * V, f, s8);
-                if (a.y) static_cast<uint4 *>(a.y)[at + c] = E::pack(f);
+                store8<P>(a.x8 + (at + c) * V, q);
+                continue;
             }
+#pragma unroll
+            for (int j = 0; j < P; ++j) f[j] = mul2(f[j], rs);
+            if (Q8 && a.x8) {
+#pragma unroll
+                for (int j = 0; j < P; ++j) q[j] = mul2(f[j], kx);
+                store8<P>(a.x8 + (at + c) * V, q);
+            }
+            if (a.w) {
+                uint64_t g[P];
+                pairs_of<BF16>(w[i], g);
+#pragma unroll
+                for (int j = 0; j < P; ++j) f[j] = mul2(f[j], g[j]);
+            }
+            if (Q8 && a.y8) {
+#pragma unroll
+                for (int j = 0; j < P; ++j) q[j] = mul2(f[j], ky);
+                store8<P>(a.y8 + (at + c) * V, q);
+            }
+            if (a.y) static_cast<uint4 *>(a.y)[at + c] = of_pairs<BF16>(f);
         }
     }
+    copy_wait<0>();
 }
 
-// KEPT8: u is x8 * x8_scale; otherwise h * rstd.
+// KEPT8: u is x8 * x8_scale; otherwise h * rstd.  The rows stay in shared memory for the second pass.
 template <int BF16, int VPT, int KEPT8>
 __global__ void __launch_bounds__(kNormThreads)
 tdp_rms_norm_grad_kernel(const __grid_constant__ norm_grad_args a)
 {
     using E = tdp_elem<BF16>;
-    constexpr int V = E::kVec;
-    extern __shared__ __align__(16) float acc[];        // [teams of a block, C]
+    constexpr int V = E::kVec, P = V / 2, IN = 3, S = 2;
+    extern __shared__ __align__(16) uint4 slots[];      // [S][IN][VPT][threads]; at the end [teams of a block, C] sums
     tdp_pdl_trigger();
     tdp_pdl_wait();
     const team t(a.lanes);
     const int64_t round = (int64_t)gridDim.x * t.rows;
+    const int32_t threads = blockDim.x;
+    const uint4 *mine = slots + threadIdx.x;
+    auto bring = [&](int64_t r0, int32_t stage) {
+        const int64_t r = r0 + t.row;
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            const int32_t c = t.lane + i * a.lanes;
+            const bool on = r < a.rows && c < a.nv;
+            const int64_t at = on ? r * a.nv + c : 0;
+            const uint32_t to = tdp_tc::smem_u32(mine + (stage * IN * VPT + i) * threads);
+            if (KEPT8) copy_async<V>(to, a.x8 + at * V, on);
+            else copy_async<16>(to, static_cast<const uint4 *>(a.h) + at, on);
+            copy_async<16>(to + VPT * threads * 16, static_cast<const uint4 *>(a.dy) + at, on);
+            if (a.dh) copy_async<16>(to + 2 * VPT * threads * 16, static_cast<const uint4 *>(a.dh) + at, on);
+        }
+        copy_commit();
+    };
+    const int64_t first = (int64_t)blockIdx.x * t.rows;
+    bring(first, 0);
     uint4 w[VPT];
-    float dw[VPT * V];
-    zero<VPT * V>(dw);
+    uint64_t dw[VPT * P];
+#pragma unroll
+    for (int i = 0; i < VPT * P; ++i) dw[i] = 0;
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
         const int32_t c = t.lane + i * a.lanes;
         w[i] = a.w && c < a.nv ? static_cast<const uint4 *>(a.w)[c] : make_uint4(0, 0, 0, 0);
     }
     int32_t turn = 0;
-    for (int64_t r0 = (int64_t)blockIdx.x * t.rows; r0 < a.rows; r0 += round, ++turn) {
+    for (int64_t r0 = first; r0 < a.rows; r0 += round, ++turn) {
+        const int32_t stage = turn & 1;
         const int64_t r = r0 + t.row;
         const bool on = r < a.rows;
-        const int64_t at = r * a.nv;
-        uint4 x[VPT], d[VPT], e[VPT];
-#pragma unroll
-        for (int i = 0; i < VPT; ++i) {
-            const int32_t c = t.lane + i * a.lanes;
-            const bool in = on && c < a.nv;
-            x[i] = d[i] = e[i] = make_uint4(0, 0, 0, 0);
-            if (!in) continue;
-            if (KEPT8) {
-                if (V == 8) {
-                    const uint2 p = __ldcs(reinterpret_cast<const uint2 *>(a.x8) + at + c);
-                    x[i].x = p.x;
-                    x[i].y = p.y;
-                } else {
-                    x[i].x = __ldcs(reinterpret_cast<const uint32_t *>(a.x8) + at + c);
-                }
-            } else {
-                x[i] = __ldcs(static_cast<const uint4 *>(a.h) + at + c);
-            }
-            d[i] = __ldcs(static_cast<const uint4 *>(a.dy) + at + c);
-            if (a.dh) e[i] = __ldcs(static_cast<const uint4 *>(a.dh) + at + c);
-        }
         const float rstd = on ? a.rstd[r] : 0.f, unit = KEPT8 ? (on ? a.x8_scale[r] : 0.f) : rstd;
-        auto rows = [&](int i, float *u, float *g) {
+        bring(r0 + round, stage ^ 1);
+        copy_wait<1>();
+        auto row = [&](int i, uint64_t *u, uint64_t *g) {
+            const uint4 *at = mine + (stage * IN * VPT + i) * threads;
             if (KEPT8) {
-                from_e4m3x4(x[i].x, u);
-                if (V == 8) from_e4m3x4(x[i].y, u + V - 4);
+                const uint2 p = *reinterpret_cast<const uint2 *>(at);
+                from_e4m3x4(p.x, u);
+                if (V == 8) from_e4m3x4(p.y, u + P - 2);
             } else {
-                E::unpack(x[i], u);
+                pairs_of<BF16>(*at, u);
             }
-#pragma unroll
-            for (int j = 0; j < V; ++j) u[j] *= unit;
-            E::unpack(d[i], g);
+            pairs_of<BF16>(at[VPT * threads], g);
         };
-        float sum = 0.f;
-        uint32_t no = 0, no2 = 0;
+        uint64_t sum2 = 0;
+        const uint64_t un = pair(unit, unit);
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
-            float u[V], g[V], k[V];
-            rows(i, u, g);
-            if (a.w) E::unpack(w[i], k);
+            uint64_t u[P], g[P], k[P];
+            row(i, u, g);
+            if (a.w) pairs_of<BF16>(w[i], k);
 #pragma unroll
-            for (int j = 0; j < V; ++j) {
-                const float p = g[j] * u[j];
-                dw[i * V + j] += p;
-                sum = a.w ? fmaf(p, k[j], sum) : sum + p;
+            for (int j = 0; j < P; ++j) {
+                const uint64_t p = mul2(g[j], mul2(u[j], un));
+                dw[i * P + j] = add2(dw[i * P + j], p);
+                sum2 = a.w ? fma2(p, k[j], sum2) : add2(sum2, p);
             }
         }
-        join(a.lanes, a.warps, turn, sum, no, no2);
-        if (!on) continue;
-        const float m = sum * a.mean;
+        float sum, other, no = 0.f, no2 = 0.f;
+        unpair(sum2, sum, other);
+        sum += other;
+        join<0>(a.lanes, a.warps, turn, sum, no, no2);
+        if (on) {
+            const float m = -sum * a.mean * unit;
+            const uint64_t m2 = pair(m, m), rs = pair(rstd, rstd);
+            uint4 *dx = static_cast<uint4 *>(a.dx) + r * a.nv;
 #pragma unroll
-        for (int i = 0; i < VPT; ++i) {
-            const int32_t c = t.lane + i * a.lanes;
-            if (c >= a.nv) break;
-            float u[V], g[V], k[V];
-            rows(i, u, g);
-            if (a.w) {
-                E::unpack(w[i], k);
+            for (int i = 0; i < VPT; ++i) {
+                const int32_t c = t.lane + i * a.lanes;
+                if (c >= a.nv) break;
+                uint64_t u[P], g[P], k[P];
+                row(i, u, g);
+                if (a.w) {
+                    pairs_of<BF16>(w[i], k);
 #pragma unroll
-                for (int j = 0; j < V; ++j) g[j] *= k[j];
+                    for (int j = 0; j < P; ++j) g[j] = mul2(g[j], k[j]);
+                }
+                if (a.dh) {
+                    pairs_of<BF16>(mine[((stage * IN + 2) * VPT + i) * threads], k);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < P; ++j) k[j] = 0;
+                }
+#pragma unroll
+                for (int j = 0; j < P; ++j) g[j] = fma2(fma2(u[j], m2, g[j]), rs, k[j]);
+                dx[c] = of_pairs<BF16>(g);
             }
-            E::unpack(e[i], k);
-#pragma unroll
-            for (int j = 0; j < V; ++j) g[j] = fmaf(fmaf(-u[j], m, g[j]), rstd, k[j]);
-            static_cast<uint4 *>(a.dx)[at + c] = E::pack(g);
         }
     }
+    copy_wait<0>();
     if (!a.part) return;
     // a block's sums for dw, its teams' in order
+    if (t.rows > 1) __syncthreads();
+    float *acc = reinterpret_cast<float *>(slots);
     float *to = t.rows > 1 ? acc + t.row * a.C : a.part + (int64_t)blockIdx.x * a.C;
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
         const int32_t c = t.lane + i * a.lanes;
         if (c < a.nv) {
 #pragma unroll
-            for (int j = 0; j < V; j += 4) *reinterpret_cast<float4 *>(to + c * V + j) = make_float4(dw[i * V + j], dw[i * V + j + 1], dw[i * V + j + 2], dw[i * V + j + 3]);
+            for (int j = 0; j < P; j += 2) *reinterpret_cast<ulonglong2 *>(to + c * V + 2 * j) = make_ulonglong2(dw[i * P + j], dw[i * P + j + 1]);
         }
     }
     if (t.rows == 1) return;
@@ -383,20 +483,24 @@ tdp_rms_norm_dw_kernel(const float *part, int32_t parts, int32_t C, float *dw)
 // How rows are dealt to teams.
 struct norm_shape {
     int32_t nv, vpt, lanes, warps, threads, rows;           // rows: of a block and round
+    int64_t blocks;
 };
 
-norm_shape norm_deal(int32_t nv, int32_t most)
+norm_shape norm_deal(int64_t rows, int32_t nv)
 {
     norm_shape s;
     s.nv = nv;
     s.lanes = 1;
     while (s.lanes < 32 && s.lanes < nv) s.lanes *= 2;
-    s.warps = std::max(1, (nv + 32 * most - 1) / (32 * most));
+    s.warps = std::min(kNormThreads / 32, (nv + 32 * kNormVecs - 1) / (32 * kNormVecs));
     s.lanes *= s.warps;
     const int32_t need = (nv + s.lanes - 1) / s.lanes;
     s.vpt = need <= 1 ? 1 : need <= 2 ? 2 : need <= 4 ? 4 : 8;
     s.threads = s.warps == 1 ? 128 : 32 * s.warps;
     s.rows = s.threads / s.lanes;
+    // as many blocks as are resident: 96 bytes of shared memory a vector, registers for 768 threads at most
+    const int32_t sm = std::max(1, std::min(kNormSmem / (96 * s.vpt), 768) / s.threads);
+    s.blocks = std::min<int64_t>((rows + s.rows - 1) / s.rows, 152 * sm);
     return s;
 }
 
@@ -412,23 +516,42 @@ tdp_status norm_check(tdp_plan_t plan, int64_t rows, int32_t C, int32_t *nv)
     return TDP_OK;
 }
 
-template <int NORM, int Q8>
+// Raise a kernel's dynamic shared-memory limit once per device (`done`: one flag each).
+template <typename K>
+cudaError_t allow_smem(K kernel, size_t bytes, std::atomic<bool> *done)
+{
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess || (dev < 64 && done[dev].load(std::memory_order_relaxed))) return e;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    if (e == cudaSuccess && dev < 64) done[dev].store(true, std::memory_order_relaxed);
+    return e;
+}
+
+template <int BF16, int VPT, int NORM, int Q8, int RES>
+cudaError_t norm_launch(const norm_shape &sh, const norm_args &a, cudaStream_t s)
+{
+    static std::atomic<bool> done[64];
+    auto *kernel = tdp_rms_norm_kernel<BF16, VPT, NORM, Q8, RES>;
+    const cudaError_t e = allow_smem(kernel, 96 * VPT * kNormThreads, done);
+    return e != cudaSuccess ? e : tdp_launch_smem(true, kernel, (unsigned)sh.blocks, sh.threads, (size_t)96 * VPT * sh.threads, s, a);
+}
+
+template <int NORM, int Q8, int RES>
 cudaError_t norm_launch(int bf16, const norm_shape &sh, const norm_args &a, cudaStream_t s)
 {
-    const unsigned grid = (unsigned)std::min<int64_t>((a.rows + sh.rows - 1) / sh.rows, 152 * (2048 / sh.threads));
-#define TDP_NORM(V) \
-    (bf16 ? tdp_launch(true, tdp_rms_norm_kernel<1, V, NORM, Q8>, grid, sh.threads, s, a) \
-          : tdp_launch(true, tdp_rms_norm_kernel<0, V, NORM, Q8>, grid, sh.threads, s, a))
+#define TDP_NORM(V) (bf16 ? norm_launch<1, V, NORM, Q8, RES>(sh, a, s) : norm_launch<0, V, NORM, Q8, RES>(sh, a, s))
     return sh.vpt == 1 ? TDP_NORM(1) : sh.vpt == 2 ? TDP_NORM(2) : sh.vpt == 4 ? TDP_NORM(4) : TDP_NORM(8);
 #undef TDP_NORM
 }
 
-// Blocks of the gradient; a block's sums for dw take `teams` rows of C floats in shared memory.
-norm_shape grad_deal(int32_t nv, int32_t C, unsigned *grid, int64_t rows)
+template <int BF16, int VPT, int KEPT8>
+cudaError_t grad_launch(const norm_shape &sh, const norm_grad_args &a, cudaStream_t s)
 {
-    norm_shape s = norm_deal(nv, kNormVecs);
-    *grid = (unsigned)std::min<int64_t>((rows + s.rows - 1) / s.rows, kGradBlocks);
-    return s;
+    static std::atomic<bool> done[64];
+    auto *kernel = tdp_rms_norm_grad_kernel<BF16, VPT, KEPT8>;
+    const cudaError_t e = allow_smem(kernel, 96 * VPT * kNormThreads, done);
+    return e != cudaSuccess ? e : tdp_launch_smem(true, kernel, (unsigned)sh.blocks, sh.threads, (size_t)96 * VPT * sh.threads, s, a);
 }
 
 }  // namespace
@@ -447,11 +570,12 @@ extern "C" tdp_status tdp_rms_norm(tdp_plan_t plan, int64_t rows, int32_t C, flo
     if (!tdp_aligned(x, 16) || !tdp_aligned(res, 16) || !tdp_aligned(w, 16) || !tdp_aligned(h, 16) || !tdp_aligned(y, 16) ||
         !tdp_aligned(y8, 16) || !tdp_aligned(x8, 16) || !tdp_aligned(rstd, 4) || !tdp_aligned(y8_scale, 4) || !tdp_aligned(x8_scale, 4))
         return tdp_fail(TDP_ERR_MISALIGNED, "rows and w need 16-byte, scales and rstd 4-byte alignment");
-    const norm_shape sh = norm_deal(nv, kNormVecs);
+    const norm_shape sh = norm_deal(rows, nv);
     norm_args a = {rows, C, nv, sh.lanes, sh.warps, eps, 1.f / (float)C, x, res, w, h, y, rstd, y8, x8, y8_scale, x8_scale};
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     const int bf16 = plan->g.dtype == TDP_BF16;
-    const cudaError_t err = y8 || x8 ? norm_launch<1, 1>(bf16, sh, a, s) : norm_launch<1, 0>(bf16, sh, a, s);
+    const cudaError_t err = y8 || x8 ? (res ? norm_launch<1, 1, 1>(bf16, sh, a, s) : norm_launch<1, 1, 0>(bf16, sh, a, s))
+                                     : (res ? norm_launch<1, 0, 1>(bf16, sh, a, s) : norm_launch<1, 0, 0>(bf16, sh, a, s));
     return err == cudaSuccess ? tdp_ok() : tdp_fail(TDP_ERR_CUDA, cudaGetErrorString(err));
 }
 
@@ -465,7 +589,7 @@ extern "C" tdp_status tdp_quant8(tdp_plan_t plan, int64_t rows, int32_t C, const
     if (!x || !x8 || !x8_scale) return tdp_fail(TDP_ERR_INVALID_ARG, "null x, x8 or x8_scale");
     if (!tdp_aligned(x, 16) || !tdp_aligned(x8, 16) || !tdp_aligned(x8_scale, 4))
         return tdp_fail(TDP_ERR_MISALIGNED, "rows need 16-byte, scales 4-byte alignment");
-    const norm_shape sh = norm_deal(nv, kNormVecs);
+    const norm_shape sh = norm_deal(rows, nv);
     norm_args a = {};
     a.rows = rows;
     a.C = C;
@@ -475,7 +599,7 @@ extern "C" tdp_status tdp_quant8(tdp_plan_t plan, int64_t rows, int32_t C, const
     a.x = x;
     a.x8 = x8;
     a.x8_scale = x8_scale;
-    const cudaError_t err = norm_launch<0, 1>(plan->g.dtype == TDP_BF16, sh, a, reinterpret_cast<cudaStream_t>(stream));
+    const cudaError_t err = norm_launch<0, 1, 0>(plan->g.dtype == TDP_BF16, sh, a, reinterpret_cast<cudaStream_t>(stream));
     return err == cudaSuccess ? tdp_ok() : tdp_fail(TDP_ERR_CUDA, cudaGetErrorString(err));
 }
 
@@ -485,9 +609,7 @@ extern "C" tdp_status tdp_rms_norm_grad_workspace(tdp_plan_t plan, int64_t rows,
     if (!bytes) return tdp_fail(TDP_ERR_INVALID_ARG, "null bytes");
     const tdp_status st = norm_check(plan, rows, C, &nv);
     if (st != TDP_OK) return st;
-    unsigned grid = 0;
-    grad_deal(nv, C, &grid, rows);
-    *bytes = (int64_t)grid * C * 4;
+    *bytes = norm_deal(rows, nv).blocks * C * 4;
     return tdp_ok();
 }
 
@@ -498,12 +620,11 @@ extern "C" tdp_status tdp_rms_norm_grad(tdp_plan_t plan, int64_t rows, int32_t C
     int32_t nv = 0;
     const tdp_status st = norm_check(plan, rows, C, &nv);
     if (st != TDP_OK) return st;
-    unsigned grid = 0;
-    const norm_shape sh = grad_deal(nv, C, &grid, rows);
+    const norm_shape sh = norm_deal(rows, nv);
     if (rows > 0) {
         if (!rstd || !dy || !dx) return tdp_fail(TDP_ERR_INVALID_ARG, "null rstd, dy or dx");
         if (!h == !x8 || !x8 != !x8_scale) return tdp_fail(TDP_ERR_INVALID_ARG, "need h, or x8 with its scales, and not both");
-        if (dw && (!ws || ws_bytes < (int64_t)grid * C * 4)) return tdp_fail(TDP_ERR_INVALID_ARG, "ws too small");
+        if (dw && (!ws || ws_bytes < sh.blocks * C * 4)) return tdp_fail(TDP_ERR_INVALID_ARG, "ws too small");
         if (!tdp_aligned(h, 16) || !tdp_aligned(x8, 16) || !tdp_aligned(w, 16) || !tdp_aligned(dy, 16) || !tdp_aligned(dh, 16) ||
             !tdp_aligned(dx, 16) || !tdp_aligned(x8_scale, 4) || !tdp_aligned(rstd, 4) || !tdp_aligned(ws, 256))
             return tdp_fail(TDP_ERR_MISALIGNED, "rows and w need 16-byte, scales and rstd 4-byte, ws 256-byte alignment");
@@ -513,17 +634,13 @@ extern "C" tdp_status tdp_rms_norm_grad(tdp_plan_t plan, int64_t rows, int32_t C
     cudaError_t err = cudaSuccess;
     if (rows > 0) {
         norm_grad_args a = {rows, C, nv, sh.lanes, sh.warps, 1.f / (float)C, h, w, dy, dh, x8, x8_scale, rstd, dx, dw ? static_cast<float *>(ws) : nullptr};
-        const size_t smem = dw && sh.rows > 1 ? (size_t)sh.rows * C * 4 : 0;        // 32 KB at most
         const int bf16 = plan->g.dtype == TDP_BF16;
 #define TDP_GRAD(V) \
-    (bf16 ? (x8 ? tdp_launch_smem(true, tdp_rms_norm_grad_kernel<1, V, 1>, grid, sh.threads, smem, s, a) \
-                : tdp_launch_smem(true, tdp_rms_norm_grad_kernel<1, V, 0>, grid, sh.threads, smem, s, a)) \
-          : (x8 ? tdp_launch_smem(true, tdp_rms_norm_grad_kernel<0, V, 1>, grid, sh.threads, smem, s, a) \
-                : tdp_launch_smem(true, tdp_rms_norm_grad_kernel<0, V, 0>, grid, sh.threads, smem, s, a)))
+    (bf16 ? (x8 ? grad_launch<1, V, 1>(sh, a, s) : grad_launch<1, V, 0>(sh, a, s)) : (x8 ? grad_launch<0, V, 1>(sh, a, s) : grad_launch<0, V, 0>(sh, a, s)))
         err = sh.vpt == 1 ? TDP_GRAD(1) : sh.vpt == 2 ? TDP_GRAD(2) : sh.vpt == 4 ? TDP_GRAD(4) : TDP_GRAD(8);
 #undef TDP_GRAD
     }
     if (err == cudaSuccess && dw)
-        err = tdp_launch(true, tdp_rms_norm_dw_kernel, (unsigned)((C + 31) / 32), 1024, s, static_cast<const float *>(ws), (int32_t)grid, C, dw);
+        err = tdp_launch(true, tdp_rms_norm_dw_kernel, (unsigned)((C + 31) / 32), 1024, s, static_cast<const float *>(ws), (int32_t)sh.blocks, C, dw);
     return err == cudaSuccess ? tdp_ok() : tdp_fail(TDP_ERR_CUDA, cudaGetErrorString(err));
 }

@@ -143,6 +143,8 @@ def test_rows_that_hold_anything(tdp, dtype, C):
         assert torch.isnan(ys[i]) and torch.isnan(y8[i].float()).all()
     assert torch.isnan(y[1]).all() and torch.isnan(rstd[1]) and rstd[2] == 0
     assert (y[3] == 0).all() and (y8[3].float() == 0).all() and abs(float(ys[3]) * 448 / 2.0 ** -100 - 1) < 1e-6
+    tdp.tdp_rms_norm(plan, x[3:4], None, None, y8=y8[3:4], y8_scale=ys[3:4], eps=1e-20)      # 448 / scale / sqrt(eps) is no float
+    assert (y8[3].float() == 0).all()
     # rows of nothing but small values
     v8, vs = torch.empty_like(y8), torch.empty_like(ys)
     tdp.tdp_quant8(plan, x, v8, vs)
