@@ -188,6 +188,7 @@ class Plan:
         self._h = ctypes.c_void_p(handle)
         self.problem = problem
         self.sizes = {}             # workspace bytes by shape
+        self.lat = None             # element types of the plan's dtype, once asked for
         self.scratch = _Scratch()
         n = ctypes.c_int32()
         tot = ctypes.c_int64()
@@ -341,14 +342,35 @@ class _Call:
     def __init__(self, where):
         self.where = where
         self.named = []
+        self.dev = None             # index of the device so far; -1: more than one
+
+    def on(self, t, name):
+        self.named.append((name, t))
+        d = t.get_device()
+        if self.dev is None:
+            self.dev = d
+        elif self.dev != d:
+            self.dev = -1
 
     def ptr(self, t, name, numel, dtypes, align):
+        if t is None:
+            return None
+        # a buffer that is as it must be is seen to be so first: a call of ten small buffers is bound by this
+        if _torch_module is not None and isinstance(t, _torch_module.Tensor) and t.is_cuda and t.dtype in dtypes and \
+                t.numel() == numel and t.is_contiguous():
+            p = t.data_ptr()
+            if not p % align:
+                self.on(t, name)
+                return p
         p = _ptr(t, name, numel, dtypes, align)
-        self.named.append((name, t))
+        self.on(t, name)
         return p
 
     def run(self, fn, *args, stream=None):
         torch = _torch()
+        if stream is None and self.dev is not None and self.dev >= 0 and _current() and self.dev == _current_device():
+            _check(fn(*args, _current_stream(self.dev)), self.where)
+            return
         dev = _common_device(self.where, self.named)
         if dev is None:
             dev = torch.device("cuda", torch.cuda.current_device())
@@ -359,8 +381,23 @@ class _Call:
             _check(fn(*args, _stream_handle(self.where, stream, dev)), self.where)
 
 
+_current_device = _current_stream = None
+
+
+def _current():
+    """Whether torch tells the current device, and a device's current stream, without objects around them."""
+    global _current_device, _current_stream
+    if _current_device is None:
+        c = _torch()._C
+        _current_stream = getattr(c, "_cuda_getCurrentRawStream", None)
+        _current_device = getattr(c, "_cuda_getDevice", None) if _current_stream is not None else False
+    return _current_device
+
+
 def _latent_dtypes(plan):
-    return (_torch().float32,) if plan.dtype == TDP_F32 else (_torch().bfloat16,)
+    if plan.lat is None:
+        plan.lat = (_torch().float32,) if plan.dtype == TDP_F32 else (_torch().bfloat16,)
+    return plan.lat
 
 
 def tdp_pos_bounds(plan: Plan, P, mn, mx, stream=None):
@@ -662,7 +699,7 @@ def _xattn_mask(c, plan, a, mask):
 
 
 def _given(c, t, name):
-    c.named.append((name, t))
+    c.on(t, name)
     return t.data_ptr()
 
 
@@ -782,10 +819,15 @@ def tdp_dropout_grad(plan: Plan, dout, p, rng, dx, stream=None):
           c.ptr(dx, "dx", n, lat, 16), stream=stream)
 
 
+_types8 = None
+
+
 def _bytes8():
     """Types of 8-bit rows: e4m3, or its bytes."""
-    torch = _torch()
-    return (torch.float8_e4m3fn, torch.uint8)
+    global _types8
+    if _types8 is None:
+        _types8 = (_torch().float8_e4m3fn, _torch().uint8)
+    return _types8
 
 
 def _matrix(x, name):

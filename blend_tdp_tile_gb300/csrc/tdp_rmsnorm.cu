@@ -29,7 +29,8 @@ using tdp_tc::pair;
 using tdp_tc::unpair;
 
 constexpr int kNormThreads = 256;           // threads of a block at most: eight warps a row
-constexpr int kNormVecs = 4;                // vectors of a lane, but for rows of more than 1024
+constexpr int kNormVecs = 8, kGradVecs = 4; // vectors of a lane, forward and gradient (more for rows of more than 1024)
+constexpr int kSMs = 152;
 constexpr int kNormSmem = 196608;           // bytes of rows that an SM has on their way and at work
 constexpr float kLeast = 0x1p-100f;
 
@@ -161,7 +162,7 @@ __device__ __forceinline__ void join(int32_t lanes, int32_t warps, int32_t turn,
         }
     }
     if (warps == 1) return;
-    const int32_t k = turn & 1, w = threadIdx.x >> 5;
+    const int32_t k = turn & 1, w = threadIdx.x >> 5, first = w - w % warps;
     if ((threadIdx.x & 31) == 0) {
         ssum[k][w] = sum;
         if (TOP) {
@@ -169,14 +170,15 @@ __device__ __forceinline__ void join(int32_t lanes, int32_t warps, int32_t turn,
             stop2[k][w] = top2;
         }
     }
-    __syncthreads();            // the other half is written next: one barrier a round is enough
+    // the team's own barrier; the other half is written next: one a round is enough
+    asm volatile("bar.sync %0, %1;" ::"r"(1 + first), "r"(lanes) : "memory");
     sum = 0.f;
     top = top2 = 0.f;
     for (int32_t i = 0; i < warps; ++i) {
-        sum += ssum[k][i];
+        sum += ssum[k][first + i];
         if (TOP) {
-            top = max_nan(top, stop[k][i]);
-            top2 = max_nan(top2, stop2[k][i]);
+            top = max_nan(top, stop[k][first + i]);
+            top2 = max_nan(top2, stop2[k][first + i]);
         }
     }
 }
@@ -486,21 +488,33 @@ struct norm_shape {
     int64_t blocks;
 };
 
-norm_shape norm_deal(int64_t rows, int32_t nv)
+// vecs: vectors of a lane at most, as long as eight warps hold a row.  Few rows take more lanes each.
+norm_shape norm_deal(int64_t rows, int32_t nv, int32_t vecs, bool wide)
 {
     norm_shape s;
     s.nv = nv;
     s.lanes = 1;
     while (s.lanes < 32 && s.lanes < nv) s.lanes *= 2;
-    s.warps = std::min(kNormThreads / 32, (nv + 32 * kNormVecs - 1) / (32 * kNormVecs));
+    if (rows <= 2 * kSMs) vecs = 2;
+    // the fewest places for the row's vectors, with few warps: 640 vectors are five a lane of four warps and not eight of three
+    // (20000 rows of 5120 bf16 into 8 bits 122 us for 189), but 160 three of two and not one of five (the gradient 40 us for 85)
+    const auto of_lane = [nv](int32_t lanes) {
+        const int32_t need = (nv + lanes - 1) / lanes;
+        return need == 7 ? 8 : need;
+    };
+    s.warps = std::min(kNormThreads / 32, (nv + 32 * vecs - 1) / (32 * vecs));
+    for (int32_t w = s.warps + 1; s.lanes == 32 && w <= kNormThreads / 32; ++w)
+        if (w * of_lane(32 * w) < s.warps * of_lane(32 * s.warps) && 2 * of_lane(32 * w) > of_lane(32 * s.warps)) s.warps = w;
     s.lanes *= s.warps;
-    const int32_t need = (nv + s.lanes - 1) / s.lanes;
-    s.vpt = need <= 1 ? 1 : need <= 2 ? 2 : need <= 4 ? 4 : 8;
-    s.threads = s.warps == 1 ? 128 : 32 * s.warps;
-    s.rows = s.threads / s.lanes;
+    s.vpt = of_lane(s.lanes);
+    // rows of a block: as many as fit where there are rows for all SMs; one of several warps in the forward
+    const int32_t least = std::max(1, 32 / s.lanes), most = s.warps > 1 && !wide ? 1 : kNormThreads / s.lanes;
+    s.rows = least;
+    while (2 * s.rows <= most && rows >= 2 * s.rows * kSMs) s.rows *= 2;
+    s.threads = s.rows * s.lanes;
     // as many blocks as are resident: 96 bytes of shared memory a vector, registers for 768 threads at most
     const int32_t sm = std::max(1, std::min(kNormSmem / (96 * s.vpt), 768) / s.threads);
-    s.blocks = std::min<int64_t>((rows + s.rows - 1) / s.rows, 152 * sm);
+    s.blocks = std::min<int64_t>((rows + s.rows - 1) / s.rows, kSMs * sm);
     return s;
 }
 
@@ -541,7 +555,15 @@ template <int NORM, int Q8, int RES>
 cudaError_t norm_launch(int bf16, const norm_shape &sh, const norm_args &a, cudaStream_t s)
 {
 #define TDP_NORM(V) (bf16 ? norm_launch<1, V, NORM, Q8, RES>(sh, a, s) : norm_launch<0, V, NORM, Q8, RES>(sh, a, s))
-    return sh.vpt == 1 ? TDP_NORM(1) : sh.vpt == 2 ? TDP_NORM(2) : sh.vpt == 4 ? TDP_NORM(4) : TDP_NORM(8);
+    switch (sh.vpt) {
+    case 1: return TDP_NORM(1);
+    case 2: return TDP_NORM(2);
+    case 3: return TDP_NORM(3);
+    case 4: return TDP_NORM(4);
+    case 5: return TDP_NORM(5);
+    case 6: return TDP_NORM(6);
+    default: return TDP_NORM(8);
+    }
 #undef TDP_NORM
 }
 
@@ -552,6 +574,20 @@ cudaError_t grad_launch(const norm_shape &sh, const norm_grad_args &a, cudaStrea
     auto *kernel = tdp_rms_norm_grad_kernel<BF16, VPT, KEPT8>;
     const cudaError_t e = allow_smem(kernel, 96 * VPT * kNormThreads, done);
     return e != cudaSuccess ? e : tdp_launch_smem(true, kernel, (unsigned)sh.blocks, sh.threads, (size_t)96 * VPT * sh.threads, s, a);
+}
+
+template <int BF16, int KEPT8>
+cudaError_t grad_launch(const norm_shape &sh, const norm_grad_args &a, cudaStream_t s)
+{
+    switch (sh.vpt) {
+    case 1: return grad_launch<BF16, 1, KEPT8>(sh, a, s);
+    case 2: return grad_launch<BF16, 2, KEPT8>(sh, a, s);
+    case 3: return grad_launch<BF16, 3, KEPT8>(sh, a, s);
+    case 4: return grad_launch<BF16, 4, KEPT8>(sh, a, s);
+    case 5: return grad_launch<BF16, 5, KEPT8>(sh, a, s);
+    case 6: return grad_launch<BF16, 6, KEPT8>(sh, a, s);
+    default: return grad_launch<BF16, 8, KEPT8>(sh, a, s);
+    }
 }
 
 }  // namespace
@@ -570,7 +606,7 @@ extern "C" tdp_status tdp_rms_norm(tdp_plan_t plan, int64_t rows, int32_t C, flo
     if (!tdp_aligned(x, 16) || !tdp_aligned(res, 16) || !tdp_aligned(w, 16) || !tdp_aligned(h, 16) || !tdp_aligned(y, 16) ||
         !tdp_aligned(y8, 16) || !tdp_aligned(x8, 16) || !tdp_aligned(rstd, 4) || !tdp_aligned(y8_scale, 4) || !tdp_aligned(x8_scale, 4))
         return tdp_fail(TDP_ERR_MISALIGNED, "rows and w need 16-byte, scales and rstd 4-byte alignment");
-    const norm_shape sh = norm_deal(rows, nv);
+    const norm_shape sh = norm_deal(rows, nv, kNormVecs, false);
     norm_args a = {rows, C, nv, sh.lanes, sh.warps, eps, 1.f / (float)C, x, res, w, h, y, rstd, y8, x8, y8_scale, x8_scale};
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     const int bf16 = plan->g.dtype == TDP_BF16;
@@ -589,7 +625,7 @@ extern "C" tdp_status tdp_quant8(tdp_plan_t plan, int64_t rows, int32_t C, const
     if (!x || !x8 || !x8_scale) return tdp_fail(TDP_ERR_INVALID_ARG, "null x, x8 or x8_scale");
     if (!tdp_aligned(x, 16) || !tdp_aligned(x8, 16) || !tdp_aligned(x8_scale, 4))
         return tdp_fail(TDP_ERR_MISALIGNED, "rows need 16-byte, scales 4-byte alignment");
-    const norm_shape sh = norm_deal(rows, nv);
+    const norm_shape sh = norm_deal(rows, nv, kNormVecs, false);
     norm_args a = {};
     a.rows = rows;
     a.C = C;
@@ -609,7 +645,7 @@ extern "C" tdp_status tdp_rms_norm_grad_workspace(tdp_plan_t plan, int64_t rows,
     if (!bytes) return tdp_fail(TDP_ERR_INVALID_ARG, "null bytes");
     const tdp_status st = norm_check(plan, rows, C, &nv);
     if (st != TDP_OK) return st;
-    *bytes = norm_deal(rows, nv).blocks * C * 4;
+    *bytes = norm_deal(rows, nv, kGradVecs, true).blocks * C * 4;
     return tdp_ok();
 }
 
@@ -620,7 +656,7 @@ extern "C" tdp_status tdp_rms_norm_grad(tdp_plan_t plan, int64_t rows, int32_t C
     int32_t nv = 0;
     const tdp_status st = norm_check(plan, rows, C, &nv);
     if (st != TDP_OK) return st;
-    const norm_shape sh = norm_deal(rows, nv);
+    const norm_shape sh = norm_deal(rows, nv, kGradVecs, true);
     if (rows > 0) {
         if (!rstd || !dy || !dx) return tdp_fail(TDP_ERR_INVALID_ARG, "null rstd, dy or dx");
         if (!h == !x8 || !x8 != !x8_scale) return tdp_fail(TDP_ERR_INVALID_ARG, "need h, or x8 with its scales, and not both");
@@ -634,11 +670,8 @@ extern "C" tdp_status tdp_rms_norm_grad(tdp_plan_t plan, int64_t rows, int32_t C
     cudaError_t err = cudaSuccess;
     if (rows > 0) {
         norm_grad_args a = {rows, C, nv, sh.lanes, sh.warps, 1.f / (float)C, h, w, dy, dh, x8, x8_scale, rstd, dx, dw ? static_cast<float *>(ws) : nullptr};
-        const int bf16 = plan->g.dtype == TDP_BF16;
-#define TDP_GRAD(V) \
-    (bf16 ? (x8 ? grad_launch<1, V, 1>(sh, a, s) : grad_launch<1, V, 0>(sh, a, s)) : (x8 ? grad_launch<0, V, 1>(sh, a, s) : grad_launch<0, V, 0>(sh, a, s)))
-        err = sh.vpt == 1 ? TDP_GRAD(1) : sh.vpt == 2 ? TDP_GRAD(2) : sh.vpt == 4 ? TDP_GRAD(4) : TDP_GRAD(8);
-#undef TDP_GRAD
+        err = plan->g.dtype == TDP_BF16 ? (x8 ? grad_launch<1, 1>(sh, a, s) : grad_launch<1, 0>(sh, a, s))
+                                        : (x8 ? grad_launch<0, 1>(sh, a, s) : grad_launch<0, 0>(sh, a, s));
     }
     if (err == cudaSuccess && dw)
         err = tdp_launch(true, tdp_rms_norm_dw_kernel, (unsigned)((C + 31) / 32), 1024, s, static_cast<const float *>(ws), (int32_t)sh.blocks, C, dw);

@@ -110,10 +110,14 @@ tdp_rope_kernel(const __grid_constant__ tdp_geom g, const __grid_constant__ rope
     if (!turns) {
         // what lies behind the pairs is copied
         if (x == out && a.x_head == a.out_head) return;
-        for (int32_t h = group; h < a.heads; h += a.groups) {
-            uint32_t u[U];
-            load<BF16, W>(x + h * a.x_head, u);
-            store<BF16, W>(out + h * a.out_head, u);
+        for (int32_t h0 = group; h0 < a.heads; h0 += 2 * kRopeAhead * a.groups) {
+            uint32_t u[2 * kRopeAhead][U];
+#pragma unroll
+            for (int k = 0; k < 2 * kRopeAhead; ++k)
+                if (h0 + k * a.groups < a.heads) load<BF16, W>(x + (h0 + k * a.groups) * a.x_head, u[k]);
+#pragma unroll
+            for (int k = 0; k < 2 * kRopeAhead; ++k)
+                if (h0 + k * a.groups < a.heads) store<BF16, W>(out + (h0 + k * a.groups) * a.out_head, u[k]);
         }
         return;
     }
