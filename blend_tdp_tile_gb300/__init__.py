@@ -625,6 +625,10 @@ def _rows(plan):
 def _strides(t, name, shape, dtypes):
     """Element strides of a tensor of `shape` whose last dimension is contiguous (0 along dimensions of one)."""
     torch = _torch()
+    if isinstance(t, torch.Tensor) and t.is_cuda and t.dtype in dtypes and t.shape == shape and 1 not in shape and 0 not in shape:
+        *st, last = t.stride()
+        if last == 1 and not t.data_ptr() % 16:
+            return tuple(st)
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name}: expected a torch.Tensor")
     if not t.is_cuda:
@@ -940,12 +944,10 @@ def _rope(where, fn, plan, x, Q, table, out, layout, at, scale, stream):
         raise TypeError(f"{where}: expected torch.Tensors")
     if x.dim() != 3:
         raise ValueError("rows must be [rows, heads, D]")
-    a = _Rope()
-    shape = (_rows(plan), int(x.shape[1]), int(x.shape[2]))
-    a.heads, a.head_dim, a.rot = shape[1], shape[2], 2 * table.numel()
-    a.layout, a.at, a.scale = _named(layout, _LAYOUTS, "layout"), _named(at, _PLACES, "at"), scale
-    a.x_row, a.x_head = _strides(x, "x", shape, lat)
-    a.out_row, a.out_head = _strides(out, "out", shape, lat)
+    R, H, D = x.shape
+    shape = (_rows(plan), H, D)
+    a = _Rope(H, D, 2 * table.numel(), _named(layout, _LAYOUTS, "layout"), _named(at, _PLACES, "at"), scale,
+              *_strides(x, "x", shape, lat), *_strides(out, "out", shape, lat))
     c = _Call(where)
     c.run(fn, plan.handle, ctypes.byref(a), _given(c, x, "x"), c.ptr(Q, "Q", 6 * shape[0], (torch.int32,), 8),
           c.ptr(table, "table", table.numel(), (torch.int64,), 8), _given(c, out, "out"), stream=stream)

@@ -483,19 +483,20 @@ cudaError_t pair_launch(args a, const void *w8, const void *x8, int64_t K, cudaS
     return launch_clusters(tdp_matmul8_pair_kernel<BF16>, 2 * std::min(a.tiles, 76), 2, kPairThreads, bytes, s, a, x, w, o);
 }
 
-// Rows of a tile, or 0 for pairs: the least time of launch and join plus rounds of resident blocks times stages of a block, in
-// us as measured.  K = N = 2048, 16 / 128 / 512 / 1024 / 2048 rows: 3.9 / 5.3 / 13.1 / 24.7 / - by 16 rows, 4.5 / 5.2 / 7.3 / 14.0 / -
-// by 32, 6.0 / 6.6 / 7.5 / 9.6 / - by 64, 8.8 / 9.3 / 9.5 / 9.8 / 10.6 by pairs; K = N = 4096: 4.7 / 9.9 / 37.7 / 70.6, 5.9 / 7.9 /
-// 21.5 / 41.5, 8.5 / 7.9 / 13.7 / 26.2 and 13.0 / 13.6 / 14.0 / 15.3 / 24.0.  (Tiles of 128 rows were never best.)
+// Rows of a tile, or 0 for pairs: the least time of the launch and of rounds of resident blocks, each so much for its end and for
+// every stage of a block, in us as measured.  K = N = 2048, 16 / 128 / 512 / 1024 / 2048 rows: 3.9 / 5.3 / 13.1 / 24.7 / - by 16 rows,
+// 4.5 / 5.2 / 7.3 / 14.0 / - by 32, 6.0 / 6.6 / 7.5 / 9.6 / - by 64, 8.8 / 9.3 / 9.5 / 9.8 / 10.6 by pairs; K = N = 4096: 4.7 / 9.9 / 37.7 /
+// 70.6, 5.9 / 7.9 / 21.5 / 41.5, 8.5 / 7.9 / 13.7 / 26.2 and 13.0 / 13.6 / 14.0 / 15.3 / 24.0.  (Tiles of 128 rows were never best;
+// eight stages in place of four, and so one block an SM, took 8.1 us where 32 rows take 5.2.)
 int choose(int64_t rows, int32_t N, int32_t kb)
 {
     constexpr int nt[3] = {16, 32, 64};
-    constexpr double base[3] = {3.3, 3.6, 4.4}, stage[3] = {0.20, 0.235, 0.285};
+    constexpr double end[3] = {2.3, 2.6, 3.4}, stage[3] = {0.20, 0.235, 0.285};
     double least = 5.0 + 0.275 * kb * (double)(((rows + 255) / 256 * ((N + 255) / 256) + 75) / 76);
     int best = 0;
     for (int i = 0; i < 3; ++i) {
         const int64_t tiles = (rows + nt[i] - 1) / nt[i] * ((N + 127) / 128), split = split_k(tiles, kb);
-        const double cost = base[i] + stage[i] * (double)((kb + split - 1) / split) * (double)((tiles * split + 303) / 304);
+        const double cost = 1.0 + (end[i] + stage[i] * (double)((kb + split - 1) / split)) * (double)((tiles * split + 303) / 304);
         if (cost < least) {
             least = cost;
             best = nt[i];

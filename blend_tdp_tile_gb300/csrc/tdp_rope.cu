@@ -86,8 +86,8 @@ __device__ __forceinline__ void pack(const float *f, uint32_t *u)
 }
 
 // HALF: element i and i + pairs are a pair, an item two vectors of W elements; otherwise elements 2 i and 2 i + 1, an item
-// one vector (W even).  W is 16 bytes where rot, and half of it, allow that.
-template <int BF16, int W, int HALF>
+// one vector (W even).  W is 16 bytes where rot, and half of it, allow that.  REST: a head has more than its pairs.
+template <int BF16, int W, int HALF, int REST>
 __global__ void __launch_bounds__(kRopeThreads)
 tdp_rope_kernel(const __grid_constant__ tdp_geom g, const __grid_constant__ rope_args a)
 {
@@ -101,7 +101,7 @@ tdp_rope_kernel(const __grid_constant__ tdp_geom g, const __grid_constant__ rope
     if (tr >= a.rows || j >= sg.T) return;
     const int32_t group = place / a.items, item = place - group * a.items;
     const int64_t row = sg.row0 + j;
-    const bool turns = item < a.turned;
+    const bool turns = !REST || item < a.turned;
     // where the item's vectors lie in a head
     const int32_t o0 = turns ? item * B : (2 * a.pairs * (BF16 ? 2 : 4) + (item - a.turned) * B);
     const int32_t o1 = o0 + a.pairs * (BF16 ? 2 : 4);
@@ -230,15 +230,14 @@ tdp_status rope(tdp_plan_t plan, const tdp_rope_shape *p, const void *x, const i
     a.scale = p->scale;
     const unsigned grid = (unsigned)(blocks * g.nt * g.B);
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-#define TDP_ROPE(BF, W) \
-    (half ? tdp_launch(true, tdp_rope_kernel<BF, W, 1>, grid, kRopeThreads, s, g, a) \
-          : tdp_launch(true, tdp_rope_kernel<BF, W, 0>, grid, kRopeThreads, s, g, a))
+    const bool rest = p->head_dim > p->rot;
+#define TDP_ROPE(BF, W, H) \
+    (rest ? tdp_launch(true, tdp_rope_kernel<BF, W, H, 1>, grid, kRopeThreads, s, g, a) : tdp_launch(true, tdp_rope_kernel<BF, W, H, 0>, grid, kRopeThreads, s, g, a))
+#define TDP_ROPE2(BF, W) (half ? TDP_ROPE(BF, W, 1) : TDP_ROPE(BF, W, 0))
     cudaError_t err;
-    if (g.dtype == TDP_BF16)
-        err = W == 8 ? TDP_ROPE(1, 8) : W == 4 ? TDP_ROPE(1, 4) : W == 2 ? TDP_ROPE(1, 2) :
-              tdp_launch(true, tdp_rope_kernel<1, 1, 1>, grid, kRopeThreads, s, g, a);      // odd halves alone
-    else
-        err = W == 4 ? TDP_ROPE(0, 4) : W == 2 ? TDP_ROPE(0, 2) : tdp_launch(true, tdp_rope_kernel<0, 1, 1>, grid, kRopeThreads, s, g, a);
+    if (g.dtype == TDP_BF16) err = W == 8 ? TDP_ROPE2(1, 8) : W == 4 ? TDP_ROPE2(1, 4) : W == 2 ? TDP_ROPE2(1, 2) : TDP_ROPE(1, 1, 1);     // odd halves alone
+    else err = W == 4 ? TDP_ROPE2(0, 4) : W == 2 ? TDP_ROPE2(0, 2) : TDP_ROPE(0, 1, 1);
+#undef TDP_ROPE2
 #undef TDP_ROPE
     return err == cudaSuccess ? tdp_ok() : tdp_fail(TDP_ERR_CUDA, cudaGetErrorString(err));
 }
