@@ -6,9 +6,12 @@ put the library's operators on tile-major rows under torch's autograd:
   group_norm(plan, x, groups, gamma, beta)   statistics of every (tile, item), channels last, SiLU
   cross_attn(plan, q, k, v, mask)            tile rows attend to an encoder's states
   dropout_add(plan, x, res, p, rng)          residual + dropout whose mask is never stored
+  rms_norm(plan, x, w, res)                  residual + root-mean-square norm; its checkpoint in 8 bits, if asked for
+  rope(plan, x, Q, table)                    heads turned by the positions that the split hands out
 
 ``TileBlock`` is one cross-attention sublayer of them: normalise, project, attend, project back,
-drop out and add.  All tiles go through each call at once; nothing is padded.  The gradients are first ones: a
+drop out and add.  ``RotaryBlock`` attends to the conditioning tokens that each tile keeps, at their positions, and serves
+with its projections in 8 bits (``Linear8``).  All tiles go through each call at once; nothing is padded.  The gradients are first ones: a
 derivative of theirs raises an error.
 """
 from __future__ import annotations
@@ -17,9 +20,10 @@ import torch
 from torch.autograd.function import once_differentiable
 
 from . import (Plan, tdp_cross_attn, tdp_cross_attn_grad, tdp_dropout_add, tdp_dropout_grad, tdp_group_norm,
-               tdp_group_norm_grad)
+               tdp_group_norm_grad, tdp_matmul8, tdp_quant8, tdp_rms_norm, tdp_rms_norm_grad, tdp_rope, tdp_rope_freqs,
+               tdp_rope_grad, tdp_rope_table)
 
-__all__ = ["group_norm", "cross_attn", "dropout_add", "TileBlock"]
+__all__ = ["group_norm", "cross_attn", "dropout_add", "rms_norm", "rope", "quant8", "Linear8", "TileBlock", "RotaryBlock"]
 
 
 def _dense(t):
@@ -91,6 +95,62 @@ class _DropoutAdd(torch.autograd.Function):
         return None, dx, dout if ctx.residual else None, None, None
 
 
+def _heads(t):
+    """t [rows, heads, D] as tdp_rope takes it: strides and start on 16 bytes."""
+    unit = 16 // t.element_size()
+    ok = t.stride(-1) == 1 and t.data_ptr() % 16 == 0 and all(s % unit == 0 for s, n in zip(t.stride()[:2], t.shape) if n > 1)
+    return t if ok else _dense(t)
+
+
+class _RmsNorm(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, plan, x, w, res, eps, keep8):
+        x = _dense(x)
+        rows = x.numel() // x.shape[-1]
+        y, rstd = torch.empty_like(x), torch.empty(rows, dtype=torch.float32, device=x.device)
+        h, res = (x, None) if res is None else (torch.empty_like(x), _dense(res))
+        x8 = torch.empty(x.shape, dtype=torch.float8_e4m3fn, device=x.device) if keep8 else None
+        scale = torch.empty_like(rstd) if keep8 else None
+        tdp_rms_norm(plan, x, w, y, res=res, h=None if res is None else h, rstd=rstd, x8=x8, x8_scale=scale, eps=eps)
+        ctx.plan, ctx.residual = plan, res is not None
+        ctx.save_for_backward(w, rstd, None if keep8 else h, x8, scale)
+        ctx.set_materialize_grads(False)
+        return (y, h) if res is not None else y
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy, dh=None):
+        w, rstd, h, x8, scale = ctx.saved_tensors
+        kept = h if x8 is None else x8
+        if dy is None:              # the norm's output has no part in it
+            dx = None if dh is None else _dense(dh)
+            return None, dx, None, dx if ctx.residual else None, None, None
+        dy = _dense(dy)
+        dx = torch.empty_like(dy)
+        dw = torch.empty(dy.shape[-1], dtype=torch.float32, device=dy.device) if ctx.needs_input_grad[2] else None
+        tdp_rms_norm_grad(ctx.plan, dy, dx, w, rstd, h=None if x8 is not None else kept, x8=x8, x8_scale=scale,
+                          dh=None if dh is None else _dense(dh), dw=dw)
+        return None, dx, None if dw is None else dw.to(w.dtype), dx if ctx.residual else None, None, None
+
+
+class _Rope(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, plan, x, Q, table, layout, at, scale):
+        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        tdp_rope(plan, _heads(x), Q, table, out, layout=layout, at=at, scale=scale)
+        ctx.plan, ctx.how = plan, dict(layout=layout, at=at, scale=scale)
+        ctx.save_for_backward(Q, table)
+        return out
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dout):
+        Q, table = ctx.saved_tensors
+        dx = torch.empty(dout.shape, dtype=dout.dtype, device=dout.device)
+        tdp_rope_grad(ctx.plan, _heads(dout), Q, table, dx, **ctx.how)
+        return None, dx, None, None, None, None, None
+
+
 def group_norm(plan: Plan, x, groups, gamma=None, beta=None, eps=1e-5, act="none"):
     """act(group norm of every (tile, item) of tile-major rows x [R, C]) with gradients for x, gamma and beta."""
     return _GroupNorm.apply(plan, x, groups, gamma, beta, eps, act)
@@ -107,6 +167,54 @@ def dropout_add(plan: Plan, x, res, p, rng):
     """res + dropout(x) with the generator of rng (two 64-bit integers on the device: seed, offset); gradients for
     x and res.  The caller moves the offset on between calls."""
     return _DropoutAdd.apply(plan, x, res, p, rng)
+
+
+def rms_norm(plan: Plan, x, w=None, res=None, eps=1e-6, keep8=False):
+    """Root-mean-square norm of the rows of x [.., C], times w [C]; with res, (the norm of x + res, x + res).  Gradients for x, w
+    and res.  keep8: what is kept for them is the normalised rows in 8 bits, a quarter of fp32's and half of bf16's bytes,
+    and the gradients are of those rows."""
+    return _RmsNorm.apply(plan, x, w, res, eps, keep8)
+
+
+def rope(plan: Plan, x, Q, table, layout="half", at="middle", scale=1.0):
+    """Tile rows x [R, heads, D], every head turned by the rows' positions Q (from tdp_split; table from tdp_rope_table);
+    gradient for x."""
+    return _Rope.apply(plan, x, Q, table, layout, at, scale)
+
+
+def quant8(plan: Plan, x):
+    """(x8, scale): the rows of x [.., C] in 8 bits.  No gradient."""
+    x = _dense(x.detach())
+    x8 = torch.empty(x.shape, dtype=torch.float8_e4m3fn, device=x.device)
+    scale = torch.empty(x.numel() // x.shape[-1], dtype=torch.float32, device=x.device)
+    tdp_quant8(plan, x, x8, scale)
+    return x8, scale
+
+
+class Linear8(torch.nn.Module):
+    """A linear layer with its weights in 8 bits, a scale an output channel, for serving: it has no gradients and raises an
+    error where one is asked for."""
+
+    def __init__(self, plan: Plan, linear: torch.nn.Linear):
+        super().__init__()
+        w8, scale = quant8(plan, linear.weight)
+        self.register_buffer("w8", w8.view(torch.uint8))         # bytes: a change of the module's dtype leaves them
+        self.register_buffer("scale", scale)
+        self.register_buffer("bias", None if linear.bias is None else linear.bias.detach().clone())
+
+    def forward(self, plan: Plan, x, scale=None, res=None):
+        """x [.., K] in the plan's dtype, or in 8 bits with its scale; res: what the product is added to, or None."""
+        if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in (x, res)):
+            raise RuntimeError("Linear8 has no gradient: call it under torch.no_grad()")
+        x8, scale = quant8(plan, x) if scale is None else (x, scale)
+        out = torch.empty((*x8.shape[:-1], self.w8.shape[0]), dtype=plan_dtype(plan), device=x8.device)
+        tdp_matmul8(plan, x8, scale, self.w8, self.scale, out, bias=self.bias, res=None if res is None else _dense(res))
+        return out
+
+
+def plan_dtype(plan: Plan):
+    """torch's name of the plan's element type."""
+    return torch.float32 if plan.esize == 4 else torch.bfloat16
 
 
 class TileBlock(torch.nn.Module):
@@ -134,3 +242,61 @@ class TileBlock(torch.nn.Module):
         kv = self.to_kv(states).view(*states.shape[:2], 2, self.kv_heads, self.head_dim)
         a = self.to_out(cross_attn(plan, q, kv[:, :, 0], kv[:, :, 1], mask).flatten(1))
         return dropout_add(plan, a, x, self.p, rng) if self.training and self.p > 0 else x + a
+
+
+class RotaryBlock(torch.nn.Module):
+    """x + dropout(W_o attn(rope(W_q rms_norm(x)), rope(W_k tokens), W_v tokens)) on tile-major rows x [R, C]: every tile's rows attend
+    to the conditioning tokens that the tile keeps, both turned by their positions.
+
+    pairs: pairs of a head on each of the three axes.  keep8: training keeps the normalised rows in 8 bits.  After to_8bit() the block
+    runs its projections in 8 bits, without gradients, until train() brings the full ones back.  rng as for TileBlock."""
+
+    def __init__(self, channels, heads, kv_heads, head_dim, context, pairs, p=0.0, keep8=False, base=10000.0, scaling="none", factor=1.0,
+                 length=1.0, dtype=torch.bfloat16, device="cuda"):
+        super().__init__()
+        kw = dict(dtype=dtype, device=device)
+        self.heads, self.kv_heads, self.head_dim, self.p, self.keep8 = heads, kv_heads, head_dim, p, keep8
+        freq, axis, self.scale = tdp_rope_freqs(pairs, base, scaling, factor, length)
+        self.register_buffer("table", tdp_rope_table(freq, axis).to(device))
+        self.w = torch.nn.Parameter(torch.ones(channels, **kw))
+        self.to_q = torch.nn.Linear(channels, heads * head_dim, bias=False, **kw)
+        self.to_kv = torch.nn.Linear(context, 2 * kv_heads * head_dim, bias=False, **kw)
+        self.to_out = torch.nn.Linear(heads * head_dim, channels, bias=False, **kw)
+        self.in8 = None
+
+    def to_8bit(self, plan: Plan):
+        self.eval()
+        self.in8 = torch.nn.ModuleDict({n: Linear8(plan, getattr(self, n)) for n in ("to_q", "to_kv", "to_out")})
+        return self
+
+    def train(self, mode=True):
+        if mode:
+            self.in8 = None
+        return super().train(mode)
+
+    def forward(self, plan: Plan, x, Q, tokens_plan: Plan, tokens, P, mask=None, rng=None):
+        """Q: tile-major positions of the rows, from tdp_split with normalize = 0, on the tokens' origin.  tokens [B, S, context] at
+        P [B, 3, S, 2], with tokens_plan an untiled plan of B items of S tokens.  mask [B, S] or [n_tiles, B, S] (tdp_norm_filter's
+        keep), or None."""
+        q, kv = (self._project8 if self.in8 is not None else self._project)(plan, x, tokens)
+        B, S = tokens.shape[:2]
+        kv = kv.view(B * S, 2, self.kv_heads, self.head_dim)
+        q = rope(plan, q.view(-1, self.heads, self.head_dim), Q, self.table, scale=self.scale)
+        k = rope(tokens_plan, kv[:, 0], P, self.table, scale=self.scale)
+        a = cross_attn(plan, q, k.view(B, S, self.kv_heads, self.head_dim), kv.view(B, S, 2, self.kv_heads, self.head_dim)[:, :, 1], mask).flatten(1)
+        if self.in8 is not None:
+            return self.in8["to_out"](plan, a, res=x)
+        a = self.to_out(a)
+        return dropout_add(plan, a, x, self.p, rng) if self.training and self.p > 0 else x + a
+
+    def _project(self, plan, x, tokens):
+        return self.to_q(rms_norm(plan, x, self.w, keep8=self.keep8)), self.to_kv(tokens)
+
+    def _project8(self, plan, x, tokens):
+        if torch.is_grad_enabled() and (x.requires_grad or tokens.requires_grad):
+            raise RuntimeError("a block in 8 bits has no gradient: call it under torch.no_grad()")
+        x = _dense(x.detach())
+        y8 = torch.empty(x.shape, dtype=torch.float8_e4m3fn, device=x.device)
+        scale = torch.empty(x.shape[0], dtype=torch.float32, device=x.device)
+        tdp_rms_norm(plan, x, self.w.detach(), None, y8=y8, y8_scale=scale)
+        return self.in8["to_q"](plan, y8, scale), self.in8["to_kv"](plan, tokens)

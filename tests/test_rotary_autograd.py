@@ -1,0 +1,157 @@
+"""The norm and the rotary positions under autograd, on the CPU: plain torch stands in for the library's calls, which like them
+fill buffers that autograd does not see."""
+import pytest
+
+torch = pytest.importorskip("torch")
+
+from test_abi_host import tdp  # noqa: E402,F401  (fixture)
+
+R, C, H, D = 6, 16, 2, 8
+
+
+def _norm(x, w, res, eps=1e-6):
+    h = x if res is None else x + res
+    return h, h * (h.square().mean(-1, keepdim=True) + eps).rsqrt() * (1 if w is None else w)
+
+
+def _turn(x, back=False):
+    """By one radian more a row."""
+    t = torch.arange(x.shape[0], dtype=x.dtype)[:, None, None] * (-1 if back else 1)
+    a, b = x[..., :D // 2], x[..., D // 2:]
+    return torch.cat((a * t.cos() - b * t.sin(), a * t.sin() + b * t.cos()), -1)
+
+
+@pytest.fixture
+def block(tdp, monkeypatch):  # noqa: F811
+    from blend_tdp_tile_gb300 import block as b
+    seen = []
+
+    def aligned(*ts):
+        for t in ts:
+            if t is not None and (not t.is_contiguous() or t.data_ptr() % 16):
+                raise ValueError("not 16-byte aligned")
+
+    def rms_norm(plan, x, w, y=None, res=None, h=None, rstd=None, y8=None, y8_scale=None, x8=None, x8_scale=None, eps=1e-6):
+        aligned(x, y, res, h)
+        s, out = _norm(x, w, res, eps)
+        y.copy_(out)
+        rstd.copy_((s.square().mean(-1) + eps).rsqrt())
+        if h is not None:
+            h.copy_(s)
+        if x8 is not None:
+            x8_scale.fill_(1 / 64)
+            x8.copy_((s * rstd[:, None] * 64).to(torch.float8_e4m3fn))
+
+    def rms_norm_grad(plan, dy, dx, w, rstd, h=None, x8=None, x8_scale=None, dh=None, dw=None):
+        aligned(dy, dx, dh)
+        assert (h is None) != (x8 is None)
+        seen.append("h" if x8 is None else "x8")
+        u = h * rstd[:, None] if x8 is None else x8.float() * x8_scale[:, None]
+        g = dy if w is None else dy * w
+        dx.copy_(rstd[:, None] * (g - u * (g * u).mean(-1, keepdim=True)) + (0 if dh is None else dh))
+        if dw is not None:
+            dw.copy_((dy * u).sum(0))
+
+    def rope(plan, x, Q, table, out, layout="half", at="middle", scale=1.0):
+        if x.data_ptr() % 16 or any(s % 4 for s in x.stride()[:2]) or x.stride(-1) != 1:
+            raise ValueError("not 16-byte aligned")
+        out.copy_(_turn(x))
+
+    def rope_grad(plan, x, Q, table, out, layout="half", at="middle", scale=1.0):
+        if x.data_ptr() % 16 or any(s % 4 for s in x.stride()[:2]) or x.stride(-1) != 1:
+            raise ValueError("not 16-byte aligned")
+        out.copy_(_turn(x, True))
+
+    for f in (rms_norm, rms_norm_grad, rope, rope_grad):
+        monkeypatch.setattr(b, "tdp_" + f.__name__, f)
+    b.seen = seen
+    return b
+
+
+def _calls(b):
+    torch.manual_seed(0)
+    w, res, Q, t = torch.randn(C), torch.randn(R, C), torch.zeros(6 * R, dtype=torch.int32), torch.zeros(D // 2, dtype=torch.int64)
+    return {"rms_norm": (lambda x: b.rms_norm(None, x, w), torch.randn(R, C).requires_grad_()),
+            "residual": (lambda x: torch.cat(b.rms_norm(None, x, w, res)), torch.randn(R, C).requires_grad_()),
+            "rope": (lambda x: b.rope(None, x, Q, t), torch.randn(R, H, D).requires_grad_())}
+
+
+@pytest.mark.parametrize("name", ["rms_norm", "residual", "rope"])
+def test_first_derivatives(block, name):
+    f, x = _calls(block)[name]
+    y = f(x)
+    w = torch.randn_like(y)
+    got, = torch.autograd.grad((y * w).sum(), x)
+    u, h = torch.randn_like(x), 2.0 ** -6
+    with torch.no_grad():
+        fd = float(((f(x + h * u).double() - f(x - h * u).double()) * w).sum()) / (2 * h)
+    assert abs(fd - float((got * u).sum())) < 1e-2 * float((got * u).abs().sum())
+
+
+@pytest.mark.parametrize("name", ["rms_norm", "residual", "rope"])
+def test_second_derivatives_are_refused(block, name):
+    f, x = _calls(block)[name]
+    g, = torch.autograd.grad(f(x).pow(2).sum() + (x ** 2).sum(), x, create_graph=True)
+    with pytest.raises(RuntimeError, match="once_differentiable"):
+        g.pow(2).sum().backward()
+
+
+@pytest.mark.parametrize("keep8", [False, True])
+@pytest.mark.parametrize("used", ["y", "h", "both"])
+def test_either_output_of_the_residual_norm(block, keep8, used):
+    """x, res and w against plain torch, whichever outputs the loss reads; the checkpoint is off by e4m3's 2^-4."""
+    torch.manual_seed(1)
+    leaves = [torch.randn(R, C, requires_grad=True), torch.randn(C, requires_grad=True), torch.randn(R, C, requires_grad=True)]
+    wy, wh = torch.randn(R, C), torch.randn(R, C)
+
+    def loss(y, h):
+        return ((y * wy).sum() if used != "h" else 0) + ((h * wh).sum() if used != "y" else 0)
+    x, w, res = leaves
+    got = torch.autograd.grad(loss(*block.rms_norm(None, x, w, res, keep8=keep8)), leaves, allow_unused=True)
+    want = torch.autograd.grad(loss(*reversed(_norm(x, w, res))), leaves, allow_unused=True)
+    assert block.seen == ([] if used == "h" else ["x8" if keep8 else "h"])
+    for a, b in zip(got, want):
+        if b is None:
+            assert a is None or float(a.abs().max()) == 0
+        else:
+            assert float((a - b).abs().max()) < (0.3 if keep8 else 1e-4) * float(b.abs().max())
+
+
+def test_a_stream_changed_before_backward_is_refused(block):
+    x = torch.randn(R, C)
+    w = torch.randn(C, requires_grad=True)
+    y = block.rms_norm(None, x, w)
+    x.zero_()
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        y.sum().backward()
+    y = block.rms_norm(None, x, w, keep8=True)       # the checkpoint is its own
+    x.fill_(1)
+    y.sum().backward()
+
+
+def test_positions_changed_before_backward_are_refused(block):
+    Q, x = torch.zeros(6 * R, dtype=torch.int32), torch.randn(R, H, D, requires_grad=True)
+    y = block.rope(None, x, Q, torch.zeros(D // 2, dtype=torch.int64))
+    Q += 1
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        y.sum().backward()
+
+
+@pytest.mark.parametrize("offset", [0, 1, 3])
+@pytest.mark.parametrize("name", ["rms_norm", "rope"])
+def test_slices_at_odd_offsets(block, name, offset):
+    f, x = _calls(block)[name]
+    w = torch.randn(offset + x.numel())
+    y = torch.cat([torch.zeros(offset, requires_grad=True) * 1, f(x).reshape(-1)])
+    got, = torch.autograd.grad((y * w).sum(), x)
+    want, = torch.autograd.grad((f(x).reshape(-1) * w[offset:].clone()).sum(), x)
+    assert torch.equal(got, want)
+    buf = torch.cat([torch.zeros(offset), x.detach().reshape(-1)])
+    assert torch.equal(f(buf[offset:].view(x.shape)), f(x.detach()))
+
+
+def test_layers_in_8_bits_refuse_gradients(block):
+    lin = block.Linear8.__new__(block.Linear8)
+    torch.nn.Module.__init__(lin)
+    with pytest.raises(RuntimeError, match="no gradient"):
+        lin(None, torch.randn(R, C, requires_grad=True))
