@@ -202,17 +202,17 @@ struct pair_smem {
     static constexpr int kStages = 5;
     static constexpr int kOut = 16384;          // two panels of outputs on their way to memory: 128 rows of 64 bytes
     static constexpr int kScales = 2048;        // a tile's scales and bias of 256 channels
-    static constexpr int kBars = 8 * (2 * kStages + 5) + 8;
+    static constexpr int kBars = 8 * (2 * kStages + 5 + 8) + 8;
     // all that a block may have but 768 bytes, which are for the start's rounding up to 1024
     static constexpr int kBytes = 232448;
     static_assert(kStages * kStage + 4 * kOut + kScales + kBars <= kBytes - 768, "room for the stages");
 };
 constexpr int kPairThreads = 640;
 
-template <int BF16>
+template <int BF16, int RES>
 __global__ void __launch_bounds__(kPairThreads, 1)
 tdp_matmul8_pair_kernel(const __grid_constant__ args a, const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_w,
-                        const __grid_constant__ CUtensorMap map_o)
+                        const __grid_constant__ CUtensorMap map_o, const __grid_constant__ CUtensorMap map_r)
 {
     using SM = pair_smem;
     using E = tdp_elem<BF16>;
@@ -224,7 +224,7 @@ tdp_matmul8_pair_kernel(const __grid_constant__ args a, const __grid_constant__ 
     float *scales = reinterpret_cast<float *>(tail);            // channels' scales, then their bias
     volatile int *dead = reinterpret_cast<int *>(tail + SM::kScales);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(tail + SM::kScales + 4);
-    const uint32_t full = smem_u32(tail + SM::kScales + 8), empty = full + 8 * NST, sums = empty + 8 * NST, taken = sums + 16, drain = taken + 16;
+    const uint32_t full = smem_u32(tail + SM::kScales + 8), empty = full + 8 * NST, sums = empty + 8 * NST, taken = sums + 16, drain = taken + 16, added = drain + 8;
     const int32_t warp = warp_id(), lane = threadIdx.x & 31;
     const uint32_t rank = cluster_rank();
     if (warp == 2) pair_alloc(smem_u32(tmem_slot), 512);
@@ -236,6 +236,7 @@ tdp_matmul8_pair_kernel(const __grid_constant__ args a, const __grid_constant__ 
             mbar_init(taken + 8 * i, 32);       // sixteen warps of either block
         }
         mbar_init(drain, 1);
+        for (int i = 0; i < 8; ++i) mbar_init(added + 8 * i, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     fence_before();
@@ -310,12 +311,23 @@ tdp_matmul8_pair_kernel(const __grid_constant__ args a, const __grid_constant__ 
         if (first < a.tiles) ask(first);
         uint32_t n = 0, panel = 0;
         constexpr int W = BF16 ? 32 : 16;       // channels of a panel
+        auto row_of = [&](int32_t t) { return (t / a.tiles_c) * 256 + (int32_t)rank * 128; };
+        auto ch_of = [&](int32_t t) { return (t % a.tiles_c) * 256 + 64 * part; };
+        // channels of a tile that this warpgroup has: panels with anything in them are stored, each
+        auto end_of = [&](int32_t t) { return row_of(t) < a.rows ? min(64, a.N - ch_of(t)) : 0; };
+        // The residual comes into the panel that its sum leaves by, a panel ahead: read by the threads, a row each, it took
+        // 125 us where this takes 107 (35840 x 2048 x 2048).
+        const uint32_t bars = added + 16 * part;
+        uint32_t phases = 0;
+        bool asked = false;
+        auto bring = [&](int32_t t, int32_t c0, uint32_t to_panel) {
+            mbar_expect(bars + 8 * to_panel, 8192);
+            tma_load2(to + to_panel * 8192, &map_r, bars + 8 * to_panel, ch_of(t) + c0, row_of(t));
+        };
 #pragma unroll 1
         for (int32_t t = first; t < a.tiles; t += step, ++n) {
             const uint32_t buf = n & 1;
-            const int32_t row0 = (t / a.tiles_c) * 256 + rank * 128, ch0 = (t % a.tiles_c) * 256 + 64 * part;
-            const int64_t row = row0 + r;
-            const bool on = row < a.rows;
+            const int32_t row0 = row_of(t), ch0 = ch_of(t), end = end_of(t);
             const float xs = x;
             if (r < 64) {
                 scales[64 * part + r] = w;
@@ -327,7 +339,6 @@ tdp_matmul8_pair_kernel(const __grid_constant__ args a, const __grid_constant__ 
             ok = __all_sync(~0u, ok && !*dead);
             fence_after();
             const uint64_t x2 = ok ? pair(xs, xs) : pair(NAN, NAN);
-            const int32_t end = row0 < a.rows ? min(64, a.N - ch0) : 0;
             auto take = [&] {
                 fence_before();
                 __syncwarp();
@@ -339,24 +350,35 @@ tdp_matmul8_pair_kernel(const __grid_constant__ args a, const __grid_constant__ 
                 uint32_t v[W];
                 if (BF16) tmem_ld32(lanes + 256 * buf + c0, v);
                 else tmem_ld16(lanes + 256 * buf + c0, v);
-                uint4 s[4];
-                if (a.res) {
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const int32_t ch = ch0 + c0 + j * E::kVec;
-                        s[j] = on && ch < a.N ? *reinterpret_cast<const uint4 *>(static_cast<const T *>(a.res) + row * a.N + ch) : make_uint4(0, 0, 0, 0);
+                if (RES) {
+                    const bool more = c0 + W < end;
+                    const int32_t t2 = more ? t : t + step, c2 = more ? c0 + W : 0;
+                    const bool next = more || (t2 < a.tiles && end_of(t2) > 0);
+                    if (r == 0) {
+                        tma_store_read();       // both panels have left
+                        if (!asked) bring(t, c0, panel);
+                        if (next) bring(t2, c2, panel ^ 1);
                     }
+                    asked = next;
                 }
                 tmem_wait_ld();
                 if (BF16) tmem_have32(v);
                 else tmem_have16(v);
                 if (c0 + W >= end) take();
-                if (r == 0) tma_store_read_but_one();   // the panel before the last has left
-                group_sync(1 + part);
+                if (RES) {
+                    if (!mbar_wait(bars + 8 * panel, (phases >> panel) & 1, dead)) {
+                        ok = false;
+                        landed(bars + 8 * panel, (phases >> panel) & 1);
+                    }
+                    phases ^= 1u << panel;
+                } else {
+                    if (r == 0) tma_store_read_but_one();       // the panel before the last has left
+                    group_sync(1 + part);
+                }
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    float f[E::kVec], g[E::kVec];
-                    if (a.res) E::unpack(s[j], g);
+                    const uint32_t at = to + panel * 8192 + r * 64 + ((j ^ ((r >> 1) & 3)) << 4);        // the 64-byte swizzle of the maps
+                    float f[E::kVec];
 #pragma unroll
                     for (int q = 0; q < E::kVec; q += 4) {
                         const int c = 64 * part + c0 + j * E::kVec + q;
@@ -365,13 +387,17 @@ tdp_matmul8_pair_kernel(const __grid_constant__ args a, const __grid_constant__ 
                         unpair(fma2(mul2(pair(__uint_as_float(u[0]), __uint_as_float(u[1])), x2), w4.x, b4.x), f[q], f[q + 1]);
                         unpair(fma2(mul2(pair(__uint_as_float(u[2]), __uint_as_float(u[3])), x2), w4.y, b4.y), f[q + 2], f[q + 3]);
                     }
-                    if (a.res) {
+                    if (RES) {
+                        float g[E::kVec];
+                        uint4 s;
+                        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(s.x), "=r"(s.y), "=r"(s.z), "=r"(s.w) : "r"(at) : "memory");
+                        E::unpack(s, g);
 #pragma unroll
-                        for (int q = 0; q < E::kVec; ++q) f[q] += g[q];
+                        for (int q = 0; q < E::kVec; ++q) f[q] = ok ? f[q] + g[q] : NAN;
                     }
                     const uint4 p = E::pack(f);
                     const uint32_t o[4] = {p.x, p.y, p.z, p.w};
-                    st_shared16(to + panel * 8192 + r * 64 + ((j ^ ((r >> 1) & 3)) << 4), o);      // the 64-byte swizzle of map_o
+                    st_shared16(at, o);
                 }
                 fence_async();
                 group_sync(1 + part);
@@ -404,7 +430,7 @@ bool map8(CUtensorMap *map, const void *p, int64_t K, int64_t rows, int box)
                   CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Map of the outputs: boxes of 64 bytes by 128 rows.
+// Map of the outputs, or of the residual: boxes of 64 bytes by 128 rows.
 bool map_out(CUtensorMap *map, void *p, int bf16, int64_t N, int64_t rows)
 {
     PFN_cuTensorMapEncodeTiled_v12000 encode = tdp_encode_tiled();
@@ -469,18 +495,20 @@ cudaError_t tile_launch(const args &a, const void *w8, const void *x8, int64_t K
     return launch_clusters(tdp_matmul8_tile_kernel<BF16, NT>, (unsigned)(tiles * split), split, kTileThreads, bytes, s, a, w, x);
 }
 
-template <int BF16>
+template <int BF16, int RES>
 cudaError_t pair_launch(args a, const void *w8, const void *x8, int64_t K, cudaStream_t s)
 {
     static std::atomic<bool> done[64];
     constexpr size_t bytes = pair_smem::kBytes;
-    cudaError_t e = allow_smem(tdp_matmul8_pair_kernel<BF16>, bytes, done);
-    CUtensorMap w, x, o;
-    if (e == cudaSuccess && (!map8(&w, w8, K, a.N, 128) || !map8(&x, x8, K, a.rows, 128) || !map_out(&o, a.out, BF16, a.N, a.rows))) e = cudaErrorInvalidValue;
+    cudaError_t e = allow_smem(tdp_matmul8_pair_kernel<BF16, RES>, bytes, done);
+    CUtensorMap w, x, o, r;
+    if (e == cudaSuccess && (!map8(&w, w8, K, a.N, 128) || !map8(&x, x8, K, a.rows, 128) || !map_out(&o, a.out, BF16, a.N, a.rows) ||
+                             !map_out(&r, RES ? const_cast<void *>(a.res) : a.out, BF16, a.N, a.rows)))
+        e = cudaErrorInvalidValue;
     if (e != cudaSuccess) return e;
     a.tiles_c = (a.N + 255) / 256;
     a.tiles = a.tiles_c * (int32_t)((a.rows + 255) / 256);
-    return launch_clusters(tdp_matmul8_pair_kernel<BF16>, 2 * std::min(a.tiles, 76), 2, kPairThreads, bytes, s, a, x, w, o);
+    return launch_clusters(tdp_matmul8_pair_kernel<BF16, RES>, 2 * std::min(a.tiles, 76), 2, kPairThreads, bytes, s, a, x, w, o, r);
 }
 
 // Rows of a tile, or 0 for pairs: the least time of the launch and of rounds of resident blocks, each so much for its end and for
@@ -512,7 +540,7 @@ cudaError_t matmul8(const args &a, const void *w8, const void *x8, int64_t K, cu
     case 16: return tile_launch<BF16, 16>(a, w8, x8, K, s);
     case 32: return tile_launch<BF16, 32>(a, w8, x8, K, s);
     case 64: return tile_launch<BF16, 64>(a, w8, x8, K, s);
-    default: return pair_launch<BF16>(a, w8, x8, K, s);
+    default: return a.res ? pair_launch<BF16, 1>(a, w8, x8, K, s) : pair_launch<BF16, 0>(a, w8, x8, K, s);
     }
 }
 
