@@ -865,6 +865,8 @@ def tdp_rms_norm_grad_workspace(plan: Plan, rows: int, C: int) -> int:
     if got is None:
         n = ctypes.c_int64()
         _check(_lib.tdp_rms_norm_grad_workspace(plan.handle, int(rows), int(C), ctypes.byref(n)), "tdp_rms_norm_grad_workspace")
+        if len(plan.sizes) > 1000:          # rows of any number come by
+            plan.sizes.clear()
         got = plan.sizes["rms", rows, C] = int(n.value)
     return got
 

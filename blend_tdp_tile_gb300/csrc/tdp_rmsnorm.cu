@@ -602,6 +602,7 @@ extern "C" tdp_status tdp_rms_norm(tdp_plan_t plan, int64_t rows, int32_t C, flo
     if (!(eps >= 0.f) || eps - eps != 0.f) return tdp_fail(TDP_ERR_INVALID_ARG, "eps must be finite and not negative");
     if (rows == 0) return tdp_ok();
     if (!x || (!y && !y8 && !x8 && !h && !rstd)) return tdp_fail(TDP_ERR_INVALID_ARG, "null x, or no output");
+    if (h && h == y) return tdp_fail(TDP_ERR_INVALID_ARG, "h and y are one buffer");
     if (!y8 != !y8_scale || !x8 != !x8_scale) return tdp_fail(TDP_ERR_INVALID_ARG, "8-bit rows and their scales come together");
     if (!tdp_aligned(x, 16) || !tdp_aligned(res, 16) || !tdp_aligned(w, 16) || !tdp_aligned(h, 16) || !tdp_aligned(y, 16) ||
         !tdp_aligned(y8, 16) || !tdp_aligned(x8, 16) || !tdp_aligned(rstd, 4) || !tdp_aligned(y8_scale, 4) || !tdp_aligned(x8_scale, 4))

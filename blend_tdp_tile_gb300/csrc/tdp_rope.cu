@@ -192,14 +192,18 @@ tdp_status rope(tdp_plan_t plan, const tdp_rope_shape *p, const void *x, const i
         if (s >= ((int64_t)1 << 38)) return tdp_fail(TDP_ERR_TOO_LARGE, "strides must be below 2^38 elements");
     }
     const int64_t R = (int64_t)g.B * g.total;
+    const __int128 most = (__int128)(p->heads - 1) * std::max(p->x_head, p->out_head) + (__int128)R * std::max(p->x_row, p->out_row);
+    if (most > ((__int128)1 << 56)) return tdp_fail(TDP_ERR_TOO_LARGE, "heads and rows past 2^56 elements");
     // a row's heads side by side, or a head's rows
-    const int64_t D = p->head_dim, oh = p->heads > 1 ? p->out_head : D, orow = R > 1 ? p->out_row : D;
+    const __int128 D = p->head_dim, oh = p->heads > 1 ? p->out_head : D, orow = R > 1 ? p->out_row : D;
     if (!(oh >= D && (R <= 1 || orow >= (p->heads - 1) * oh + D)) && !(orow >= D && (p->heads == 1 || oh >= (R - 1) * orow + D)))
         return tdp_fail(TDP_ERR_INVALID_ARG, "out's rows and heads overlap");
     if (R == 0) return tdp_ok();
     if (!x || !pos || !table || !out) return tdp_fail(TDP_ERR_INVALID_ARG, "null x, positions, table or out");
     if (!tdp_aligned(x, 16) || !tdp_aligned(out, 16) || !tdp_aligned(pos, 8) || !tdp_aligned(table, 8))
         return tdp_fail(TDP_ERR_MISALIGNED, "heads need 16-byte, positions and table 8-byte alignment");
+    if (x == out && ((p->heads > 1 && p->x_head != p->out_head) || (R > 1 && p->x_row != p->out_row)))
+        return tdp_fail(TDP_ERR_INVALID_ARG, "in place with other strides");
     // the widest vector that half of rot (or rot) is a multiple of
     const int32_t half = p->layout == TDP_ROPE_HALF;
     int32_t W = (int32_t)V;

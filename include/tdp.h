@@ -568,11 +568,12 @@ tdp_status tdp_dropout_grad(tdp_plan_t plan, int64_t n, double p, const uint64_t
  *   x, res      device [rows, C] (plan dtype), read; res may be NULL.
  *   w           device [C] (plan dtype), read; NULL: 1.
  *   h, y        device [rows, C] (plan dtype), written; either may be NULL, and either may be x
- *               or res itself (not both the same).
+ *               or res itself, but not both the same buffer.
  *   rstd        device fp32 [rows], written; or NULL.  The gradient reads it.
  *   y8, y8_scale   y in 8 bits: device uint8 [rows, C] and fp32 [rows], written; or both NULL.
  *   x8, x8_scale   u in 8 bits, as a checkpoint for the gradient in place of h; or both NULL.
- * At least one output.  Rows start on 16 bytes.
+ * At least one output.  Rows start on 16 bytes.  The first call on a device raises the kernels'
+ * shared-memory limits; make it, and the gradient's, before capturing a stream into a CUDA graph.
  */
 tdp_status tdp_rms_norm(tdp_plan_t plan, int64_t rows, int32_t C, float eps, const void *x, const void *res,
                         const void *w, void *h, void *y, float *rstd, uint8_t *y8, float *y8_scale, uint8_t *x8,
@@ -685,8 +686,8 @@ tdp_status tdp_rope_table(int32_t pairs, const double *freq, const int32_t *axis
  *   a' = scale * (a cos(p f_i) - b sin(p f_i)),  b' = scale * (a sin(p f_i) + b cos(p f_i));
  * the gradient turns dout by -p f_i.  Angles are exact to 2^-30 turns at any int32 positions.
  *
- *   x, out     device [R, heads, head_dim] by their strides (plan dtype); out may be x itself with the same
- *              strides, and must not overlap it otherwise.
+ *   x, out     device [R, heads, head_dim] by their strides (plan dtype); x may be broadcast (stride 0); out
+ *              may be x itself with the same strides, and must not overlap it otherwise.
  *   Q          device tile-major positions from tdp_split (int32, B * total_tile_tokens * 6), read.  Tokens of
  *              a plan with one tile a dimension have positions [B, 3, T, 2], conditioning tokens among them.
  *   table      device int64 [rot / 2] from tdp_rope_table, read.

@@ -22,7 +22,7 @@ def test_rms_norm_refused(tdp):  # noqa: F811
     lib, plan = tdp._lib, _plan(tdp)
 
     def fwd(h=plan.handle, rows=4, C=64, eps=1e-5, **kw):
-        b = dict(x=P, res=None, w=P, h=P, y=P, rstd=P, y8=P, ys=P, x8=P, xs=P) | kw
+        b = dict(x=P, res=None, w=P, h=P, y=3 * P, rstd=P, y8=P, ys=P, x8=P, xs=P) | kw
         return lib.tdp_rms_norm(h, rows, C, eps, *b.values(), None)
 
     def quant(h=plan.handle, rows=4, C=64, x=P, x8=P, xs=P):
@@ -38,6 +38,7 @@ def test_rms_norm_refused(tdp):  # noqa: F811
     assert lib.tdp_rms_norm(plan.handle, 4, 64, 0.1, P, None, P, *[None] * 7, None) == 1
     assert [fwd(**{k: P + 8}) for k in ("res", "w", "y", "y8")] == [4] * 4 and fwd(rstd=P + 1) == 4 and fwd(ys=P + 2) == 4
     assert quant(x8=None) == 1
+    assert lib.tdp_rms_norm(plan.handle, 4, 64, 0.1, P, None, P, 2 * P, 2 * P, *[None] * 5, None) == 1      # h and y in one place
 
 
 @no_gpu_only
@@ -82,7 +83,8 @@ def _shape(tdp, **kw):
 @pytest.mark.parametrize("kw,status", [
     (dict(heads=0), 1), (dict(head_dim=0), 1), (dict(rot=0), 1), (dict(rot=31), 1), (dict(rot=66), 1), (dict(layout=2), 1), (dict(at=-1), 1),
     (dict(scale=float("nan")), 1), (dict(scale=float("inf")), 1), (dict(x_row=-8), 1), (dict(out_row=64), 1), (dict(out_head=0), 1), (dict(out_head=32), 1),
-    (dict(out_row=200), 1), (dict(out_row=0), 1), (dict(out_row=64, out_head=640), 1),
+    (dict(out_row=200), 1), (dict(out_row=0), 1), (dict(out_row=64, out_head=640), 1), (dict(x_row=512), 1), (dict(x_head=0), 1),
+    (dict(heads=(1 << 31) - 1, out_head=(1 << 38) - 8, x_head=(1 << 38) - 8), 5),
     (dict(head_dim=60, rot=32), 4), (dict(x_row=252), 4), (dict(out_head=65), 4), (dict(head_dim=264), 5), (dict(x_head=1 << 38), 5),
 ])
 @no_gpu_only
