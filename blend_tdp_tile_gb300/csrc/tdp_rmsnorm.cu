@@ -494,8 +494,8 @@ norm_shape norm_deal(int64_t rows, int32_t nv, int32_t vecs, bool wide)
     norm_shape s;
     s.nv = nv;
     s.lanes = 1;
-    while (s.lanes < 32 && s.lanes < nv) s.lanes *= 2;
     if (rows <= 2 * kSMs) vecs = 2;
+    while (s.lanes < 32 && nv > s.lanes * std::min(vecs, 4)) s.lanes *= 2;
     // the fewest places for the row's vectors, with few warps: 640 vectors are five a lane of four warps and not eight of three
     // (20000 rows of 5120 bf16 into 8 bits 122 us for 189), but 160 three of two and not one of five (the gradient 40 us for 85)
     const auto of_lane = [nv](int32_t lanes) {
