@@ -495,7 +495,9 @@ norm_shape norm_deal(int64_t rows, int32_t nv, int32_t vecs, bool wide)
     s.nv = nv;
     s.lanes = 1;
     if (rows <= 2 * kSMs) vecs = 2;
-    while (s.lanes < 32 && nv > s.lanes * std::min(vecs, 4)) s.lanes *= 2;
+    // narrow rows: four vectors a lane, not one (1 million rows of 128 bf16: quantised in 63 us for 98, the gradient 153 for 178);
+    // eight only from 96 on (160000 rows of 768 into 8 bits 145 us for 161; rows of 64 would take 293 for 156)
+    while (s.lanes < 32 && nv > s.lanes * (nv < 96 ? std::min(vecs, 4) : vecs)) s.lanes *= 2;
     // the fewest places for the row's vectors, with few warps: 640 vectors are five a lane of four warps and not eight of three
     // (20000 rows of 5120 bf16 into 8 bits 122 us for 189), but 160 three of two and not one of five (the gradient 40 us for 85)
     const auto of_lane = [nv](int32_t lanes) {
@@ -507,7 +509,8 @@ norm_shape norm_deal(int64_t rows, int32_t nv, int32_t vecs, bool wide)
         if (w * of_lane(32 * w) < s.warps * of_lane(32 * s.warps) && 2 * of_lane(32 * w) > of_lane(32 * s.warps)) s.warps = w;
     s.lanes *= s.warps;
     s.vpt = of_lane(s.lanes);
-    // rows of a block: as many as fit where there are rows for all SMs; one of several warps in the forward
+    // rows of a block: as many as fit where there are rows for all SMs (eight of a warp each: 168960 x 2048 quantised in 153 us, four
+    // 177); of several warps one in the forward (40000 x 4096 into 8 bits 179 us, four 192), all in the gradient (200 us for 261)
     const int32_t least = std::max(1, 32 / s.lanes), most = s.warps > 1 && !wide ? 1 : kNormThreads / s.lanes;
     s.rows = least;
     while (2 * s.rows <= most && rows >= 2 * s.rows * kSMs) s.rows *= 2;
