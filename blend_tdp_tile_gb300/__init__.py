@@ -32,7 +32,7 @@ __all__ = [
     "tdp_tile_mean", "tdp_blend_partial", "tdp_blend_store", "tdp_blend_cond",
     "TDP_MAX_HEAD_DIM", "TDP_MAX_STATES", "tdp_cross_attn", "tdp_cross_attn_grad", "tdp_cross_attn_workspace",
     "tdp_group_norm", "tdp_group_norm_grad", "tdp_group_norm_workspace", "tdp_dropout_add", "tdp_dropout_grad",
-    "TDP_MAX_NORM_BYTES", "TDP_MAX_MATMUL8", "TDP_MAX_MATMUL8_ROWS", "TDP_MAX_ROPE_DIM", "tdp_rms_norm", "tdp_rms_norm_grad",
+    "TDP_MAX_NORM_BYTES", "TDP_MAX_MATMUL8", "TDP_MAX_MATMUL8_ROWS", "TDP_MAX_ROPE_DIM", "TDP_MAX_ROPE_HEADS", "tdp_rms_norm", "tdp_rms_norm_grad",
     "tdp_rms_norm_grad_workspace", "tdp_quant8", "tdp_matmul8", "tdp_rope_freqs", "tdp_rope_table", "tdp_rope", "tdp_rope_grad",
     "tdp_balanced_tile_split", "tdp_tiles_for_size", "tdp_rank_tiles",
     "tdp_status_str", "tdp_last_error_detail",
@@ -50,6 +50,7 @@ TDP_MAX_NORM_BYTES = 32768
 TDP_MAX_MATMUL8 = 1 << 20
 TDP_MAX_MATMUL8_ROWS = 1 << 30
 TDP_MAX_ROPE_DIM = 256
+TDP_MAX_ROPE_HEADS = 1 << 20
 _ACTS = {"none": 0, "silu": 1}
 _LAYOUTS = {"half": 0, "interleaved": 1}
 _PLACES = {"start": 0, "middle": 1}

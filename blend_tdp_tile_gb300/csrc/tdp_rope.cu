@@ -216,7 +216,8 @@ tdp_status rope(tdp_plan_t plan, const tdp_rope_shape *p, const void *x, const i
     if ((p->layout != TDP_ROPE_HALF && p->layout != TDP_ROPE_INTERLEAVED) || (p->at != TDP_ROPE_START && p->at != TDP_ROPE_MIDDLE))
         return tdp_fail(TDP_ERR_INVALID_ARG, "unknown layout or place in the interval");
     if (!(p->scale - p->scale == 0.f)) return tdp_fail(TDP_ERR_INVALID_ARG, "scale must be finite");
-    if (p->head_dim > TDP_MAX_ROPE_DIM) return tdp_fail(TDP_ERR_TOO_LARGE, "head_dim above TDP_MAX_ROPE_DIM");
+    if (p->head_dim > TDP_MAX_ROPE_DIM || p->heads > TDP_MAX_ROPE_HEADS)
+        return tdp_fail(TDP_ERR_TOO_LARGE, "head_dim above TDP_MAX_ROPE_DIM or heads above TDP_MAX_ROPE_HEADS");
     const int64_t V = 16 / g.esize, strides[4] = {p->x_row, p->x_head, p->out_row, p->out_head};
     if (p->head_dim % V != 0) return tdp_fail(TDP_ERR_MISALIGNED, "head_dim * element size must be a multiple of 16 bytes");
     for (int64_t s : strides) {

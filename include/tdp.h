@@ -641,8 +641,9 @@ typedef enum { TDP_ROPE_HALF = 0, TDP_ROPE_INTERLEAVED = 1 } tdp_rope_layout;
 typedef enum { TDP_ROPE_START = 0, TDP_ROPE_MIDDLE = 1 } tdp_rope_at;
 typedef enum { TDP_ROPE_UNSCALED = 0, TDP_ROPE_LINEAR = 1, TDP_ROPE_NTK = 2, TDP_ROPE_YARN = 3 } tdp_rope_scaling;
 
-/* Largest head dimension of tdp_rope. */
+/* Largest head dimension and most heads of tdp_rope. */
 #define TDP_MAX_ROPE_DIM 256
+#define TDP_MAX_ROPE_HEADS (1 << 20)
 
 /* Strides count elements; the head dimension is contiguous.  head_dim and strides are multiples of 16 bytes,
  * and a dimension of one ignores its stride.  out's rows and heads must not overlap. */

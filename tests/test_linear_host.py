@@ -84,7 +84,7 @@ def _shape(tdp, **kw):
     (dict(heads=0), 1), (dict(head_dim=0), 1), (dict(rot=0), 1), (dict(rot=31), 1), (dict(rot=66), 1), (dict(layout=2), 1), (dict(at=-1), 1),
     (dict(scale=float("nan")), 1), (dict(scale=float("inf")), 1), (dict(x_row=-8), 1), (dict(out_row=64), 1), (dict(out_head=0), 1), (dict(out_head=32), 1),
     (dict(out_row=200), 1), (dict(out_row=0), 1), (dict(out_row=64, out_head=640), 1), (dict(x_row=512), 1), (dict(x_head=0), 1),
-    (dict(heads=(1 << 31) - 1, out_head=(1 << 38) - 8, x_head=(1 << 38) - 8), 5),
+    (dict(heads=1 << 20, out_head=(1 << 38) - 8, x_head=(1 << 38) - 8), 5), (dict(heads=(1 << 20) + 1), 5),
     (dict(head_dim=60, rot=32), 4), (dict(x_row=252), 4), (dict(out_head=65), 4), (dict(head_dim=264), 5), (dict(x_head=1 << 38), 5),
 ])
 @no_gpu_only
@@ -173,4 +173,5 @@ def test_header_and_binding_agree(tdp):  # noqa: F811
     assert f"#define TDP_MAX_NORM_BYTES {tdp.TDP_MAX_NORM_BYTES}" in src and f"#define TDP_MAX_ROPE_DIM {tdp.TDP_MAX_ROPE_DIM}" in src
     assert "#define TDP_MAX_MATMUL8 (1 << 20)" in src and tdp.TDP_MAX_MATMUL8 == 1 << 20
     assert "#define TDP_MAX_MATMUL8_ROWS (1 << 30)" in src and tdp.TDP_MAX_MATMUL8_ROWS == 1 << 30
+    assert "#define TDP_MAX_ROPE_HEADS (1 << 20)" in src and tdp.TDP_MAX_ROPE_HEADS == 1 << 20
     assert ctypes.sizeof(tdp._Rope) == 6 * 4 + 4 * 8
