@@ -200,12 +200,12 @@ tdp_matmul8_tile_kernel(const __grid_constant__ args a, const __grid_constant__ 
 struct pair_smem {
     static constexpr int kStage = 32768;
     static constexpr int kStages = 5;
-    static constexpr int kOut = 16384;          // two panels of outputs on their way to memory: 128 rows of 64 bytes
+    static constexpr int kOut = 4096;           // two panels of a warp's outputs on their way to memory: 32 rows of 64 bytes
     static constexpr int kScales = 2048;        // a tile's scales and bias of 256 channels
-    static constexpr int kBars = 8 * (2 * kStages + 5 + 8) + 8;
-    // all that a block may have but 768 bytes, which are for the start's rounding up to 1024
+    static constexpr int kBars = 8 * (2 * kStages + 5 + 32) + 8;
+    // all that a block may have; the start is a multiple of 1024, as nothing but this lies in shared memory
     static constexpr int kBytes = 232448;
-    static_assert(kStages * kStage + 4 * kOut + kScales + kBars <= kBytes - 768, "room for the stages");
+    static_assert(kStages * kStage + 16 * kOut + kScales + kBars <= kBytes - 512, "room for the stages");
 };
 constexpr int kPairThreads = 640;
 
@@ -220,7 +220,7 @@ tdp_matmul8_pair_kernel(const __grid_constant__ args a, const __grid_constant__ 
     constexpr int NST = SM::kStages;
     extern __shared__ __align__(1024) unsigned char raw[];
     const uint32_t base = (smem_u32(raw) + 1023u) & ~1023u, out_s = base + NST * SM::kStage;
-    unsigned char *tail = raw + (base - smem_u32(raw)) + NST * SM::kStage + 4 * SM::kOut;
+    unsigned char *tail = raw + (base - smem_u32(raw)) + NST * SM::kStage + 16 * SM::kOut;
     float *scales = reinterpret_cast<float *>(tail);            // channels' scales, then their bias
     volatile int *dead = reinterpret_cast<int *>(tail + SM::kScales);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(tail + SM::kScales + 4);
@@ -236,7 +236,7 @@ tdp_matmul8_pair_kernel(const __grid_constant__ args a, const __grid_constant__ 
             mbar_init(taken + 8 * i, 32);       // sixteen warps of either block
         }
         mbar_init(drain, 1);
-        for (int i = 0; i < 8; ++i) mbar_init(added + 8 * i, 1);
+        for (int i = 0; i < 32; ++i) mbar_init(added + 8 * i, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     fence_before();
@@ -297,7 +297,7 @@ tdp_matmul8_pair_kernel(const __grid_constant__ args a, const __grid_constant__ 
         landed(drain, 0);
     } else if (warp >= 4) {
         const int32_t r = threadIdx.x & 127, part = (warp - 4) >> 2;
-        const uint32_t lanes = tm + ((uint32_t)(warp & 3) << 21) + 64 * part, to = out_s + part * SM::kOut;
+        const uint32_t lanes = tm + ((uint32_t)(warp & 3) << 21) + 64 * part, to = out_s + (warp - 4) * SM::kOut;
         // A tile's scales and bias are asked for while the tile before is worked on.
         float x, w, b;
         auto ask = [&](int32_t t) {
@@ -311,30 +311,32 @@ tdp_matmul8_pair_kernel(const __grid_constant__ args a, const __grid_constant__ 
         if (first < a.tiles) ask(first);
         uint32_t n = 0, panel = 0;
         constexpr int W = BF16 ? 32 : 16;       // channels of a panel
-        auto row_of = [&](int32_t t) { return (t / a.tiles_c) * 256 + (int32_t)rank * 128; };
+        auto row_of = [&](int32_t t) { return (t / a.tiles_c) * 256 + (int32_t)rank * 128 + 32 * (warp & 3); };
         auto ch_of = [&](int32_t t) { return (t % a.tiles_c) * 256 + 64 * part; };
-        // channels of a tile that this warpgroup has: panels with anything in them are stored, each
+        // channels of a tile that this warp has: panels with anything in them are stored, each by the warp that filled it (by the
+        // warpgroup, behind its barriers, 100000 x 64 x 1024 takes 57.6 us where this takes 54.4)
         auto end_of = [&](int32_t t) { return row_of(t) < a.rows ? min(64, a.N - ch_of(t)) : 0; };
         // The residual comes into the panel that its sum leaves by, a panel ahead: read by the threads, a row each, it took
         // 125 us where this takes 107 (35840 x 2048 x 2048).
-        const uint32_t bars = added + 16 * part;
+        const uint32_t bars = added + 16 * (warp - 4);
         uint32_t phases = 0;
         bool asked = false;
         auto bring = [&](int32_t t, int32_t c0, uint32_t to_panel) {
-            mbar_expect(bars + 8 * to_panel, 8192);
-            tma_load2(to + to_panel * 8192, &map_r, bars + 8 * to_panel, ch_of(t) + c0, row_of(t));
+            mbar_expect(bars + 8 * to_panel, 2048);
+            tma_load2(to + to_panel * 2048, &map_r, bars + 8 * to_panel, ch_of(t) + c0, row_of(t));
         };
 #pragma unroll 1
         for (int32_t t = first; t < a.tiles; t += step, ++n) {
             const uint32_t buf = n & 1;
             const int32_t row0 = row_of(t), ch0 = ch_of(t), end = end_of(t);
             const float xs = x;
+            group_sync(1 + part);           // the last tile's have been read
             if (r < 64) {
                 scales[64 * part + r] = w;
                 scales[256 + 64 * part + r] = b;
             }
             if (t + step < a.tiles) ask(t + step);
-            group_sync(1 + part);           // they are read before the panels' last barrier, and written behind it
+            group_sync(1 + part);
             if (ok) ok = mbar_wait(sums + 8 * buf, (n >> 1) & 1, dead);
             ok = __all_sync(~0u, ok && !*dead);
             fence_after();
@@ -354,7 +356,7 @@ tdp_matmul8_pair_kernel(const __grid_constant__ args a, const __grid_constant__ 
                     const bool more = c0 + W < end;
                     const int32_t t2 = more ? t : t + step, c2 = more ? c0 + W : 0;
                     const bool next = more || (t2 < a.tiles && end_of(t2) > 0);
-                    if (r == 0) {
+                    if (lane == 0) {
                         tma_store_read();       // both panels have left
                         if (!asked) bring(t, c0, panel);
                         if (next) bring(t2, c2, panel ^ 1);
@@ -372,12 +374,12 @@ tdp_matmul8_pair_kernel(const __grid_constant__ args a, const __grid_constant__ 
                     }
                     phases ^= 1u << panel;
                 } else {
-                    if (r == 0) tma_store_read_but_one();       // the panel before the last has left
-                    group_sync(1 + part);
+                    if (lane == 0) tma_store_read_but_one();    // the panel before the last has left
+                    __syncwarp();
                 }
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    const uint32_t at = to + panel * 8192 + r * 64 + ((j ^ ((r >> 1) & 3)) << 4);        // the 64-byte swizzle of the maps
+                    const uint32_t at = to + panel * 2048 + lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4);        // the 64-byte swizzle of the maps
                     float f[E::kVec];
 #pragma unroll
                     for (int q = 0; q < E::kVec; q += 4) {
@@ -400,12 +402,12 @@ tdp_matmul8_pair_kernel(const __grid_constant__ args a, const __grid_constant__ 
                     st_shared16(at, o);
                 }
                 fence_async();
-                group_sync(1 + part);
-                if (r == 0) tma_store2(&map_o, to + panel * 8192, ch0 + c0, row0);
+                __syncwarp();
+                if (lane == 0) tma_store2(&map_o, to + panel * 2048, ch0 + c0, row0);
                 panel ^= 1;
             }
         }
-        if (r == 0) tma_store_done();
+        if (lane == 0) tma_store_done();
     }
     __syncwarp();
     fence_before();
@@ -430,13 +432,13 @@ bool map8(CUtensorMap *map, const void *p, int64_t K, int64_t rows, int box)
                   CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Map of the outputs, or of the residual: boxes of 64 bytes by 128 rows.
+// Map of the outputs, or of the residual: boxes of 64 bytes by 32 rows.
 bool map_out(CUtensorMap *map, void *p, int bf16, int64_t N, int64_t rows)
 {
     PFN_cuTensorMapEncodeTiled_v12000 encode = tdp_encode_tiled();
     if (!encode) return false;
     const cuuint64_t extent[2] = {(cuuint64_t)N, (cuuint64_t)rows}, stride[1] = {(cuuint64_t)N * (bf16 ? 2 : 4)};
-    const cuuint32_t b[2] = {bf16 ? 32u : 16u, 128}, one[2] = {1, 1};
+    const cuuint32_t b[2] = {bf16 ? 32u : 16u, 32}, one[2] = {1, 1};
     return encode(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, p, extent, stride, b, one,
                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
