@@ -340,42 +340,54 @@ class _Call:
     """Marshals one entry-point call: checks each buffer (size, dtype, contiguity,
     alignment, one common device), then calls the library with that device current."""
 
+    __slots__ = ("where", "first", "dev")
+
     def __init__(self, where):
         self.where = where
-        self.named = []
-        self.dev = None             # index of the device so far; -1: more than one
+        self.first = None           # the first buffer and its name
+        self.dev = None             # index of the buffers' device
 
     def on(self, t, name):
-        self.named.append((name, t))
         d = t.get_device()
+        if d != self.dev:
+            self._device(t, name, d)
+
+    def _device(self, t, name, d):
         if self.dev is None:
-            self.dev = d
-        elif self.dev != d:
-            self.dev = -1
+            self.dev, self.first = d, (name, t)
+        else:
+            _common_device(self.where, (self.first, (name, t)))
 
     def ptr(self, t, name, numel, dtypes, align):
         if t is None:
             return None
         # a buffer that is as it must be is seen to be so first: a call of ten small buffers is bound by this
-        if _torch_module is not None and isinstance(t, _torch_module.Tensor) and t.is_cuda and t.dtype in dtypes and \
-                t.numel() == numel and t.is_contiguous():
-            p = t.data_ptr()
-            if not p % align:
-                self.on(t, name)
-                return p
+        try:
+            d = t.get_device()
+            if d >= 0 and t.dtype in dtypes and t.numel() == numel and t.is_contiguous():
+                p = t.data_ptr()
+                if not p % align:
+                    if d != self.dev:
+                        self._device(t, name, d)
+                    return p
+        except (AttributeError, RuntimeError):
+            pass                    # no tensor, or one without memory
         p = _ptr(t, name, numel, dtypes, align)
         self.on(t, name)
         return p
 
     def run(self, fn, *args, stream=None):
-        torch = _torch()
-        if stream is None and self.dev is not None and self.dev >= 0 and _current() and self.dev == _current_device():
-            _check(fn(*args, _current_stream(self.dev)), self.where)
+        d = self.dev
+        if stream is None and d is not None and (_current_device or _current()) and d == _current_device():
+            status = fn(*args, _current_stream(d))
+            if status:
+                raise TdpError(status, self.where)
             return
-        dev = _common_device(self.where, self.named)
-        if dev is None:
-            dev = torch.device("cuda", torch.cuda.current_device())
-        if dev.index == torch.cuda.current_device():
+        torch = _torch()
+        if d is None:
+            d = torch.cuda.current_device()
+        dev = torch.device("cuda", d)
+        if d == torch.cuda.current_device():
             _check(fn(*args, _stream_handle(self.where, stream, dev)), self.where)
             return
         with torch.cuda.device(dev):
@@ -824,7 +836,13 @@ def tdp_dropout_grad(plan: Plan, dout, p, rng, dx, stream=None):
           c.ptr(dx, "dx", n, lat, 16), stream=stream)
 
 
-_types8 = None
+_types8 = _types32 = None
+
+
+def _floats32():
+    global _types32
+    _types32 = (_torch().float32,)
+    return _types32
 
 
 def _bytes8():
@@ -837,11 +855,13 @@ def _bytes8():
 
 def _matrix(x, name):
     """(rows, columns) of a tensor taken as rows of its last dimension."""
-    if not isinstance(x, _torch().Tensor):
-        raise TypeError(f"{name}: expected a torch.Tensor")
-    if x.dim() < 1 or x.shape[-1] < 1:
-        raise ValueError(f"{name}: shape {tuple(x.shape)} has no rows")
-    return x.numel() // x.shape[-1], int(x.shape[-1])
+    try:
+        C = x.shape[-1]
+        return x.numel() // C, C
+    except (AttributeError, IndexError, TypeError, ZeroDivisionError):
+        if not isinstance(x, _torch().Tensor):
+            raise TypeError(f"{name}: expected a torch.Tensor") from None
+        raise ValueError(f"{name}: shape {tuple(x.shape)} has no rows") from None
 
 
 def tdp_rms_norm(plan: Plan, x, w, y=None, res=None, h=None, rstd=None, y8=None, y8_scale=None, x8=None, x8_scale=None, eps=1e-6,
@@ -850,7 +870,7 @@ def tdp_rms_norm(plan: Plan, x, w, y=None, res=None, h=None, rstd=None, y8=None,
 
     Outputs, each or None: y and h in the plan's dtype, rstd [rows] in fp32, y8 with y8_scale [rows]: y in 8 bits (e4m3), x8 with
     x8_scale: the rows before w, a checkpoint for tdp_rms_norm_grad."""
-    f32, lat, b8 = (_torch().float32,), _latent_dtypes(plan), _bytes8()
+    f32, lat, b8 = _types32 or _floats32(), plan.lat or _latent_dtypes(plan), _types8 or _bytes8()
     rows, C = _matrix(x, "x")
     n = rows * C
     c = _Call("tdp_rms_norm")
@@ -875,7 +895,7 @@ def tdp_rms_norm_grad_workspace(plan: Plan, rows: int, C: int) -> int:
 def tdp_rms_norm_grad(plan: Plan, dy, dx, w, rstd, h=None, x8=None, x8_scale=None, dh=None, dw=None, ws=None, stream=None):
     """Gradients of tdp_rms_norm: dx [.., C] (of x, and of res alike) and, unless None, dw [C] in fp32, from h as the forward
     left it or from its checkpoint x8, x8_scale.  dh: the gradient that comes by way of h, or None."""
-    f32, lat = (_torch().float32,), _latent_dtypes(plan)
+    f32, lat = _types32 or _floats32(), plan.lat or _latent_dtypes(plan)
     rows, C = _matrix(dy, "dy")
     n = rows * C
     if dw is not None:
@@ -892,14 +912,14 @@ def tdp_quant8(plan: Plan, x, x8, x8_scale, stream=None):
     """x8 [.., C] (e4m3) and x8_scale [rows]: the rows of x [.., C] in 8 bits, a scale a row."""
     rows, C = _matrix(x, "x")
     c = _Call("tdp_quant8")
-    c.run(_lib.tdp_quant8, plan.handle, rows, C, c.ptr(x, "x", rows * C, _latent_dtypes(plan), 16),
-          c.ptr(x8, "x8", rows * C, _bytes8(), 16), c.ptr(x8_scale, "x8_scale", rows, (_torch().float32,), 4), stream=stream)
+    c.run(_lib.tdp_quant8, plan.handle, rows, C, c.ptr(x, "x", rows * C, plan.lat or _latent_dtypes(plan), 16),
+          c.ptr(x8, "x8", rows * C, _types8 or _bytes8(), 16), c.ptr(x8_scale, "x8_scale", rows, _types32 or _floats32(), 4), stream=stream)
 
 
 def tdp_matmul8(plan: Plan, x8, x8_scale, w8, w8_scale, out, bias=None, res=None, stream=None):
     """out [.., N] = 8-bit rows x8 [.., K] (scales [rows]) times 8-bit weights w8 [N, K] (scales [N]), plus bias [N] and
     res [.., N] (each or None)."""
-    f32, lat, b8 = (_torch().float32,), _latent_dtypes(plan), _bytes8()
+    f32, lat, b8 = _types32 or _floats32(), plan.lat or _latent_dtypes(plan), _types8 or _bytes8()
     (rows, K), (N, Kw) = _matrix(x8, "x8"), _matrix(w8, "w8")
     if Kw != K:
         raise ValueError(f"w8: rows of {Kw} values, x8 has {K}")
