@@ -105,7 +105,7 @@ def _heads(t):
 class _RmsNorm(torch.autograd.Function):
     @staticmethod
     def forward(ctx, plan, x, w, res, eps, keep8):
-        x = _dense(x)
+        x, w = _dense(x), None if w is None else _dense(w)
         rows = x.numel() // x.shape[-1]
         y, rstd = torch.empty_like(x), torch.empty(rows, dtype=torch.float32, device=x.device)
         h, res = (x, None) if res is None else (torch.empty_like(x), _dense(res))
@@ -249,7 +249,8 @@ class RotaryBlock(torch.nn.Module):
     to the conditioning tokens that the tile keeps, both turned by their positions.
 
     pairs: pairs of a head on each of the three axes.  keep8: training keeps the normalised rows in 8 bits.  After to_8bit() the block
-    runs its projections in 8 bits, without gradients, until train() brings the full ones back.  rng as for TileBlock."""
+    runs its projections in 8 bits, without gradients, until train() brings the full ones back; weights that change in between
+    need another to_8bit().  rng as for TileBlock."""
 
     def __init__(self, channels, heads, kv_heads, head_dim, context, pairs, p=0.0, keep8=False, base=10000.0, scaling="none", factor=1.0,
                  length=1.0, dtype=torch.bfloat16, device="cuda"):

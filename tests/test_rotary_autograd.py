@@ -32,7 +32,7 @@ def block(tdp, monkeypatch):  # noqa: F811
                 raise ValueError("not 16-byte aligned")
 
     def rms_norm(plan, x, w, y=None, res=None, h=None, rstd=None, y8=None, y8_scale=None, x8=None, x8_scale=None, eps=1e-6):
-        aligned(x, y, res, h)
+        aligned(x, y, res, h, w)
         s, out = _norm(x, w, res, eps)
         y.copy_(out)
         rstd.copy_((s.square().mean(-1) + eps).rsqrt())
@@ -146,6 +146,9 @@ def test_slices_at_odd_offsets(block, name, offset):
     got, = torch.autograd.grad((y * w).sum(), x)
     want, = torch.autograd.grad((f(x).reshape(-1) * w[offset:].clone()).sum(), x)
     assert torch.equal(got, want)
+    if name == "rms_norm":          # the weight too
+        w1 = torch.cat([torch.zeros(offset), torch.ones(C)])[offset:]
+        assert torch.equal(block.rms_norm(None, x.detach(), w1), block.rms_norm(None, x.detach(), w1.clone()))
     buf = torch.cat([torch.zeros(offset), x.detach().reshape(-1)])
     assert torch.equal(f(buf[offset:].view(x.shape)), f(x.detach()))
 
