@@ -342,6 +342,7 @@ extern "C" tdp_status tdp_rope_freqs(const int32_t *pairs, double base, int32_t 
 {
     if (!pairs || !freq || !axis || !scale) return tdp_fail(TDP_ERR_INVALID_ARG, "null array");
     if (pairs[0] < 0 || pairs[1] < 0 || pairs[2] < 0) return tdp_fail(TDP_ERR_INVALID_ARG, "negative pairs");
+    if ((int64_t)pairs[0] + pairs[1] + pairs[2] > TDP_MAX_ROPE_DIM / 2) return tdp_fail(TDP_ERR_TOO_LARGE, "more pairs than TDP_MAX_ROPE_DIM / 2");
     if (!(base > 0) || !std::isfinite(base) || scaling < TDP_ROPE_UNSCALED || scaling > TDP_ROPE_YARN)
         return tdp_fail(TDP_ERR_INVALID_ARG, "need a finite base > 0 and a known scaling");
     if (scaling != TDP_ROPE_UNSCALED && (!(factor >= 1) || !std::isfinite(factor))) return tdp_fail(TDP_ERR_INVALID_ARG, "need a finite factor >= 1");

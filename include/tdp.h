@@ -660,7 +660,7 @@ typedef struct {
 /*
  * tdp_rope_freqs -- frequencies of a head's pairs over three axes (host only).
  *
- * Axis a has pairs[a] pairs, axis 0's first: f_i = base^(-i / pairs[a]), i = 0..pairs[a]-1.  Scaled by `factor` >= 1:
+ * Axis a has pairs[a] pairs (at most TDP_MAX_ROPE_DIM / 2 in all), axis 0's first: f_i = base^(-i / pairs[a]), i = 0..pairs[a]-1.  Scaled by `factor` >= 1:
  *   linear  f / factor (Chen et al., "Extending context window of large language models via positional
  *           interpolation", 2023);
  *   NTK     base * factor^(n / (n - 1)) for base, n = pairs[a]: the lowest frequency falls by factor;

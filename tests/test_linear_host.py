@@ -129,6 +129,10 @@ def test_table_and_freqs_refused(tdp):  # noqa: F811
                dict(scaling="yarn", factor=2.0, length=0.0)):
         with pytest.raises(tdp.TdpError):
             tdp.tdp_rope_freqs(**{"pairs": (4, 2, 2), **kw})
+    for pairs in ((129, 0, 0), (64, 64, 1), ((1 << 31) - 1,) * 3):
+        with pytest.raises(tdp.TdpError) as e:
+            tdp.tdp_rope_freqs(pairs)
+        assert e.value.status == 5
     with pytest.raises(ValueError):
         tdp.tdp_rope_freqs((1, 2))
     with pytest.raises(ValueError):
