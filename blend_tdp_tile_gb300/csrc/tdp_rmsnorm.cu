@@ -472,8 +472,14 @@ tdp_rms_norm_dw_kernel(const float *part, int32_t parts, int32_t C, float *dw)
     tdp_pdl_wait();
     const int32_t lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = blockIdx.x * 32 + lane;
     float f = 0.f;
-    if (c < C)
-        for (int32_t p = warp; p < parts; p += 32) f += part[(int64_t)p * C + c];
+    constexpr int U = 16;               // parts whose loads a thread has under way: a warp's share is 10 to 38
+    for (int32_t p0 = warp; p0 < parts; p0 += 32 * U) {
+        float v[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) v[u] = c < C && p0 + 32 * u < parts ? part[(int64_t)(p0 + 32 * u) * C + c] : 0.f;
+#pragma unroll
+        for (int u = 0; u < U; ++u) f += v[u];
+    }
     s[warp][lane] = f;
     __syncthreads();
     f = s[lane][warp];
