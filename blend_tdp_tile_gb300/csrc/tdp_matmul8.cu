@@ -76,7 +76,7 @@ tdp_matmul8_tile_kernel(const __grid_constant__ args a, const __grid_constant__ 
             if (!(ok = mbar_wait(empty + 8 * st, ((made / NST) & 1) ^ 1, dead))) break;
             if (elect_one()) {
                 const uint32_t to = base + st * SM::kStage;
-                mbar_expect(full + 8 * st, SM::kStage);
+                mbar_expect(full + 8 * st, (uint32_t)(a.w_box + a.x_box) * kK);
                 tma_load2(to, &map_w, full + 8 * st, (k0 + made) * kK, ch0);
                 tma_load2(to + 16384, &map_x, full + 8 * st, (k0 + made) * kK, (int32_t)row0);
             }
@@ -255,14 +255,17 @@ tdp_matmul8_pair_kernel(const __grid_constant__ args a, const __grid_constant__ 
 #pragma unroll 1
         for (int32_t t = first; t < a.tiles && ok; t += step) {
             const int32_t row = (t / a.tiles_c) * 256 + rank * 128, ch = (t % a.tiles_c) * 256 + rank * 128;
+            // the second block has no channels where the tile has 128 or fewer
+            const bool both = (t % a.tiles_c) * 256 + 128 < a.N, mine = rank == 0 || both;
+            const uint32_t bytes = 2 * 16384 + (both ? 2 : 1) * (uint32_t)a.w_box * kK;
 #pragma unroll 1
             for (int32_t k = 0; k < a.kb; ++k, ++i) {
                 const uint32_t st = i % NST, to = base + st * SM::kStage;
                 if (!(ok = mbar_wait(empty + 8 * st, ((i / NST) & 1) ^ 1, dead))) break;
                 if (elect_one()) {
-                    if (rank == 0) mbar_expect(full + 8 * st, 2 * SM::kStage);      // both blocks' loads complete here
+                    if (rank == 0) mbar_expect(full + 8 * st, bytes);       // both blocks' loads complete here
                     pair_load2(to, &map_x, lead + 8 * st, k * kK, row);
-                    pair_load2(to + 16384, &map_w, lead + 8 * st, k * kK, ch);
+                    if (mine) pair_load2(to + 16384, &map_w, lead + 8 * st, k * kK, ch);
                 }
                 __syncwarp();
             }
@@ -484,13 +487,15 @@ unsigned split_k(int64_t tiles, int32_t kb)
 }
 
 template <int BF16, int NT>
-cudaError_t tile_launch(const args &a, const void *w8, const void *x8, int64_t K, cudaStream_t s)
+cudaError_t tile_launch(args a, const void *w8, const void *x8, int64_t K, cudaStream_t s)
 {
     static std::atomic<bool> done[64];
     constexpr size_t bytes = tile_smem<NT>::kBytes;
     cudaError_t e = allow_smem(tdp_matmul8_tile_kernel<BF16, NT>, bytes, done);
     CUtensorMap w, x;
-    if (e == cudaSuccess && (!map8(&w, w8, K, a.N, 128) || !map8(&x, x8, K, a.rows, NT))) e = cudaErrorInvalidValue;
+    a.w_box = std::min(128, a.N);
+    a.x_box = (int32_t)std::min<int64_t>(NT, a.rows);
+    if (e == cudaSuccess && (!map8(&w, w8, K, a.N, a.w_box) || !map8(&x, x8, K, a.rows, a.x_box))) e = cudaErrorInvalidValue;
     if (e != cudaSuccess) return e;
     const int64_t tiles = (int64_t)a.tiles_c * ((a.rows + NT - 1) / NT);
     const unsigned split = split_k(tiles, a.kb);
@@ -504,7 +509,9 @@ cudaError_t pair_launch(args a, const void *w8, const void *x8, int64_t K, cudaS
     constexpr size_t bytes = pair_smem::kBytes;
     cudaError_t e = allow_smem(tdp_matmul8_pair_kernel<BF16, RES>, bytes, done);
     CUtensorMap w, x, o, r;
-    if (e == cudaSuccess && (!map8(&w, w8, K, a.N, 128) || !map8(&x, x8, K, a.rows, 128) || !map_out(&o, a.out, BF16, a.N, a.rows) ||
+    a.w_box = std::min(128, a.N);
+    a.x_box = 128;
+    if (e == cudaSuccess && (!map8(&w, w8, K, a.N, a.w_box) || !map8(&x, x8, K, a.rows, a.x_box) || !map_out(&o, a.out, BF16, a.N, a.rows) ||
                              !map_out(&r, RES ? const_cast<void *>(a.res) : a.out, BF16, a.N, a.rows)))
         e = cudaErrorInvalidValue;
     if (e != cudaSuccess) return e;
@@ -517,16 +524,19 @@ cudaError_t pair_launch(args a, const void *w8, const void *x8, int64_t K, cudaS
 // every stage of a block, in us as measured.  K = N = 2048, 16 / 128 / 512 / 1024 / 2048 rows: 3.9 / 5.3 / 13.1 / 24.7 / - by 16 rows,
 // 4.5 / 5.2 / 7.3 / 14.0 / - by 32, 6.0 / 6.6 / 7.5 / 9.6 / - by 64, 8.8 / 9.3 / 9.5 / 9.8 / 10.6 by pairs; K = N = 4096: 4.7 / 9.9 / 37.7 /
 // 70.6, 5.9 / 7.9 / 21.5 / 41.5, 8.5 / 7.9 / 13.7 / 26.2 and 13.0 / 13.6 / 14.0 / 15.3 / 24.0.  (Tiles of 128 rows were never best;
-// eight stages in place of four, and so one block an SM, took 8.1 us where 32 rows take 5.2.)
-int choose(int64_t rows, int32_t N, int32_t kb)
+// eight stages in place of four, and so one block an SM, took 8.1 us where 32 rows take 5.2.)  Rows of K values that are no multiple of 128
+// lie across lines, of 32 across sectors, which costs the smaller tiles more: 12982 x 128, K = 1280 / 1296 / 1312, takes 8.3 / 14.8 / 9.9 us by 64
+// rows, x 136 by pairs 7.6 / 8.9 / 7.9.
+int choose(int64_t rows, int32_t N, int64_t K, int32_t kb)
 {
+    const double across = K % 32 ? 1.9 : K % 128 ? 1.25 : 1.0, across2 = K % 32 ? 1.2 : 1.0;
     constexpr int nt[3] = {16, 32, 64};
     constexpr double end[3] = {2.3, 2.6, 3.4}, stage[3] = {0.20, 0.235, 0.285};
-    double least = 5.0 + 0.275 * kb * (double)(((rows + 255) / 256 * ((N + 255) / 256) + 75) / 76);
+    double least = 5.0 + 0.275 * across2 * kb * (double)(((rows + 255) / 256 * ((N + 255) / 256) + 75) / 76);
     int best = 0;
     for (int i = 0; i < 3; ++i) {
         const int64_t tiles = (rows + nt[i] - 1) / nt[i] * ((N + 127) / 128), split = split_k(tiles, kb);
-        const double cost = 1.0 + (end[i] + stage[i] * (double)((kb + split - 1) / split)) * (double)((tiles * split + 303) / 304);
+        const double cost = 1.0 + (end[i] + stage[i] * across * (double)((kb + split - 1) / split)) * (double)((tiles * split + 303) / 304);
         if (cost < least) {
             least = cost;
             best = nt[i];
@@ -538,7 +548,7 @@ int choose(int64_t rows, int32_t N, int32_t kb)
 template <int BF16>
 cudaError_t matmul8(const args &a, const void *w8, const void *x8, int64_t K, cudaStream_t s)
 {
-    switch (choose(a.rows, a.N, a.kb)) {
+    switch (choose(a.rows, a.N, K, a.kb)) {
     case 16: return tile_launch<BF16, 16>(a, w8, x8, K, s);
     case 32: return tile_launch<BF16, 32>(a, w8, x8, K, s);
     case 64: return tile_launch<BF16, 64>(a, w8, x8, K, s);
@@ -565,7 +575,7 @@ extern "C" tdp_status tdp_matmul8(tdp_plan_t plan, int64_t rows, int32_t K, int3
         !tdp_aligned(x8_scale, 4) || !tdp_aligned(w8_scale, 16))
         return tdp_fail(TDP_ERR_MISALIGNED, "rows, w8_scale and bias need 16-byte, x8_scale 4-byte alignment");
     if ((rows + 127) / 128 * ((N + 127) / 128) > (1 << 28)) return tdp_fail(TDP_ERR_TOO_LARGE, "rows * N above 2^42");
-    args a = {x8_scale, w8_scale, bias, res, out, rows, N, (K + kK - 1) / kK, (N + 127) / 128, 0};
+    args a = {x8_scale, w8_scale, bias, res, out, rows, N, (K + kK - 1) / kK, (N + 127) / 128, 0, 0, 0};
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     const cudaError_t err = g.dtype == TDP_BF16 ? matmul8<1>(a, w8, x8, K, s) : matmul8<0>(a, w8, x8, K, s);
     return err == cudaSuccess ? tdp_ok() : tdp_fail(TDP_ERR_CUDA, cudaGetErrorString(err));

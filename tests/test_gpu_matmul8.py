@@ -55,7 +55,7 @@ def _check(tdp, dtype, rows, K, N, bias=True, res=True):
         assert float((got - want).norm() / want.norm()) < 2 * (K ** 0.5 + 8) * U
 
 
-SIZES = [(60000, 64, 8), (33, 2048, 2048), (400, 2048, 2048), (1024, 4096, 1024)] + [(1, 16, 8), (8, 4096, 4096), (3, 32, 24), (16, 1040, 136), (17, 128, 128), (40, 48, 1000), (64, 272, 264), (65, 4096, 72), (100, 96, 2048),
+SIZES = [(60000, 64, 8), (30000, 512, 72), (20000, 128, 128), (19000, 256, 384), (300, 96, 8), (70000, 272, 40), (13000, 512, 136), (33, 2048, 2048), (400, 2048, 2048), (1024, 4096, 1024)] + [(1, 16, 8), (8, 4096, 4096), (3, 32, 24), (16, 1040, 136), (17, 128, 128), (40, 48, 1000), (64, 272, 264), (65, 4096, 72), (100, 96, 2048),
          (128, 512, 256), (129, 1040, 1004), (300, 2048, 640), (1237, 1040, 1004), (700, 16, 3000), (4000, 640, 520), (19500, 256, 264),
          (5121, 144, 1000), (10000, 2048, 512)]
 
