@@ -6,7 +6,7 @@
 // 8 bits (e4m3, a scale a row): v -> e4m3(448 v / m), m the row's largest |v|, scale m / 448.
 //
 // Bound by memory.  A row is read once: a team of lanes (a part of a warp, a warp, or up to eight warps) brings it to shared
-// memory, each lane its own 16-byte vectors, two rows ahead (the gradient one), some 130 KB an SM on their way; sums and largest
+// memory, each lane its own 16-byte vectors, a row ahead, some 100 KB an SM on their way; sums and largest
 // values are joined over the team, and the second pass reads shared memory or registers.  Nobody but the lane itself reads its
 // vectors, so no barrier stands between a copy and its use.  The gradient keeps its sums for dw in registers over all its rows, joins
 // a block's in shared memory and the blocks' in a second launch, in a fixed order.
@@ -28,8 +28,11 @@ using tdp_tc::mul2;
 using tdp_tc::pair;
 using tdp_tc::unpair;
 
-constexpr int kNormThreads = 256;           // threads of a block at most: eight warps a row
-constexpr int kNormVecs = 8, kGradVecs = 4; // vectors of a lane, forward and gradient (more for rows of more than 1024)
+// Threads of a block at most: a lane's registers hold its vectors, and in the gradient their sums for dw.
+constexpr int kNormThreads = 512;
+constexpr int norm_threads(int vpt, bool grad) { return vpt <= (grad ? 4 : 6) ? kNormThreads : 256; }
+constexpr int kNormWarps = 8;               // warps of a row at most
+constexpr int kNormVecs = 6, kGradVecs = 4; // vectors of a lane, forward and gradient (eight where eight warps need them)
 constexpr int kSMs = 152;
 constexpr int kNormSmem = 196608;           // bytes of rows that an SM has on their way and at work
 constexpr float kLeast = 0x1p-100f;
@@ -185,11 +188,11 @@ __device__ __forceinline__ void join(int32_t lanes, int32_t warps, int32_t turn,
 
 // NORM 0: the rows themselves, in 8 bits.  Q8: with outputs in 8 bits.  RES: with a residual.
 template <int BF16, int VPT, int NORM, int Q8, int RES>
-__global__ void __launch_bounds__(kNormThreads)
+__global__ void __launch_bounds__(norm_threads(VPT, false))
 tdp_rms_norm_kernel(const __grid_constant__ norm_args a)
 {
     using E = tdp_elem<BF16>;
-    constexpr int V = E::kVec, P = V / 2, IN = 1 + RES, S = RES ? 3 : 6;     // inputs, rows in shared memory
+    constexpr int V = E::kVec, P = V / 2, IN = 1 + RES, S = 2;       // inputs, rows in shared memory
     extern __shared__ __align__(16) uint4 slots[];      // [S][IN][VPT][threads]
     tdp_pdl_trigger();
     tdp_pdl_wait();
@@ -338,7 +341,7 @@ tdp_rms_norm_kernel(const __grid_constant__ norm_args a)
 
 // KEPT8: u is x8 * x8_scale; otherwise h * rstd.  The rows stay in shared memory for the second pass.
 template <int BF16, int VPT, int KEPT8>
-__global__ void __launch_bounds__(kNormThreads)
+__global__ void __launch_bounds__(norm_threads(VPT, true))
 tdp_rms_norm_grad_kernel(const __grid_constant__ norm_grad_args a)
 {
     using E = tdp_elem<BF16>;
@@ -490,39 +493,33 @@ tdp_rms_norm_dw_kernel(const float *part, int32_t parts, int32_t C, float *dw)
 
 // How rows are dealt to teams.
 struct norm_shape {
-    int32_t nv, vpt, lanes, warps, threads, rows;           // rows: of a block and round
+    int32_t vpt, lanes, warps, threads, rows;           // rows: of a block and round
     int64_t blocks;
 };
 
-// vecs: vectors of a lane at most, as long as eight warps hold a row.  Few rows take more lanes each.
-norm_shape norm_deal(int64_t rows, int32_t nv, int32_t vecs, bool wide)
+// vecs: vectors of a lane at most, as long as eight warps hold a row; inputs: of a row in shared memory, twice; busy: threads that an
+// SM is to have.  Measured (bf16, 400 million values, floors 177, 412 and 236 us): best are four to six vectors a lane and one row
+// ahead, 384 threads for a norm into 8 bits with a residual (2992 channels 406 us, 4096 443, 768 406; one warp of eight vectors, two rows
+// ahead and 256 threads take 490 to 670), 512 without 8 bits (236 to 253), 768 for rows into 8 bits (174 to 190; eight vectors and 256
+// threads up to 390), 512 in the gradient; large blocks before small ones.
+norm_shape norm_deal(int64_t rows, int32_t nv, int32_t vecs, int32_t inputs, int32_t busy, bool grad = false)
 {
     norm_shape s;
-    s.nv = nv;
+    if (rows <= 2 * kSMs) vecs = 2;         // few rows take more lanes each
     s.lanes = 1;
-    if (rows <= 2 * kSMs) vecs = 2;
-    // narrow rows: four vectors a lane, not one (1 million rows of 128 bf16: quantised in 63 us for 98, the gradient 153 for 178);
-    // eight only from 96 on (160000 rows of 768 into 8 bits 145 us for 161; rows of 64 would take 293 for 156)
-    while (s.lanes < 32 && nv > s.lanes * (nv < 96 ? std::min(vecs, 4) : vecs)) s.lanes *= 2;
-    // the fewest places for the row's vectors, with few warps: 640 vectors are five a lane of four warps and not eight of three
-    // (20000 rows of 5120 bf16 into 8 bits 122 us for 189), but 160 three of two and not one of five (the gradient 40 us for 85)
-    const auto of_lane = [nv](int32_t lanes) {
-        const int32_t need = (nv + lanes - 1) / lanes;
-        return need == 7 ? 8 : need;
-    };
-    s.warps = std::min(kNormThreads / 32, (nv + 32 * vecs - 1) / (32 * vecs));
-    for (int32_t w = s.warps + 1; s.lanes == 32 && w <= kNormThreads / 32; ++w)
-        if (w * of_lane(32 * w) < s.warps * of_lane(32 * s.warps) && 2 * of_lane(32 * w) > of_lane(32 * s.warps)) s.warps = w;
+    // narrow rows: four vectors a lane, not one (1 million rows of 128 bf16: quantised in 63 us for 98, the gradient 153 for 178)
+    while (s.lanes < 32 && nv > s.lanes * std::min(vecs, 4)) s.lanes *= 2;
+    s.warps = s.lanes < 32 ? 1 : std::min(kNormWarps, (nv + 32 * vecs - 1) / (32 * vecs));
     s.lanes *= s.warps;
-    s.vpt = of_lane(s.lanes);
-    // rows of a block: as many as fit where there are rows for all SMs (eight of a warp each: 168960 x 2048 quantised in 153 us, four
-    // 177); of several warps one in the forward (40000 x 4096 into 8 bits 179 us, four 192), all in the gradient (200 us for 261)
-    const int32_t least = std::max(1, 32 / s.lanes), most = s.warps > 1 && !wide ? 1 : kNormThreads / s.lanes;
-    s.rows = least;
-    while (2 * s.rows <= most && rows >= 2 * s.rows * kSMs) s.rows *= 2;
+    s.vpt = (nv + s.lanes - 1) / s.lanes;
+    if (s.vpt == 7) s.vpt = 8;
+    // rows of a block: whole warps, and blocks for all SMs
+    const int32_t bytes = inputs * 2 * 16 * s.vpt * s.lanes, least = std::max(1, 32 / s.lanes);
+    const int32_t most = std::max(1, std::min({std::min(busy, norm_threads(s.vpt, grad)) / s.lanes, kNormSmem / bytes}));
+    s.rows = (int32_t)std::min<int64_t>(most, std::max<int64_t>(rows / kSMs, 1));
+    s.rows = std::max(least, s.rows / least * least);
     s.threads = s.rows * s.lanes;
-    // as many blocks as are resident: 96 bytes of shared memory a vector, registers for 768 threads at most
-    const int32_t sm = std::max(1, std::min(kNormSmem / (96 * s.vpt), 768) / s.threads);
+    const int32_t sm = std::max(1, std::min((busy + s.threads / 2) / s.threads, kNormSmem / (bytes * s.rows)));
     s.blocks = std::min<int64_t>((rows + s.rows - 1) / s.rows, kSMs * sm);
     return s;
 }
@@ -556,8 +553,8 @@ cudaError_t norm_launch(const norm_shape &sh, const norm_args &a, cudaStream_t s
 {
     static std::atomic<bool> done[64];
     auto *kernel = tdp_rms_norm_kernel<BF16, VPT, NORM, Q8, RES>;
-    const cudaError_t e = allow_smem(kernel, 96 * VPT * kNormThreads, done);
-    return e != cudaSuccess ? e : tdp_launch_smem(true, kernel, (unsigned)sh.blocks, sh.threads, (size_t)96 * VPT * sh.threads, s, a);
+    const cudaError_t e = allow_smem(kernel, kNormSmem, done);
+    return e != cudaSuccess ? e : tdp_launch_smem(true, kernel, (unsigned)sh.blocks, sh.threads, (size_t)32 * (1 + RES) * VPT * sh.threads, s, a);
 }
 
 template <int NORM, int Q8, int RES>
@@ -581,7 +578,7 @@ cudaError_t grad_launch(const norm_shape &sh, const norm_grad_args &a, cudaStrea
 {
     static std::atomic<bool> done[64];
     auto *kernel = tdp_rms_norm_grad_kernel<BF16, VPT, KEPT8>;
-    const cudaError_t e = allow_smem(kernel, 96 * VPT * kNormThreads, done);
+    const cudaError_t e = allow_smem(kernel, kNormSmem, done);
     return e != cudaSuccess ? e : tdp_launch_smem(true, kernel, (unsigned)sh.blocks, sh.threads, (size_t)96 * VPT * sh.threads, s, a);
 }
 
@@ -616,7 +613,7 @@ extern "C" tdp_status tdp_rms_norm(tdp_plan_t plan, int64_t rows, int32_t C, flo
     if (!tdp_aligned(x, 16) || !tdp_aligned(res, 16) || !tdp_aligned(w, 16) || !tdp_aligned(h, 16) || !tdp_aligned(y, 16) ||
         !tdp_aligned(y8, 16) || !tdp_aligned(x8, 16) || !tdp_aligned(rstd, 4) || !tdp_aligned(y8_scale, 4) || !tdp_aligned(x8_scale, 4))
         return tdp_fail(TDP_ERR_MISALIGNED, "rows and w need 16-byte, scales and rstd 4-byte alignment");
-    const norm_shape sh = norm_deal(rows, nv, kNormVecs, false);
+    const norm_shape sh = norm_deal(rows, nv, kNormVecs, res ? 2 : 1, y8 || x8 ? 384 : 512);
     norm_args a = {rows, C, nv, sh.lanes, sh.warps, eps, 1.f / (float)C, x, res, w, h, y, rstd, y8, x8, y8_scale, x8_scale};
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     const int bf16 = plan->g.dtype == TDP_BF16;
@@ -635,7 +632,7 @@ extern "C" tdp_status tdp_quant8(tdp_plan_t plan, int64_t rows, int32_t C, const
     if (!x || !x8 || !x8_scale) return tdp_fail(TDP_ERR_INVALID_ARG, "null x, x8 or x8_scale");
     if (!tdp_aligned(x, 16) || !tdp_aligned(x8, 16) || !tdp_aligned(x8_scale, 4))
         return tdp_fail(TDP_ERR_MISALIGNED, "rows need 16-byte, scales 4-byte alignment");
-    const norm_shape sh = norm_deal(rows, nv, kNormVecs, false);
+    const norm_shape sh = norm_deal(rows, nv, kNormVecs, 1, 768);
     norm_args a = {};
     a.rows = rows;
     a.C = C;
@@ -655,7 +652,7 @@ extern "C" tdp_status tdp_rms_norm_grad_workspace(tdp_plan_t plan, int64_t rows,
     if (!bytes) return tdp_fail(TDP_ERR_INVALID_ARG, "null bytes");
     const tdp_status st = norm_check(plan, rows, C, &nv);
     if (st != TDP_OK) return st;
-    *bytes = norm_deal(rows, nv, kGradVecs, true).blocks * C * 4;
+    *bytes = norm_deal(rows, nv, kGradVecs, 3, 512, true).blocks * C * 4;
     return tdp_ok();
 }
 
@@ -666,7 +663,7 @@ extern "C" tdp_status tdp_rms_norm_grad(tdp_plan_t plan, int64_t rows, int32_t C
     int32_t nv = 0;
     const tdp_status st = norm_check(plan, rows, C, &nv);
     if (st != TDP_OK) return st;
-    const norm_shape sh = norm_deal(rows, nv, kGradVecs, true);
+    const norm_shape sh = norm_deal(rows, nv, kGradVecs, 3, 512, true);
     if (rows > 0) {
         if (!rstd || !dy || !dx) return tdp_fail(TDP_ERR_INVALID_ARG, "null rstd, dy or dx");
         if (!h == !x8 || !x8 != !x8_scale) return tdp_fail(TDP_ERR_INVALID_ARG, "need h, or x8 with its scales, and not both");
