@@ -622,7 +622,8 @@ tdp_status tdp_quant8(tdp_plan_t plan, int64_t rows, int32_t C, const void *x, u
  * out, it gives up and fills its outputs with NaN.)
  *
  *   rows, K, N     K a multiple of 16 (of 128 is best, and of 32 better than of 16, for the rows' memory lines), N *
- *                  element size a multiple of 16; at most TDP_MAX_MATMUL8 each, rows at most TDP_MAX_MATMUL8_ROWS, rows * N at most 2^42.
+ *                  element size a multiple of 16 (of 32 is best: outputs that share memory sectors cost up to twice the
+ *                  time of their stores); at most TDP_MAX_MATMUL8 each, rows at most TDP_MAX_MATMUL8_ROWS, rows * N at most 2^42.
  *   x8, x8_scale   device e4m3 [rows, K] and fp32 [rows], read.
  *   w8, w8_scale   device e4m3 [N, K] (an output channel a row) and fp32 [N] (16-byte aligned), read.
  *   bias           device [N] (plan dtype), read; or NULL.
