@@ -33,6 +33,7 @@ def _guarded(n, kind, fill=3.0):
 
 
 # an element, less and more than a warp, an odd number of vectors, one warp's most, several warps, the longest rows
+MANY = [(5000, 24), (3001, 136), (2000, 768), (1300, 1040), (2500, 2048), (700, 2992), (999, 4096), (641, 5120), (330, 8192)]        # rows for every SM
 SHAPES = [(1, 8), (5, 16), (131, 24), (67, 136), (33, 1000), (200, 2048), (9, 2056), (1, 4096), (3, 8192)]
 
 
@@ -50,7 +51,7 @@ def _roundings(C):
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
-@pytest.mark.parametrize("rows,C", SHAPES)
+@pytest.mark.parametrize("rows,C", SHAPES + MANY)
 @pytest.mark.parametrize("res,weight", [(True, True), (False, True), (True, False)])
 def test_forward(tdp, dtype, rows, C, res, weight):
     import torch
@@ -86,7 +87,7 @@ def test_forward(tdp, dtype, rows, C, res, weight):
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
-@pytest.mark.parametrize("rows,C", SHAPES + [(70, 4096)])
+@pytest.mark.parametrize("rows,C", SHAPES + MANY + [(70, 4096)])
 def test_quant(tdp, dtype, rows, C):
     """To the value: of bf16 rows 448 v / m is a quotient of whole numbers below 2^9 and 2^8 times a power of two, and 2^-17
     away from any tie that it does not meet; of fp32 rows those within 2^-21 of a tie may go either way."""
@@ -158,7 +159,7 @@ def test_rows_that_hold_anything(tdp, dtype, C):
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
-@pytest.mark.parametrize("rows,C", SHAPES + [(1500, 64), (700, 2048), (650, 4096)])
+@pytest.mark.parametrize("rows,C", SHAPES + [(1500, 64), (700, 2048), (650, 4096), (690, 1040), (700, 2992), (310, 8192)])
 @pytest.mark.parametrize("kept", ["h", "x8"])
 @pytest.mark.parametrize("dh,weight", [(True, True), (False, False)])
 def test_gradients(tdp, dtype, rows, C, kept, dh, weight):
@@ -231,6 +232,36 @@ def test_in_place_and_nothing(tdp):
     tdp.tdp_quant8(plan, none, none.to(torch.float8_e4m3fn), torch.empty(0, device="cuda"))
     tdp.tdp_rms_norm_grad(plan, none, none, w, torch.empty(0, device="cuda"), h=none, dw=dw)
     assert (dw == 0).all()
+
+
+@pytest.mark.parametrize("rows,C,dtype", [(400, 16384, "bf16"), (310, 14000, "bf16"), (400, 8192, "f32"), (2, 16384, "bf16")])
+def test_longest_rows(tdp, rows, C, dtype):
+    """Eight warps a row, eight vectors a lane: the row's result as torch's in 64 bits, forward alone (with and without 8 bits), and
+    the gradient's two forms against each other's formula by way of test_gradients' bounds."""
+    import torch
+    dt = torch.float32 if dtype == "f32" else torch.bfloat16
+    x, s, w, dy, _ = _inputs(rows, C, dt, 9)
+    plan, y, y2, h = _plan(tdp, dtype), torch.empty_like(x), torch.empty_like(x), torch.empty_like(x)
+    rstd, y8, ys = torch.empty(rows, device="cuda"), torch.empty(x.shape, dtype=torch.float8_e4m3fn, device="cuda"), torch.empty(rows, device="cuda")
+    tdp.tdp_rms_norm(plan, x, w, y, res=s, h=h, rstd=rstd)
+    tdp.tdp_rms_norm(plan, x, w, y2, res=s, y8=y8, y8_scale=ys)
+    hd, wd = h.double(), w.double()
+    r = (hd.square().mean(1) + 1e-6).rsqrt()
+    want = hd * r[:, None] * wd
+    k = _roundings(C) * U
+    assert ((rstd.double() - r).abs() <= k * r).all()
+    tol = (k + 2 * U) * want.abs() + (2.0 ** -8 * want.abs() if dtype == "bf16" else 0) + 1e-37
+    assert ((y.double() - want).abs() <= tol).all() and ((y2.double() - want).abs() <= tol).all()
+    assert ((y8.double() * ys.double()[:, None] - want).abs() <= ys.double()[:, None] * 2.0 ** -10 + 1.001 * 2.0 ** -4 * want.abs()).all()
+    dx, dw = torch.empty_like(x), torch.empty(C, device="cuda")
+    tdp.tdp_rms_norm_grad(plan, dy, dx, w, rstd, h=h, dw=dw)
+    u = hd * rstd.double()[:, None]
+    g = dy.double() * wd
+    size = rstd.double()[:, None] * (g.abs() + u.abs() * (g * u).abs().mean(1, keepdim=True))
+    want = rstd.double()[:, None] * (g - u * (g * u).mean(1, keepdim=True))
+    assert ((dx.double() - want).abs() <= 88 * U * size + (2.0 ** -8 * want.abs() if dtype == "bf16" else 0) + 1e-37).all()
+    terms = dy.double() * u
+    assert ((dw.double() - terms.sum(0)).abs() <= (rows + 3) * U * terms.abs().sum(0)).all()
 
 
 def test_captured_and_on_streams(tdp):
