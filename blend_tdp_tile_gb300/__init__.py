@@ -189,6 +189,7 @@ class Plan:
         self._h = ctypes.c_void_p(handle)
         self.problem = problem
         self.sizes = {}             # workspace bytes by shape
+        self.ropes = {}             # tdp_rope's C shapes
         self.lat = None             # element types of the plan's dtype, once asked for
         self.scratch = _Scratch()
         n = ctypes.c_int32()
@@ -962,18 +963,30 @@ def tdp_rope_table(freq, axis):
 
 def _rope(where, fn, plan, x, Q, table, out, layout, at, scale, stream):
     torch = _torch()
-    lat = _latent_dtypes(plan)
-    if not isinstance(x, torch.Tensor) or not isinstance(table, torch.Tensor):
+    lat = plan.lat or _latent_dtypes(plan)
+    if not isinstance(x, torch.Tensor) or not isinstance(out, torch.Tensor) or not isinstance(table, torch.Tensor):
         raise TypeError(f"{where}: expected torch.Tensors")
     if x.dim() != 3:
         raise ValueError("rows must be [rows, heads, D]")
-    R, H, D = x.shape
+    # the C shape of these shapes, strides and names, made and seen to be right once
+    R, H, D = xs = x.shape
     shape = (_rows(plan), H, D)
-    a = _Rope(H, D, 2 * table.numel(), _named(layout, _LAYOUTS, "layout"), _named(at, _PLACES, "at"), scale,
-              *_strides(x, "x", shape, lat), *_strides(out, "out", shape, lat))
+    if not x.is_cuda or not out.is_cuda:
+        _strides(x, "x", shape, lat), _strides(out, "out", shape, lat)          # says so
+    xp, op, pairs = x.data_ptr(), out.data_ptr(), table.numel()
+    key = (xs, out.shape, x.stride(), out.stride(), pairs, layout, at, scale)
+    a = plan.ropes.get(key)
+    if a is None or xp % 16 or op % 16 or x.dtype not in lat or out.dtype not in lat:
+        a = _Rope(H, D, 2 * pairs, _named(layout, _LAYOUTS, "layout"), _named(at, _PLACES, "at"), scale,
+                  *_strides(x, "x", shape, lat), *_strides(out, "out", shape, lat))
+        if len(plan.ropes) > 1000:
+            plan.ropes.clear()
+        plan.ropes[key] = a
     c = _Call(where)
-    c.run(fn, plan.handle, ctypes.byref(a), _given(c, x, "x"), c.ptr(Q, "Q", 6 * shape[0], (torch.int32,), 8),
-          c.ptr(table, "table", table.numel(), (torch.int64,), 8), _given(c, out, "out"), stream=stream)
+    c.on(x, "x")
+    q, t = c.ptr(Q, "Q", 6 * xs[0], (torch.int32,), 8), c.ptr(table, "table", pairs, (torch.int64,), 8)
+    c.on(out, "out")
+    c.run(fn, plan.handle, ctypes.byref(a), xp, q, t, op, stream=stream)
 
 
 def tdp_rope(plan: Plan, x, Q, table, out, layout="half", at="middle", scale=1.0, stream=None):

@@ -135,6 +135,18 @@ def test_broadcast_and_refused_strides(tdp):
     for bad in (many[:, :, ::2], many.transpose(1, 2)[:, :, :6]):
         with pytest.raises(ValueError):
             tdp.tdp_rope(s["plan"], bad, s["Q"], s["table"], torch.empty_like(bad))
+    # what is kept of a shape that was right says nothing of the next call's buffers
+    buf = torch.empty(40 * 6 * 64 + 8, dtype=torch.bfloat16, device="cuda")
+    with pytest.raises(ValueError, match="aligned"):
+        tdp.tdp_rope(s["plan"], many, s["Q"], s["table"], buf[1:1 + many.numel()].view(many.shape))
+    with pytest.raises(ValueError, match="dtype"):
+        tdp.tdp_rope(s["plan"], many.float(), s["Q"], s["table"], many)
+    with pytest.raises(ValueError, match="shape"):
+        tdp.tdp_rope(s["plan"], many, s["Q"], s["table"], many[:, :5])
+    with pytest.raises(ValueError, match="elements"):
+        tdp.tdp_rope(s["plan"], many, s["Q"][:-1], s["table"], many)
+    with pytest.raises(ValueError, match="layout"):
+        tdp.tdp_rope(s["plan"], many, s["Q"], s["table"], many, layout="other")
     with pytest.raises(ValueError, match="contiguous"):
         tdp.tdp_rms_norm(s["plan"], s["x"][:, ::2], None, s["y"][:, ::2])
     with pytest.raises(ValueError, match="dtype"):

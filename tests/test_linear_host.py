@@ -168,8 +168,12 @@ def test_binding_refuses(tdp):  # noqa: F811
         tdp.tdp_matmul8(plan, x, x, torch.zeros(8, 32), x, x)
     with pytest.raises(ValueError, match="rows must be"):
         tdp.tdp_rope(plan, x, x, torch.zeros(4, dtype=torch.int64), x)
-    with pytest.raises(ValueError, match="layout"):
-        tdp.tdp_rope(plan, torch.zeros(plan.total_tile_tokens, 2, 64), x, torch.zeros(4, dtype=torch.int64), x, layout="other")
+    heads = torch.zeros(plan.total_tile_tokens, 2, 64)
+    for other in (heads, heads.to_sparse(), heads.to("meta")):
+        with pytest.raises(ValueError, match="CUDA"):
+            tdp.tdp_rope(plan, other, x, torch.zeros(4, dtype=torch.int64), other)
+    with pytest.raises(TypeError):
+        tdp.tdp_rope(plan, heads, x, torch.zeros(4, dtype=torch.int64), None)
 
 
 def test_header_and_binding_agree(tdp):  # noqa: F811
