@@ -141,6 +141,34 @@ __device__ __forceinline__ void store8(uint8_t *p, const uint64_t *v)
 // and NaN in every place; 2^-100 for less.
 __device__ __forceinline__ float top8(float top) { return top < INFINITY ? fmaxf(top, kLeast) : NAN; }
 
+// How a norm's rows v rstd become e4m3: 448 v rstd / m.  m is rstd times the row's largest |v|, `top`, so rstd cancels and 448 v / top
+// is left, a quotient of numbers as they came: of bf16 rows (h, or h w, which fp32 holds) often midway between two of e4m3's.  The
+// factor is kept in two parts, so that one rounding is left and such a value stays where it is and goes to the even one; a product
+// with the first part alone puts 0.05 % of x8's values on the wrong side.
+struct code8 {
+    uint64_t k, rest;
+    // y = top * rstd, m = top8(y); lift: what v is multiplied by before, 1 or 2^100.  top * lift is 2^-118 at least, or y below 2^-100.
+    __device__ __forceinline__ void make(float top, float rstd, float y, float m, float lift)
+    {
+        const float den = m < INFINITY ? top * lift : NAN;
+        float inv;
+        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(den * (1 / 64.f)));      // neither is too small for fp32
+        float f = inv * 7.f, r = fmaf(-f, den, 448.f) * (inv * (1 / 64.f));
+        if (y < kLeast) {           // m counts as 2^-100
+            f = 448.f / kLeast / lift * rstd;
+            r = 0.f;
+        }
+        k = pair(f, f);
+        rest = pair(r, r);
+    }
+    template <int P>
+    __device__ __forceinline__ void of(uint64_t *v) const
+    {
+#pragma unroll
+        for (int j = 0; j < P; ++j) v[j] = fma2(v[j], k, mul2(v[j], rest));
+    }
+};
+
 // A thread's place: its row among those of a round, its lane in the row's team.
 struct team {
     int32_t lane, row, rows;        // rows: of a block and round
@@ -186,13 +214,18 @@ __device__ __forceinline__ void join(int32_t lanes, int32_t warps, int32_t turn,
     }
 }
 
-// NORM 0: the rows themselves, in 8 bits.  Q8: with outputs in 8 bits.  RES: with a residual.
+// What is written in 8 bits: nothing; the checkpoint x8 and no y8; y8, or both; the same where eps leaves rstd above 2^18 (see
+// code8::make).  The checkpoint has a form of its own as y goes with it: 168960 rows of 2048 bf16 take 272 us by it and 338 by the next.
+enum { kPlain = 0, kKept8 = 1, kAny8 = 2, kSmall8 = 3 };
+
+// NORM 0: the rows themselves, in 8 bits.  RES: with a residual.
 template <int BF16, int VPT, int NORM, int Q8, int RES>
 __global__ void __launch_bounds__(norm_threads(VPT, false))
 tdp_rms_norm_kernel(const __grid_constant__ norm_args a)
 {
     using E = tdp_elem<BF16>;
     constexpr int V = E::kVec, P = V / 2, IN = 1 + RES, S = 2;       // inputs, rows in shared memory
+    constexpr bool Y8 = Q8 >= kAny8, SMALL = Q8 == kSmall8;
     extern __shared__ __align__(16) uint4 slots[];      // [S][IN][VPT][threads]
     tdp_pdl_trigger();
     tdp_pdl_wait();
@@ -255,8 +288,8 @@ tdp_rms_norm_kernel(const __grid_constant__ norm_args a)
 #pragma unroll
                 for (int j = 0; j < P; ++j) sum2 = fma2(f[j], f[j], sum2);
             }
-            if (Q8 && (!NORM || a.x8)) top_of<P>(f, top2);
-            if (NORM && Q8 && a.y8) {
+            if (Q8 && (!NORM || !Y8 || a.x8)) top_of<P>(f, top2);
+            if (NORM && Y8 && a.y8) {
                 if (a.w) {
                     uint64_t g[P];
                     pairs_of<BF16>(w[i], g);
@@ -273,38 +306,61 @@ tdp_rms_norm_kernel(const __grid_constant__ norm_args a)
         join<Q8>(a.lanes, a.warps, turn, sum, top, top2);
         const float rstd = NORM ? __frcp_rn(__fsqrt_rn(fmaf(sum, a.mean, a.eps))) : 1.f;
         if (NORM && a.rstd && on && t.lane == 0) a.rstd[r] = rstd;
-        uint64_t ky = 0, kx = 0;
         float part = 0.f, inv = 0.f;
-        if (Q8 && NORM && a.y8) {
-            const float m = top8(top * rstd);
+        code8 cy = {}, cx = {};
+        const float lift_y = SMALL && top < kLeast ? 1 / kLeast : 1.f, lift_x = SMALL && top2 < kLeast ? 1 / kLeast : 1.f;
+        if (Y8 && NORM && a.y8) {
+            const float y = top * rstd, m = top8(y);
             if (on && t.lane == 0) a.y8_scale[r] = __fdiv_rn(m, 448.f);
-            const float k = __fdiv_rn(448.f, m);
-            ky = pair(k, k);
+            cy.make(top, rstd, y, m, lift_y);
         }
-        if (Q8 && a.x8) {
-            const float m = top8(top2 * rstd);
-            if (on && t.lane == 0) a.x8_scale[r] = __fdiv_rn(m, 448.f);
+        if (Q8 && (!Y8 || a.x8)) {
             if (NORM) {
-                const float k = __fdiv_rn(448.f, m);
-                kx = pair(k, k);
+                const float y = top2 * rstd, m = top8(y);
+                if (on && t.lane == 0) a.x8_scale[r] = __fdiv_rn(m, 448.f);
+                cx.make(top2, rstd, y, m, lift_x);
             } else {
+                const float m = top8(top2);
+                if (on && t.lane == 0) a.x8_scale[r] = __fdiv_rn(m, 448.f);
                 part = -m * (1.f / 512);
                 inv = __frcp_rn(-part);
             }
         }
         if (!on) continue;
         const uint64_t rs = pair(rstd, rstd);
+        // y beside y8: h rstd before w, as without 8 bits.  Within the loop below it costs calls without y a tenth; before it, more
+        // than four vectors a lane want more registers than there are, and behind it 168960 x 2048 with a residual take 2 % longer.
+        auto plain = [&] {
+            if (!NORM || !Y8 || !a.y) return;
+#pragma unroll
+            for (int i = 0; i < VPT; ++i) {
+                const int32_t c = t.lane + i * a.lanes;
+                if (c >= a.nv) break;
+                uint64_t f[P], g[P];
+                pairs_of<BF16>(x[i], f);
+                if (a.w) pairs_of<BF16>(w[i], g);
+#pragma unroll
+                for (int j = 0; j < P; ++j) {
+                    f[j] = mul2(f[j], rs);
+                    if (a.w) f[j] = mul2(f[j], g[j]);
+                }
+                static_cast<uint4 *>(a.y)[at + c] = of_pairs<BF16>(f);
+            }
+        };
+        if (VPT <= 4) plain();
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
             const int32_t c = t.lane + i * a.lanes;
             if (c >= a.nv) break;
             uint64_t f[P], q[P];
+            // h w is made again: carried over from the first pass in registers, 8192 channels take 25 % longer
+            if (Y8 && VPT > 4) asm volatile("" : "+r"(x[i].x), "+r"(x[i].y), "+r"(x[i].z), "+r"(x[i].w));
             pairs_of<BF16>(x[i], f);
             if (!NORM) {
                 // 448 v / m as (0.875 v) / (m / 512): no product overflows and a value midway between two of e4m3's comes out
                 // exact, so that it goes to the even one.  The quotient is corrected by its remainder (P. Markstein, "Computation of
                 // elementary functions on the IBM RISC System/6000 processor", 1990): the plain product v * inv put 0.5 % of
-                // bf16's values on the wrong side.  (A norm's rows have no such values: there the product does.)
+                // bf16's values on the wrong side.
                 const uint64_t e = pair(0.875f, 0.875f), n = pair(part, part), k = pair(inv, inv);
 #pragma unroll
                 for (int j = 0; j < P; ++j) {
@@ -315,12 +371,15 @@ tdp_rms_norm_kernel(const __grid_constant__ norm_args a)
                 store8<P>(a.x8 + (at + c) * V, q);
                 continue;
             }
+            if (Q8 && (!Y8 || a.x8)) {
 #pragma unroll
-            for (int j = 0; j < P; ++j) f[j] = mul2(f[j], rs);
-            if (Q8 && a.x8) {
-#pragma unroll
-                for (int j = 0; j < P; ++j) q[j] = mul2(f[j], kx);
+                for (int j = 0; j < P; ++j) q[j] = SMALL ? mul2(f[j], pair(lift_x, lift_x)) : f[j];
+                cx.of<P>(q);
                 store8<P>(a.x8 + (at + c) * V, q);
+            }
+            if (!Y8) {
+#pragma unroll
+                for (int j = 0; j < P; ++j) f[j] = mul2(f[j], rs);
             }
             if (a.w) {
                 uint64_t g[P];
@@ -328,13 +387,15 @@ tdp_rms_norm_kernel(const __grid_constant__ norm_args a)
 #pragma unroll
                 for (int j = 0; j < P; ++j) f[j] = mul2(f[j], g[j]);
             }
-            if (Q8 && a.y8) {
+            if (Y8 && a.y8) {
 #pragma unroll
-                for (int j = 0; j < P; ++j) q[j] = mul2(f[j], ky);
+                for (int j = 0; j < P; ++j) q[j] = SMALL ? mul2(f[j], pair(lift_y, lift_y)) : f[j];
+                cy.of<P>(q);
                 store8<P>(a.y8 + (at + c) * V, q);
             }
-            if (a.y) static_cast<uint4 *>(a.y)[at + c] = of_pairs<BF16>(f);
+            if (!Y8 && a.y) static_cast<uint4 *>(a.y)[at + c] = of_pairs<BF16>(f);
         }
+        if (VPT > 4) plain();
     }
     copy_wait<0>();
 }
@@ -500,7 +561,8 @@ struct norm_shape {
 // vecs: vectors of a lane at most, as long as eight warps hold a row; inputs: of a row in shared memory, twice; busy: threads that an
 // SM is to have.  Measured (bf16, 400 million values, floors 177, 412 and 236 us): best are four to six vectors a lane and one row
 // ahead, 384 threads for a norm into 8 bits with a residual (2992 channels 406 us, 4096 443, 768 406; one warp of eight vectors, two rows
-// ahead and 256 threads take 490 to 670), 512 without 8 bits (236 to 253), 768 for rows into 8 bits (174 to 190; eight vectors and 256
+// ahead and 256 threads take 490 to 670) or with y (2048 channels 272 us for 170 million values; 512 threads 275), 512 into 8 bits alone (2048
+// channels 264 us for 346 million values; 384 threads 300) and without 8 bits (236 to 253), 768 for rows into 8 bits (174 to 190; eight vectors and 256
 // threads up to 390), 512 in the gradient; large blocks before small ones.
 norm_shape norm_deal(int64_t rows, int32_t nv, int32_t vecs, int32_t inputs, int32_t busy, bool grad = false)
 {
@@ -555,6 +617,13 @@ cudaError_t norm_launch(const norm_shape &sh, const norm_args &a, cudaStream_t s
     auto *kernel = tdp_rms_norm_kernel<BF16, VPT, NORM, Q8, RES>;
     const cudaError_t e = allow_smem(kernel, kNormSmem, done);
     return e != cudaSuccess ? e : tdp_launch_smem(true, kernel, (unsigned)sh.blocks, sh.threads, (size_t)32 * (1 + RES) * VPT * sh.threads, s, a);
+}
+
+// Any row as one of eight vectors a lane (norm_deal's for 256 threads).
+template <int RES>
+cudaError_t norm_launch_small(int bf16, const norm_shape &sh, const norm_args &a, cudaStream_t s)
+{
+    return bf16 ? norm_launch<1, 8, 1, kSmall8, RES>(sh, a, s) : norm_launch<0, 8, 1, kSmall8, RES>(sh, a, s);
 }
 
 template <int NORM, int Q8, int RES>
@@ -613,12 +682,15 @@ extern "C" tdp_status tdp_rms_norm(tdp_plan_t plan, int64_t rows, int32_t C, flo
     if (!tdp_aligned(x, 16) || !tdp_aligned(res, 16) || !tdp_aligned(w, 16) || !tdp_aligned(h, 16) || !tdp_aligned(y, 16) ||
         !tdp_aligned(y8, 16) || !tdp_aligned(x8, 16) || !tdp_aligned(rstd, 4) || !tdp_aligned(y8_scale, 4) || !tdp_aligned(x8_scale, 4))
         return tdp_fail(TDP_ERR_MISALIGNED, "rows and w need 16-byte, scales and rstd 4-byte alignment");
-    const norm_shape sh = norm_deal(rows, nv, kNormVecs, res ? 2 : 1, y8 || x8 ? 384 : 512);
+    const bool small = (y8 || x8) && eps < 0x1p-36f;
+    const norm_shape sh = norm_deal(rows, nv, kNormVecs, res ? 2 : 1, small ? 256 : (y8 || x8) && (res || y) ? 384 : 512);
     norm_args a = {rows, C, nv, sh.lanes, sh.warps, eps, 1.f / (float)C, x, res, w, h, y, rstd, y8, x8, y8_scale, x8_scale};
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     const int bf16 = plan->g.dtype == TDP_BF16;
-    const cudaError_t err = y8 || x8 ? (res ? norm_launch<1, 1, 1>(bf16, sh, a, s) : norm_launch<1, 1, 0>(bf16, sh, a, s))
-                                     : (res ? norm_launch<1, 0, 1>(bf16, sh, a, s) : norm_launch<1, 0, 0>(bf16, sh, a, s));
+    const cudaError_t err = small  ? (res ? norm_launch_small<1>(bf16, sh, a, s) : norm_launch_small<0>(bf16, sh, a, s))
+                            : y8   ? (res ? norm_launch<1, kAny8, 1>(bf16, sh, a, s) : norm_launch<1, kAny8, 0>(bf16, sh, a, s))
+                            : x8   ? (res ? norm_launch<1, kKept8, 1>(bf16, sh, a, s) : norm_launch<1, kKept8, 0>(bf16, sh, a, s))
+                                   : (res ? norm_launch<1, kPlain, 1>(bf16, sh, a, s) : norm_launch<1, kPlain, 0>(bf16, sh, a, s));
     return err == cudaSuccess ? tdp_ok() : tdp_fail(TDP_ERR_CUDA, cudaGetErrorString(err));
 }
 
@@ -642,7 +714,7 @@ extern "C" tdp_status tdp_quant8(tdp_plan_t plan, int64_t rows, int32_t C, const
     a.x = x;
     a.x8 = x8;
     a.x8_scale = x8_scale;
-    const cudaError_t err = norm_launch<0, 1, 0>(plan->g.dtype == TDP_BF16, sh, a, reinterpret_cast<cudaStream_t>(stream));
+    const cudaError_t err = norm_launch<0, kKept8, 0>(plan->g.dtype == TDP_BF16, sh, a, reinterpret_cast<cudaStream_t>(stream));
     return err == cudaSuccess ? tdp_ok() : tdp_fail(TDP_ERR_CUDA, cudaGetErrorString(err));
 }
 

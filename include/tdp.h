@@ -559,9 +559,11 @@ tdp_status tdp_dropout_grad(tdp_plan_t plan, int64_t n, double p, const uint64_t
  *   rstd = 1 / sqrt(mean h^2 + eps),  u = h * rstd,  y = u * w.
  * 8 bits are e4m3 (one byte a value) with a scale a row: of a row v with largest magnitude m,
  * counted as 2^-100 where it is less, the values are 448 v / m, to the nearest of e4m3's (the even one of two),
- * and the scale is m / 448; value * scale is v to within half a step.  A row that holds NaN or
- * an infinity has scale NaN and NaN in every place.  (Rows whose sum of squares is above the
- * largest float have rstd = 0.)
+ * and the scale is m / 448; value * scale is v to within half a step.  Where m is not below 2^-100 the quotient is
+ * formed as 448 h / max |h|, of y as 448 h w / max |h w|, in fp32: of bf16 rows it is the nearest value always, of
+ * fp32 rows but for the roundings of h w and of the quotient.  A row that holds NaN or
+ * an infinity has scale NaN and NaN in every place; so has, in y8, a row in which h w is no float.  (Rows whose sum of
+ * squares is above the largest float have rstd = 0.)
  *
  *   rows, C     any number of rows (tile-major rows, heads, states) of C values; C * element
  *               size a multiple of 16 and at most TDP_MAX_NORM_BYTES.

@@ -306,3 +306,60 @@ def test_elements_past_32_bits(tdp):
     tdp.tdp_rms_norm(plan, few, None, y, y8=w8, y8_scale=ws)
     tdp.tdp_rms_norm(plan, x, None, x, y8=v8, y8_scale=vs)
     assert torch.equal(x[-2:], y) and torch.equal(v8[-2:], w8) and torch.equal(vs[-2:], ws)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("rows,C", [(200, 2048), (33, 1000), (2000, 768), (1500, 64), (700, 2992), (400, 8192)])
+@pytest.mark.parametrize("res,weight", [(True, True), (False, False)])
+def test_norm_rows_in_8_bits_to_the_value(tdp, dtype, rows, C, res, weight):
+    """rstd stands in a value and in its row's largest alike: x8 is e4m3 of 448 h / max|h|, y8 of 448 h w / max|h w|, ties to the even one.
+    Of bf16 rows h w has 16 digits, and 448 h w / m is 2^-21 away from any tie that it does not meet; of fp32 rows those within 2^-21 of
+    a tie (roundings of h w, of the largest and of the quotient: 3 * 2^-24) may go either way."""
+    import torch
+    dt = torch.float32 if dtype == "f32" else torch.bfloat16
+    x, s, w, _, _ = _inputs(rows, C, dt, 21)
+    s, w = s if res else None, w if weight else None
+    x8, y8 = (torch.empty((rows, C), dtype=torch.float8_e4m3fn, device="cuda") for _ in range(2))
+    xs, ys = torch.empty(rows, device="cuda"), torch.empty(rows, device="cuda")
+    plan = _plan(tdp, dtype)
+    tdp.tdp_rms_norm(plan, x, w, None, res=s, y8=y8, y8_scale=ys, x8=x8, x8_scale=xs)
+    h = _np((x.float() + s.float()).to(dt) if res else x)
+    for got, v in ((x8, h), (y8, h * (_np(w) if weight else 1.0))):
+        got, v = _np(got.float()), ref.rows8(v)[0]
+        want = ref.e4m3(v)
+        if dtype == "f32":
+            near = ref.e4m3(v * (1 + 2.0 ** -21)) != ref.e4m3(v * (1 - 2.0 ** -21))
+            got, want = got[~near], want[~near]
+        assert np.array_equal(got, want)
+    # the same with one of them alone, and beside y
+    one, y = torch.empty_like(y8), torch.empty_like(x)
+    tdp.tdp_rms_norm(plan, x, w, y, res=s, y8=one, y8_scale=ys)
+    assert torch.equal(one.view(torch.uint8), y8.view(torch.uint8))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("eps", [1e-6, 1e-30])
+def test_norm_rows_of_small_values_in_8_bits(tdp, dtype, eps):
+    """Rows of 2^-111 and of 2^-118: at eps = 1e-30 (rstd 1e15) their largest value is above 2^-100 and cancels as it does in other rows, at
+    1e-6 (rstd 1000) it counts as 2^-100.  The fp32 value before its rounding to e4m3 is 3 * 2^-24 off, with rstd 2^-22."""
+    import torch
+    dt = torch.float32 if dtype == "f32" else torch.bfloat16
+    rows, C = 64, 512
+    x = _inputs(rows, C, torch.bfloat16, 2)[0].double()
+    x /= x.abs().amax(1, keepdim=True)
+    x[::2] *= 2.0 ** -111
+    x[1::2] *= 2.0 ** -118
+    x = x.to(dt)
+    x8, xs = torch.empty((rows, C), dtype=torch.float8_e4m3fn, device="cuda"), torch.empty(rows, device="cuda")
+    tdp.tdp_rms_norm(_plan(tdp, dtype), x, None, None, x8=x8, x8_scale=xs, eps=eps)
+    h = _np(x)
+    rstd = float(np.float32(eps)) ** -0.5             # the squares are no floats
+    least = np.abs(h).max(1) * rstd < ref.LEAST
+    assert least.all() if eps == 1e-6 else not least.any()
+    v = h * rstd * 448 / ref.LEAST if eps == 1e-6 else ref.rows8(h * 2.0 ** 100)[0]
+    off = np.abs(_np(x8.float()) - v)
+    assert (off <= ref.half_step8(v) * (1 + 2.0 ** -18) + np.abs(v) * 2.0 ** -20).all()
+    if eps == 1e-30 and dtype == "bf16":
+        assert np.array_equal(_np(x8.float()), ref.e4m3(v))
+    m = np.maximum(np.abs(h).max(1) * rstd, ref.LEAST)
+    assert (np.abs(_np(xs) - m / 448) <= 8 * U * m / 448).all()
