@@ -193,14 +193,25 @@ def quant8(plan: Plan, x):
 
 class Linear8(torch.nn.Module):
     """A linear layer with its weights in 8 bits, a scale an output channel, for serving: it has no gradients and raises an
-    error where one is asked for."""
+    error where one is asked for.  A change of the module's dtype leaves it alone."""
 
     def __init__(self, plan: Plan, linear: torch.nn.Linear):
         super().__init__()
         w8, scale = quant8(plan, linear.weight)
-        self.register_buffer("w8", w8.view(torch.uint8))         # bytes: a change of the module's dtype leaves them
+        self.register_buffer("w8", w8.view(torch.uint8))
         self.register_buffer("scale", scale)
         self.register_buffer("bias", None if linear.bias is None else linear.bias.detach().clone())
+
+    def _apply(self, fn, recurse=True):
+        """Moves what the layer holds; a change of dtype sees bytes, and leaves weights, scales and bias as they are."""
+        kept = {n: b.dtype for n, b in self._buffers.items() if b is not None}
+        for n in kept:
+            self._buffers[n] = self._buffers[n].view(torch.uint8)
+        try:
+            return super()._apply(fn, recurse)
+        finally:
+            for n, dtype in kept.items():
+                self._buffers[n] = self._buffers[n].view(dtype)
 
     def forward(self, plan: Plan, x, scale=None, res=None):
         """x [.., K] in the plan's dtype, or in 8 bits with its scale; res: what the product is added to, or None."""

@@ -203,3 +203,25 @@ def test_example_runs(tdp, name):
     assert torch.isfinite(Z.float()).all() and torch.isfinite(Z8.float()).all() and not torch.equal(Z, Z8)
     assert set(grads) == {"w", "to_q.weight", "to_kv.weight", "to_out.weight"}
     assert all(torch.isfinite(g.float()).all() and float(g.float().abs().max()) > 0 for g in grads.values())
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_changes_of_dtype_leave_8_bits_alone(tdp, dtype):
+    """Weights, scales and bias in 8 bits are the same to the bit behind any change of dtype; a block served in 8 bits comes back
+    with its weights."""
+    import torch
+    from blend_tdp_tile_gb300.block import Linear8
+    torch.manual_seed(5)
+    dt = torch.float32 if dtype == "f32" else torch.bfloat16
+    plan = tdp.tdp_plan_create(1, 1, 1, 1, 8, dtype, (1, 1, 1), (0, 0, 0))
+    few, x = Linear8(plan, torch.nn.Linear(144, 200, device="cuda", dtype=dt)), torch.randn(37, 144, device="cuda").to(dt)
+    with torch.no_grad():
+        want = few(plan, x)
+        for change in (lambda: few.to(torch.bfloat16), lambda: few.float(), lambda: few.half().double()):
+            change()
+            assert torch.equal(few(plan, x), want)
+    plan, tokens_plan, segs, R, block, x, tokens, Q, P, mask = _make(tdp, "bf16")
+    with torch.no_grad():
+        want = block.to_8bit(plan)(plan, x, Q, tokens_plan, tokens, P, mask)
+        block.float().bfloat16()
+        assert torch.equal(block(plan, x, Q, tokens_plan, tokens, P, mask), want)

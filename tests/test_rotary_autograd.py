@@ -158,3 +158,44 @@ def test_layers_in_8_bits_refuse_gradients(block):
     torch.nn.Module.__init__(lin)
     with pytest.raises(RuntimeError, match="no gradient"):
         lin(None, torch.randn(R, C, requires_grad=True))
+
+
+class _BfPlan:
+    esize = 2
+
+
+@pytest.fixture
+def block8(block, monkeypatch):
+    """Plain products in 8 bits, which take what the library's take."""
+    def quant8(plan, x, x8, x8_scale):
+        assert x.dtype == torch.bfloat16
+        x8_scale.copy_(x.float().abs().amax(-1).reshape(-1) / 448)
+        x8.copy_((x.float() / x8_scale.view(*x.shape[:-1], 1)).to(torch.float8_e4m3fn))
+
+    def matmul8(plan, x8, x8_scale, w8, w8_scale, out, bias=None, res=None):
+        if w8.dtype not in (torch.uint8, torch.float8_e4m3fn) or w8_scale.dtype != torch.float32 or any(t is not None and t.dtype != torch.bfloat16 for t in (bias, res)):
+            raise ValueError("dtype")
+        y = (x8.float() * x8_scale.view(*x8.shape[:-1], 1)) @ (w8.view(torch.float8_e4m3fn).float() * w8_scale[:, None]).T
+        out.copy_(y + (0 if bias is None else bias.float()) + (0 if res is None else res.float()))
+    monkeypatch.setattr(block, "tdp_quant8", quant8)
+    monkeypatch.setattr(block, "tdp_matmul8", matmul8)
+    return block
+
+
+@pytest.mark.parametrize("bias", [False, True])
+@pytest.mark.parametrize("change", [lambda m: m.to(torch.bfloat16), lambda m: m.bfloat16().float(), lambda m: m.half().double(), lambda m: m.float()])
+def test_layers_in_8_bits_outlive_a_change_of_dtype(block8, bias, change):
+    """Weights, scales and bias are what they were made as, whatever the module around them becomes."""
+    torch.manual_seed(2)
+    full = torch.nn.Linear(C, 24, bias=bias, dtype=torch.bfloat16)
+    lin, x = block8.Linear8(_BfPlan, full), torch.randn(R, C).bfloat16()
+    with torch.no_grad():
+        want = lin(_BfPlan, x)
+        around = change(torch.nn.Sequential(lin))
+        assert torch.equal(around[0](_BfPlan, x), want)
+    assert [(k, v.dtype) for k, v in lin.state_dict().items()] == \
+        [("w8", torch.uint8), ("scale", torch.float32)] + ([("bias", torch.bfloat16)] if bias else [])
+    other = block8.Linear8(_BfPlan, torch.nn.Linear(C, 24, bias=bias, dtype=torch.bfloat16))
+    other.load_state_dict(lin.state_dict())
+    with torch.no_grad():
+        assert torch.equal(other(_BfPlan, x), want)
