@@ -286,6 +286,12 @@ class RotaryBlock(torch.nn.Module):
             self.in8 = None
         return super().train(mode)
 
+    def _load_from_state_dict(self, state_dict, prefix, *args):
+        # a served block's state has its projections in 8 bits too: a block without them takes the weights
+        if self.in8 is None:
+            state_dict = {k: v for k, v in state_dict.items() if not k.startswith(prefix + "in8.")}
+        super()._load_from_state_dict(state_dict, prefix, *args)
+
     def forward(self, plan: Plan, x, Q, tokens_plan: Plan, tokens, P, mask=None, rng=None):
         """Q: tile-major positions of the rows, from tdp_split with normalize = 0, on the tokens' origin.  tokens [B, S, context] at
         P [B, 3, S, 2], with tokens_plan an untiled plan of B items of S tokens.  mask [B, S] or [n_tiles, B, S] (tdp_norm_filter's

@@ -199,3 +199,26 @@ def test_layers_in_8_bits_outlive_a_change_of_dtype(block8, bias, change):
     other.load_state_dict(lin.state_dict())
     with torch.no_grad():
         assert torch.equal(other(_BfPlan, x), want)
+
+
+def _rotary(b, seed):
+    torch.manual_seed(seed)
+    return b.RotaryBlock(C, 2, 1, 8, 24, (2, 1, 1), dtype=torch.bfloat16, device="cpu")
+
+
+def test_a_served_block_s_state_loads(block8):
+    """Into a block that is not served in 8 bits, its weights; into one that is, those in 8 bits too."""
+    served, fresh, other = _rotary(block8, 1).to_8bit(_BfPlan), _rotary(block8, 2), _rotary(block8, 3).to_8bit(_BfPlan)
+    state = served.state_dict()
+    fresh.load_state_dict(state)
+    assert all(torch.equal(v, state[k]) for k, v in fresh.state_dict().items()) and fresh.in8 is None
+    outer = torch.nn.ModuleDict({"a": _rotary(block8, 4)})
+    outer.load_state_dict({"a." + k: v for k, v in state.items()})
+    assert torch.equal(outer["a"].to_q.weight, served.to_q.weight)
+    other.load_state_dict(state)
+    for n, lin in other.in8.items():
+        assert torch.equal(lin.w8, served.in8[n].w8) and torch.equal(lin.scale, served.in8[n].scale)
+    with pytest.raises(RuntimeError, match="in8"):          # weights of another block beside 8-bit ones of this
+        other.load_state_dict(fresh.state_dict())
+    with pytest.raises(RuntimeError, match="other"):
+        fresh.load_state_dict(state | {"other": torch.zeros(1)})
