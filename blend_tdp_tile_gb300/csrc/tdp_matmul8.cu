@@ -5,6 +5,7 @@
 // at the end.
 #include <algorithm>
 #include <atomic>
+#include <type_traits>
 
 #include "tdp.h"
 #include "tdp_internal.h"
@@ -39,13 +40,13 @@ tdp_matmul8_tile_kernel(const __grid_constant__ args a, const __grid_constant__ 
     __shared__ uint64_t bar_mem[2 * NST + 1];
     __shared__ float xs[NT];
     __shared__ uint32_t tmem_slot;
-    __shared__ int dead_flag;
+    __shared__ int dead_flag, far_flag;
     volatile int *dead = &dead_flag;
     const uint32_t base = (smem_u32(raw) + 1023u) & ~1023u, full = smem_u32(bar_mem), empty = full + 8 * NST, done = empty + 8 * NST;
     const int32_t warp = warp_id(), lane = threadIdx.x & 31;
     if (warp == 5) tmem_alloc(smem_u32(&tmem_slot), kCols);
     if (threadIdx.x == 0) {
-        dead_flag = 0;
+        dead_flag = far_flag = 0;
         for (int i = 0; i < 2 * NST + 1; ++i) mbar_init(full + 8 * i, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -103,7 +104,11 @@ tdp_matmul8_tile_kernel(const __grid_constant__ args a, const __grid_constant__ 
         landed(done, 0);
     } else {
         // what the end takes besides the sums, asked for under the products
-        if (threadIdx.x < NT) xs[threadIdx.x] = row0 + threadIdx.x < a.rows ? __ldcg(a.xs + row0 + threadIdx.x) : 0.f;
+        if (threadIdx.x < NT) {
+            const float x = row0 + threadIdx.x < a.rows ? __ldcg(a.xs + row0 + threadIdx.x) : 1.f;
+            xs[threadIdx.x] = x;
+            if (!plain_scale(x)) far_flag = 1;
+        }
         if (in) {
             w = __ldcg(reinterpret_cast<const float2 *>(a.ws + ch));
             if (bias) b = make_float2((float)bias[ch], (float)bias[ch + 1]);
@@ -146,45 +151,55 @@ tdp_matmul8_tile_kernel(const __grid_constant__ args a, const __grid_constant__ 
         const float *part = reinterpret_cast<const float *>(raw + (base - smem_u32(raw))) + 2 * (threadIdx.x & 63);
         const int64_t first = row0 + (int64_t)rank * share;
         const int32_t end = (int32_t)min((int64_t)share, a.rows - first);
+        auto rows_out = [&](auto any_far) {
+            constexpr bool FAR = decltype(any_far)::value;
 #pragma unroll 1
-        for (int32_t r0 = threadIdx.x >> 6; r0 < end; r0 += 2 * U) {
-            uint2 s[U];
-            if (a.res) {
-#pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    const T *at = static_cast<const T *>(a.res) + (first + min(r0 + 2 * u, end - 1)) * a.N + ch;
-                    if (BF16) s[u].x = *reinterpret_cast<const uint32_t *>(at);
-                    else s[u] = *reinterpret_cast<const uint2 *>(at);
-                }
-            }
-            float2 sum[U];
-#pragma unroll
-            for (int u = 0; u < U; ++u) sum[u] = make_float2(0.f, 0.f);
-            for (uint32_t f = 0; f < split; ++f) {
-#pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    const float2 p = *reinterpret_cast<const float2 *>(part + ((f << shift) + min(r0 + 2 * u, end - 1)) * 128);
-                    sum[u].x += p.x;
-                    sum[u].y += p.y;
-                }
-            }
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int32_t r = r0 + 2 * u;
-                if (r >= end) break;
-                float2 v = sum[u];
-                const float x = xs[rank * share + r];
-                v.x = fmaf(v.x * x, w.x, b.x);
-                v.y = fmaf(v.y * x, w.y, b.y);
+            for (int32_t r0 = threadIdx.x >> 6; r0 < end; r0 += 2 * U) {
+                uint2 s[U];
                 if (a.res) {
-                    v.x += BF16 ? tdp_bf16_lo(s[u].x) : __uint_as_float(s[u].x);
-                    v.y += BF16 ? tdp_bf16_hi(s[u].x) : __uint_as_float(s[u].y);
+#pragma unroll
+                    for (int u = 0; u < U; ++u) {
+                        const T *at = static_cast<const T *>(a.res) + (first + min(r0 + 2 * u, end - 1)) * a.N + ch;
+                        if (BF16) s[u].x = *reinterpret_cast<const uint32_t *>(at);
+                        else s[u] = *reinterpret_cast<const uint2 *>(at);
+                    }
                 }
-                T *to = static_cast<T *>(a.out) + (first + r) * a.N + ch;
-                if (BF16) *reinterpret_cast<uint32_t *>(to) = tdp_pack_bf16x2(v.x, v.y);
-                else *reinterpret_cast<float2 *>(to) = v;
+                float2 sum[U];
+#pragma unroll
+                for (int u = 0; u < U; ++u) sum[u] = make_float2(0.f, 0.f);
+                for (uint32_t f = 0; f < split; ++f) {
+#pragma unroll
+                    for (int u = 0; u < U; ++u) {
+                        const float2 p = *reinterpret_cast<const float2 *>(part + ((f << shift) + min(r0 + 2 * u, end - 1)) * 128);
+                        sum[u].x += p.x;
+                        sum[u].y += p.y;
+                    }
+                }
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    const int32_t r = r0 + 2 * u;
+                    if (r >= end) break;
+                    float2 v = sum[u];
+                    const float x = xs[rank * share + r];
+                    if (!FAR || plain_scale(x)) {
+                        v.x = fmaf(v.x * x, w.x, b.x);
+                        v.y = fmaf(v.y * x, w.y, b.y);
+                    } else {
+                        v.x = far_scaled(v.x, x, w.x, b.x);
+                        v.y = far_scaled(v.y, x, w.y, b.y);
+                    }
+                    if (a.res) {
+                        v.x += BF16 ? tdp_bf16_lo(s[u].x) : __uint_as_float(s[u].x);
+                        v.y += BF16 ? tdp_bf16_hi(s[u].x) : __uint_as_float(s[u].y);
+                    }
+                    T *to = static_cast<T *>(a.out) + (first + r) * a.N + ch;
+                    if (BF16) *reinterpret_cast<uint32_t *>(to) = tdp_pack_bf16x2(v.x, v.y);
+                    else *reinterpret_cast<float2 *>(to) = v;
+                }
             }
-        }
+        };
+        if (far_flag) rows_out(std::true_type{});
+        else rows_out(std::false_type{});
     }
     fence_before();
     __syncthreads();
@@ -307,7 +322,7 @@ tdp_matmul8_pair_kernel(const __grid_constant__ args a, const __grid_constant__ 
             const int64_t row = (int64_t)(t / a.tiles_c) * 256 + rank * 128 + r;
             const int32_t ch = (t % a.tiles_c) * 256 + 64 * part + r;
             const bool in = r < 64 && ch < a.N;
-            x = row < a.rows ? __ldcg(a.xs + row) : 0.f;
+            x = row < a.rows ? __ldcg(a.xs + row) : 1.f;
             w = in ? __ldcg(a.ws + ch) : 0.f;
             b = in && a.bias ? (float)static_cast<const T *>(a.bias)[ch] : 0.f;
         };
@@ -344,6 +359,7 @@ tdp_matmul8_pair_kernel(const __grid_constant__ args a, const __grid_constant__ 
             ok = __all_sync(~0u, ok && !*dead);
             fence_after();
             const uint64_t x2 = ok ? pair(xs, xs) : pair(NAN, NAN);
+            const bool far = __any_sync(~0u, !plain_scale(xs));
             auto take = [&] {
                 fence_before();
                 __syncwarp();
@@ -380,30 +396,40 @@ tdp_matmul8_pair_kernel(const __grid_constant__ args a, const __grid_constant__ 
                     if (lane == 0) tma_store_read_but_one();    // the panel before the last has left
                     __syncwarp();
                 }
+                // (rows with far scales have a loop of their own: asked for at each value, 48862 x 448 x 4864 takes 204 us where this takes 177)
+                auto sums_out = [&](auto any_far) {
+                    constexpr bool FAR = decltype(any_far)::value;
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const uint32_t at = to + panel * 2048 + lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4);        // the 64-byte swizzle of the maps
-                    float f[E::kVec];
+                    for (int j = 0; j < 4; ++j) {
+                        const uint32_t at = to + panel * 2048 + lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4);        // the 64-byte swizzle of the maps
+                        float f[E::kVec];
 #pragma unroll
-                    for (int q = 0; q < E::kVec; q += 4) {
-                        const int c = 64 * part + c0 + j * E::kVec + q;
-                        const ulonglong2 w4 = *reinterpret_cast<const ulonglong2 *>(scales + c), b4 = *reinterpret_cast<const ulonglong2 *>(scales + 256 + c);
-                        const uint32_t *u = v + j * E::kVec + q;
-                        unpair(fma2(mul2(pair(__uint_as_float(u[0]), __uint_as_float(u[1])), x2), w4.x, b4.x), f[q], f[q + 1]);
-                        unpair(fma2(mul2(pair(__uint_as_float(u[2]), __uint_as_float(u[3])), x2), w4.y, b4.y), f[q + 2], f[q + 3]);
+                        for (int q = 0; q < E::kVec; q += 4) {
+                            const int c = 64 * part + c0 + j * E::kVec + q;
+                            const ulonglong2 w4 = *reinterpret_cast<const ulonglong2 *>(scales + c), b4 = *reinterpret_cast<const ulonglong2 *>(scales + 256 + c);
+                            const uint32_t *u = v + j * E::kVec + q;
+                            unpair(fma2(mul2(pair(__uint_as_float(u[0]), __uint_as_float(u[1])), x2), w4.x, b4.x), f[q], f[q + 1]);
+                            unpair(fma2(mul2(pair(__uint_as_float(u[2]), __uint_as_float(u[3])), x2), w4.y, b4.y), f[q + 2], f[q + 3]);
+                            if (FAR && !plain_scale(xs)) {
+#pragma unroll
+                                for (int i = 0; i < 4; ++i) f[q + i] = far_scaled(ok ? __uint_as_float(u[i]) : NAN, xs, scales[c + i], scales[256 + c + i]);
+                            }
+                        }
+                        if (RES) {
+                            float g[E::kVec];
+                            uint4 s;
+                            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(s.x), "=r"(s.y), "=r"(s.z), "=r"(s.w) : "r"(at) : "memory");
+                            E::unpack(s, g);
+#pragma unroll
+                            for (int q = 0; q < E::kVec; ++q) f[q] = ok ? f[q] + g[q] : NAN;
+                        }
+                        const uint4 p = E::pack(f);
+                        const uint32_t o[4] = {p.x, p.y, p.z, p.w};
+                        st_shared16(at, o);
                     }
-                    if (RES) {
-                        float g[E::kVec];
-                        uint4 s;
-                        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(s.x), "=r"(s.y), "=r"(s.z), "=r"(s.w) : "r"(at) : "memory");
-                        E::unpack(s, g);
-#pragma unroll
-                        for (int q = 0; q < E::kVec; ++q) f[q] = ok ? f[q] + g[q] : NAN;
-                    }
-                    const uint4 p = E::pack(f);
-                    const uint32_t o[4] = {p.x, p.y, p.z, p.w};
-                    st_shared16(at, o);
-                }
+                };
+                if (far) sums_out(std::true_type{});
+                else sums_out(std::false_type{});
                 fence_async();
                 __syncwarp();
                 if (lane == 0) tma_store2(&map_o, to + panel * 2048, ch0 + c0, row0);

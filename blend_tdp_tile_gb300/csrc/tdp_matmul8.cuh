@@ -119,6 +119,17 @@ __device__ __forceinline__ void tma_store2(const CUtensorMap *map, uint32_t src,
 // All but the last store have been read.
 __device__ __forceinline__ void tma_store_read_but_one() { asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory"); }
 
+// Sums are 0 or from 2^-18 to 2^38 (products of e4m3, K of them at most): with a row's scale inside these bounds neither that product nor
+// one with a channel's scale leaves fp32's range unless the result does.
+__device__ __forceinline__ bool plain_scale(float xs) { return fabsf(xs) >= 0x1p-109f && fabsf(xs) <= 0x1p90f; }
+// sum * xs * w + b for a row's scale outside them, by parts that stay inside.
+__device__ __forceinline__ float far_scaled(float sum, float xs, float w, float b)
+{
+    const bool large = fabsf(xs) > 1.f, one = large ? fabsf(w) < 1.f : fabsf(w) > 1.f;        // one: the power of two that xs lacks goes to w
+    const float up = large ? 0x1p64f : 0x1p-64f, down = large ? 0x1p-64f : 0x1p64f;
+    return fmaf(sum * (xs * down) * (one ? w * up : w), one ? 1.f : up, b);
+}
+
 // Waits, with a limit, for what is on its way to `bar`.
 __device__ __forceinline__ void landed(uint32_t bar, uint32_t parity)
 {

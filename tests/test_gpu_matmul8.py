@@ -191,3 +191,35 @@ def test_block_in_8_bits(tdp):
     err = n(out) - hd - part
     # e4m3 twice through y and wq into scores of spread one, and twice in the last product: four times 0.027 in the mean square
     assert np.linalg.norm(err) < 4 * 0.027 * np.linalg.norm(part) + 2.0 ** -8 * np.linalg.norm(hd)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("rows,N", [(9, 264), (70, 520), (500, 1032), (20000, 264)])
+def test_scales_of_any_size(tdp, dtype, rows, N):
+    """Rows and weights whose scales are no middling numbers, from the smallest float to those of rows of the largest: the product of
+    both scales and the sum is as exact as any where it is a float itself, infinite past that.  The bound counts the sum's roundings, four
+    behind it and the smallest float's step."""
+    import torch
+    K, dt = 528, torch.float32 if dtype == "f32" else torch.bfloat16
+    x8, xs, w8, ws, b, s = _case(rows, K, N, dt)
+    far = torch.tensor([2.0 ** -149, 2.0 ** -130, 2.0 ** -109, 1e-20, 1.0, 1e20, 2.0 ** 90, 1e34, 2.0 ** 119, 3e38, 0.0], device="cuda")
+    row, ch = torch.arange(rows, device="cuda"), torch.arange(N, device="cuda")
+    xs = torch.where(row % 2 == 1, far[row % 11], xs)
+    ws = torch.where(ch % 3 == 1, far[ch % 11], ws)
+    # whole small numbers, exact in any order, some of them 0
+    z = torch.randint(-2, 3, (N, K), device="cuda", generator=torch.Generator(device="cuda").manual_seed(rows)).float()
+    z[::5, 2:] = 0
+    w8 = torch.where((ch % 2 == 0)[:, None], z, w8.float()).to(torch.float8_e4m3fn)
+    out = torch.empty(rows, N, dtype=dt, device="cuda")
+    for bias, res in ((None, None), (b, s)):
+        tdp.tdp_matmul8(_plan(tdp, dtype), x8, xs, w8, ws, out, bias=bias, res=res)
+        x, w = x8.double() * xs.double()[:, None], w8.double() * ws.double()[:, None]
+        want, size = x @ w.T, x.abs() @ w.abs().T
+        if res is not None:
+            want, size = want + b.double() + s.double(), size + b.double().abs() + s.double().abs()
+        tol = 2 * (K + 8) * U * size + 8 * 2.0 ** -149 + (2.0 ** -8 * want.abs() + 2.0 ** -133 if dtype == "bf16" else 0)
+        most, got = float(torch.finfo(dt).max), out.double()
+        inside, past = want.abs() + tol < most, want.abs() - tol > most * (1 + 2.0 ** -8)
+        assert int(inside.sum()) > rows * N // 2 and int(past.sum()) > 0
+        assert ((got - want).abs() <= tol)[inside].all()
+        assert (got == torch.copysign(torch.full_like(want, float("inf")), want))[past].all()
