@@ -4,7 +4,7 @@
 //   a' = scale (a cos(p f) - b sin(p f)),  b' = scale (a sin(p f) + b cos(p f));  the gradient turns by -p f.
 // An angle is kept in turns: p f / 2 pi, of which only the fraction counts, is the low 64 bits of the product of an integer
 // position and the frequency in 2^-64 turns.  No reduction loses digits however far the position is: 2^32 positions off
-// the origin the angle is 2^-30 turns off, and 64-bit floats, a fiftieth of the rate of 32-bit ones here, are not needed.
+// the origin this is 2^-30 turns off, what fp32 then holds of it 2^-28 (2^-24 in bf16's fast form), and 64-bit floats, a fiftieth of the rate of 32-bit ones here, are not needed.
 //
 // Bound by memory.  A thread makes the sines of its pairs once and takes them through the heads of its row, 16 bytes at
 // a time where the layout allows, several heads' loads ahead.
@@ -175,14 +175,22 @@ tdp_rope_kernel(const __grid_constant__ tdp_geom g, const __grid_constant__ rope
             const int64_t f = a.table[item * P + i];
             const int32_t axis = (int32_t)f & 3;
             const uint64_t turn = (uint64_t)(f & ~3ll) * (uint64_t)(axis == 0 ? p[0] : axis == 1 ? p[1] : p[2]);
-            const float half = (float)(int32_t)(turn >> 32) * 0x1p-31f;       // half turns, -1 to 1
+            const uint32_t t = (uint32_t)(turn >> 32);
             if (BF16) {
+                const float half = (float)(int32_t)t * 0x1p-31f;        // half turns, -1 to 1
                 // the fast functions, off by 2^-21 within half a turn: a thousandth of what bf16's outputs are rounded by, and a tenth of
                 // the instructions (822528 rows of 8 heads of 64: 251 us for 256, 35840 rows of one head 5.2 for 5.6)
                 c[i] = __cosf(half * 3.14159265f);
                 s[i] = __sinf(half * 3.14159265f);
             } else {
-                sincospif(half, &s[i], &c[i]);
+                // the nearest quarter turn, and at most an eighth on top, which fp32 holds to 2^-28 turns; of a whole turn it holds 2^-26
+                const uint32_t q = (t + 0x20000000u) >> 30;
+                float p, r;
+                sincospif((float)(int32_t)(t - (q << 30)) * 0x1p-31f, &r, &p);
+                c[i] = q & 1 ? r : p;
+                s[i] = q & 1 ? p : r;
+                if ((q + 1) & 2) c[i] = -c[i];
+                if (q & 2) s[i] = -s[i];
             }
             c[i] *= a.scale;
             s[i] *= a.sign * a.scale;

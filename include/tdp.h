@@ -688,7 +688,8 @@ tdp_status tdp_rope_table(int32_t pairs, const double *freq, const int32_t *axis
  * Pair i, (a, b), of every head of the row of token j of (tile t, item b), p the token's position (start or
  * middle of its interval) on the pair's axis:
  *   a' = scale * (a cos(p f_i) - b sin(p f_i)),  b' = scale * (a sin(p f_i) + b cos(p f_i));
- * the gradient turns dout by -p f_i.  Angles are exact to 2^-30 turns at any int32 positions.
+ * the gradient turns dout by -p f_i.  At any int32 positions angles are off by at most 2^-27 turns in fp32 plans, and cos and sin by a
+ * unit of 2^-23 of themselves beside; in bf16 plans angles by 2^-24 turns and cos and sin by 2^-21.
  *
  *   x, out     device [R, heads, head_dim] by their strides (plan dtype); x may be broadcast (stride 0); out
  *              may be x itself with the same strides, and must not overlap it otherwise.

@@ -176,3 +176,28 @@ def test_elements_past_32_bits(tdp):
     tdp.tdp_rope(few, x[-3:].clone(), Q.view(3, n, 2)[:, -3:].contiguous(), table, want)
     tdp.tdp_rope(plan, x, Q, table, x)
     assert torch.equal(x[-3:], want)
+
+
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
+def test_sines_of_every_angle(tdp, layout):
+    """fp32: an angle is taken to its nearest quarter turn and a remainder of at most an eighth, which 24 bits hold to 2^-28 turns (and
+    2^-32 for the last bits of 64 that are left out); the sines then are a unit of 2^-23 off and no more, small ones too."""
+    import torch
+    plan, segs, R, Q = _make(tdp, "line", "f32", 1 << 12, seed=5)
+    r = np.random.default_rng(6)
+    n = 120
+    freq, axis = np.pi * (1 + r.integers(0, 64, n) / 32) * (1 + 2.0 ** -r.uniform(8, 24, n)), r.integers(0, 3, n)       # next to parts of a turn
+    freq[::3] = r.random(n // 3)
+    x = torch.zeros(R, 1, 2 * n, device="cuda")
+    (x[..., 0::2] if layout == "interleaved" else x[..., :n]).fill_(1)
+    Qd, table = torch.from_numpy(Q).cuda(), tdp.tdp_rope_table(freq, axis).cuda()
+    _, angle = ref.angles(segs, Q, freq, axis, True)
+    for f, sign in ((tdp.tdp_rope, 1), (tdp.tdp_rope_grad, -1)):
+        out = torch.empty_like(x)
+        f(plan, x, Qd, table, out, layout=layout)
+        got = out[:, 0].double().cpu().numpy()
+        c, s = (got[:, 0::2], got[:, 1::2]) if layout == "interleaved" else (got[:, :n], got[:, n:])
+        # angles of 64 bits are 2^-53 of themselves off, twice, up to 2^12 * 10
+        turn = 2 * np.pi * (2.0 ** -28 + 2.0 ** -32) + 4 * np.abs(angle) * 2.0 ** -53
+        for v, want, slope in ((c, np.cos(angle), np.sin(angle)), (s, sign * np.sin(angle), np.cos(angle))):
+            assert (np.abs(v - want) <= turn * (np.abs(slope) + turn) + 2.0 ** -23 * np.abs(want) + 1e-12).all()
