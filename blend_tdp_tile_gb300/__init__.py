@@ -973,7 +973,7 @@ def _rope(where, fn, plan, x, Q, table, out, layout, at, scale, stream):
     shape = (_rows(plan), H, D)
     if not x.is_cuda or not out.is_cuda:
         _strides(x, "x", shape, lat), _strides(out, "out", shape, lat)          # says so
-    xp, op, pairs = x.data_ptr(), out.data_ptr(), table.numel()
+    xp, op, pairs, scale = x.data_ptr(), out.data_ptr(), table.numel(), float(scale)        # a number, not what held it
     key = (xs, out.shape, x.stride(), out.stride(), pairs, layout, at, scale)
     a = plan.ropes.get(key)
     if a is None or xp % 16 or op % 16 or x.dtype not in lat or out.dtype not in lat:

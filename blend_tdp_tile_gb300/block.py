@@ -179,7 +179,7 @@ def rms_norm(plan: Plan, x, w=None, res=None, eps=1e-6, keep8=False):
 def rope(plan: Plan, x, Q, table, layout="half", at="middle", scale=1.0):
     """Tile rows x [R, heads, D], every head turned by the rows' positions Q (from tdp_split; table from tdp_rope_table);
     gradient for x."""
-    return _Rope.apply(plan, x, Q, table, layout, at, scale)
+    return _Rope.apply(plan, x, Q, table, layout, at, float(scale))      # the gradient's too, whatever held it becomes
 
 
 def quant8(plan: Plan, x):

@@ -201,3 +201,18 @@ def test_sines_of_every_angle(tdp, layout):
         turn = 2 * np.pi * (2.0 ** -28 + 2.0 ** -32) + 4 * np.abs(angle) * 2.0 ** -53
         for v, want, slope in ((c, np.cos(angle), np.sin(angle)), (s, sign * np.sin(angle), np.cos(angle))):
             assert (np.abs(v - want) <= turn * (np.abs(slope) + turn) + 2.0 ** -23 * np.abs(want) + 1e-12).all()
+
+
+def test_scale_is_read_in_every_call(tdp):
+    """A factor that a program keeps in a tensor and changes there."""
+    import torch
+    plan, segs, R, Q = _make(tdp, "frames", "f32")
+    Qd, table = torch.from_numpy(Q).cuda(), tdp.tdp_rope_table(*tdp.tdp_rope_freqs((8, 8, 8))[:2]).cuda()
+    x = torch.randn(R, 2, 48, device="cuda")
+    one, two, want = (torch.empty_like(x) for _ in range(3))
+    for scale in (torch.tensor(1.0), np.array(1.0, np.float32)):
+        tdp.tdp_rope(plan, x, Qd, table, one, scale=scale)
+        scale += 1
+        tdp.tdp_rope(plan, x, Qd, table, two, scale=scale)
+        tdp.tdp_rope(plan, x, Qd, table, want, scale=2.0)
+        assert torch.equal(two, want) and not torch.equal(one, two)

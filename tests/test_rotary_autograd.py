@@ -222,3 +222,15 @@ def test_a_served_block_s_state_loads(block8):
         other.load_state_dict(fresh.state_dict())
     with pytest.raises(RuntimeError, match="other"):
         fresh.load_state_dict(state | {"other": torch.zeros(1)})
+
+
+def test_the_gradient_takes_the_forward_s_scale(block, monkeypatch):
+    """A factor in a tensor that changes between the two."""
+    seen = []
+    for name in ("tdp_rope", "tdp_rope_grad"):
+        monkeypatch.setattr(block, name, lambda plan, x, Q, table, out, layout, at, scale: (seen.append(float(scale)), out.copy_(x)))
+    scale, x = torch.tensor(1.5), torch.randn(R, H, D, requires_grad=True)
+    y = block.rope(None, x, torch.zeros(6 * R, dtype=torch.int32), torch.zeros(D // 2, dtype=torch.int64), scale=scale)
+    scale += 1
+    y.sum().backward()
+    assert seen == [1.5, 1.5]
