@@ -15,6 +15,15 @@ static inline bool tdp_aligned(const void *p, uintptr_t a)
     return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0;
 }
 
+// Whether two buffers (either may be NULL) have a byte in common.
+static inline bool tdp_overlap(const void *p, int64_t n, const void *q, int64_t m)
+{
+    const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
+    return p && q && a < b + (uintptr_t)m && b < a + (uintptr_t)n;
+}
+// The same, but one buffer for both is fine.
+static inline bool tdp_partly(const void *p, const void *q, int64_t n) { return p != q && tdp_overlap(p, n, q, n); }
+
 #ifdef __CUDACC__
 #include <cuda_runtime.h>
 

@@ -601,6 +601,9 @@ extern "C" tdp_status tdp_matmul8(tdp_plan_t plan, int64_t rows, int32_t K, int3
         !tdp_aligned(x8_scale, 4) || !tdp_aligned(w8_scale, 16))
         return tdp_fail(TDP_ERR_MISALIGNED, "rows, w8_scale and bias need 16-byte, x8_scale 4-byte alignment");
     if ((rows + 127) / 128 * ((N + 127) / 128) > (1 << 28)) return tdp_fail(TDP_ERR_TOO_LARGE, "rows * N above 2^42");
+    const int64_t n = rows * N * g.esize;
+    if (tdp_overlap(out, n, x8, rows * K) || tdp_overlap(out, n, w8, (int64_t)N * K) || tdp_partly(out, res, n))
+        return tdp_fail(TDP_ERR_INVALID_ARG, "out over x8, w8 or a part of res");
     args a = {x8_scale, w8_scale, bias, res, out, rows, N, (K + kK - 1) / kK, (N + 127) / 128, 0, 0, 0};
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     const cudaError_t err = g.dtype == TDP_BF16 ? matmul8<1>(a, w8, x8, K, s) : matmul8<0>(a, w8, x8, K, s);

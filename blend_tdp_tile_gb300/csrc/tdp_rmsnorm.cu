@@ -656,11 +656,18 @@ extern "C" tdp_status tdp_rms_norm(tdp_plan_t plan, int64_t rows, int32_t C, flo
     if (!(eps >= 0.f) || eps - eps != 0.f) return tdp_fail(TDP_ERR_INVALID_ARG, "eps must be finite and not negative");
     if (rows == 0) return tdp_ok();
     if (!x || (!y && !y8 && !x8 && !h && !rstd)) return tdp_fail(TDP_ERR_INVALID_ARG, "null x, or no output");
-    if (h && h == y) return tdp_fail(TDP_ERR_INVALID_ARG, "h and y are one buffer");
     if (!y8 != !y8_scale || !x8 != !x8_scale) return tdp_fail(TDP_ERR_INVALID_ARG, "8-bit rows and their scales come together");
     if (!tdp_aligned(x, 16) || !tdp_aligned(res, 16) || !tdp_aligned(w, 16) || !tdp_aligned(h, 16) || !tdp_aligned(y, 16) ||
         !tdp_aligned(y8, 16) || !tdp_aligned(x8, 16) || !tdp_aligned(rstd, 4) || !tdp_aligned(y8_scale, 4) || !tdp_aligned(x8_scale, 4))
         return tdp_fail(TDP_ERR_MISALIGNED, "rows and w need 16-byte, scales and rstd 4-byte alignment");
+    const int64_t n = rows * C * plan->g.esize, n8 = rows * C, nr = rows * 4;
+    if (tdp_overlap(h, n, y, n) || tdp_overlap(y8, n8, x8, n8) || tdp_overlap(rstd, nr, y8_scale, nr) || tdp_overlap(rstd, nr, x8_scale, nr) ||
+        tdp_overlap(y8_scale, nr, x8_scale, nr))
+        return tdp_fail(TDP_ERR_INVALID_ARG, "two outputs in one buffer");
+    for (const void *p : {x, res, static_cast<const void *>(h), static_cast<const void *>(y)})
+        if (tdp_overlap(y8, n8, p, n) || tdp_overlap(x8, n8, p, n)) return tdp_fail(TDP_ERR_INVALID_ARG, "8-bit rows over others");
+    if (tdp_partly(h, x, n) || tdp_partly(h, res, n) || tdp_partly(y, x, n) || tdp_partly(y, res, n))
+        return tdp_fail(TDP_ERR_INVALID_ARG, "h or y over a part of x or res");
     const bool small = (y8 || x8) && eps < 0x1p-36f;
     const norm_shape sh = norm_deal(rows, nv, kNormVecs, res ? 2 : 1, small ? 256 : (y8 || x8) && (res || y) ? 384 : 512);
     norm_args a = {rows, C, nv, sh.lanes, sh.warps, eps, 1.f / (float)C, x, res, w, h, y, rstd, y8, x8, y8_scale, x8_scale};
@@ -683,6 +690,7 @@ extern "C" tdp_status tdp_quant8(tdp_plan_t plan, int64_t rows, int32_t C, const
     if (!x || !x8 || !x8_scale) return tdp_fail(TDP_ERR_INVALID_ARG, "null x, x8 or x8_scale");
     if (!tdp_aligned(x, 16) || !tdp_aligned(x8, 16) || !tdp_aligned(x8_scale, 4))
         return tdp_fail(TDP_ERR_MISALIGNED, "rows need 16-byte, scales 4-byte alignment");
+    if (tdp_overlap(x8, rows * C, x, rows * C * plan->g.esize)) return tdp_fail(TDP_ERR_INVALID_ARG, "8-bit rows over x");
     const norm_shape sh = norm_deal(rows, nv, kNormVecs, 1, 768);
     norm_args a = {};
     a.rows = rows;
@@ -722,6 +730,9 @@ extern "C" tdp_status tdp_rms_norm_grad(tdp_plan_t plan, int64_t rows, int32_t C
         if (!tdp_aligned(h, 16) || !tdp_aligned(x8, 16) || !tdp_aligned(w, 16) || !tdp_aligned(dy, 16) || !tdp_aligned(dh, 16) ||
             !tdp_aligned(dx, 16) || !tdp_aligned(x8_scale, 4) || !tdp_aligned(rstd, 4) || !tdp_aligned(ws, 256))
             return tdp_fail(TDP_ERR_MISALIGNED, "rows and w need 16-byte, scales and rstd 4-byte, ws 256-byte alignment");
+        const int64_t n = rows * C * plan->g.esize;
+        if (tdp_overlap(dx, n, x8, rows * C) || tdp_partly(dx, h, n) || tdp_partly(dx, dy, n) || tdp_partly(dx, dh, n))
+            return tdp_fail(TDP_ERR_INVALID_ARG, "dx over x8, or a part of h, dy or dh");
     }
     if (!tdp_aligned(dw, 4)) return tdp_fail(TDP_ERR_MISALIGNED, "dw needs 4-byte alignment");
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);

@@ -570,7 +570,8 @@ tdp_status tdp_dropout_grad(tdp_plan_t plan, int64_t n, double p, const uint64_t
  *   x, res      device [rows, C] (plan dtype), read; res may be NULL.
  *   w           device [C] (plan dtype), read; NULL: 1.
  *   h, y        device [rows, C] (plan dtype), written; either may be NULL, and either may be x
- *               or res itself, but not both the same buffer.
+ *               or res itself, but not both the same buffer.  Rows in 8 bits lie apart from all others, and no two
+ *               outputs share memory.
  *   rstd        device fp32 [rows], written; or NULL.  The gradient reads it.
  *   y8, y8_scale   y in 8 bits: device uint8 [rows, C] and fp32 [rows], written; or both NULL.
  *   x8, x8_scale   u in 8 bits, as a checkpoint for the gradient in place of h; or both NULL.
@@ -594,7 +595,7 @@ tdp_status tdp_rms_norm(tdp_plan_t plan, int64_t rows, int32_t C, float eps, con
  *   w            as for tdp_rms_norm.
  *   dy           device [rows, C] (plan dtype), read.
  *   dh           device [rows, C] (plan dtype), the gradient that comes by way of h, read; or NULL: 0.
- *   dx           device [rows, C] (plan dtype), written; may be dy or dh itself.
+ *   dx           device [rows, C] (plan dtype), written; may be dy, dh or h itself.
  *   dw           device fp32 [C], written (zero without rows); or NULL.
  *   ws           device workspace of tdp_rms_norm_grad_workspace(plan, rows, C, ...) bytes; not used without dw.
  */
@@ -611,7 +612,7 @@ tdp_status tdp_rms_norm_grad(tdp_plan_t plan, int64_t rows, int32_t C, const voi
  * tdp_quant8 -- rows in 8 bits as tdp_rms_norm writes them: weights (a scale an output channel), attention outputs.
  *
  *   x             device [rows, C] (plan dtype), read; C as for tdp_rms_norm.
- *   x8, x8_scale  device uint8 [rows, C] and fp32 [rows], written.
+ *   x8, x8_scale  device uint8 [rows, C] and fp32 [rows], written; not over x.
  */
 tdp_status tdp_quant8(tdp_plan_t plan, int64_t rows, int32_t C, const void *x, uint8_t *x8, float *x8_scale,
                       tdp_stream_t stream);
@@ -630,7 +631,7 @@ tdp_status tdp_quant8(tdp_plan_t plan, int64_t rows, int32_t C, const void *x, u
  *   w8, w8_scale   device e4m3 [N, K] (an output channel a row) and fp32 [N] (16-byte aligned), read.
  *   bias           device [N] (plan dtype), read; or NULL.
  *   res            device [rows, N] (plan dtype), read; or NULL.
- *   out            device [rows, N] (plan dtype), written; may be res itself.
+ *   out            device [rows, N] (plan dtype), written; may be res itself, and not over a part of it, x8 or w8.
  * The first call on a device raises the kernels' shared-memory limits; make it before
  * capturing a stream into a CUDA graph.
  */

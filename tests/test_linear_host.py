@@ -183,3 +183,36 @@ def test_header_and_binding_agree(tdp):  # noqa: F811
     assert "#define TDP_MAX_MATMUL8_ROWS (1 << 30)" in src and tdp.TDP_MAX_MATMUL8_ROWS == 1 << 30
     assert "#define TDP_MAX_ROPE_HEADS (1 << 20)" in src and tdp.TDP_MAX_ROPE_HEADS == 1 << 20
     assert ctypes.sizeof(tdp._Rope) == 6 * 4 + 4 * 8
+
+
+@no_gpu_only
+def test_outputs_in_one_place_refused(tdp):  # noqa: F811
+    """Outputs on top of one another, or over a part of what others still read; 4 rows of 64 bf16 are 512 bytes, 256 in 8 bits."""
+    lib, plan = tdp._lib, _plan(tdp)
+    far = {n: (i + 2) << 16 for i, n in enumerate(("x", "res", "w", "h", "y", "rstd", "y8", "ys", "x8", "xs"))}
+
+    def fwd(**kw):
+        return lib.tdp_rms_norm(plan.handle, 4, 64, 1e-5, *(far | {k: far.get(v[0], 0) + v[1] for k, v in kw.items()}).values(), None)
+    ok = (0, 6)             # launched, as far as that goes without a GPU
+    assert fwd() in ok
+    for a, b in (("h", "x"), ("h", "res"), ("y", "x"), ("y", "res")):
+        assert fwd(**{a: (b, 0)}) in ok and fwd(**{a: (b, 16)}) == 1 and fwd(**{a: (b, -496)}) == 1 and fwd(**{a: (b, 512)}) in ok
+    for a in ("y8", "x8"):
+        for b in ("x", "res", "h", "y"):
+            assert fwd(**{a: (b, 0)}) == 1 and fwd(**{a: (b, 496)}) == 1 and fwd(**{a: (b, 512)}) in ok and fwd(**{a: (b, -256)}) in ok
+    assert fwd(y8=("x8", 0)) == 1 and fwd(y8=("x8", 240)) == 1 and fwd(y8=("x8", 256)) in ok and fwd(h=("y", 16)) == 1 and fwd(h=("y", 0)) == 1
+    for a, b in (("rstd", "ys"), ("rstd", "xs"), ("ys", "xs")):
+        assert fwd(**{a: (b, 0)}) == 1 and fwd(**{a: (b, 12)}) == 1 and fwd(**{a: (b, 16)}) in ok
+    X = 1 << 20
+    assert lib.tdp_quant8(plan.handle, 4, 64, X, X, 4 * X, None) == 1 and lib.tdp_quant8(plan.handle, 4, 64, X, X + 496, 4 * X, None) == 1
+    assert lib.tdp_quant8(plan.handle, 4, 64, X, X + 512, 4 * X, None) in ok
+
+    def grad(dx, h=None, x8=None):
+        return lib.tdp_rms_norm_grad(plan.handle, 4, 64, h, x8, x8 and 5 * X, 6 * X, None, 2 * X, 3 * X, dx, None, None, 0, None)
+    assert all(grad(d, h=X) in ok for d in (X, 2 * X, 3 * X, 4 * X)) and all(grad(d + 16, h=X) == 1 for d in (X, 2 * X, 3 * X))
+    assert grad(X, x8=X) == 1 and grad(X - 496, x8=X) == 1 and grad(X - 512, x8=X) in ok
+
+    def mm(out, res=None):
+        return lib.tdp_matmul8(plan.handle, 4, 64, 64, X, 5 * X, 2 * X, 6 * X, None, res, out, None)
+    assert mm(3 * X) in ok and mm(X) == 1 and mm(X + 240) == 1 and mm(2 * X + 4080) == 1 and mm(2 * X + 4096) in ok
+    assert mm(3 * X, 3 * X) in ok and mm(3 * X, 3 * X + 16) == 1
