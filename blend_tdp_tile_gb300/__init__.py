@@ -377,6 +377,23 @@ class _Call:
         self.on(t, name)
         return p
 
+    def rows(self, t, name, shape, n, C, dtypes):
+        """ptr of n values as rows of C: of this shape, or any that has such rows."""
+        if t is None:
+            return None
+        try:
+            d = t.get_device()
+            if d >= 0 and t.dtype in dtypes and t.shape == shape and t.is_contiguous():
+                p = t.data_ptr()
+                if not p % 16:
+                    if d != self.dev:
+                        self._device(t, name, d)
+                    return p
+        except (AttributeError, RuntimeError):
+            pass
+        _ends(t, name, C)
+        return self.ptr(t, name, n, dtypes, 16)
+
     def run(self, fn, *args, stream=None):
         d = self.dev
         if stream is None and d is not None and (_current_device or _current()) and d == _current_device():
@@ -865,6 +882,18 @@ def _matrix(x, name):
         raise ValueError(f"{name}: shape {tuple(x.shape)} has no rows") from None
 
 
+def _ends(t, name, C):
+    """Refuses a tensor whose rows are not C values: it may be flat, or end in dimensions of C values in all."""
+    if t is None or not isinstance(t, _torch().Tensor) or t.dim() < 2 or t.size(-1) == C:
+        return
+    n = 1
+    for s in reversed(t.shape):
+        n *= s
+        if n == C:
+            return
+    raise ValueError(f"{name}: shape {tuple(t.shape)}, expected rows of {C} values")
+
+
 def tdp_rms_norm(plan: Plan, x, w, y=None, res=None, h=None, rstd=None, y8=None, y8_scale=None, x8=None, x8_scale=None, eps=1e-6,
                  stream=None):
     """y = root-mean-square norm of the rows of h = x + res [.., C], times w [C] (res, w: or None).
@@ -874,10 +903,11 @@ def tdp_rms_norm(plan: Plan, x, w, y=None, res=None, h=None, rstd=None, y8=None,
     f32, lat, b8 = _types32 or _floats32(), plan.lat or _latent_dtypes(plan), _types8 or _bytes8()
     rows, C = _matrix(x, "x")
     n = rows * C
+    xs = x.shape
     c = _Call("tdp_rms_norm")
-    c.run(_lib.tdp_rms_norm, plan.handle, rows, C, float(eps), c.ptr(x, "x", n, lat, 16), c.ptr(res, "res", n, lat, 16),
-          c.ptr(w, "w", C, lat, 16), c.ptr(h, "h", n, lat, 16), c.ptr(y, "y", n, lat, 16), c.ptr(rstd, "rstd", rows, f32, 4),
-          c.ptr(y8, "y8", n, b8, 16), c.ptr(y8_scale, "y8_scale", rows, f32, 4), c.ptr(x8, "x8", n, b8, 16),
+    c.run(_lib.tdp_rms_norm, plan.handle, rows, C, float(eps), c.ptr(x, "x", n, lat, 16), c.rows(res, "res", xs, n, C, lat),
+          c.ptr(w, "w", C, lat, 16), c.rows(h, "h", xs, n, C, lat), c.rows(y, "y", xs, n, C, lat), c.ptr(rstd, "rstd", rows, f32, 4),
+          c.rows(y8, "y8", xs, n, C, b8), c.ptr(y8_scale, "y8_scale", rows, f32, 4), c.rows(x8, "x8", xs, n, C, b8),
           c.ptr(x8_scale, "x8_scale", rows, f32, 4), stream=stream)
 
 
@@ -901,10 +931,11 @@ def tdp_rms_norm_grad(plan: Plan, dy, dx, w, rstd, h=None, x8=None, x8_scale=Non
     n = rows * C
     if dw is not None:
         ws = _workspace(ws, tdp_rms_norm_grad_workspace(plan, rows, C), dy, stream, plan)
+    xs = dy.shape
     c = _Call("tdp_rms_norm_grad")
-    c.run(_lib.tdp_rms_norm_grad, plan.handle, rows, C, c.ptr(h, "h", n, lat, 16), c.ptr(x8, "x8", n, _bytes8(), 16),
+    c.run(_lib.tdp_rms_norm_grad, plan.handle, rows, C, c.rows(h, "h", xs, n, C, lat), c.rows(x8, "x8", xs, n, C, _types8 or _bytes8()),
           c.ptr(x8_scale, "x8_scale", rows, f32, 4), c.ptr(rstd, "rstd", rows, f32, 4), c.ptr(w, "w", C, lat, 16),
-          c.ptr(dy, "dy", n, lat, 16), c.ptr(dh, "dh", n, lat, 16), c.ptr(dx, "dx", n, lat, 16), c.ptr(dw, "dw", C, f32, 4),
+          c.ptr(dy, "dy", n, lat, 16), c.rows(dh, "dh", xs, n, C, lat), c.rows(dx, "dx", xs, n, C, lat), c.ptr(dw, "dw", C, f32, 4),
           None if ws is None else c.ptr(ws, "ws", ws.numel(), (_torch().uint8,), 256),
           0 if ws is None else ws.numel(), stream=stream)
 
@@ -914,7 +945,7 @@ def tdp_quant8(plan: Plan, x, x8, x8_scale, stream=None):
     rows, C = _matrix(x, "x")
     c = _Call("tdp_quant8")
     c.run(_lib.tdp_quant8, plan.handle, rows, C, c.ptr(x, "x", rows * C, plan.lat or _latent_dtypes(plan), 16),
-          c.ptr(x8, "x8", rows * C, _types8 or _bytes8(), 16), c.ptr(x8_scale, "x8_scale", rows, _types32 or _floats32(), 4), stream=stream)
+          c.rows(x8, "x8", x.shape, rows * C, C, _types8 or _bytes8()), c.ptr(x8_scale, "x8_scale", rows, _types32 or _floats32(), 4), stream=stream)
 
 
 def tdp_matmul8(plan: Plan, x8, x8_scale, w8, w8_scale, out, bias=None, res=None, stream=None):
@@ -924,10 +955,11 @@ def tdp_matmul8(plan: Plan, x8, x8_scale, w8, w8_scale, out, bias=None, res=None
     (rows, K), (N, Kw) = _matrix(x8, "x8"), _matrix(w8, "w8")
     if Kw != K:
         raise ValueError(f"w8: rows of {Kw} values, x8 has {K}")
+    xs = (rows, N)
     c = _Call("tdp_matmul8")
     c.run(_lib.tdp_matmul8, plan.handle, rows, K, N, c.ptr(x8, "x8", rows * K, b8, 16), c.ptr(x8_scale, "x8_scale", rows, f32, 4),
           c.ptr(w8, "w8", N * K, b8, 16), c.ptr(w8_scale, "w8_scale", N, f32, 16), c.ptr(bias, "bias", N, lat, 16),
-          c.ptr(res, "res", rows * N, lat, 16), c.ptr(out, "out", rows * N, lat, 16), stream=stream)
+          c.rows(res, "res", xs, rows * N, N, lat), c.rows(out, "out", xs, rows * N, N, lat), stream=stream)
 
 
 def _named(value, names, what):

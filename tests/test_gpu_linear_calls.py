@@ -155,3 +155,38 @@ def test_broadcast_and_refused_strides(tdp):
         tdp.tdp_matmul8(s["plan"], s["y8"], s["ys"][:-1], s["w8"], s["ws"], s["out"])
     with pytest.raises(tdp.TdpError):
         tdp.tdp_rms_norm(s["plan"], s["x"], None, s["y"], h=s["y"])
+
+
+def test_rows_of_another_shape_are_refused(tdp):
+    """As many values in another order; flat ones, and dimensions that a row falls into, give what rows give."""
+    import torch
+    s = _state(tdp, 4, 40)
+    p, x, r, dy = s["plan"], s["x"], s["res"], s["dy"]
+    rows, C = x.shape
+    dt, rstd = x.dtype, torch.rand(rows, device="cuda")
+    e = lambda *n, k=dt: torch.empty(n or (rows, C), dtype=k, device="cuda")  # noqa: E731
+    ys, b8 = e(rows, k=torch.float32), torch.uint8
+    calls = {"res": lambda t, o: tdp.tdp_rms_norm(p, x, None, o, res=t), "dh": lambda t, o: tdp.tdp_rms_norm_grad(p, dy, o, None, rstd, h=x, dh=t),
+             "kept": lambda t, o: tdp.tdp_rms_norm_grad(p, dy, o, None, rstd, h=t)}
+    for f in calls.values():
+        want = e()
+        f(r, want)
+        for shape in ((rows * C,), (2, rows // 2, C), (rows, 8, C // 8)):
+            got = e(*shape)
+            f(r.view(shape), got)
+            assert torch.equal(got.view(rows, C), want)
+        for t in (r.view(C, rows), r.view(2 * rows, C // 2)):
+            with pytest.raises(ValueError, match="rows of"):
+                f(t, want)
+            with pytest.raises(ValueError, match="rows of"):
+                f(r, e(*t.shape))
+    for f in (lambda t: tdp.tdp_rms_norm(p, x, None, None, h=t), lambda t: tdp.tdp_rms_norm(p, x, None, None, y8=t.view(b8)[..., ::2].contiguous(), y8_scale=ys),
+              lambda t: tdp.tdp_quant8(p, x, t.view(b8)[..., ::2].contiguous(), ys)):
+        f(e())
+        with pytest.raises(ValueError, match="rows of"):
+            f(e(C, rows))
+    N = s["out"].shape[1]
+    for f in (lambda t: tdp.tdp_matmul8(p, s["y8"], s["ys"], s["w8"], s["ws"], t), lambda t: tdp.tdp_matmul8(p, s["y8"], s["ys"], s["w8"], s["ws"], s["out"], res=t)):
+        f(e(rows, N)), f(e(rows * N)), f(e(rows, N // 64, 64))
+        with pytest.raises(ValueError, match="rows of"):
+            f(e(N, rows))

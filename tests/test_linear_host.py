@@ -216,3 +216,14 @@ def test_outputs_in_one_place_refused(tdp):  # noqa: F811
         return lib.tdp_matmul8(plan.handle, 4, 64, 64, X, 5 * X, 2 * X, 6 * X, None, res, out, None)
     assert mm(3 * X) in ok and mm(X) == 1 and mm(X + 240) == 1 and mm(2 * X + 4080) == 1 and mm(2 * X + 4096) in ok
     assert mm(3 * X, 3 * X) in ok and mm(3 * X, 3 * X + 16) == 1
+
+
+def test_rows_of_another_shape_refused(tdp):  # noqa: F811
+    """As many values in another order are not taken as they lie; flat ones, and dimensions that a row falls into, are."""
+    import torch
+    x = torch.zeros(8, 64)
+    for bad in (torch.zeros(64, 8), torch.zeros(16, 32), torch.zeros(2, 2, 128)):
+        with pytest.raises(ValueError, match="rows of 64"):
+            tdp._ends(bad, "res", 64)
+    for good in (x, x.view(-1), x.view(2, 4, 64), x.view(8, 4, 16), x.view(1, 8, 64), x.view(8, 64, 1)):
+        tdp._ends(good, "res", 64)
