@@ -972,8 +972,8 @@ def tdp_rope_freqs(pairs, base=10000.0, scaling="none", factor=1.0, length=1.0):
     """(freq float64 [n], axis int32 [n], scale) of a head's pairs, pairs = (a number an axis): base^(-i / pairs[a]), scaled for long contexts
     by "linear", "ntk" or "yarn" (`length`: the trained one)."""
     p = np.asarray(pairs, np.int32)
-    if p.shape != (3,):
-        raise ValueError("pairs: a number for each of the three axes")
+    if p.shape != (3,) or not np.array_equal(p, np.asarray(pairs)):
+        raise ValueError("pairs: a whole number for each of the three axes")
     n = min(int(np.maximum(p, 0).sum(dtype=np.int64)), TDP_MAX_ROPE_DIM // 2)       # more are refused
     freq, axis, scale = np.zeros(n, np.float64), np.zeros(n, np.int32), ctypes.c_float()
     _check(_lib.tdp_rope_freqs(p.ctypes.data_as(ctypes.c_void_p), float(base), _named(scaling, _SCALINGS, "scaling"), float(factor), float(length),

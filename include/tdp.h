@@ -667,7 +667,7 @@ typedef struct {
  * Axis a has pairs[a] pairs (at most TDP_MAX_ROPE_DIM / 2 in all), axis 0's first: f_i = base^(-i / pairs[a]), i = 0..pairs[a]-1.  Scaled by `factor` >= 1:
  *   linear  f / factor (Chen et al., "Extending context window of large language models via positional
  *           interpolation", 2023);
- *   NTK     base * factor^(n / (n - 1)) for base, n = pairs[a]: the lowest frequency falls by factor;
+ *   NTK     base * factor^(n / (n - 1)) for base, n = pairs[a]: the lowest frequency falls by factor (one pair alone, f = 1, stays);
  *   YaRN    f * k + f / factor * (1 - k), k = clamp((length f / 2 pi - 1) / 31, 0, 1), and scale = 0.1 ln factor + 1
  *           (Peng et al., "YaRN: efficient context window extension of large language models", 2023).
  *   freq, axis   [pairs[0] + pairs[1] + pairs[2]], written.   scale  written (1 but for YaRN).

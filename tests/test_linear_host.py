@@ -227,3 +227,11 @@ def test_rows_of_another_shape_refused(tdp):  # noqa: F811
             tdp._ends(bad, "res", 64)
     for good in (x, x.view(-1), x.view(2, 4, 64), x.view(8, 4, 16), x.view(1, 8, 64), x.view(8, 64, 1)):
         tdp._ends(good, "res", 64)
+
+
+def test_parts_of_a_pair_are_refused(tdp):  # noqa: F811
+    for pairs in ((6.5, 5, 5), (6, 5, 0.5), np.array([6, 5, 5.25], np.float32)):
+        with pytest.raises(ValueError, match="whole number"):
+            tdp.tdp_rope_freqs(pairs)
+    for pairs in (np.array([6, 5, 5], np.uint8), (6.0, 5, 5)):
+        assert len(tdp.tdp_rope_freqs(pairs)[0]) == 16
