@@ -380,3 +380,24 @@ def test_quant_of_fp32_ties(tdp):
     x8, xs = torch.empty((rows, C), dtype=torch.float8_e4m3fn, device="cuda"), torch.empty(rows, device="cuda")
     tdp.tdp_quant8(_plan(tdp, "f32"), torch.from_numpy(x.astype(np.float32)).cuda(), x8, xs)
     assert np.array_equal(_np(x8.float()), ref.e4m3(t))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("rows,C", [(9, 16), (900, 136), (700, 1040), (400, 8192), (2, 8192)])
+@pytest.mark.parametrize("res", [False, True])
+def test_smallest_eps_takes_the_same_rows(tdp, dtype, rows, C, res):
+    """Below 2^-36 eps has kernels of its own; rstd, of ordinary rows the same to a rounding, stands in no value of 8 bits."""
+    import torch
+    dt = torch.float32 if dtype == "f32" else torch.bfloat16
+    x, s, w, _, _ = _inputs(rows, C, dt, 30)
+    plan, got = _plan(tdp, dtype), []
+    for eps in (2.0 ** -36, 2.0 ** -37, 0.0):
+        b = {k: torch.empty((rows, C), dtype=torch.uint8, device="cuda") for k in ("x8", "y8")} | {k: torch.empty(rows, device="cuda") for k in ("x8_scale", "y8_scale", "rstd")}
+        h, y = torch.empty_like(x), torch.empty_like(x)
+        tdp.tdp_rms_norm(plan, x, w, y, res=s if res else None, h=h, eps=eps, **b)
+        got.append(b | {"h": h, "y": y})
+    for b in got[1:]:
+        assert torch.equal(b["x8"], got[0]["x8"]) and torch.equal(b["y8"], got[0]["y8"]) and torch.equal(b["h"], got[0]["h"])
+        for k in ("x8_scale", "y8_scale", "rstd"):
+            assert ((b[k] - got[0][k]).abs() <= 8 * U * got[0][k]).all()         # two ways of summing; eps is 2^-37 of it at rstd 1
+        assert ((b["y"].double() - got[0]["y"].double()).abs() <= (2 * 2.0 ** -8 if dtype == "bf16" else 2.0 ** -20) * got[0]["y"].double().abs() + 1e-37).all()
