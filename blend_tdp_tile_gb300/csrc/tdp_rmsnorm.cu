@@ -141,11 +141,10 @@ __device__ __forceinline__ void store8(uint8_t *p, const uint64_t *v)
 // and NaN in every place; 2^-100 for less.
 __device__ __forceinline__ float top8(float top) { return top < INFINITY ? fmaxf(top, kLeast) : NAN; }
 
-// How rows v rstd (of a norm; or v, with rstd 1) become e4m3: 448 v rstd / m.  m is rstd times the row's largest |v|, `top`, so rstd cancels and 448 v / top
+// How a norm's rows v rstd become e4m3: 448 v rstd / m.  m is rstd times the row's largest |v|, `top`, so rstd cancels and 448 v / top
 // is left, a quotient of numbers as they came: of bf16 rows (h, or h w, which fp32 holds) often midway between two of e4m3's.  The
 // factor is kept in two parts, so that one rounding is left and such a value stays where it is and goes to the even one; a product
-// with the first part alone puts 0.05 % of x8's values on the wrong side.  (With 0.875 v before a quotient corrected by its remainder, fp32
-// rows lost ties to the product: 7 v has up to three digits more.)
+// with the first part alone puts 0.05 % of x8's values on the wrong side.
 struct code8 {
     uint64_t k, rest;
     // y = top * rstd, m = top8(y); lift: what v is multiplied by before, 1 or 2^100.  top * lift is 2^-118 at least, or y below 2^-100.
@@ -307,6 +306,7 @@ tdp_rms_norm_kernel(const __grid_constant__ norm_args a)
         join<Q8>(a.lanes, a.warps, turn, sum, top, top2);
         const float rstd = NORM ? __frcp_rn(__fsqrt_rn(fmaf(sum, a.mean, a.eps))) : 1.f;
         if (NORM && a.rstd && on && t.lane == 0) a.rstd[r] = rstd;
+        float part = 0.f, inv = 0.f;
         code8 cy = {}, cx = {};
         const float lift_y = SMALL && top < kLeast ? 1 / kLeast : 1.f, lift_x = SMALL && top2 < kLeast ? 1 / kLeast : 1.f;
         if (Y8 && NORM && a.y8) {
@@ -315,9 +315,16 @@ tdp_rms_norm_kernel(const __grid_constant__ norm_args a)
             cy.make(top, rstd, y, m, lift_y);
         }
         if (Q8 && (!Y8 || a.x8)) {
-            const float y = top2 * rstd, m = top8(y);
-            if (on && t.lane == 0) a.x8_scale[r] = __fdiv_rn(m, 448.f);
-            cx.make(top2, rstd, y, m, lift_x);
+            if (NORM) {
+                const float y = top2 * rstd, m = top8(y);
+                if (on && t.lane == 0) a.x8_scale[r] = __fdiv_rn(m, 448.f);
+                cx.make(top2, rstd, y, m, lift_x);
+            } else {
+                const float m = top8(top2);
+                if (on && t.lane == 0) a.x8_scale[r] = __fdiv_rn(m, 448.f);
+                part = -m * (1.f / 512);
+                inv = __frcp_rn(-part);
+            }
         }
         if (!on) continue;
         const uint64_t rs = pair(rstd, rstd);
@@ -349,13 +356,27 @@ tdp_rms_norm_kernel(const __grid_constant__ norm_args a)
             // h w is made again: carried over from the first pass in registers, 8192 channels take 25 % longer
             if (Y8 && VPT > 4) asm volatile("" : "+r"(x[i].x), "+r"(x[i].y), "+r"(x[i].z), "+r"(x[i].w));
             pairs_of<BF16>(x[i], f);
+            if (!NORM) {
+                // 448 v / m as (0.875 v) / (m / 512): no product overflows and a value midway between two of e4m3's comes out
+                // exact, so that it goes to the even one.  The quotient is corrected by its remainder (P. Markstein, "Computation of
+                // elementary functions on the IBM RISC System/6000 processor", 1990): the plain product v * inv put 0.5 % of
+                // bf16's values on the wrong side.
+                const uint64_t e = pair(0.875f, 0.875f), n = pair(part, part), k = pair(inv, inv);
+#pragma unroll
+                for (int j = 0; j < P; ++j) {
+                    const uint64_t v = mul2(f[j], e);
+                    q[j] = mul2(v, k);
+                    q[j] = fma2(fma2(q[j], n, v), k, q[j]);
+                }
+                store8<P>(a.x8 + (at + c) * V, q);
+                continue;
+            }
             if (Q8 && (!Y8 || a.x8)) {
 #pragma unroll
                 for (int j = 0; j < P; ++j) q[j] = SMALL ? mul2(f[j], pair(lift_x, lift_x)) : f[j];
                 cx.of<P>(q);
                 store8<P>(a.x8 + (at + c) * V, q);
             }
-            if (!NORM) continue;
             if (!Y8) {
 #pragma unroll
                 for (int j = 0; j < P; ++j) f[j] = mul2(f[j], rs);

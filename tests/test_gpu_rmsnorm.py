@@ -365,23 +365,6 @@ def test_norm_rows_of_small_values_in_8_bits(tdp, dtype, eps):
     assert (np.abs(_np(xs) - m / 448) <= 8 * U * m / 448).all()
 
 
-def test_quant_of_fp32_ties(tdp):
-    """v = j k and m = 7 k: 448 v / m is 64 j, with j odd and below 32 midway between two of e4m3's when scaled into them.  Both factors
-    fill fp32's digits, so that 7 v / 8 has more than it holds."""
-    import torch
-    r = np.random.default_rng(4)
-    rows, C = 256, 1024
-    k = r.integers(1 << 19, (1 << 24) // 31 + 1, (rows, 1)).astype(np.float64)
-    e = r.integers(-6, 9, (rows, C)).astype(np.float64)
-    t = np.minimum(r.integers(0, 16, (rows, C)) * 2 + 1, 31) * 2.0 ** (e - 5)        # j 2^(e-5): odd digits below e4m3's last
-    t[:, 0] = 448
-    x = t * 7 * k / 448
-    assert (x.astype(np.float32) == x).all()
-    x8, xs = torch.empty((rows, C), dtype=torch.float8_e4m3fn, device="cuda"), torch.empty(rows, device="cuda")
-    tdp.tdp_quant8(_plan(tdp, "f32"), torch.from_numpy(x.astype(np.float32)).cuda(), x8, xs)
-    assert np.array_equal(_np(x8.float()), ref.e4m3(t))
-
-
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("rows,C", [(9, 16), (900, 136), (700, 1040), (400, 8192), (2, 8192)])
 @pytest.mark.parametrize("res", [False, True])
