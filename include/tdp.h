@@ -611,6 +611,9 @@ tdp_status tdp_rms_norm_grad(tdp_plan_t plan, int64_t rows, int32_t C, const voi
 /*
  * tdp_quant8 -- rows in 8 bits as tdp_rms_norm writes them: weights (a scale an output channel), attention outputs.
  *
+ * The values are those next to the fp32 quotient of 0.875 v by m / 512: of bf16 rows the ones next to 448 v / m always, ties to the
+ * even one; of fp32 rows 0.875 v is rounded too, which moves values within 2^-23 of a tie either way.
+ *
  *   x             device [rows, C] (plan dtype), read; C as for tdp_rms_norm.
  *   x8, x8_scale  device uint8 [rows, C] and fp32 [rows], written; not over x.
  */

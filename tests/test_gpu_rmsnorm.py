@@ -384,3 +384,16 @@ def test_smallest_eps_takes_the_same_rows(tdp, dtype, rows, C, res):
         for k in ("x8_scale", "y8_scale", "rstd"):
             assert ((b[k] - got[0][k]).abs() <= 8 * U * got[0][k]).all()         # two ways of summing; eps is 2^-37 of it at rstd 1
         assert ((b["y"].double() - got[0]["y"].double()).abs() <= (2 * 2.0 ** -8 if dtype == "bf16" else 2.0 ** -20) * got[0]["y"].double().abs() + 1e-37).all()
+
+
+@pytest.mark.parametrize("rows,C", [(3000, 1024), (200, 8192), (40000, 64)])
+def test_quant_of_fp32_rows_to_the_value(tdp, rows, C):
+    """The fp32 quotient of 0.875 v by m / 512, both rounded as fp32 rounds, and the value next to it: every code, those near a tie too."""
+    import torch
+    x = _inputs(rows, C, torch.float32, 8)[0]
+    x[:, 5::7] = x.abs().amax(1, keepdim=True) * (torch.randint(1, 32, x[:, 5::7].shape, device="cuda").float() / 64)     # next to ties
+    x8, xs = torch.empty((rows, C), dtype=torch.float8_e4m3fn, device="cuda"), torch.empty(rows, device="cuda")
+    tdp.tdp_quant8(_plan(tdp, "f32"), x, x8, xs)
+    v = x.cpu().numpy()
+    q = (np.float32(0.875) * v) / (np.abs(v).max(1, keepdims=True) / np.float32(512))
+    assert q.dtype == np.float32 and np.array_equal(_np(x8.float()), ref.e4m3(q))
