@@ -472,18 +472,6 @@ bool map_out(CUtensorMap *map, void *p, int bf16, int64_t N, int64_t rows)
                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Raise a kernel's dynamic shared-memory limit once per device (`done`: one flag each).
-template <typename K>
-cudaError_t allow_smem(K kernel, size_t bytes, std::atomic<bool> *done)
-{
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess || (dev < 64 && done[dev].load(std::memory_order_relaxed))) return e;
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
-    if (e == cudaSuccess && dev < 64) done[dev].store(true, std::memory_order_relaxed);
-    return e;
-}
-
 // A dependent launch of clusters of `size` blocks.
 template <typename... KArgs, typename... Args>
 cudaError_t launch_clusters(void (*kernel)(KArgs...), unsigned grid, unsigned size, unsigned block, size_t smem, cudaStream_t s, Args &&...args)
@@ -517,7 +505,7 @@ cudaError_t tile_launch(args a, const void *w8, const void *x8, int64_t K, cudaS
 {
     static std::atomic<bool> done[64];
     constexpr size_t bytes = tile_smem<NT>::kBytes;
-    cudaError_t e = allow_smem(tdp_matmul8_tile_kernel<BF16, NT>, bytes, done);
+    cudaError_t e = tdp_allow_smem(tdp_matmul8_tile_kernel<BF16, NT>, bytes, done);
     CUtensorMap w, x;
     a.w_box = std::min(128, a.N);
     a.x_box = (int32_t)std::min<int64_t>(NT, a.rows);
@@ -533,7 +521,7 @@ cudaError_t pair_launch(args a, const void *w8, const void *x8, int64_t K, cudaS
 {
     static std::atomic<bool> done[64];
     constexpr size_t bytes = pair_smem::kBytes;
-    cudaError_t e = allow_smem(tdp_matmul8_pair_kernel<BF16, RES>, bytes, done);
+    cudaError_t e = tdp_allow_smem(tdp_matmul8_pair_kernel<BF16, RES>, bytes, done);
     CUtensorMap w, x, o, r;
     a.w_box = std::min(128, a.N);
     a.x_box = 128;

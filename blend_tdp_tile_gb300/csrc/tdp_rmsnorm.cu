@@ -598,24 +598,12 @@ tdp_status norm_check(tdp_plan_t plan, int64_t rows, int32_t C, int32_t *nv)
     return TDP_OK;
 }
 
-// Raise a kernel's dynamic shared-memory limit once per device (`done`: one flag each).
-template <typename K>
-cudaError_t allow_smem(K kernel, size_t bytes, std::atomic<bool> *done)
-{
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess || (dev < 64 && done[dev].load(std::memory_order_relaxed))) return e;
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
-    if (e == cudaSuccess && dev < 64) done[dev].store(true, std::memory_order_relaxed);
-    return e;
-}
-
 template <int BF16, int VPT, int NORM, int Q8, int RES>
 cudaError_t norm_launch(const norm_shape &sh, const norm_args &a, cudaStream_t s)
 {
     static std::atomic<bool> done[64];
     auto *kernel = tdp_rms_norm_kernel<BF16, VPT, NORM, Q8, RES>;
-    const cudaError_t e = allow_smem(kernel, kNormSmem, done);
+    const cudaError_t e = tdp_allow_smem(kernel, kNormSmem, done);
     return e != cudaSuccess ? e : tdp_launch_smem(true, kernel, (unsigned)sh.blocks, sh.threads, (size_t)32 * (1 + RES) * VPT * sh.threads, s, a);
 }
 
@@ -647,7 +635,7 @@ cudaError_t grad_launch(const norm_shape &sh, const norm_grad_args &a, cudaStrea
 {
     static std::atomic<bool> done[64];
     auto *kernel = tdp_rms_norm_grad_kernel<BF16, VPT, KEPT8>;
-    const cudaError_t e = allow_smem(kernel, kNormSmem, done);
+    const cudaError_t e = tdp_allow_smem(kernel, kNormSmem, done);
     return e != cudaSuccess ? e : tdp_launch_smem(true, kernel, (unsigned)sh.blocks, sh.threads, (size_t)96 * VPT * sh.threads, s, a);
 }
 

@@ -682,18 +682,6 @@ int sm_count()
     return n;
 }
 
-// Raise a kernel's dynamic shared-memory limit once per device (`done`: one flag each).
-template <typename K>
-cudaError_t allow_smem(K kernel, size_t bytes, std::atomic<bool> *done)
-{
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess || (dev < 64 && done[dev].load(std::memory_order_relaxed))) return e;
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
-    if (e == cudaSuccess && dev < 64) done[dev].store(true, std::memory_order_relaxed);
-    return e;
-}
-
 // bf16: the lists of kept tiles, then the product kernel.
 cudaError_t tc_kept(const xattn_shape &sh, xattn_args *a, unsigned char *ws, cudaStream_t s)
 {
@@ -744,7 +732,7 @@ cudaError_t tc_forward(const tdp_geom &g, const xattn_args &a, cudaStream_t s)
 {
     static std::atomic<bool> done[64];
     constexpr size_t bytes = tdp_xt::fwd_smem<DP>::kBytes;
-    cudaError_t e = allow_smem(tdp_xt::tdp_xattn_tc_kernel<DP>, bytes, done);
+    cudaError_t e = tdp_allow_smem(tdp_xt::tdp_xattn_tc_kernel<DP>, bytes, done);
     CUtensorMap q, k, v, o;
     // with no states the kernel loads nothing: q stands in for the maps of k and v
     if (e == cudaSuccess &&
@@ -763,8 +751,8 @@ cudaError_t tc_grad(const tdp_geom &g, const xattn_args &a, cudaStream_t s)
 {
     static std::atomic<bool> done_q[64], done_kv[64];
     constexpr size_t bytes_q = tdp_xt::dq_smem<DP>::kBytes, bytes_kv = tdp_xt::dkv_smem<DP>::kBytes;
-    cudaError_t e = allow_smem(tdp_xt::tdp_xattn_dq_kernel<DP>, bytes_q, done_q);
-    if (e == cudaSuccess) e = allow_smem(tdp_xt::tdp_xattn_dkv_kernel<DP>, bytes_kv, done_kv);
+    cudaError_t e = tdp_allow_smem(tdp_xt::tdp_xattn_dq_kernel<DP>, bytes_q, done_q);
+    if (e == cudaSuccess) e = tdp_allow_smem(tdp_xt::tdp_xattn_dkv_kernel<DP>, bytes_kv, done_kv);
     CUtensorMap q, o, d, k, v;
     const int64_t row = (int64_t)a.Hq * a.D;
     if (e == cudaSuccess &&
