@@ -8,6 +8,7 @@
 #include <type_traits>
 
 #include "tdp.h"
+#include "tdp_host.h"
 #include "tdp_internal.h"
 #include "tdp_matmul8.cuh"
 #include "tdp_tensor_map.h"

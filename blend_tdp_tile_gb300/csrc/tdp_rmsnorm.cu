@@ -16,6 +16,7 @@
 #include <atomic>
 
 #include "tdp.h"
+#include "tdp_host.h"
 #include "tdp_internal.h"
 #include "tdp_rows.cuh"
 #include "tdp_tc.cuh"
